@@ -1,0 +1,87 @@
+// Token embedding lookup with scaling: out[t] = scale * E[P[x_t]].
+//
+// Bound by memory: N d (s_in + s_out) bytes and one multiply a value. One warp serves up to
+// 1024 columns of one token, so that a decode step's few rows still spread over several SMs
+// and a wide row is read by consecutive warps; each lane has up to four 16-byte loads in
+// flight (fp32: eight) before it stores.
+#include "pg_hash.cuh"
+#include "pg_vec.cuh"
+
+namespace pg {
+namespace {
+
+constexpr int kEmbedWarps = 8;
+constexpr int kEmbedCols = 1024;  // columns of a row that one warp serves
+
+template <int IN, int OUT, bool VEC>
+__global__ void __launch_bounds__(32 * kEmbedWarps)
+    embed_kernel(const int32_t* __restrict__ tokens, int64_t tasks, int parts, uint32_t vocab,
+                 const uint32_t* __restrict__ canon_map, const void* __restrict__ table, uint32_t rows, int d,
+                 float scale, void* __restrict__ out, int32_t* err) {
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kEmbedWarps + (threadIdx.x >> 5);
+  if (task >= tasks) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = task / parts;
+  const int c0 = static_cast<int>(task - t * parts) * kEmbedCols;
+  const uint32_t row = embed_row(tokens, canon_map, vocab, rows, t);
+  if (row == kNoRow && err && lane == 0 && c0 == 0)
+    atomicMin(reinterpret_cast<unsigned int*>(err), static_cast<unsigned int>(t));
+  const int64_t src = static_cast<int64_t>(row == kNoRow ? 0 : row) * d, dst = t * d;
+  constexpr int kStep = VEC ? 8 : 1;
+  constexpr int kUnroll = 4;
+  const int end = min(d, c0 + kEmbedCols);
+  for (int c = c0 + lane * kStep; c < end; c += 32 * kStep * kUnroll) {
+    float x[kUnroll][kStep];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int cc = c + u * 32 * kStep;
+      if (cc < end) load_cols<IN, kStep>(table, src + cc, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int cc = c + u * 32 * kStep;
+      if (cc >= end) continue;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) x[u][i] = row == kNoRow ? 0.f : __fmul_rn(x[u][i], scale);
+      store_cols<OUT, kStep>(out, dst + cc, x[u]);
+    }
+  }
+}
+
+using EmbedFn = void (*)(const int32_t*, int64_t, int, uint32_t, const uint32_t*, const void*, uint32_t, int, float,
+                         void*, int32_t*);
+
+template <bool VEC>
+EmbedFn embed_fn(int in, int out) {
+  if (in == PG_F32) return out == PG_F32 ? embed_kernel<PG_F32, PG_F32, VEC> : embed_kernel<PG_F32, PG_BF16, VEC>;
+  return out == PG_F32 ? embed_kernel<PG_BF16, PG_F32, VEC> : embed_kernel<PG_BF16, PG_BF16, VEC>;
+}
+
+}  // namespace
+}  // namespace pg
+
+extern "C" pg_status pg_embed(const int32_t* tokens, int64_t N, uint32_t vocab, const uint32_t* canon_map,
+                              const void* table, int32_t table_dtype, int64_t rows, int32_t d, float scale, void* out,
+                              int32_t out_dtype, int32_t* err_index, pg_stream_t stream) {
+  using namespace pg;
+  if (N < 0 || N >= (1ll << 31) || rows < 1 || rows >= (1ll << 31) || d < 1 || d > kMaxEmbedWidth || vocab == 0)
+    return PG_ERR_SHAPE;
+  if (!real_dtype(table_dtype) || !real_dtype(out_dtype)) return PG_ERR_DTYPE;
+  if (N == 0) return PG_OK;
+  if (!tokens || !table || !out) return PG_ERR_NULL;
+  if (!aligned(tokens, 4) || !aligned(canon_map, 4) || !aligned(err_index, 4) ||
+      !aligned(table, dtype_bytes(table_dtype)) || !aligned(out, dtype_bytes(out_dtype)))
+    return PG_ERR_ALIGN;
+  const int parts = (d + kEmbedCols - 1) / kEmbedCols;
+  const int64_t tasks = N * parts, blocks = (tasks + kEmbedWarps - 1) / kEmbedWarps;
+  if (blocks >= (1ll << 31)) return PG_ERR_SHAPE;
+  if (device_cc() != 103) return PG_ERR_DEVICE;
+  pg_status st = prepare_err(err_index, stream);
+  if (st != PG_OK) return st;
+  const bool vec = d % 8 == 0 && aligned(table, 16) && aligned(out, 16);
+  EmbedFn fn = vec ? embed_fn<true>(table_dtype, out_dtype) : embed_fn<false>(table_dtype, out_dtype);
+  fn<<<static_cast<unsigned>(blocks), 32 * kEmbedWarps, 0, stream>>>(tokens, tasks, parts, vocab, canon_map, table,
+                                                                    static_cast<uint32_t>(rows), d, scale, out,
+                                                                    err_index);
+  return after_launch(1);
+}

@@ -1,0 +1,568 @@
+// Gradients of table lookups by sorted references: pg_embed_grad (the token embedding) and
+// pg_lookup_grad (the hashed multi-head table, PageGram report 9.4, check 4).
+//
+// A reference is one read of a table row: (t) for the embedding, (t, order, head) for the
+// hashed lookup, n of them in that order. With their rows sorted (stably), the references of
+// a row are neighbours and its gradient is one segmented sum:
+//
+//   1. rowgrad_sort_kernel: rows of the references (embedding: the canonical ID; hashed
+//      lookup: the hashes of pg_hash.cuh), a stable radix sort of (row, reference) with
+//      digits of up to 11 bits, and the segments of equal rows. One cooperative launch; the
+//      blocks meet at a grid barrier between the phases. Every block owns a contiguous share
+//      of the references, so ranks follow from counts alone and no order depends on timing.
+//   2. rowgrad_sum_kernel: the sums, fp32, in ascending order of the references.
+#include "pg_async.cuh"
+#include "pg_hash.cuh"
+#include "pg_vec.cuh"
+
+namespace pg {
+namespace {
+
+constexpr int kErrGradBarrier = 131072;  // device error bit: a block gave up at the grid barrier
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortItems = 8;                          // references a thread holds per tile
+constexpr int kSortTile = kSortThreads * kSortItems;   // 4096
+constexpr int kMaxDigitBits = 11;
+constexpr int kMaxDigits = 1 << kMaxDigitBits;
+constexpr int kMaxSortBlocks = 152;                    // one per SM
+constexpr int kRefsPerBlock = 2048;                    // at least, before another block joins
+constexpr int kHashItems = 32;                         // (order, head) items of a table
+
+struct SortCtrl {
+  uint32_t barrier;  // arrivals at the grid barrier, all phases
+  uint32_t done;     // blocks that finished the sort
+  uint32_t count;    // segments
+  uint32_t pad[61];
+};
+
+// Where the references' rows come from.
+struct RefSource {
+  const int32_t* tokens;
+  const uint32_t* canon_map;
+  int32_t* err;
+  uint32_t vocab;
+  uint32_t rows;     // embedding: table rows; rows itself is the key of padding
+  uint32_t L;        // hashed lookup: sequence length
+  int32_t items;     // hashed lookup: references per token
+  int32_t mode;
+  ItemConst ic[kHashItems];
+};
+
+struct SortBuffers {
+  SortCtrl* ctrl;
+  uint32_t* hist;      // [digits][blocks]
+  uint32_t* totals;    // [digits]
+  uint32_t* segs;      // [blocks] segments that start in a block's share
+  uint32_t* key[2];    // [n]
+  uint32_t* ref[2];    // [n]
+  uint32_t* seg_start; // [n + 1]
+  uint32_t* seg_row;   // [n] (embedding; the hashed lookup's is the caller's rows_out)
+  uint64_t* sign;      // [n] sign hashes of the references (hashed lookup)
+};
+
+constexpr size_t kCtrlBytes = sizeof(SortCtrl);
+
+inline size_t up16(size_t x) { return (x + 15) / 16 * 16; }
+
+// Carves the buffers from `base`; returns the bytes they take (base may be null to size them).
+size_t carve(uint8_t* base, int64_t n, bool hashed, SortBuffers* b) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base ? base + at : nullptr;
+    at += up16(bytes);
+    return p;
+  };
+  const size_t un = static_cast<size_t>(n);
+  b->ctrl = reinterpret_cast<SortCtrl*>(take(kCtrlBytes));
+  b->hist = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits * kMaxSortBlocks));
+  b->totals = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits));
+  b->segs = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxSortBlocks));
+  for (int i = 0; i < 2; ++i) {
+    b->key[i] = reinterpret_cast<uint32_t*>(take(4 * un));
+    b->ref[i] = reinterpret_cast<uint32_t*>(take(4 * un));
+  }
+  b->seg_start = reinterpret_cast<uint32_t*>(take(4 * (un + 1)));
+  b->seg_row = hashed ? nullptr : reinterpret_cast<uint32_t*>(take(4 * un));
+  b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un)) : nullptr;
+  return at;
+}
+
+// ------------------------------------------------------------------------------- the sort
+
+// All blocks of the grid; false after a time limit of about one second (then every block
+// gives up, since the count it waits for is not reached). `phase` counts the barriers.
+__device__ __forceinline__ bool grid_barrier(uint32_t* counter, uint32_t* phase, int* s_ok, int* err_word) {
+  *phase += 1;
+  __syncthreads();
+  if (gridDim.x == 1) return true;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(counter, 1u);
+    const uint32_t want = *phase * gridDim.x;
+    const uint64_t t0 = now_ns();
+    uint32_t seen;
+    bool ok = true;
+    for (;;) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(counter) : "memory");
+      if (seen >= want) break;
+      if (now_ns() - t0 > kAsyncWaitNs) {
+        ok = false;
+        if (err_word) atomicOr(err_word, kErrGradBarrier);
+        break;
+      }
+    }
+    __threadfence();
+    *s_ok = ok;
+  }
+  __syncthreads();
+  return *s_ok != 0;
+}
+
+__device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// Exclusive scan of one value per thread over the block, and the total.
+__device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* s_warp, uint32_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint32_t inc = warp_incl_scan(v, lane);
+  __syncthreads();
+  if (lane == 31) s_warp[w] = inc;
+  __syncthreads();
+  if (w == 0) {
+    const uint32_t x = lane < kSortWarps ? s_warp[lane] : 0u;
+    const uint32_t xi = warp_incl_scan(x, lane);
+    if (lane < kSortWarps) s_warp[lane] = xi - x;
+    if (lane == kSortWarps - 1) s_warp[kSortWarps] = xi;
+  }
+  __syncthreads();
+  *total = s_warp[kSortWarps];
+  return s_warp[w] + inc - v;
+}
+
+template <bool HASHED>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    rowgrad_sort_kernel(const __grid_constant__ RefSource src, SortBuffers b, uint32_t n, uint32_t share, int passes,
+                        int bits, uint32_t* __restrict__ rows_out, int32_t* __restrict__ count_out, int* err_word) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);                    // [warps][digits]
+  uint32_t* s_base = reinterpret_cast<uint32_t*>(s_raw + kSortWarps * kMaxDigits * 2);  // [digits]
+  __shared__ uint32_t s_warp[kSortWarps + 1];
+  __shared__ int s_ok;
+  __shared__ ItemConst s_ic[HASHED ? kHashItems : 1];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t lo = min(n, blockIdx.x * share), hi = min(n, lo + share);
+  const int digits = 1 << bits;
+  const uint32_t mask = static_cast<uint32_t>(digits - 1);
+  const uint32_t G = gridDim.x;
+  uint32_t phase = 0;
+
+  if (HASHED) {
+    const int words = src.items * static_cast<int>(sizeof(ItemConst) / 4);
+    for (int i = tid; i < words; i += kSortThreads)
+      reinterpret_cast<uint32_t*>(s_ic)[i] = reinterpret_cast<const uint32_t*>(src.ic)[i];
+    __syncthreads();
+  }
+
+  int cur = 0;  // buffer that holds the references in the current order
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * bits;
+    // ---- how many references of this share have each digit
+    for (int d = tid; d < digits; d += kSortThreads) s_base[d] = 0;
+    __syncthreads();
+    for (uint32_t i = lo + tid; i < hi; i += kSortThreads) {
+      uint32_t key;
+      if (p == 0) {
+        if constexpr (HASHED) {
+          const uint32_t tok = i / src.items;
+          uint64_t hs;
+          key = item_row(s_ic[i - tok * src.items], src.mode, src.tokens, src.canon_map, src.vocab, tok, tok % src.L,
+                         src.err, &hs);
+          b.sign[i] = hs;
+        } else {
+          key = embed_row(src.tokens, src.canon_map, src.vocab, src.rows, i);
+          if (key == kNoRow) {
+            key = src.rows;
+            if (src.err) atomicMin(reinterpret_cast<unsigned int*>(src.err), i);
+          }
+        }
+        b.key[0][i] = key;
+      } else {
+        key = __ldcg(b.key[cur] + i);
+      }
+      atomicAdd(&s_base[(key >> shift) & mask], 1u);
+    }
+    __syncthreads();
+    for (int d = tid; d < digits; d += kSortThreads) b.hist[d * G + blockIdx.x] = s_base[d];
+    if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+
+    // ---- per digit: exclusive scan of its counts over the blocks, and its total
+    for (int d = blockIdx.x * kSortWarps + warp; d < digits; d += G * kSortWarps) {
+      uint32_t run = 0;
+      for (uint32_t k0 = 0; k0 < G; k0 += 32) {
+        const uint32_t k = k0 + lane;
+        const uint32_t v = k < G ? __ldcg(b.hist + d * G + k) : 0u;
+        const uint32_t inc = warp_incl_scan(v, lane);
+        if (k < G) b.hist[d * G + k] = run + inc - v;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) b.totals[d] = run;
+    }
+    if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+
+    // ---- where this block's first reference of each digit goes
+    uint32_t carry = 0;
+    for (int d0 = 0; d0 < digits; d0 += kSortThreads) {
+      const int d = d0 + tid;
+      const uint32_t v = d < digits ? __ldcg(b.totals + d) : 0u;
+      uint32_t total;
+      const uint32_t ex = block_excl_scan(v, s_warp, &total);
+      if (d < digits) s_base[d] = carry + ex + __ldcg(b.hist + d * G + blockIdx.x);
+      carry += total;
+    }
+
+    // ---- scatter, tile by tile; a warp holds 32 * items consecutive references
+    for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
+      const uint32_t left = min(hi - t0, static_cast<uint32_t>(kSortTile));
+      const int items = static_cast<int>((left + kSortThreads - 1) / kSortThreads);
+      uint32_t key[kSortItems], ref[kSortItems], rank[kSortItems];
+      const uint32_t first = t0 + warp * 32 * items;
+#pragma unroll
+      for (int j = 0; j < kSortItems; ++j) {
+        const uint32_t i = first + j * 32 + lane;
+        const bool in = j < items && i < t0 + left;
+        key[j] = in ? __ldcg(b.key[cur] + i) : 0u;
+        ref[j] = in ? (p == 0 ? i : __ldcg(b.ref[cur] + i)) : 0u;
+      }
+      __syncthreads();  // the previous tile is done with s_cnt and s_base
+      uint32_t* clear = reinterpret_cast<uint32_t*>(s_cnt);
+      for (int w = tid; w < kSortWarps * digits / 2; w += kSortThreads) clear[w] = 0;
+      __syncthreads();
+      uint16_t* cnt = s_cnt + warp * digits;
+#pragma unroll
+      for (int j = 0; j < kSortItems; ++j) {
+        const bool in = j < items && first + j * 32 + lane < t0 + left;
+        const uint32_t dig = (key[j] >> shift) & mask;
+        uint32_t peers = __ballot_sync(0xffffffffu, in);
+        for (int q = 0; q < bits; ++q) {
+          const bool bit = (dig >> q) & 1u;
+          const uint32_t set = __ballot_sync(0xffffffffu, bit);
+          peers &= bit ? set : ~set;
+        }
+        const uint32_t before = in ? cnt[dig] : 0u;
+        rank[j] = before + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (in && lane == 31 - __clz(peers)) cnt[dig] = static_cast<uint16_t>(before + __popc(peers));
+        __syncwarp();
+      }
+      __syncthreads();
+      // per digit: the tile's counts over its warps become offsets
+      uint32_t tile_total[kMaxDigits / kSortThreads];
+#pragma unroll
+      for (int q = 0; q < kMaxDigits / kSortThreads; ++q) {
+        const int d = q * kSortThreads + tid;
+        uint32_t run = 0;
+        if (d < digits) {
+#pragma unroll
+          for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = s_cnt[w * digits + d];
+            s_cnt[w * digits + d] = static_cast<uint16_t>(run);
+            run += c;
+          }
+        }
+        tile_total[q] = run;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kSortItems; ++j) {
+        if (j < items && first + j * 32 + lane < t0 + left) {
+          const uint32_t dig = (key[j] >> shift) & mask;
+          const uint32_t to = s_base[dig] + cnt[dig] + rank[j];
+          b.key[cur ^ 1][to] = key[j];
+          b.ref[cur ^ 1][to] = ref[j];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kMaxDigits / kSortThreads; ++q) {
+        const int d = q * kSortThreads + tid;
+        if (d < digits) s_base[d] += tile_total[q];
+      }
+    }
+    cur ^= 1;
+    if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+  }
+
+  // ---- segments of equal rows; the embedding's padding (key = rows) sorts last and has none
+  const uint32_t* key = b.key[cur];
+  const uint32_t none = HASHED ? kNoRow : src.rows;
+  auto starts = [&](uint32_t i) {
+    const uint32_t k = __ldcg(key + i);
+    return k != none && (i == 0 || __ldcg(key + i - 1) != k);
+  };
+  uint32_t mine = 0, total;
+  for (uint32_t i = lo + tid; i < hi; i += kSortThreads) mine += starts(i);
+  block_excl_scan(mine, s_warp, &total);
+  if (tid == 0) b.segs[blockIdx.x] = total;
+  if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+  __shared__ uint32_t s_first;
+  const uint32_t ex = block_excl_scan(tid < G ? __ldcg(b.segs + tid) : 0u, s_warp, &total);
+  if (tid == blockIdx.x) s_first = ex;
+  __syncthreads();
+  const uint32_t count = total;
+  uint32_t u0 = s_first;
+  uint32_t* rows_of = HASHED ? rows_out : b.seg_row;
+  for (uint32_t t0 = lo; t0 < hi; t0 += kSortThreads) {
+    const uint32_t i = t0 + tid;
+    const bool st = i < hi && starts(i);
+    uint32_t in_tile;
+    const uint32_t u = u0 + block_excl_scan(st, s_warp, &in_tile);
+    if (i < hi) {
+      const uint32_t k = __ldcg(key + i);
+      if (st) {
+        rows_of[u] = k;
+        b.seg_start[u] = i;
+      }
+      if (k != none && (i + 1 == n || __ldcg(key + i + 1) == none)) b.seg_start[count] = i + 1;
+      if (HASHED && i >= count) rows_out[i] = kNoRow;
+    }
+    u0 += in_tile;
+  }
+  if (tid == 0) {
+    if (blockIdx.x == 0) {
+      if (count == 0) b.seg_start[0] = 0;
+      b.ctrl->count = count;
+      if (count_out) *count_out = static_cast<int32_t>(count);
+    }
+    atomicAdd(&b.ctrl->done, 1u);
+  }
+}
+
+// ------------------------------------------------------------------------------- the sums
+
+struct SumArgs {
+  const void* grad;          // summands, rows of r values; reference i has row i / share
+  const uint64_t* sign;      // sign hashes of the references, or null
+  const uint32_t* ref;       // references in sorted order
+  const uint32_t* seg_start;
+  const uint32_t* seg_row;   // output row of a segment; null: the segment's number
+  const SortCtrl* ctrl;
+  void* out;
+  uint32_t n, share, blocks; // blocks: of the sort (all have to have finished)
+  int32_t r, accumulate;
+  float scale;
+};
+
+// One warp per segment and 32 * COLS columns.
+template <int IN, int OUT, int COLS>
+__global__ void __launch_bounds__(256) rowgrad_sum_kernel(SumArgs a) {
+  if (a.ctrl->done != a.blocks) return;
+  const int lane = threadIdx.x & 31;
+  const uint32_t u = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int c = (blockIdx.y * 32 + lane) * COLS;
+  const uint32_t count = a.ctrl->count;
+  if (c >= a.r || u >= (a.seg_row ? count : a.n)) return;
+  float acc[COLS] = {};
+  if (u < count) {
+    const uint32_t end = a.seg_start[u + 1];
+    for (uint32_t i = a.seg_start[u]; i < end; ++i) {
+      const uint32_t ref = a.ref[i];
+      float x[COLS];
+      load_cols<IN, COLS>(a.grad, static_cast<int64_t>(ref / a.share) * a.r + c, x);
+      uint32_t neg = 0;
+      if (a.sign) neg = static_cast<uint32_t>(mix64(a.sign[ref] + kGolden * ((c >> 6) + 1)) >> (c & 63));
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] += ((neg >> j) & 1u) ? -x[j] : x[j];
+    }
+  }
+  const int64_t at = static_cast<int64_t>(a.seg_row ? a.seg_row[u] : u) * a.r + c;
+  float y[COLS] = {};
+  if (a.accumulate) load_cols<OUT, COLS>(a.out, at, y);
+#pragma unroll
+  for (int j = 0; j < COLS; ++j) y[j] = fmaf(acc[j], a.scale, y[j]);
+  store_cols<OUT, COLS>(a.out, at, y);
+}
+
+using SumFn = void (*)(SumArgs);
+
+template <int COLS>
+SumFn sum_fn(int in, int out) {
+  if (in == PG_F32)
+    return out == PG_F32 ? rowgrad_sum_kernel<PG_F32, PG_F32, COLS> : rowgrad_sum_kernel<PG_F32, PG_BF16, COLS>;
+  return out == PG_F32 ? rowgrad_sum_kernel<PG_BF16, PG_F32, COLS> : rowgrad_sum_kernel<PG_BF16, PG_BF16, COLS>;
+}
+
+// Sorts the references and writes the sums. n >= 1; `keys` the largest key.
+template <bool HASHED>
+pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs a, int in, int out, void* workspace,
+                        uint32_t* rows_out, int32_t* count_out, cudaStream_t stream) {
+  SortBuffers b;
+  carve(static_cast<uint8_t*>(workspace), n, HASHED, &b);
+  int key_bits = 1;
+  while (key_bits < 32 && (keys >> key_bits)) ++key_bits;
+  const int passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
+  const int bits = (key_bits + passes - 1) / passes;
+  uint32_t G = (n + kRefsPerBlock - 1) / kRefsPerBlock;
+  G = min(G, static_cast<uint32_t>(min(sm_count(), kMaxSortBlocks)));
+  uint32_t share = (n + G - 1) / G;
+  G = (n + share - 1) / share;
+
+  cudaError_t e = cudaMemsetAsync(b.ctrl, 0, kCtrlBytes, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  auto sort = rowgrad_sort_kernel<HASHED>;
+  const int smem = kSortWarps * kMaxDigits * 2 + kMaxDigits * 4;
+  e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(G);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // the blocks meet at a grid barrier
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, share, passes, bits, rows_out, count_out, device_error_word());
+  if (e != cudaSuccess) return cuda_fail(e);
+  pg_status st = after_launch(1);
+  if (st != PG_OK) return st;
+
+  a.ref = b.ref[passes & 1];
+  a.seg_start = b.seg_start;
+  a.seg_row = b.seg_row;
+  a.sign = b.sign;
+  a.ctrl = b.ctrl;
+  a.n = n;
+  a.blocks = G;
+  const bool vec = a.r % 8 == 0 && aligned(a.grad, 16) && aligned(a.out, 16);
+  const int cols = 32 * (vec ? 8 : 1);
+  const uint32_t segs = HASHED ? n : min(n, keys);
+  const dim3 grid((segs + 7) / 8, (a.r + cols - 1) / cols);
+  (vec ? sum_fn<8>(in, out) : sum_fn<1>(in, out))<<<grid, 256, 0, stream>>>(a);
+  return after_launch(1);
+}
+
+}  // namespace
+}  // namespace pg
+
+using namespace pg;
+
+extern "C" pg_status pg_embed_grad_workspace_size(int64_t N, int64_t rows, int32_t d, size_t* bytes) {
+  if (!bytes) return PG_ERR_NULL;
+  if (N < 0 || N >= (1ll << 31) || rows < 1 || rows >= (1ll << 31) || d < 1 || d > kMaxEmbedWidth)
+    return PG_ERR_SHAPE;
+  SortBuffers b;
+  *bytes = N == 0 ? 0 : carve(nullptr, N, false, &b);
+  return PG_OK;
+}
+
+extern "C" pg_status pg_embed_grad(const int32_t* tokens, int64_t N, uint32_t vocab, const uint32_t* canon_map,
+                                   const void* grad_out, int32_t grad_dtype, int64_t rows, int32_t d, float scale,
+                                   int32_t accumulate, void* grad_table, int32_t table_dtype, void* workspace,
+                                   size_t workspace_bytes, int32_t* err_index, pg_stream_t stream) {
+  size_t need;
+  if (vocab == 0) return PG_ERR_SHAPE;
+  pg_status st = pg_embed_grad_workspace_size(N, rows, d, &need);
+  if (st != PG_OK) return st;
+  if (!real_dtype(grad_dtype) || !real_dtype(table_dtype)) return PG_ERR_DTYPE;
+  if (!grad_table || (N > 0 && (!tokens || !grad_out))) return PG_ERR_NULL;
+  if (!aligned(tokens, 4) || !aligned(canon_map, 4) || !aligned(err_index, 4) ||
+      !aligned(grad_out, dtype_bytes(grad_dtype)) || !aligned(grad_table, dtype_bytes(table_dtype)) ||
+      !aligned(workspace, 16))
+    return PG_ERR_ALIGN;
+  if (workspace_bytes < need || (need && !workspace)) return PG_ERR_WORKSPACE;
+  if (device_cc() != 103) return PG_ERR_DEVICE;
+  st = prepare_err(err_index, stream);
+  if (st != PG_OK) return st;
+  if (!accumulate) {
+    const size_t bytes = static_cast<size_t>(rows) * d * dtype_bytes(table_dtype);
+    cudaError_t e = cudaMemsetAsync(grad_table, 0, bytes, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (N == 0) return PG_OK;
+  RefSource src = {};
+  src.tokens = tokens;
+  src.canon_map = canon_map;
+  src.err = err_index;
+  src.vocab = vocab;
+  src.rows = static_cast<uint32_t>(rows);
+  SumArgs a = {};
+  a.grad = grad_out;
+  a.out = grad_table;
+  a.share = 1;
+  a.r = d;
+  a.accumulate = accumulate;
+  a.scale = scale;
+  return row_gradients<false>(src, static_cast<uint32_t>(N), src.rows, a, grad_dtype, table_dtype, workspace, nullptr,
+                              nullptr, stream);
+}
+
+extern "C" pg_status pg_lookup_grad_workspace_size(const pg_table_desc* desc, int64_t N, size_t* bytes) {
+  if (!bytes) return PG_ERR_NULL;
+  Geometry g;
+  pg_status st = validate_desc(desc, &g);
+  if (st != PG_OK) return st;
+  if (N < 0 || N * g.O * g.H >= (1ll << 31)) return PG_ERR_SHAPE;
+  SortBuffers b;
+  *bytes = N == 0 ? 0 : carve(nullptr, N * g.O * g.H, true, &b);
+  return PG_OK;
+}
+
+extern "C" pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32_t B, int32_t L,
+                                    const uint32_t* canon_map, const void* grad_e, int32_t grad_dtype,
+                                    uint32_t* rows_out, void* grads_out, int32_t out_dtype, int32_t* count_out,
+                                    void* workspace, size_t workspace_bytes, int32_t* err_index, pg_stream_t stream) {
+  Geometry g;
+  pg_status st = validate_desc(desc, &g);
+  if (st != PG_OK) return st;
+  if (desc->hash_kind != PG_HASH_MULXOR) return PG_ERR_UNSUPPORTED;
+  if (B < 0 || L < 0) return PG_ERR_SHAPE;
+  const int items = g.O * g.H;
+  if (items > kHashItems || desc->r > kMaxEmbedWidth) return PG_ERR_UNSUPPORTED;
+  const int64_t N = static_cast<int64_t>(B) * L;
+  if (N >= (1ll << 31)) return PG_ERR_SHAPE;
+  size_t need;
+  st = pg_lookup_grad_workspace_size(desc, N, &need);
+  if (st != PG_OK) return st;
+  if (!real_dtype(grad_dtype) || !real_dtype(out_dtype)) return PG_ERR_DTYPE;
+  if (!count_out || (N > 0 && (!tokens || !grad_e || !rows_out || !grads_out))) return PG_ERR_NULL;
+  if (!aligned(tokens, 4) || !aligned(canon_map, 4) || !aligned(err_index, 4) || !aligned(rows_out, 4) ||
+      !aligned(count_out, 4) || !aligned(grad_e, dtype_bytes(grad_dtype)) ||
+      !aligned(grads_out, dtype_bytes(out_dtype)) || !aligned(workspace, 16))
+    return PG_ERR_ALIGN;
+  if (workspace_bytes < need || (need && !workspace)) return PG_ERR_WORKSPACE;
+  if (device_cc() != 103) return PG_ERR_DEVICE;
+  st = prepare_err(err_index, stream);
+  if (st != PG_OK) return st;
+  if (N == 0) {
+    cudaError_t e = cudaMemsetAsync(count_out, 0, sizeof(int32_t), stream);
+    return e == cudaSuccess ? PG_OK : cuda_fail(e);
+  }
+  RefSource src = {};
+  src.tokens = tokens;
+  src.canon_map = canon_map;
+  src.err = err_index;
+  src.vocab = desc->vocab;
+  src.L = static_cast<uint32_t>(L);
+  src.items = items;
+  src.mode = desc->mode;
+  HashParams P;
+  fill_hash_params(desc, g, &P);
+  for (int i = 0; i < items; ++i) init_item_const(src.ic[i], P, desc->hash_seed, i);
+  SumArgs a = {};
+  a.grad = grad_e;
+  a.out = grads_out;
+  a.share = desc->mode == PG_FLAT ? static_cast<uint32_t>(items) : 1u;
+  a.r = desc->r;
+  a.scale = 1.f;
+  return row_gradients<true>(src, static_cast<uint32_t>(N * items), static_cast<uint32_t>(g.rows - 1), a, grad_dtype,
+                             out_dtype, workspace, rows_out, count_out, stream);
+}

@@ -1,0 +1,83 @@
+// Small helpers of the training calls: fp32 values of 8 (or 1) consecutive columns of an fp32
+// or bf16 array, the embedding's row of a position, and the host checks they share.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "pg_internal.cuh"
+
+namespace pg {
+namespace {
+
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+constexpr int kMaxEmbedWidth = 1 << 20;  // columns of an embedding row
+
+inline bool real_dtype(int dtype) { return dtype == PG_F32 || dtype == PG_BF16; }
+inline size_t dtype_bytes(int dtype) { return dtype == PG_F32 ? 4 : 2; }
+inline bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// Table row of position t, or kNoRow for padding (a token outside [0, vocab), or a canonical
+// ID that the table does not have).
+__device__ __forceinline__ uint32_t embed_row(const int32_t* __restrict__ tokens,
+                                              const uint32_t* __restrict__ canon_map, uint32_t vocab, uint32_t rows,
+                                              int64_t t) {
+  const uint32_t x = static_cast<uint32_t>(__ldg(tokens + t));  // negative: not below vocab <= 2^31
+  if (x >= vocab || x >= 0x80000000u) return kNoRow;
+  const uint32_t row = canon_map ? __ldg(canon_map + x) : x;
+  return row < rows ? row : kNoRow;
+}
+
+// 8 columns with 16-byte accesses (the address is 16-byte aligned), or 1.
+template <int DT, int COLS>
+__device__ __forceinline__ void load_cols(const void* __restrict__ base, int64_t at, float (&x)[COLS]) {
+  static_assert(COLS == 1 || COLS == 8, "");
+  if constexpr (DT == PG_F32) {
+    const float* p = static_cast<const float*>(base) + at;
+    if constexpr (COLS == 1) {
+      x[0] = __ldg(p);
+    } else {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if constexpr (COLS == 1) {
+      x[0] = __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+    } else {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+      x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+      x[4] = __uint_as_float(w.z << 16); x[5] = __uint_as_float(w.z & 0xFFFF0000u);
+      x[6] = __uint_as_float(w.w << 16); x[7] = __uint_as_float(w.w & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+template <int DT, int COLS>
+__device__ __forceinline__ void store_cols(void* base, int64_t at, const float (&x)[COLS]) {
+  if constexpr (DT == PG_F32) {
+    float* p = static_cast<float*>(base) + at;
+    if constexpr (COLS == 1) {
+      *p = x[0];
+    } else {
+      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+  } else {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at;
+    if constexpr (COLS == 1)
+      *p = __float2bfloat16_rn(x[0]);
+    else
+      *reinterpret_cast<uint4*>(p) = make_uint4(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]),
+                                                two_bf16(x[6], x[7]));
+  }
+}
+
+}  // namespace
+}  // namespace pg

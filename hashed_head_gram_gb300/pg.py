@@ -173,6 +173,21 @@ def _load():
     L.pg_row_copy_window.argtypes = [u32, ctypes.POINTER(u32)]
     L.pg_row_copy.restype = ctypes.c_int
     L.pg_row_copy.argtypes = [vp, u64, u32, vp, ctypes.c_int64, vp, u32, vp]
+    i64 = ctypes.c_int64
+    L.pg_embed.restype = ctypes.c_int
+    L.pg_embed.argtypes = [vp, i64, u32, vp, vp, i32, i64, i32, f32, vp, i32, vp, vp]
+    L.pg_embed_grad_workspace_size.restype = ctypes.c_int
+    L.pg_embed_grad_workspace_size.argtypes = [i64, i64, i32, ctypes.POINTER(sz)]
+    L.pg_embed_grad.restype = ctypes.c_int
+    L.pg_embed_grad.argtypes = [vp, i64, u32, vp, vp, i32, i64, i32, f32, i32, vp, i32, vp, sz, vp, vp]
+    L.pg_lookup_grad_workspace_size.restype = ctypes.c_int
+    L.pg_lookup_grad_workspace_size.argtypes = [dp, i64, ctypes.POINTER(sz)]
+    L.pg_lookup_grad.restype = ctypes.c_int
+    L.pg_lookup_grad.argtypes = [dp, vp, i32, i32, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp, vp]
+    L.pg_orthogonalize_workspace_size.restype = ctypes.c_int
+    L.pg_orthogonalize_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+    L.pg_orthogonalize.restype = ctypes.c_int
+    L.pg_orthogonalize.argtypes = [vp, i32, i32, i32, i32, i32, f32, f32, f32, f32, f32, vp, vp, sz, vp]
     return L
 
 
@@ -563,3 +578,105 @@ __all__ = ["PgError", "TableDesc", "table_desc", "table_geometry", "canon_hash",
            "row_copy_window", "row_copy", "lib",
            "FLAT", "ENGRAM", "PAGEGRAM", "F32", "BF16", "NF4", "GATE_NONE", "GATE_SCALAR", "GATE_CONTEXT",
            "HASH_MULXOR", "HASH_TOY", "PG_NO_ROW"]
+
+
+# ------------------------------------------------------------------------------ training
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"dtype {t.dtype} is not float32 or bfloat16")
+    return _DTYPES[t.dtype]
+
+
+def _expect(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ids(tokens: torch.Tensor, canon_map: Optional[torch.Tensor], vocab: int, err_index: Optional[torch.Tensor]):
+    _expect(tokens.dtype == torch.int32, "tokens must be int32")
+    _expect(canon_map is None or (canon_map.element_size() == 4 and canon_map.numel() >= vocab),
+            "canon_map must hold a 32-bit ID for each of the vocab tokens")
+    _expect(err_index is None or (err_index.dtype == torch.int32 and err_index.numel() >= 1),
+            "err_index must be an int32 tensor")
+
+
+def embed(tokens: torch.Tensor, table: torch.Tensor, out: torch.Tensor, vocab: int, scale: float = 1.0,
+          canon_map: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
+    """out[t] = scale * table[canon(tokens[t])]; tokens int32 of any shape, table [rows, d],
+    out [tokens.numel(), d] (or tokens.shape + (d,))."""
+    rows, d = table.shape
+    N = tokens.numel()
+    _ids(tokens, canon_map, vocab, err_index)
+    _expect(out.numel() == N * d and out.shape[-1] == d, "out must hold one row of table's width per token")
+    _check(_lib.pg_embed(_ptr(tokens), N, vocab, _ptr(canon_map), _ptr(table), _dtype(table), rows, d, scale, _ptr(out),
+                         _dtype(out), _ptr(err_index), _stream(stream)), "pg_embed")
+
+
+def embed_grad_workspace_size(N: int, rows: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pg_embed_grad_workspace_size(N, rows, d, ctypes.byref(n)), "pg_embed_grad_workspace_size")
+    return n.value
+
+
+def embed_grad(tokens: torch.Tensor, grad_out: torch.Tensor, grad_table: torch.Tensor, vocab: int,
+               workspace: Optional[torch.Tensor], scale: float = 1.0, accumulate: bool = False,
+               canon_map: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
+    """grad_table[v] = scale * sum of the rows of grad_out whose token has canonical ID v
+    (added to what is there when accumulate is set)."""
+    rows, d = grad_table.shape
+    N = tokens.numel()
+    _ids(tokens, canon_map, vocab, err_index)
+    _expect(grad_out.numel() == N * d and grad_out.shape[-1] == d, "grad_out must hold one row of the table's width per token")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_embed_grad(_ptr(tokens), N, vocab, _ptr(canon_map), _ptr(grad_out), _dtype(grad_out), rows, d, scale,
+                              1 if accumulate else 0, _ptr(grad_table), _dtype(grad_table), _ptr(workspace), ws_bytes,
+                              _ptr(err_index), _stream(stream)), "pg_embed_grad")
+
+
+def lookup_grad_workspace_size(desc: TableDesc, N: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pg_lookup_grad_workspace_size(ctypes.byref(desc), N, ctypes.byref(n)), "pg_lookup_grad_workspace_size")
+    return n.value
+
+
+def lookup_grad(desc: TableDesc, tokens: torch.Tensor, grad_e: torch.Tensor, rows_out: torch.Tensor,
+                grads_out: torch.Tensor, count_out: torch.Tensor, workspace: Optional[torch.Tensor],
+                canon_map: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
+    """The hashed table's gradient: rows_out (int32 or uint32 [n], n = tokens.numel() * heads per token) the
+    distinct rows read, ascending, then PG_NO_ROW; grads_out [n, r] their gradients, then zeros;
+    count_out int32 [1]."""
+    B, L = tokens.shape
+    heads = desc.num_orders * (1 if desc.mode == FLAT else desc.K)
+    n, width = B * L * heads, (1 if desc.mode == FLAT else heads) * desc.r
+    _ids(tokens, canon_map, desc.vocab, err_index)
+    _expect(grad_e.numel() == B * L * width and grad_e.shape[-1] == width, "grad_e must be [B * L, e_width]")
+    _expect(rows_out.element_size() == 4 and rows_out.numel() == n, "rows_out must hold one 32-bit row per read")
+    _expect(grads_out.numel() == n * desc.r and grads_out.shape[-1] == desc.r, "grads_out must hold one row of width r per read")
+    _expect(count_out.dtype == torch.int32 and count_out.numel() >= 1, "count_out must be an int32 tensor")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_lookup_grad(ctypes.byref(desc), _ptr(tokens), B, L, _ptr(canon_map), _ptr(grad_e), _dtype(grad_e),
+                               _ptr(rows_out), _ptr(grads_out), _dtype(grads_out), _ptr(count_out), _ptr(workspace),
+                               ws_bytes, _ptr(err_index), _stream(stream)), "pg_lookup_grad")
+
+
+def orthogonalize_workspace_size(batch: int, m: int, n: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.pg_orthogonalize_workspace_size(batch, m, n, ctypes.byref(b)), "pg_orthogonalize_workspace_size")
+    return b.value
+
+
+def orthogonalize(G: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, steps: int = 5,
+                  coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0, stream=None):
+    """out (bf16) = scale * the orthogonalised G [m, n] or [batch, m, n] after `steps` Newton-Schulz steps."""
+    _expect(G.dim() in (2, 3) and out.shape == G.shape, "G and out must both be [m, n] or [batch, m, n]")
+    _expect(out.dtype == torch.bfloat16, "out must be bfloat16")
+    batch = G.shape[0] if G.dim() == 3 else 1
+    m, n = G.shape[-2:]
+    a, b, c = coeffs
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_orthogonalize(_ptr(G), _dtype(G), batch, m, n, steps, a, b, c, eps, scale, _ptr(out), _ptr(workspace),
+                                 ws_bytes, _stream(stream)), "pg_orthogonalize")

@@ -138,7 +138,8 @@ uint64_t pg_launch_count(void);
  * group too large to compare pairwise; those n-grams or pairs were left out), and of
  * pg_selftest_bounded_waits (2048, 4096), and of pg_project_gate_conv (16384 = a conv item's wait
  * for the tiles of its m-blocks), and of pg_decode_step (32768 = a block's wait at the grid
- * barrier, 65536 = a wait for a row of W).
+ * barrier, 65536 = a wait for a row of W), and of the training calls (131072 = the gradients'
+ * grid barrier, 262144 = a wait of pg_orthogonalize's products).
  * Synchronizes the device. With clear != 0 the word is reset to 0.
  */
 pg_status pg_device_error(int32_t* code, int32_t clear);
@@ -637,6 +638,101 @@ pg_status pg_collision_counts_workspace_size(int64_t n, uint32_t row0_span, size
 pg_status pg_collision_counts(const uint32_t* rows, int64_t n, int32_t K, int64_t stride, uint32_t row0_lo,
                               uint32_t row0_span, uint64_t* counts_out, void* workspace, size_t workspace_bytes,
                               pg_stream_t stream);
+
+/*
+ * Training (PageGram report 9.4, check 4: sparse row gradients equal dense ones): the token
+ * embedding under the memory with its gradient, the gradient of the hashed table, and the
+ * orthogonalised update of the projection's matrices. The hashed lookup's forward pass is
+ * pg_gather_sign_concat; the projection's own gradients are plain matrix products.
+ *
+ * The gradients add what belongs to one row in fp32, in an order that depends on the inputs
+ * alone (references in ascending order, split at fixed places), so equal inputs give equal
+ * bits. A device wait of these calls that runs out sets device error bit 131072 (the grid
+ * barrier of the gradients' sort) or 262144 (the products of pg_orthogonalize); the call's
+ * outputs are then undefined.
+ *
+ * pg_embed -- out[t] = scale * table[c(x_t)] with c the canonical map (identity when NULL):
+ * the input rows of the model the memory plugs into.
+ *  tokens     device int32 [N], 4-byte aligned
+ *  vocab      V: token IDs lie in [0, V); canon_map device uint32 [V] or NULL
+ *  table      device [rows, d], PG_F32 or PG_BF16, aligned to its element
+ *  out        device [N, d], PG_F32 or PG_BF16, aligned to its element; must not overlap table.
+ *             The product is rounded once to fp32 and once to out_dtype
+ *  err_index  device int32 [1], or NULL: the smallest t whose token is outside [0, V) or whose
+ *             canonical ID is not below `rows`, else -1. Such a position is padding: its row of
+ *             `out` is zero and it has no gradient (use -1 for padding on purpose).
+ * 1 <= rows < 2^31, 1 <= d <= 2^20, 0 <= N < 2^31; N == 0 enqueues nothing. d % 8 == 0 with 16-byte
+ * aligned table and out takes 16-byte accesses.
+ */
+pg_status pg_embed(const int32_t* tokens, int64_t N, uint32_t vocab, const uint32_t* canon_map, const void* table,
+                   int32_t table_dtype, int64_t rows, int32_t d, float scale, void* out, int32_t out_dtype,
+                   int32_t* err_index, pg_stream_t stream);
+
+/*
+ * pg_embed_grad -- the gradient of pg_embed with respect to its table:
+ *   grad_table[v] = scale * sum over t with c(x_t) = v of grad_out[t]        (accumulate == 0)
+ *   grad_table[v] += that sum, for the rows that the tokens name only        (accumulate != 0)
+ * Without accumulate every row is written (zero where no token names it).
+ *  grad_out    device [N, d], PG_F32 or PG_BF16; grad_table device [rows, d], PG_F32 or PG_BF16;
+ *              aligned to their elements; they must not overlap
+ *  tokens, vocab, canon_map, rows, d, scale, err_index, padding as in pg_embed
+ *  workspace   device, 16-byte aligned, >= pg_embed_grad_workspace_size bytes, scratch
+ * N == 0 with accumulate == 0 writes zeros.
+ */
+pg_status pg_embed_grad_workspace_size(int64_t N, int64_t rows, int32_t d, size_t* bytes);
+
+pg_status pg_embed_grad(const int32_t* tokens, int64_t N, uint32_t vocab, const uint32_t* canon_map,
+                        const void* grad_out, int32_t grad_dtype, int64_t rows, int32_t d, float scale,
+                        int32_t accumulate, void* grad_table, int32_t table_dtype, void* workspace,
+                        size_t workspace_bytes, int32_t* err_index, pg_stream_t stream);
+
+/*
+ * pg_lookup_grad -- the gradient of pg_gather_sign_concat with respect to its table, as the
+ * distinct rows that the batch read and one gradient row for each: with the n = B L O H reads
+ * (t, o, k) of rows row(t, o, k) under sign masks s(t, o, k),
+ *   grads_out[u] = sum over reads of row rows_out[u] of s(t, o, k) * g(t, o, k)
+ * where g(t, o, k) is columns (o K + k) r .. + r of grad_e[t] (flat: all of grad_e[t], for
+ * every order).
+ *  desc, tokens, B, L, canon_map, err_index   as in pg_gather_sign_concat (row_dtype does not
+ *              matter here; a token outside [0, vocab) is read as ID 0, as the lookup reads it)
+ *  grad_e      device [B*L, e_width], PG_F32 or PG_BF16, aligned to its element
+ *  rows_out    device uint32 [n]: the distinct rows in ascending order, then PG_NO_ROW
+ *  grads_out   device [n, r], PG_F32 or PG_BF16: their gradients, then zeros (so both arrays can
+ *              be used whole, without the count having to reach the host)
+ *  count_out   device int32 [1]: how many distinct rows there are
+ *  workspace   device, 16-byte aligned, >= pg_lookup_grad_workspace_size bytes, scratch
+ * n < 2^31; O * H <= 32 and r <= 2^20 (else PG_ERR_UNSUPPORTED); PG_HASH_TOY is PG_ERR_UNSUPPORTED. B*L == 0
+ * writes a zero count. r % 8 == 0 with 16-byte aligned grad_e and grads_out takes 16-byte
+ * accesses.
+ */
+pg_status pg_lookup_grad_workspace_size(const pg_table_desc* desc, int64_t N, size_t* bytes);
+
+pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32_t B, int32_t L,
+                         const uint32_t* canon_map, const void* grad_e, int32_t grad_dtype, uint32_t* rows_out,
+                         void* grads_out, int32_t out_dtype, int32_t* count_out, void* workspace,
+                         size_t workspace_bytes, int32_t* err_index, pg_stream_t stream);
+
+/*
+ * pg_orthogonalize -- the orthogonalised update of `batch` matrices [m, n] by Newton-Schulz
+ * steps (the projection's [W_V; W_K^(1..M)] is M + 1 of them, stored one after the other):
+ *   X = G / (|G|_F + eps); `steps` times: A = X X^T, X <- a X + (b A + c A A) X;  out = scale X
+ * computed on the shorter side (m > n: on G^T). With the usual a, b, c = 3.4445, -4.7750,
+ * 2.0315 five steps bring every singular value that started above ~1 % into about [0.7, 1.2].
+ *  G    device [batch, m, n], PG_F32 or PG_BF16, aligned to its element
+ *  out  device bf16 [batch, m, n], 2-byte aligned; may be G itself when G is bf16
+ * The products run on the tensor cores with fp16 operands and fp32 sums: X, A and b A + c A A
+ * are stored scaled by 2^10 in fp16 between them (11 significant bits: three more than the
+ * result's; the scale puts magnitudes 6e-8 .. 63 into fp16's normal range, where a norm of at
+ * most 1 and the usual coefficients keep them below 3).
+ * A zero matrix gives zeros; infinities and NaN in G make its own matrix NaN.
+ *  1 <= m, n <= 16384; 0 <= batch <= 4096; 1 <= steps <= 32; workspace device, 16-byte aligned,
+ *  >= pg_orthogonalize_workspace_size bytes, scratch. batch == 0 enqueues nothing.
+ */
+pg_status pg_orthogonalize_workspace_size(int32_t batch, int32_t m, int32_t n, size_t* bytes);
+
+pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batch, int32_t m, int32_t n, int32_t steps, float a,
+                           float b, float c, float eps, float scale, void* out, void* workspace,
+                           size_t workspace_bytes, pg_stream_t stream);
 
 /*
  * Diagnostic, no counterpart on the pages: the memory access pattern of a lookup on its
