@@ -5,7 +5,7 @@
 // and a wide row is read by consecutive warps; each lane has up to four 16-byte loads in
 // flight (fp32: eight) before it stores.
 #include "pg_hash.cuh"
-#include "pg_vec.cuh"
+#include "pg_vec.h"
 
 namespace pg {
 namespace {

@@ -7,64 +7,307 @@
 //   X  <- a X + Bm X       [p, q]
 // Each is D = alpha P Q^T + beta C with P and Q row-major: X is kept in both orientations (XT
 // [q, p] is the second operand of the last product), and the symmetric matrices are their own
-// transposes. So one kernel does all three; it writes a tile where it belongs and, transposed,
+// transposes. So one code does all three; it writes a tile where it belongs and, transposed,
 // in the second array, which for the symmetric products is the mirrored tile of the same
 // matrix: their tiles below the diagonal are never computed.
 //
 // Between the products X, A and Bm are held as fp16 scaled by 2^10 (pg.h): 11 significant
 // bits, against the 8 of the bf16 result.
+//
+// One cooperative launch does the whole update: norm, scaling, and 3 * steps products on the
+// tensor cores, the blocks meeting at a grid barrier between them. The intermediate matrices
+// stay in L2 where they fit (a step reads each of them once per tile row or column).
+//   warp 0      TMA producer: 64-column k-blocks of P and Q, 128-byte swizzle, into a ring
+//   warp 1      tcgen05.mma issuer, two accumulators in TMEM
+//   warps 2..9  epilogue: tcgen05.ld, alpha / beta / C, fp16 in both orientations
+#include <cuda.h>
 #include <cuda_fp16.h>
 
-#include "pg_vec.cuh"
+#include <algorithm>
+#include <atomic>
+
+#include "pg_async.cuh"
+#include "pg_vec.h"
 
 namespace pg {
 namespace {
 
+constexpr int kErrOrtho = 262144;       // device error bit: a wait of this kernel gave up
 constexpr int kMaxSide = 16384;
 constexpr int kMaxBatch = 4096;
 constexpr float kHold = 1024.f;         // X, A and Bm are stored times 2^10
 constexpr float kUnhold = 1.f / 1024.f;
-constexpr int kNormBlocks = 64;         // blocks of partial sums per matrix, at most
-constexpr int kTr = 32;                 // tile of the transposing passes
+constexpr int kNormParts = 128;         // partial sums of squares per matrix, at most
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kStageBytes = 32 * 32 * 2;  // an epilogue warp's staged 32 x 32 chunk, in each orientation
+constexpr int kBK = 64;                 // columns of a k-block: 128 bytes of fp16
+constexpr int kRowsP = 128;             // rows of P that a CTA stages
+constexpr int kScaleRows = 128, kScaleCols = 64;  // tile of the scaling pass
+constexpr int kScaleStride = kScaleRows + 2;      // halves; 65 words keep its column walks off one bank
+static_assert(kScaleCols * kScaleStride * 2 <= kEpiWarps * 2 * kStageBytes, "the scaling tile fits the epilogue's room");
 
-// Sums of squares over one matrix's share, of x, 2^64 x and 2^-64 x: whichever of the three
-// neither overflows nor vanishes gives the norm.
-__global__ void __launch_bounds__(256) ortho_norm_kernel(const void* __restrict__ G, int dtype, int64_t size,
-                                                         float* __restrict__ partial) {
-  __shared__ float s[3][8];
-  const int64_t base = static_cast<int64_t>(blockIdx.y) * size;
+// Tiles: a CTA pair computes 256 x 256 (each CTA stages 128 rows of P and 128 of Q and
+// accumulates 128 rows), a single CTA 128 x 64.
+template <bool PAIR>
+struct Tile {
+  static constexpr int kM = PAIR ? 256 : 128;
+  static constexpr int kN = PAIR ? 256 : 64;
+  static constexpr int kBox = PAIR ? 128 : 64;         // rows of a TMA box
+  static constexpr int kRowsQ = PAIR ? 128 : 64;
+  static constexpr int kPBytes = kRowsP * kBK * 2;
+  static constexpr int kQBytes = kRowsQ * kBK * 2;
+  static constexpr int kStages = PAIR ? 6 : 8;
+  static constexpr int kTmemCols = 2 * kN;
+  static constexpr int kChunks = kN / 64;              // 32-column chunks of an epilogue warp
+  static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands, K-major
+      (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
+  static constexpr size_t kRing = static_cast<size_t>(kStages) * (kPBytes + kQBytes);
+  static constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kStageBytes;
+};
+
+struct OrthoCtrl {
+  uint32_t barrier;
+  uint32_t pad[63];
+};
+
+struct OrthoArgs {
+  const void* G;
+  __nv_bfloat16* out;
+  OrthoCtrl* ctrl;
+  float* partial;            // [batch][parts][3]
+  __half *X[2], *XT[2], *A, *Bm;
+  int* err_word;
+  int64_t size;              // m n
+  int batch, m, n, p, q, ldp, ldq, parts, steps, dtype;
+  int flip, g_vec, out_vec;  // X = G^T; 16-byte accesses to G; to out
+  float a, b, c, eps, scale;
+};
+
+struct Maps {
+  CUtensorMap X[2], XT[2], A, Bm;
+};
+
+// ------------------------------------------------------------------------------ wrappers
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  if constexpr (!PAIR) {
+    return bar_try_wait(bar, parity);
+  } else {  // threads of the peer CTA arrive on it
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  }
+}
+
+template <bool PAIR>
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = now_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (poll<PAIR>(bar, parity)) return true;
+    if (*abort || now_ns() - t0 > kAsyncWaitNs) return false;
+  }
+}
+
+// Waits for the phase of `parity`; false after about a second or once another role gave up.
+template <bool PAIR>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return poll<PAIR>(bar, parity) || wait_slow<PAIR>(bar, parity, abort);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y),
+        "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y),
+        "r"(z)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+
+// One arrival on `bar` (PAIR: of both CTAs) when the MMAs issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    commit<false>(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Orders generic-proxy accesses to global memory before TMA accesses (and back).
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes: lane i gets row i.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory descriptor of a K-major operand written by TMA with 128-byte swizzle: start
+// address >> 4 (bits 0-13), 1024 bytes between 8-row groups (32-45), version 1 (46-47),
+// 128-byte swizzle (61-63 = 2).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// --------------------------------------------------------------------- norm and scaling
+
+// Partial sums of squares, of x, 2^64 x and 2^-64 x: whichever of the three neither overflows
+// nor vanishes gives the norm. Part `part` of matrix `b` is a contiguous share of it.
+__device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kThreads / 32]) {
+  const int64_t share = ((g.size + g.parts - 1) / g.parts + 7) / 8 * 8;
+  const int64_t lo = part * share, hi = min(g.size, lo + share), base = b * g.size;
   float sum[3] = {};
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < size; i += gridDim.x * 256ll) {
-    float x[1];
-    if (dtype == PG_F32)
-      load_cols<PG_F32, 1>(G, base + i, x);
-    else
-      load_cols<PG_BF16, 1>(G, base + i, x);
-    const float up = x[0] * 0x1p64f, down = x[0] * 0x1p-64f;
-    sum[0] = fmaf(x[0], x[0], sum[0]);
+  auto add = [&](float x) {
+    const float up = x * 0x1p64f, down = x * 0x1p-64f;
+    sum[0] = fmaf(x, x, sum[0]);
     sum[1] = fmaf(up, up, sum[1]);
     sum[2] = fmaf(down, down, sum[2]);
+  };
+  if (g.g_vec) {
+    constexpr int kFly = 4;  // 16-byte (fp32: two) loads in flight
+    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kFly * kThreads * 8) {
+      float x[kFly][8];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        const int64_t at = i + u * kThreads * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[u][k] = 0.f;
+        if (at >= hi) continue;
+        if (g.dtype == PG_F32)
+          load_cols<PG_F32, 8>(g.G, base + at, x[u]);
+        else
+          load_cols<PG_BF16, 8>(g.G, base + at, x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kFly; ++u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add(x[u][k]);
+    }
+  } else {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+      float x[1];
+      if (g.dtype == PG_F32)
+        load_cols<PG_F32, 1>(g.G, base + i, x);
+      else
+        load_cols<PG_BF16, 1>(g.G, base + i, x);
+      add(x[0]);
+    }
   }
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-    if ((threadIdx.x & 31) == 0) s[k][threadIdx.x >> 5] = sum[k];
+    if ((threadIdx.x & 31) == 0) s_sum[k][threadIdx.x >> 5] = sum[k];
   }
   __syncthreads();
   if (threadIdx.x < 3) {
     float t = 0.f;
-    for (int w = 0; w < 8; ++w) t += s[threadIdx.x][w];
-    partial[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 3 + threadIdx.x] = t;
+    for (int w = 0; w < kThreads / 32; ++w) t += s_sum[threadIdx.x][w];
+    g.partial[(static_cast<int64_t>(b) * g.parts + part) * 3 + threadIdx.x] = t;
   }
 }
 
-// 2^10 / (|G|_F + eps) from the partial sums, added in their order.
-__device__ __forceinline__ float held_scale(const float* partial, int parts, float eps) {
+// 2^10 / (|G|_F + eps) of matrix b, by one warp: lane-strided sums and an xor tree, a fixed order.
+__device__ float held_scale(const OrthoArgs& g, int b) {
+  const int lane = threadIdx.x & 31;
   float s[3] = {};
-  for (int i = 0; i < parts; ++i)
+  for (int i = lane; i < g.parts; i += 32)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) s[k] += partial[3 * i + k];
+    for (int k = 0; k < 3; ++k) s[k] += __ldcg(g.partial + (static_cast<int64_t>(b) * g.parts + i) * 3 + k);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
   float norm;
   if (s[0] > 0x1p-60f && s[0] < 0x1p120f)
     norm = sqrtf(s[0]);
@@ -72,130 +315,655 @@ __device__ __forceinline__ float held_scale(const float* partial, int parts, flo
     norm = sqrtf(s[1]) * 0x1p-64f;
   else
     norm = sqrtf(s[2]) * 0x1p64f;  // also NaN and infinities
-  return kHold / (norm + eps);
+  return kHold / (norm + g.eps);
 }
 
-// X0 in both orientations from G: dst[i, j] and dstT[j, i] of G's own orientation.
-__global__ void __launch_bounds__(256) ortho_scale_kernel(const void* __restrict__ G, int dtype, int m, int n,
-                                                          const float* __restrict__ partial, int parts, float eps,
-                                                          __half* dst, int ld, int64_t dst_size, __half* dstT, int ldT,
-                                                          int64_t dstT_size) {
-  __shared__ float s_scale;
-  __shared__ __half tile[kTr][kTr + 1];
-  const int64_t b = blockIdx.z;
-  if (threadIdx.x == 0) s_scale = held_scale(partial + b * parts * 3, parts, eps);
-  __syncthreads();
-  const float scale = s_scale;
-  const int j0 = blockIdx.x * kTr, i0 = blockIdx.y * kTr;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  for (int r = ty; r < kTr; r += 8) {
-    const int i = i0 + r, j = j0 + tx;
-    if (i < m && j < n) {
-      const int64_t at = (b * m + i) * n + j;
-      float x[1];
-      if (dtype == PG_F32)
-        load_cols<PG_F32, 1>(G, at, x);
+__device__ __forceinline__ uint32_t two_half(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One kScaleRows x kScaleCols tile of X0, in both orientations: the loads of a tile and its
+// stores are apart, so that the next tile's loads are in flight under this one's stores.
+// Columns up to the row strides are written (zeros past the matrix).
+constexpr int kScaleVecs = kScaleRows * (kScaleCols / 8);
+constexpr int kScalePer = (kScaleVecs + kThreads - 1) / kThreads;
+
+__device__ __forceinline__ void scale_load(const OrthoArgs& g, int b, int i0, int j0, float (&x)[kScalePer][8]) {
+#pragma unroll
+  for (int u = 0; u < kScalePer; ++u) {
+    const int v = u * kThreads + threadIdx.x, i = i0 + v / 8, j = j0 + v % 8 * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[u][k] = 0.f;
+    if (v >= kScaleVecs || i >= g.m || j >= g.n) continue;
+    const int64_t at = (static_cast<int64_t>(b) * g.m + i) * g.n + j;
+    if (g.g_vec) {
+      if (g.dtype == PG_F32)
+        load_cols<PG_F32, 8>(g.G, at, x[u]);
       else
-        load_cols<PG_BF16, 1>(G, at, x);
-      const __half h = __float2half_rn(x[0] * scale);
-      tile[r][tx] = h;
-      dst[b * dst_size + static_cast<int64_t>(i) * ld + j] = h;
-    }
-  }
-  __syncthreads();
-  for (int r = ty; r < kTr; r += 8) {
-    const int j = j0 + r, i = i0 + tx;
-    if (i < m && j < n) dstT[b * dstT_size + static_cast<int64_t>(j) * ldT + i] = tile[tx][r];
-  }
-}
-
-// D = alpha P Q^T + beta C for one batch entry; see the top of the file.
-struct Product {
-  const __half* P;
-  const __half* Q;
-  const __half* C;       // laid out as D, or null
-  __half* D;             // [M, N] (ld), null for the last product of the last step
-  __half* DT;            // D transposed [N, M] (ldT); symmetric: D itself
-  __nv_bfloat16* out;    // last product: scale * D, as [M, N] or, flip, [N, M], dense
-  int64_t sP, sQ, sC, sD, sDT, sOut;  // batch strides, elements
-  int ldP, ldQ, ldC, ldD, ldDT;
-  int M, N, K;
-  float alpha, beta, scale;
-  int symmetric, flip;
-};
-
-constexpr int kSimt = 64;
-
-__global__ void __launch_bounds__(256) ortho_product_kernel(const Product g) {
-  if (g.symmetric && blockIdx.x < blockIdx.y) return;  // below the diagonal: the mirrored tile
-  __shared__ float sp[16][kSimt + 1], sq[16][kSimt + 1];
-  const int64_t b = blockIdx.z;
-  const int i0 = blockIdx.y * kSimt, j0 = blockIdx.x * kSimt;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < g.K; k0 += 16) {
-    for (int e = threadIdx.x; e < kSimt * 16; e += 256) {
-      const int r = e >> 4, k = e & 15;
-      sp[k][r] = i0 + r < g.M && k0 + k < g.K
-                     ? __half2float(g.P[b * g.sP + static_cast<int64_t>(i0 + r) * g.ldP + k0 + k]) : 0.f;
-      sq[k][r] = j0 + r < g.N && k0 + k < g.K
-                     ? __half2float(g.Q[b * g.sQ + static_cast<int64_t>(j0 + r) * g.ldQ + k0 + k]) : 0.f;
-    }
-    __syncthreads();
+        load_cols<PG_BF16, 8>(g.G, at, x[u]);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sp[k][ty + 16 * i], sq[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-      if (r >= g.M || c >= g.N) continue;
-      float x = g.alpha * acc[i][j];
-      if (g.C) x = fmaf(g.beta, __half2float(g.C[b * g.sC + static_cast<int64_t>(r) * g.ldC + c]), x);
-      if (g.out) {
-        g.out[b * g.sOut + (g.flip ? static_cast<int64_t>(c) * g.M + r : static_cast<int64_t>(r) * g.N + c)] =
-            __float2bfloat16_rn(x * g.scale);
-      } else {
-        const __half h = __float2half_rn(x);
-        g.D[b * g.sD + static_cast<int64_t>(r) * g.ldD + c] = h;
-        if (!g.symmetric || blockIdx.x != blockIdx.y) g.DT[b * g.sDT + static_cast<int64_t>(c) * g.ldDT + r] = h;
+      for (int k = 0; k < 8; ++k) {
+        float y[1] = {0.f};
+        if (j + k < g.n) {
+          if (g.dtype == PG_F32)
+            load_cols<PG_F32, 1>(g.G, at + k, y);
+          else
+            load_cols<PG_BF16, 1>(g.G, at + k, y);
+        }
+        x[u][k] = y[0];
       }
     }
+  }
 }
 
-struct OrthoBuffers {
-  float* partial;
-  __half *X[2], *XT[2], *A, *Bm;
-  int ldq, ldp;  // row strides: q and p rounded up to 8 (16 bytes)
+__device__ __forceinline__ void scale_pack(float scale, const float (&x)[kScalePer][8], uint4 (&w)[kScalePer]) {
+#pragma unroll
+  for (int u = 0; u < kScalePer; ++u)
+    w[u] = make_uint4(two_half(x[u][0] * scale, x[u][1] * scale), two_half(x[u][2] * scale, x[u][3] * scale),
+                      two_half(x[u][4] * scale, x[u][5] * scale), two_half(x[u][6] * scale, x[u][7] * scale));
+}
+
+__device__ __forceinline__ void scale_store(const OrthoArgs& g, int b, int i0, int j0, const uint4 (&w)[kScalePer],
+                                            __half* s_t) {
+  __half* dst = (g.flip ? g.XT[0] : g.X[0]);
+  __half* dstT = (g.flip ? g.X[0] : g.XT[0]);
+  const int ld = g.flip ? g.ldp : g.ldq, ldT = g.flip ? g.ldq : g.ldp;
+  dst += static_cast<int64_t>(b) * g.m * ld;
+  dstT += static_cast<int64_t>(b) * g.n * ldT;
+  __syncthreads();  // the previous tile has left s_t
+#pragma unroll
+  for (int u = 0; u < kScalePer; ++u) {
+    const int v = u * kThreads + threadIdx.x, r = v / 8, c = v % 8 * 8;
+    if (v >= kScaleVecs) continue;
+    if (i0 + r < g.m) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i0 + r) * ld + j0 + c) = w[u];
+    const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      s_t[(c + k) * kScaleStride + r] = __ushort_as_half(static_cast<uint16_t>(ww[k / 2] >> (16 * (k & 1))));
+  }
+  __syncthreads();
+  for (int v = threadIdx.x; v < kScaleVecs; v += kThreads) {
+    const int c = v / (kScaleRows / 8), r = v % (kScaleRows / 8) * 8;
+    if (j0 + c >= g.n || i0 + r >= ldT) continue;
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(s_t + c * kScaleStride + r);
+    *reinterpret_cast<uint4*>(dstT + static_cast<int64_t>(j0 + c) * ldT + i0 + r) = make_uint4(s[0], s[1], s[2], s[3]);
+  }
+}
+
+// --------------------------------------------------------------------------- the products
+
+// D = alpha P Q^T + beta C; see the top of the file.
+struct Product {
+  const CUtensorMap *P, *Q;
+  const __half* C;       // laid out as D, or null
+  __half* D;             // [M, N]; null for the last product (out)
+  __half* DT;            // D transposed [N, M]; symmetric: D itself
+  int64_t strideD, strideDT;  // between matrices, elements
+  int ldD, ldDT, M, N, K;
+  float alpha, beta;
+  bool symmetric;
 };
 
-size_t carve_ortho(uint8_t* base, int64_t batch, int p, int q, OrthoBuffers* o) {
+__device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& maps, int step, int kind) {
+  const int cur = step & 1;
+  Product r;
+  r.M = g.p;
+  if (kind == 0) {         // A = X X^T
+    r.P = r.Q = &maps.X[cur];
+    r.C = nullptr;
+    r.D = r.DT = g.A;
+    r.K = g.q;
+    r.alpha = kUnhold;
+    r.beta = 0.f;
+  } else if (kind == 1) {  // Bm = b A + c A A
+    r.P = r.Q = &maps.A;
+    r.C = g.A;
+    r.D = r.DT = g.Bm;
+    r.K = g.p;
+    r.alpha = g.c * kUnhold;
+    r.beta = g.b;
+  } else {                 // X <- a X + Bm X
+    r.P = &maps.Bm;
+    r.Q = &maps.XT[cur];
+    r.C = g.X[cur];
+    r.D = step + 1 == g.steps ? nullptr : g.X[cur ^ 1];
+    r.DT = g.XT[cur ^ 1];
+    r.K = g.p;
+    r.alpha = kUnhold;
+    r.beta = g.a;
+  }
+  r.symmetric = kind < 2;
+  r.N = r.symmetric ? g.p : g.q;
+  r.ldD = r.symmetric ? g.ldp : g.ldq;
+  r.ldDT = g.ldp;
+  r.strideD = static_cast<int64_t>(g.p) * r.ldD;
+  r.strideDT = static_cast<int64_t>(r.N) * g.ldp;
+  return r;
+}
+
+// Tiles of one matrix; symmetric: those that reach the diagonal or lie above it.
+template <bool PAIR>
+__host__ __device__ __forceinline__ int tiles_of(int M, int N, bool symmetric) {
+  constexpr int kM = Tile<PAIR>::kM, kN = Tile<PAIR>::kN, kR = kM / kN;
+  const int nm = (M + kM - 1) / kM, nn = (N + kN - 1) / kN;
+  return symmetric ? nm * nn - kR * (nm * (nm - 1) / 2) : nm * nn;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tile_at(const Product& g, int per, int t, int* b, int* i, int* j) {
+  constexpr int kN = Tile<PAIR>::kN, kR = Tile<PAIR>::kM / kN;
+  const int nn = (g.N + kN - 1) / kN;
+  *b = t / per;
+  int r = t - *b * per;
+  if (g.symmetric) {
+    int row = 0;
+    for (int left = nn; r >= left; left -= kR) {
+      r -= left;
+      ++row;
+    }
+    *i = row;
+    *j = row * kR + r;
+  } else {
+    *i = r / nn;
+    *j = r - *i * nn;
+  }
+}
+
+template <int S>
+struct Bars {
+  uint64_t full[S], empty[S], acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int abort, ok;
+};
+
+// The grid barrier: every thread's global writes so far are visible to every block's loads
+// after it, TMA loads by thread 0 among them. False once a block gave up (about a second).
+template <int S>
+__device__ __forceinline__ bool grid_meet(const OrthoArgs& g, Bars<S>* bars, uint32_t* phase) {
+  fence_async_global();
+  __syncthreads();
+  *phase += 1;
+  if (threadIdx.x == 0) {
+    bool ok = !*static_cast<volatile int*>(&bars->abort);
+    if (ok) {
+      __threadfence();
+      atomicAdd(&g.ctrl->barrier, 1u);
+      const uint32_t want = *phase * gridDim.x;
+      const uint64_t t0 = now_ns();
+      for (;;) {
+        uint32_t seen;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(&g.ctrl->barrier) : "memory");
+        if (seen >= want) break;
+        if (now_ns() - t0 > kAsyncWaitNs) {
+          ok = false;
+          atomicOr(g.err_word, kErrOrtho);
+          break;
+        }
+      }
+      __threadfence();
+      fence_async_global();
+    }
+    bars->ok = ok;
+  }
+  __syncthreads();
+  return bars->ok != 0;
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    ortho_kernel(const __grid_constant__ Maps maps, const __grid_constant__ OrthoArgs g) {
+  using T = Tile<PAIR>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars<S> bars_s;
+  __shared__ float s_sum[3][kThreads / 32];
+  __shared__ float s_scale;
+  uint8_t* s_epi = ring + T::kRing;                       // the epilogue warps' staging
+  __half* s_t = reinterpret_cast<__half*>(s_epi);         // scaling: the transposed tile
+  Bars<S>* bars = &bars_s;
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cta_rank() : 0u;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      bar_init(smem_addr(&bars->full[s]), 1);
+      bar_init(smem_addr(&bars->empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(smem_addr(&bars->acc_full[s]), 1);
+      bar_init(smem_addr(&bars->acc_empty[s]), (PAIR ? 2 : 1) * kEpiWarps);
+    }
+    bar_init(smem_addr(&bars->done), 1);
+    bars->abort = 0;
+    bar_init_fence();
+    fence_async_smem();
+  }
+  if (warp == 1) tmem_alloc<PAIR>(smem_addr(&bars->tmem), T::kTmemCols);
+  fence_before();
+  __syncthreads();
+  if constexpr (PAIR) pair_sync();  // both CTAs' barriers and TMEM exist before any remote use
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  // ---- |G|_F and X0
+  uint32_t phase = 0;
+  for (int w = blockIdx.x; w < g.batch * g.parts; w += gridDim.x) norm_part(g, w / g.parts, w % g.parts, s_sum);
+  bool ok = grid_meet(g, bars, &phase);
+  if (ok) {
+    const int nj = (g.n + kScaleCols - 1) / kScaleCols, ni = (g.m + kScaleRows - 1) / kScaleRows;
+    const int items = g.batch * ni * nj;
+    auto load = [&](int w, float (&x)[kScalePer][8]) {
+      const int b = w / (ni * nj), r = w - b * ni * nj;
+      scale_load(g, b, r / nj * kScaleRows, r % nj * kScaleCols, x);
+    };
+    int last = -1;
+    float x[kScalePer][8];
+    if (static_cast<int>(blockIdx.x) < items) load(blockIdx.x, x);
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      const int b = w / (ni * nj), r = w - b * ni * nj;
+      if (b != last) {
+        __syncthreads();
+        if (warp == 0) {
+          const float s = held_scale(g, b);
+          if (lane == 0) s_scale = s;
+        }
+        __syncthreads();
+        last = b;
+      }
+      uint4 packed[kScalePer];
+      scale_pack(s_scale, x, packed);
+      if (w + static_cast<int>(gridDim.x) < items) load(w + gridDim.x, x);
+      scale_store(g, b, r / nj * kScaleRows, r % nj * kScaleCols, packed, s_t);
+    }
+    ok = grid_meet(g, bars, &phase);
+  }
+
+  // ---- the products; each role carries its place in the ring and the accumulators along
+  int stage = 0, acc = 0;
+  uint32_t ring_phase = 0, acc_phase = 0;
+  for (int prod = 0; ok && prod < 3 * g.steps; ++prod) {
+    const Product pr = product_of(g, maps, prod / 3, prod % 3);
+    const int per = tiles_of<PAIR>(pr.M, pr.N, pr.symmetric), total = per * g.batch;
+    const int num_kb = (pr.K + kBK - 1) / kBK;
+    if (warp == 0) {
+      if (lane == 0) {
+        bool fine = true;
+        for (int t = unit; fine && t < total; t += units) {
+          int b, i, j;
+          tile_at<PAIR>(pr, per, t, &b, &i, &j);
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!wait<PAIR>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
+              fine = false;
+              break;
+            }
+            const uint32_t full = smem_addr(&bars->full[stage]);
+            const uint32_t dp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes)), dq = dp + T::kPBytes;
+            if constexpr (PAIR) {
+              if (rank == 0) bar_expect(full, 2 * (T::kPBytes + T::kQBytes));
+              const uint32_t full0 = in_cta(full, 0);
+              load_box<true>(dp, pr.P, full0, kb * kBK, i * T::kM + rank * kRowsP, b);
+              load_box<true>(dq, pr.Q, full0, kb * kBK, j * T::kN + rank * T::kRowsQ, b);
+            } else {
+              bar_expect(full, T::kPBytes + T::kQBytes);
+              load_box<false>(dp, pr.P, full, kb * kBK, i * T::kM, b);
+              load_box<false>(dp + T::kPBytes / 2, pr.P, full, kb * kBK, i * T::kM + T::kBox, b);
+              load_box<false>(dq, pr.Q, full, kb * kBK, j * T::kN, b);
+            }
+            if (++stage == S) {
+              stage = 0;
+              ring_phase ^= 1u;
+            }
+          }
+        }
+        if (!fine) {
+          atomicOr(g.err_word, kErrOrtho);
+          *abort = 1;
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && rank == 0) {
+        bool fine = true;
+        for (int t = unit; fine && t < total; t += units) {
+          if (!wait<PAIR>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
+            fine = false;
+            break;
+          }
+          fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * T::kN);
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!wait<PAIR>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
+              fine = false;
+              break;
+            }
+            fence_after();
+            const uint32_t sp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes));
+            const uint64_t dp = operand_desc(sp), dq = operand_desc(sp + T::kPBytes);
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)  // 16 columns = 32 bytes = 2 address units
+              mma_f16<PAIR>(d, dp + 2u * k, dq + 2u * k, T::kIdesc, (kb | k) != 0);
+            commit<PAIR>(smem_addr(&bars->empty[stage]));
+            if (++stage == S) {
+              stage = 0;
+              ring_phase ^= 1u;
+            }
+          }
+          if (!fine) break;
+          commit<PAIR>(smem_addr(&bars->acc_full[acc]));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        if (!fine) {
+          atomicOr(g.err_word, kErrOrtho);
+          *abort = 1;
+        }
+      }
+    } else {
+      // A warp takes 32 rows of the tile (its TMEM lanes) in chunks of 32 columns. TMEM gives a
+      // lane one row; global memory wants neighbouring lanes on one row. So a chunk passes
+      // through 2 KB of the warp's shared memory in each orientation, C the same way in:
+      // lane-per-row accesses to global memory (32 lines each) took half of the kernel's time.
+      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      uint8_t* s_row = s_epi + (warp - 2) * 2 * kStageBytes;  // [32 rows][32 columns], 16-byte pieces swizzled
+      uint8_t* s_col = s_row + kStageBytes;                   // [32 columns][32 rows]
+      auto piece = [&](int r, int c) { return reinterpret_cast<uint4*>(s_row + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); };
+      const int lr = lane >> 2, lc = lane & 3;                // this lane's row (of 8) and piece in a coalesced access
+      bool fine = true;
+      for (int t = unit; t < total; t += units) {
+        int b, i, j;
+        tile_at<PAIR>(pr, per, t, &b, &i, &j);
+        const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
+        const bool mirror = !pr.symmetric || j * T::kN >= (i + 1) * T::kM;  // else the tile holds its own mirror image
+        const int col0 = j * T::kN + half * (T::kChunks * 32);
+        const bool some = row0 < pr.M;
+        const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
+        uint4 cw[4];  // C of the next chunk, in coalesced order
+        auto load_c = [&](int ch) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            cw[k] = make_uint4(0, 0, 0, 0);
+            if (row0 + lr + 8 * k < pr.M && col0 + ch * 32 < pr.N)
+              cw[k] = __ldcg(reinterpret_cast<const uint4*>(pr.C + at + static_cast<int64_t>(8 * k) * pr.ldD + ch * 32));
+          }
+        };
+        if (pr.C) load_c(0);
+        if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
+          fine = false;
+          break;
+        }
+        fence_after();
+#pragma unroll 1
+        for (int ch = 0; some && ch < T::kChunks; ++ch) {
+          const int c0 = col0 + ch * 32;
+          if (c0 >= pr.N) break;
+          uint32_t r[32];
+          tmem_load(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * T::kN) +
+                        static_cast<uint32_t>(half * (T::kChunks * 32) + ch * 32), r);
+          float x[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = pr.alpha * __uint_as_float(r[k]);
+          if (pr.C) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *piece(lr + 8 * k, lc) = cw[k];
+            if (ch + 1 < T::kChunks) load_c(ch + 1);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 q = *piece(lane, k);
+              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
+                x[8 * k + 2 * h] = fmaf(pr.beta, f.x, x[8 * k + 2 * h]);
+                x[8 * k + 2 * h + 1] = fmaf(pr.beta, f.y, x[8 * k + 2 * h + 1]);
+              }
+            }
+          }
+          uint32_t h[16];  // two columns each: fp16, or the result in bf16
+          if (pr.D) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) h[k] = two_half(x[2 * k], x[2 * k + 1]);
+          } else {
+            const float s = g.scale * kUnhold;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) h[k] = two_bf16(x[2 * k] * s, x[2 * k + 1] * s);
+          }
+          // where the rows and the columns of this chunk go: row r at `rows` + r * ldr, column c
+          // at `cols` + c * ldc (16-bit elements); `whole`: in 16-byte pieces
+          uint16_t *rows = nullptr, *cols = nullptr;
+          int64_t ldr = 0, ldc = 0;
+          bool whole = true;
+          if (pr.D) {
+            rows = reinterpret_cast<uint16_t*>(pr.D) + b * pr.strideD + static_cast<int64_t>(row0) * pr.ldD + c0;
+            ldr = pr.ldD;
+            if (mirror) {
+              cols = reinterpret_cast<uint16_t*>(pr.DT) + b * pr.strideDT + static_cast<int64_t>(c0) * pr.ldDT + row0;
+              ldc = pr.ldDT;
+            }
+          } else {
+            uint16_t* out = reinterpret_cast<uint16_t*>(g.out) + b * g.size;
+            if (g.flip) {
+              cols = out + static_cast<int64_t>(c0) * pr.M + row0;
+              ldc = pr.M;
+              whole = g.out_vec && row0 + 32 <= pr.M;
+            } else {
+              rows = out + static_cast<int64_t>(row0) * pr.N + c0;
+              ldr = pr.N;
+              whole = g.out_vec && c0 + 32 <= pr.N;
+            }
+          }
+          if (!whole) {  // a ragged edge of the result, or one at an odd address
+            if (row0 + lane < pr.M)
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (c0 + k < pr.N)
+                  (rows ? rows + lane * ldr + k : cols + k * ldc + lane)[0] =
+                      static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+            __syncwarp();
+            continue;
+          }
+          if (rows) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *piece(lane, k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+          }
+          if (cols) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              reinterpret_cast<uint16_t*>(s_col)[k * 32 + lane] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+          }
+          __syncwarp();
+          if (rows) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (row0 + lr + 8 * k < pr.M)
+                *reinterpret_cast<uint4*>(rows + (lr + 8 * k) * ldr + lc * 8) = *piece(lr + 8 * k, lc);
+          }
+          if (cols) {
+            // (rows past the last one land in the padding up to ldDT)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (c0 + lr + 8 * k < pr.N)
+                *reinterpret_cast<uint4*>(cols + (lr + 8 * k) * ldc + lc * 8) =
+                    reinterpret_cast<const uint4*>(s_col)[(lr + 8 * k) * 4 + lc];
+          }
+          __syncwarp();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_addr(&bars->acc_empty[acc]);
+          if constexpr (PAIR)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
+          else
+            bar_arrive(bar);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!fine) {
+        if (lane == 0) atomicOr(g.err_word, kErrOrtho);
+        *abort = 1;
+      }
+    }
+    __syncwarp();
+    if (prod + 1 < 3 * g.steps) ok = grid_meet(g, bars, &phase);
+  }
+
+  // ---- teardown: every copy has landed and every MMA and commit has finished before the CTA
+  // (or its peer) may exit and its TMEM is given back
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      const uint64_t t0 = now_ns();
+      while (!poll<PAIR>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u) && now_ns() - t0 < kAsyncWaitNs / 8) {
+      }
+      if (++stage == S) {
+        stage = 0;
+        ring_phase ^= 1u;
+      }
+    }
+  }
+  if (warp == 1 && lane == 0 && rank == 0) {
+    commit_here<PAIR>(smem_addr(&bars->done));
+    const uint64_t t0 = now_ns();
+    while (!poll<PAIR>(smem_addr(&bars->done), 0) && now_ns() - t0 < kAsyncWaitNs) {
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if constexpr (PAIR) pair_sync();
+  if (warp == 1) tmem_free<PAIR>(tmem, T::kTmemCols);
+}
+
+// ------------------------------------------------------------------------------ host side
+
+size_t carve_ortho(uint8_t* base, int64_t batch, int p, int q, OrthoArgs* o) {
+  uint8_t* first = base ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 127) & ~uintptr_t(127)) : nullptr;
   size_t at = 0;
   auto take = [&](size_t bytes) {
-    uint8_t* ptr = base ? base + at : nullptr;
-    at += (bytes + 15) / 16 * 16;
+    uint8_t* ptr = first ? first + at : nullptr;
+    at += (bytes + 127) / 128 * 128;
     return ptr;
   };
-  o->ldq = (q + 7) / 8 * 8;
-  o->ldp = (p + 7) / 8 * 8;
-  o->partial = reinterpret_cast<float*>(take(batch * kNormBlocks * 3 * sizeof(float)));
+  o->ldq = (q + 63) / 64 * 64;  // whole k-blocks: rows start on 128 bytes
+  o->ldp = (p + 63) / 64 * 64;
+  o->ctrl = reinterpret_cast<OrthoCtrl*>(take(sizeof(OrthoCtrl)));
+  o->partial = reinterpret_cast<float*>(take(batch * kNormParts * 3 * sizeof(float)));
   for (int i = 0; i < 2; ++i) {
     o->X[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldq));
     o->XT[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * q * o->ldp));
   }
   o->A = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
   o->Bm = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
-  return at;
+  return at + 128;
 }
 
-pg_status launch_product(const Product& g, int batch, cudaStream_t stream) {
-  const dim3 grid((g.N + kSimt - 1) / kSimt, (g.M + kSimt - 1) / kSimt, batch);
-  ortho_product_kernel<<<grid, 256, 0, stream>>>(g);
+// [batch, rows, cols] fp16 with row stride ld, boxes of `box` rows x 64 columns, 128-byte swizzle.
+bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, int ld, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(rows) * ld * 2};
+  cuuint32_t box[3] = {kBK, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+// Units (CTAs, or CTA pairs) of the kernel that are resident at once on the current device.
+template <bool PAIR>
+pg_status resident_units(int* units) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return PG_ERR_DEVICE;
+  *units = known[dev].load(std::memory_order_relaxed);
+  if (*units) return PG_OK;
+  auto kern = ortho_kernel<PAIR>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Tile<PAIR>::kSmem));
+  if (e != cudaSuccess) return cuda_fail(e);
+  int n = 0;
+  if (PAIR) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * static_cast<unsigned>(sm_count()));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Tile<PAIR>::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+  } else {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, Tile<PAIR>::kSmem);
+    n = std::min(n, 1) * sm_count();
+  }
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (n < 1) return PG_ERR_DEVICE;
+  known[dev].store(n, std::memory_order_relaxed);
+  *units = n;
+  return PG_OK;
+}
+
+template <bool PAIR>
+pg_status launch_ortho(const OrthoArgs& g, cudaStream_t stream) {
+  int units;
+  pg_status st = resident_units<PAIR>(&units);
+  if (st != PG_OK) return st;
+  constexpr int box = Tile<PAIR>::kBox;
+  Maps maps;
+  for (int i = 0; i < 2; ++i)
+    if (!held_map(&maps.X[i], g.X[i], g.batch, g.p, g.q, g.ldq, box) ||
+        !held_map(&maps.XT[i], g.XT[i], g.batch, g.q, g.p, g.ldp, box))
+      return PG_ERR_CUDA;
+  if (!held_map(&maps.A, g.A, g.batch, g.p, g.p, g.ldp, box) || !held_map(&maps.Bm, g.Bm, g.batch, g.p, g.p, g.ldp, box))
+    return PG_ERR_CUDA;
+  // no more units than the widest phase has work for: the fewer blocks, the quicker they meet
+  const int64_t tiles = static_cast<int64_t>(g.batch) * std::max(tiles_of<PAIR>(g.p, g.q, false), tiles_of<PAIR>(g.p, g.p, true));
+  const int64_t scale = static_cast<int64_t>(g.batch) * ((g.m + kScaleRows - 1) / kScaleRows) * ((g.n + kScaleCols - 1) / kScaleCols);
+  units = static_cast<int>(std::min<int64_t>(units, std::max(tiles, PAIR ? (scale + 1) / 2 : scale)));
+  cudaError_t e = cudaMemsetAsync(g.ctrl, 0, sizeof(OrthoCtrl), stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((PAIR ? 2u : 1u) * static_cast<unsigned>(units));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Tile<PAIR>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, ortho_kernel<PAIR>, maps, g);
+  if (e != cudaSuccess) return cuda_fail(e);
   return after_launch(1);
+}
+
+// Whether 256 x 256 pair tiles finish sooner than 128 x 64 tiles: k-blocks walked one after
+// another by the busiest unit, times the cycles of one (a pair's 512 are its MMAs; a single
+// CTA's ~400 its 24 KB from L2), over a step's three products.
+bool use_pairs(const OrthoArgs& g, int sms) {
+  auto cost = [&](bool pair, int N, int K, bool sym) {
+    const int64_t per = pair ? tiles_of<true>(g.p, N, sym) : tiles_of<false>(g.p, N, sym);
+    const int64_t units = pair ? sms / 2 : sms;
+    return (per * g.batch + units - 1) / units * ((K + kBK - 1) / kBK) * (pair ? 512 : 400);
+  };
+  auto step = [&](bool pair) {
+    return cost(pair, g.p, g.q, true) + cost(pair, g.p, g.p, true) + cost(pair, g.q, g.p, false);
+  };
+  return step(true) < step(false);
 }
 
 }  // namespace
@@ -206,7 +974,7 @@ using namespace pg;
 extern "C" pg_status pg_orthogonalize_workspace_size(int32_t batch, int32_t m, int32_t n, size_t* bytes) {
   if (!bytes) return PG_ERR_NULL;
   if (batch < 0 || batch > kMaxBatch || m < 1 || n < 1 || m > kMaxSide || n > kMaxSide) return PG_ERR_SHAPE;
-  OrthoBuffers o;
+  OrthoArgs o;
   *bytes = batch == 0 ? 0 : carve_ortho(nullptr, batch, m < n ? m : n, m < n ? n : m, &o);
   return PG_OK;
 }
@@ -225,72 +993,27 @@ extern "C" pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batc
   if (workspace_bytes < need || !workspace) return PG_ERR_WORKSPACE;
   if (device_cc() != 103) return PG_ERR_DEVICE;
 
-  const bool flip = m > n;  // X = G^T
-  const int p = flip ? n : m, q = flip ? m : n;
-  OrthoBuffers o;
-  carve_ortho(static_cast<uint8_t*>(workspace), batch, p, q, &o);
-  const int64_t sX = static_cast<int64_t>(p) * o.ldq, sXT = static_cast<int64_t>(q) * o.ldp;
-  const int64_t sA = static_cast<int64_t>(p) * o.ldp, size = static_cast<int64_t>(m) * n;
-  const int parts = static_cast<int>(min(static_cast<int64_t>(kNormBlocks), (size + 4095) / 4096));
-  ortho_norm_kernel<<<dim3(parts, batch), 256, 0, stream>>>(G, dtype, size, o.partial);
-  st = after_launch(1);
-  if (st != PG_OK) return st;
-  ortho_scale_kernel<<<dim3((n + kTr - 1) / kTr, (m + kTr - 1) / kTr, batch), 256, 0, stream>>>(
-      G, dtype, m, n, o.partial, parts, eps, flip ? o.XT[0] : o.X[0], flip ? o.ldp : o.ldq, flip ? sXT : sX,
-      flip ? o.X[0] : o.XT[0], flip ? o.ldq : o.ldp, flip ? sX : sXT);
-  st = after_launch(1);
-  if (st != PG_OK) return st;
-
-  int cur = 0;
-  for (int s = 0; s < steps; ++s) {
-    Product g = {};
-    // A = X X^T
-    g.P = g.Q = o.X[cur];
-    g.sP = g.sQ = sX;
-    g.ldP = g.ldQ = o.ldq;
-    g.D = g.DT = o.A;
-    g.sD = g.sDT = sA;
-    g.ldD = g.ldDT = o.ldp;
-    g.M = g.N = p;
-    g.K = q;
-    g.alpha = kUnhold;
-    g.symmetric = 1;
-    if ((st = launch_product(g, batch, stream)) != PG_OK) return st;
-    // Bm = b A + c A A
-    g.P = g.Q = g.C = o.A;
-    g.sP = g.sQ = g.sC = sA;
-    g.ldP = g.ldQ = g.ldC = o.ldp;
-    g.D = g.DT = o.Bm;
-    g.K = p;
-    g.alpha = c * kUnhold;
-    g.beta = b;
-    if ((st = launch_product(g, batch, stream)) != PG_OK) return st;
-    // X <- a X + Bm X
-    g.P = o.Bm;
-    g.Q = o.XT[cur];
-    g.sQ = sXT;
-    g.C = o.X[cur];
-    g.sC = sX;
-    g.ldC = o.ldq;
-    g.D = o.X[cur ^ 1];
-    g.sD = sX;
-    g.ldD = o.ldq;
-    g.DT = o.XT[cur ^ 1];
-    g.sDT = sXT;
-    g.ldDT = o.ldp;
-    g.N = q;
-    g.alpha = kUnhold;
-    g.beta = a;
-    g.symmetric = 0;
-    if (s + 1 == steps) {
-      g.D = g.DT = nullptr;
-      g.out = static_cast<__nv_bfloat16*>(out);
-      g.sOut = size;
-      g.scale = scale * kUnhold;
-      g.flip = flip;
-    }
-    if ((st = launch_product(g, batch, stream)) != PG_OK) return st;
-    cur ^= 1;
-  }
-  return PG_OK;
+  OrthoArgs g = {};
+  g.G = G;
+  g.out = static_cast<__nv_bfloat16*>(out);
+  g.err_word = device_error_word();
+  g.size = static_cast<int64_t>(m) * n;
+  g.batch = batch;
+  g.m = m;
+  g.n = n;
+  g.flip = m > n;  // X = G^T
+  g.p = g.flip ? n : m;
+  g.q = g.flip ? m : n;
+  carve_ortho(static_cast<uint8_t*>(workspace), batch, g.p, g.q, &g);
+  g.parts = static_cast<int>(std::min<int64_t>(kNormParts, (g.size + 4095) / 4096));
+  g.steps = steps;
+  g.dtype = dtype;
+  g.g_vec = n % 8 == 0 && aligned(G, 16);
+  g.out_vec = n % 8 == 0 && aligned(out, 16);
+  g.a = a;
+  g.b = b;
+  g.c = c;
+  g.eps = eps;
+  g.scale = scale;
+  return use_pairs(g, sm_count()) ? launch_ortho<true>(g, stream) : launch_ortho<false>(g, stream);
 }

@@ -13,7 +13,7 @@
 //   2. rowgrad_sum_kernel: the sums, fp32, in ascending order of the references.
 #include "pg_async.cuh"
 #include "pg_hash.cuh"
-#include "pg_vec.cuh"
+#include "pg_vec.h"
 
 namespace pg {
 namespace {

@@ -432,7 +432,8 @@ FORMULA = 1.4e-2 + 2.0 ** -8
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("b,m,n", [(1, 1, 1), (1, 1, 300), (2, 200, 1), (3, 7, 5), (1, 64, 64), (2, 128, 256), (1, 256, 1024),
                                    (2, 129, 130), (1, 131, 515), (3, 515, 131), (1, 768, 1024), (2, 640, 320),
-                                   (1, 1000, 777)])
+                                   (1, 1000, 777), (6, 520, 1030), (3, 1001, 1111), (3, 1111, 1001), (1, 2560, 1280),
+                                   (5, 1040, 640)])
 def test_orthogonalize(cuda, b, m, n, dtype):
     pg = _pg()
     G = gaussian(torch.Generator().manual_seed(m * n), b, m, n, dtype, cuda)
