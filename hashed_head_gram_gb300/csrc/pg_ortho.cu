@@ -1,25 +1,24 @@
 // Orthogonalised updates by Newton-Schulz steps (pg_orthogonalize), for a batch of matrices.
 //
-// With p = min(m, n), q = max(m, n) and X [p, q] (G or its transpose, divided by its Frobenius
-// norm), a step is three products:
-//   A  = X X^T             [p, p], symmetric
-//   Bm = b A + c A A       [p, p], symmetric
-//   X  <- a X + Bm X       [p, q]
-// Each is D = alpha P Q^T + beta C with P and Q row-major: X is kept in both orientations (XT
-// [q, p] is the second operand of the last product), and the symmetric matrices are their own
-// transposes. So one code does all three; it writes a tile where it belongs and, transposed,
-// in the second array, which for the symmetric products is the mirrored tile of the same
-// matrix: their tiles below the diagonal are never computed.
+// X [m, n] is G divided by its Frobenius norm; p = min(m, n), q = max(m, n). A step is
+//   A  = X X^T (m <= n) or X^T X     [p, p], symmetric
+//   Bm = a I + b A + c A A           [p, p], symmetric
+//   X  <- Bm X (m <= n) or X Bm      [m, n]
+// three products of 2 p p q, 2 p p p and 2 p p q operations, the symmetric ones half of that.
+// X stays in G's orientation: where a product needs its columns as the long rows of an
+// operand, the tensor core reads the tile "MN-major" (the descriptor's transpose), and since
+// Bm holds a I the last product has nothing to add. The tiles of A and Bm below the diagonal
+// are not computed: each tile above it is also written, transposed, where its mirror image is.
 //
 // Between the products X, A and Bm are held as fp16 scaled by 2^10 (pg.h): 11 significant
 // bits, against the 8 of the bf16 result.
 //
 // One cooperative launch does the whole update: norm, scaling, and 3 * steps products on the
-// tensor cores, the blocks meeting at a grid barrier between them. The intermediate matrices
-// stay in L2 where they fit (a step reads each of them once per tile row or column).
-//   warp 0      TMA producer: 64-column k-blocks of P and Q, 128-byte swizzle, into a ring
+// tensor cores, the blocks meeting at a grid barrier between them. The held matrices stay in
+// L2 where they fit.
+//   warp 0      TMA producer: 64-deep k-blocks of both operands, 128-byte swizzle, into a ring
 //   warp 1      tcgen05.mma issuer, two accumulators in TMEM
-//   warps 2..9  epilogue: tcgen05.ld, alpha / beta / C, fp16 in both orientations
+//   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -43,9 +42,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kStageBytes = 32 * 32 * 2;  // an epilogue warp's staged 32 x 32 chunk, in each orientation
 constexpr int kBK = 64;                 // columns of a k-block: 128 bytes of fp16
 constexpr int kRowsP = 128;             // rows of P that a CTA stages
-constexpr int kScaleRows = 128, kScaleCols = 64;  // tile of the scaling pass
-constexpr int kScaleStride = kScaleRows + 2;      // halves; 65 words keep its column walks off one bank
-static_assert(kScaleCols * kScaleStride * 2 <= kEpiWarps * 2 * kStageBytes, "the scaling tile fits the epilogue's room");
+constexpr int kBox = 64;                // rows and columns of a TMA box (8 KB)
+constexpr int kBoxBytes = kBox * kBox * 2;
 
 // Tiles: a CTA pair computes 256 x 256 (each CTA stages 128 rows of P and 128 of Q and
 // accumulates 128 rows), a single CTA 128 x 64.
@@ -53,14 +51,13 @@ template <bool PAIR>
 struct Tile {
   static constexpr int kM = PAIR ? 256 : 128;
   static constexpr int kN = PAIR ? 256 : 64;
-  static constexpr int kBox = PAIR ? 128 : 64;         // rows of a TMA box
   static constexpr int kRowsQ = PAIR ? 128 : 64;
   static constexpr int kPBytes = kRowsP * kBK * 2;
   static constexpr int kQBytes = kRowsQ * kBK * 2;
   static constexpr int kStages = PAIR ? 6 : 8;
   static constexpr int kTmemCols = 2 * kN;
   static constexpr int kChunks = kN / 64;              // 32-column chunks of an epilogue warp
-  static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands, K-major
+  static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands
       (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
   static constexpr size_t kRing = static_cast<size_t>(kStages) * (kPBytes + kQBytes);
   static constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kStageBytes;
@@ -76,16 +73,16 @@ struct OrthoArgs {
   __nv_bfloat16* out;
   OrthoCtrl* ctrl;
   float* partial;            // [batch][parts][3]
-  __half *X[2], *XT[2], *A, *Bm;
+  __half *X[2], *A, *Bm;     // [batch][m][ldx], [batch][p][ldp]
   int* err_word;
   int64_t size;              // m n
-  int batch, m, n, p, q, ldp, ldq, parts, steps, dtype;
-  int flip, g_vec, out_vec;  // X = G^T; 16-byte accesses to G; to out
+  int batch, m, n, p, ldx, ldp, parts, steps, dtype;
+  int g_vec, out_vec;        // 16-byte accesses to G; to out
   float a, b, c, eps, scale;
 };
 
 struct Maps {
-  CUtensorMap X[2], XT[2], A, Bm;
+  CUtensorMap X[2], A, Bm;
 };
 
 // ------------------------------------------------------------------------------ wrappers
@@ -231,11 +228,14 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory descriptor of a K-major operand written by TMA with 128-byte swizzle: start
-// address >> 4 (bits 0-13), 1024 bytes between 8-row groups (32-45), version 1 (46-47),
-// 128-byte swizzle (61-63 = 2).
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory descriptor of an operand tile of 64 x 64 boxes written by TMA with 128-byte
+// swizzle (61-63 = 2; version 1 at 46-47; start address >> 4 at 0-13). K-major: a box holds 64
+// rows of the operand, and 8-row groups lie 1024 bytes apart (bits 32-45), the boxes' too.
+// MN-major: a box holds 64 of the operand's rows along its 128-byte lines and 64 k down them;
+// 8-k groups lie 1024 bytes apart (32-45) and the next 64 rows one box further (16-29).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(mn ? kBoxBytes >> 4 : 1) << 16) |
+         (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
 // --------------------------------------------------------------------- norm and scaling
@@ -253,7 +253,7 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kT
     sum[2] = fmaf(down, down, sum[2]);
   };
   if (g.g_vec) {
-    constexpr int kFly = 4;  // 16-byte (fp32: two) loads in flight
+    constexpr int kFly = 8;  // 16-byte (fp32: two) loads in flight
     for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kFly * kThreads * 8) {
       float x[kFly][8];
 #pragma unroll
@@ -323,123 +323,113 @@ __device__ __forceinline__ uint32_t two_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One kScaleRows x kScaleCols tile of X0, in both orientations: the loads of a tile and its
-// stores are apart, so that the next tile's loads are in flight under this one's stores.
-// Columns up to the row strides are written (zeros past the matrix).
-constexpr int kScaleVecs = kScaleRows * (kScaleCols / 8);
-constexpr int kScalePer = (kScaleVecs + kThreads - 1) / kThreads;
-
-__device__ __forceinline__ void scale_load(const OrthoArgs& g, int b, int i0, int j0, float (&x)[kScalePer][8]) {
+// X0: rows of G scaled and rounded into rows of stride ldx, 8 columns at a time. A block owns a
+// contiguous share of the rows of all matrices.
+__device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
+  const uint32_t per_row = (g.n + 7) / 8;
+  const int64_t rows = static_cast<int64_t>(g.batch) * g.m;
+  const int64_t lo = rows * blockIdx.x / gridDim.x, hi = rows * (blockIdx.x + 1) / gridDim.x;
+  for (int64_t r0 = lo; r0 < hi;) {
+    const int b = static_cast<int>(r0 / g.m);
+    const int64_t r1 = min(hi, static_cast<int64_t>(b + 1) * g.m);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const float s = held_scale(g, b);
+      if (threadIdx.x == 0) *s_scale = s;
+    }
+    __syncthreads();
+    const float scale = *s_scale;
+    const uint32_t vecs = static_cast<uint32_t>(r1 - r0) * per_row;  // < 2^31: at most m of at most 2048
+    constexpr int kFly = 4;
+    for (uint32_t v0 = threadIdx.x; v0 < vecs; v0 += kFly * kThreads) {
+      float x[kFly][8];
 #pragma unroll
-  for (int u = 0; u < kScalePer; ++u) {
-    const int v = u * kThreads + threadIdx.x, i = i0 + v / 8, j = j0 + v % 8 * 8;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[u][k] = 0.f;
-    if (v >= kScaleVecs || i >= g.m || j >= g.n) continue;
-    const int64_t at = (static_cast<int64_t>(b) * g.m + i) * g.n + j;
-    if (g.g_vec) {
-      if (g.dtype == PG_F32)
-        load_cols<PG_F32, 8>(g.G, at, x[u]);
-      else
-        load_cols<PG_BF16, 8>(g.G, at, x[u]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float y[1] = {0.f};
-        if (j + k < g.n) {
+      for (int u = 0; u < kFly; ++u) {
+        const uint32_t v = v0 + u * kThreads;
+        if (v >= vecs) continue;
+        const int64_t r = r0 + v / per_row;
+        const int j = static_cast<int>(v % per_row) * 8;
+        const int64_t at = r * g.n + j;
+        if (g.g_vec) {
           if (g.dtype == PG_F32)
-            load_cols<PG_F32, 1>(g.G, at + k, y);
+            load_cols<PG_F32, 8>(g.G, at, x[u]);
           else
-            load_cols<PG_BF16, 1>(g.G, at + k, y);
+            load_cols<PG_BF16, 8>(g.G, at, x[u]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float y[1] = {0.f};
+            if (j + k < g.n) {
+              if (g.dtype == PG_F32)
+                load_cols<PG_F32, 1>(g.G, at + k, y);
+              else
+                load_cols<PG_BF16, 1>(g.G, at + k, y);
+            }
+            x[u][k] = y[0];
+          }
         }
-        x[u][k] = y[0];
+      }
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        const uint32_t v = v0 + u * kThreads;
+        if (v >= vecs) continue;
+        const int64_t r = r0 + v / per_row;
+        const int j = static_cast<int>(v % per_row) * 8;
+        *reinterpret_cast<uint4*>(g.X[0] + r * g.ldx + j) =
+            make_uint4(two_half(x[u][0] * scale, x[u][1] * scale), two_half(x[u][2] * scale, x[u][3] * scale),
+                       two_half(x[u][4] * scale, x[u][5] * scale), two_half(x[u][6] * scale, x[u][7] * scale));
       }
     }
-  }
-}
-
-__device__ __forceinline__ void scale_pack(float scale, const float (&x)[kScalePer][8], uint4 (&w)[kScalePer]) {
-#pragma unroll
-  for (int u = 0; u < kScalePer; ++u)
-    w[u] = make_uint4(two_half(x[u][0] * scale, x[u][1] * scale), two_half(x[u][2] * scale, x[u][3] * scale),
-                      two_half(x[u][4] * scale, x[u][5] * scale), two_half(x[u][6] * scale, x[u][7] * scale));
-}
-
-__device__ __forceinline__ void scale_store(const OrthoArgs& g, int b, int i0, int j0, const uint4 (&w)[kScalePer],
-                                            __half* s_t) {
-  __half* dst = (g.flip ? g.XT[0] : g.X[0]);
-  __half* dstT = (g.flip ? g.X[0] : g.XT[0]);
-  const int ld = g.flip ? g.ldp : g.ldq, ldT = g.flip ? g.ldq : g.ldp;
-  dst += static_cast<int64_t>(b) * g.m * ld;
-  dstT += static_cast<int64_t>(b) * g.n * ldT;
-  __syncthreads();  // the previous tile has left s_t
-#pragma unroll
-  for (int u = 0; u < kScalePer; ++u) {
-    const int v = u * kThreads + threadIdx.x, r = v / 8, c = v % 8 * 8;
-    if (v >= kScaleVecs) continue;
-    if (i0 + r < g.m) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i0 + r) * ld + j0 + c) = w[u];
-    const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      s_t[(c + k) * kScaleStride + r] = __ushort_as_half(static_cast<uint16_t>(ww[k / 2] >> (16 * (k & 1))));
-  }
-  __syncthreads();
-  for (int v = threadIdx.x; v < kScaleVecs; v += kThreads) {
-    const int c = v / (kScaleRows / 8), r = v % (kScaleRows / 8) * 8;
-    if (j0 + c >= g.n || i0 + r >= ldT) continue;
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(s_t + c * kScaleStride + r);
-    *reinterpret_cast<uint4*>(dstT + static_cast<int64_t>(j0 + c) * ldT + i0 + r) = make_uint4(s[0], s[1], s[2], s[3]);
+    r0 = r1;
   }
 }
 
 // --------------------------------------------------------------------------- the products
 
-// D = alpha P Q^T + beta C; see the top of the file.
+// D = alpha P Q^T + beta C + diag I; see the top of the file.
 struct Product {
   const CUtensorMap *P, *Q;
   const __half* C;       // laid out as D, or null
   __half* D;             // [M, N]; null for the last product (out)
-  __half* DT;            // D transposed [N, M]; symmetric: D itself
-  int64_t strideD, strideDT;  // between matrices, elements
-  int ldD, ldDT, M, N, K;
-  float alpha, beta;
-  bool symmetric;
+  int64_t strideD;       // between matrices, elements
+  int ldD, M, N, K;
+  float alpha, beta, diag;
+  bool symmetric, p_mn, q_mn;  // MN-major operands
 };
 
 __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& maps, int step, int kind) {
   const int cur = step & 1;
+  const bool wide = g.m <= g.n;
   Product r;
-  r.M = g.p;
-  if (kind == 0) {         // A = X X^T
+  r.symmetric = kind < 2;
+  r.M = r.N = r.K = g.p;
+  r.C = nullptr;
+  r.alpha = kUnhold;
+  r.beta = r.diag = 0.f;
+  r.p_mn = r.q_mn = false;
+  r.ldD = g.ldp;
+  if (kind == 0) {         // A
     r.P = r.Q = &maps.X[cur];
-    r.C = nullptr;
-    r.D = r.DT = g.A;
-    r.K = g.q;
-    r.alpha = kUnhold;
-    r.beta = 0.f;
-  } else if (kind == 1) {  // Bm = b A + c A A
+    r.p_mn = r.q_mn = !wide;
+    r.D = g.A;
+    r.K = wide ? g.n : g.m;
+  } else if (kind == 1) {  // Bm
     r.P = r.Q = &maps.A;
     r.C = g.A;
-    r.D = r.DT = g.Bm;
-    r.K = g.p;
+    r.D = g.Bm;
     r.alpha = g.c * kUnhold;
     r.beta = g.b;
-  } else {                 // X <- a X + Bm X
-    r.P = &maps.Bm;
-    r.Q = &maps.XT[cur];
-    r.C = g.X[cur];
+    r.diag = g.a * kHold;
+  } else {                 // X
+    r.P = wide ? &maps.Bm : &maps.X[cur];
+    r.Q = wide ? &maps.X[cur] : &maps.Bm;
+    r.q_mn = wide;
     r.D = step + 1 == g.steps ? nullptr : g.X[cur ^ 1];
-    r.DT = g.XT[cur ^ 1];
-    r.K = g.p;
-    r.alpha = kUnhold;
-    r.beta = g.a;
+    r.M = g.m;
+    r.N = g.n;
+    r.ldD = g.ldx;
   }
-  r.symmetric = kind < 2;
-  r.N = r.symmetric ? g.p : g.q;
-  r.ldD = r.symmetric ? g.ldp : g.ldq;
-  r.ldDT = g.ldp;
-  r.strideD = static_cast<int64_t>(g.p) * r.ldD;
-  r.strideDT = static_cast<int64_t>(r.N) * g.ldp;
+  r.strideD = static_cast<int64_t>(r.M) * r.ldD;
   return r;
 }
 
@@ -479,10 +469,10 @@ struct Bars {
 };
 
 // The grid barrier: every thread's global writes so far are visible to every block's loads
-// after it, TMA loads by thread 0 among them. False once a block gave up (about a second).
+// after it; thread 0, which issues the TMA loads, orders what it has seen before them. False
+// once a block gave up (about a second).
 template <int S>
 __device__ __forceinline__ bool grid_meet(const OrthoArgs& g, Bars<S>* bars, uint32_t* phase) {
-  fence_async_global();
   __syncthreads();
   *phase += 1;
   if (threadIdx.x == 0) {
@@ -522,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_sum[3][kThreads / 32];
   __shared__ float s_scale;
   uint8_t* s_epi = ring + T::kRing;                       // the epilogue warps' staging
-  __half* s_t = reinterpret_cast<__half*>(s_epi);         // scaling: the transposed tile
   Bars<S>* bars = &bars_s;
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -555,31 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int w = blockIdx.x; w < g.batch * g.parts; w += gridDim.x) norm_part(g, w / g.parts, w % g.parts, s_sum);
   bool ok = grid_meet(g, bars, &phase);
   if (ok) {
-    const int nj = (g.n + kScaleCols - 1) / kScaleCols, ni = (g.m + kScaleRows - 1) / kScaleRows;
-    const int items = g.batch * ni * nj;
-    auto load = [&](int w, float (&x)[kScalePer][8]) {
-      const int b = w / (ni * nj), r = w - b * ni * nj;
-      scale_load(g, b, r / nj * kScaleRows, r % nj * kScaleCols, x);
-    };
-    int last = -1;
-    float x[kScalePer][8];
-    if (static_cast<int>(blockIdx.x) < items) load(blockIdx.x, x);
-    for (int w = blockIdx.x; w < items; w += gridDim.x) {
-      const int b = w / (ni * nj), r = w - b * ni * nj;
-      if (b != last) {
-        __syncthreads();
-        if (warp == 0) {
-          const float s = held_scale(g, b);
-          if (lane == 0) s_scale = s;
-        }
-        __syncthreads();
-        last = b;
-      }
-      uint4 packed[kScalePer];
-      scale_pack(s_scale, x, packed);
-      if (w + static_cast<int>(gridDim.x) < items) load(w + gridDim.x, x);
-      scale_store(g, b, r / nj * kScaleRows, r % nj * kScaleCols, packed, s_t);
-    }
+    scale_rows(g, &s_scale);
     ok = grid_meet(g, bars, &phase);
   }
 
@@ -603,16 +568,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t full = smem_addr(&bars->full[stage]);
             const uint32_t dp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes)), dq = dp + T::kPBytes;
-            if constexpr (PAIR) {
-              if (rank == 0) bar_expect(full, 2 * (T::kPBytes + T::kQBytes));
-              const uint32_t full0 = in_cta(full, 0);
-              load_box<true>(dp, pr.P, full0, kb * kBK, i * T::kM + rank * kRowsP, b);
-              load_box<true>(dq, pr.Q, full0, kb * kBK, j * T::kN + rank * T::kRowsQ, b);
-            } else {
-              bar_expect(full, T::kPBytes + T::kQBytes);
-              load_box<false>(dp, pr.P, full, kb * kBK, i * T::kM, b);
-              load_box<false>(dp + T::kPBytes / 2, pr.P, full, kb * kBK, i * T::kM + T::kBox, b);
-              load_box<false>(dq, pr.Q, full, kb * kBK, j * T::kN, b);
+            const uint32_t bar = PAIR ? in_cta(full, 0) : full;
+            if (rank == 0) bar_expect(full, (PAIR ? 2 : 1) * (T::kPBytes + T::kQBytes));
+            const int k0 = kb * kBK;
+            const int p0 = i * T::kM + static_cast<int>(rank) * kRowsP, q0 = j * T::kN + static_cast<int>(rank) * T::kRowsQ;
+#pragma unroll
+            for (int h = 0; h < kRowsP / kBox; ++h) {
+              const int r = p0 + h * kBox;
+              load_box<PAIR>(dp + h * kBoxBytes, pr.P, bar, pr.p_mn ? r : k0, pr.p_mn ? k0 : r, b);
+            }
+#pragma unroll
+            for (int h = 0; h < T::kRowsQ / kBox; ++h) {
+              const int r = q0 + h * kBox;
+              load_box<PAIR>(dq + h * kBoxBytes, pr.Q, bar, pr.q_mn ? r : k0, pr.q_mn ? k0 : r, b);
             }
             if (++stage == S) {
               stage = 0;
@@ -628,6 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (lane == 0 && rank == 0) {
         bool fine = true;
+        const uint32_t idesc = T::kIdesc | (pr.p_mn ? 1u << 15 : 0u) | (pr.q_mn ? 1u << 16 : 0u);
+        // 16 k further: 32 bytes along a K-major row, two 8-k groups of an MN-major box
+        const uint32_t step_p = pr.p_mn ? 2048 >> 4 : 2u, step_q = pr.q_mn ? 2048 >> 4 : 2u;
         for (int t = unit; fine && t < total; t += units) {
           if (!wait<PAIR>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
             fine = false;
@@ -642,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_after();
             const uint32_t sp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes));
-            const uint64_t dp = operand_desc(sp), dq = operand_desc(sp + T::kPBytes);
+            const uint64_t dp = operand_desc(sp, pr.p_mn), dq = operand_desc(sp + T::kPBytes, pr.q_mn);
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)  // 16 columns = 32 bytes = 2 address units
-              mma_f16<PAIR>(d, dp + 2u * k, dq + 2u * k, T::kIdesc, (kb | k) != 0);
+            for (int k = 0; k < kBK / 16; ++k)
+              mma_f16<PAIR>(d, dp + step_p * k, dq + step_q * k, idesc, (kb | k) != 0);
             commit<PAIR>(smem_addr(&bars->empty[stage]));
             if (++stage == S) {
               stage = 0;
@@ -677,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int b, i, j;
         tile_at<PAIR>(pr, per, t, &b, &i, &j);
         const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
-        const bool mirror = !pr.symmetric || j * T::kN >= (i + 1) * T::kM;  // else the tile holds its own mirror image
+        const bool mirror = pr.symmetric && j * T::kN >= (i + 1) * T::kM;  // else the tile holds its own mirror image
         const int col0 = j * T::kN + half * (T::kChunks * 32);
         const bool some = row0 < pr.M;
         const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
@@ -723,6 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          if (pr.diag != 0.f && c0 < row0 + 32 && row0 < c0 + 32) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c0 + k == row0 + lane) x[k] += pr.diag;
+          }
           uint32_t h[16];  // two columns each: fp16, or the result in bf16
           if (pr.D) {
 #pragma unroll
@@ -732,62 +708,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 16; ++k) h[k] = two_bf16(x[2 * k] * s, x[2 * k + 1] * s);
           }
-          // where the rows and the columns of this chunk go: row r at `rows` + r * ldr, column c
-          // at `cols` + c * ldc (16-bit elements); `whole`: in 16-byte pieces
-          uint16_t *rows = nullptr, *cols = nullptr;
-          int64_t ldr = 0, ldc = 0;
+          uint16_t* rows;
+          int64_t ldr;
           bool whole = true;
           if (pr.D) {
             rows = reinterpret_cast<uint16_t*>(pr.D) + b * pr.strideD + static_cast<int64_t>(row0) * pr.ldD + c0;
             ldr = pr.ldD;
-            if (mirror) {
-              cols = reinterpret_cast<uint16_t*>(pr.DT) + b * pr.strideDT + static_cast<int64_t>(c0) * pr.ldDT + row0;
-              ldc = pr.ldDT;
-            }
           } else {
-            uint16_t* out = reinterpret_cast<uint16_t*>(g.out) + b * g.size;
-            if (g.flip) {
-              cols = out + static_cast<int64_t>(c0) * pr.M + row0;
-              ldc = pr.M;
-              whole = g.out_vec && row0 + 32 <= pr.M;
-            } else {
-              rows = out + static_cast<int64_t>(row0) * pr.N + c0;
-              ldr = pr.N;
-              whole = g.out_vec && c0 + 32 <= pr.N;
-            }
+            rows = reinterpret_cast<uint16_t*>(g.out) + b * g.size + static_cast<int64_t>(row0) * pr.N + c0;
+            ldr = pr.N;
+            whole = g.out_vec && c0 + 32 <= pr.N;
           }
           if (!whole) {  // a ragged edge of the result, or one at an odd address
             if (row0 + lane < pr.M)
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (c0 + k < pr.N)
-                  (rows ? rows + lane * ldr + k : cols + k * ldc + lane)[0] =
-                      static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+                if (c0 + k < pr.N) rows[lane * ldr + k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
             __syncwarp();
             continue;
           }
-          if (rows) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) *piece(lane, k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-          }
-          if (cols) {
+          for (int k = 0; k < 4; ++k) *piece(lane, k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+          if (mirror) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               reinterpret_cast<uint16_t*>(s_col)[k * 32 + lane] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
           }
           __syncwarp();
-          if (rows) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (row0 + lr + 8 * k < pr.M)
-                *reinterpret_cast<uint4*>(rows + (lr + 8 * k) * ldr + lc * 8) = *piece(lr + 8 * k, lc);
-          }
-          if (cols) {
-            // (rows past the last one land in the padding up to ldDT)
+          for (int k = 0; k < 4; ++k)
+            if (row0 + lr + 8 * k < pr.M)
+              *reinterpret_cast<uint4*>(rows + (lr + 8 * k) * ldr + lc * 8) = *piece(lr + 8 * k, lc);
+          if (mirror) {  // (rows past the last one land in the padding up to ldD)
+            uint16_t* cols = reinterpret_cast<uint16_t*>(pr.D) + b * pr.strideD + static_cast<int64_t>(c0) * pr.ldD + row0;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (c0 + lr + 8 * k < pr.N)
-                *reinterpret_cast<uint4*>(cols + (lr + 8 * k) * ldc + lc * 8) =
+                *reinterpret_cast<uint4*>(cols + static_cast<int64_t>(lr + 8 * k) * pr.ldD + lc * 8) =
                     reinterpret_cast<const uint4*>(s_col)[(lr + 8 * k) * 4 + lc];
           }
           __syncwarp();
@@ -841,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------ host side
 
-size_t carve_ortho(uint8_t* base, int64_t batch, int p, int q, OrthoArgs* o) {
+size_t carve_ortho(uint8_t* base, int64_t batch, int m, int n, OrthoArgs* o) {
   uint8_t* first = base ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 127) & ~uintptr_t(127)) : nullptr;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -849,26 +806,24 @@ size_t carve_ortho(uint8_t* base, int64_t batch, int p, int q, OrthoArgs* o) {
     at += (bytes + 127) / 128 * 128;
     return ptr;
   };
-  o->ldq = (q + 63) / 64 * 64;  // whole k-blocks: rows start on 128 bytes
+  const int p = std::min(m, n);
+  o->ldx = (n + 63) / 64 * 64;  // rows start on 128 bytes
   o->ldp = (p + 63) / 64 * 64;
   o->ctrl = reinterpret_cast<OrthoCtrl*>(take(sizeof(OrthoCtrl)));
   o->partial = reinterpret_cast<float*>(take(batch * kNormParts * 3 * sizeof(float)));
-  for (int i = 0; i < 2; ++i) {
-    o->X[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldq));
-    o->XT[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * q * o->ldp));
-  }
+  for (int i = 0; i < 2; ++i) o->X[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * m * o->ldx));
   o->A = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
   o->Bm = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
   return at + 128;
 }
 
-// [batch, rows, cols] fp16 with row stride ld, boxes of `box` rows x 64 columns, 128-byte swizzle.
-bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, int ld, int box_rows) {
+// [batch, rows, cols] fp16 with row stride ld, boxes of 64 x 64, 128-byte swizzle.
+bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, int ld) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(rows) * ld * 2};
-  cuuint32_t box[3] = {kBK, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[3] = {kBox, kBox, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -915,22 +870,21 @@ pg_status resident_units(int* units) {
 }
 
 template <bool PAIR>
-pg_status launch_ortho(const OrthoArgs& g, cudaStream_t stream) {
+pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   int units;
   pg_status st = resident_units<PAIR>(&units);
   if (st != PG_OK) return st;
-  constexpr int box = Tile<PAIR>::kBox;
   Maps maps;
-  for (int i = 0; i < 2; ++i)
-    if (!held_map(&maps.X[i], g.X[i], g.batch, g.p, g.q, g.ldq, box) ||
-        !held_map(&maps.XT[i], g.XT[i], g.batch, g.q, g.p, g.ldp, box))
-      return PG_ERR_CUDA;
-  if (!held_map(&maps.A, g.A, g.batch, g.p, g.p, g.ldp, box) || !held_map(&maps.Bm, g.Bm, g.batch, g.p, g.p, g.ldp, box))
+  if (!held_map(&maps.X[0], g.X[0], g.batch, g.m, g.n, g.ldx) || !held_map(&maps.X[1], g.X[1], g.batch, g.m, g.n, g.ldx) ||
+      !held_map(&maps.A, g.A, g.batch, g.p, g.p, g.ldp) || !held_map(&maps.Bm, g.Bm, g.batch, g.p, g.p, g.ldp))
     return PG_ERR_CUDA;
   // no more units than the widest phase has work for: the fewer blocks, the quicker they meet
-  const int64_t tiles = static_cast<int64_t>(g.batch) * std::max(tiles_of<PAIR>(g.p, g.q, false), tiles_of<PAIR>(g.p, g.p, true));
-  const int64_t scale = static_cast<int64_t>(g.batch) * ((g.m + kScaleRows - 1) / kScaleRows) * ((g.n + kScaleCols - 1) / kScaleCols);
-  units = static_cast<int>(std::min<int64_t>(units, std::max(tiles, PAIR ? (scale + 1) / 2 : scale)));
+  const int64_t tiles = static_cast<int64_t>(g.batch) * std::max(tiles_of<PAIR>(g.m, g.n, false), tiles_of<PAIR>(g.p, g.p, true));
+  const int64_t reads = (static_cast<int64_t>(g.batch) * g.size + 8 * kThreads - 1) / (8 * kThreads);  // of the norm and scaling
+  units = static_cast<int>(std::min<int64_t>(units, std::max(tiles, PAIR ? (reads + 1) / 2 : reads)));
+  // one round of partial sums over the blocks
+  const int blocks = (PAIR ? 2 : 1) * units;
+  g.parts = static_cast<int>(std::min<int64_t>({kNormParts, std::max(1, blocks / g.batch), (g.size + 8 * kThreads - 1) / (8 * kThreads)}));
   cudaError_t e = cudaMemsetAsync(g.ctrl, 0, sizeof(OrthoCtrl), stream);
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchAttribute attr[2];
@@ -955,13 +909,14 @@ pg_status launch_ortho(const OrthoArgs& g, cudaStream_t stream) {
 // another by the busiest unit, times the cycles of one (a pair's 512 are its MMAs; a single
 // CTA's ~400 its 24 KB from L2), over a step's three products.
 bool use_pairs(const OrthoArgs& g, int sms) {
-  auto cost = [&](bool pair, int N, int K, bool sym) {
-    const int64_t per = pair ? tiles_of<true>(g.p, N, sym) : tiles_of<false>(g.p, N, sym);
+  const int q = std::max(g.m, g.n);
+  auto cost = [&](bool pair, int M, int N, int K, bool sym) {
+    const int64_t per = pair ? tiles_of<true>(M, N, sym) : tiles_of<false>(M, N, sym);
     const int64_t units = pair ? sms / 2 : sms;
     return (per * g.batch + units - 1) / units * ((K + kBK - 1) / kBK) * (pair ? 512 : 400);
   };
   auto step = [&](bool pair) {
-    return cost(pair, g.p, g.q, true) + cost(pair, g.p, g.p, true) + cost(pair, g.q, g.p, false);
+    return cost(pair, g.p, g.p, q, true) + cost(pair, g.p, g.p, g.p, true) + cost(pair, g.m, g.n, g.p, false);
   };
   return step(true) < step(false);
 }
@@ -975,7 +930,7 @@ extern "C" pg_status pg_orthogonalize_workspace_size(int32_t batch, int32_t m, i
   if (!bytes) return PG_ERR_NULL;
   if (batch < 0 || batch > kMaxBatch || m < 1 || n < 1 || m > kMaxSide || n > kMaxSide) return PG_ERR_SHAPE;
   OrthoArgs o;
-  *bytes = batch == 0 ? 0 : carve_ortho(nullptr, batch, m < n ? m : n, m < n ? n : m, &o);
+  *bytes = batch == 0 ? 0 : carve_ortho(nullptr, batch, m, n, &o);
   return PG_OK;
 }
 
@@ -1001,11 +956,8 @@ extern "C" pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batc
   g.batch = batch;
   g.m = m;
   g.n = n;
-  g.flip = m > n;  // X = G^T
-  g.p = g.flip ? n : m;
-  g.q = g.flip ? m : n;
-  carve_ortho(static_cast<uint8_t*>(workspace), batch, g.p, g.q, &g);
-  g.parts = static_cast<int>(std::min<int64_t>(kNormParts, (g.size + 4095) / 4096));
+  g.p = std::min(m, n);
+  carve_ortho(static_cast<uint8_t*>(workspace), batch, m, n, &g);
   g.steps = steps;
   g.dtype = dtype;
   g.g_vec = n % 8 == 0 && aligned(G, 16);

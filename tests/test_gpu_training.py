@@ -380,7 +380,7 @@ COEFFS = (3.4445, -4.7750, 2.0315)
 
 
 def ortho_reference(G, steps, coeffs=COEFFS, eps=1e-7, scale=1.0, hold=None):
-    """The formulas in 64 bits; `hold` rounds X, A and b A + c A A where the kernel stores them."""
+    """The formulas in 64 bits; `hold` rounds X, A and a I + b A + c A A where the kernel stores them."""
     a, b, c = coeffs
     hold = hold or (lambda x: x)
     outs = []
@@ -389,7 +389,7 @@ def ortho_reference(G, steps, coeffs=COEFFS, eps=1e-7, scale=1.0, hold=None):
         x = hold(x / (torch.linalg.norm(x) + eps))
         for s in range(steps):
             A = hold(x @ x.T)
-            x = a * x + hold(b * A + c * (A @ A)) @ x
+            x = hold(a * torch.eye(len(A), dtype=A.dtype, device=A.device) + b * A + c * (A @ A)) @ x
             if s + 1 < steps:
                 x = hold(x)
         outs.append(scale * (x if g.shape[0] <= g.shape[1] else x.T))
