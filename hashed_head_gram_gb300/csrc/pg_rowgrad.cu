@@ -10,7 +10,11 @@
 //      digits of up to 11 bits, and the segments of equal rows. One cooperative launch; the
 //      blocks meet at a grid barrier between the phases. Every block owns a contiguous share
 //      of the references, so ranks follow from counts alone and no order depends on timing.
-//   2. rowgrad_sum_kernel: the sums, fp32, in ascending order of the references.
+//   2. rowgrad_sum_kernel: the sums, fp32, in ascending order of the references. The sorted
+//      references are cut into tiles of a fixed size, whatever the segments' lengths (one ID
+//      can take a tenth of a batch): a group of lanes walks a tile, writes the rows that lie
+//      wholly in it and leaves the sums of the others for
+//   3. rowgrad_join_kernel, which adds the parts of a row that crosses tiles, in their order.
 #include "pg_async.cuh"
 #include "pg_hash.cuh"
 #include "pg_vec.h"
@@ -56,17 +60,25 @@ struct SortBuffers {
   uint32_t* segs;      // [blocks] segments that start in a block's share
   uint32_t* key[2];    // [n]
   uint32_t* ref[2];    // [n]
+  uint32_t* seg;       // [n] segment of each sorted reference
   uint32_t* seg_start; // [n + 1]
   uint32_t* seg_row;   // [n] (embedding; the hashed lookup's is the caller's rows_out)
   uint64_t* sign;      // [n] sign hashes of the references (hashed lookup)
+  float* parts;        // [tiles][2][r] sums of segments that cross a tile's start, its end
 };
 
 constexpr size_t kCtrlBytes = sizeof(SortCtrl);
 
 inline size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
+// References per tile of the sums: 32, and 8 while 32 would leave the GPU short of warps
+// (kFewLanes lanes of 8 columns: 16 warps an SM).
+constexpr int64_t kFewLanes = 152 * 16 * 32;
+
+inline int tile_refs(int64_t n, int r) { return n * ((r + 7) / 8) / 32 >= kFewLanes ? 32 : 8; }
+
 // Carves the buffers from `base`; returns the bytes they take (base may be null to size them).
-size_t carve(uint8_t* base, int64_t n, bool hashed, SortBuffers* b) {
+size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* p = base ? base + at : nullptr;
@@ -82,9 +94,12 @@ size_t carve(uint8_t* base, int64_t n, bool hashed, SortBuffers* b) {
     b->key[i] = reinterpret_cast<uint32_t*>(take(4 * un));
     b->ref[i] = reinterpret_cast<uint32_t*>(take(4 * un));
   }
+  b->seg = reinterpret_cast<uint32_t*>(take(4 * un));
   b->seg_start = reinterpret_cast<uint32_t*>(take(4 * (un + 1)));
   b->seg_row = hashed ? nullptr : reinterpret_cast<uint32_t*>(take(4 * un));
   b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un)) : nullptr;
+  const size_t T = tile_refs(n, r);
+  b->parts = reinterpret_cast<float*>(take((un + T - 1) / T * 2 * r * sizeof(float)));
   return at;
 }
 
@@ -330,6 +345,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         rows_of[u] = k;
         b.seg_start[u] = i;
       }
+      b.seg[i] = st ? u : u - 1;  // (padding: unused)
       if (k != none && (i + 1 == n || __ldcg(key + i + 1) == none)) b.seg_start[count] = i + 1;
       if (HASHED && i >= count) rows_out[i] = kNoRow;
     }
@@ -351,46 +367,165 @@ struct SumArgs {
   const void* grad;          // summands, rows of r values; reference i has row i / share
   const uint64_t* sign;      // sign hashes of the references, or null
   const uint32_t* ref;       // references in sorted order
+  const uint32_t* seg;       // their segments
   const uint32_t* seg_start;
   const uint32_t* seg_row;   // output row of a segment; null: the segment's number
   const SortCtrl* ctrl;
+  float* parts;
   void* out;
   uint32_t n, share, blocks; // blocks: of the sort (all have to have finished)
+  uint32_t tiles;
   int32_t r, accumulate;
   float scale;
 };
 
-// One warp per segment and 32 * COLS columns.
-template <int IN, int OUT, int COLS>
-__global__ void __launch_bounds__(256) rowgrad_sum_kernel(SumArgs a) {
-  if (a.ctrl->done != a.blocks) return;
-  const int lane = threadIdx.x & 31;
-  const uint32_t u = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int c = (blockIdx.y * 32 + lane) * COLS;
-  const uint32_t count = a.ctrl->count;
-  if (c >= a.r || u >= (a.seg_row ? count : a.n)) return;
-  float acc[COLS] = {};
-  if (u < count) {
-    const uint32_t end = a.seg_start[u + 1];
-    for (uint32_t i = a.seg_start[u]; i < end; ++i) {
-      const uint32_t ref = a.ref[i];
-      float x[COLS];
-      load_cols<IN, COLS>(a.grad, static_cast<int64_t>(ref / a.share) * a.r + c, x);
-      uint32_t neg = 0;
-      if (a.sign) neg = static_cast<uint32_t>(mix64(a.sign[ref] + kGolden * ((c >> 6) + 1)) >> (c & 63));
-#pragma unroll
-      for (int j = 0; j < COLS; ++j) acc[j] += ((neg >> j) & 1u) ? -x[j] : x[j];
-    }
-  }
-  const int64_t at = static_cast<int64_t>(a.seg_row ? a.seg_row[u] : u) * a.r + c;
+template <int OUT, int COLS>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t u, int c, const float (&acc)[COLS]) {
+  const int64_t at = static_cast<int64_t>(a.seg_row ? __ldg(a.seg_row + u) : u) * a.r + c;
   float y[COLS] = {};
-  if (a.accumulate) load_cols<OUT, COLS>(a.out, at, y);
+  if (a.accumulate) read_cols<OUT, COLS>(a.out, at, y);
 #pragma unroll
   for (int j = 0; j < COLS; ++j) y[j] = fmaf(acc[j], a.scale, y[j]);
   store_cols<OUT, COLS>(a.out, at, y);
 }
 
-using SumFn = void (*)(SumArgs);
+// A group of `lanes` lanes (a power of two) per tile of T references and lanes * COLS columns.
+template <int IN, int OUT, int COLS>
+__global__ void __launch_bounds__(256) rowgrad_sum_kernel(const SumArgs a, int lanes, int T) {
+  if (a.ctrl->done != a.blocks) return;
+  const int per_block = 256 / lanes;
+  const uint32_t tile = blockIdx.x * per_block + threadIdx.x / lanes;
+  const int c = (blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * COLS;
+  if (tile >= a.tiles || c >= a.r) return;
+  const uint32_t count = a.ctrl->count;
+  const uint32_t p0 = tile * T, p1 = min(p0 + T, __ldg(a.seg_start + count));
+  if (!a.seg_row) {  // rows past the last segment are zero: row p for each position p of the tile
+    const float zero[COLS] = {};
+    for (uint32_t u = max(p0, count); u < min(p0 + T, a.n); ++u)
+      store_cols<OUT, COLS>(a.out, static_cast<int64_t>(u) * a.r + c, zero);
+  }
+  if (p0 >= p1) return;
+  const uint32_t first = __ldg(a.seg + p0), last = __ldg(a.seg + p1 - 1);
+  const bool from_before = __ldg(a.seg_start + first) < p0;
+  const bool goes_on = __ldg(a.seg_start + last + 1) > p1;
+  float* part = a.parts + static_cast<int64_t>(tile) * 2 * a.r + c;
+  float acc[COLS] = {};
+  uint32_t cur = first;
+  constexpr int kFly = 8;  // rows in flight
+  for (uint32_t q0 = p0; q0 < p1; q0 += kFly) {
+    uint32_t seg[kFly];
+    float x[kFly][COLS];
+    uint64_t hs[kFly];
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      seg[k] = last;
+      if (q0 + k < p1) {
+        const uint32_t ref = __ldg(a.ref + q0 + k);
+        seg[k] = __ldg(a.seg + q0 + k);
+        load_cols<IN, COLS>(a.grad, static_cast<int64_t>(a.share == 1 ? ref : ref / a.share) * a.r + c, x[k]);
+        hs[k] = a.sign ? __ldg(a.sign + ref) : 0ull;
+      } else {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) x[k][j] = 0.f;
+        hs[k] = 0ull;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      if (seg[k] != cur) {
+        if (cur == first && from_before) {
+          store_cols<PG_F32, COLS>(part, 0, acc);
+        } else {
+          write_row<OUT, COLS>(a, cur, c, acc);
+        }
+        cur = seg[k];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      }
+      uint32_t neg = 0;
+      if (a.sign) neg = static_cast<uint32_t>(mix64(hs[k] + kGolden * ((c >> 6) + 1)) >> (c & 63));
+#pragma unroll
+      for (int j = 0; j < COLS; ++j)
+        acc[j] += __uint_as_float(__float_as_uint(x[k][j]) ^ ((neg << (31 - j)) & 0x80000000u));
+    }
+  }
+  if (cur == first && from_before) {
+    store_cols<PG_F32, COLS>(part, 0, acc);
+  } else if (goes_on) {
+    store_cols<PG_F32, COLS>(part, a.r, acc);
+  } else {
+    write_row<OUT, COLS>(a, cur, c, acc);
+  }
+}
+
+// Rows that cross tiles: the tile a row starts in adds its parts. A group of lanes per tile, as
+// above; a row of more than kLongRow tiles is added by the whole block, group k taking every
+// per_block-th part (at most one such row starts in a block's tiles: a block has no more than
+// kLongRow of them).
+constexpr int kLongRow = 256;
+
+template <int OUT, int COLS>
+__global__ void __launch_bounds__(256) rowgrad_join_kernel(const SumArgs a, int lanes, int T) {
+  __shared__ float s_acc[256][COLS];
+  __shared__ uint32_t s_long;
+  if (a.ctrl->done != a.blocks) return;
+  const int per_block = 256 / lanes, group = threadIdx.x / lanes;
+  const uint32_t tile = blockIdx.x * per_block + group;
+  const int c = (blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * COLS;
+  if (threadIdx.x == 0) s_long = kNoRow;
+  __syncthreads();
+  const uint32_t nvalid = __ldg(a.seg_start + a.ctrl->count);
+  const uint32_t p0 = tile * T, p1 = p0 + T;
+  constexpr int kFly = 4;
+  auto add = [&](uint32_t k, uint32_t end, uint32_t step, float (&acc)[COLS]) {  // first parts of tiles k, k + step, ..
+    for (; k < end; k += kFly * step) {
+      float x[kFly][COLS];
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) x[f][j] = 0.f;
+        if (k + f * step < end) load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(k + f * step) * 2 * a.r + c, x[f]);
+      }
+#pragma unroll
+      for (int f = 0; f < kFly; ++f)
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) acc[j] += x[f][j];
+    }
+  };
+  if (tile < a.tiles && p1 < nvalid) {
+    const uint32_t u = __ldg(a.seg + p1);
+    if (__ldg(a.seg + p1 - 1) == u && __ldg(a.seg_start + u) >= p0) {
+      const uint32_t end = (__ldg(a.seg_start + u + 1) - 1) / T + 1;
+      if (end - tile > kLongRow) {
+        s_long = tile;
+      } else if (c < a.r) {
+        float acc[COLS];
+        load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(tile) * 2 * a.r + a.r + c, acc);
+        add(tile + 1, end, 1, acc);
+        write_row<OUT, COLS>(a, u, c, acc);
+      }
+    }
+  }
+  __syncthreads();
+  if (s_long == kNoRow) return;
+  const uint32_t u = __ldg(a.seg + (s_long + 1) * T), end = (__ldg(a.seg_start + u + 1) - 1) / T + 1;
+  float acc[COLS] = {};
+  if (c < a.r) {
+    if (group == 0) load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(s_long) * 2 * a.r + a.r + c, acc);
+    add(s_long + 1 + group, end, per_block, acc);
+  }
+#pragma unroll
+  for (int j = 0; j < COLS; ++j) s_acc[threadIdx.x][j] = acc[j];
+  __syncthreads();
+  if (group == 0 && c < a.r) {
+    for (int k = 1; k < per_block; ++k)
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] += s_acc[k * lanes + threadIdx.x][j];
+    write_row<OUT, COLS>(a, u, c, acc);
+  }
+}
+
+using SumFn = void (*)(SumArgs, int, int);
 
 template <int COLS>
 SumFn sum_fn(int in, int out) {
@@ -399,12 +534,17 @@ SumFn sum_fn(int in, int out) {
   return out == PG_F32 ? rowgrad_sum_kernel<PG_BF16, PG_F32, COLS> : rowgrad_sum_kernel<PG_BF16, PG_BF16, COLS>;
 }
 
+template <int COLS>
+SumFn join_fn(int out) {
+  return out == PG_F32 ? rowgrad_join_kernel<PG_F32, COLS> : rowgrad_join_kernel<PG_BF16, COLS>;
+}
+
 // Sorts the references and writes the sums. n >= 1; `keys` the largest key.
 template <bool HASHED>
 pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs a, int in, int out, void* workspace,
                         uint32_t* rows_out, int32_t* count_out, cudaStream_t stream) {
   SortBuffers b;
-  carve(static_cast<uint8_t*>(workspace), n, HASHED, &b);
+  carve(static_cast<uint8_t*>(workspace), n, a.r, HASHED, &b);
   int key_bits = 1;
   while (key_bits < 32 && (keys >> key_bits)) ++key_bits;
   const int passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
@@ -436,17 +576,26 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   if (st != PG_OK) return st;
 
   a.ref = b.ref[passes & 1];
+  a.seg = b.seg;
   a.seg_start = b.seg_start;
   a.seg_row = b.seg_row;
   a.sign = b.sign;
   a.ctrl = b.ctrl;
+  a.parts = b.parts;
   a.n = n;
   a.blocks = G;
+  const int T = tile_refs(n, a.r);
+  a.tiles = (n + T - 1) / T;
   const bool vec = a.r % 8 == 0 && aligned(a.grad, 16) && aligned(a.out, 16);
-  const int cols = 32 * (vec ? 8 : 1);
-  const uint32_t segs = HASHED ? n : min(n, keys);
-  const dim3 grid((segs + 7) / 8, (a.r + cols - 1) / cols);
-  (vec ? sum_fn<8>(in, out) : sum_fn<1>(in, out))<<<grid, 256, 0, stream>>>(a);
+  const int cols = vec ? 8 : 1;
+  int lanes = 1;
+  while (lanes < 32 && lanes * cols < a.r) lanes *= 2;
+  const uint32_t per_block = 256 / lanes;
+  const dim3 grid((a.tiles + per_block - 1) / per_block, (a.r + lanes * cols - 1) / (lanes * cols));
+  (vec ? sum_fn<8>(in, out) : sum_fn<1>(in, out))<<<grid, 256, 0, stream>>>(a, lanes, T);
+  st = after_launch(1);
+  if (st != PG_OK) return st;
+  (vec ? join_fn<8>(out) : join_fn<1>(out))<<<grid, 256, 0, stream>>>(a, lanes, T);
   return after_launch(1);
 }
 
@@ -460,7 +609,7 @@ extern "C" pg_status pg_embed_grad_workspace_size(int64_t N, int64_t rows, int32
   if (N < 0 || N >= (1ll << 31) || rows < 1 || rows >= (1ll << 31) || d < 1 || d > kMaxEmbedWidth)
     return PG_ERR_SHAPE;
   SortBuffers b;
-  *bytes = N == 0 ? 0 : carve(nullptr, N, false, &b);
+  *bytes = N == 0 ? 0 : carve(nullptr, N, d, false, &b);
   return PG_OK;
 }
 
@@ -512,7 +661,7 @@ extern "C" pg_status pg_lookup_grad_workspace_size(const pg_table_desc* desc, in
   if (st != PG_OK) return st;
   if (N < 0 || N * g.O * g.H >= (1ll << 31)) return PG_ERR_SHAPE;
   SortBuffers b;
-  *bytes = N == 0 ? 0 : carve(nullptr, N * g.O * g.H, true, &b);
+  *bytes = N == 0 ? 0 : carve(nullptr, N * g.O * g.H, desc->r, true, &b);
   return PG_OK;
 }
 

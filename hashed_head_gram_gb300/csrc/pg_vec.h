@@ -54,6 +54,15 @@ __device__ __forceinline__ void load_cols(const void* __restrict__ base, int64_t
   }
 }
 
+// The same from memory that this kernel writes (no read-only cache).
+template <int DT, int COLS>
+__device__ __forceinline__ void read_cols(const void* base, int64_t at, float (&x)[COLS]) {
+#pragma unroll
+  for (int j = 0; j < COLS; ++j)
+    x[j] = DT == PG_F32 ? static_cast<const float*>(base)[at + j]
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at + j]);
+}
+
 __device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
