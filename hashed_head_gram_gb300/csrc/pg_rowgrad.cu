@@ -23,20 +23,23 @@ namespace pg {
 namespace {
 
 constexpr int kErrGradBarrier = 131072;  // device error bit: a block gave up at the grid barrier
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 8;                          // references a thread holds per tile
-constexpr int kSortTile = kSortThreads * kSortItems;   // 4096
+constexpr int kSortTile = kSortThreads * kSortItems;   // 8192
 constexpr int kMaxDigitBits = 11;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
+constexpr int kDigitsPerThread = kMaxDigits / kSortThreads;
 constexpr int kMaxSortBlocks = 152;                    // one per SM
-constexpr int kRefsPerBlock = 2048;                    // at least, before another block joins
+constexpr int kScanIters = (kMaxSortBlocks + 31) / 32;
+constexpr uint32_t kRefsPerBlock = 4096;               // at least, before another block joins
+constexpr uint32_t kDirectCounts = 16384;              // counts that every block reads for itself
 constexpr int kHashItems = 32;                         // (order, head) items of a table
 
 struct SortCtrl {
   uint32_t barrier;  // arrivals at the grid barrier, all phases
   uint32_t done;     // blocks that finished the sort
-  uint32_t count;    // segments
+  uint32_t count;    // segments (hashed lookup)
   uint32_t pad[61];
 };
 
@@ -60,11 +63,8 @@ struct SortBuffers {
   uint32_t* segs;      // [blocks] segments that start in a block's share
   uint32_t* key[2];    // [n]
   uint32_t* ref[2];    // [n]
-  uint32_t* seg;       // [n] segment of each sorted reference
-  uint32_t* seg_start; // [n + 1]
-  uint32_t* seg_row;   // [n] (embedding; the hashed lookup's is the caller's rows_out)
   uint64_t* sign;      // [n] sign hashes of the references (hashed lookup)
-  float* parts;        // [tiles][2][r] sums of segments that cross a tile's start, its end
+  float* parts;        // [tiles][2][r] sums of rows that cross a tile's start, its end
 };
 
 constexpr size_t kCtrlBytes = sizeof(SortCtrl);
@@ -72,7 +72,7 @@ constexpr size_t kCtrlBytes = sizeof(SortCtrl);
 inline size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
 // References per tile of the sums: 32, and 8 while 32 would leave the GPU short of warps
-// (kFewLanes lanes of 8 columns: 16 warps an SM).
+// (lanes of 8 columns: 16 warps an SM).
 constexpr int64_t kFewLanes = 152 * 16 * 32;
 
 inline int tile_refs(int64_t n, int r) { return n * ((r + 7) / 8) / 32 >= kFewLanes ? 32 : 8; }
@@ -94,9 +94,6 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
     b->key[i] = reinterpret_cast<uint32_t*>(take(4 * un));
     b->ref[i] = reinterpret_cast<uint32_t*>(take(4 * un));
   }
-  b->seg = reinterpret_cast<uint32_t*>(take(4 * un));
-  b->seg_start = reinterpret_cast<uint32_t*>(take(4 * (un + 1)));
-  b->seg_row = hashed ? nullptr : reinterpret_cast<uint32_t*>(take(4 * un));
   b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un)) : nullptr;
   const size_t T = tile_refs(n, r);
   b->parts = reinterpret_cast<float*>(take((un + T - 1) / T * 2 * r * sizeof(float)));
@@ -151,32 +148,113 @@ __device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* s_warp
   if (lane == 31) s_warp[w] = inc;
   __syncthreads();
   if (w == 0) {
-    const uint32_t x = lane < kSortWarps ? s_warp[lane] : 0u;
+    const uint32_t x = s_warp[lane];
     const uint32_t xi = warp_incl_scan(x, lane);
-    if (lane < kSortWarps) s_warp[lane] = xi - x;
-    if (lane == kSortWarps - 1) s_warp[kSortWarps] = xi;
+    s_warp[lane] = xi - x;
+    if (lane == 31) s_warp[kSortWarps] = xi;
   }
   __syncthreads();
   *total = s_warp[kSortWarps];
   return s_warp[w] + inc - v;
 }
+static_assert(kSortWarps == 32, "block_excl_scan: one lane a warp");
+
+// What a block keeps of a tile of references between counting and scattering. A warp holds
+// 32 * items consecutive references, lane l the l-th of each 32.
+struct Held {
+  uint32_t key[kSortItems], ref[kSortItems];
+  uint32_t rank[kSortItems];  // among the warp's references of the same digit
+};
+
+__device__ __forceinline__ int tile_items(uint32_t left) {
+  return static_cast<int>((min(left, static_cast<uint32_t>(kSortTile)) + kSortThreads - 1) / kSortThreads);
+}
+
+// Ranks a tile's references by the digit of `key`, stably, with per-warp counts in s_cnt
+// [warps][digits], which become exclusive offsets over the warps; totals[q] gets the tile's
+// count of digit q * threads + tid. Equal digits of a warp meet by one ballot a bit.
+__device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end, int items, int shift, int bits,
+                                          uint16_t* s_cnt, uint32_t (&totals)[kDigitsPerThread]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int digits = 1 << bits;
+  const uint32_t mask = static_cast<uint32_t>(digits - 1);
+  __syncthreads();  // whoever used s_cnt is done
+  uint32_t* clear = reinterpret_cast<uint32_t*>(s_cnt);
+  for (int w = tid; w < kSortWarps * digits / 2; w += kSortThreads) clear[w] = 0;
+  __syncthreads();
+  uint16_t* cnt = s_cnt + warp * digits;
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    if (j >= items) break;
+    const bool in = first + j * 32 + lane < end;
+    const uint32_t dig = (h.key[j] >> shift) & mask;
+    uint32_t peers = __ballot_sync(0xffffffffu, in);
+    for (int q = 0; q < bits; ++q) {
+      const bool bit = (dig >> q) & 1u;
+      const uint32_t set = __ballot_sync(0xffffffffu, bit);
+      peers &= bit ? set : ~set;
+    }
+    const uint32_t before = in ? cnt[dig] : 0u;
+    h.rank[j] = before + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (in && lane == 31 - __clz(peers)) cnt[dig] = static_cast<uint16_t>(before + __popc(peers));
+    __syncwarp();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kDigitsPerThread; ++q) {
+    const int d = q * kSortThreads + tid;
+    uint32_t run = 0;
+    if (d < digits) {
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = s_cnt[w * digits + d];
+        s_cnt[w * digits + d] = static_cast<uint16_t>(run);
+        run += c;
+      }
+    }
+    totals[q] = run;
+  }
+}
+
+// The reference's row (and, hashed lookup, its sign hash) on the first pass.
+template <bool HASHED>
+__device__ __forceinline__ uint32_t first_key(const RefSource& src, const ItemConst* s_ic, uint64_t* sign, uint32_t i) {
+  uint32_t key;
+  if constexpr (HASHED) {
+    const uint32_t tok = i / src.items;
+    uint64_t hs;
+    key = item_row(s_ic[i - tok * src.items], src.mode, src.tokens, src.canon_map, src.vocab, tok, tok % src.L, src.err,
+                   &hs);
+    sign[i] = hs;
+  } else {
+    key = embed_row(src.tokens, src.canon_map, src.vocab, src.rows, i);
+    if (key == kNoRow) {
+      key = src.rows;
+      if (src.err) atomicMin(reinterpret_cast<unsigned int*>(src.err), i);
+    }
+  }
+  return key;
+}
 
 template <bool HASHED>
 __global__ void __launch_bounds__(kSortThreads, 1)
-    rowgrad_sort_kernel(const __grid_constant__ RefSource src, SortBuffers b, uint32_t n, uint32_t share, int passes,
-                        int bits, uint32_t* __restrict__ rows_out, int32_t* __restrict__ count_out, int* err_word) {
+    rowgrad_sort_kernel(const __grid_constant__ RefSource src, const __grid_constant__ SortBuffers b, uint32_t n,
+                        uint32_t share, int passes, int bits, uint32_t* __restrict__ rows_out,
+                        int32_t* __restrict__ count_out, int* err_word) {
   extern __shared__ __align__(16) uint8_t s_raw[];
-  uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);                    // [warps][digits]
+  uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);                                 // [warps][digits]
   uint32_t* s_base = reinterpret_cast<uint32_t*>(s_raw + kSortWarps * kMaxDigits * 2);  // [digits]
   __shared__ uint32_t s_warp[kSortWarps + 1];
+  __shared__ uint32_t s_first;
   __shared__ int s_ok;
   __shared__ ItemConst s_ic[HASHED ? kHashItems : 1];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t lo = min(n, blockIdx.x * share), hi = min(n, lo + share);
   const int digits = 1 << bits;
-  const uint32_t mask = static_cast<uint32_t>(digits - 1);
   const uint32_t G = gridDim.x;
+  const bool one = share <= kSortTile;  // the share stays in registers between counting and scattering
   uint32_t phase = 0;
 
   if (HASHED) {
@@ -186,179 +264,201 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     __syncthreads();
   }
 
-  int cur = 0;  // buffer that holds the references in the current order
+  uint32_t *key_in = b.key[0], *key_out = b.key[1], *ref_in = b.ref[0], *ref_out = b.ref[1];
   for (int p = 0; p < passes; ++p) {
     const int shift = p * bits;
-    // ---- how many references of this share have each digit
-    for (int d = tid; d < digits; d += kSortThreads) s_base[d] = 0;
-    __syncthreads();
-    for (uint32_t i = lo + tid; i < hi; i += kSortThreads) {
-      uint32_t key;
-      if (p == 0) {
-        if constexpr (HASHED) {
-          const uint32_t tok = i / src.items;
-          uint64_t hs;
-          key = item_row(s_ic[i - tok * src.items], src.mode, src.tokens, src.canon_map, src.vocab, tok, tok % src.L,
-                         src.err, &hs);
-          b.sign[i] = hs;
-        } else {
-          key = embed_row(src.tokens, src.canon_map, src.vocab, src.rows, i);
-          if (key == kNoRow) {
-            key = src.rows;
-            if (src.err) atomicMin(reinterpret_cast<unsigned int*>(src.err), i);
-          }
-        }
-        b.key[0][i] = key;
-      } else {
-        key = __ldcg(b.key[cur] + i);
-      }
-      atomicAdd(&s_base[(key >> shift) & mask], 1u);
-    }
-    __syncthreads();
-    for (int d = tid; d < digits; d += kSortThreads) b.hist[d * G + blockIdx.x] = s_base[d];
-    if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-
-    // ---- per digit: exclusive scan of its counts over the blocks, and its total
-    for (int d = blockIdx.x * kSortWarps + warp; d < digits; d += G * kSortWarps) {
-      uint32_t run = 0;
-      for (uint32_t k0 = 0; k0 < G; k0 += 32) {
-        const uint32_t k = k0 + lane;
-        const uint32_t v = k < G ? __ldcg(b.hist + d * G + k) : 0u;
-        const uint32_t inc = warp_incl_scan(v, lane);
-        if (k < G) b.hist[d * G + k] = run + inc - v;
-        run += __shfl_sync(0xffffffffu, inc, 31);
-      }
-      if (lane == 0) b.totals[d] = run;
-    }
-    if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-
-    // ---- where this block's first reference of each digit goes
-    uint32_t carry = 0;
-    for (int d0 = 0; d0 < digits; d0 += kSortThreads) {
-      const int d = d0 + tid;
-      const uint32_t v = d < digits ? __ldcg(b.totals + d) : 0u;
-      uint32_t total;
-      const uint32_t ex = block_excl_scan(v, s_warp, &total);
-      if (d < digits) s_base[d] = carry + ex + __ldcg(b.hist + d * G + blockIdx.x);
-      carry += total;
-    }
-
-    // ---- scatter, tile by tile; a warp holds 32 * items consecutive references
+    Held h;
+    uint32_t mine[kDigitsPerThread];  // this share's counts of digits q * threads + tid
+#pragma unroll
+    for (int q = 0; q < kDigitsPerThread; ++q) mine[q] = 0;
+    // ---- ranks and counts. A share of several tiles is read again for the scatter.
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
-      const uint32_t left = min(hi - t0, static_cast<uint32_t>(kSortTile));
-      const int items = static_cast<int>((left + kSortThreads - 1) / kSortThreads);
-      uint32_t key[kSortItems], ref[kSortItems], rank[kSortItems];
-      const uint32_t first = t0 + warp * 32 * items;
+      const int items = tile_items(hi - t0);
+      const uint32_t first = t0 + warp * 32 * items, end = min(hi, t0 + kSortTile);
 #pragma unroll
       for (int j = 0; j < kSortItems; ++j) {
         const uint32_t i = first + j * 32 + lane;
-        const bool in = j < items && i < t0 + left;
-        key[j] = in ? __ldcg(b.key[cur] + i) : 0u;
-        ref[j] = in ? (p == 0 ? i : __ldcg(b.ref[cur] + i)) : 0u;
-      }
-      __syncthreads();  // the previous tile is done with s_cnt and s_base
-      uint32_t* clear = reinterpret_cast<uint32_t*>(s_cnt);
-      for (int w = tid; w < kSortWarps * digits / 2; w += kSortThreads) clear[w] = 0;
-      __syncthreads();
-      uint16_t* cnt = s_cnt + warp * digits;
-#pragma unroll
-      for (int j = 0; j < kSortItems; ++j) {
-        const bool in = j < items && first + j * 32 + lane < t0 + left;
-        const uint32_t dig = (key[j] >> shift) & mask;
-        uint32_t peers = __ballot_sync(0xffffffffu, in);
-        for (int q = 0; q < bits; ++q) {
-          const bool bit = (dig >> q) & 1u;
-          const uint32_t set = __ballot_sync(0xffffffffu, bit);
-          peers &= bit ? set : ~set;
+        const bool in = j < items && i < end;
+        h.key[j] = 0;
+        h.ref[j] = i;
+        if (in && p == 0) {
+          h.key[j] = first_key<HASHED>(src, s_ic, b.sign, i);
+          if (!one) key_in[i] = h.key[j];
+        } else if (in) {
+          h.key[j] = __ldcg(key_in + i);
+          if (one) h.ref[j] = __ldcg(ref_in + i);
         }
-        const uint32_t before = in ? cnt[dig] : 0u;
-        rank[j] = before + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (in && lane == 31 - __clz(peers)) cnt[dig] = static_cast<uint16_t>(before + __popc(peers));
-        __syncwarp();
       }
-      __syncthreads();
-      // per digit: the tile's counts over its warps become offsets
-      uint32_t tile_total[kMaxDigits / kSortThreads];
+      uint32_t totals[kDigitsPerThread];
+      rank_tile(h, first, end, items, shift, bits, s_cnt, totals);
 #pragma unroll
-      for (int q = 0; q < kMaxDigits / kSortThreads; ++q) {
+      for (int q = 0; q < kDigitsPerThread; ++q) mine[q] += totals[q];
+    }
+
+    // ---- where this block's first reference of each digit goes: the digits before it, and the
+    // same digit in the blocks before it
+    uint32_t below[kDigitsPerThread], total_of[kDigitsPerThread];
+    if (G == 1) {
+#pragma unroll
+      for (int q = 0; q < kDigitsPerThread; ++q) {
+        below[q] = 0;
+        total_of[q] = mine[q];
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kDigitsPerThread; ++q) {
         const int d = q * kSortThreads + tid;
-        uint32_t run = 0;
-        if (d < digits) {
+        if (d < digits) b.hist[d * G + blockIdx.x] = mine[q];
+      }
+      if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+      if (digits * G <= kDirectCounts) {
 #pragma unroll
-          for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = s_cnt[w * digits + d];
-            s_cnt[w * digits + d] = static_cast<uint16_t>(run);
-            run += c;
+        for (int q = 0; q < kDigitsPerThread; ++q) {
+          const int d = q * kSortThreads + tid;
+          below[q] = total_of[q] = 0;
+          if (d < digits)
+#pragma unroll 8
+            for (uint32_t k = 0; k < G; ++k) {
+              const uint32_t v = __ldcg(b.hist + d * G + k);
+              if (k < blockIdx.x) below[q] += v;
+              total_of[q] += v;
+            }
+        }
+      } else {  // one warp a digit scans its counts over the blocks
+        for (int d = blockIdx.x * kSortWarps + warp; d < digits; d += G * kSortWarps) {
+          uint32_t v[kScanIters], run = 0;
+#pragma unroll
+          for (int k = 0; k < kScanIters; ++k) v[k] = k * 32 + lane < G ? __ldcg(b.hist + d * G + k * 32 + lane) : 0u;
+#pragma unroll
+          for (int k = 0; k < kScanIters; ++k) {
+            const uint32_t inc = warp_incl_scan(v[k], lane);
+            if (k * 32 + lane < G) b.hist[d * G + k * 32 + lane] = run + inc - v[k];
+            run += __shfl_sync(0xffffffffu, inc, 31);
           }
+          if (lane == 0) b.totals[d] = run;
         }
-        tile_total[q] = run;
-      }
-      __syncthreads();
+        if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
 #pragma unroll
-      for (int j = 0; j < kSortItems; ++j) {
-        if (j < items && first + j * 32 + lane < t0 + left) {
-          const uint32_t dig = (key[j] >> shift) & mask;
-          const uint32_t to = s_base[dig] + cnt[dig] + rank[j];
-          b.key[cur ^ 1][to] = key[j];
-          b.ref[cur ^ 1][to] = ref[j];
+        for (int q = 0; q < kDigitsPerThread; ++q) {
+          const int d = q * kSortThreads + tid;
+          below[q] = d < digits ? __ldcg(b.hist + d * G + blockIdx.x) : 0u;
+          total_of[q] = d < digits ? __ldcg(b.totals + d) : 0u;
         }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kMaxDigits / kSortThreads; ++q) {
-        const int d = q * kSortThreads + tid;
-        if (d < digits) s_base[d] += tile_total[q];
       }
     }
-    cur ^= 1;
-    if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+    uint32_t carry = 0;
+#pragma unroll
+    for (int q = 0; q < kDigitsPerThread; ++q) {
+      const int d = q * kSortThreads + tid;
+      if (q * kSortThreads >= digits) break;
+      uint32_t total;
+      const uint32_t ex = block_excl_scan(total_of[q], s_warp, &total);
+      if (d < digits) s_base[d] = carry + ex + below[q];
+      carry += total;
+    }
+    __syncthreads();
+
+    // ---- scatter
+    const uint32_t mask = static_cast<uint32_t>(digits - 1);
+    for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
+      const int items = tile_items(hi - t0);
+      const uint32_t first = t0 + warp * 32 * items, end = min(hi, t0 + kSortTile);
+      uint32_t totals[kDigitsPerThread];
+      if (!one) {
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+          const uint32_t i = first + j * 32 + lane;
+          const bool in = j < items && i < end;
+          h.key[j] = in ? __ldcg(key_in + i) : 0u;
+          h.ref[j] = in && p > 0 ? __ldcg(ref_in + i) : i;
+        }
+        rank_tile(h, first, end, items, shift, bits, s_cnt, totals);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < kSortItems; ++j) {
+        if (j < items && first + j * 32 + lane < end) {
+          const uint32_t dig = (h.key[j] >> shift) & mask;
+          const uint32_t to = s_base[dig] + s_cnt[warp * digits + dig] + h.rank[j];
+          key_out[to] = h.key[j];
+          ref_out[to] = h.ref[j];
+        }
+      }
+      if (!one) {
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kDigitsPerThread; ++q) {
+          const int d = q * kSortThreads + tid;
+          if (d < digits) s_base[d] += totals[q];
+        }
+      }
+    }
+    uint32_t* t = key_in;
+    key_in = key_out;
+    key_out = t;
+    t = ref_in;
+    ref_in = ref_out;
+    ref_out = t;
+    if ((HASHED || p + 1 < passes) && !grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
   }
 
-  // ---- segments of equal rows; the embedding's padding (key = rows) sorts last and has none
-  const uint32_t* key = b.key[cur];
-  const uint32_t none = HASHED ? kNoRow : src.rows;
-  auto starts = [&](uint32_t i) {
-    const uint32_t k = __ldcg(key + i);
-    return k != none && (i == 0 || __ldcg(key + i - 1) != k);
-  };
-  uint32_t mine = 0, total;
-  for (uint32_t i = lo + tid; i < hi; i += kSortThreads) mine += starts(i);
-  block_excl_scan(mine, s_warp, &total);
-  if (tid == 0) b.segs[blockIdx.x] = total;
-  if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-  __shared__ uint32_t s_first;
-  const uint32_t ex = block_excl_scan(tid < G ? __ldcg(b.segs + tid) : 0u, s_warp, &total);
-  if (tid == blockIdx.x) s_first = ex;
-  __syncthreads();
-  const uint32_t count = total;
-  uint32_t u0 = s_first;
-  uint32_t* rows_of = HASHED ? rows_out : b.seg_row;
-  for (uint32_t t0 = lo; t0 < hi; t0 += kSortThreads) {
-    const uint32_t i = t0 + tid;
-    const bool st = i < hi && starts(i);
-    uint32_t in_tile;
-    const uint32_t u = u0 + block_excl_scan(st, s_warp, &in_tile);
-    if (i < hi) {
-      const uint32_t k = __ldcg(key + i);
-      if (st) {
-        rows_of[u] = k;
-        b.seg_start[u] = i;
+  if constexpr (HASHED) {
+    // ---- segments of equal rows: their numbers replace the keys (into the free buffer), the rows
+    // go to rows_out. A thread takes 8 consecutive references at a time.
+    auto flags = [&](uint32_t i, uint32_t (&k)[8]) -> uint32_t {  // bit j: a segment starts at i + j
+      uint32_t prev = i > 0 && i < hi ? __ldcg(key_in + i - 1) : 0u, f = 0;
+      if (i + 8 <= hi) {  // shares start at multiples of 8
+        const uint4 x = __ldcg(reinterpret_cast<const uint4*>(key_in + i)), y = __ldcg(reinterpret_cast<const uint4*>(key_in + i) + 1);
+        k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
+        k[4] = y.x; k[5] = y.y; k[6] = y.z; k[7] = y.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) k[j] = i + j < hi ? __ldcg(key_in + i + j) : 0u;
       }
-      b.seg[i] = st ? u : u - 1;  // (padding: unused)
-      if (k != none && (i + 1 == n || __ldcg(key + i + 1) == none)) b.seg_start[count] = i + 1;
-      if (HASHED && i >= count) rows_out[i] = kNoRow;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (i + j < hi && (i + j == 0 || k[j] != prev)) f |= 1u << j;
+        prev = k[j];
+      }
+      return f;
+    };
+    uint32_t k[8], f = 0, starts = 0, total;
+    for (uint32_t i = lo + 8 * tid; i < hi; i += kSortTile) {
+      f = flags(i, k);
+      starts += __popc(f);
     }
-    u0 += in_tile;
-  }
-  if (tid == 0) {
-    if (blockIdx.x == 0) {
-      if (count == 0) b.seg_start[0] = 0;
+    uint32_t count, u0 = 0;
+    block_excl_scan(starts, s_warp, &total);
+    if (G == 1) {
+      count = total;
+    } else {
+      if (tid == 0) b.segs[blockIdx.x] = total;
+      if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+      const uint32_t ex = block_excl_scan(tid < G ? __ldcg(b.segs + tid) : 0u, s_warp, &count);
+      if (tid == blockIdx.x) s_first = ex;
+      __syncthreads();
+      u0 = s_first;
+    }
+    for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
+      const uint32_t i = t0 + 8 * tid;
+      if (!one) f = flags(i, k);
+      uint32_t in_tile;
+      uint32_t u = u0 + block_excl_scan(__popc(f), s_warp, &in_tile);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (i + j >= hi) break;
+        if ((f >> j) & 1u) rows_out[u++] = k[j];
+        key_out[i + j] = u - 1;
+        if (i + j >= count) rows_out[i + j] = PG_NO_ROW;
+      }
+      u0 += in_tile;
+    }
+    if (tid == 0 && blockIdx.x == 0) {
       b.ctrl->count = count;
-      if (count_out) *count_out = static_cast<int32_t>(count);
+      *count_out = static_cast<int32_t>(count);
     }
-    atomicAdd(&b.ctrl->done, 1u);
   }
+  if (tid == 0) atomicAdd(&b.ctrl->done, 1u);
 }
 
 // ------------------------------------------------------------------------------- the sums
@@ -367,21 +467,54 @@ struct SumArgs {
   const void* grad;          // summands, rows of r values; reference i has row i / share
   const uint64_t* sign;      // sign hashes of the references, or null
   const uint32_t* ref;       // references in sorted order
-  const uint32_t* seg;       // their segments
-  const uint32_t* seg_start;
-  const uint32_t* seg_row;   // output row of a segment; null: the segment's number
+  const uint32_t* seg;       // the output row of each, ascending
   const SortCtrl* ctrl;
   float* parts;
   void* out;
   uint32_t n, share, blocks; // blocks: of the sort (all have to have finished)
-  uint32_t tiles;
-  int32_t r, accumulate;
+  uint32_t tiles, none;      // none: the output row of padding, which has none
+  int32_t r, accumulate, compact;  // compact: rows from the count on are written as zeros
   float scale;
 };
 
+// 8 columns (or 1) of a summand as they lie in memory.
+template <int IN, int COLS>
+struct Raw {
+  uint32_t w[COLS == 1 ? 1 : IN == PG_F32 ? 8 : 4];
+
+  __device__ __forceinline__ void load(const void* __restrict__ base, int64_t at) {
+    if constexpr (COLS == 1) {
+      w[0] = IN == PG_F32 ? __ldg(static_cast<const uint32_t*>(base) + at)
+                          : static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(base) + at));
+    } else if constexpr (IN == PG_F32) {
+      const uint4 x = ldg_stream(static_cast<const float*>(base) + at), y = ldg_stream(static_cast<const float*>(base) + at + 4);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    } else {
+      const uint4 x = ldg_stream(static_cast<const uint16_t*>(base) + at);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    }
+  }
+
+  // acc += the columns, those with a bit in `neg` negated
+  __device__ __forceinline__ void add(float (&acc)[COLS], uint32_t neg) const {
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) {
+      uint32_t v;
+      if constexpr (IN == PG_F32)
+        v = w[j];
+      else if constexpr (COLS == 1)
+        v = w[0] << 16;
+      else
+        v = (j & 1) ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16;
+      acc[j] += __uint_as_float(v ^ ((neg << (31 - j)) & 0x80000000u));
+    }
+  }
+};
+
 template <int OUT, int COLS>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t u, int c, const float (&acc)[COLS]) {
-  const int64_t at = static_cast<int64_t>(a.seg_row ? __ldg(a.seg_row + u) : u) * a.r + c;
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int c, const float (&acc)[COLS]) {
+  const int64_t at = static_cast<int64_t>(row) * a.r + c;
   float y[COLS] = {};
   if (a.accumulate) read_cols<OUT, COLS>(a.out, at, y);
 #pragma unroll
@@ -390,91 +523,99 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t u, int c, c
 }
 
 // A group of `lanes` lanes (a power of two) per tile of T references and lanes * COLS columns.
+// The loads of 8 summands (fp32: 4) are in flight at a time, and behind them those of the next
+// references' numbers.
 template <int IN, int OUT, int COLS>
-__global__ void __launch_bounds__(256) rowgrad_sum_kernel(const SumArgs a, int lanes, int T) {
-  if (a.ctrl->done != a.blocks) return;
+__global__ void __launch_bounds__(256, 2)
+    rowgrad_sum_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
   const int per_block = 256 / lanes;
   const uint32_t tile = blockIdx.x * per_block + threadIdx.x / lanes;
   const int c = (blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * COLS;
-  if (tile >= a.tiles || c >= a.r) return;
-  const uint32_t count = a.ctrl->count;
-  const uint32_t p0 = tile * T, p1 = min(p0 + T, __ldg(a.seg_start + count));
-  if (!a.seg_row) {  // rows past the last segment are zero: row p for each position p of the tile
-    const float zero[COLS] = {};
-    for (uint32_t u = max(p0, count); u < min(p0 + T, a.n); ++u)
-      store_cols<OUT, COLS>(a.out, static_cast<int64_t>(u) * a.r + c, zero);
-  }
-  if (p0 >= p1) return;
-  const uint32_t first = __ldg(a.seg + p0), last = __ldg(a.seg + p1 - 1);
-  const bool from_before = __ldg(a.seg_start + first) < p0;
-  const bool goes_on = __ldg(a.seg_start + last + 1) > p1;
-  float* part = a.parts + static_cast<int64_t>(tile) * 2 * a.r + c;
-  float acc[COLS] = {};
-  uint32_t cur = first;
-  constexpr int kFly = 8;  // rows in flight
-  for (uint32_t q0 = p0; q0 < p1; q0 += kFly) {
-    uint32_t seg[kFly];
-    float x[kFly][COLS];
-    uint64_t hs[kFly];
+  if (tile >= a.tiles || c >= a.r || a.ctrl->done != a.blocks) return;
+  const uint32_t p0 = tile * T, p1 = min(p0 + T, a.n);
+  constexpr int kFly = IN == PG_F32 && COLS == 8 ? 4 : 8;
+  uint32_t ref[kFly], seg[kFly];
+  auto numbers = [&](uint32_t q0) {
+    if (q0 + kFly <= p1) {  // p0 is a multiple of 8
 #pragma unroll
-    for (int k = 0; k < kFly; ++k) {
-      seg[k] = last;
-      if (q0 + k < p1) {
-        const uint32_t ref = __ldg(a.ref + q0 + k);
-        seg[k] = __ldg(a.seg + q0 + k);
-        load_cols<IN, COLS>(a.grad, static_cast<int64_t>(a.share == 1 ? ref : ref / a.share) * a.r + c, x[k]);
-        hs[k] = a.sign ? __ldg(a.sign + ref) : 0ull;
-      } else {
+      for (int k = 0; k < kFly; k += 4) {
+        const uint4 r = __ldg(reinterpret_cast<const uint4*>(a.ref + q0 + k));
+        const uint4 s = __ldg(reinterpret_cast<const uint4*>(a.seg + q0 + k));
+        ref[k] = r.x; ref[k + 1] = r.y; ref[k + 2] = r.z; ref[k + 3] = r.w;
+        seg[k] = s.x; seg[k + 1] = s.y; seg[k + 2] = s.z; seg[k + 3] = s.w;
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) x[k][j] = 0.f;
-        hs[k] = 0ull;
+      for (int k = 0; k < kFly; ++k) {
+        const uint32_t q = min(q0 + k, p1 - 1);
+        ref[k] = __ldg(a.ref + q);
+        seg[k] = q0 + k < p1 ? __ldg(a.seg + q) : kNoRow;
       }
     }
+  };
+  numbers(p0);
+  const uint32_t before = p0 > 0 ? __ldg(a.seg + p0 - 1) : kNoRow, after = p1 < a.n ? __ldg(a.seg + p1) : kNoRow;
+  if (a.compact) {  // rows past the last distinct one are zero: row p for each position p of the tile
+    const float zero[COLS] = {};
+    for (uint32_t u = max(p0, a.ctrl->count); u < p1; ++u)
+      store_cols<OUT, COLS>(a.out, static_cast<int64_t>(u) * a.r + c, zero);
+  }
+  float* part = a.parts + static_cast<int64_t>(tile) * 2 * a.r + c;
+  float acc[COLS] = {};
+  uint32_t cur = seg[0];
+  bool from_before = before == cur;  // the row of `cur` began in an earlier tile
+  for (uint32_t q0 = p0; q0 < p1 && cur != a.none; q0 += kFly) {
+    Raw<IN, COLS> x[kFly];
+    uint64_t hs[kFly];
+    uint32_t sg[kFly];
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
-      if (seg[k] != cur) {
-        if (cur == first && from_before) {
+      x[k].load(a.grad, static_cast<int64_t>(a.share == 1 ? ref[k] : ref[k] / a.share) * a.r + c);
+      hs[k] = a.sign ? __ldg(a.sign + ref[k]) : 0ull;
+      sg[k] = seg[k];
+    }
+    if (q0 + kFly < p1) numbers(q0 + kFly);
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      if (q0 + k >= p1) break;
+      if (sg[k] != cur) {
+        if (from_before)
           store_cols<PG_F32, COLS>(part, 0, acc);
-        } else {
+        else
           write_row<OUT, COLS>(a, cur, c, acc);
-        }
-        cur = seg[k];
+        from_before = false;
+        cur = sg[k];
+        if (cur == a.none) break;
 #pragma unroll
         for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
       }
       uint32_t neg = 0;
       if (a.sign) neg = static_cast<uint32_t>(mix64(hs[k] + kGolden * ((c >> 6) + 1)) >> (c & 63));
-#pragma unroll
-      for (int j = 0; j < COLS; ++j)
-        acc[j] += __uint_as_float(__float_as_uint(x[k][j]) ^ ((neg << (31 - j)) & 0x80000000u));
+      x[k].add(acc, neg);
     }
   }
-  if (cur == first && from_before) {
+  if (cur == a.none) return;
+  if (from_before)
     store_cols<PG_F32, COLS>(part, 0, acc);
-  } else if (goes_on) {
+  else if (after == cur)
     store_cols<PG_F32, COLS>(part, a.r, acc);
-  } else {
+  else
     write_row<OUT, COLS>(a, cur, c, acc);
-  }
 }
 
 // Rows that cross tiles: the tile a row starts in adds its parts. A group of lanes per tile, as
-// above; a row of more than kLongRow tiles is added by the whole block, group k taking every
-// per_block-th part (at most one such row starts in a block's tiles: a block has no more than
-// kLongRow of them).
-constexpr int kLongRow = 256;
-
+// above; a row over more tiles than a block has groups is added by the whole block, group k
+// taking every per_block-th part (at most one such row starts in a block's tiles).
 template <int OUT, int COLS>
-__global__ void __launch_bounds__(256) rowgrad_join_kernel(const SumArgs a, int lanes, int T) {
+__global__ void __launch_bounds__(256) rowgrad_join_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
   __shared__ float s_acc[256][COLS];
-  __shared__ uint32_t s_long;
+  __shared__ uint32_t s_long, s_end;
   if (a.ctrl->done != a.blocks) return;
   const int per_block = 256 / lanes, group = threadIdx.x / lanes;
   const uint32_t tile = blockIdx.x * per_block + group;
   const int c = (blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * COLS;
   if (threadIdx.x == 0) s_long = kNoRow;
   __syncthreads();
-  const uint32_t nvalid = __ldg(a.seg_start + a.ctrl->count);
   const uint32_t p0 = tile * T, p1 = p0 + T;
   constexpr int kFly = 4;
   auto add = [&](uint32_t k, uint32_t end, uint32_t step, float (&acc)[COLS]) {  // first parts of tiles k, k + step, ..
@@ -492,12 +633,23 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(const SumArgs a, int 
         for (int j = 0; j < COLS; ++j) acc[j] += x[f][j];
     }
   };
-  if (tile < a.tiles && p1 < nvalid) {
-    const uint32_t u = __ldg(a.seg + p1);
-    if (__ldg(a.seg + p1 - 1) == u && __ldg(a.seg_start + u) >= p0) {
-      const uint32_t end = (__ldg(a.seg_start + u + 1) - 1) / T + 1;
-      if (end - tile > kLongRow) {
+  if (tile < a.tiles && p1 < a.n) {
+    const uint32_t u = __ldg(a.seg + p1), prev = __ldg(a.seg + p1 - 1);
+    const uint32_t before = p0 > 0 ? __ldg(a.seg + p0 - 1) : kNoRow;
+    const uint32_t next = p1 + T < a.n ? __ldg(a.seg + p1 + T) : kNoRow;
+    if (u == prev && u != before && u != a.none) {
+      uint32_t end = tile + 2;  // past the last tile with a part
+      if (next == u) {          // the row's end lies further: the first position with another row
+        uint32_t lo = p1 + T, hi = a.n;
+        while (hi - lo > 1) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          (__ldg(a.seg + mid) == u ? lo : hi) = mid;
+        }
+        end = lo / T + 1;
+      }
+      if (end - tile > static_cast<uint32_t>(per_block)) {
         s_long = tile;
+        s_end = end;
       } else if (c < a.r) {
         float acc[COLS];
         load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(tile) * 2 * a.r + a.r + c, acc);
@@ -508,11 +660,10 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(const SumArgs a, int 
   }
   __syncthreads();
   if (s_long == kNoRow) return;
-  const uint32_t u = __ldg(a.seg + (s_long + 1) * T), end = (__ldg(a.seg_start + u + 1) - 1) / T + 1;
   float acc[COLS] = {};
   if (c < a.r) {
     if (group == 0) load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(s_long) * 2 * a.r + a.r + c, acc);
-    add(s_long + 1 + group, end, per_block, acc);
+    add(s_long + 1 + group, s_end, per_block, acc);
   }
 #pragma unroll
   for (int j = 0; j < COLS; ++j) s_acc[threadIdx.x][j] = acc[j];
@@ -521,7 +672,7 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(const SumArgs a, int 
     for (int k = 1; k < per_block; ++k)
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] += s_acc[k * lanes + threadIdx.x][j];
-    write_row<OUT, COLS>(a, u, c, acc);
+    write_row<OUT, COLS>(a, __ldg(a.seg + (s_long + 1) * T), c, acc);
   }
 }
 
@@ -549,9 +700,8 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   while (key_bits < 32 && (keys >> key_bits)) ++key_bits;
   const int passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
   const int bits = (key_bits + passes - 1) / passes;
-  uint32_t G = (n + kRefsPerBlock - 1) / kRefsPerBlock;
-  G = min(G, static_cast<uint32_t>(min(sm_count(), kMaxSortBlocks)));
-  uint32_t share = (n + G - 1) / G;
+  uint32_t G = min((n + kRefsPerBlock - 1) / kRefsPerBlock, static_cast<uint32_t>(min(sm_count(), kMaxSortBlocks)));
+  const uint32_t share = (n + G - 1) / G / 8 * 8 + 8;  // whole groups of 8 references
   G = (n + share - 1) / share;
 
   cudaError_t e = cudaMemsetAsync(b.ctrl, 0, kCtrlBytes, stream);
@@ -569,16 +719,17 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   attr[0].id = cudaLaunchAttributeCooperative;  // the blocks meet at a grid barrier
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = G > 1 ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, sort, src, b, n, share, passes, bits, rows_out, count_out, device_error_word());
   if (e != cudaSuccess) return cuda_fail(e);
   pg_status st = after_launch(1);
   if (st != PG_OK) return st;
 
-  a.ref = b.ref[passes & 1];
-  a.seg = b.seg;
-  a.seg_start = b.seg_start;
-  a.seg_row = b.seg_row;
+  const int sorted = passes & 1;  // the buffer of the last pass; the segment numbers lie in the other one
+  a.ref = b.ref[sorted];
+  a.seg = b.key[HASHED ? sorted ^ 1 : sorted];
+  a.none = HASHED ? kNoRow : src.rows;
+  a.compact = HASHED;
   a.sign = b.sign;
   a.ctrl = b.ctrl;
   a.parts = b.parts;
