@@ -2,8 +2,8 @@
 //
 // Bound by memory: N d (s_in + s_out) bytes and one multiply a value. One warp serves up to
 // 1024 columns of one token, so that a decode step's few rows still spread over several SMs
-// and a wide row is read by consecutive warps; each lane has up to four 16-byte loads in
-// flight (fp32: eight) before it stores.
+// and a wide row is read by consecutive warps; each lane has four loads of 16 bytes (fp32:
+// 32) in flight before it stores.
 #include "pg_hash.cuh"
 #include "pg_vec.h"
 
@@ -78,7 +78,7 @@ extern "C" pg_status pg_embed(const int32_t* tokens, int64_t N, uint32_t vocab, 
   if (device_cc() != 103) return PG_ERR_DEVICE;
   pg_status st = prepare_err(err_index, stream);
   if (st != PG_OK) return st;
-  const bool vec = d % 8 == 0 && aligned(table, 16) && aligned(out, 16);
+  const bool vec = d % 8 == 0 && aligned(table, vec_bytes(table_dtype)) && aligned(out, vec_bytes(out_dtype));
   EmbedFn fn = vec ? embed_fn<true>(table_dtype, out_dtype) : embed_fn<false>(table_dtype, out_dtype);
   fn<<<static_cast<unsigned>(blocks), 32 * kEmbedWarps, 0, stream>>>(tokens, tasks, parts, vocab, canon_map, table,
                                                                     static_cast<uint32_t>(rows), d, scale, out,

@@ -77,7 +77,7 @@ struct OrthoArgs {
   int* err_word;
   int64_t size;              // m n
   int batch, m, n, p, ldx, ldp, parts, steps, dtype;
-  int g_vec, out_vec;        // 16-byte accesses to G; to out
+  int g_vec, out_vec;        // accesses of 8 columns to G; to out
   float a, b, c, eps, scale;
 };
 
@@ -253,7 +253,7 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kT
     sum[2] = fmaf(down, down, sum[2]);
   };
   if (g.g_vec) {
-    constexpr int kFly = 8;  // 16-byte (fp32: two) loads in flight
+    constexpr int kFly = 8;  // loads in flight
     for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kFly * kThreads * 8) {
       float x[kFly][8];
 #pragma unroll
@@ -960,7 +960,7 @@ extern "C" pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batc
   carve_ortho(static_cast<uint8_t*>(workspace), batch, m, n, &g);
   g.steps = steps;
   g.dtype = dtype;
-  g.g_vec = n % 8 == 0 && aligned(G, 16);
+  g.g_vec = n % 8 == 0 && aligned(G, vec_bytes(dtype));
   g.out_vec = n % 8 == 0 && aligned(out, 16);
   g.a = a;
   g.b = b;

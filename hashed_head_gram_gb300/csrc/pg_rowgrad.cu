@@ -29,10 +29,10 @@ constexpr int kSortItems = 8;                          // references a thread ho
 constexpr int kSortTile = kSortThreads * kSortItems;   // 8192
 constexpr int kMaxDigitBits = 11;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
-constexpr int kDigitsPerThread = kMaxDigits / kSortThreads;
+constexpr int kDigitsPerThread = 2;                    // digits 2 tid and 2 tid + 1
 constexpr int kMaxSortBlocks = 152;                    // one per SM
 constexpr int kScanIters = (kMaxSortBlocks + 31) / 32;
-constexpr uint32_t kRefsPerBlock = 4096;               // at least, before another block joins
+constexpr uint32_t kRefsPerBlock = 2048;               // at least, before another block joins
 constexpr uint32_t kDirectCounts = 16384;              // counts that every block reads for itself
 constexpr int kHashItems = 32;                         // (order, head) items of a table
 
@@ -51,7 +51,9 @@ struct RefSource {
   uint32_t vocab;
   uint32_t rows;     // embedding: table rows; rows itself is the key of padding
   uint32_t L;        // hashed lookup: sequence length
+  uint64_t fm_L;     // its fastmod constant
   int32_t items;     // hashed lookup: references per token
+  uint32_t per;      // 2^32 / items, rounded up: tile-local token numbers
   int32_t mode;
   ItemConst ic[kHashItems];
 };
@@ -61,15 +63,14 @@ struct SortBuffers {
   uint32_t* hist;      // [digits][blocks]
   uint32_t* totals;    // [digits]
   uint32_t* segs;      // [blocks] segments that start in a block's share
-  uint32_t* key[2];    // [n]
-  uint32_t* ref[2];    // [n]
+  uint2* pair[2];      // [n] (row, reference)
   uint64_t* sign;      // [n] sign hashes of the references (hashed lookup)
   float* parts;        // [tiles][2][r] sums of rows that cross a tile's start, its end
 };
 
 constexpr size_t kCtrlBytes = sizeof(SortCtrl);
 
-inline size_t up16(size_t x) { return (x + 15) / 16 * 16; }
+inline size_t up32(size_t x) { return (x + 31) / 32 * 32; }
 
 // References per tile of the sums: 32, and 8 while 32 would leave the GPU short of warps
 // (lanes of 8 columns: 16 warps an SM).
@@ -80,9 +81,10 @@ inline int tile_refs(int64_t n, int r) { return n * ((r + 7) / 8) / 32 >= kFewLa
 // Carves the buffers from `base`; returns the bytes they take (base may be null to size them).
 size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   size_t at = 0;
+  if (base) base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 31) & ~uintptr_t(31));
   auto take = [&](size_t bytes) {
     uint8_t* p = base ? base + at : nullptr;
-    at += up16(bytes);
+    at += up32(bytes);
     return p;
   };
   const size_t un = static_cast<size_t>(n);
@@ -90,14 +92,11 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   b->hist = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits * kMaxSortBlocks));
   b->totals = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits));
   b->segs = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxSortBlocks));
-  for (int i = 0; i < 2; ++i) {
-    b->key[i] = reinterpret_cast<uint32_t*>(take(4 * un));
-    b->ref[i] = reinterpret_cast<uint32_t*>(take(4 * un));
-  }
+  for (int i = 0; i < 2; ++i) b->pair[i] = reinterpret_cast<uint2*>(take(8 * un));
   b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un)) : nullptr;
   const size_t T = tile_refs(n, r);
   b->parts = reinterpret_cast<float*>(take((un + T - 1) / T * 2 * r * sizeof(float)));
-  return at;
+  return at + 32;
 }
 
 // ------------------------------------------------------------------------------- the sort
@@ -157,6 +156,7 @@ __device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* s_warp
   *total = s_warp[kSortWarps];
   return s_warp[w] + inc - v;
 }
+static_assert(kDigitsPerThread * kSortThreads == kMaxDigits, "");
 static_assert(kSortWarps == 32, "block_excl_scan: one lane a warp");
 
 // What a block keeps of a tile of references between counting and scattering. A warp holds
@@ -172,7 +172,7 @@ __device__ __forceinline__ int tile_items(uint32_t left) {
 
 // Ranks a tile's references by the digit of `key`, stably, with per-warp counts in s_cnt
 // [warps][digits], which become exclusive offsets over the warps; totals[q] gets the tile's
-// count of digit q * threads + tid. Equal digits of a warp meet by one ballot a bit.
+// count of digit 2 tid + q. Equal digits of a warp meet by one ballot a bit.
 __device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end, int items, int shift, int bits,
                                           uint16_t* s_cnt, uint32_t (&totals)[kDigitsPerThread]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -201,40 +201,49 @@ __device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end,
     __syncwarp();
   }
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < kDigitsPerThread; ++q) {
-    const int d = q * kSortThreads + tid;
-    uint32_t run = 0;
-    if (d < digits) {
+  // two digits a thread: their 16-bit counts (at most 8192 in all) ride in one word
+  uint32_t run = 0;
+  if (2 * tid < digits) {
+    uint32_t* word = reinterpret_cast<uint32_t*>(s_cnt) + tid;
 #pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = s_cnt[w * digits + d];
-        s_cnt[w * digits + d] = static_cast<uint16_t>(run);
-        run += c;
-      }
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = word[w * digits / 2];
+      word[w * digits / 2] = run;
+      run += c;
     }
-    totals[q] = run;
   }
+  totals[0] = run & 0xFFFFu;
+  totals[1] = run >> 16;
 }
 
-// The reference's row (and, hashed lookup, its sign hash) on the first pass.
-template <bool HASHED>
-__device__ __forceinline__ uint32_t first_key(const RefSource& src, const ItemConst* s_ic, uint64_t* sign, uint32_t i) {
-  uint32_t key;
-  if constexpr (HASHED) {
-    const uint32_t tok = i / src.items;
-    uint64_t hs;
-    key = item_row(s_ic[i - tok * src.items], src.mode, src.tokens, src.canon_map, src.vocab, tok, tok % src.L, src.err,
-                   &hs);
-    sign[i] = hs;
-  } else {
-    key = embed_row(src.tokens, src.canon_map, src.vocab, src.rows, i);
-    if (key == kNoRow) {
-      key = src.rows;
-      if (src.err) atomicMin(reinterpret_cast<unsigned int*>(src.err), i);
-    }
-  }
-  return key;
+// Canonical IDs of the tokens that the references [t0, end) and their n-grams read, into s_id
+// (token tok0 - 3 first): one read of the token and of the map for all of a token's heads.
+__device__ __forceinline__ void stage_ids(const RefSource& src, uint32_t t0, uint32_t end, uint32_t* s_id) {
+  const int64_t tok0 = static_cast<int64_t>(t0 / src.items) - 3;
+  const int count = static_cast<int>((end - 1) / src.items - tok0) + 1;
+  for (int k = threadIdx.x; k < count; k += kSortThreads)
+    s_id[k] = tok0 + k >= 0 ? canon_token(src.tokens, src.canon_map, src.vocab, tok0 + k, src.err) : 0u;
+}
+
+// Hashed lookup: the reference's row and its sign hash.
+__device__ __forceinline__ uint32_t hashed_key(const RefSource& src, const ItemConst* s_ic, const uint32_t* s_id,
+                                               uint32_t t0, uint32_t i, uint64_t* hs) {
+  const uint32_t tok0 = t0 / src.items, local = i - tok0 * src.items;  // local < 8192 + 32
+  const uint32_t s = __umulhi(local, src.per) + (src.items == 1 ? local : 0u);
+  const ItemConst& it = s_ic[local - s * src.items];
+  const uint32_t t = fastmod(tok0 + s, src.fm_L, src.L);
+  uint64_t c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = t >= static_cast<uint32_t>(j) ? s_id[s + 3 - j] : kPad;
+  return item_row_ids(it, src.mode, c, hs);
+}
+
+// Embedding: the position's row; padding gets the key `rows`.
+__device__ __forceinline__ uint32_t embed_key(const RefSource& src, uint32_t i) {
+  const uint32_t row = embed_row(src.tokens, src.canon_map, src.vocab, src.rows, i);
+  if (row != kNoRow) return row;
+  if (src.err) atomicMin(reinterpret_cast<unsigned int*>(src.err), i);
+  return src.rows;
 }
 
 template <bool HASHED>
@@ -264,30 +273,42 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     __syncthreads();
   }
 
-  uint32_t *key_in = b.key[0], *key_out = b.key[1], *ref_in = b.ref[0], *ref_out = b.ref[1];
+  uint2 *in_order = b.pair[0], *out_order = b.pair[1];
   for (int p = 0; p < passes; ++p) {
     const int shift = p * bits;
     Held h;
-    uint32_t mine[kDigitsPerThread];  // this share's counts of digits q * threads + tid
+    uint32_t mine[kDigitsPerThread];  // this share's counts of digits 2 tid + q
 #pragma unroll
     for (int q = 0; q < kDigitsPerThread; ++q) mine[q] = 0;
     // ---- ranks and counts. A share of several tiles is read again for the scatter.
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
       const int items = tile_items(hi - t0);
       const uint32_t first = t0 + warp * 32 * items, end = min(hi, t0 + kSortTile);
+      if (HASHED && p == 0) {
+        __syncthreads();
+        stage_ids(src, t0, end, reinterpret_cast<uint32_t*>(s_cnt));
+        __syncthreads();
+      }
 #pragma unroll
       for (int j = 0; j < kSortItems; ++j) {
         const uint32_t i = first + j * 32 + lane;
-        const bool in = j < items && i < end;
-        h.key[j] = 0;
-        h.ref[j] = i;
-        if (in && p == 0) {
-          h.key[j] = first_key<HASHED>(src, s_ic, b.sign, i);
-          if (!one) key_in[i] = h.key[j];
-        } else if (in) {
-          h.key[j] = __ldcg(key_in + i);
-          if (one) h.ref[j] = __ldcg(ref_in + i);
+        uint2 v = make_uint2(0u, i);
+        if (j < items && i < end) {
+          if (p > 0) {
+            v = __ldcg(in_order + i);
+          } else {
+            if constexpr (HASHED) {
+              uint64_t hs;
+              v.x = hashed_key(src, s_ic, reinterpret_cast<const uint32_t*>(s_cnt), t0, i, &hs);
+              b.sign[i] = hs;
+            } else {
+              v.x = embed_key(src, i);
+            }
+            if (!one) in_order[i] = v;
+          }
         }
+        h.key[j] = v.x;
+        h.ref[j] = v.y;
       }
       uint32_t totals[kDigitsPerThread];
       rank_tile(h, first, end, items, shift, bits, s_cnt, totals);
@@ -307,14 +328,14 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     } else {
 #pragma unroll
       for (int q = 0; q < kDigitsPerThread; ++q) {
-        const int d = q * kSortThreads + tid;
+        const int d = 2 * tid + q;
         if (d < digits) b.hist[d * G + blockIdx.x] = mine[q];
       }
       if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
       if (digits * G <= kDirectCounts) {
 #pragma unroll
         for (int q = 0; q < kDigitsPerThread; ++q) {
-          const int d = q * kSortThreads + tid;
+          const int d = 2 * tid + q;
           below[q] = total_of[q] = 0;
           if (d < digits)
 #pragma unroll 8
@@ -340,21 +361,18 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
 #pragma unroll
         for (int q = 0; q < kDigitsPerThread; ++q) {
-          const int d = q * kSortThreads + tid;
+          const int d = 2 * tid + q;
           below[q] = d < digits ? __ldcg(b.hist + d * G + blockIdx.x) : 0u;
           total_of[q] = d < digits ? __ldcg(b.totals + d) : 0u;
         }
       }
     }
-    uint32_t carry = 0;
+    uint32_t all;
+    uint32_t ex = block_excl_scan(total_of[0] + total_of[1], s_warp, &all);
 #pragma unroll
     for (int q = 0; q < kDigitsPerThread; ++q) {
-      const int d = q * kSortThreads + tid;
-      if (q * kSortThreads >= digits) break;
-      uint32_t total;
-      const uint32_t ex = block_excl_scan(total_of[q], s_warp, &total);
-      if (d < digits) s_base[d] = carry + ex + below[q];
-      carry += total;
+      if (2 * tid + q < digits) s_base[2 * tid + q] = ex + below[q];
+      ex += total_of[q];
     }
     __syncthreads();
 
@@ -368,9 +386,9 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
           const uint32_t i = first + j * 32 + lane;
-          const bool in = j < items && i < end;
-          h.key[j] = in ? __ldcg(key_in + i) : 0u;
-          h.ref[j] = in && p > 0 ? __ldcg(ref_in + i) : i;
+          const uint2 v = j < items && i < end ? __ldcg(in_order + i) : make_uint2(0u, i);
+          h.key[j] = v.x;
+          h.ref[j] = v.y;
         }
         rank_tile(h, first, end, items, shift, bits, s_cnt, totals);
         __syncthreads();
@@ -380,51 +398,51 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         if (j < items && first + j * 32 + lane < end) {
           const uint32_t dig = (h.key[j] >> shift) & mask;
           const uint32_t to = s_base[dig] + s_cnt[warp * digits + dig] + h.rank[j];
-          key_out[to] = h.key[j];
-          ref_out[to] = h.ref[j];
+          out_order[to] = make_uint2(h.key[j], h.ref[j]);
         }
       }
       if (!one) {
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < kDigitsPerThread; ++q) {
-          const int d = q * kSortThreads + tid;
+          const int d = 2 * tid + q;
           if (d < digits) s_base[d] += totals[q];
         }
       }
     }
-    uint32_t* t = key_in;
-    key_in = key_out;
-    key_out = t;
-    t = ref_in;
-    ref_in = ref_out;
-    ref_out = t;
+    uint2* swap = in_order;
+    in_order = out_order;
+    out_order = swap;
     if ((HASHED || p + 1 < passes) && !grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
   }
 
   if constexpr (HASHED) {
-    // ---- segments of equal rows: their numbers replace the keys (into the free buffer), the rows
+    // ---- segments of equal rows: their numbers replace the rows (in the free buffer), the rows
     // go to rows_out. A thread takes 8 consecutive references at a time.
-    auto flags = [&](uint32_t i, uint32_t (&k)[8]) -> uint32_t {  // bit j: a segment starts at i + j
-      uint32_t prev = i > 0 && i < hi ? __ldcg(key_in + i - 1) : 0u, f = 0;
+    auto flags = [&](uint32_t i, uint2 (&v)[8]) -> uint32_t {  // bit j: a segment starts at i + j
+      uint32_t prev = i > 0 && i < hi ? __ldcg(&in_order[i - 1].x) : 0u, f = 0;
       if (i + 8 <= hi) {  // shares start at multiples of 8
-        const uint4 x = __ldcg(reinterpret_cast<const uint4*>(key_in + i)), y = __ldcg(reinterpret_cast<const uint4*>(key_in + i) + 1);
-        k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
-        k[4] = y.x; k[5] = y.y; k[6] = y.z; k[7] = y.w;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint4 x = __ldcg(reinterpret_cast<const uint4*>(in_order + i + j));
+          v[j] = make_uint2(x.x, x.y);
+          v[j + 1] = make_uint2(x.z, x.w);
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) k[j] = i + j < hi ? __ldcg(key_in + i + j) : 0u;
+        for (int j = 0; j < 8; ++j) v[j] = i + j < hi ? __ldcg(in_order + i + j) : make_uint2(0u, 0u);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (i + j < hi && (i + j == 0 || k[j] != prev)) f |= 1u << j;
-        prev = k[j];
+        if (i + j < hi && (i + j == 0 || v[j].x != prev)) f |= 1u << j;
+        prev = v[j].x;
       }
       return f;
     };
-    uint32_t k[8], f = 0, starts = 0, total;
+    uint2 v[8];
+    uint32_t f = 0, starts = 0, total;
     for (uint32_t i = lo + 8 * tid; i < hi; i += kSortTile) {
-      f = flags(i, k);
+      f = flags(i, v);
       starts += __popc(f);
     }
     uint32_t count, u0 = 0;
@@ -441,15 +459,24 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     }
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
       const uint32_t i = t0 + 8 * tid;
-      if (!one) f = flags(i, k);
+      if (!one) f = flags(i, v);
       uint32_t in_tile;
       uint32_t u = u0 + block_excl_scan(__popc(f), s_warp, &in_tile);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (i + j >= hi) break;
-        if ((f >> j) & 1u) rows_out[u++] = k[j];
-        key_out[i + j] = u - 1;
+        if ((f >> j) & 1u) rows_out[u++] = v[j].x;
+        v[j].x = u - 1;
         if (i + j >= count) rows_out[i + j] = PG_NO_ROW;
+      }
+      if (i + 8 <= hi) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          *reinterpret_cast<uint4*>(out_order + i + j) = make_uint4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < hi) out_order[i + j] = v[j];
       }
       u0 += in_tile;
     }
@@ -466,8 +493,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 struct SumArgs {
   const void* grad;          // summands, rows of r values; reference i has row i / share
   const uint64_t* sign;      // sign hashes of the references, or null
-  const uint32_t* ref;       // references in sorted order
-  const uint32_t* seg;       // the output row of each, ascending
+  const uint2* order;        // (output row, reference), rows ascending
   const SortCtrl* ctrl;
   float* parts;
   void* out;
@@ -538,23 +564,21 @@ __global__ void __launch_bounds__(256, 2)
   auto numbers = [&](uint32_t q0) {
     if (q0 + kFly <= p1) {  // p0 is a multiple of 8
 #pragma unroll
-      for (int k = 0; k < kFly; k += 4) {
-        const uint4 r = __ldg(reinterpret_cast<const uint4*>(a.ref + q0 + k));
-        const uint4 s = __ldg(reinterpret_cast<const uint4*>(a.seg + q0 + k));
-        ref[k] = r.x; ref[k + 1] = r.y; ref[k + 2] = r.z; ref[k + 3] = r.w;
-        seg[k] = s.x; seg[k + 1] = s.y; seg[k + 2] = s.z; seg[k + 3] = s.w;
+      for (int k = 0; k < kFly; k += 2) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.order + q0 + k));
+        seg[k] = v.x; ref[k] = v.y; seg[k + 1] = v.z; ref[k + 1] = v.w;
       }
     } else {
 #pragma unroll
       for (int k = 0; k < kFly; ++k) {
-        const uint32_t q = min(q0 + k, p1 - 1);
-        ref[k] = __ldg(a.ref + q);
-        seg[k] = q0 + k < p1 ? __ldg(a.seg + q) : kNoRow;
+        const uint2 v = __ldg(a.order + min(q0 + k, p1 - 1));
+        ref[k] = v.y;
+        seg[k] = v.x;  // (past p1: not used)
       }
     }
   };
   numbers(p0);
-  const uint32_t before = p0 > 0 ? __ldg(a.seg + p0 - 1) : kNoRow, after = p1 < a.n ? __ldg(a.seg + p1) : kNoRow;
+  const uint32_t before = p0 > 0 ? __ldg(&a.order[p0 - 1].x) : kNoRow, after = p1 < a.n ? __ldg(&a.order[p1].x) : kNoRow;
   if (a.compact) {  // rows past the last distinct one are zero: row p for each position p of the tile
     const float zero[COLS] = {};
     for (uint32_t u = max(p0, a.ctrl->count); u < p1; ++u)
@@ -634,16 +658,16 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(const __grid_constant
     }
   };
   if (tile < a.tiles && p1 < a.n) {
-    const uint32_t u = __ldg(a.seg + p1), prev = __ldg(a.seg + p1 - 1);
-    const uint32_t before = p0 > 0 ? __ldg(a.seg + p0 - 1) : kNoRow;
-    const uint32_t next = p1 + T < a.n ? __ldg(a.seg + p1 + T) : kNoRow;
+    const uint32_t u = __ldg(&a.order[p1].x), prev = __ldg(&a.order[p1 - 1].x);
+    const uint32_t before = p0 > 0 ? __ldg(&a.order[p0 - 1].x) : kNoRow;
+    const uint32_t next = p1 + T < a.n ? __ldg(&a.order[p1 + T].x) : kNoRow;
     if (u == prev && u != before && u != a.none) {
       uint32_t end = tile + 2;  // past the last tile with a part
       if (next == u) {          // the row's end lies further: the first position with another row
         uint32_t lo = p1 + T, hi = a.n;
         while (hi - lo > 1) {
           const uint32_t mid = lo + (hi - lo) / 2;
-          (__ldg(a.seg + mid) == u ? lo : hi) = mid;
+          (__ldg(&a.order[mid].x) == u ? lo : hi) = mid;
         }
         end = lo / T + 1;
       }
@@ -672,7 +696,7 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(const __grid_constant
     for (int k = 1; k < per_block; ++k)
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] += s_acc[k * lanes + threadIdx.x][j];
-    write_row<OUT, COLS>(a, __ldg(a.seg + (s_long + 1) * T), c, acc);
+    write_row<OUT, COLS>(a, __ldg(&a.order[(s_long + 1) * T].x), c, acc);
   }
 }
 
@@ -725,9 +749,7 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   pg_status st = after_launch(1);
   if (st != PG_OK) return st;
 
-  const int sorted = passes & 1;  // the buffer of the last pass; the segment numbers lie in the other one
-  a.ref = b.ref[sorted];
-  a.seg = b.key[HASHED ? sorted ^ 1 : sorted];
+  a.order = b.pair[HASHED ? (passes & 1) ^ 1 : passes & 1];  // hashed lookup: with segment numbers
   a.none = HASHED ? kNoRow : src.rows;
   a.compact = HASHED;
   a.sign = b.sign;
@@ -737,7 +759,7 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   a.blocks = G;
   const int T = tile_refs(n, a.r);
   a.tiles = (n + T - 1) / T;
-  const bool vec = a.r % 8 == 0 && aligned(a.grad, 16) && aligned(a.out, 16);
+  const bool vec = a.r % 8 == 0 && aligned(a.grad, vec_bytes(in)) && aligned(a.out, vec_bytes(out));
   const int cols = vec ? 8 : 1;
   int lanes = 1;
   while (lanes < 32 && lanes * cols < a.r) lanes *= 2;
@@ -852,7 +874,9 @@ extern "C" pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* to
   src.err = err_index;
   src.vocab = desc->vocab;
   src.L = static_cast<uint32_t>(L);
+  src.fm_L = fastmod_constant(src.L);
   src.items = items;
+  src.per = static_cast<uint32_t>(((1ull << 32) + items - 1) / items);  // (1 item: 0, see hashed_key)
   src.mode = desc->mode;
   HashParams P;
   fill_hash_params(desc, g, &P);

@@ -14,6 +14,7 @@ constexpr int kMaxEmbedWidth = 1 << 20;  // columns of an embedding row
 
 inline bool real_dtype(int dtype) { return dtype == PG_F32 || dtype == PG_BF16; }
 inline size_t dtype_bytes(int dtype) { return dtype == PG_F32 ? 4 : 2; }
+inline size_t vec_bytes(int dtype) { return 8 * dtype_bytes(dtype); }  // 8 columns: one access of 16 or 32 bytes
 inline bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 // Table row of position t, or kNoRow for padding (a token outside [0, vocab), or a canonical
@@ -27,7 +28,20 @@ __device__ __forceinline__ uint32_t embed_row(const int32_t* __restrict__ tokens
   return row < rows ? row : kNoRow;
 }
 
-// 8 columns with 16-byte accesses (the address is 16-byte aligned), or 1.
+// 32 bytes with one access (sm_100 and later), 32-byte aligned.
+__device__ __forceinline__ void load32(const void* p, float (&x)[8]) {
+  asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+      : "l"(p));
+}
+
+__device__ __forceinline__ void store32(void* p, const float (&x)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
+// 8 columns with one access (the address is aligned to it), or 1.
 template <int DT, int COLS>
 __device__ __forceinline__ void load_cols(const void* __restrict__ base, int64_t at, float (&x)[COLS]) {
   static_assert(COLS == 1 || COLS == 8, "");
@@ -36,9 +50,7 @@ __device__ __forceinline__ void load_cols(const void* __restrict__ base, int64_t
     if constexpr (COLS == 1) {
       x[0] = __ldg(p);
     } else {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      load32(p, x);
     }
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
@@ -75,8 +87,7 @@ __device__ __forceinline__ void store_cols(void* base, int64_t at, const float (
     if constexpr (COLS == 1) {
       *p = x[0];
     } else {
-      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+      store32(p, x);
     }
   } else {
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at;

@@ -661,8 +661,8 @@ pg_status pg_collision_counts(const uint32_t* rows, int64_t n, int32_t K, int64_
  *  err_index  device int32 [1], or NULL: the smallest t whose token is outside [0, V) or whose
  *             canonical ID is not below `rows`, else -1. Such a position is padding: its row of
  *             `out` is zero and it has no gradient (use -1 for padding on purpose).
- * 1 <= rows < 2^31, 1 <= d <= 2^20, 0 <= N < 2^31; N == 0 enqueues nothing. d % 8 == 0 with 16-byte
- * aligned table and out takes 16-byte accesses.
+ * 1 <= rows < 2^31, 1 <= d <= 2^20, 0 <= N < 2^31; N == 0 enqueues nothing. d % 8 == 0 with
+ * table and out aligned to 8 elements takes 16- and 32-byte accesses.
  */
 pg_status pg_embed(const int32_t* tokens, int64_t N, uint32_t vocab, const uint32_t* canon_map, const void* table,
                    int32_t table_dtype, int64_t rows, int32_t d, float scale, void* out, int32_t out_dtype,
@@ -702,8 +702,8 @@ pg_status pg_embed_grad(const int32_t* tokens, int64_t N, uint32_t vocab, const 
  *  count_out   device int32 [1]: how many distinct rows there are
  *  workspace   device, 16-byte aligned, >= pg_lookup_grad_workspace_size bytes, scratch
  * n < 2^31; O * H <= 32 and r <= 2^20 (else PG_ERR_UNSUPPORTED); PG_HASH_TOY is PG_ERR_UNSUPPORTED. B*L == 0
- * writes a zero count. r % 8 == 0 with 16-byte aligned grad_e and grads_out takes 16-byte
- * accesses.
+ * writes a zero count. r % 8 == 0 with grad_e and grads_out aligned to 8 elements takes 16-
+ * and 32-byte accesses.
  */
 pg_status pg_lookup_grad_workspace_size(const pg_table_desc* desc, int64_t N, size_t* bytes);
 

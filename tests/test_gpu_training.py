@@ -78,7 +78,7 @@ def embed_rows(tokens, cmap, vocab, rows):
 
 @pytest.mark.parametrize("table_dtype", [F32, BF16])
 @pytest.mark.parametrize("out_dtype", [F32, BF16])
-@pytest.mark.parametrize("N,d,shift", [(1, 1, 0), (7, 33, 0), (300, 96, 0), (300, 96, 1), (5, 2560, 0), (129, 1032, 0),
+@pytest.mark.parametrize("N,d,shift", [(1, 1, 0), (7, 33, 0), (300, 96, 0), (300, 96, 1), (300, 96, 4), (5, 2560, 0), (129, 1032, 0),
                                        (64, 1025, 0)])
 def test_embed(cuda, table_dtype, out_dtype, N, d, shift):
     pg = _pg()
@@ -297,7 +297,8 @@ def test_lookup_grad_many_reads_and_large_row_numbers(cuda):
 def test_lookup_grad_unaligned(cuda):
     rng = np.random.default_rng(8)
     tokens = rng.integers(0, 300, (2, 90)).astype(np.int32)
-    check_lookup_grad(cuda, SPECS["pagegram"](), tokens, 300, None, BF16, F32, shift=1)
+    for shift in (1, 4):
+        check_lookup_grad(cuda, SPECS["pagegram"](), tokens, 300, None, BF16, F32, shift=shift)
 
 
 def test_lookup_grad_reads_bad_tokens_as_id_0(cuda):
