@@ -34,6 +34,7 @@ constexpr int kMaxSortBlocks = 152;                    // one per SM
 constexpr int kScanIters = (kMaxSortBlocks + 31) / 32;
 constexpr uint32_t kRefsPerBlock = 2048;               // at least, before another block joins
 constexpr uint32_t kDirectBlocks = 16;                 // up to here every block adds up all the counts itself
+constexpr uint64_t kFillPerBlock = 256 << 10;          // bytes of zeros, before another block joins
 constexpr int kHashItems = 32;                         // (order, head) items of a table
 
 struct SortCtrl {
@@ -55,6 +56,7 @@ struct RefSource {
   int32_t items;     // hashed lookup: references per token
   uint32_t per;      // 2^32 / items, rounded up: tile-local token numbers
   int32_t mode;
+  int32_t words;     // hashed lookup: sign words of a reference
   ItemConst ic[kHashItems];
 };
 
@@ -64,7 +66,7 @@ struct SortBuffers {
   uint32_t* totals;    // [digits]
   uint32_t* segs;      // [blocks] segments that start in a block's share
   uint2* pair[2];      // [n] (row, reference)
-  uint64_t* sign;      // [n] sign hashes of the references (hashed lookup)
+  uint64_t* sign;      // [n][ceil(r / 64)] sign words of the references (hashed lookup)
   float* parts;        // [tiles][2][r] sums of rows that cross a tile's start, its end
 };
 
@@ -93,7 +95,7 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   b->totals = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits));
   b->segs = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxSortBlocks));
   for (int i = 0; i < 2; ++i) b->pair[i] = reinterpret_cast<uint2*>(take(8 * un));
-  b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un)) : nullptr;
+  b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un * ((r + 63) / 64))) : nullptr;
   const size_t T = tile_refs(n, r);
   b->parts = reinterpret_cast<float*>(take((un + T - 1) / T * 2 * r * sizeof(float)));
   return at + 32;
@@ -101,16 +103,21 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
 
 // ------------------------------------------------------------------------------- the sort
 
-// All blocks of the grid; false after a time limit of about one second (then every block
+// A later kernel of the same call may be scheduled from here on; it waits for this one's end
+// (grid_dep_wait) before it reads anything.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The G sorting blocks of the grid; false after a time limit of about one second (then every block
 // gives up, since the count it waits for is not reached). `phase` counts the barriers.
-__device__ __forceinline__ bool grid_barrier(uint32_t* counter, uint32_t* phase, int* s_ok, int* err_word) {
+__device__ __forceinline__ bool grid_barrier(uint32_t G, uint32_t* counter, uint32_t* phase, int* s_ok, int* err_word) {
   *phase += 1;
   __syncthreads();
-  if (gridDim.x == 1) return true;
+  if (G == 1) return true;
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(counter, 1u);
-    const uint32_t want = *phase * gridDim.x;
+    const uint32_t want = *phase * G;
     const uint64_t t0 = now_ns();
     uint32_t seen;
     bool ok = true;
@@ -249,11 +256,32 @@ __device__ __forceinline__ uint32_t embed_key(const RefSource& src, uint32_t i) 
   return src.rows;
 }
 
+// Zeros over [p, p + bytes), p and bytes even: block `part` of `parts`.
+__device__ __forceinline__ void fill_zeros(uint8_t* p, uint64_t bytes, uint32_t part, uint32_t parts) {
+  uint8_t* first = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 31) & ~uintptr_t(31));
+  uint8_t* end = p + bytes;
+  uint8_t* last = reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(31));
+  if (first > last) first = last = end;  // no whole 32 bytes
+  const uint64_t pieces = static_cast<uint64_t>(last - first) / 32;
+  const float zero[8] = {};
+  for (uint64_t i = static_cast<uint64_t>(part) * kSortThreads + threadIdx.x; i < pieces;
+       i += static_cast<uint64_t>(parts) * kSortThreads)
+    store32(first + 32 * i, zero);
+  if (part == 0) {
+    for (uint8_t* q = p + 2 * threadIdx.x; q < first; q += 2 * kSortThreads) *reinterpret_cast<uint16_t*>(q) = 0;
+    for (uint8_t* q = last + 2 * threadIdx.x; q < end; q += 2 * kSortThreads) *reinterpret_cast<uint16_t*>(q) = 0;
+  }
+}
+
+// The first G blocks sort. Blocks past them, or the same ones afterwards where the grid has no
+// others, zero the embedding's gradient (`fill`): writing all of it here, under a sort that uses
+// few SMs and no bandwidth, is cheaper than knowing which rows will be written.
 template <bool HASHED>
 __global__ void __launch_bounds__(kSortThreads, 1)
     rowgrad_sort_kernel(const __grid_constant__ RefSource src, const __grid_constant__ SortBuffers b, uint32_t n,
                         uint32_t share, int passes, int bits, uint32_t* __restrict__ rows_out,
-                        int32_t* __restrict__ count_out, int* err_word) {
+                        int32_t* __restrict__ count_out, uint32_t G, uint8_t* fill, uint64_t fill_bytes,
+                        int* err_word) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);                                 // [warps][digits]
   uint32_t* s_base = reinterpret_cast<uint32_t*>(s_raw + kSortWarps * kMaxDigits * 2);  // [digits]
@@ -265,10 +293,13 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t lo = min(n, blockIdx.x * share), hi = min(n, lo + share);
   const int digits = 1 << bits;
-  const uint32_t G = gridDim.x;
   const bool one = share <= kSortTile;  // the share stays in registers between counting and scattering
   uint32_t phase = 0;
 
+  if (blockIdx.x >= G) {
+    fill_zeros(fill, fill_bytes, blockIdx.x - G, gridDim.x - G);
+    return;
+  }
   if (HASHED) {
     const int words = src.items * static_cast<int>(sizeof(ItemConst) / 4);
     for (int i = tid; i < words; i += kSortThreads)
@@ -303,7 +334,8 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             if constexpr (HASHED) {
               uint64_t hs;
               v.x = hashed_key(src, s_ic, reinterpret_cast<const uint32_t*>(s_cnt), t0, i, &hs);
-              b.sign[i] = hs;
+              uint64_t* sign = b.sign + static_cast<int64_t>(i) * src.words;
+              for (int q = 0; q < src.words; ++q) sign[q] = mix64(hs + kGolden * static_cast<uint64_t>(q + 1));
             } else {
               v.x = embed_key(src, i);
             }
@@ -331,7 +363,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     } else {
 if (2 * tid < digits)
         *reinterpret_cast<uint2*>(b.hist + blockIdx.x * digits + 2 * tid) = make_uint2(mine[0], mine[1]);
-      if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+      if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
       if (G <= kDirectBlocks) {  // every block adds up the counts itself
         below[0] = below[1] = total_of[0] = total_of[1] = 0;
         if (2 * tid < digits) {
@@ -363,7 +395,7 @@ if (2 * tid < digits)
           }
           if (lane == 0) *reinterpret_cast<uint2*>(b.totals + d) = make_uint2(run0, run1);
         }
-        if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+        if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
         const bool has = 2 * tid < digits;
         const uint2 x = has ? __ldcg(reinterpret_cast<const uint2*>(b.hist + blockIdx.x * digits + 2 * tid)) : make_uint2(0u, 0u);
         const uint2 y = has ? __ldcg(reinterpret_cast<const uint2*>(b.totals + 2 * tid)) : make_uint2(0u, 0u);
@@ -419,7 +451,7 @@ if (2 * tid < digits)
     uint2* swap = in_order;
     in_order = out_order;
     out_order = swap;
-    if ((HASHED || p + 1 < passes) && !grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+    if ((HASHED || p + 1 < passes) && !grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
   }
 
   if constexpr (HASHED) {
@@ -457,7 +489,7 @@ if (2 * tid < digits)
       count = total;
     } else {
       if (tid == 0) b.segs[blockIdx.x] = total;
-      if (!grid_barrier(&b.ctrl->barrier, &phase, &s_ok, err_word)) return;
+      if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
       const uint32_t ex = block_excl_scan(tid < G ? __ldcg(b.segs + tid) : 0u, s_warp, &count);
       if (tid == blockIdx.x) s_first = ex;
       __syncthreads();
@@ -491,19 +523,29 @@ if (2 * tid < digits)
       *count_out = static_cast<int32_t>(count);
     }
   }
-  if (tid == 0) atomicAdd(&b.ctrl->done, 1u);
+  if (fill_bytes && gridDim.x == G) fill_zeros(fill, fill_bytes, blockIdx.x, G);
+  if (tid == 0) {
+    if (G == 1)
+      b.ctrl->done = 1;  // (nothing zeroed it)
+    else
+      atomicAdd(&b.ctrl->done, 1u);
+  }
 }
 
 // ------------------------------------------------------------------------------- the sums
 
+constexpr int kSumThreads = 128;   // small blocks: the last wave of them is short
+constexpr int kJoinThreads = 256;
+
 struct SumArgs {
   const void* grad;          // summands, rows of r values; reference i has row i / share
-  const uint64_t* sign;      // sign hashes of the references, or null
+  const uint8_t* sign;       // sign bits of the references, a byte for 8 columns, or null
   const uint2* order;        // (output row, reference), rows ascending
   const SortCtrl* ctrl;
   float* parts;
   void* out;
   uint32_t n, share, blocks; // blocks: of the sort (all have to have finished)
+  uint32_t sign_bytes;       // of a reference
   uint32_t tiles, none;      // none: the output row of padding, which has none
   int32_t r, accumulate, compact;  // compact: rows from the count on are written as zeros
   float scale;
@@ -554,16 +596,19 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int c,
   store_cols<OUT, COLS>(a.out, at, y);
 }
 
-// A group of `lanes` lanes (a power of two) per tile of T references and lanes * COLS columns.
+// A group of `lanes` consecutive threads per tile of T references and lanes * COLS columns.
 // The loads of 8 summands (fp32: 4) are in flight at a time, and behind them those of the next
 // references' numbers.
 template <int IN, int OUT, int COLS>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kSumThreads, 5)
     rowgrad_sum_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
-  const int per_block = 256 / lanes;
-  const uint32_t tile = blockIdx.x * per_block + threadIdx.x / lanes;
-  const int c = (blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * COLS;
-  if (tile >= a.tiles || c >= a.r || a.ctrl->done != a.blocks) return;
+  const int per_block = kSumThreads / lanes;
+  const int group = threadIdx.x / lanes;
+  const uint32_t tile = blockIdx.x * per_block + group;
+  const int c = (blockIdx.y * lanes + threadIdx.x - group * lanes) * COLS;
+  grid_dep_launch();
+  grid_dep_wait();
+  if (group >= per_block || tile >= a.tiles || c >= a.r || a.ctrl->done != a.blocks) return;
   const uint32_t p0 = tile * T, p1 = min(p0 + T, a.n);
   constexpr int kFly = IN == PG_F32 && COLS == 8 ? 4 : 8;
   uint32_t ref[kFly], seg[kFly];
@@ -596,12 +641,12 @@ __global__ void __launch_bounds__(256, 2)
   bool from_before = before == cur;  // the row of `cur` began in an earlier tile
   for (uint32_t q0 = p0; q0 < p1 && cur != a.none; q0 += kFly) {
     Raw<IN, COLS> x[kFly];
-    uint64_t hs[kFly];
+    uint32_t neg[kFly];
     uint32_t sg[kFly];
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       x[k].load(a.grad, static_cast<int64_t>(a.share == 1 ? ref[k] : ref[k] / a.share) * a.r + c);
-      hs[k] = a.sign ? __ldg(a.sign + ref[k]) : 0ull;
+      neg[k] = a.sign ? __ldg(a.sign + static_cast<int64_t>(ref[k]) * a.sign_bytes + (c >> 3)) >> (c & 7) : 0u;
       sg[k] = seg[k];
     }
     if (q0 + kFly < p1) numbers(q0 + kFly);
@@ -619,9 +664,7 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
         for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
       }
-      uint32_t neg = 0;
-      if (a.sign) neg = static_cast<uint32_t>(mix64(hs[k] + kGolden * ((c >> 6) + 1)) >> (c & 63));
-      x[k].add(acc, neg);
+      x[k].add(acc, neg[k]);
     }
   }
   if (cur == a.none) return;
@@ -637,17 +680,18 @@ __global__ void __launch_bounds__(256, 2)
 // above; a row over more tiles than a block has groups is added by the whole block, group k
 // taking every per_block-th part (at most one such row starts in a block's tiles).
 template <int OUT, int COLS>
-__global__ void __launch_bounds__(256) rowgrad_join_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
-  __shared__ float s_acc[256][COLS];
+__global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
+  __shared__ float s_acc[kJoinThreads][COLS];
   __shared__ uint32_t s_long, s_end;
+  grid_dep_wait();
   if (a.ctrl->done != a.blocks) return;
-  const int per_block = 256 / lanes, group = threadIdx.x / lanes;
+  const int per_block = kJoinThreads / lanes, group = threadIdx.x / lanes;
   const uint32_t tile = blockIdx.x * per_block + group;
-  const int c = (blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * COLS;
+  const int c = group < per_block ? (blockIdx.y * lanes + threadIdx.x - group * lanes) * COLS : a.r;
   if (threadIdx.x == 0) s_long = kNoRow;
   __syncthreads();
   const uint32_t p0 = tile * T, p1 = p0 + T;
-  constexpr int kFly = 4;
+  constexpr int kFly = 8;
   auto add = [&](uint32_t k, uint32_t end, uint32_t step, float (&acc)[COLS]) {  // first parts of tiles k, k + step, ..
     for (; k < end; k += kFly * step) {
       float x[kFly][COLS];
@@ -663,7 +707,7 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(const __grid_constant
         for (int j = 0; j < COLS; ++j) acc[j] += x[f][j];
     }
   };
-  if (tile < a.tiles && p1 < a.n) {
+  if (group < per_block && tile < a.tiles && p1 < a.n) {
     const uint32_t u = __ldg(&a.order[p1].x), prev = __ldg(&a.order[p1 - 1].x);
     const uint32_t before = p0 > 0 ? __ldg(&a.order[p0 - 1].x) : kNoRow;
     const uint32_t next = p1 + T < a.n ? __ldg(&a.order[p1 + T].x) : kNoRow;
@@ -749,14 +793,20 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   const uint32_t share = (n + G - 1) / G / 8 * 8 + 8;  // whole groups of 8 references
   G = (n + share - 1) / share;
 
-  cudaError_t e = cudaMemsetAsync(b.ctrl, 0, kCtrlBytes, stream);
+  const uint64_t fill_bytes = HASHED || a.accumulate ? 0 : static_cast<uint64_t>(src.rows) * a.r * dtype_bytes(out);
+  const uint64_t fill_blocks = (fill_bytes + kFillPerBlock - 1) / kFillPerBlock;
+  const uint32_t grid_blocks = static_cast<uint32_t>(
+      min(G + fill_blocks, static_cast<uint64_t>(max(static_cast<int>(G), min(sm_count(), kMaxSortBlocks)))));
+
+  cudaError_t e = cudaSuccess;
+  if (G > 1) e = cudaMemsetAsync(b.ctrl, 0, kCtrlBytes, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   auto sort = rowgrad_sort_kernel<HASHED>;
   const int smem = kSortWarps * kMaxDigits * 2 + kMaxDigits * 4;
   e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(G);
+  cfg.gridDim = dim3(grid_blocks);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -765,7 +815,8 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = G > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, share, passes, bits, rows_out, count_out, device_error_word());
+  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, share, passes, bits, rows_out, count_out, G,
+                         static_cast<uint8_t*>(a.out), fill_bytes, device_error_word());
   if (e != cudaSuccess) return cuda_fail(e);
   pg_status st = after_launch(1);
   if (st != PG_OK) return st;
@@ -773,7 +824,8 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   a.order = b.pair[HASHED ? (passes & 1) ^ 1 : passes & 1];  // hashed lookup: with segment numbers
   a.none = HASHED ? kNoRow : src.rows;
   a.compact = HASHED;
-  a.sign = b.sign;
+  a.sign = reinterpret_cast<const uint8_t*>(b.sign);
+  a.sign_bytes = 8 * static_cast<uint32_t>(src.words);
   a.ctrl = b.ctrl;
   a.parts = b.parts;
   a.n = n;
@@ -782,15 +834,27 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   a.tiles = (n + T - 1) / T;
   const bool vec = a.r % 8 == 0 && aligned(a.grad, vec_bytes(in)) && aligned(a.out, vec_bytes(out));
   const int cols = vec ? 8 : 1;
-  int lanes = 1;
-  while (lanes < 32 && lanes * cols < a.r) lanes *= 2;
-  const uint32_t per_block = 256 / lanes;
-  const dim3 grid((a.tiles + per_block - 1) / per_block, (a.r + lanes * cols - 1) / (lanes * cols));
-  (vec ? sum_fn<8>(in, out) : sum_fn<1>(in, out))<<<grid, 256, 0, stream>>>(a, lanes, T);
-  st = after_launch(1);
+  // threads a row, in equal column blocks of at most 32 (an 80-wide head takes 10, 12 tiles a block)
+  const int row_threads = (a.r + cols - 1) / cols, col_blocks = (row_threads + 31) / 32;
+  const int lanes = (row_threads + col_blocks - 1) / col_blocks;
+  // each is scheduled while the kernel before it runs out, and waits for its end
+  auto launch = [&](SumFn fn, int threads) -> pg_status {
+    const uint32_t per_block = threads / lanes;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((a.tiles + per_block - 1) / per_block, col_blocks);
+    c.blockDim = dim3(threads);
+    c.stream = stream;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = early;
+    c.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&c, fn, a, lanes, T);
+    return err == cudaSuccess ? after_launch(1) : cuda_fail(err);
+  };
+  st = launch(vec ? sum_fn<8>(in, out) : sum_fn<1>(in, out), kSumThreads);
   if (st != PG_OK) return st;
-  (vec ? join_fn<8>(out) : join_fn<1>(out))<<<grid, 256, 0, stream>>>(a, lanes, T);
-  return after_launch(1);
+  return launch(vec ? join_fn<8>(out) : join_fn<1>(out), kJoinThreads);
 }
 
 }  // namespace
@@ -825,12 +889,12 @@ extern "C" pg_status pg_embed_grad(const int32_t* tokens, int64_t N, uint32_t vo
   if (device_cc() != 103) return PG_ERR_DEVICE;
   st = prepare_err(err_index, stream);
   if (st != PG_OK) return st;
-  if (!accumulate) {
-    const size_t bytes = static_cast<size_t>(rows) * d * dtype_bytes(table_dtype);
-    cudaError_t e = cudaMemsetAsync(grad_table, 0, bytes, stream);
-    if (e != cudaSuccess) return cuda_fail(e);
+  if (N == 0) {
+    if (accumulate) return PG_OK;
+    const cudaError_t e =
+        cudaMemsetAsync(grad_table, 0, static_cast<size_t>(rows) * d * dtype_bytes(table_dtype), stream);
+    return e == cudaSuccess ? PG_OK : cuda_fail(e);
   }
-  if (N == 0) return PG_OK;
   RefSource src = {};
   src.tokens = tokens;
   src.canon_map = canon_map;
@@ -899,6 +963,7 @@ extern "C" pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* to
   src.items = items;
   src.per = static_cast<uint32_t>(((1ull << 32) + items - 1) / items);  // (1 item: 0, see hashed_key)
   src.mode = desc->mode;
+  src.words = g.W;
   HashParams P;
   fill_hash_params(desc, g, &P);
   for (int i = 0; i < items; ++i) init_item_const(src.ic[i], P, desc->hash_seed, i);
