@@ -54,19 +54,20 @@ struct RefSource {
   uint32_t L;        // hashed lookup: sequence length
   uint64_t fm_L;     // its fastmod constant
   int32_t items;     // hashed lookup: references per token
-  uint32_t per;      // 2^32 / items, rounded up: tile-local token numbers
+  int32_t heads;     // of them in a group (items, where there is one group)
+  uint32_t per;      // 2^32 / heads, rounded up: tile-local token numbers
   int32_t mode;
-  int32_t words;     // hashed lookup: sign words of a reference
+  int32_t words;     // hashed lookup: sign words of a reference (1, or an even number)
   ItemConst ic[kHashItems];
 };
 
 struct SortBuffers {
   SortCtrl* ctrl;
   uint32_t* hist;      // [blocks][digits]
-  uint32_t* totals;    // [digits]
+  uint32_t* totals;    // [groups][digits]
   uint32_t* segs;      // [blocks] segments that start in a block's share
   uint2* pair[2];      // [n] (row, reference)
-  uint64_t* sign;      // [n][ceil(r / 64)] sign words of the references (hashed lookup)
+  uint64_t* sign;      // [n][words] sign words of the references (hashed lookup)
   float* parts;        // [tiles][2][r] sums of rows that cross a tile's start, its end
 };
 
@@ -80,6 +81,9 @@ constexpr int64_t kFewLanes = 152 * 16 * 32;
 
 inline int tile_refs(int64_t n, int r) { return n * ((r + 7) / 8) / 32 >= kFewLanes ? 32 : 8; }
 
+// Sign words kept for a reference of r columns.
+inline int sign_words(int r) { return r <= 64 ? 1 : (r + 127) / 128 * 2; }
+
 // Carves the buffers from `base`; returns the bytes they take (base may be null to size them).
 size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   size_t at = 0;
@@ -92,10 +96,10 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   const size_t un = static_cast<size_t>(n);
   b->ctrl = reinterpret_cast<SortCtrl*>(take(kCtrlBytes));
   b->hist = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits * kMaxSortBlocks));
-  b->totals = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits));
+  b->totals = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits * (hashed ? kHashItems : 1)));
   b->segs = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxSortBlocks));
   for (int i = 0; i < 2; ++i) b->pair[i] = reinterpret_cast<uint2*>(take(8 * un));
-  b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un * ((r + 63) / 64))) : nullptr;
+  b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un * sign_words(r))) : nullptr;
   const size_t T = tile_refs(n, r);
   b->parts = reinterpret_cast<float*>(take((un + T - 1) / T * 2 * r * sizeof(float)));
   return at + 32;
@@ -226,26 +230,45 @@ __device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end,
   totals[1] = run >> 16;
 }
 
-// Canonical IDs of the tokens that the references [t0, end) and their n-grams read, into s_id
-// (token tok0 - 3 first): one read of the token and of the map for all of a token's heads.
-__device__ __forceinline__ void stage_ids(const RefSource& src, uint32_t t0, uint32_t end, uint32_t* s_id) {
-  const int64_t tok0 = static_cast<int64_t>(t0 / src.items) - 3;
-  const int count = static_cast<int>((end - 1) / src.items - tok0) + 1;
+// The hashed lookup's references are numbered group by group: the rows of a group (one subtable,
+// PageGram one order) lie in a range of their own, so each group is sorted by itself, by rows
+// that count from its first: fewer digits, and counts of fewer blocks to add up. Reference j of
+// a group is head j mod `heads` of token j / heads.
+
+// Canonical IDs of the tokens that a group's references [t0, end) and their n-grams read, into
+// s_id (token tok0 - 3 first, tok0 that of t0): one read of the token and of the map for all of
+// its heads.
+__device__ __forceinline__ void stage_ids(const RefSource& src, uint32_t tok0, uint32_t end, uint32_t* s_id) {
+  const int64_t first = static_cast<int64_t>(tok0) - 3;
+  const int count = static_cast<int>((end - 1) / src.heads - first) + 1;
   for (int k = threadIdx.x; k < count; k += kSortThreads)
-    s_id[k] = tok0 + k >= 0 ? canon_token(src.tokens, src.canon_map, src.vocab, tok0 + k, src.err) : 0u;
+    s_id[k] = first + k >= 0 ? canon_token(src.tokens, src.canon_map, src.vocab, first + k, src.err) : 0u;
 }
 
-// Hashed lookup: the reference's row and its sign hash.
+// Row and sign hash of the reference `local` places after head 0 of token tok0 (local < 8192 +
+// 32); *ref = its number by tokens (t * items + item), the row of its gradient.
 __device__ __forceinline__ uint32_t hashed_key(const RefSource& src, const ItemConst* s_ic, const uint32_t* s_id,
-                                               uint32_t t0, uint32_t i, uint64_t* hs) {
-  const uint32_t tok0 = t0 / src.items, local = i - tok0 * src.items;  // local < 8192 + 32
-  const uint32_t s = __umulhi(local, src.per) + (src.items == 1 ? local : 0u);
-  const ItemConst& it = s_ic[local - s * src.items];
+                                               uint32_t item0, uint32_t tok0, uint32_t local, uint32_t* ref, uint64_t* hs) {
+  const uint32_t s = __umulhi(local, src.per) + (src.heads == 1 ? local : 0u);
+  const uint32_t item = item0 + local - s * src.heads;
   const uint32_t t = fastmod(tok0 + s, src.fm_L, src.L);
   uint64_t c[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) c[j] = t >= static_cast<uint32_t>(j) ? s_id[s + 3 - j] : kPad;
-  return item_row_ids(it, src.mode, c, hs);
+  *ref = (tok0 + s) * src.items + item;
+  return item_row_ids(s_ic[item], src.mode, c, hs);
+}
+
+// The sign words of reference `ref` (an even number of them beyond one: 16 bytes at a time).
+__device__ __forceinline__ void store_signs(uint64_t* sign, uint32_t ref, int words, uint64_t hs) {
+  if (words == 1) {
+    sign[ref] = mix64(hs + kGolden);
+    return;
+  }
+  ulonglong2* at = reinterpret_cast<ulonglong2*>(sign + static_cast<int64_t>(ref) * words);
+  for (int q = 0; q < words; q += 2)
+    at[q / 2] = make_ulonglong2(mix64(hs + kGolden * static_cast<uint64_t>(q + 1)),
+                                mix64(hs + kGolden * static_cast<uint64_t>(q + 2)));
 }
 
 // Embedding: the position's row; padding gets the key `rows`.
@@ -273,13 +296,14 @@ __device__ __forceinline__ void fill_zeros(uint8_t* p, uint64_t bytes, uint32_t 
   }
 }
 
-// The first G blocks sort. Blocks past them, or the same ones afterwards where the grid has no
+// The first G blocks sort, `per_group` of them each of the groups of `size` references, a block
+// `share` consecutive ones. Blocks past them, or the same ones afterwards where the grid has no
 // others, zero the embedding's gradient (`fill`): writing all of it here, under a sort that uses
 // few SMs and no bandwidth, is cheaper than knowing which rows will be written.
 template <bool HASHED>
 __global__ void __launch_bounds__(kSortThreads, 1)
     rowgrad_sort_kernel(const __grid_constant__ RefSource src, const __grid_constant__ SortBuffers b, uint32_t n,
-                        uint32_t share, int passes, int bits, uint32_t* __restrict__ rows_out,
+                        uint32_t size, uint32_t per_group, uint32_t share, int passes, int bits, uint32_t* __restrict__ rows_out,
                         int32_t* __restrict__ count_out, uint32_t G, uint8_t* fill, uint64_t fill_bytes,
                         int* err_word) {
   extern __shared__ __align__(16) uint8_t s_raw[];
@@ -291,10 +315,11 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   __shared__ ItemConst s_ic[HASHED ? kHashItems : 1];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t lo = min(n, blockIdx.x * share), hi = min(n, lo + share);
+  const uint32_t group = blockIdx.x / per_group, part = blockIdx.x - group * per_group, start = group * size;
+  const uint32_t lo = start + min(size, part * share), hi = start + min(size, (part + 1) * share);
   const int digits = 1 << bits;
   const bool one = share <= kSortTile;  // the share stays in registers between counting and scattering
-  uint32_t phase = 0;
+  uint32_t phase = 0, row0 = 0;
 
   if (blockIdx.x >= G) {
     fill_zeros(fill, fill_bytes, blockIdx.x - G, gridDim.x - G);
@@ -304,6 +329,10 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     const int words = src.items * static_cast<int>(sizeof(ItemConst) / 4);
     for (int i = tid; i < words; i += kSortThreads)
       reinterpret_cast<uint32_t*>(s_ic)[i] = reinterpret_cast<const uint32_t*>(src.ic)[i];
+    __syncthreads();
+    row0 = s_ic[group * src.heads].base;  // the group's first row: keys count from it
+    __syncthreads();
+    if (tid < src.items) s_ic[tid].base -= row0;
     __syncthreads();
   }
 
@@ -318,9 +347,12 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
       const int items = tile_items(hi - t0);
       const uint32_t first = t0 + warp * 32 * items, end = min(hi, t0 + kSortTile);
+      uint32_t tok0 = 0, head0 = 0;  // hashed lookup: the tile's first token, and where in it
       if (HASHED && p == 0) {
+        tok0 = (t0 - start) / src.heads;
+        head0 = t0 - start - tok0 * src.heads;
         __syncthreads();
-        stage_ids(src, t0, end, reinterpret_cast<uint32_t*>(s_cnt));
+        stage_ids(src, tok0, end - start, reinterpret_cast<uint32_t*>(s_cnt));
         __syncthreads();
       }
 #pragma unroll
@@ -333,9 +365,9 @@ __global__ void __launch_bounds__(kSortThreads, 1)
           } else {
             if constexpr (HASHED) {
               uint64_t hs;
-              v.x = hashed_key(src, s_ic, reinterpret_cast<const uint32_t*>(s_cnt), t0, i, &hs);
-              uint64_t* sign = b.sign + static_cast<int64_t>(i) * src.words;
-              for (int q = 0; q < src.words; ++q) sign[q] = mix64(hs + kGolden * static_cast<uint64_t>(q + 1));
+              v.x = hashed_key(src, s_ic, reinterpret_cast<const uint32_t*>(s_cnt), group * src.heads, tok0,
+                               i - t0 + head0, &v.y, &hs);
+              store_signs(b.sign, v.y, src.words, hs);
             } else {
               v.x = embed_key(src, i);
             }
@@ -361,44 +393,46 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         total_of[q] = mine[q];
       }
     } else {
-if (2 * tid < digits)
-        *reinterpret_cast<uint2*>(b.hist + blockIdx.x * digits + 2 * tid) = make_uint2(mine[0], mine[1]);
+      const bool has = 2 * tid < digits;
+      if (has) *reinterpret_cast<uint2*>(b.hist + blockIdx.x * digits + 2 * tid) = make_uint2(mine[0], mine[1]);
       if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-      if (G <= kDirectBlocks) {  // every block adds up the counts itself
+      if (per_group <= kDirectBlocks) {  // every block adds up its group's counts itself
         below[0] = below[1] = total_of[0] = total_of[1] = 0;
-        if (2 * tid < digits) {
+        if (has) {
+          const uint32_t* counts = b.hist + group * per_group * digits + 2 * tid;
 #pragma unroll 8
-          for (uint32_t k = 0; k < G; ++k) {
-            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(b.hist + k * digits + 2 * tid));
-            below[0] += k < blockIdx.x ? v.x : 0u;
-            below[1] += k < blockIdx.x ? v.y : 0u;
+          for (uint32_t k = 0; k < per_group; ++k) {
+            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(counts + k * digits));
+            below[0] += k < part ? v.x : 0u;
+            below[1] += k < part ? v.y : 0u;
             total_of[0] += v.x;
             total_of[1] += v.y;
           }
         }
-      } else {  // a warp scans two digits' counts over the blocks
-        for (int d = 2 * (warp * G + blockIdx.x); d < digits; d += 2 * G * kSortWarps) {
+      } else {  // a warp scans two digits' counts over a group's blocks
+        const uint32_t pairs = digits / 2, groups = G / per_group;
+        for (uint32_t w = warp * G + blockIdx.x; w < groups * pairs; w += G * kSortWarps) {
+          const uint32_t of = w / pairs, d = 2 * (w - of * pairs);
+          uint32_t* counts = b.hist + of * per_group * digits + d;
           uint2 v[kScanIters];
           uint32_t run0 = 0, run1 = 0;
 #pragma unroll
           for (int k = 0; k < kScanIters; ++k)
-            v[k] = k * 32 + lane < G ? __ldcg(reinterpret_cast<const uint2*>(b.hist + (k * 32 + lane) * digits + d))
-                                     : make_uint2(0u, 0u);
+            v[k] = k * 32 + lane < per_group ? __ldcg(reinterpret_cast<const uint2*>(counts + (k * 32 + lane) * digits))
+                                             : make_uint2(0u, 0u);
 #pragma unroll
           for (int k = 0; k < kScanIters; ++k) {
             const uint32_t i0 = warp_incl_scan(v[k].x, lane), i1 = warp_incl_scan(v[k].y, lane);
-            if (k * 32 + lane < G)
-              *reinterpret_cast<uint2*>(b.hist + (k * 32 + lane) * digits + d) =
-                  make_uint2(run0 + i0 - v[k].x, run1 + i1 - v[k].y);
+            if (k * 32 + lane < per_group)
+              *reinterpret_cast<uint2*>(counts + (k * 32 + lane) * digits) = make_uint2(run0 + i0 - v[k].x, run1 + i1 - v[k].y);
             run0 += __shfl_sync(0xffffffffu, i0, 31);
             run1 += __shfl_sync(0xffffffffu, i1, 31);
           }
-          if (lane == 0) *reinterpret_cast<uint2*>(b.totals + d) = make_uint2(run0, run1);
+          if (lane == 0) *reinterpret_cast<uint2*>(b.totals + of * digits + d) = make_uint2(run0, run1);
         }
         if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-        const bool has = 2 * tid < digits;
         const uint2 x = has ? __ldcg(reinterpret_cast<const uint2*>(b.hist + blockIdx.x * digits + 2 * tid)) : make_uint2(0u, 0u);
-        const uint2 y = has ? __ldcg(reinterpret_cast<const uint2*>(b.totals + 2 * tid)) : make_uint2(0u, 0u);
+        const uint2 y = has ? __ldcg(reinterpret_cast<const uint2*>(b.totals + group * digits + 2 * tid)) : make_uint2(0u, 0u);
         below[0] = x.x;
         below[1] = x.y;
         total_of[0] = y.x;
@@ -409,7 +443,7 @@ if (2 * tid < digits)
     uint32_t ex = block_excl_scan(total_of[0] + total_of[1], s_warp, &all);
 #pragma unroll
     for (int q = 0; q < kDigitsPerThread; ++q) {
-      if (2 * tid + q < digits) s_base[2 * tid + q] = ex + below[q];
+      if (2 * tid + q < digits) s_base[2 * tid + q] = start + ex + below[q];
       ex += total_of[q];
     }
     __syncthreads();
@@ -458,8 +492,8 @@ if (2 * tid < digits)
     // ---- segments of equal rows: their numbers replace the rows (in the free buffer), the rows
     // go to rows_out. A thread takes 8 consecutive references at a time.
     auto flags = [&](uint32_t i, uint2 (&v)[8]) -> uint32_t {  // bit j: a segment starts at i + j
-      uint32_t prev = i > 0 && i < hi ? __ldcg(&in_order[i - 1].x) : 0u, f = 0;
-      if (i + 8 <= hi) {  // shares start at multiples of 8
+      uint32_t prev = i > start && i < hi ? __ldcg(&in_order[i - 1].x) : 0u, f = 0;
+      if (i + 8 <= hi && i % 2 == 0) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const uint4 x = __ldcg(reinterpret_cast<const uint4*>(in_order + i + j));
@@ -472,7 +506,7 @@ if (2 * tid < digits)
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (i + j < hi && (i + j == 0 || v[j].x != prev)) f |= 1u << j;
+        if (i + j < hi && (i + j == start || v[j].x != prev)) f |= 1u << j;
         prev = v[j].x;
       }
       return f;
@@ -503,11 +537,11 @@ if (2 * tid < digits)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (i + j >= hi) break;
-        if ((f >> j) & 1u) rows_out[u++] = v[j].x;
+        if ((f >> j) & 1u) rows_out[u++] = row0 + v[j].x;
         v[j].x = u - 1;
         if (i + j >= count) rows_out[i + j] = PG_NO_ROW;
       }
-      if (i + 8 <= hi) {
+      if (i + 8 <= hi && i % 2 == 0) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2)
           *reinterpret_cast<uint4*>(out_order + i + j) = make_uint4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
@@ -779,9 +813,9 @@ SumFn join_fn(int out) {
   return out == PG_F32 ? rowgrad_join_kernel<PG_F32, COLS> : rowgrad_join_kernel<PG_BF16, COLS>;
 }
 
-// Sorts the references and writes the sums. n >= 1; `keys` the largest key.
+// Sorts the references and writes the sums. n >= 1, in `groups` groups; `keys` the largest key.
 template <bool HASHED>
-pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs a, int in, int out, void* workspace,
+pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint32_t keys, SumArgs a, int in, int out, void* workspace,
                         uint32_t* rows_out, int32_t* count_out, cudaStream_t stream) {
   SortBuffers b;
   carve(static_cast<uint8_t*>(workspace), n, a.r, HASHED, &b);
@@ -789,14 +823,16 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   while (key_bits < 32 && (keys >> key_bits)) ++key_bits;
   const int passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
   const int bits = (key_bits + passes - 1) / passes;
-  uint32_t G = min((n + kRefsPerBlock - 1) / kRefsPerBlock, static_cast<uint32_t>(min(sm_count(), kMaxSortBlocks)));
-  const uint32_t share = (n + G - 1) / G / 8 * 8 + 8;  // whole groups of 8 references
-  G = (n + share - 1) / share;
+  const uint32_t sms = static_cast<uint32_t>(min(sm_count(), kMaxSortBlocks)), size = n / groups;
+  uint32_t per_group = max(1u, min((size + kRefsPerBlock - 1) / kRefsPerBlock, sms / groups));
+  const uint32_t share = (size + per_group - 1) / per_group;
+  per_group = (size + share - 1) / share;
+  const uint32_t G = groups * per_group;
 
   const uint64_t fill_bytes = HASHED || a.accumulate ? 0 : static_cast<uint64_t>(src.rows) * a.r * dtype_bytes(out);
   const uint64_t fill_blocks = (fill_bytes + kFillPerBlock - 1) / kFillPerBlock;
   const uint32_t grid_blocks = static_cast<uint32_t>(
-      min(G + fill_blocks, static_cast<uint64_t>(max(static_cast<int>(G), min(sm_count(), kMaxSortBlocks)))));
+      min(G + fill_blocks, static_cast<uint64_t>(max(G, sms))));
 
   cudaError_t e = cudaSuccess;
   if (G > 1) e = cudaMemsetAsync(b.ctrl, 0, kCtrlBytes, stream);
@@ -815,7 +851,7 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t keys, SumArgs
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = G > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, share, passes, bits, rows_out, count_out, G,
+  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, size, per_group, share, passes, bits, rows_out, count_out, G,
                          static_cast<uint8_t*>(a.out), fill_bytes, device_error_word());
   if (e != cudaSuccess) return cuda_fail(e);
   pg_status st = after_launch(1);
@@ -908,7 +944,7 @@ extern "C" pg_status pg_embed_grad(const int32_t* tokens, int64_t N, uint32_t vo
   a.r = d;
   a.accumulate = accumulate;
   a.scale = scale;
-  return row_gradients<false>(src, static_cast<uint32_t>(N), src.rows, a, grad_dtype, table_dtype, workspace, nullptr,
+  return row_gradients<false>(src, static_cast<uint32_t>(N), 1, src.rows, a, grad_dtype, table_dtype, workspace, nullptr,
                               nullptr, stream);
 }
 
@@ -961,9 +997,13 @@ extern "C" pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* to
   src.L = static_cast<uint32_t>(L);
   src.fm_L = fastmod_constant(src.L);
   src.items = items;
-  src.per = static_cast<uint32_t>(((1ull << 32) + items - 1) / items);  // (1 item: 0, see hashed_key)
+  // groups (see stage_ids), unless one block sorts all of it
+  const uint32_t n = static_cast<uint32_t>(N * items);
+  const uint32_t groups = n <= static_cast<uint32_t>(kSortTile) ? 1u : desc->mode == PG_ENGRAM ? items : g.O;
+  src.heads = items / static_cast<int>(groups);
+  src.per = static_cast<uint32_t>(((1ull << 32) + src.heads - 1) / src.heads);  // (1 head: 0, see hashed_key)
   src.mode = desc->mode;
-  src.words = g.W;
+  src.words = sign_words(desc->r);
   HashParams P;
   fill_hash_params(desc, g, &P);
   for (int i = 0; i < items; ++i) init_item_const(src.ic[i], P, desc->hash_seed, i);
@@ -973,6 +1013,14 @@ extern "C" pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* to
   a.share = desc->mode == PG_FLAT ? static_cast<uint32_t>(items) : 1u;
   a.r = desc->r;
   a.scale = 1.f;
-  return row_gradients<true>(src, static_cast<uint32_t>(N * items), static_cast<uint32_t>(g.rows - 1), a, grad_dtype,
-                             out_dtype, workspace, rows_out, count_out, stream);
+  uint32_t keys = static_cast<uint32_t>(g.rows - 1);
+  if (groups > 1) {
+    keys = 0;
+    for (uint32_t i = 0; i < groups; ++i) {
+      const ItemConst& it = src.ic[i * src.heads];
+      const uint64_t rows = static_cast<uint64_t>(it.div_main) * (desc->mode == PG_PAGEGRAM ? it.stride : 1u);
+      keys = max(keys, static_cast<uint32_t>(rows - 1));
+    }
+  }
+  return row_gradients<true>(src, n, groups, keys, a, grad_dtype, out_dtype, workspace, rows_out, count_out, stream);
 }
