@@ -528,3 +528,15 @@ def test_gradients_in_a_graph(cuda):
         torch.cuda.synchronize()
         assert torch.equal(rows, want[0]) and torch.equal(out, want[1]) and torch.equal(count, want[2])
         assert torch.equal(table, expect)
+
+
+# ------------------------------------------------------------------------------ together
+
+
+def test_training_example_learns(cuda):
+    # embedding, lookup, projection, both gradients and the orthogonalised update in one loop
+    from examples.train_memory import train
+    losses = train(steps=30, n_tokens=4096).tolist()
+    assert all(math.isfinite(x) for x in losses)
+    assert losses[-1] < 0.5 * losses[0], losses
+    assert _pg().device_error() == 0
