@@ -8,7 +8,7 @@
 // X stays in G's orientation: where a product needs its columns as the long rows of an
 // operand, the tensor core reads the tile "MN-major" (the descriptor's transpose), and since
 // Bm holds a I the last product has nothing to add. The tiles of A and Bm below the diagonal
-// are not computed: each tile above it is also written, transposed, where its mirror image is.
+// are neither computed nor stored: an operand that needs one reads its mirror image MN-major.
 //
 // Between the products X, A and Bm are held as fp16 scaled by 2^10 (pg.h): 11 significant
 // bits, against the 8 of the bf16 result.
@@ -39,7 +39,7 @@ constexpr float kUnhold = 1.f / 1024.f;
 constexpr int kNormParts = 128;         // partial sums of squares per matrix, at most
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kStageBytes = 32 * 32 * 2;  // an epilogue warp's staged 32 x 32 chunk, in each orientation
+constexpr int kStageBytes = 32 * 32 * 2;  // an epilogue warp's staged 32 x 32 chunk
 constexpr int kBK = 64;                 // columns of a k-block: 128 bytes of fp16
 constexpr int kRowsP = 128;             // rows of P that a CTA stages
 constexpr int kBox = 64;                // rows and columns of a TMA box (8 KB)
@@ -55,12 +55,12 @@ struct Tile {
   static constexpr int kPBytes = kRowsP * kBK * 2;
   static constexpr int kQBytes = kRowsQ * kBK * 2;
   static constexpr int kStages = PAIR ? 6 : 8;
-  static constexpr int kTmemCols = 2 * kN;
   static constexpr int kChunks = kN / 64;              // 32-column chunks of an epilogue warp
+  static constexpr int kTmemCols = 2 * kN;
   static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands
       (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
   static constexpr size_t kRing = static_cast<size_t>(kStages) * (kPBytes + kQBytes);
-  static constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kStageBytes;
+  static constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kStageBytes;
 };
 
 struct OrthoCtrl {
@@ -240,8 +240,33 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
 
 // --------------------------------------------------------------------- norm and scaling
 
+// 8 consecutive values of G as they lie in memory, so that many loads can be in flight.
+template <int DT>
+struct Raw8 {
+  float f[DT == PG_F32 ? 8 : 1];
+  uint4 h;
+
+  __device__ __forceinline__ void load(const void* G, int64_t at) {
+    if constexpr (DT == PG_F32)
+      load32(static_cast<const float*>(G) + at, f);
+    else
+      h = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(G) + at));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (DT == PG_F32) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = f[k];
+    } else {
+      const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = __uint_as_float((k & 1) ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+    }
+  }
+};
+
 // Partial sums of squares, of x, 2^64 x and 2^-64 x: whichever of the three neither overflows
 // nor vanishes gives the norm. Part `part` of matrix `b` is a contiguous share of it.
+template <int DT>
 __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kThreads / 32]) {
   const int64_t share = ((g.size + g.parts - 1) / g.parts + 7) / 8 * 8;
   const int64_t lo = part * share, hi = min(g.size, lo + share), base = b * g.size;
@@ -253,32 +278,24 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kT
     sum[2] = fmaf(down, down, sum[2]);
   };
   if (g.g_vec) {
-    constexpr int kFly = 8;  // loads in flight
+    constexpr int kFly = DT == PG_F32 ? 8 : 16;  // loads in flight
     for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kFly * kThreads * 8) {
-      float x[kFly][8];
+      Raw8<DT> raw[kFly];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) raw[u].load(g.G, base + min(i + u * kThreads * 8, hi - 8));
 #pragma unroll
       for (int u = 0; u < kFly; ++u) {
-        const int64_t at = i + u * kThreads * 8;
+        if (i + u * kThreads * 8 >= hi) break;
+        float x[8];
+        raw[u].get(x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[u][k] = 0.f;
-        if (at >= hi) continue;
-        if (g.dtype == PG_F32)
-          load_cols<PG_F32, 8>(g.G, base + at, x[u]);
-        else
-          load_cols<PG_BF16, 8>(g.G, base + at, x[u]);
+        for (int k = 0; k < 8; ++k) add(x[k]);
       }
-#pragma unroll
-      for (int u = 0; u < kFly; ++u)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) add(x[u][k]);
     }
   } else {
     for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
       float x[1];
-      if (g.dtype == PG_F32)
-        load_cols<PG_F32, 1>(g.G, base + i, x);
-      else
-        load_cols<PG_BF16, 1>(g.G, base + i, x);
+      load_cols<DT, 1>(g.G, base + i, x);
       add(x[0]);
     }
   }
@@ -325,6 +342,7 @@ __device__ __forceinline__ uint32_t two_half(float lo, float hi) {
 
 // X0: rows of G scaled and rounded into rows of stride ldx, 8 columns at a time. A block owns a
 // contiguous share of the rows of all matrices.
+template <int DT>
 __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
   const uint32_t per_row = (g.n + 7) / 8;
   const int64_t rows = static_cast<int64_t>(g.batch) * g.m;
@@ -340,44 +358,38 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
     __syncthreads();
     const float scale = *s_scale;
     const uint32_t vecs = static_cast<uint32_t>(r1 - r0) * per_row;  // < 2^31: at most m of at most 2048
-    constexpr int kFly = 4;
-    for (uint32_t v0 = threadIdx.x; v0 < vecs; v0 += kFly * kThreads) {
-      float x[kFly][8];
+    auto store = [&](uint32_t v, const float (&x)[8]) {
+      const uint32_t r = v / per_row, j = (v - r * per_row) * 8;
+      *reinterpret_cast<uint4*>(g.X[0] + (r0 + r) * g.ldx + j) =
+          make_uint4(two_half(x[0] * scale, x[1] * scale), two_half(x[2] * scale, x[3] * scale),
+                     two_half(x[4] * scale, x[5] * scale), two_half(x[6] * scale, x[7] * scale));
+    };
+    if (g.g_vec) {  // n % 8 == 0: a row's pieces follow the row before's
+      constexpr int kFly = DT == PG_F32 ? 8 : 16;
+      for (uint32_t v0 = threadIdx.x; v0 < vecs; v0 += kFly * kThreads) {
+        Raw8<DT> raw[kFly];
 #pragma unroll
-      for (int u = 0; u < kFly; ++u) {
-        const uint32_t v = v0 + u * kThreads;
-        if (v >= vecs) continue;
-        const int64_t r = r0 + v / per_row;
-        const int j = static_cast<int>(v % per_row) * 8;
-        const int64_t at = r * g.n + j;
-        if (g.g_vec) {
-          if (g.dtype == PG_F32)
-            load_cols<PG_F32, 8>(g.G, at, x[u]);
-          else
-            load_cols<PG_BF16, 8>(g.G, at, x[u]);
-        } else {
+        for (int u = 0; u < kFly; ++u)
+          raw[u].load(g.G, r0 * g.n + 8ll * min(v0 + u * kThreads, vecs - 1));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float y[1] = {0.f};
-            if (j + k < g.n) {
-              if (g.dtype == PG_F32)
-                load_cols<PG_F32, 1>(g.G, at + k, y);
-              else
-                load_cols<PG_BF16, 1>(g.G, at + k, y);
-            }
-            x[u][k] = y[0];
-          }
+        for (int u = 0; u < kFly; ++u) {
+          if (v0 + u * kThreads >= vecs) break;
+          float x[8];
+          raw[u].get(x);
+          store(v0 + u * kThreads, x);
         }
       }
+    } else {
+      for (uint32_t v = threadIdx.x; v < vecs; v += kThreads) {
+        const uint32_t r = v / per_row, j = (v - r * per_row) * 8;
+        float x[8];
 #pragma unroll
-      for (int u = 0; u < kFly; ++u) {
-        const uint32_t v = v0 + u * kThreads;
-        if (v >= vecs) continue;
-        const int64_t r = r0 + v / per_row;
-        const int j = static_cast<int>(v % per_row) * 8;
-        *reinterpret_cast<uint4*>(g.X[0] + r * g.ldx + j) =
-            make_uint4(two_half(x[u][0] * scale, x[u][1] * scale), two_half(x[u][2] * scale, x[u][3] * scale),
-                       two_half(x[u][4] * scale, x[u][5] * scale), two_half(x[u][6] * scale, x[u][7] * scale));
+        for (int k = 0; k < 8; ++k) {
+          float y[1] = {0.f};
+          if (j + k < static_cast<uint32_t>(g.n)) load_cols<DT, 1>(g.G, (r0 + r) * g.n + j + k, y);
+          x[k] = y[0];
+        }
+        store(v, x);
       }
     }
     r0 = r1;
@@ -394,8 +406,18 @@ struct Product {
   int64_t strideD;       // between matrices, elements
   int ldD, M, N, K;
   float alpha, beta, diag;
-  bool symmetric, p_mn, q_mn;  // MN-major operands
+  bool symmetric;
+  // An operand is K-major (its rows are the matrix's), MN-major (the matrix's columns), or, A
+  // and Bm, symmetric with only the tiles that reach the diagonal or lie above it stored: those
+  // K-major, the others as the MN-major mirror image.
+  enum Layout { kRows, kColumns, kUpper } p_in, q_in;
 };
+
+// Whether k-block k0 of the operand's rows from r0 on is read MN-major.
+template <bool PAIR>
+__device__ __forceinline__ bool reads_mn(Product::Layout in, int r0, int k0) {
+  return in == Product::kColumns || (in == Product::kUpper && k0 / Tile<PAIR>::kM < r0 / Tile<PAIR>::kM);
+}
 
 __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& maps, int step, int kind) {
   const int cur = step & 1;
@@ -406,15 +428,15 @@ __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& ma
   r.C = nullptr;
   r.alpha = kUnhold;
   r.beta = r.diag = 0.f;
-  r.p_mn = r.q_mn = false;
   r.ldD = g.ldp;
   if (kind == 0) {         // A
     r.P = r.Q = &maps.X[cur];
-    r.p_mn = r.q_mn = !wide;
+    r.p_in = r.q_in = wide ? Product::kRows : Product::kColumns;
     r.D = g.A;
     r.K = wide ? g.n : g.m;
   } else if (kind == 1) {  // Bm
     r.P = r.Q = &maps.A;
+    r.p_in = r.q_in = Product::kUpper;
     r.C = g.A;
     r.D = g.Bm;
     r.alpha = g.c * kUnhold;
@@ -423,7 +445,8 @@ __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& ma
   } else {                 // X
     r.P = wide ? &maps.Bm : &maps.X[cur];
     r.Q = wide ? &maps.X[cur] : &maps.Bm;
-    r.q_mn = wide;
+    r.p_in = wide ? Product::kUpper : Product::kRows;
+    r.q_in = wide ? Product::kColumns : Product::kUpper;
     r.D = step + 1 == g.steps ? nullptr : g.X[cur ^ 1];
     r.M = g.m;
     r.N = g.n;
@@ -541,10 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- |G|_F and X0
   uint32_t phase = 0;
-  for (int w = blockIdx.x; w < g.batch * g.parts; w += gridDim.x) norm_part(g, w / g.parts, w % g.parts, s_sum);
+  const bool f32 = g.dtype == PG_F32;
+  for (int w = blockIdx.x; w < g.batch * g.parts; w += gridDim.x)
+    f32 ? norm_part<PG_F32>(g, w / g.parts, w % g.parts, s_sum) : norm_part<PG_BF16>(g, w / g.parts, w % g.parts, s_sum);
   bool ok = grid_meet(g, bars, &phase);
   if (ok) {
-    scale_rows(g, &s_scale);
+    f32 ? scale_rows<PG_F32>(g, &s_scale) : scale_rows<PG_BF16>(g, &s_scale);
     ok = grid_meet(g, bars, &phase);
   }
 
@@ -572,15 +597,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) bar_expect(full, (PAIR ? 2 : 1) * (T::kPBytes + T::kQBytes));
             const int k0 = kb * kBK;
             const int p0 = i * T::kM + static_cast<int>(rank) * kRowsP, q0 = j * T::kN + static_cast<int>(rank) * T::kRowsQ;
+            const bool p_mn = reads_mn<PAIR>(pr.p_in, i * T::kM, k0), q_mn = reads_mn<PAIR>(pr.q_in, j * T::kN, k0);
 #pragma unroll
             for (int h = 0; h < kRowsP / kBox; ++h) {
               const int r = p0 + h * kBox;
-              load_box<PAIR>(dp + h * kBoxBytes, pr.P, bar, pr.p_mn ? r : k0, pr.p_mn ? k0 : r, b);
+              load_box<PAIR>(dp + h * kBoxBytes, pr.P, bar, p_mn ? r : k0, p_mn ? k0 : r, b);
             }
 #pragma unroll
             for (int h = 0; h < T::kRowsQ / kBox; ++h) {
               const int r = q0 + h * kBox;
-              load_box<PAIR>(dq + h * kBoxBytes, pr.Q, bar, pr.q_mn ? r : k0, pr.q_mn ? k0 : r, b);
+              load_box<PAIR>(dq + h * kBoxBytes, pr.Q, bar, q_mn ? r : k0, q_mn ? k0 : r, b);
             }
             if (++stage == S) {
               stage = 0;
@@ -596,15 +622,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (lane == 0 && rank == 0) {
         bool fine = true;
-        const uint32_t idesc = T::kIdesc | (pr.p_mn ? 1u << 15 : 0u) | (pr.q_mn ? 1u << 16 : 0u);
-        // 16 k further: 32 bytes along a K-major row, two 8-k groups of an MN-major box
-        const uint32_t step_p = pr.p_mn ? 2048 >> 4 : 2u, step_q = pr.q_mn ? 2048 >> 4 : 2u;
         for (int t = unit; fine && t < total; t += units) {
           if (!wait<PAIR>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
             fine = false;
             break;
           }
           fence_after();
+          int b, i, j;
+          tile_at<PAIR>(pr, per, t, &b, &i, &j);
           const uint32_t d = tmem + static_cast<uint32_t>(acc * T::kN);
           for (int kb = 0; kb < num_kb; ++kb) {
             if (!wait<PAIR>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
@@ -613,7 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_after();
             const uint32_t sp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes));
-            const uint64_t dp = operand_desc(sp, pr.p_mn), dq = operand_desc(sp + T::kPBytes, pr.q_mn);
+            const bool p_mn = reads_mn<PAIR>(pr.p_in, i * T::kM, kb * kBK), q_mn = reads_mn<PAIR>(pr.q_in, j * T::kN, kb * kBK);
+            const uint64_t dp = operand_desc(sp, p_mn), dq = operand_desc(sp + T::kPBytes, q_mn);
+            const uint32_t idesc = T::kIdesc | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u);
+            // 16 k further: 32 bytes along a K-major row, two 8-k groups of an MN-major box
+            const uint32_t step_p = p_mn ? 2048 >> 4 : 2u, step_q = q_mn ? 2048 >> 4 : 2u;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
               mma_f16<PAIR>(d, dp + step_p * k, dq + step_q * k, idesc, (kb | k) != 0);
@@ -636,19 +665,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // A warp takes 32 rows of the tile (its TMEM lanes) in chunks of 32 columns. TMEM gives a
       // lane one row; global memory wants neighbouring lanes on one row. So a chunk passes
-      // through 2 KB of the warp's shared memory in each orientation, C the same way in:
-      // lane-per-row accesses to global memory (32 lines each) took half of the kernel's time.
+      // through 2 KB of the warp's shared memory, C the same way in: lane-per-row accesses to
+      // global memory (32 lines each) took half of the kernel's time.
       const int quarter = warp & 3, half = (warp - 2) >> 2;
-      uint8_t* s_row = s_epi + (warp - 2) * 2 * kStageBytes;  // [32 rows][32 columns], 16-byte pieces swizzled
-      uint8_t* s_col = s_row + kStageBytes;                   // [32 columns][32 rows]
+      uint8_t* s_row = s_epi + (warp - 2) * kStageBytes;  // [32 rows][32 columns], 16-byte pieces swizzled
       auto piece = [&](int r, int c) { return reinterpret_cast<uint4*>(s_row + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); };
-      const int lr = lane >> 2, lc = lane & 3;                // this lane's row (of 8) and piece in a coalesced access
+      const int lr = lane >> 2, lc = lane & 3;            // this lane's row (of 8) and piece in a coalesced access
       bool fine = true;
       for (int t = unit; t < total; t += units) {
         int b, i, j;
         tile_at<PAIR>(pr, per, t, &b, &i, &j);
         const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
-        const bool mirror = pr.symmetric && j * T::kN >= (i + 1) * T::kM;  // else the tile holds its own mirror image
         const int col0 = j * T::kN + half * (T::kChunks * 32);
         const bool some = row0 < pr.M;
         const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
@@ -729,24 +756,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) *piece(lane, k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-          if (mirror) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              reinterpret_cast<uint16_t*>(s_col)[k * 32 + lane] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
-          }
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (row0 + lr + 8 * k < pr.M)
               *reinterpret_cast<uint4*>(rows + (lr + 8 * k) * ldr + lc * 8) = *piece(lr + 8 * k, lc);
-          if (mirror) {  // (rows past the last one land in the padding up to ldD)
-            uint16_t* cols = reinterpret_cast<uint16_t*>(pr.D) + b * pr.strideD + static_cast<int64_t>(c0) * pr.ldD + row0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (c0 + lr + 8 * k < pr.N)
-                *reinterpret_cast<uint4*>(cols + static_cast<int64_t>(lr + 8 * k) * pr.ldD + lc * 8) =
-                    reinterpret_cast<const uint4*>(s_col)[(lr + 8 * k) * 4 + lc];
-          }
           __syncwarp();
         }
         fence_before();
@@ -880,11 +894,12 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
     return PG_ERR_CUDA;
   // no more units than the widest phase has work for: the fewer blocks, the quicker they meet
   const int64_t tiles = static_cast<int64_t>(g.batch) * std::max(tiles_of<PAIR>(g.m, g.n, false), tiles_of<PAIR>(g.p, g.p, true));
-  const int64_t reads = (static_cast<int64_t>(g.batch) * g.size + 8 * kThreads - 1) / (8 * kThreads);  // of the norm and scaling
+  const int64_t piece = 8 * kThreads;  // what a block's threads read at a time in the norm and the scaling
+  const int64_t reads = (static_cast<int64_t>(g.batch) * g.size + piece - 1) / piece;
   units = static_cast<int>(std::min<int64_t>(units, std::max(tiles, PAIR ? (reads + 1) / 2 : reads)));
   // one round of partial sums over the blocks
   const int blocks = (PAIR ? 2 : 1) * units;
-  g.parts = static_cast<int>(std::min<int64_t>({kNormParts, std::max(1, blocks / g.batch), (g.size + 8 * kThreads - 1) / (8 * kThreads)}));
+  g.parts = static_cast<int>(std::min<int64_t>({kNormParts, std::max(1, blocks / g.batch), (g.size + piece - 1) / piece}));
   cudaError_t e = cudaMemsetAsync(g.ctrl, 0, sizeof(OrthoCtrl), stream);
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchAttribute attr[2];
