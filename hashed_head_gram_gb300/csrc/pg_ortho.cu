@@ -16,7 +16,7 @@
 // One cooperative launch does the whole update: norm, scaling, and 3 * steps products on the
 // tensor cores, the blocks meeting at a grid barrier between them. The held matrices stay in
 // L2 where they fit.
-//   warp 0      TMA producer: 64-deep k-blocks of both operands, 128-byte swizzle, into a ring
+//   warp 0      TMA producer: 128-deep k-blocks of both operands, 128-byte swizzle, into a ring
 //   warp 1      tcgen05.mma issuer, two accumulators in TMEM
 //   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
 #include <cuda.h>
@@ -40,10 +40,11 @@ constexpr int kNormParts = 128;         // partial sums of squares per matrix, a
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kStageBytes = 32 * 32 * 2;  // an epilogue warp's staged 32 x 32 chunk
-constexpr int kBK = 64;                 // columns of a k-block: 128 bytes of fp16
+// A k-block is 128 deep: with 64 the waits, copies and commits that a block costs its two
+// issuing threads, and not the tensor core, set the pace (1280 x 2560: 45 us a step, 41 with 128).
+constexpr int kBK = 128;
+constexpr int kLine = 64;               // fp16 of a 128-byte line: the inner extent of a TMA box
 constexpr int kRowsP = 128;             // rows of P that a CTA stages
-constexpr int kBox = 64;                // rows and columns of a TMA box (8 KB)
-constexpr int kBoxBytes = kBox * kBox * 2;
 
 // Tiles: a CTA pair computes 256 x 256 (each CTA stages 128 rows of P and 128 of Q and
 // accumulates 128 rows), a single CTA 128 x 64.
@@ -54,7 +55,7 @@ struct Tile {
   static constexpr int kRowsQ = PAIR ? 128 : 64;
   static constexpr int kPBytes = kRowsP * kBK * 2;
   static constexpr int kQBytes = kRowsQ * kBK * 2;
-  static constexpr int kStages = PAIR ? 6 : 8;
+  static constexpr int kStages = PAIR ? 3 : 4;
   static constexpr int kChunks = kN / 64;              // 32-column chunks of an epilogue warp
   static constexpr int kTmemCols = 2 * kN;
   static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands
@@ -81,8 +82,10 @@ struct OrthoArgs {
   float a, b, c, eps, scale;
 };
 
+// Boxes of 64 columns and 128 rows; for the single CTA's 64 rows of Q, K-major, of 64 rows too.
 struct Maps {
   CUtensorMap X[2], A, Bm;
+  CUtensorMap Xq[2], Aq, Bmq;
 };
 
 // ------------------------------------------------------------------------------ wrappers
@@ -228,14 +231,30 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory descriptor of an operand tile of 64 x 64 boxes written by TMA with 128-byte
-// swizzle (61-63 = 2; version 1 at 46-47; start address >> 4 at 0-13). K-major: a box holds 64
-// rows of the operand, and 8-row groups lie 1024 bytes apart (bits 32-45), the boxes' too.
-// MN-major: a box holds 64 of the operand's rows along its 128-byte lines and 64 k down them;
-// 8-k groups lie 1024 bytes apart (32-45) and the next 64 rows one box further (16-29).
+// Shared-memory descriptor of an operand tile written by TMA with 128-byte swizzle (61-63 = 2;
+// version 1 at 46-47; start address >> 4 at 0-13), in lines of 64 fp16.
+//   K-major: the lines are operand rows, 8-row groups 1024 bytes apart (bits 32-45), and the 64
+//   deeper half of a k-block lies behind all the rows.
+//   MN-major: a line holds 64 operand rows at one k, 8-k groups lie 1024 bytes apart (32-45), and
+//   the next 64 rows lie behind the 128 lines of the first (bits 16-29).
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(mn ? kBoxBytes >> 4 : 1) << 16) |
-         (64ull << 32) | (1ull << 46) | (2ull << 61);
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>(mn ? kBK * kLine * 2 >> 4 : 1) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The copies of one operand's k-block k0: its rows from r0 on.
+template <bool PAIR, int ROWS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, const CUtensorMap* map_rows,
+                                             bool mn, int r0, int k0, int b, uint32_t bar) {
+  if (mn) {
+#pragma unroll
+    for (int h = 0; h < ROWS / kLine; ++h)
+      load_box<PAIR>(dst + h * (kBK * kLine * 2), map, bar, r0 + h * kLine, k0, b);
+  } else {
+#pragma unroll
+    for (int h = 0; h < kBK / kLine; ++h)
+      load_box<PAIR>(dst + h * (ROWS * kLine * 2), map_rows, bar, k0 + h * kLine, r0, b);
+  }
 }
 
 // --------------------------------------------------------------------- norm and scaling
@@ -400,7 +419,7 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
 
 // D = alpha P Q^T + beta C + diag I; see the top of the file.
 struct Product {
-  const CUtensorMap *P, *Q;
+  const CUtensorMap *P, *Q, *Qrows;  // Qrows: Q in boxes of as many rows as a CTA stages of it
   const __half* C;       // laid out as D, or null
   __half* D;             // [M, N]; null for the last product (out)
   int64_t strideD;       // between matrices, elements
@@ -419,6 +438,7 @@ __device__ __forceinline__ bool reads_mn(Product::Layout in, int r0, int k0) {
   return in == Product::kColumns || (in == Product::kUpper && k0 / Tile<PAIR>::kM < r0 / Tile<PAIR>::kM);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& maps, int step, int kind) {
   const int cur = step & 1;
   const bool wide = g.m <= g.n;
@@ -431,11 +451,13 @@ __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& ma
   r.ldD = g.ldp;
   if (kind == 0) {         // A
     r.P = r.Q = &maps.X[cur];
+    r.Qrows = PAIR ? r.Q : &maps.Xq[cur];
     r.p_in = r.q_in = wide ? Product::kRows : Product::kColumns;
     r.D = g.A;
     r.K = wide ? g.n : g.m;
   } else if (kind == 1) {  // Bm
     r.P = r.Q = &maps.A;
+    r.Qrows = PAIR ? r.Q : &maps.Aq;
     r.p_in = r.q_in = Product::kUpper;
     r.C = g.A;
     r.D = g.Bm;
@@ -445,6 +467,7 @@ __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& ma
   } else {                 // X
     r.P = wide ? &maps.Bm : &maps.X[cur];
     r.Q = wide ? &maps.X[cur] : &maps.Bm;
+    r.Qrows = PAIR ? r.Q : wide ? &maps.Xq[cur] : &maps.Bmq;
     r.p_in = wide ? Product::kUpper : Product::kRows;
     r.q_in = wide ? Product::kColumns : Product::kUpper;
     r.D = step + 1 == g.steps ? nullptr : g.X[cur ^ 1];
@@ -577,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int stage = 0, acc = 0;
   uint32_t ring_phase = 0, acc_phase = 0;
   for (int prod = 0; ok && prod < 3 * g.steps; ++prod) {
-    const Product pr = product_of(g, maps, prod / 3, prod % 3);
+    const Product pr = product_of<PAIR>(g, maps, prod / 3, prod % 3);
     const int per = tiles_of<PAIR>(pr.M, pr.N, pr.symmetric), total = per * g.batch;
     const int num_kb = (pr.K + kBK - 1) / kBK;
     if (warp == 0) {
@@ -598,16 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int k0 = kb * kBK;
             const int p0 = i * T::kM + static_cast<int>(rank) * kRowsP, q0 = j * T::kN + static_cast<int>(rank) * T::kRowsQ;
             const bool p_mn = reads_mn<PAIR>(pr.p_in, i * T::kM, k0), q_mn = reads_mn<PAIR>(pr.q_in, j * T::kN, k0);
-#pragma unroll
-            for (int h = 0; h < kRowsP / kBox; ++h) {
-              const int r = p0 + h * kBox;
-              load_box<PAIR>(dp + h * kBoxBytes, pr.P, bar, p_mn ? r : k0, p_mn ? k0 : r, b);
-            }
-#pragma unroll
-            for (int h = 0; h < T::kRowsQ / kBox; ++h) {
-              const int r = q0 + h * kBox;
-              load_box<PAIR>(dq + h * kBoxBytes, pr.Q, bar, q_mn ? r : k0, q_mn ? k0 : r, b);
-            }
+            load_operand<PAIR, kRowsP>(dp, pr.P, pr.P, p_mn, p0, k0, b, bar);
+            load_operand<PAIR, T::kRowsQ>(dq, pr.Q, pr.Qrows, q_mn, q0, k0, b, bar);
             if (++stage == S) {
               stage = 0;
               ring_phase ^= 1u;
@@ -641,11 +656,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool p_mn = reads_mn<PAIR>(pr.p_in, i * T::kM, kb * kBK), q_mn = reads_mn<PAIR>(pr.q_in, j * T::kN, kb * kBK);
             const uint64_t dp = operand_desc(sp, p_mn), dq = operand_desc(sp + T::kPBytes, q_mn);
             const uint32_t idesc = T::kIdesc | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u);
-            // 16 k further: 32 bytes along a K-major row, two 8-k groups of an MN-major box
-            const uint32_t step_p = p_mn ? 2048 >> 4 : 2u, step_q = q_mn ? 2048 >> 4 : 2u;
+            // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
+            // groups of an MN-major tile
+            const uint32_t step_p = p_mn ? 2048 >> 4 : 32 >> 4, step_q = q_mn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t half_p = p_mn ? 4 * step_p : T::kPBytes / 2 >> 4, half_q = q_mn ? 4 * step_q : T::kQBytes / 2 >> 4;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-              mma_f16<PAIR>(d, dp + step_p * k, dq + step_q * k, idesc, (kb | k) != 0);
+              mma_f16<PAIR>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
+                            (kb | k) != 0);
             commit<PAIR>(smem_addr(&bars->empty[stage]));
             if (++stage == S) {
               stage = 0;
@@ -831,13 +849,13 @@ size_t carve_ortho(uint8_t* base, int64_t batch, int m, int n, OrthoArgs* o) {
   return at + 128;
 }
 
-// [batch, rows, cols] fp16 with row stride ld, boxes of 64 x 64, 128-byte swizzle.
-bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, int ld) {
+// [batch, rows, cols] fp16 with row stride ld, boxes of 64 columns, 128-byte swizzle.
+bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, int ld, int box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(rows) * ld * 2};
-  cuuint32_t box[3] = {kBox, kBox, 1};
+  cuuint32_t box[3] = {kLine, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -889,8 +907,12 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   pg_status st = resident_units<PAIR>(&units);
   if (st != PG_OK) return st;
   Maps maps;
-  if (!held_map(&maps.X[0], g.X[0], g.batch, g.m, g.n, g.ldx) || !held_map(&maps.X[1], g.X[1], g.batch, g.m, g.n, g.ldx) ||
-      !held_map(&maps.A, g.A, g.batch, g.p, g.p, g.ldp) || !held_map(&maps.Bm, g.Bm, g.batch, g.p, g.p, g.ldp))
+  auto encode = [&](CUtensorMap (&X)[2], CUtensorMap& A, CUtensorMap& Bm, int box_rows) {
+    return held_map(&X[0], g.X[0], g.batch, g.m, g.n, g.ldx, box_rows) &&
+           held_map(&X[1], g.X[1], g.batch, g.m, g.n, g.ldx, box_rows) &&
+           held_map(&A, g.A, g.batch, g.p, g.p, g.ldp, box_rows) && held_map(&Bm, g.Bm, g.batch, g.p, g.p, g.ldp, box_rows);
+  };
+  if (!encode(maps.X, maps.A, maps.Bm, kRowsP) || (!PAIR && !encode(maps.Xq, maps.Aq, maps.Bmq, Tile<false>::kRowsQ)))
     return PG_ERR_CUDA;
   // no more units than the widest phase has work for: the fewer blocks, the quicker they meet
   const int64_t tiles = static_cast<int64_t>(g.batch) * std::max(tiles_of<PAIR>(g.m, g.n, false), tiles_of<PAIR>(g.p, g.p, true));
