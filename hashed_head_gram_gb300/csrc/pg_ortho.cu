@@ -39,12 +39,12 @@ constexpr float kUnhold = 1.f / 1024.f;
 constexpr int kNormParts = 128;         // partial sums of squares per matrix, at most
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kStageBytes = 32 * 32 * 2;  // an epilogue warp's staged 32 x 32 chunk
 // A k-block is 128 deep: with 64 the waits, copies and commits that a block costs its two
 // issuing threads, and not the tensor core, set the pace (1280 x 2560: 45 us a step, 41 with 128).
 constexpr int kBK = 128;
 constexpr int kLine = 64;               // fp16 of a 128-byte line: the inner extent of a TMA box
 constexpr int kRowsP = 128;             // rows of P that a CTA stages
+static_assert(kRowsP == kBK, "one box shape serves both layouts");
 
 // Tiles: a CTA pair computes 256 x 256 (each CTA stages 128 rows of P and 128 of Q and
 // accumulates 128 rows), a single CTA 128 x 64.
@@ -56,7 +56,9 @@ struct Tile {
   static constexpr int kPBytes = kRowsP * kBK * 2;
   static constexpr int kQBytes = kRowsQ * kBK * 2;
   static constexpr int kStages = PAIR ? 3 : 4;
-  static constexpr int kChunks = kN / 64;              // 32-column chunks of an epilogue warp
+  static constexpr int kChunkN = 32;       // columns that an epilogue warp stages at a time
+  static constexpr int kChunks = kN / 2 / kChunkN;     // of its half of the tile
+  static constexpr int kStageBytes = 32 * kChunkN * 2;
   static constexpr int kTmemCols = 2 * kN;
   static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands
       (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
@@ -217,8 +219,8 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // Orders generic-proxy accesses to global memory before TMA accesses (and back).
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// 32 consecutive fp32 columns of this warp's 32 TMEM lanes: lane i gets row i.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes: lane i gets row i (after tmem_wait).
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -228,7 +230,14 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
+}
+
+// Waits for the loads into r, which nothing reads before this.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
 }
 
 // Shared-memory descriptor of an operand tile written by TMA with 128-byte swizzle (61-63 = 2;
@@ -259,7 +268,8 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 
 // --------------------------------------------------------------------- norm and scaling
 
-// 8 consecutive values of G as they lie in memory, so that many loads can be in flight.
+// 8 consecutive values of G as they lie in memory; the loads are volatile so that they stay
+// together, ahead of their uses.
 template <int DT>
 struct Raw8 {
   float f[DT == PG_F32 ? 8 : 1];
@@ -267,9 +277,13 @@ struct Raw8 {
 
   __device__ __forceinline__ void load(const void* G, int64_t at) {
     if constexpr (DT == PG_F32)
-      load32(static_cast<const float*>(G) + at, f);
+      asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                   : "l"(static_cast<const float*>(G) + at));
     else
-      h = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(G) + at));
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
+                   : "l"(static_cast<const uint16_t*>(G) + at));
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     if constexpr (DT == PG_F32) {
@@ -547,6 +561,132 @@ __device__ __forceinline__ bool grid_meet(const OrthoArgs& g, Bars<S>* bars, uin
   return bars->ok != 0;
 }
 
+// What an epilogue writes. One instance each: its body has no branches between the columns, so
+// that the arithmetic of a chunk overlaps (with them a chunk took twice as long).
+enum Kind { kMakeA, kMakeB, kMakeX, kMakeOut };
+
+// A warp takes 32 rows of a tile (its TMEM lanes) and half of its columns, in chunks. TMEM gives
+// a lane one row; global memory wants neighbouring lanes on one row. So a chunk passes through
+// the warp's shared memory, C the same way in: lane-per-row accesses to global memory (32 lines
+// each) took half of the kernel's time. False once a wait gave up.
+template <bool PAIR, int KIND, int S>
+__device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, Bars<S>* bars, uint8_t* s_epi, uint32_t tmem,
+                                         int unit, int units, uint32_t rank, int* acc_io, uint32_t* acc_phase_io) {
+  using T = Tile<PAIR>;
+  constexpr int kC = T::kChunkN, kPieces = kC / 8, kSide = 32 / kPieces;  // 16-byte pieces a row; rows an access covers
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  uint8_t* s_row = s_epi + (warp - 2) * T::kStageBytes;  // [32 rows][kC columns], pieces swizzled over the banks
+  auto piece = [&](int r, int c) {
+    return reinterpret_cast<uint4*>(s_row + r * (2 * kC) + ((c ^ (r * kPieces / 8 % kPieces)) << 4));
+  };
+  const int lr = lane / kPieces, lc = lane % kPieces;    // this lane's row (of kSide) and piece in a coalesced access
+  const int per = tiles_of<PAIR>(pr.M, pr.N, pr.symmetric), total = per * g.batch;
+  const float alpha = KIND == kMakeOut ? pr.alpha * g.scale * kUnhold : pr.alpha;
+  int acc = *acc_io;
+  uint32_t acc_phase = *acc_phase_io;
+  for (int t = unit; t < total; t += units) {
+    int b, i, j;
+    tile_at<PAIR>(pr, per, t, &b, &i, &j);
+    const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
+    const int col0 = j * T::kN + half * (T::kN / 2);
+    const bool some = row0 < pr.M;
+    const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
+    uint4 cw[kPieces];  // C of the next chunk, in coalesced order
+    auto load_c = [&](int ch) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        cw[k] = make_uint4(0, 0, 0, 0);
+        if (row0 + lr + kSide * k < pr.M && col0 + ch * kC + lc * 8 < pr.ldD)
+          cw[k] = __ldcg(reinterpret_cast<const uint4*>(pr.C + at + static_cast<int64_t>(kSide * k) * pr.ldD + ch * kC));
+      }
+    };
+    if (KIND == kMakeB) load_c(0);
+    if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, &bars->abort))) return false;
+    fence_after();
+#pragma unroll 1
+    for (int ch = 0; some && ch < T::kChunks; ++ch) {
+      const int c0 = col0 + ch * kC;
+      if (c0 >= pr.N) break;
+      uint32_t r[kC];
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * T::kN) +
+                            static_cast<uint32_t>(half * (T::kN / 2) + ch * kC);
+#pragma unroll
+      for (int k = 0; k < kC; k += 32) tmem_load(from + k, r + k);
+      if (KIND == kMakeB) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) *piece(lr + kSide * k, lc) = cw[k];
+        if (ch + 1 < T::kChunks) load_c(ch + 1);
+        __syncwarp();
+      }
+      tmem_wait(r);
+      float x[kC];
+#pragma unroll
+      for (int k = 0; k < kC; ++k) x[k] = alpha * __uint_as_float(r[k]);
+      if (KIND == kMakeB) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          const uint4 q = *piece(lane, k);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e / 2]));
+            x[8 * k + e] = fmaf(pr.beta, f.x, x[8 * k + e]);
+            x[8 * k + e + 1] = fmaf(pr.beta, f.y, x[8 * k + e + 1]);
+          }
+        }
+        if (c0 < row0 + 32 && row0 < c0 + kC) {  // the diagonal crosses the chunk
+#pragma unroll
+          for (int k = 0; k < kC; ++k)
+            if (c0 + k == row0 + lane) x[k] += pr.diag;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {  // two columns a word: fp16, or the result in bf16
+        const float* v = x + 8 * k;
+        *piece(lane, k) = KIND == kMakeOut
+            ? make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]))
+            : make_uint4(two_half(v[0], v[1]), two_half(v[2], v[3]), two_half(v[4], v[5]), two_half(v[6], v[7]));
+      }
+      __syncwarp();
+      if (KIND != kMakeOut || (g.out_vec && c0 + kC <= pr.N)) {  // (columns past N land in the padding of D's rows)
+        uint16_t* to = KIND != kMakeOut ? reinterpret_cast<uint16_t*>(pr.D) + at + ch * kC
+                                        : reinterpret_cast<uint16_t*>(g.out) + b * g.size +
+                                              static_cast<int64_t>(row0 + lr) * pr.N + c0 + lc * 8;
+        const int64_t ld = KIND != kMakeOut ? pr.ldD : pr.N;
+        uint4 q[kPieces];
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) q[k] = *piece(lr + kSide * k, lc);
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+          if (row0 + lr + kSide * k < pr.M) *reinterpret_cast<uint4*>(to + kSide * k * ld) = q[k];
+      } else {  // a ragged edge of the result, or one at an odd address
+        uint16_t* to = reinterpret_cast<uint16_t*>(g.out) + b * g.size + static_cast<int64_t>(row0) * pr.N + c0;
+        for (int e = lane; e < 32 * kC; e += 32) {
+          const int rr = e / kC, cc = e % kC;
+          if (row0 + rr < pr.M && c0 + cc < pr.N)
+            to[static_cast<int64_t>(rr) * pr.N + cc] = reinterpret_cast<const uint16_t*>(piece(rr, cc / 8))[cc % 8];
+        }
+      }
+      __syncwarp();
+    }
+    fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t bar = smem_addr(&bars->acc_empty[acc]);
+      if constexpr (PAIR)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
+      else
+        bar_arrive(bar);
+    }
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+  }
+  *acc_io = acc;
+  *acc_phase_io = acc_phase;
+  return true;
+}
+
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     ortho_kernel(const __grid_constant__ Maps maps, const __grid_constant__ OrthoArgs g) {
@@ -681,118 +821,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // A warp takes 32 rows of the tile (its TMEM lanes) in chunks of 32 columns. TMEM gives a
-      // lane one row; global memory wants neighbouring lanes on one row. So a chunk passes
-      // through 2 KB of the warp's shared memory, C the same way in: lane-per-row accesses to
-      // global memory (32 lines each) took half of the kernel's time.
-      const int quarter = warp & 3, half = (warp - 2) >> 2;
-      uint8_t* s_row = s_epi + (warp - 2) * kStageBytes;  // [32 rows][32 columns], 16-byte pieces swizzled
-      auto piece = [&](int r, int c) { return reinterpret_cast<uint4*>(s_row + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); };
-      const int lr = lane >> 2, lc = lane & 3;            // this lane's row (of 8) and piece in a coalesced access
-      bool fine = true;
-      for (int t = unit; t < total; t += units) {
-        int b, i, j;
-        tile_at<PAIR>(pr, per, t, &b, &i, &j);
-        const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
-        const int col0 = j * T::kN + half * (T::kChunks * 32);
-        const bool some = row0 < pr.M;
-        const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
-        uint4 cw[4];  // C of the next chunk, in coalesced order
-        auto load_c = [&](int ch) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            cw[k] = make_uint4(0, 0, 0, 0);
-            if (row0 + lr + 8 * k < pr.M && col0 + ch * 32 < pr.N)
-              cw[k] = __ldcg(reinterpret_cast<const uint4*>(pr.C + at + static_cast<int64_t>(8 * k) * pr.ldD + ch * 32));
-          }
-        };
-        if (pr.C) load_c(0);
-        if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
-          fine = false;
-          break;
-        }
-        fence_after();
-#pragma unroll 1
-        for (int ch = 0; some && ch < T::kChunks; ++ch) {
-          const int c0 = col0 + ch * 32;
-          if (c0 >= pr.N) break;
-          uint32_t r[32];
-          tmem_load(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * T::kN) +
-                        static_cast<uint32_t>(half * (T::kChunks * 32) + ch * 32), r);
-          float x[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = pr.alpha * __uint_as_float(r[k]);
-          if (pr.C) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) *piece(lr + 8 * k, lc) = cw[k];
-            if (ch + 1 < T::kChunks) load_c(ch + 1);
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 q = *piece(lane, k);
-              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[h]));
-                x[8 * k + 2 * h] = fmaf(pr.beta, f.x, x[8 * k + 2 * h]);
-                x[8 * k + 2 * h + 1] = fmaf(pr.beta, f.y, x[8 * k + 2 * h + 1]);
-              }
-            }
-          }
-          if (pr.diag != 0.f && c0 < row0 + 32 && row0 < c0 + 32) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c0 + k == row0 + lane) x[k] += pr.diag;
-          }
-          uint32_t h[16];  // two columns each: fp16, or the result in bf16
-          if (pr.D) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) h[k] = two_half(x[2 * k], x[2 * k + 1]);
-          } else {
-            const float s = g.scale * kUnhold;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) h[k] = two_bf16(x[2 * k] * s, x[2 * k + 1] * s);
-          }
-          uint16_t* rows;
-          int64_t ldr;
-          bool whole = true;
-          if (pr.D) {
-            rows = reinterpret_cast<uint16_t*>(pr.D) + b * pr.strideD + static_cast<int64_t>(row0) * pr.ldD + c0;
-            ldr = pr.ldD;
-          } else {
-            rows = reinterpret_cast<uint16_t*>(g.out) + b * g.size + static_cast<int64_t>(row0) * pr.N + c0;
-            ldr = pr.N;
-            whole = g.out_vec && c0 + 32 <= pr.N;
-          }
-          if (!whole) {  // a ragged edge of the result, or one at an odd address
-            if (row0 + lane < pr.M)
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (c0 + k < pr.N) rows[lane * ldr + k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
-            __syncwarp();
-            continue;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) *piece(lane, k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (row0 + lr + 8 * k < pr.M)
-              *reinterpret_cast<uint4*>(rows + (lr + 8 * k) * ldr + lc * 8) = *piece(lr + 8 * k, lc);
-          __syncwarp();
-        }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t bar = smem_addr(&bars->acc_empty[acc]);
-          if constexpr (PAIR)
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
-          else
-            bar_arrive(bar);
-        }
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
-      }
+      bool fine;
+      if (prod % 3 == 0)
+        fine = epilogue<PAIR, kMakeA>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
+      else if (prod % 3 == 1)
+        fine = epilogue<PAIR, kMakeB>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
+      else if (pr.D)
+        fine = epilogue<PAIR, kMakeX>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
+      else
+        fine = epilogue<PAIR, kMakeOut>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
       if (!fine) {
         if (lane == 0) atomicOr(g.err_word, kErrOrtho);
         *abort = 1;
