@@ -13,9 +13,9 @@
 // Between the products X, A and Bm are held as fp16 scaled by 2^10 (pg.h): 11 significant
 // bits, against the 8 of the bf16 result.
 //
-// One cooperative launch does the whole update: norm, scaling, and 3 * steps products on the
-// tensor cores, the blocks meeting at a grid barrier between them. The held matrices stay in
-// L2 where they fit.
+// One cooperative launch does the whole update (large batches: norm and scaling before it): norm,
+// scaling, and 3 * steps products on the tensor cores, the blocks meeting at a grid barrier between
+// them. The held matrices stay in L2 where they fit.
 //   warp 0      TMA producer: 128-deep k-blocks of both operands, 128-byte swizzle, into a ring
 //   warp 1      tcgen05.mma issuer, two accumulators in TMEM
 //   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
@@ -81,6 +81,7 @@ struct OrthoArgs {
   int64_t size;              // m n
   int batch, m, n, p, ldx, ldp, parts, steps, dtype;
   int g_vec, out_vec;        // accesses of 8 columns to G; to out
+  int prepared;              // X0 is there already
   float a, b, c, eps, scale;
 };
 
@@ -299,8 +300,8 @@ struct Raw8 {
 
 // Partial sums of squares, of x, 2^64 x and 2^-64 x: whichever of the three neither overflows
 // nor vanishes gives the norm. Part `part` of matrix `b` is a contiguous share of it.
-template <int DT>
-__device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kThreads / 32]) {
+template <int DT, int THREADS>
+__device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[THREADS / 32]) {
   const int64_t share = ((g.size + g.parts - 1) / g.parts + 7) / 8 * 8;
   const int64_t lo = part * share, hi = min(g.size, lo + share), base = b * g.size;
   float sum[3] = {};
@@ -311,14 +312,14 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kT
     sum[2] = fmaf(down, down, sum[2]);
   };
   if (g.g_vec) {
-    constexpr int kFly = DT == PG_F32 ? 8 : 16;  // loads in flight
-    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kFly * kThreads * 8) {
+    constexpr int kFly = (DT == PG_F32 ? 8 : 16) * kThreads / THREADS;  // loads in flight
+    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kFly * THREADS * 8) {
       Raw8<DT> raw[kFly];
 #pragma unroll
-      for (int u = 0; u < kFly; ++u) raw[u].load(g.G, base + min(i + u * kThreads * 8, hi - 8));
+      for (int u = 0; u < kFly; ++u) raw[u].load(g.G, base + min(i + u * THREADS * 8, hi - 8));
 #pragma unroll
       for (int u = 0; u < kFly; ++u) {
-        if (i + u * kThreads * 8 >= hi) break;
+        if (i + u * THREADS * 8 >= hi) break;
         float x[8];
         raw[u].get(x);
 #pragma unroll
@@ -326,7 +327,7 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kT
       }
     }
   } else {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += THREADS) {
       float x[1];
       load_cols<DT, 1>(g.G, base + i, x);
       add(x[0]);
@@ -342,7 +343,7 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[kT
   __syncthreads();
   if (threadIdx.x < 3) {
     float t = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) t += s_sum[threadIdx.x][w];
+    for (int w = 0; w < THREADS / 32; ++w) t += s_sum[threadIdx.x][w];
     g.partial[(static_cast<int64_t>(b) * g.parts + part) * 3 + threadIdx.x] = t;
   }
 }
@@ -375,7 +376,7 @@ __device__ __forceinline__ uint32_t two_half(float lo, float hi) {
 
 // X0: rows of G scaled and rounded into rows of stride ldx, 8 columns at a time. A block owns a
 // contiguous share of the rows of all matrices.
-template <int DT>
+template <int DT, int THREADS>
 __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
   const uint32_t per_row = (g.n + 7) / 8;
   const int64_t rows = static_cast<int64_t>(g.batch) * g.m;
@@ -398,22 +399,22 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
                      two_half(x[4] * scale, x[5] * scale), two_half(x[6] * scale, x[7] * scale));
     };
     if (g.g_vec) {  // n % 8 == 0: a row's pieces follow the row before's
-      constexpr int kFly = DT == PG_F32 ? 8 : 16;
-      for (uint32_t v0 = threadIdx.x; v0 < vecs; v0 += kFly * kThreads) {
+      constexpr int kFly = (DT == PG_F32 ? 8 : 16) * kThreads / THREADS;
+      for (uint32_t v0 = threadIdx.x; v0 < vecs; v0 += kFly * THREADS) {
         Raw8<DT> raw[kFly];
 #pragma unroll
         for (int u = 0; u < kFly; ++u)
-          raw[u].load(g.G, r0 * g.n + 8ll * min(v0 + u * kThreads, vecs - 1));
+          raw[u].load(g.G, r0 * g.n + 8ll * min(v0 + u * THREADS, vecs - 1));
 #pragma unroll
         for (int u = 0; u < kFly; ++u) {
-          if (v0 + u * kThreads >= vecs) break;
+          if (v0 + u * THREADS >= vecs) break;
           float x[8];
           raw[u].get(x);
-          store(v0 + u * kThreads, x);
+          store(v0 + u * THREADS, x);
         }
       }
     } else {
-      for (uint32_t v = threadIdx.x; v < vecs; v += kThreads) {
+      for (uint32_t v = threadIdx.x; v < vecs; v += THREADS) {
         const uint32_t r = v / per_row, j = (v - r * per_row) * 8;
         float x[8];
 #pragma unroll
@@ -427,6 +428,21 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
     }
     r0 = r1;
   }
+}
+
+// The two as launches of their own, for large batches (see pg_orthogonalize).
+constexpr int kPrepThreads = 640;
+
+template <int DT>
+__global__ void __launch_bounds__(kPrepThreads, 2) ortho_norm_kernel(const __grid_constant__ OrthoArgs g) {
+  __shared__ float s_sum[3][kPrepThreads / 32];
+  norm_part<DT, kPrepThreads>(g, blockIdx.x / g.parts, blockIdx.x % g.parts, s_sum);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kPrepThreads, 2) ortho_scale_kernel(const __grid_constant__ OrthoArgs g) {
+  __shared__ float s_scale;
+  scale_rows<DT, kPrepThreads>(g, &s_scale);
 }
 
 // --------------------------------------------------------------------------- the products
@@ -727,13 +743,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- |G|_F and X0
   uint32_t phase = 0;
-  const bool f32 = g.dtype == PG_F32;
-  for (int w = blockIdx.x; w < g.batch * g.parts; w += gridDim.x)
-    f32 ? norm_part<PG_F32>(g, w / g.parts, w % g.parts, s_sum) : norm_part<PG_BF16>(g, w / g.parts, w % g.parts, s_sum);
-  bool ok = grid_meet(g, bars, &phase);
-  if (ok) {
-    f32 ? scale_rows<PG_F32>(g, &s_scale) : scale_rows<PG_BF16>(g, &s_scale);
+  bool ok = true;
+  if (!g.prepared) {
+    const bool f32 = g.dtype == PG_F32;
+    for (int w = blockIdx.x; w < g.batch * g.parts; w += gridDim.x)
+      f32 ? norm_part<PG_F32, kThreads>(g, w / g.parts, w % g.parts, s_sum)
+          : norm_part<PG_BF16, kThreads>(g, w / g.parts, w % g.parts, s_sum);
     ok = grid_meet(g, bars, &phase);
+    if (ok) {
+      f32 ? scale_rows<PG_F32, kThreads>(g, &s_scale) : scale_rows<PG_BF16, kThreads>(g, &s_scale);
+      ok = grid_meet(g, bars, &phase);
+    }
   }
 
   // ---- the products; each role carries its place in the ring and the accumulators along
@@ -900,6 +920,10 @@ bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, 
 }
 
 constexpr int kMaxDevices = 64;
+// From this many values on, norm and scaling are launches of their own, with more threads an SM
+// than the products leave them: 5 x 2560 x 1280 366 -> 350 us, 1280 x 2560 213 / 213, and below the
+// two launches cost more than they save (768 x 1024 113 -> 117).
+constexpr int64_t kPrepareFrom = 4 << 20;
 
 // Units (CTAs, or CTA pairs) of the kernel that are resident at once on the current device.
 template <bool PAIR>
@@ -957,10 +981,18 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   const int64_t reads = (static_cast<int64_t>(g.batch) * g.size + piece - 1) / piece;
   units = static_cast<int>(std::min<int64_t>(units, std::max(tiles, PAIR ? (reads + 1) / 2 : reads)));
   // one round of partial sums over the blocks
-  const int blocks = (PAIR ? 2 : 1) * units;
+  g.prepared = static_cast<int64_t>(g.batch) * g.size >= kPrepareFrom;
+  const int blocks = g.prepared ? 2 * sm_count() : (PAIR ? 2 : 1) * units;
   g.parts = static_cast<int>(std::min<int64_t>({kNormParts, std::max(1, blocks / g.batch), (g.size + piece - 1) / piece}));
   cudaError_t e = cudaMemsetAsync(g.ctrl, 0, sizeof(OrthoCtrl), stream);
   if (e != cudaSuccess) return cuda_fail(e);
+  if (g.prepared) {
+    const bool f32 = g.dtype == PG_F32;
+    (f32 ? ortho_norm_kernel<PG_F32> : ortho_norm_kernel<PG_BF16>)<<<g.batch * g.parts, kPrepThreads, 0, stream>>>(g);
+    if ((st = after_launch(1)) != PG_OK) return st;
+    (f32 ? ortho_scale_kernel<PG_F32> : ortho_scale_kernel<PG_BF16>)<<<blocks, kPrepThreads, 0, stream>>>(g);
+    if ((st = after_launch(1)) != PG_OK) return st;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
@@ -979,20 +1011,22 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   return after_launch(1);
 }
 
-// Whether 256 x 256 pair tiles finish sooner than 128 x 64 tiles: k-blocks walked one after
-// another by the busiest unit, times the cycles of one (a pair's 512 are its MMAs; a single
-// CTA's ~400 its 24 KB from L2), over a step's three products.
+// Whether 256 x 256 pair tiles finish sooner than 128 x 64 tiles: the k-blocks that the busiest
+// unit walks in a step at 0.62 us each (a pair's MMAs) against 0.53 us (a single CTA's 48 KB from
+// L2), and 6.4 us a step more for a pair's pipeline to fill and empty three times. Measured over 5
+// steps, pair and single, in us: 768 x 1024 154 / 114, 4 of them 161 / 189; 1280 x 2560 217 / 221;
+// 1280 x 1280 185 / 167.
 bool use_pairs(const OrthoArgs& g, int sms) {
   const int q = std::max(g.m, g.n);
-  auto cost = [&](bool pair, int M, int N, int K, bool sym) {
+  auto blocks = [&](bool pair, int M, int N, int K, bool sym) {
     const int64_t per = pair ? tiles_of<true>(M, N, sym) : tiles_of<false>(M, N, sym);
     const int64_t units = pair ? sms / 2 : sms;
-    return (per * g.batch + units - 1) / units * ((K + kBK - 1) / kBK) * (pair ? 512 : 400);
+    return (per * g.batch + units - 1) / units * ((K + kBK - 1) / kBK);
   };
   auto step = [&](bool pair) {
-    return cost(pair, g.p, g.p, q, true) + cost(pair, g.p, g.p, g.p, true) + cost(pair, g.m, g.n, g.p, false);
+    return blocks(pair, g.p, g.p, q, true) + blocks(pair, g.p, g.p, g.p, true) + blocks(pair, g.m, g.n, g.p, false);
   };
-  return step(true) < step(false);
+  return 62 * step(true) + 640 < 53 * step(false);
 }
 
 }  // namespace
