@@ -27,14 +27,19 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 8;                          // references a thread holds per tile
 constexpr int kSortTile = kSortThreads * kSortItems;   // 8192
+// Digits of 6 to 9 bits, where many blocks share a group, and of up to 11 in groups of few blocks:
+// every block adds up its group's counts itself. (11 bits everywhere, with a shared scan of the
+// counts and a second grid barrier a pass, sorted a million references no sooner in two passes
+// than 7 bits do in three: 73 us each.)
+constexpr int kMinDigitBits = 6;
+constexpr int kManyBits = 9;
 constexpr int kMaxDigitBits = 11;
+constexpr uint32_t kFewBlocks = 16;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
-constexpr int kDigitsPerThread = 2;                    // digits 2 tid and 2 tid + 1
 constexpr int kMaxSortBlocks = 152;                    // one per SM
-constexpr int kScanIters = (kMaxSortBlocks + 31) / 32;
 constexpr uint32_t kRefsPerBlock = 2048;               // at least, before another block joins
-constexpr uint32_t kDirectBlocks = 16;                 // up to here every block adds up all the counts itself
 constexpr uint64_t kFillPerBlock = 256 << 10;          // bytes of zeros, before another block joins
+constexpr int kIdBytes = 4 * (kSortTile + 8);          // a tile's canonical IDs, at one head a token
 constexpr int kHashItems = 32;                         // (order, head) items of a table
 
 struct SortCtrl {
@@ -64,7 +69,6 @@ struct RefSource {
 struct SortBuffers {
   SortCtrl* ctrl;
   uint32_t* hist;      // [blocks][digits]
-  uint32_t* totals;    // [groups][digits]
   uint32_t* segs;      // [blocks] segments that start in a block's share
   uint2* pair[2];      // [n] (row, reference)
   uint64_t* sign;      // [n][words] sign words of the references (hashed lookup)
@@ -96,7 +100,6 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
   const size_t un = static_cast<size_t>(n);
   b->ctrl = reinterpret_cast<SortCtrl*>(take(kCtrlBytes));
   b->hist = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits * kMaxSortBlocks));
-  b->totals = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxDigits * (hashed ? kHashItems : 1)));
   b->segs = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * kMaxSortBlocks));
   for (int i = 0; i < 2; ++i) b->pair[i] = reinterpret_cast<uint2*>(take(8 * un));
   b->sign = hashed ? reinterpret_cast<uint64_t*>(take(8 * un * sign_words(r))) : nullptr;
@@ -167,7 +170,6 @@ __device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t* s_warp
   *total = s_warp[kSortWarps];
   return s_warp[w] + inc - v;
 }
-static_assert(kDigitsPerThread * kSortThreads == kMaxDigits, "");
 static_assert(kSortWarps == 32, "block_excl_scan: one lane a warp");
 
 // What a block keeps of a tile of references between counting and scattering. A warp holds
@@ -182,31 +184,32 @@ __device__ __forceinline__ int tile_items(uint32_t left) {
 }
 
 // Ranks a tile's references by the digit of `key`, stably, with per-warp counts in s_cnt
-// [warps][digits], which become exclusive offsets over the warps; totals[q] gets the tile's
-// count of digit 2 tid + q. Equal digits of a warp find one another by one ballot a bit (the
-// match instruction takes a turn per distinct value: 9.2 against 7.8 us on the first pass of a
-// million references).
-__device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end, int items, int shift, int bits,
-                                          uint16_t* s_cnt, uint32_t (&totals)[kDigitsPerThread]) {
+// [warps][digits], which become exclusive offsets over the warps; *total gets, in the first
+// digits / 2 threads, the tile's counts of digits 2 tid (low half) and 2 tid + 1. Equal digits of a
+// warp find one another by one ballot a bit (the match instruction takes a turn per distinct value).
+template <int BITS>
+__device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end, int items, int shift, uint16_t* s_cnt,
+                                          uint32_t* s_part, uint32_t* total) {
+  constexpr int kDigits = 1 << BITS, kPairs = kDigits / 2;
+  constexpr int kParts = kSortThreads / kPairs < kSortWarps ? kSortThreads / kPairs : kSortWarps;
+  constexpr int kWarpsPerPart = kSortWarps / kParts;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int digits = 1 << bits;
-  const uint32_t mask = static_cast<uint32_t>(digits - 1);
   __syncthreads();  // whoever used s_cnt is done
-  uint32_t* clear = reinterpret_cast<uint32_t*>(s_cnt);
-  for (int w = tid; w < kSortWarps * digits / 2; w += kSortThreads) clear[w] = 0;
+  uint4* clear = reinterpret_cast<uint4*>(s_cnt);
+  for (int w = tid; w < kSortWarps * kDigits / 8; w += kSortThreads) clear[w] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  uint16_t* cnt = s_cnt + warp * digits;
+  uint16_t* cnt = s_cnt + warp * kDigits;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
     if (j >= items) break;
     const bool in = first + j * 32 + lane < end;
-    const uint32_t dig = (h.key[j] >> shift) & mask;
+    const uint32_t dig = (h.key[j] >> shift) & (kDigits - 1);
     uint32_t peers = __ballot_sync(0xffffffffu, in);
 #pragma unroll
-    for (int q = 0; q < kMaxDigitBits; ++q) {
-      if (q >= bits) break;
-      const uint32_t set = __ballot_sync(0xffffffffu, dig & (1u << q));
-      peers &= ~(set ^ static_cast<uint32_t>(static_cast<int32_t>(dig << (31 - q)) >> 31));
+    for (int q = 0; q < BITS; ++q) {
+      const bool bit = dig & (1u << q);
+      const uint32_t set = __ballot_sync(0xffffffffu, bit);
+      peers &= bit ? set : ~set;
     }
     const uint32_t before = in ? cnt[dig] : 0u;
     h.rank[j] = before + __popc(peers & ((1u << lane) - 1u));
@@ -215,19 +218,33 @@ __device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end,
     __syncwarp();
   }
   __syncthreads();
-  // two digits a thread: their 16-bit counts (at most 8192 in all) ride in one word
-  uint32_t run = 0;
-  if (2 * tid < digits) {
-    uint32_t* word = reinterpret_cast<uint32_t*>(s_cnt) + tid;
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = word[w * digits / 2];
-      word[w * digits / 2] = run;
+  // Counts to offsets, two digits a word (at most 8192 in all, so the halves do not meet): thread
+  // (part, pair) adds up its warps' words, then the parts before it, and walks its warps again.
+  const int pair = tid % kPairs, part = tid / kPairs;
+  uint32_t* word = reinterpret_cast<uint32_t*>(s_cnt) + pair;
+  if (part < kParts) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarpsPerPart; ++w) sum += word[(part * kWarpsPerPart + w) * kPairs];
+    s_part[part * kPairs + pair] = sum;
+  }
+  __syncthreads();
+  uint32_t run = 0, all = 0;
+  if (part < kParts) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const uint32_t c = s_part[k * kPairs + pair];
+      if (k < part) run += c;
+      all += c;
+    }
+#pragma unroll
+    for (int w = 0; w < kWarpsPerPart; ++w) {
+      const uint32_t c = word[(part * kWarpsPerPart + w) * kPairs];
+      word[(part * kWarpsPerPart + w) * kPairs] = run;
       run += c;
     }
   }
-  totals[0] = run & 0xFFFFu;
-  totals[1] = run >> 16;
+  *total = all;  // (threads of part 0)
 }
 
 // The hashed lookup's references are numbered group by group: the rows of a group (one subtable,
@@ -247,16 +264,28 @@ __device__ __forceinline__ void stage_ids(const RefSource& src, uint32_t tok0, u
 
 // Row and sign hash of the reference `local` places after head 0 of token tok0 (local < 8192 +
 // 32); *ref = its number by tokens (t * items + item), the row of its gradient.
+template <bool PAGED>
 __device__ __forceinline__ uint32_t hashed_key(const RefSource& src, const ItemConst* s_ic, const uint32_t* s_id,
                                                uint32_t item0, uint32_t tok0, uint32_t local, uint32_t* ref, uint64_t* hs) {
   const uint32_t s = __umulhi(local, src.per) + (src.heads == 1 ? local : 0u);
   const uint32_t item = item0 + local - s * src.heads;
   const uint32_t t = fastmod(tok0 + s, src.fm_L, src.L);
-  uint64_t c[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = t >= static_cast<uint32_t>(j) ? s_id[s + 3 - j] : kPad;
   *ref = (tok0 + s) * src.items + item;
-  return item_row_ids(s_ic[item], src.mode, c, hs);
+  const ItemConst& it = s_ic[item];
+  // (item_row_ids without the page hash where there are no pages: a quarter of its multiplications)
+  uint64_t hp = 0, hh = 0, h2 = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= it.n) break;
+    const uint64_t c = t >= static_cast<uint32_t>(j) ? s_id[s + 3 - j] : kPad;
+    if (PAGED) hp ^= c * it.mp[j];
+    hh ^= c * it.mh[j];
+    h2 ^= c * it.ms[j];
+  }
+  *hs = h2;
+  if (PAGED)
+    return it.base + fastmod(fold32(hp), it.fm_main, it.div_main) * it.stride + fastmod(fold32(hh), it.fm_slot, it.slots);
+  return it.base + fastmod(fold32(hh), it.fm_main, it.div_main);
 }
 
 // The sign words of reference `ref` (an even number of them beyond one: 16 bytes at a time).
@@ -300,15 +329,16 @@ __device__ __forceinline__ void fill_zeros(uint8_t* p, uint64_t bytes, uint32_t 
 // `share` consecutive ones. Blocks past them, or the same ones afterwards where the grid has no
 // others, zero the embedding's gradient (`fill`): writing all of it here, under a sort that uses
 // few SMs and no bandwidth, is cheaper than knowing which rows will be written.
-template <bool HASHED>
+template <bool HASHED, int BITS>
 __global__ void __launch_bounds__(kSortThreads, 1)
     rowgrad_sort_kernel(const __grid_constant__ RefSource src, const __grid_constant__ SortBuffers b, uint32_t n,
-                        uint32_t size, uint32_t per_group, uint32_t share, int passes, int bits, uint32_t* __restrict__ rows_out,
+                        uint32_t size, uint32_t per_group, uint32_t share, int passes, uint32_t* __restrict__ rows_out,
                         int32_t* __restrict__ count_out, uint32_t G, uint8_t* fill, uint64_t fill_bytes,
                         int* err_word) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);                                 // [warps][digits]
-  uint32_t* s_base = reinterpret_cast<uint32_t*>(s_raw + kSortWarps * kMaxDigits * 2);  // [digits]
+  constexpr int kDigits = 1 << BITS, kPairs = kDigits / 2;
+  __shared__ uint32_t s_base[kDigits], s_part[kSortThreads];
   __shared__ uint32_t s_warp[kSortWarps + 1];
   __shared__ uint32_t s_first;
   __shared__ int s_ok;
@@ -317,7 +347,6 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t group = blockIdx.x / per_group, part = blockIdx.x - group * per_group, start = group * size;
   const uint32_t lo = start + min(size, part * share), hi = start + min(size, (part + 1) * share);
-  const int digits = 1 << bits;
   const bool one = share <= kSortTile;  // the share stays in registers between counting and scattering
   uint32_t phase = 0, row0 = 0;
 
@@ -338,11 +367,9 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 
   uint2 *in_order = b.pair[0], *out_order = b.pair[1];
   for (int p = 0; p < passes; ++p) {
-    const int shift = p * bits;
+    const int shift = p * BITS;
     Held h;
-    uint32_t mine[kDigitsPerThread];  // this share's counts of digits 2 tid + q
-#pragma unroll
-    for (int q = 0; q < kDigitsPerThread; ++q) mine[q] = 0;
+    uint2 mine = make_uint2(0u, 0u);  // this share's counts of digits 2 tid and 2 tid + 1 (tid < kPairs)
     // ---- ranks and counts. A share of several tiles is read again for the scatter.
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
       const int items = tile_items(hi - t0);
@@ -365,8 +392,10 @@ __global__ void __launch_bounds__(kSortThreads, 1)
           } else {
             if constexpr (HASHED) {
               uint64_t hs;
-              v.x = hashed_key(src, s_ic, reinterpret_cast<const uint32_t*>(s_cnt), group * src.heads, tok0,
-                               i - t0 + head0, &v.y, &hs);
+              const uint32_t* ids = reinterpret_cast<const uint32_t*>(s_cnt);
+              v.x = src.mode == PG_PAGEGRAM
+                        ? hashed_key<true>(src, s_ic, ids, group * src.heads, tok0, i - t0 + head0, &v.y, &hs)
+                        : hashed_key<false>(src, s_ic, ids, group * src.heads, tok0, i - t0 + head0, &v.y, &hs);
               store_signs(b.sign, v.y, src.words, hs);
             } else {
               v.x = embed_key(src, i);
@@ -377,83 +406,61 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         h.key[j] = v.x;
         h.ref[j] = v.y;
       }
-      uint32_t totals[kDigitsPerThread];
-      rank_tile(h, first, end, items, shift, bits, s_cnt, totals);
-#pragma unroll
-      for (int q = 0; q < kDigitsPerThread; ++q) mine[q] += totals[q];
+      uint32_t total;
+      rank_tile<BITS>(h, first, end, items, shift, s_cnt, s_part, &total);
+      if (tid < kPairs) {
+        mine.x += total & 0xFFFFu;
+        mine.y += total >> 16;
+      }
     }
 
     // ---- where this block's first reference of each digit goes: the digits before it, and the
     // same digit in the blocks before it
-    uint32_t below[kDigitsPerThread], total_of[kDigitsPerThread];
-    if (G == 1) {
-#pragma unroll
-      for (int q = 0; q < kDigitsPerThread; ++q) {
-        below[q] = 0;
-        total_of[q] = mine[q];
-      }
-    } else {
-      const bool has = 2 * tid < digits;
-      if (has) *reinterpret_cast<uint2*>(b.hist + blockIdx.x * digits + 2 * tid) = make_uint2(mine[0], mine[1]);
+    uint2 below = make_uint2(0u, 0u), total_of = mine;
+    if (G > 1) {
+      if (tid < kPairs) *reinterpret_cast<uint2*>(b.hist + blockIdx.x * kDigits + 2 * tid) = mine;
       if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-      if (per_group <= kDirectBlocks) {  // every block adds up its group's counts itself
-        below[0] = below[1] = total_of[0] = total_of[1] = 0;
-        if (has) {
-          const uint32_t* counts = b.hist + group * per_group * digits + 2 * tid;
+      // the group's counts, kSortThreads / kPairs blocks at a time
+      constexpr int kAtOnce = kSortThreads / kPairs;
+      const uint2* counts = reinterpret_cast<const uint2*>(b.hist + group * per_group * kDigits) + tid % kPairs;
+      total_of = make_uint2(0u, 0u);
 #pragma unroll 8
-          for (uint32_t k = 0; k < per_group; ++k) {
-            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(counts + k * digits));
-            below[0] += k < part ? v.x : 0u;
-            below[1] += k < part ? v.y : 0u;
-            total_of[0] += v.x;
-            total_of[1] += v.y;
-          }
-        }
-      } else {  // a warp scans two digits' counts over a group's blocks
-        const uint32_t pairs = digits / 2, groups = G / per_group;
-        for (uint32_t w = warp * G + blockIdx.x; w < groups * pairs; w += G * kSortWarps) {
-          const uint32_t of = w / pairs, d = 2 * (w - of * pairs);
-          uint32_t* counts = b.hist + of * per_group * digits + d;
-          uint2 v[kScanIters];
-          uint32_t run0 = 0, run1 = 0;
-#pragma unroll
-          for (int k = 0; k < kScanIters; ++k)
-            v[k] = k * 32 + lane < per_group ? __ldcg(reinterpret_cast<const uint2*>(counts + (k * 32 + lane) * digits))
-                                             : make_uint2(0u, 0u);
-#pragma unroll
-          for (int k = 0; k < kScanIters; ++k) {
-            const uint32_t i0 = warp_incl_scan(v[k].x, lane), i1 = warp_incl_scan(v[k].y, lane);
-            if (k * 32 + lane < per_group)
-              *reinterpret_cast<uint2*>(counts + (k * 32 + lane) * digits) = make_uint2(run0 + i0 - v[k].x, run1 + i1 - v[k].y);
-            run0 += __shfl_sync(0xffffffffu, i0, 31);
-            run1 += __shfl_sync(0xffffffffu, i1, 31);
-          }
-          if (lane == 0) *reinterpret_cast<uint2*>(b.totals + of * digits + d) = make_uint2(run0, run1);
-        }
-        if (!grid_barrier(G, &b.ctrl->barrier, &phase, &s_ok, err_word)) return;
-        const uint2 x = has ? __ldcg(reinterpret_cast<const uint2*>(b.hist + blockIdx.x * digits + 2 * tid)) : make_uint2(0u, 0u);
-        const uint2 y = has ? __ldcg(reinterpret_cast<const uint2*>(b.totals + group * digits + 2 * tid)) : make_uint2(0u, 0u);
-        below[0] = x.x;
-        below[1] = x.y;
-        total_of[0] = y.x;
-        total_of[1] = y.y;
+      for (uint32_t k = tid / kPairs; k < per_group; k += kAtOnce) {
+        const uint2 v = __ldcg(counts + k * kPairs);
+        below.x += k < part ? v.x : 0u;
+        below.y += k < part ? v.y : 0u;
+        total_of.x += v.x;
+        total_of.y += v.y;
       }
+      // join the kAtOnce partial sums, through the room of the counts that the scatter does not need
+#pragma unroll
+      for (int step = 0; step < 4; ++step) {
+        uint32_t& mine_of = step == 0 ? below.x : step == 1 ? below.y : step == 2 ? total_of.x : total_of.y;
+        s_part[tid] = mine_of;
+        __syncthreads();
+        if (tid < kPairs) {
+          uint32_t sum = 0;
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) sum += s_part[k * kPairs + tid];
+          mine_of = sum;
+        }
+        __syncthreads();
+      }
+      if (tid >= kPairs) below = total_of = make_uint2(0u, 0u);
     }
     uint32_t all;
-    uint32_t ex = block_excl_scan(total_of[0] + total_of[1], s_warp, &all);
-#pragma unroll
-    for (int q = 0; q < kDigitsPerThread; ++q) {
-      if (2 * tid + q < digits) s_base[2 * tid + q] = start + ex + below[q];
-      ex += total_of[q];
+    const uint32_t ex = block_excl_scan(total_of.x + total_of.y, s_warp, &all);
+    if (tid < kPairs) {
+      s_base[2 * tid] = start + ex + below.x;
+      s_base[2 * tid + 1] = start + ex + total_of.x + below.y;
     }
     __syncthreads();
 
     // ---- scatter
-    const uint32_t mask = static_cast<uint32_t>(digits - 1);
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
       const int items = tile_items(hi - t0);
       const uint32_t first = t0 + warp * 32 * items, end = min(hi, t0 + kSortTile);
-      uint32_t totals[kDigitsPerThread];
+      uint32_t total = 0;
       if (!one) {
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
@@ -462,23 +469,22 @@ __global__ void __launch_bounds__(kSortThreads, 1)
           h.key[j] = v.x;
           h.ref[j] = v.y;
         }
-        rank_tile(h, first, end, items, shift, bits, s_cnt, totals);
+        rank_tile<BITS>(h, first, end, items, shift, s_cnt, s_part, &total);
         __syncthreads();
       }
 #pragma unroll
       for (int j = 0; j < kSortItems; ++j) {
         if (j < items && first + j * 32 + lane < end) {
-          const uint32_t dig = (h.key[j] >> shift) & mask;
-          const uint32_t to = s_base[dig] + s_cnt[warp * digits + dig] + h.rank[j];
+          const uint32_t dig = (h.key[j] >> shift) & (kDigits - 1);
+          const uint32_t to = s_base[dig] + s_cnt[warp * kDigits + dig] + h.rank[j];
           out_order[to] = make_uint2(h.key[j], h.ref[j]);
         }
       }
       if (!one) {
         __syncthreads();
-#pragma unroll
-        for (int q = 0; q < kDigitsPerThread; ++q) {
-          const int d = 2 * tid + q;
-          if (d < digits) s_base[d] += totals[q];
+        if (tid < kPairs) {
+          s_base[2 * tid] += total & 0xFFFFu;
+          s_base[2 * tid + 1] += total >> 16;
         }
       }
     }
@@ -821,13 +827,14 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
   carve(static_cast<uint8_t*>(workspace), n, a.r, HASHED, &b);
   int key_bits = 1;
   while (key_bits < 32 && (keys >> key_bits)) ++key_bits;
-  const int passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
-  const int bits = (key_bits + passes - 1) / passes;
   const uint32_t sms = static_cast<uint32_t>(min(sm_count(), kMaxSortBlocks)), size = n / groups;
   uint32_t per_group = max(1u, min((size + kRefsPerBlock - 1) / kRefsPerBlock, sms / groups));
   const uint32_t share = (size + per_group - 1) / per_group;
   per_group = (size + share - 1) / share;
   const uint32_t G = groups * per_group;
+  const int most = per_group <= kFewBlocks ? kMaxDigitBits : kManyBits;
+  const int passes = (key_bits + most - 1) / most;
+  const int bits = max((key_bits + passes - 1) / passes, kMinDigitBits);
 
   const uint64_t fill_bytes = HASHED || a.accumulate ? 0 : static_cast<uint64_t>(src.rows) * a.r * dtype_bytes(out);
   const uint64_t fill_blocks = (fill_bytes + kFillPerBlock - 1) / kFillPerBlock;
@@ -837,8 +844,13 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
   cudaError_t e = cudaSuccess;
   if (G > 1) e = cudaMemsetAsync(b.ctrl, 0, kCtrlBytes, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  auto sort = rowgrad_sort_kernel<HASHED>;
-  const int smem = kSortWarps * kMaxDigits * 2 + kMaxDigits * 4;
+  auto sort = bits == 6    ? rowgrad_sort_kernel<HASHED, 6>
+              : bits == 7  ? rowgrad_sort_kernel<HASHED, 7>
+              : bits == 8  ? rowgrad_sort_kernel<HASHED, 8>
+              : bits == 9  ? rowgrad_sort_kernel<HASHED, 9>
+              : bits == 10 ? rowgrad_sort_kernel<HASHED, 10>
+                           : rowgrad_sort_kernel<HASHED, 11>;
+  const int smem = max(kSortWarps * (2 << bits), HASHED ? kIdBytes : 0);  // the counts; before them, the canonical IDs
   e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
@@ -851,7 +863,7 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = G > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, size, per_group, share, passes, bits, rows_out, count_out, G,
+  e = cudaLaunchKernelEx(&cfg, sort, src, b, n, size, per_group, share, passes, rows_out, count_out, G,
                          static_cast<uint8_t*>(a.out), fill_bytes, device_error_word());
   if (e != cudaSuccess) return cuda_fail(e);
   pg_status st = after_launch(1);
