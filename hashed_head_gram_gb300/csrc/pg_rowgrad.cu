@@ -252,14 +252,32 @@ __device__ __forceinline__ void rank_tile(Held& h, uint32_t first, uint32_t end,
 // that count from its first: fewer digits, and counts of fewer blocks to add up. Reference j of
 // a group is head j mod `heads` of token j / heads.
 
-// Canonical IDs of the tokens that a group's references [t0, end) and their n-grams read, into
-// s_id (token tok0 - 3 first, tok0 that of t0): one read of the token and of the map for all of
-// its heads.
+// Canonical IDs of the tokens that a group's references [.., end) and their n-grams read, tok0 the
+// tile's first token; four reads of the token and then of the map in flight a thread.
 __device__ __forceinline__ void stage_ids(const RefSource& src, uint32_t tok0, uint32_t end, uint32_t* s_id) {
+  constexpr int kFly = 4;
   const int64_t first = static_cast<int64_t>(tok0) - 3;
   const int count = static_cast<int>((end - 1) / src.heads - first) + 1;
-  for (int k = threadIdx.x; k < count; k += kSortThreads)
-    s_id[k] = first + k >= 0 ? canon_token(src.tokens, src.canon_map, src.vocab, first + k, src.err) : 0u;
+  for (int k0 = threadIdx.x; k0 < count; k0 += kFly * kSortThreads) {
+    int32_t x[kFly];
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      const int64_t at = first + k0 + f * kSortThreads;
+      x[f] = k0 + f * kSortThreads < count && at >= 0 ? __ldg(src.tokens + at) : 0;
+    }
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      const int64_t at = first + k0 + f * kSortThreads;
+      if (x[f] < 0 || static_cast<uint32_t>(x[f]) >= src.vocab) {  // read as ID 0, and reported
+        if (src.err) atomicMin(reinterpret_cast<unsigned int*>(src.err), static_cast<unsigned int>(at));
+        x[f] = 0;
+      }
+      if (src.canon_map) x[f] = static_cast<int32_t>(__ldg(src.canon_map + x[f]));
+    }
+#pragma unroll
+    for (int f = 0; f < kFly; ++f)
+      if (k0 + f * kSortThreads < count) s_id[k0 + f * kSortThreads] = static_cast<uint32_t>(x[f]);
+  }
 }
 
 // Row and sign hash of the reference `local` places after head 0 of token tok0 (local < 8192 +
@@ -272,7 +290,7 @@ __device__ __forceinline__ uint32_t hashed_key(const RefSource& src, const ItemC
   const uint32_t t = fastmod(tok0 + s, src.fm_L, src.L);
   *ref = (tok0 + s) * src.items + item;
   const ItemConst& it = s_ic[item];
-  // (item_row_ids without the page hash where there are no pages: a quarter of its multiplications)
+  // (item_row_ids without the page hash where there are no pages: a third of its multiplications)
   uint64_t hp = 0, hh = 0, h2 = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -646,8 +664,8 @@ __global__ void __launch_bounds__(kSumThreads, 5)
   const int group = threadIdx.x / lanes;
   const uint32_t tile = blockIdx.x * per_block + group;
   const int c = (blockIdx.y * lanes + threadIdx.x - group * lanes) * COLS;
-  grid_dep_launch();
   grid_dep_wait();
+  grid_dep_launch();  // after the wait: the join may read what the sort wrote as soon as it runs
   if (group >= per_block || tile >= a.tiles || c >= a.r || a.ctrl->done != a.blocks) return;
   const uint32_t p0 = tile * T, p1 = min(p0 + T, a.n);
   constexpr int kFly = IN == PG_F32 && COLS == 8 ? 4 : 8;
@@ -723,8 +741,10 @@ template <int OUT, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
   __shared__ float s_acc[kJoinThreads][COLS];
   __shared__ uint32_t s_long, s_end;
-  grid_dep_wait();
-  if (a.ctrl->done != a.blocks) return;
+  if (a.ctrl->done != a.blocks) {
+    grid_dep_wait();
+    return;
+  }
   const int per_block = kJoinThreads / lanes, group = threadIdx.x / lanes;
   const uint32_t tile = blockIdx.x * per_block + group;
   const int c = group < per_block ? (blockIdx.y * lanes + threadIdx.x - group * lanes) * COLS : a.r;
@@ -747,12 +767,14 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
         for (int j = 0; j < COLS; ++j) acc[j] += x[f][j];
     }
   };
+  uint32_t row = kNoRow, end = 0;  // the row that starts in this tile and goes on; past the last tile with a part
   if (group < per_block && tile < a.tiles && p1 < a.n) {
     const uint32_t u = __ldg(&a.order[p1].x), prev = __ldg(&a.order[p1 - 1].x);
     const uint32_t before = p0 > 0 ? __ldg(&a.order[p0 - 1].x) : kNoRow;
     const uint32_t next = p1 + T < a.n ? __ldg(&a.order[p1 + T].x) : kNoRow;
     if (u == prev && u != before && u != a.none) {
-      uint32_t end = tile + 2;  // past the last tile with a part
+      row = u;
+      end = tile + 2;
       if (next == u) {
         // The row goes on past the next tile: how many tiles start with it. Eight probes at a
         // time, the gap between them growing eightfold while all hold it and shrinking after.
@@ -776,15 +798,18 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
         }
         end = k + 1;
       }
-      if (end - tile > static_cast<uint32_t>(per_block)) {
-        s_long = tile;
-        s_end = end;
-      } else if (c < a.r) {
-        float acc[COLS];
-        load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(tile) * 2 * a.r + a.r + c, acc);
-        add(tile + 1, end, 1, acc);
-        write_row<OUT, COLS>(a, u, c, acc);
-      }
+    }
+  }
+  grid_dep_wait();  // the sums' parts
+  if (row != kNoRow) {
+    if (end - tile > static_cast<uint32_t>(per_block)) {
+      s_long = tile;
+      s_end = end;
+    } else if (c < a.r) {
+      float acc[COLS];
+      load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(tile) * 2 * a.r + a.r + c, acc);
+      add(tile + 1, end, 1, acc);
+      write_row<OUT, COLS>(a, row, c, acc);
     }
   }
   __syncthreads();

@@ -591,6 +591,13 @@ def _dtype(t: torch.Tensor) -> int:
     return _DTYPES[t.dtype]
 
 
+def _at(t: Optional[torch.Tensor]):
+    """_ptr as a plain integer (a small call's latency is mostly argument marshalling)."""
+    if t is None or not (t.is_cuda and t.is_contiguous()):
+        return _ptr(t)
+    return t.data_ptr()
+
+
 def _expect(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
@@ -612,8 +619,8 @@ def embed(tokens: torch.Tensor, table: torch.Tensor, out: torch.Tensor, vocab: i
     N = tokens.numel()
     _ids(tokens, canon_map, vocab, err_index)
     _expect(out.numel() == N * d and out.shape[-1] == d, "out must hold one row of table's width per token")
-    _check(_lib.pg_embed(_ptr(tokens), N, vocab, _ptr(canon_map), _ptr(table), _dtype(table), rows, d, scale, _ptr(out),
-                         _dtype(out), _ptr(err_index), _stream(stream)), "pg_embed")
+    _check(_lib.pg_embed(_at(tokens), N, vocab, _at(canon_map), _at(table), _dtype(table), rows, d, scale, _at(out),
+                         _dtype(out), _at(err_index), _stream(stream)), "pg_embed")
 
 
 def embed_grad_workspace_size(N: int, rows: int, d: int) -> int:
@@ -632,9 +639,9 @@ def embed_grad(tokens: torch.Tensor, grad_out: torch.Tensor, grad_table: torch.T
     _ids(tokens, canon_map, vocab, err_index)
     _expect(grad_out.numel() == N * d and grad_out.shape[-1] == d, "grad_out must hold one row of the table's width per token")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_embed_grad(_ptr(tokens), N, vocab, _ptr(canon_map), _ptr(grad_out), _dtype(grad_out), rows, d, scale,
-                              1 if accumulate else 0, _ptr(grad_table), _dtype(grad_table), _ptr(workspace), ws_bytes,
-                              _ptr(err_index), _stream(stream)), "pg_embed_grad")
+    _check(_lib.pg_embed_grad(_at(tokens), N, vocab, _at(canon_map), _at(grad_out), _dtype(grad_out), rows, d, scale,
+                              1 if accumulate else 0, _at(grad_table), _dtype(grad_table), _at(workspace), ws_bytes,
+                              _at(err_index), _stream(stream)), "pg_embed_grad")
 
 
 def lookup_grad_workspace_size(desc: TableDesc, N: int) -> int:
@@ -658,9 +665,9 @@ def lookup_grad(desc: TableDesc, tokens: torch.Tensor, grad_e: torch.Tensor, row
     _expect(grads_out.numel() == n * desc.r and grads_out.shape[-1] == desc.r, "grads_out must hold one row of width r per read")
     _expect(count_out.dtype == torch.int32 and count_out.numel() >= 1, "count_out must be an int32 tensor")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_lookup_grad(ctypes.byref(desc), _ptr(tokens), B, L, _ptr(canon_map), _ptr(grad_e), _dtype(grad_e),
-                               _ptr(rows_out), _ptr(grads_out), _dtype(grads_out), _ptr(count_out), _ptr(workspace),
-                               ws_bytes, _ptr(err_index), _stream(stream)), "pg_lookup_grad")
+    _check(_lib.pg_lookup_grad(ctypes.byref(desc), _at(tokens), B, L, _at(canon_map), _at(grad_e), _dtype(grad_e),
+                               _at(rows_out), _at(grads_out), _dtype(grads_out), _at(count_out), _at(workspace),
+                               ws_bytes, _at(err_index), _stream(stream)), "pg_lookup_grad")
 
 
 def orthogonalize_workspace_size(batch: int, m: int, n: int) -> int:
@@ -678,5 +685,5 @@ def orthogonalize(G: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, s
     m, n = G.shape[-2:]
     a, b, c = coeffs
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_orthogonalize(_ptr(G), _dtype(G), batch, m, n, steps, a, b, c, eps, scale, _ptr(out), _ptr(workspace),
+    _check(_lib.pg_orthogonalize(_at(G), _dtype(G), batch, m, n, steps, a, b, c, eps, scale, _at(out), _at(workspace),
                                  ws_bytes, _stream(stream)), "pg_orthogonalize")
