@@ -724,7 +724,7 @@ pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32
  * are stored scaled by 2^10 in fp16 between them (11 significant bits: three more than the
  * result's; the scale puts magnitudes 6e-8 .. 63 into fp16's normal range, where a norm of at
  * most 1 and the usual coefficients keep them below 3).
- * A zero matrix gives zeros; infinities and NaN in G make its own matrix NaN.
+ * A zero matrix gives zeros (eps > 0); infinities and NaN in G make its own matrix NaN.
  *  1 <= m, n <= 16384; 0 <= batch <= 4096; 1 <= steps <= 32; workspace device, 16-byte aligned,
  *  >= pg_orthogonalize_workspace_size bytes, scratch. batch == 0 enqueues nothing.
  */

@@ -79,7 +79,7 @@ def embed_rows(tokens, cmap, vocab, rows):
 @pytest.mark.parametrize("table_dtype", [F32, BF16])
 @pytest.mark.parametrize("out_dtype", [F32, BF16])
 @pytest.mark.parametrize("N,d,shift", [(1, 1, 0), (7, 33, 0), (300, 96, 0), (300, 96, 1), (300, 96, 4), (5, 2560, 0), (129, 1032, 0),
-                                       (64, 1025, 0)])
+                                       (64, 1025, 0), (40001, 24, 0), (39999, 13, 0)])
 def test_embed(cuda, table_dtype, out_dtype, N, d, shift):
     pg = _pg()
     gen = torch.Generator().manual_seed(N * 1000 + d)
@@ -292,6 +292,46 @@ def test_lookup_grad_many_reads_and_large_row_numbers(cuda):
     # rows past 2^31: the keys' top bit counts
     huge = dataclasses.replace(spec, K=2, rows=[[1_500_000_007, 1_000_000_007], [900_000_011, 800_000_011]])
     check_lookup_grad(cuda, huge, tokens[:2], 50000, None, F32, F32)
+
+
+@pytest.mark.parametrize("name", ["pagegram", "orders1-4", "flat-odd"])
+def test_lookup_grad_shares_of_several_tiles(cuda, name):
+    # more reads than the sort's blocks hold at once (152 * 8192)
+    spec = dataclasses.replace(SPECS[name](), r=8)
+    reads = len(spec.orders) * (1 if spec.mode == W.MODE_FLAT else spec.K)
+    L = 2_700_000 // reads // 3
+    rng = np.random.default_rng(17)
+    tokens = np.minimum(rng.zipf(1.2, (3, L)) - 1, 299).astype(np.int32)
+    check_lookup_grad(cuda, spec, tokens, 300, None, F32, F32)
+
+
+def test_embed_grad_shares_of_several_tiles(cuda):
+    check_embed_grad(cuda, 1_400_003, 8, 70_000, 60_000, "mixed", BF16, F32)
+    check_embed_grad(cuda, 1_300_000, 8, 300, 200, "skewed", F32, F32, accumulate=True, canon=False)
+
+
+def test_offsets_past_32_bits(cuda):
+    # tables of more than 2^32 elements: only the rows looked at are checked
+    pg = _pg()
+    rows, d = 70_000, 65_600
+    at = torch.tensor([0, 1, 65_472, 65_473, 69_999, 33_000, 69_999], dtype=torch.int32, device=cuda)
+    table = torch.empty(rows, d, dtype=BF16, device=cuda)
+    gen = torch.Generator(device=cuda).manual_seed(1)
+    vals = torch.randn(len(at), d, generator=gen, device=cuda).to(BF16)
+    table[at.long()] = vals
+    out = torch.empty(len(at), d, dtype=BF16, device=cuda)
+    pg.embed(at, table, out, rows, scale=2.0)
+    assert torch.equal(out, table[at.long()] * 2)
+    grad = torch.randn(len(at), d, generator=gen, device=cuda).to(BF16)
+    ws = torch.empty(pg.embed_grad_workspace_size(len(at), rows, d), dtype=torch.uint8, device=cuda)
+    pg.embed_grad(at, grad, table, rows, ws)
+    want = grad.clone()
+    want[4] = want[6] = (grad[4].float() + grad[6].float()).to(BF16)
+    assert torch.equal(table[at.long()], want)
+    rest = torch.ones(rows, dtype=torch.bool, device=cuda)
+    rest[at.long()] = False
+    for part in torch.nonzero(rest)[:, 0].split(8000):
+        assert not table[part].any()
 
 
 def test_lookup_grad_unaligned(cuda):
