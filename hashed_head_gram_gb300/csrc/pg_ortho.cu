@@ -14,13 +14,19 @@
 // bits, against the 8 of the bf16 result.
 //
 // One cooperative launch does the whole update (large batches: norm and scaling before it): norm,
-// scaling, and 3 * steps products on the tensor cores, the blocks meeting at a grid barrier between
-// them. The held matrices stay in L2 where they fit.
+// scaling, and 3 * steps products on the tensor cores. The tiles of all products stand in one list,
+// product by product and matrix by matrix; unit u takes tiles u, u + units, .. of it, and a tile's
+// loads wait until all tiles of the product before it of the same matrix are stored (a counter a
+// matrix). So no unit waits for matrices that it does not touch, and the last round of one product
+// is filled up with the next one's tiles. Every wait is for tiles earlier in the list, which every
+// unit walks in order: all waits end. The held matrices stay in L2 where they fit.
 //   warp 0      TMA producer: 128-deep k-blocks of both operands, 128-byte swizzle, into a ring
 //   warp 1      tcgen05.mma issuer, two accumulators in TMEM
 //   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
 #include <cuda.h>
 #include <cuda_fp16.h>
+
+#include <stddef.h>
 
 #include <algorithm>
 #include <atomic>
@@ -68,7 +74,8 @@ struct Tile {
 
 struct OrthoCtrl {
   uint32_t barrier;
-  uint32_t pad[63];
+  uint32_t pad[31];
+  uint32_t stored[kMaxBatch];  // per matrix: epilogue warps that have stored their part of a tile
 };
 
 struct OrthoArgs {
@@ -82,6 +89,7 @@ struct OrthoArgs {
   int batch, m, n, p, ldx, ldp, parts, steps, dtype;
   int g_vec, out_vec;        // accesses of 8 columns to G; to out
   int prepared;              // X0 is there already
+  int tiles[3];              // of one matrix, of each product
   float a, b, c, eps, scale;
 };
 
@@ -517,23 +525,55 @@ __host__ __device__ __forceinline__ int tiles_of(int M, int N, bool symmetric) {
   return symmetric ? nm * nn - kR * (nm * (nm - 1) / 2) : nm * nn;
 }
 
+// Tile t of the list of all products: its product, matrix and place, and how many of the matrix's
+// tiles have to be stored before.
+struct Work {
+  int step, kind, b, i, j, before;
+};
+
 template <bool PAIR>
-__device__ __forceinline__ void tile_at(const Product& g, int per, int t, int* b, int* i, int* j) {
+__device__ __forceinline__ Work work_at(const OrthoArgs& g, int t) {
+  const int one = g.tiles[0] + g.tiles[1] + g.tiles[2], per_step = g.batch * one;
+  Work w;
+  w.step = t / per_step;
+  int r = t - w.step * per_step;
+  w.kind = 0;
+  w.before = w.step * one;
+  while (r >= g.batch * g.tiles[w.kind]) {
+    r -= g.batch * g.tiles[w.kind];
+    w.before += g.tiles[w.kind];
+    ++w.kind;
+  }
+  w.b = r / g.tiles[w.kind];
+  r -= w.b * g.tiles[w.kind];
   constexpr int kN = Tile<PAIR>::kN, kR = Tile<PAIR>::kM / kN;
-  const int nn = (g.N + kN - 1) / kN;
-  *b = t / per;
-  int r = t - *b * per;
-  if (g.symmetric) {
-    int row = 0;
+  const int nn = ((w.kind == 2 ? g.n : g.p) + kN - 1) / kN;
+  if (w.kind < 2) {
+    w.i = 0;
     for (int left = nn; r >= left; left -= kR) {
       r -= left;
-      ++row;
+      ++w.i;
     }
-    *i = row;
-    *j = row * kR + r;
+    w.j = w.i * kR + r;
   } else {
-    *i = r / nn;
-    *j = r - *i * nn;
+    w.i = r / nn;
+    w.j = r - w.i * nn;
+  }
+  return w;
+}
+
+// Waits until matrix b has `want` stored parts; false as `wait`.
+__device__ __forceinline__ bool wait_stored(const OrthoArgs& g, int b, uint32_t want, volatile int* abort) {
+  const uint32_t* at = &g.ctrl->stored[b];
+  uint64_t t0 = 0;
+  for (;;) {
+    for (int k = 0; k < 64; ++k) {
+      uint32_t seen;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(at) : "memory");
+      if (seen >= want) return true;
+    }
+    if (t0 == 0) t0 = now_ns();
+    if (*abort || now_ns() - t0 > kAsyncWaitNs) return false;
   }
 }
 
@@ -586,8 +626,8 @@ enum Kind { kMakeA, kMakeB, kMakeX, kMakeOut };
 // the warp's shared memory, C the same way in: lane-per-row accesses to global memory (32 lines
 // each) took half of the kernel's time. False once a wait gave up.
 template <bool PAIR, int KIND, int S>
-__device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, Bars<S>* bars, uint8_t* s_epi, uint32_t tmem,
-                                         int unit, int units, uint32_t rank, int* acc_io, uint32_t* acc_phase_io) {
+__device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, const Work& w, Bars<S>* bars, uint8_t* s_epi,
+                                         uint32_t tmem, uint32_t rank, int acc, uint32_t acc_phase) {
   using T = Tile<PAIR>;
   constexpr int kC = T::kChunkN, kPieces = kC / 8, kSide = 32 / kPieces;  // 16-byte pieces a row; rows an access covers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -597,109 +637,103 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
     return reinterpret_cast<uint4*>(s_row + r * (2 * kC) + ((c ^ (r * kPieces / 8 % kPieces)) << 4));
   };
   const int lr = lane / kPieces, lc = lane % kPieces;    // this lane's row (of kSide) and piece in a coalesced access
-  const int per = tiles_of<PAIR>(pr.M, pr.N, pr.symmetric), total = per * g.batch;
   const float alpha = KIND == kMakeOut ? pr.alpha * g.scale * kUnhold : pr.alpha;
-  int acc = *acc_io;
-  uint32_t acc_phase = *acc_phase_io;
-  for (int t = unit; t < total; t += units) {
-    int b, i, j;
-    tile_at<PAIR>(pr, per, t, &b, &i, &j);
-    const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
-    const int col0 = j * T::kN + half * (T::kN / 2);
-    const bool some = row0 < pr.M;
-    const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
-    uint4 cw[kPieces];  // C of the next chunk, in coalesced order
-    auto load_c = [&](int ch) {
+  const int b = w.b, i = w.i, j = w.j;
+  const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
+  const int col0 = j * T::kN + half * (T::kN / 2);
+  const bool some = row0 < pr.M;
+  const int64_t at = b * pr.strideD + static_cast<int64_t>(row0 + lr) * pr.ldD + col0 + lc * 8;
+  uint4 cw[kPieces];  // C of the next chunk, in coalesced order
+  auto load_c = [&](int ch) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      cw[k] = make_uint4(0, 0, 0, 0);
+      if (row0 + lr + kSide * k < pr.M && col0 + ch * kC + lc * 8 < pr.ldD)
+        cw[k] = __ldcg(reinterpret_cast<const uint4*>(pr.C + at + static_cast<int64_t>(kSide * k) * pr.ldD + ch * kC));
+    }
+  };
+  if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, &bars->abort))) return false;
+  fence_after();
+  if (KIND == kMakeB) load_c(0);  // (A is there: the tile's loads waited for it)
+#pragma unroll 1
+  for (int ch = 0; some && ch < T::kChunks; ++ch) {
+    const int c0 = col0 + ch * kC;
+    if (c0 >= pr.N) break;
+    uint32_t r[kC];
+    const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * T::kN) +
+                          static_cast<uint32_t>(half * (T::kN / 2) + ch * kC);
+#pragma unroll
+    for (int k = 0; k < kC; k += 32) tmem_load(from + k, r + k);
+    if (KIND == kMakeB) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) *piece(lr + kSide * k, lc) = cw[k];
+      if (ch + 1 < T::kChunks) load_c(ch + 1);
+      __syncwarp();
+    }
+    tmem_wait(r);
+    float x[kC];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) x[k] = alpha * __uint_as_float(r[k]);
+    if (KIND == kMakeB) {
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
-        cw[k] = make_uint4(0, 0, 0, 0);
-        if (row0 + lr + kSide * k < pr.M && col0 + ch * kC + lc * 8 < pr.ldD)
-          cw[k] = __ldcg(reinterpret_cast<const uint4*>(pr.C + at + static_cast<int64_t>(kSide * k) * pr.ldD + ch * kC));
-      }
-    };
-    if (KIND == kMakeB) load_c(0);
-    if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, &bars->abort))) return false;
-    fence_after();
-#pragma unroll 1
-    for (int ch = 0; some && ch < T::kChunks; ++ch) {
-      const int c0 = col0 + ch * kC;
-      if (c0 >= pr.N) break;
-      uint32_t r[kC];
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * T::kN) +
-                            static_cast<uint32_t>(half * (T::kN / 2) + ch * kC);
+        const uint4 q = *piece(lane, k);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int k = 0; k < kC; k += 32) tmem_load(from + k, r + k);
-      if (KIND == kMakeB) {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) *piece(lr + kSide * k, lc) = cw[k];
-        if (ch + 1 < T::kChunks) load_c(ch + 1);
-        __syncwarp();
-      }
-      tmem_wait(r);
-      float x[kC];
-#pragma unroll
-      for (int k = 0; k < kC; ++k) x[k] = alpha * __uint_as_float(r[k]);
-      if (KIND == kMakeB) {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-          const uint4 q = *piece(lane, k);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e / 2]));
-            x[8 * k + e] = fmaf(pr.beta, f.x, x[8 * k + e]);
-            x[8 * k + e + 1] = fmaf(pr.beta, f.y, x[8 * k + e + 1]);
-          }
-        }
-        if (c0 < row0 + 32 && row0 < c0 + kC) {  // the diagonal crosses the chunk
-#pragma unroll
-          for (int k = 0; k < kC; ++k)
-            if (c0 + k == row0 + lane) x[k] += pr.diag;
+        for (int e = 0; e < 8; e += 2) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e / 2]));
+          x[8 * k + e] = fmaf(pr.beta, f.x, x[8 * k + e]);
+          x[8 * k + e + 1] = fmaf(pr.beta, f.y, x[8 * k + e + 1]);
         }
       }
+      if (c0 < row0 + 32 && row0 < c0 + kC) {  // the diagonal crosses the chunk
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) {  // two columns a word: fp16, or the result in bf16
-        const float* v = x + 8 * k;
-        *piece(lane, k) = KIND == kMakeOut
-            ? make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]))
-            : make_uint4(two_half(v[0], v[1]), two_half(v[2], v[3]), two_half(v[4], v[5]), two_half(v[6], v[7]));
+        for (int k = 0; k < kC; ++k)
+          if (c0 + k == row0 + lane) x[k] += pr.diag;
       }
-      __syncwarp();
-      if (KIND != kMakeOut || (g.out_vec && c0 + kC <= pr.N)) {  // (columns past N land in the padding of D's rows)
-        uint16_t* to = KIND != kMakeOut ? reinterpret_cast<uint16_t*>(pr.D) + at + ch * kC
-                                        : reinterpret_cast<uint16_t*>(g.out) + b * g.size +
-                                              static_cast<int64_t>(row0 + lr) * pr.N + c0 + lc * 8;
-        const int64_t ld = KIND != kMakeOut ? pr.ldD : pr.N;
-        uint4 q[kPieces];
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) q[k] = *piece(lr + kSide * k, lc);
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k)
-          if (row0 + lr + kSide * k < pr.M) *reinterpret_cast<uint4*>(to + kSide * k * ld) = q[k];
-      } else {  // a ragged edge of the result, or one at an odd address
-        uint16_t* to = reinterpret_cast<uint16_t*>(g.out) + b * g.size + static_cast<int64_t>(row0) * pr.N + c0;
-        for (int e = lane; e < 32 * kC; e += 32) {
-          const int rr = e / kC, cc = e % kC;
-          if (row0 + rr < pr.M && c0 + cc < pr.N)
-            to[static_cast<int64_t>(rr) * pr.N + cc] = reinterpret_cast<const uint16_t*>(piece(rr, cc / 8))[cc % 8];
-        }
-      }
-      __syncwarp();
     }
-    fence_before();
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {  // two columns a word: fp16, or the result in bf16
+      const float* v = x + 8 * k;
+      *piece(lane, k) = KIND == kMakeOut
+          ? make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]))
+          : make_uint4(two_half(v[0], v[1]), two_half(v[2], v[3]), two_half(v[4], v[5]), two_half(v[6], v[7]));
+    }
     __syncwarp();
-    if (lane == 0) {
-      const uint32_t bar = smem_addr(&bars->acc_empty[acc]);
-      if constexpr (PAIR)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
-      else
-        bar_arrive(bar);
+    if (KIND != kMakeOut || (g.out_vec && c0 + kC <= pr.N)) {  // (columns past N land in the padding of D's rows)
+      uint16_t* to = KIND != kMakeOut ? reinterpret_cast<uint16_t*>(pr.D) + at + ch * kC
+                                      : reinterpret_cast<uint16_t*>(g.out) + b * g.size +
+                                            static_cast<int64_t>(row0 + lr) * pr.N + c0 + lc * 8;
+      const int64_t ld = KIND != kMakeOut ? pr.ldD : pr.N;
+      uint4 q[kPieces];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) q[k] = *piece(lr + kSide * k, lc);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        if (row0 + lr + kSide * k < pr.M) *reinterpret_cast<uint4*>(to + kSide * k * ld) = q[k];
+    } else {  // a ragged edge of the result, or one at an odd address
+      uint16_t* to = reinterpret_cast<uint16_t*>(g.out) + b * g.size + static_cast<int64_t>(row0) * pr.N + c0;
+      for (int e = lane; e < 32 * kC; e += 32) {
+        const int rr = e / kC, cc = e % kC;
+        if (row0 + rr < pr.M && c0 + cc < pr.N)
+          to[static_cast<int64_t>(rr) * pr.N + cc] = reinterpret_cast<const uint16_t*>(piece(rr, cc / 8))[cc % 8];
+      }
     }
-    acc ^= 1;
-    if (acc == 0) acc_phase ^= 1u;
+    __syncwarp();
   }
-  *acc_io = acc;
-  *acc_phase_io = acc_phase;
+  fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    const uint32_t bar = smem_addr(&bars->acc_empty[acc]);
+    if constexpr (PAIR)
+      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
+    else
+      bar_arrive(bar);
+    if (KIND != kMakeOut) {  // this warp's part of the tile is stored
+      __threadfence();
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(&g.ctrl->stored[b]) : "memory");
+    }
+  }
   return true;
 }
 
@@ -756,108 +790,116 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  // ---- the products; each role carries its place in the ring and the accumulators along
+  // ---- the products; each role walks this unit's tiles of the list, carrying its place in the ring
+  // and the accumulators along
   int stage = 0, acc = 0;
   uint32_t ring_phase = 0, acc_phase = 0;
-  for (int prod = 0; ok && prod < 3 * g.steps; ++prod) {
-    const Product pr = product_of<PAIR>(g, maps, prod / 3, prod % 3);
-    const int per = tiles_of<PAIR>(pr.M, pr.N, pr.symmetric), total = per * g.batch;
-    const int num_kb = (pr.K + kBK - 1) / kBK;
-    if (warp == 0) {
-      if (lane == 0) {
-        bool fine = true;
-        for (int t = unit; fine && t < total; t += units) {
-          int b, i, j;
-          tile_at<PAIR>(pr, per, t, &b, &i, &j);
-          for (int kb = 0; kb < num_kb; ++kb) {
-            if (!wait<PAIR>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
-              fine = false;
-              break;
-            }
-            const uint32_t full = smem_addr(&bars->full[stage]);
-            const uint32_t dp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes)), dq = dp + T::kPBytes;
-            const uint32_t bar = PAIR ? in_cta(full, 0) : full;
-            if (rank == 0) bar_expect(full, (PAIR ? 2 : 1) * (T::kPBytes + T::kQBytes));
-            const int k0 = kb * kBK;
-            const int p0 = i * T::kM + static_cast<int>(rank) * kRowsP, q0 = j * T::kN + static_cast<int>(rank) * T::kRowsQ;
-            const bool p_mn = reads_mn<PAIR>(pr.p_in, i * T::kM, k0), q_mn = reads_mn<PAIR>(pr.q_in, j * T::kN, k0);
-            load_operand<PAIR, kRowsP>(dp, pr.P, pr.P, p_mn, p0, k0, b, bar);
-            load_operand<PAIR, T::kRowsQ>(dq, pr.Q, pr.Qrows, q_mn, q0, k0, b, bar);
-            if (++stage == S) {
-              stage = 0;
-              ring_phase ^= 1u;
-            }
+  const int total = ok ? g.steps * g.batch * (g.tiles[0] + g.tiles[1] + g.tiles[2]) : 0;
+  if (warp == 0) {
+    if (lane == 0) {
+      bool fine = true;
+      for (int t = unit; fine && t < total; t += units) {
+        const Work w = work_at<PAIR>(g, t);
+        const Product pr = product_of<PAIR>(g, maps, w.step, w.kind);
+        if (!wait_stored(g, w.b, static_cast<uint32_t>(w.before) * ((PAIR ? 2 : 1) * kEpiWarps), abort)) {
+          fine = false;
+          break;
+        }
+        fence_async_global();  // what the epilogues stored, before the TMA reads it
+        const int num_kb = (pr.K + kBK - 1) / kBK;
+        const int p0 = w.i * T::kM + static_cast<int>(rank) * kRowsP, q0 = w.j * T::kN + static_cast<int>(rank) * T::kRowsQ;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!wait<PAIR>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
+            fine = false;
+            break;
+          }
+          const uint32_t full = smem_addr(&bars->full[stage]);
+          const uint32_t dp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes)), dq = dp + T::kPBytes;
+          const uint32_t bar = PAIR ? in_cta(full, 0) : full;
+          if (rank == 0) bar_expect(full, (PAIR ? 2 : 1) * (T::kPBytes + T::kQBytes));
+          const int k0 = kb * kBK;
+          load_operand<PAIR, kRowsP>(dp, pr.P, pr.P, reads_mn<PAIR>(pr.p_in, w.i * T::kM, k0), p0, k0, w.b, bar);
+          load_operand<PAIR, T::kRowsQ>(dq, pr.Q, pr.Qrows, reads_mn<PAIR>(pr.q_in, w.j * T::kN, k0), q0, k0, w.b, bar);
+          if (++stage == S) {
+            stage = 0;
+            ring_phase ^= 1u;
           }
         }
-        if (!fine) {
-          atomicOr(g.err_word, kErrOrtho);
-          *abort = 1;
-        }
       }
-    } else if (warp == 1) {
-      if (lane == 0 && rank == 0) {
-        bool fine = true;
-        for (int t = unit; fine && t < total; t += units) {
-          if (!wait<PAIR>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
+      if (!fine) {
+        atomicOr(g.err_word, kErrOrtho);
+        *abort = 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      bool fine = true;
+      for (int t = unit; fine && t < total; t += units) {
+        const Work w = work_at<PAIR>(g, t);
+        const Product pr = product_of<PAIR>(g, maps, w.step, w.kind);
+        if (!wait<PAIR>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
+          fine = false;
+          break;
+        }
+        fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * T::kN);
+        const int num_kb = (pr.K + kBK - 1) / kBK;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!wait<PAIR>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
             fine = false;
             break;
           }
           fence_after();
-          int b, i, j;
-          tile_at<PAIR>(pr, per, t, &b, &i, &j);
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * T::kN);
-          for (int kb = 0; kb < num_kb; ++kb) {
-            if (!wait<PAIR>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
-              fine = false;
-              break;
-            }
-            fence_after();
-            const uint32_t sp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes));
-            const bool p_mn = reads_mn<PAIR>(pr.p_in, i * T::kM, kb * kBK), q_mn = reads_mn<PAIR>(pr.q_in, j * T::kN, kb * kBK);
-            const uint64_t dp = operand_desc(sp, p_mn), dq = operand_desc(sp + T::kPBytes, q_mn);
-            const uint32_t idesc = T::kIdesc | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u);
-            // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
-            // groups of an MN-major tile
-            const uint32_t step_p = p_mn ? 2048 >> 4 : 32 >> 4, step_q = q_mn ? 2048 >> 4 : 32 >> 4;
-            const uint32_t half_p = p_mn ? 4 * step_p : T::kPBytes / 2 >> 4, half_q = q_mn ? 4 * step_q : T::kQBytes / 2 >> 4;
+          const uint32_t sp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes));
+          const bool p_mn = reads_mn<PAIR>(pr.p_in, w.i * T::kM, kb * kBK), q_mn = reads_mn<PAIR>(pr.q_in, w.j * T::kN, kb * kBK);
+          const uint64_t dp = operand_desc(sp, p_mn), dq = operand_desc(sp + T::kPBytes, q_mn);
+          const uint32_t idesc = T::kIdesc | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u);
+          // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
+          // groups of an MN-major tile
+          const uint32_t step_p = p_mn ? 2048 >> 4 : 32 >> 4, step_q = q_mn ? 2048 >> 4 : 32 >> 4;
+          const uint32_t half_p = p_mn ? 4 * step_p : T::kPBytes / 2 >> 4, half_q = q_mn ? 4 * step_q : T::kQBytes / 2 >> 4;
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              mma_f16<PAIR>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
-                            (kb | k) != 0);
-            commit<PAIR>(smem_addr(&bars->empty[stage]));
-            if (++stage == S) {
-              stage = 0;
-              ring_phase ^= 1u;
-            }
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_f16<PAIR>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
+                          (kb | k) != 0);
+          commit<PAIR>(smem_addr(&bars->empty[stage]));
+          if (++stage == S) {
+            stage = 0;
+            ring_phase ^= 1u;
           }
-          if (!fine) break;
-          commit<PAIR>(smem_addr(&bars->acc_full[acc]));
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!fine) {
-          atomicOr(g.err_word, kErrOrtho);
-          *abort = 1;
-        }
+        if (!fine) break;
+        commit<PAIR>(smem_addr(&bars->acc_full[acc]));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-    } else {
-      bool fine;
-      if (prod % 3 == 0)
-        fine = epilogue<PAIR, kMakeA>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
-      else if (prod % 3 == 1)
-        fine = epilogue<PAIR, kMakeB>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
-      else if (pr.D)
-        fine = epilogue<PAIR, kMakeX>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
-      else
-        fine = epilogue<PAIR, kMakeOut>(g, pr, bars, s_epi, tmem, unit, units, rank, &acc, &acc_phase);
       if (!fine) {
-        if (lane == 0) atomicOr(g.err_word, kErrOrtho);
+        atomicOr(g.err_word, kErrOrtho);
         *abort = 1;
       }
     }
-    __syncwarp();
-    if (prod + 1 < 3 * g.steps) ok = grid_meet(g, bars, &phase);
+  } else {
+    bool fine = true;
+    for (int t = unit; fine && t < total; t += units) {
+      const Work w = work_at<PAIR>(g, t);
+      const Product pr = product_of<PAIR>(g, maps, w.step, w.kind);
+      if (w.kind == 0)
+        fine = epilogue<PAIR, kMakeA>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+      else if (w.kind == 1)
+        fine = epilogue<PAIR, kMakeB>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+      else if (pr.D)
+        fine = epilogue<PAIR, kMakeX>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+      else
+        fine = epilogue<PAIR, kMakeOut>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (!fine) {
+      if (lane == 0) atomicOr(g.err_word, kErrOrtho);
+      *abort = 1;
+    }
   }
+  __syncwarp();
 
   // ---- teardown: every copy has landed and every MMA and commit has finished before the CTA
   // (or its peer) may exit and its TMEM is given back
@@ -887,6 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------ host side
 
+size_t ctrl_bytes(int64_t batch) { return offsetof(OrthoCtrl, stored) + batch * sizeof(uint32_t); }
+
 size_t carve_ortho(uint8_t* base, int64_t batch, int m, int n, OrthoArgs* o) {
   uint8_t* first = base ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 127) & ~uintptr_t(127)) : nullptr;
   size_t at = 0;
@@ -898,7 +942,7 @@ size_t carve_ortho(uint8_t* base, int64_t batch, int m, int n, OrthoArgs* o) {
   const int p = std::min(m, n);
   o->ldx = (n + 63) / 64 * 64;  // rows start on 128 bytes
   o->ldp = (p + 63) / 64 * 64;
-  o->ctrl = reinterpret_cast<OrthoCtrl*>(take(sizeof(OrthoCtrl)));
+  o->ctrl = reinterpret_cast<OrthoCtrl*>(take(ctrl_bytes(batch)));
   o->partial = reinterpret_cast<float*>(take(batch * kNormParts * 3 * sizeof(float)));
   for (int i = 0; i < 2; ++i) o->X[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * m * o->ldx));
   o->A = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
@@ -975,6 +1019,9 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   };
   if (!encode(maps.X, maps.A, maps.Bm, kRowsP) || (!PAIR && !encode(maps.Xq, maps.Aq, maps.Bmq, Tile<false>::kRowsQ)))
     return PG_ERR_CUDA;
+  g.tiles[0] = g.tiles[1] = tiles_of<PAIR>(g.p, g.p, true);
+  g.tiles[2] = tiles_of<PAIR>(g.m, g.n, false);
+  if (static_cast<int64_t>(g.steps) * g.batch * (g.tiles[0] + g.tiles[1] + g.tiles[2]) >= (1ll << 31)) return PG_ERR_SHAPE;
   // no more units than the widest phase has work for: the fewer blocks, the quicker they meet
   const int64_t tiles = static_cast<int64_t>(g.batch) * std::max(tiles_of<PAIR>(g.m, g.n, false), tiles_of<PAIR>(g.p, g.p, true));
   const int64_t piece = 8 * kThreads;  // what a block's threads read at a time in the norm and the scaling
@@ -984,7 +1031,7 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   g.prepared = static_cast<int64_t>(g.batch) * g.size >= kPrepareFrom;
   const int blocks = g.prepared ? 2 * sm_count() : (PAIR ? 2 : 1) * units;
   g.parts = static_cast<int>(std::min<int64_t>({kNormParts, std::max(1, blocks / g.batch), (g.size + piece - 1) / piece}));
-  cudaError_t e = cudaMemsetAsync(g.ctrl, 0, sizeof(OrthoCtrl), stream);
+  cudaError_t e = cudaMemsetAsync(g.ctrl, 0, ctrl_bytes(g.batch), stream);
   if (e != cudaSuccess) return cuda_fail(e);
   if (g.prepared) {
     const bool f32 = g.dtype == PG_F32;
@@ -1011,22 +1058,28 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
   return after_launch(1);
 }
 
-// Whether 256 x 256 pair tiles finish sooner than 128 x 64 tiles: the k-blocks that the busiest
-// unit walks in a step at 0.62 us each (a pair's MMAs) against 0.53 us (a single CTA's 48 KB from
-// L2), and 6.4 us a step more for a pair's pipeline to fill and empty three times. Measured over 5
-// steps, pair and single, in us: 768 x 1024 154 / 114, 4 of them 161 / 189; 1280 x 2560 217 / 221;
-// 1280 x 1280 185 / 167.
+// Whether 256 x 256 pair tiles finish sooner than 128 x 64 tiles. A step takes the k-blocks that a
+// unit walks (those of one matrix alone, product after product, or all of them spread evenly,
+// whichever is more) at 0.62 us each (a pair's MMAs) against 0.53 us (a single CTA's 48 KB from L2),
+// and 6.4 us more for a pair's pipeline to fill and empty three times. Measured over 5 steps, pair
+// and single, in us: 768 x 1024 150 / 113, 4 of them 161 / 142; 1280 x 1280 184 / 169; 1280 x 2560
+// 217 / 223; 5 of 640 x 1280 164 / 145.
 bool use_pairs(const OrthoArgs& g, int sms) {
   const int q = std::max(g.m, g.n);
-  auto blocks = [&](bool pair, int M, int N, int K, bool sym) {
-    const int64_t per = pair ? tiles_of<true>(M, N, sym) : tiles_of<false>(M, N, sym);
-    const int64_t units = pair ? sms / 2 : sms;
-    return (per * g.batch + units - 1) / units * ((K + kBK - 1) / kBK);
-  };
   auto step = [&](bool pair) {
-    return blocks(pair, g.p, g.p, q, true) + blocks(pair, g.p, g.p, g.p, true) + blocks(pair, g.m, g.n, g.p, false);
+    const int units = pair ? sms / 2 : sms;
+    double alone = 0, all = 0;
+    auto product = [&](int M, int N, int K, bool sym) {
+      const int tiles = pair ? tiles_of<true>(M, N, sym) : tiles_of<false>(M, N, sym), blocks = (K + kBK - 1) / kBK;
+      alone += static_cast<double>((tiles + units - 1) / units) * blocks;
+      all += static_cast<double>(g.batch) * tiles * blocks / units;
+    };
+    product(g.p, g.p, q, true);
+    product(g.p, g.p, g.p, true);
+    product(g.m, g.n, g.p, false);
+    return std::max(alone, all);
   };
-  return 62 * step(true) + 640 < 53 * step(false);
+  return 0.62 * step(true) + 6.4 < 0.53 * step(false);
 }
 
 }  // namespace

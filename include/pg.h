@@ -725,7 +725,7 @@ pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32
  * result's; the scale puts magnitudes 6e-8 .. 63 into fp16's normal range, where a norm of at
  * most 1 and the usual coefficients keep them below 3).
  * A zero matrix gives zeros (eps > 0); infinities and NaN in G make its own matrix NaN.
- *  1 <= m, n <= 16384; 0 <= batch <= 4096; 1 <= steps <= 32; workspace device, 16-byte aligned,
+ *  1 <= m, n <= 16384; 0 <= batch <= 4096; 1 <= steps <= 32 (and fewer than 2^31 tiles in all); workspace device, 16-byte aligned,
  *  >= pg_orthogonalize_workspace_size bytes, scratch. batch == 0 enqueues nothing.
  */
 pg_status pg_orthogonalize_workspace_size(int32_t batch, int32_t m, int32_t n, size_t* bytes);
