@@ -729,10 +729,9 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
       asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
     else
       bar_arrive(bar);
-    if (KIND != kMakeOut) {  // this warp's part of the tile is stored
-      __threadfence();
+    // this warp's part of the tile is stored (the release covers what its lanes wrote before __syncwarp)
+    if (KIND != kMakeOut)
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(&g.ctrl->stored[b]) : "memory");
-    }
   }
   return true;
 }

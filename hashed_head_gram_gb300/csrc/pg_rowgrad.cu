@@ -373,13 +373,17 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     return;
   }
   if (HASHED) {
-    const int words = src.items * static_cast<int>(sizeof(ItemConst) / 4);
-    for (int i = tid; i < words; i += kSortThreads)
-      reinterpret_cast<uint32_t*>(s_ic)[i] = reinterpret_cast<const uint32_t*>(src.ic)[i];
+    // the group's items, a warp a word: the parameter bank serves one address at a time
+    constexpr int kWords = static_cast<int>(sizeof(ItemConst) / 4);
+    const int first = static_cast<int>(group) * src.heads * kWords, last = first + src.heads * kWords;
+    for (int i = first + warp; i < last; i += kSortWarps) {
+      const uint32_t x = reinterpret_cast<const uint32_t*>(src.ic)[i];
+      if (lane == 0) reinterpret_cast<uint32_t*>(s_ic)[i] = x;
+    }
     __syncthreads();
     row0 = s_ic[group * src.heads].base;  // the group's first row: keys count from it
     __syncthreads();
-    if (tid < src.items) s_ic[tid].base -= row0;
+    if (tid < src.heads) s_ic[group * src.heads + tid].base -= row0;
     __syncthreads();
   }
 
