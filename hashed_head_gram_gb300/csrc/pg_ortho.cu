@@ -594,8 +594,7 @@ __device__ __forceinline__ bool grid_meet(const OrthoArgs& g, Bars<S>* bars, uin
   if (threadIdx.x == 0) {
     bool ok = !*static_cast<volatile int*>(&bars->abort);
     if (ok) {
-      __threadfence();
-      atomicAdd(&g.ctrl->barrier, 1u);
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(&g.ctrl->barrier) : "memory");
       const uint32_t want = *phase * gridDim.x;
       const uint64_t t0 = now_ns();
       for (;;) {
@@ -608,7 +607,6 @@ __device__ __forceinline__ bool grid_meet(const OrthoArgs& g, Bars<S>* bars, uin
           break;
         }
       }
-      __threadfence();
       fence_async_global();
     }
     bars->ok = ok;

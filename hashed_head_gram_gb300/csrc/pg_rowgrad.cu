@@ -122,8 +122,8 @@ __device__ __forceinline__ bool grid_barrier(uint32_t G, uint32_t* counter, uint
   __syncthreads();
   if (G == 1) return true;
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(counter, 1u);
+    // (the release covers what the block's threads wrote before __syncthreads)
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
     const uint32_t want = *phase * G;
     const uint64_t t0 = now_ns();
     uint32_t seen;
@@ -137,7 +137,6 @@ __device__ __forceinline__ bool grid_barrier(uint32_t G, uint32_t* counter, uint
         break;
       }
     }
-    __threadfence();
     *s_ok = ok;
   }
   __syncthreads();
