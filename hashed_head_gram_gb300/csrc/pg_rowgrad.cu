@@ -600,7 +600,7 @@ constexpr int kJoinThreads = 256;
 
 struct SumArgs {
   const void* grad;          // summands, rows of r values; reference i has row i / share
-  const uint8_t* sign;       // sign bits of the references, a byte for 8 columns, or null
+  const uint8_t* sign;       // sign bits of the references, a byte for 8 columns (hashed lookup)
   const uint2* order;        // (output row, reference), rows ascending
   const SortCtrl* ctrl;
   float* parts;
@@ -631,10 +631,10 @@ struct Raw {
     }
   }
 
-  // acc += the columns, those with a bit in `neg` negated
+  // acc += the columns, two at a time; SIGNED: those with a bit in `neg` negated
+  template <bool SIGNED>
   __device__ __forceinline__ void add(float (&acc)[COLS], uint32_t neg) const {
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) {
+    auto value = [&](int j) -> uint32_t {
       uint32_t v;
       if constexpr (IN == PG_F32)
         v = w[j];
@@ -642,7 +642,17 @@ struct Raw {
         v = w[0] << 16;
       else
         v = (j & 1) ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16;
-      acc[j] += __uint_as_float(v ^ ((neg << (31 - j)) & 0x80000000u));
+      return SIGNED ? v ^ ((neg << (31 - j)) & 0x80000000u) : v;
+    };
+    if constexpr (COLS == 1) {
+      acc[0] += __uint_as_float(value(0));
+    } else {
+#pragma unroll
+      for (int j = 0; j < COLS; j += 2)
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+            "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "+f"(acc[j]), "+f"(acc[j + 1])
+            : "r"(value(j)), "r"(value(j + 1)));
     }
   }
 };
@@ -660,7 +670,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int c,
 // A group of `lanes` consecutive threads per tile of T references and lanes * COLS columns.
 // The loads of 8 summands (fp32: 4) are in flight at a time, and behind them those of the next
 // references' numbers.
-template <int IN, int OUT, int COLS>
+template <int IN, int OUT, int COLS, bool SIGNED>
 __global__ void __launch_bounds__(kSumThreads, 5)
     rowgrad_sum_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
   const int per_block = kSumThreads / lanes;
@@ -707,7 +717,7 @@ __global__ void __launch_bounds__(kSumThreads, 5)
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       x[k].load(a.grad, static_cast<int64_t>(a.share == 1 ? ref[k] : ref[k] / a.share) * a.r + c);
-      neg[k] = a.sign ? __ldg(a.sign + static_cast<int64_t>(ref[k]) * a.sign_bytes + (c >> 3)) >> (c & 7) : 0u;
+      neg[k] = SIGNED ? __ldg(a.sign + static_cast<int64_t>(ref[k]) * a.sign_bytes + (c >> 3)) >> (c & 7) : 0u;
       sg[k] = seg[k];
     }
     if (q0 + kFly < p1) numbers(q0 + kFly);
@@ -725,7 +735,7 @@ __global__ void __launch_bounds__(kSumThreads, 5)
 #pragma unroll
         for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
       }
-      x[k].add(acc, neg[k]);
+      x[k].template add<SIGNED>(acc, neg[k]);
     }
   }
   if (cur == a.none) return;
@@ -835,11 +845,11 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
 
 using SumFn = void (*)(SumArgs, int, int);
 
-template <int COLS>
+template <int COLS, bool SIGNED>
 SumFn sum_fn(int in, int out) {
   if (in == PG_F32)
-    return out == PG_F32 ? rowgrad_sum_kernel<PG_F32, PG_F32, COLS> : rowgrad_sum_kernel<PG_F32, PG_BF16, COLS>;
-  return out == PG_F32 ? rowgrad_sum_kernel<PG_BF16, PG_F32, COLS> : rowgrad_sum_kernel<PG_BF16, PG_BF16, COLS>;
+    return out == PG_F32 ? rowgrad_sum_kernel<PG_F32, PG_F32, COLS, SIGNED> : rowgrad_sum_kernel<PG_F32, PG_BF16, COLS, SIGNED>;
+  return out == PG_F32 ? rowgrad_sum_kernel<PG_BF16, PG_F32, COLS, SIGNED> : rowgrad_sum_kernel<PG_BF16, PG_BF16, COLS, SIGNED>;
 }
 
 template <int COLS>
@@ -928,7 +938,7 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
     const cudaError_t err = cudaLaunchKernelEx(&c, fn, a, lanes, T);
     return err == cudaSuccess ? after_launch(1) : cuda_fail(err);
   };
-  st = launch(vec ? sum_fn<8>(in, out) : sum_fn<1>(in, out), kSumThreads);
+  st = launch(vec ? sum_fn<8, HASHED>(in, out) : sum_fn<1, HASHED>(in, out), kSumThreads);
   if (st != PG_OK) return st;
   return launch(vec ? join_fn<8>(out) : join_fn<1>(out), kJoinThreads);
 }
