@@ -2,19 +2,29 @@
 // pg_lookup_grad (the hashed multi-head table, PageGram report 9.4, check 4).
 //
 // A reference is one read of a table row: (t) for the embedding, (t, order, head) for the
-// hashed lookup, n of them in that order. With their rows sorted (stably), the references of
-// a row are neighbours and its gradient is one segmented sum:
+// hashed lookup, n of them. With their rows sorted (stably), the references of a row are
+// neighbours and its gradient is one segmented sum:
 //
 //   1. rowgrad_sort_kernel: rows of the references (embedding: the canonical ID; hashed
 //      lookup: the hashes of pg_hash.cuh), a stable radix sort of (row, reference) with
-//      digits of up to 11 bits, and the segments of equal rows. One cooperative launch; the
+//      digits of up to 11 bits, and the numbers of the distinct rows. One cooperative launch; the
 //      blocks meet at a grid barrier between the phases. Every block owns a contiguous share
 //      of the references, so ranks follow from counts alone and no order depends on timing.
+//      Everything it moves stays in L2; its time is latency and instructions: of 72 us for a
+//      million reads (PageGram, three digits) 9 are the hashes, 14 the ranks, 10 the scattered
+//      stores and 25 the barriers and what is read right after them.
 //   2. rowgrad_sum_kernel: the sums, fp32, in ascending order of the references. The sorted
-//      references are cut into tiles of a fixed size, whatever the segments' lengths (one ID
-//      can take a tenth of a batch): a group of lanes walks a tile, writes the rows that lie
-//      wholly in it and leaves the sums of the others for
+//      references are cut into tiles of a fixed size, whatever the rows' shares (one ID can take
+//      a tenth of a batch): a group of lanes walks a tile, writes the rows that lie wholly in it
+//      and leaves the sums of the others for
 //   3. rowgrad_join_kernel, which adds the parts of a row that crosses tiles, in their order.
+//
+// The floor is the gradient read once and the output written once: 407 MB, 60 us for the million
+// reads of 64 columns. The sums alone take 72 us (372 MB through DRAM while they run, 66 % of its
+// peak: random 128-byte reads, 16-byte loads 8 deep in 5 blocks of 128 threads an SM; 6 blocks
+// spill, 24 % slower, and tiles of 16 or 64 move 12 % between this kernel and the join), and the
+// sort comes before them: 159 us in all. The embedding's sort runs on 32 SMs for 65,536 tokens
+// while the other blocks zero the gradient.
 #include "pg_async.cuh"
 #include "pg_hash.cuh"
 #include "pg_vec.h"
