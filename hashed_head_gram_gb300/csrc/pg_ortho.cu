@@ -25,9 +25,10 @@
 //   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
 //
 // Bound by the tensor cores where the tiles fill them: five 2560 x 1280 matrices need 367 GFLOP
-// (189 us at the measured bf16 rate) and take 320 us, 0.59 of that rate: 35 us are the norm, the
-// scaling and the launches, each k-block takes 0.65 us (the rate of a large library product), and
-// the rest is the chain of a step: 75 tiles of A, 75 of Bm and 250 of X on 76 CTA pairs, each
+// (189 us at the measured bf16 rate) and take 320 us, 0.59 of that rate. A step takes 51 us, all
+// that is there once 49 (norm 13, scaling 14, launches, the first fill, the last epilogue). A k-block
+// takes 0.65 us (the rate of a large library product), 41 us of a step; the rest of it is the chain:
+// 75 tiles of A, 75 of Bm and 250 of X on 76 CTA pairs, each
 // product's first loads behind the last stores of the one before. One 768 x 1024 matrix (11 GFLOP)
 // takes 104 us for 15 products: 7 us each of loads from L2 (48 KB a k-block and SM at some 90 GB/s),
 // the first copy, the last epilogue and the counter.
