@@ -945,11 +945,11 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
   a.tiles = (n + T - 1) / T;
   const bool vec = a.r % 8 == 0 && aligned(a.grad, vec_bytes(in)) && aligned(a.out, vec_bytes(out));
   const int cols = vec ? 8 : 1;
-  // threads a row, in equal column blocks of at most 32 (an 80-wide head takes 10, 12 tiles a block)
-  const int row_threads = (a.r + cols - 1) / cols, col_blocks = (row_threads + 31) / 32;
-  const int lanes = (row_threads + col_blocks - 1) / col_blocks;
   // each is scheduled while the kernel before it runs out, and waits for its end
-  auto launch = [&](SumFn fn, int threads) -> pg_status {
+  auto launch = [&](SumFn fn, int threads, int most) -> pg_status {
+    // threads a row, in equal column blocks of at most `most` (an 80-wide head takes 10, 12 tiles a block)
+    const int row_threads = (a.r + cols - 1) / cols, col_blocks = (row_threads + most - 1) / most;
+    const int lanes = (row_threads + col_blocks - 1) / col_blocks;
     const uint32_t per_block = threads / lanes;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((a.tiles + per_block - 1) / per_block, col_blocks);
@@ -963,9 +963,12 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
     const cudaError_t err = cudaLaunchKernelEx(&c, fn, a, lanes, T);
     return err == cudaSuccess ? after_launch(1) : cuda_fail(err);
   };
-  st = launch(vec ? sum_fn<8, HASHED>(in, out) : sum_fn<1, HASHED>(in, out), kSumThreads);
+  st = launch(vec ? sum_fn<8, HASHED>(in, out) : sum_fn<1, HASHED>(in, out), kSumThreads, 32);
   if (st != PG_OK) return st;
-  return launch(vec ? join_fn<8>(out) : join_fn<1>(out), kJoinThreads);
+  // A common token's row has parts in hundreds of tiles: narrower blocks add more of them at a time
+  // (65,536 x 768: 74 us at 32 lanes, 69 at 16, 71 at 8). Hashed rows are shorter, and every column
+  // block looks for the ends of its rows again (flat, 768 columns: 143 at 32, 146 at 16, 149 at 8).
+  return launch(vec ? join_fn<8>(out) : join_fn<1>(out), kJoinThreads, HASHED ? 32 : 16);
 }
 
 }  // namespace
