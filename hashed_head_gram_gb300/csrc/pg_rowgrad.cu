@@ -10,7 +10,7 @@
 //      digits of up to 11 bits, and the numbers of the distinct rows. One cooperative launch; the
 //      blocks meet at a grid barrier between the phases. Every block owns a contiguous share
 //      of the references, so ranks follow from counts alone and no order depends on timing.
-//      Everything it moves stays in L2; its time is latency and instructions: of 72 us for a
+//      Everything it moves stays in L2; its time is latency and instructions: of 71 us for a
 //      million reads (PageGram, three digits) 9 are the hashes, 14 the ranks, 10 the scattered
 //      stores and 25 the barriers and what is read right after them.
 //   2. rowgrad_sum_kernel: the sums, fp32, in ascending order of the references. The sorted
@@ -20,11 +20,11 @@
 //   3. rowgrad_join_kernel, which adds the parts of a row that crosses tiles, in their order.
 //
 // The floor is the gradient read once and the output written once: 407 MB, 60 us for the million
-// reads of 64 columns. The sums alone take 72 us (372 MB through DRAM while they run, 66 % of its
+// reads of 64 columns. The sums alone take 71 us (372 MB through DRAM while they run, 66 % of its
 // peak: random 128-byte reads, 16-byte loads 8 deep in 5 blocks of 128 threads an SM; 6 blocks
 // spill, 24 % slower; whole calls with tiles of 16 or 64 references are within 3 %, but 13 % slower
 // at 16 where one row takes a tenth of the batch and 8 % at 64 for this one), and the sort comes
-// before them: 159 us in all. The embedding's sort runs on 32 SMs for 65,536 tokens
+// before them: 155 us in all. The embedding's sort runs on 32 SMs for 65,536 tokens
 // while the other blocks zero the gradient.
 #include "pg_async.cuh"
 #include "pg_hash.cuh"
