@@ -23,8 +23,8 @@
 // reads of 64 columns. The sums alone take 71 us (372 MB through DRAM while they run, 66 % of its
 // peak: random 128-byte reads, 16-byte loads 8 deep in 5 blocks of 128 threads an SM; 6 blocks
 // spill, 24 % slower; tiles of 16 references make the embedding's calls 6 and 13 % slower, of 64
-// this one 8 %, the other calls within 4 %), and the sort comes before them: 155 us in all. The embedding's sort runs on 32 SMs for 65,536 tokens
-// while the other blocks zero the gradient.
+// this one 8 %, the other calls within 4 %), and the sort comes before them: 155 us in all. The
+// embedding's sort runs on 32 SMs for 65,536 tokens while the other blocks zero the gradient.
 #include "pg_async.cuh"
 #include "pg_hash.cuh"
 #include "pg_vec.h"
