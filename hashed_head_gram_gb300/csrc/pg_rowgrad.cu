@@ -966,8 +966,9 @@ pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint3
   if (st != PG_OK) return st;
   // A common token's row has parts in hundreds of tiles: narrower blocks add more of them at a time
   // (65,536 x 768: 74 us at 32 lanes, 69 at 16, 71 at 8). Hashed rows are shorter, and every column
-  // block looks for the ends of its rows again (flat, 768 columns: 143 at 32, 146 at 16, 149 at 8).
-  return launch(vec ? join_fn<8>(out) : join_fn<1>(out), kJoinThreads, HASHED ? 32 : 16);
+  // block looks for the ends of its rows again (flat, 768 columns: 143 at 32, 146 at 16, 149 at 8);
+  // and a column a thread, 16 would take more than 65,535 blocks in y for the widest rows.
+  return launch(vec ? join_fn<8>(out) : join_fn<1>(out), kJoinThreads, HASHED || !vec ? 32 : 16);
 }
 
 }  // namespace

@@ -169,6 +169,11 @@ def test_embed_grad_unaligned_and_one_row(cuda):
     check_embed_grad(cuda, 40000, 2, 3, 2, "mixed", F32, F32, canon=False)
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+def test_embed_grad_widest_rows(cuda, shift):
+    check_embed_grad(cuda, 20, 1 << 20, 4, 3, "mixed", F32, BF16, shift=shift)
+
+
 def test_embed_grad_of_no_tokens(cuda):
     pg = _pg()
     out = torch.ones(5, 8, device=cuda)
