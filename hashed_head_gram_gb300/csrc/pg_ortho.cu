@@ -11,7 +11,17 @@
 // are neither computed nor stored: an operand that needs one reads its mirror image MN-major.
 //
 // Between the products X, A and Bm are held as fp16 scaled by 2^10 (pg.h): 11 significant
-// bits, against the 8 of the bf16 result.
+// bits, against the 8 of the bf16 result. That is enough for A and Bm: they multiply X, so their
+// roundings stay small relative to the directions that X has. It is not for X itself: its rounding
+// spreads over all singular directions, and each later step multiplies by a = 3.44 what lies in those
+// that G does not have, 485-fold from X0 on (256 x 1024 of rank 1: 15 % of the result, of rank 4: 7 %).
+// So X is held as a sum hi + lo of two fp16 numbers, 22 bits. A is made of hi alone (its error is
+// one of A's own size), and the last step takes hi alone (its rounding grows a-fold at most).
+// The other steps' X <- Bm (hi + lo) is Bm hi + a lo, the addend in the epilogue: Bm differs from a I
+// where X has directions, and there lo is a rounding that does not grow. Where Bm is one k-block
+// deep (p <= 128), Bm lo is one more k-block and is taken whole. Relative to the formulas the results
+// are 0.0020-0.0028 off, of which 0.0017 are the bf16 result's own rounding (0.0020 of Gaussian
+// matrices with hi alone; with Bm lo at every size the products would take half as long again).
 //
 // One cooperative launch does the whole update (large batches: norm and scaling before it): norm,
 // scaling, and 3 * steps products on the tensor cores. The tiles of all products stand in one list,
@@ -93,18 +103,20 @@ struct OrthoArgs {
   OrthoCtrl* ctrl;
   float* partial;            // [batch][parts][3]
   __half *X[2], *A, *Bm;     // [batch][m][ldx], [batch][p][ldp]
+  __half* L[2];              // what X's rounding to fp16 left, as X; one buffer unless lo_product
   int* err_word;
   int64_t size;              // m n
   int batch, m, n, p, ldx, ldp, parts, steps, dtype;
   int g_vec, out_vec;        // accesses of 8 columns to G; to out
   int prepared;              // X0 is there already
+  int lo_product;            // Bm lo is a k-block of the product; else a lo is added
   int tiles[3];              // of one matrix, of each product
   float a, b, c, eps, scale;
 };
 
 // Boxes of 64 columns and 128 rows; for the single CTA's 64 rows of Q, K-major, of 64 rows too.
 struct Maps {
-  CUtensorMap X[2], A, Bm;
+  CUtensorMap X[2], A, Bm, L[2];
   CUtensorMap Xq[2], Aq, Bmq;
 };
 
@@ -391,6 +403,12 @@ __device__ __forceinline__ uint32_t two_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// What rounding `hi` of two values left.
+__device__ __forceinline__ uint32_t two_left(uint32_t hi, float x0, float x1) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return two_half(x0 - f.x, x1 - f.y);
+}
+
 // X0: rows of G scaled and rounded into rows of stride ldx, 8 columns at a time. A block owns a
 // contiguous share of the rows of all matrices.
 template <int DT, int THREADS>
@@ -411,12 +429,18 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
     const uint32_t vecs = static_cast<uint32_t>(r1 - r0) * per_row;  // < 2^31: at most m of at most 2048
     auto store = [&](uint32_t v, const float (&x)[8]) {
       const uint32_t r = v / per_row, j = (v - r * per_row) * 8;
-      *reinterpret_cast<uint4*>(g.X[0] + (r0 + r) * g.ldx + j) =
-          make_uint4(two_half(x[0] * scale, x[1] * scale), two_half(x[2] * scale, x[3] * scale),
-                     two_half(x[4] * scale, x[5] * scale), two_half(x[6] * scale, x[7] * scale));
+      const int64_t at = (r0 + r) * g.ldx + j;
+      uint32_t hi[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) hi[k] = two_half(x[2 * k] * scale, x[2 * k + 1] * scale);
+      *reinterpret_cast<uint4*>(g.X[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (g.steps == 1) return;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) hi[k] = two_left(hi[k], x[2 * k] * scale, x[2 * k + 1] * scale);
+      *reinterpret_cast<uint4*>(g.L[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     };
     if (g.g_vec) {  // n % 8 == 0: a row's pieces follow the row before's
-      constexpr int kFly = (DT == PG_F32 ? 8 : 16) * kThreads / THREADS;
+      constexpr int kFly = (DT == PG_F32 ? 8 : 12) * kThreads / THREADS;
       for (uint32_t v0 = threadIdx.x; v0 < vecs; v0 += kFly * THREADS) {
         Raw8<DT> raw[kFly];
 #pragma unroll
@@ -464,15 +488,17 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ortho_scale_kernel(const __gr
 
 // --------------------------------------------------------------------------- the products
 
-// D = alpha P Q^T + beta C + diag I; see the top of the file.
+// D = alpha (P Q^T + P2 Q2^T) + beta C + diag I; see the top of the file.
 struct Product {
   const CUtensorMap *P, *Q, *Qrows;  // Qrows: Q in boxes of as many rows as a CTA stages of it
+  const CUtensorMap *P2, *Q2;        // the low part's operands, laid out as P and Q, one k-block deep
   const __half* C;       // laid out as D, or null
   __half* D;             // [M, N]; null for the last product (out)
+  __half* Dlo;           // what rounding D left, or null
   int64_t strideD;       // between matrices, elements
   int ldD, M, N, K;
   float alpha, beta, diag;
-  bool symmetric;
+  bool symmetric, low;   // low: there are P2 and Q2
   // An operand is K-major (its rows are the matrix's), MN-major (the matrix's columns), or, A
   // and Bm, symmetric with only the tiles that reach the diagonal or lie above it stored: those
   // K-major, the others as the MN-major mirror image.
@@ -492,7 +518,10 @@ __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& ma
   Product r;
   r.symmetric = kind < 2;
   r.M = r.N = r.K = g.p;
+  r.P2 = r.Q2 = nullptr;
+  r.low = false;
   r.C = nullptr;
+  r.Dlo = nullptr;
   r.alpha = kUnhold;
   r.beta = r.diag = 0.f;
   r.ldD = g.ldp;
@@ -518,6 +547,15 @@ __device__ __forceinline__ Product product_of(const OrthoArgs& g, const Maps& ma
     r.p_in = wide ? Product::kUpper : Product::kRows;
     r.q_in = wide ? Product::kColumns : Product::kUpper;
     r.D = step + 1 == g.steps ? nullptr : g.X[cur ^ 1];
+    r.Dlo = step + 2 < g.steps ? g.L[cur ^ 1] : nullptr;
+    if (g.lo_product) {
+      r.low = step + 1 < g.steps;
+      r.P2 = wide ? r.P : &maps.L[cur];
+      r.Q2 = wide ? &maps.L[cur] : r.Q;
+    } else {               // (a tile reads the part of lo that it writes)
+      r.C = g.L[cur];
+      r.beta = g.a;
+    }
     r.M = g.m;
     r.N = g.n;
     r.ldD = g.ldx;
@@ -626,7 +664,7 @@ __device__ __forceinline__ bool grid_meet(const OrthoArgs& g, Bars<S>* bars, uin
 
 // What an epilogue writes. One instance each: its body has no branches between the columns, so
 // that the arithmetic of a chunk overlaps (with them a chunk took twice as long).
-enum Kind { kMakeA, kMakeB, kMakeX, kMakeOut };
+enum Kind { kMakeA, kMakeB, kMakeX, kMakeXPlain, kMakeOut };  // kMakeXPlain: without an addend
 
 // A warp takes 32 rows of a tile (its TMEM lanes) and half of its columns, in chunks. TMEM gives
 // a lane one row; global memory wants neighbouring lanes on one row. So a chunk passes through
@@ -645,6 +683,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
   };
   const int lr = lane / kPieces, lc = lane % kPieces;    // this lane's row (of kSide) and piece in a coalesced access
   const float alpha = KIND == kMakeOut ? pr.alpha * g.scale * kUnhold : pr.alpha;
+  constexpr bool kAdds = KIND == kMakeB || KIND == kMakeX;
   const int b = w.b, i = w.i, j = w.j;
   const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
   const int col0 = j * T::kN + half * (T::kN / 2);
@@ -661,7 +700,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
   };
   if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, &bars->abort))) return false;
   fence_after();
-  if (KIND == kMakeB) load_c(0);  // (A is there: the tile's loads waited for it)
+  if (kAdds) load_c(0);  // (C is there: the tile's loads waited for it)
 #pragma unroll 1
   for (int ch = 0; some && ch < T::kChunks; ++ch) {
     const int c0 = col0 + ch * kC;
@@ -671,7 +710,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
                           static_cast<uint32_t>(half * (T::kN / 2) + ch * kC);
 #pragma unroll
     for (int k = 0; k < kC; k += 32) tmem_load(from + k, r + k);
-    if (KIND == kMakeB) {
+    if (kAdds) {
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) *piece(lr + kSide * k, lc) = cw[k];
       if (ch + 1 < T::kChunks) load_c(ch + 1);
@@ -681,7 +720,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
     float x[kC];
 #pragma unroll
     for (int k = 0; k < kC; ++k) x[k] = alpha * __uint_as_float(r[k]);
-    if (KIND == kMakeB) {
+    if (kAdds) {
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const uint4 q = *piece(lane, k);
@@ -693,7 +732,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
           x[8 * k + e + 1] = fmaf(pr.beta, f.y, x[8 * k + e + 1]);
         }
       }
-      if (c0 < row0 + 32 && row0 < c0 + kC) {  // the diagonal crosses the chunk
+      if (KIND == kMakeB && c0 < row0 + 32 && row0 < c0 + kC) {  // the diagonal crosses the chunk
 #pragma unroll
         for (int k = 0; k < kC; ++k)
           if (c0 + k == row0 + lane) x[k] += pr.diag;
@@ -707,17 +746,19 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
           : make_uint4(two_half(v[0], v[1]), two_half(v[2], v[3]), two_half(v[4], v[5]), two_half(v[6], v[7]));
     }
     __syncwarp();
-    if (KIND != kMakeOut || (g.out_vec && c0 + kC <= pr.N)) {  // (columns past N land in the padding of D's rows)
-      uint16_t* to = KIND != kMakeOut ? reinterpret_cast<uint16_t*>(pr.D) + at + ch * kC
-                                      : reinterpret_cast<uint16_t*>(g.out) + b * g.size +
-                                            static_cast<int64_t>(row0 + lr) * pr.N + c0 + lc * 8;
-      const int64_t ld = KIND != kMakeOut ? pr.ldD : pr.N;
+    auto store = [&](uint16_t* to, int64_t ld) {  // the staged chunk, rows of stride ld; to: this lane's first piece
       uint4 q[kPieces];
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) q[k] = *piece(lr + kSide * k, lc);
 #pragma unroll
       for (int k = 0; k < kPieces; ++k)
         if (row0 + lr + kSide * k < pr.M) *reinterpret_cast<uint4*>(to + kSide * k * ld) = q[k];
+    };
+    if (KIND != kMakeOut || (g.out_vec && c0 + kC <= pr.N)) {  // (columns past N land in the padding of D's rows)
+      store(KIND != kMakeOut ? reinterpret_cast<uint16_t*>(pr.D) + at + ch * kC
+                             : reinterpret_cast<uint16_t*>(g.out) + b * g.size +
+                                   static_cast<int64_t>(row0 + lr) * pr.N + c0 + lc * 8,
+            KIND != kMakeOut ? pr.ldD : pr.N);
     } else {  // a ragged edge of the result, or one at an odd address
       uint16_t* to = reinterpret_cast<uint16_t*>(g.out) + b * g.size + static_cast<int64_t>(row0) * pr.N + c0;
       for (int e = lane; e < 32 * kC; e += 32) {
@@ -727,6 +768,18 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
       }
     }
     __syncwarp();
+    if ((KIND == kMakeX || KIND == kMakeXPlain) && pr.Dlo) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const float* v = x + 8 * k;
+        const uint4 q = *piece(lane, k);
+        *piece(lane, k) = make_uint4(two_left(q.x, v[0], v[1]), two_left(q.y, v[2], v[3]), two_left(q.z, v[4], v[5]),
+                                     two_left(q.w, v[6], v[7]));
+      }
+      __syncwarp();
+      store(reinterpret_cast<uint16_t*>(pr.Dlo) + at + ch * kC, pr.ldD);
+      __syncwarp();
+    }
   }
   fence_before();
   __syncwarp();
@@ -812,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         fence_async_global();  // what the epilogues stored, before the TMA reads it
-        const int num_kb = (pr.K + kBK - 1) / kBK;
+        const int high_kb = (pr.K + kBK - 1) / kBK, num_kb = high_kb + pr.low;
         const int p0 = w.i * T::kM + static_cast<int>(rank) * kRowsP, q0 = w.j * T::kN + static_cast<int>(rank) * T::kRowsQ;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!wait<PAIR>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
@@ -823,9 +876,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes)), dq = dp + T::kPBytes;
           const uint32_t bar = PAIR ? in_cta(full, 0) : full;
           if (rank == 0) bar_expect(full, (PAIR ? 2 : 1) * (T::kPBytes + T::kQBytes));
-          const int k0 = kb * kBK;
-          load_operand<PAIR, kRowsP>(dp, pr.P, pr.P, reads_mn<PAIR>(pr.p_in, w.i * T::kM, k0), p0, k0, w.b, bar);
-          load_operand<PAIR, T::kRowsQ>(dq, pr.Q, pr.Qrows, reads_mn<PAIR>(pr.q_in, w.j * T::kN, k0), q0, k0, w.b, bar);
+          const bool low = kb == high_kb;  // (P2 is K-major or Bm, Q2 MN-major or Bm: Qrows serves both)
+          const int k0 = low ? 0 : kb * kBK;
+          const CUtensorMap* P = low ? pr.P2 : pr.P;
+          load_operand<PAIR, kRowsP>(dp, P, P, reads_mn<PAIR>(pr.p_in, w.i * T::kM, k0), p0, k0, w.b, bar);
+          load_operand<PAIR, T::kRowsQ>(dq, low ? pr.Q2 : pr.Q, pr.Qrows, reads_mn<PAIR>(pr.q_in, w.j * T::kN, k0), q0, k0,
+                                        w.b, bar);
           if (++stage == S) {
             stage = 0;
             ring_phase ^= 1u;
@@ -849,15 +905,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * T::kN);
-        const int num_kb = (pr.K + kBK - 1) / kBK;
+        const int high_kb = (pr.K + kBK - 1) / kBK, num_kb = high_kb + pr.low;
         for (int kb = 0; kb < num_kb; ++kb) {
+          const int k0 = kb == high_kb ? 0 : kb * kBK;
           if (!wait<PAIR>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
             fine = false;
             break;
           }
           fence_after();
           const uint32_t sp = smem_addr(ring + stage * (T::kPBytes + T::kQBytes));
-          const bool p_mn = reads_mn<PAIR>(pr.p_in, w.i * T::kM, kb * kBK), q_mn = reads_mn<PAIR>(pr.q_in, w.j * T::kN, kb * kBK);
+          const bool p_mn = reads_mn<PAIR>(pr.p_in, w.i * T::kM, k0), q_mn = reads_mn<PAIR>(pr.q_in, w.j * T::kN, k0);
           const uint64_t dp = operand_desc(sp, p_mn), dq = operand_desc(sp + T::kPBytes, q_mn);
           const uint32_t idesc = T::kIdesc | (p_mn ? 1u << 15 : 0u) | (q_mn ? 1u << 16 : 0u);
           // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
@@ -893,8 +950,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         fine = epilogue<PAIR, kMakeA>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
       else if (w.kind == 1)
         fine = epilogue<PAIR, kMakeB>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
-      else if (pr.D)
+      else if (pr.D && pr.C)
         fine = epilogue<PAIR, kMakeX>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+      else if (pr.D)
+        fine = epilogue<PAIR, kMakeXPlain>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
       else
         fine = epilogue<PAIR, kMakeOut>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
       acc ^= 1;
@@ -953,6 +1012,9 @@ size_t carve_ortho(uint8_t* base, int64_t batch, int m, int n, OrthoArgs* o) {
   for (int i = 0; i < 2; ++i) o->X[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * m * o->ldx));
   o->A = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
   o->Bm = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
+  o->lo_product = p <= kBK;
+  for (int i = 0; i < 2; ++i)
+    o->L[i] = i && !o->lo_product ? o->L[0] : reinterpret_cast<__half*>(take(sizeof(__half) * batch * m * o->ldx));
   return at + 128;
 }
 
@@ -1023,6 +1085,8 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
            held_map(&X[1], g.X[1], g.batch, g.m, g.n, g.ldx, box_rows) &&
            held_map(&A, g.A, g.batch, g.p, g.p, g.ldp, box_rows) && held_map(&Bm, g.Bm, g.batch, g.p, g.p, g.ldp, box_rows);
   };
+  for (int i = 0; g.lo_product && i < 2; ++i)
+    if (!held_map(&maps.L[i], g.L[i], g.batch, g.m, g.n, g.ldx, kRowsP)) return PG_ERR_CUDA;
   if (!encode(maps.X, maps.A, maps.Bm, kRowsP) || (!PAIR && !encode(maps.Xq, maps.Aq, maps.Bmq, Tile<false>::kRowsQ)))
     return PG_ERR_CUDA;
   g.tiles[0] = g.tiles[1] = tiles_of<PAIR>(g.p, g.p, true);

@@ -720,10 +720,14 @@ pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32
  * 2.0315 five steps bring every singular value that started above ~1 % into about [0.7, 1.2].
  *  G    device [batch, m, n], PG_F32 or PG_BF16, aligned to its element
  *  out  device bf16 [batch, m, n], 2-byte aligned; may be G itself when G is bf16
- * The products run on the tensor cores with fp16 operands and fp32 sums: X, A and
- * a I + b A + c A A are stored scaled by 2^10 in fp16 between them (11 significant bits: three
- * more than the result's; the scale puts magnitudes 6e-8 .. 63 into fp16's normal range, where a
- * norm of at most 1 and the usual coefficients keep them below 4).
+ * The products run on the tensor cores with fp16 operands and fp32 sums. Between them A and
+ * a I + b A + c A A are stored scaled by 2^10 in fp16 (11 significant bits: three more than the
+ * result's; the scale puts magnitudes 6e-8 .. 63 into fp16's normal range, where a norm of at most 1
+ * and the usual coefficients keep them below 4), and X as the sum of two such numbers (22 bits;
+ * in the last step of the first alone): what rounds X lies in all singular directions, and those that
+ * G does not have grow a-fold a step. With the usual coefficients and five steps the result is
+ * within 0.002 to 0.0035 of the formulas, relative, 0.0017 of it the bf16 result's rounding, whatever
+ * the rank and the spectrum of G.
  * A zero matrix gives zeros (eps > 0); infinities and NaN in G make its own matrix NaN.
  *  1 <= m, n <= 16384; 0 <= batch <= 4096; 1 <= steps <= 32 (fewer than 2^31 tiles in all);
  *  workspace device, 16-byte aligned, >= pg_orthogonalize_workspace_size bytes, scratch.
