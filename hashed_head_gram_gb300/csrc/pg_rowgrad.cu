@@ -691,6 +691,10 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t row, int c,
   store_out<OUT, COLS>(a.out, at, y);
 }
 
+// This kernel and the join are scheduled before the kernels ahead of them have ended, so what those
+// write (order, sign, parts) is read by coherent loads, which no compiler moves ahead of the wait; the
+// join reads what the sort wrote, whose end every block of this kernel has waited for, from L2.
+//
 // A group of `lanes` consecutive threads per tile of T references and lanes * COLS columns.
 // The loads of 8 summands (fp32: 4) are in flight at a time, and behind them those of the next
 // references' numbers.
@@ -711,20 +715,20 @@ __global__ void __launch_bounds__(kSumThreads, 5)
     if (q0 + kFly <= p1) {  // p0 is a multiple of 8
 #pragma unroll
       for (int k = 0; k < kFly; k += 2) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.order + q0 + k));
+        const uint4 v = *reinterpret_cast<const uint4*>(a.order + q0 + k);
         seg[k] = v.x; ref[k] = v.y; seg[k + 1] = v.z; ref[k + 1] = v.w;
       }
     } else {
 #pragma unroll
       for (int k = 0; k < kFly; ++k) {
-        const uint2 v = __ldg(a.order + min(q0 + k, p1 - 1));
+        const uint2 v = a.order[min(q0 + k, p1 - 1)];
         ref[k] = v.y;
         seg[k] = v.x;  // (past p1: not used)
       }
     }
   };
   numbers(p0);
-  const uint32_t before = p0 > 0 ? __ldg(&a.order[p0 - 1].x) : kNoRow, after = p1 < a.n ? __ldg(&a.order[p1].x) : kNoRow;
+  const uint32_t before = p0 > 0 ? a.order[p0 - 1].x : kNoRow, after = p1 < a.n ? a.order[p1].x : kNoRow;
   if (a.compact) {  // rows past the last distinct one are zero: row p for each position p of the tile
     const float zero[COLS] = {};
     for (uint32_t u = max(p0, a.ctrl->count); u < p1; ++u)
@@ -741,7 +745,7 @@ __global__ void __launch_bounds__(kSumThreads, 5)
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       x[k].load(a.grad, static_cast<int64_t>(a.share == 1 ? ref[k] : ref[k] / a.share) * a.r + c);
-      neg[k] = SIGNED ? __ldg(a.sign + static_cast<int64_t>(ref[k]) * a.sign_bytes + (c >> 3)) >> (c & 7) : 0u;
+      neg[k] = SIGNED ? a.sign[static_cast<int64_t>(ref[k]) * a.sign_bytes + (c >> 3)] >> (c & 7) : 0u;
       sg[k] = seg[k];
     }
     if (q0 + kFly < p1) numbers(q0 + kFly);
@@ -778,7 +782,7 @@ template <int OUT, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
   __shared__ float s_acc[kJoinThreads][COLS];
   __shared__ uint32_t s_long, s_end;
-  if (a.ctrl->done != a.blocks) {
+  if (__ldcg(&a.ctrl->done) != a.blocks) {
     grid_dep_wait();
     return;
   }
@@ -796,7 +800,7 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
       for (int f = 0; f < kFly; ++f) {
 #pragma unroll
         for (int j = 0; j < COLS; ++j) x[f][j] = 0.f;
-        if (k + f * step < end) load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(k + f * step) * 2 * a.r + c, x[f]);
+        if (k + f * step < end) load_now<COLS>(a.parts + static_cast<int64_t>(k + f * step) * 2 * a.r + c, x[f]);
       }
 #pragma unroll
       for (int f = 0; f < kFly; ++f)
@@ -806,9 +810,9 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
   };
   uint32_t row = kNoRow, end = 0;  // the row that starts in this tile and goes on; past the last tile with a part
   if (group < per_block && tile < a.tiles && p1 < a.n) {
-    const uint32_t u = __ldg(&a.order[p1].x), prev = __ldg(&a.order[p1 - 1].x);
-    const uint32_t before = p0 > 0 ? __ldg(&a.order[p0 - 1].x) : kNoRow;
-    const uint32_t next = p1 + T < a.n ? __ldg(&a.order[p1 + T].x) : kNoRow;
+    const uint32_t u = __ldcg(&a.order[p1].x), prev = __ldcg(&a.order[p1 - 1].x);
+    const uint32_t before = p0 > 0 ? __ldcg(&a.order[p0 - 1].x) : kNoRow;
+    const uint32_t next = p1 + T < a.n ? __ldcg(&a.order[p1 + T].x) : kNoRow;
     if (u == prev && u != before && u != a.none) {
       row = u;
       end = tile + 2;
@@ -822,7 +826,7 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
 #pragma unroll
           for (uint32_t f = 1; f <= 8; ++f) {
             const uint64_t at = (static_cast<uint64_t>(k) + f * static_cast<uint64_t>(gap)) * T;
-            held += at < a.n && __ldg(&a.order[at].x) == u;
+            held += at < a.n && __ldcg(&a.order[at].x) == u;
           }
           k += held * gap;
           grow = grow && held == 8;
@@ -844,7 +848,7 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
       s_end = end;
     } else if (c < a.r) {
       float acc[COLS];
-      load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(tile) * 2 * a.r + a.r + c, acc);
+      load_now<COLS>(a.parts + static_cast<int64_t>(tile) * 2 * a.r + a.r + c, acc);
       add(tile + 1, end, 1, acc);
       write_row<OUT, COLS>(a, row, c, acc);
     }
@@ -853,7 +857,7 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
   if (s_long == kNoRow) return;
   float acc[COLS] = {};
   if (c < a.r) {
-    if (group == 0) load_cols<PG_F32, COLS>(a.parts, static_cast<int64_t>(s_long) * 2 * a.r + a.r + c, acc);
+    if (group == 0) load_now<COLS>(a.parts + static_cast<int64_t>(s_long) * 2 * a.r + a.r + c, acc);
     add(s_long + 1 + group, s_end, per_block, acc);
   }
 #pragma unroll
@@ -863,7 +867,7 @@ __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid
     for (int k = 1; k < per_block; ++k)
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] += s_acc[k * lanes + threadIdx.x][j];
-    write_row<OUT, COLS>(a, __ldg(&a.order[(s_long + 1) * T].x), c, acc);
+    write_row<OUT, COLS>(a, __ldcg(&a.order[(s_long + 1) * T].x), c, acc);
   }
 }
 

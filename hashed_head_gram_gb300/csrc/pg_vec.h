@@ -66,7 +66,22 @@ __device__ __forceinline__ void load_cols(const void* __restrict__ base, int64_t
   }
 }
 
-// The same from memory that this kernel writes (no read-only cache).
+// fp32 that an earlier kernel writes while this one already runs, after the wait for its end: coherent
+// loads that stay behind that wait. (The read-only path of load_cols is for what nothing writes
+// during the kernel, and its loads may move.)
+template <int COLS>
+__device__ __forceinline__ void load_now(const float* p, float (&x)[COLS]) {
+  static_assert(COLS == 1 || COLS == 8, "");
+  if constexpr (COLS == 1)
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(x[0]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// The same as load_cols from memory that this kernel writes (no read-only cache).
 template <int DT, int COLS>
 __device__ __forceinline__ void read_cols(const void* base, int64_t at, float (&x)[COLS]) {
 #pragma unroll
