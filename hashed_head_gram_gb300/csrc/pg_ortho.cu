@@ -299,7 +299,8 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 // --------------------------------------------------------------------- norm and scaling
 
 // 8 consecutive values of G as they lie in memory; the loads are volatile so that they stay
-// together, ahead of their uses.
+// together, ahead of their uses. They are coherent ones: the result may lie in G's place, and the
+// launch that reads G may write it.
 template <int DT>
 struct Raw8 {
   float f[DT == PG_F32 ? 8 : 1];
@@ -307,13 +308,15 @@ struct Raw8 {
 
   __device__ __forceinline__ void load(const void* G, int64_t at) {
     if constexpr (DT == PG_F32)
-      asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                   : "l"(static_cast<const float*>(G) + at));
+                   : "l"(static_cast<const float*>(G) + at)
+                   : "memory");
     else
-      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
-                   : "l"(static_cast<const uint16_t*>(G) + at));
+                   : "l"(static_cast<const uint16_t*>(G) + at)
+                   : "memory");
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     if constexpr (DT == PG_F32) {
@@ -358,7 +361,7 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[TH
   } else {
     for (int64_t i = lo + threadIdx.x; i < hi; i += THREADS) {
       float x[1];
-      load_cols<DT, 1>(g.G, base + i, x);
+      read_cols<DT, 1>(g.G, base + i, x);
       add(x[0]);
     }
   }
@@ -461,7 +464,7 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           float y[1] = {0.f};
-          if (j + k < static_cast<uint32_t>(g.n)) load_cols<DT, 1>(g.G, (r0 + r) * g.n + j + k, y);
+          if (j + k < static_cast<uint32_t>(g.n)) read_cols<DT, 1>(g.G, (r0 + r) * g.n + j + k, y);
           x[k] = y[0];
         }
         store(v, x);

@@ -45,3 +45,15 @@ def test_the_join_reads_parts_after_its_wait():
     before = text[:text.rindex("grid_dep_wait()")]
     assert "a.parts" not in before[:before.index("auto add =")] and before.count("add(") == 0
     assert READ_ONLY.search(body("pg_vec.h", "load_now")) is None
+
+
+@pytest.mark.parametrize("name", ["norm_part", "scale_rows"])
+def test_orthogonalize_reads_g_coherently(name):
+    # the result may lie in G's place, written by the launch that reads G
+    assert not READ_ONLY.search(body("pg_ortho.cu", name))
+
+
+def test_orthogonalize_wide_loads_are_coherent():
+    text = open(os.path.join(CSRC, "pg_ortho.cu")).read()
+    raw8 = text[text.index("struct Raw8"):text.index("void norm_part")]
+    assert "ld.global" in raw8 and not READ_ONLY.search(raw8)
