@@ -87,3 +87,56 @@ def test_one_direction_per_matrix_of_a_batch(cuda):
     want = ortho_reference(G, 5)
     for i in range(4):
         assert rel(out[i], want[i]) <= FORMULA, i
+
+
+# From 4,194,304 values on, norm and scaling are launches of their own, with other blocks and shares.
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("b,m,n,shift", [(5, 2560, 1280, 0), (1, 2048, 2048, 0), (1, 2047, 2049, 0), (3, 1201, 1203, 0),
+                                         (400, 104, 104, 0), (700, 79, 77, 0), (2, 1500, 1400, 1), (2, 1400, 1504, 4)])
+def test_large_batches(cuda, b, m, n, shift, dtype):
+    # 400 and 700 matrices: one part each, and blocks of the scaling that cross matrices; an odd n or an
+    # address off by `shift` values: a column at a time
+    assert b * m * n >= 4 << 20 or (b, m, n) == (1, 2047, 2049)  # one value short: the single launch
+    pg = _pg()
+    G = offset_view(gaussian(torch.Generator().manual_seed(b + m * n), b, m, n, dtype, cuda), shift)
+    out = offset_view(torch.full((b, m, n), float("nan"), dtype=BF16, device=cuda), shift)
+    ws = torch.full((pg.orthogonalize_workspace_size(b, m, n),), 0xA5, dtype=torch.uint8, device=cuda)
+    pg.orthogonalize(G, out, ws)
+    assert pg.device_error() == 0
+    assert rel(out, held_reference(G)) <= SAME_PLACES
+    assert rel(out, ortho_reference(G, 5)) <= FORMULA
+
+
+@pytest.mark.parametrize("b,m,n", [(5, 1000, 1000), (3, 1201, 1203), (2, 300, 200), (1, 131, 129)])
+def test_in_place(cuda, b, m, n):
+    pg = _pg()
+    G = gaussian(torch.Generator().manual_seed(b), b, m, n, BF16, cuda)
+    want = run_ortho(pg, G)
+    ws = torch.empty(pg.orthogonalize_workspace_size(b, m, n), dtype=torch.uint8, device=cuda)
+    for _ in range(3):
+        buf = G.clone()
+        pg.orthogonalize(buf, buf, ws)
+        assert torch.equal(buf, want)
+
+
+def test_large_zero_nan_and_neighbours(cuda):
+    pg = _pg()
+    for n in (1000, 1001):
+        G = gaussian(torch.Generator().manual_seed(8), 5, 1100, n, F32, cuda)
+        G[1] = 0
+        G[2, 3, 4] = math.nan
+        G[3, 1099, n - 1] = math.inf
+        out = run_ortho(pg, G)
+        assert rel(out[0], ortho_reference(G[:1], 5)[0]) <= FORMULA
+        assert bool((out[1] == 0).all())
+        assert bool(out[2].isnan().all()) and bool(out[3].isnan().all())
+        assert rel(out[4], ortho_reference(G[4:], 5)[0]) <= FORMULA
+
+
+@pytest.mark.parametrize("std", [1e-30, 1e30])
+def test_large_of_any_magnitude(cuda, std):
+    G = gaussian(torch.Generator().manual_seed(9), 3, 1200, 1200, F32, cuda, std)
+    out = run_ortho(_pg(), G, eps=0.0)
+    assert rel(out, held_reference(G, eps=0.0)) <= SAME_PLACES
