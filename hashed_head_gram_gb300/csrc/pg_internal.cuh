@@ -108,6 +108,10 @@ pg_status launch_small_rows_bf16(int N, int Din, int d, int M, int gate_kind, co
                                  const void* x, const void* h, const float* gamma_h, const float* gamma_k, void* out,
                                  float* partials, float* vpart, cudaStream_t stream);
 
+// pg_selftest_training_waits: the waits of pg_orthogonalize, one after the other, on zeroed `counters` (256 bytes);
+// gave_up[0] and [1] become 1 (the grid barrier, the wait for stored tiles). One launch.
+pg_status launch_ortho_wait_selftest(void* counters, int* gave_up, cudaStream_t stream);
+
 // W == NULL: out = e, or x + g e for the scalar gate, over n elements of dtype (n % 8 == 0,
 // 16-byte aligned). One launch.
 pg_status launch_identity_gate(int64_t n, int dtype, int gate_kind, const void* e, const void* x, float g,

@@ -995,6 +995,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_free<PAIR>(tmem, T::kTmemCols);
 }
 
+// Block 0 of two waits for the other at the grid barrier and for a tile that nothing stores.
+__global__ void __launch_bounds__(64) ortho_wait_selftest_kernel(OrthoCtrl* ctrl, int* gave_up, int* err_word) {
+  __shared__ Bars<1> bars;
+  if (blockIdx.x != 0) return;
+  if (threadIdx.x == 0) bars.abort = 0;
+  __syncthreads();
+  OrthoArgs g = {};
+  g.ctrl = ctrl;
+  g.err_word = err_word;
+  uint32_t phase = 0;
+  if (!grid_meet(g, &bars, &phase) && threadIdx.x == 0) gave_up[0] = 1;
+  if (threadIdx.x == 0 && !wait_stored(g, 0, 1u, &bars.abort)) {
+    gave_up[1] = 1;
+    atomicOr(err_word, kErrOrtho);
+  }
+}
+
 // ------------------------------------------------------------------------------ host side
 
 size_t ctrl_bytes(int64_t batch) { return offsetof(OrthoCtrl, stored) + batch * sizeof(uint32_t); }
@@ -1156,6 +1173,12 @@ bool use_pairs(const OrthoArgs& g, int sms) {
 }
 
 }  // namespace
+
+pg_status launch_ortho_wait_selftest(void* counters, int* gave_up, cudaStream_t stream) {
+  ortho_wait_selftest_kernel<<<2, 64, 0, stream>>>(static_cast<OrthoCtrl*>(counters), gave_up, device_error_word());
+  return after_launch(1);
+}
+
 }  // namespace pg
 
 using namespace pg;

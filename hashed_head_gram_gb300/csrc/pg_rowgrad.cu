@@ -125,8 +125,10 @@ size_t carve(uint8_t* base, int64_t n, int r, bool hashed, SortBuffers* b) {
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The G sorting blocks of the grid; false after a time limit of about one second (then every block
-// gives up, since the count it waits for is not reached). `phase` counts the barriers.
+// The G sorting blocks of the grid; false after a time limit of about one second. `phase` counts the
+// barriers. A block that arrives after others have given up still completes the count and goes on:
+// what they wrote before they arrived is all that it reads, and at its next barrier it gives up too. Its
+// writes stay in range, and as `done` falls short of G the later kernels write nothing.
 __device__ __forceinline__ bool grid_barrier(uint32_t G, uint32_t* counter, uint32_t* phase, int* s_ok, int* err_word) {
   *phase += 1;
   __syncthreads();
@@ -885,6 +887,18 @@ SumFn join_fn(int out) {
   return out == PG_F32 ? rowgrad_join_kernel<PG_F32, COLS> : rowgrad_join_kernel<PG_BF16, COLS>;
 }
 
+// One block of two arrives at the barrier, gives up and leaves without raising `done`, as a sorting
+// block does.
+__global__ void __launch_bounds__(64) grad_wait_selftest_kernel(SortCtrl* ctrl, int* gave_up, int* err_word) {
+  __shared__ int s_ok;
+  uint32_t phase = 0;
+  if (!grid_barrier(2, &ctrl->barrier, &phase, &s_ok, err_word)) {
+    if (threadIdx.x == 0) *gave_up = 1;
+    return;
+  }
+  if (threadIdx.x == 0) atomicAdd(&ctrl->done, 1u);
+}
+
 // Sorts the references and writes the sums. n >= 1, in `groups` groups; `keys` the largest key.
 template <bool HASHED>
 pg_status row_gradients(const RefSource& src, uint32_t n, uint32_t groups, uint32_t keys, SumArgs a, int in, int out, void* workspace,
@@ -1105,4 +1119,39 @@ extern "C" pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* to
     }
   }
   return row_gradients<true>(src, n, groups, keys, a, grad_dtype, out_dtype, workspace, rows_out, count_out, stream);
+}
+
+// Layout of the scratch: see pg.h. The sums and the join would add the zeros there into `sums` if they did not
+// see that the sort did not finish; sizes and numbers are such that this too stays within both.
+extern "C" pg_status pg_selftest_training_waits(void* scratch, float* sums, pg_stream_t stream) {
+  if (!scratch || !sums) return PG_ERR_NULL;
+  if (!aligned(scratch, 128) || !aligned(sums, 32)) return PG_ERR_ALIGN;
+  if (device_cc() != 103) return PG_ERR_DEVICE;
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  cudaError_t e = cudaMemsetAsync(scratch, 0, PG_SELFTEST_SCRATCH, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  int* gave_up = reinterpret_cast<int*>(base);
+  SortCtrl* ctrl = reinterpret_cast<SortCtrl*>(base + 128);  // 256 bytes
+  grad_wait_selftest_kernel<<<1, 64, 0, stream>>>(ctrl, gave_up, device_error_word());
+  pg_status st = after_launch(1);
+  if (st != PG_OK) return st;
+  constexpr int kR = 8, kT = 8, kTiles = 2;
+  SumArgs a = {};
+  a.order = reinterpret_cast<const uint2*>(base + 384);      // 16 x (row 0, reference 0)
+  a.grad = base + 512;                                       // a row of 8 zeros
+  a.parts = reinterpret_cast<float*>(base + 640);            // [2][2][8]
+  a.ctrl = ctrl;
+  a.out = sums;
+  a.n = kTiles * kT;
+  a.share = 1;
+  a.blocks = 2;
+  a.tiles = kTiles;
+  a.none = kNoRow;
+  a.r = kR;
+  a.scale = 1.f;
+  sum_fn<8, false>(PG_F32, PG_F32)<<<1, kSumThreads, 0, stream>>>(a, 1, kT);
+  if ((st = after_launch(1)) != PG_OK) return st;
+  join_fn<8>(PG_F32)<<<1, kJoinThreads, 0, stream>>>(a, 1, kT);
+  if ((st = after_launch(1)) != PG_OK) return st;
+  return launch_ortho_wait_selftest(base + 1024, gave_up + 1, stream);
 }

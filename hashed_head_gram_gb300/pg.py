@@ -169,6 +169,8 @@ def _load():
     L.pg_conv_residual.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, f32, vp, vp]
     L.pg_selftest_bounded_waits.restype = ctypes.c_int
     L.pg_selftest_bounded_waits.argtypes = [vp, vp]
+    L.pg_selftest_training_waits.restype = ctypes.c_int
+    L.pg_selftest_training_waits.argtypes = [vp, vp, vp]
     L.pg_row_copy_window.restype = ctypes.c_int
     L.pg_row_copy_window.argtypes = [u32, ctypes.POINTER(u32)]
     L.pg_row_copy.restype = ctypes.c_int
@@ -550,6 +552,15 @@ def selftest_bounded_waits(zero_word: torch.Tensor, stream=None):
     _check(_lib.pg_selftest_bounded_waits(_ptr(zero_word), _stream(stream)), "pg_selftest_bounded_waits")
 
 
+def selftest_training_waits(scratch: torch.Tensor, sums: torch.Tensor, stream=None):
+    """scratch: a device tensor of 2048 bytes (zeroed by the call); sums: float32 [8]. Afterwards (about
+    3 s on the device) the device error word holds 131072 | 262144 and the first three int32 of scratch
+    are 1 when the training calls' waits gave up as they should; sums is unchanged."""
+    if scratch.numel() * scratch.element_size() < 2048 or sums.dtype != torch.float32 or sums.numel() < 8:
+        raise ValueError("scratch must hold 2048 bytes and sums 8 float32")
+    _check(_lib.pg_selftest_training_waits(_ptr(scratch), _ptr(sums), _stream(stream)), "pg_selftest_training_waits")
+
+
 def row_copy_window(row_bytes: int) -> int:
     w = ctypes.c_uint32()
     _check(_lib.pg_row_copy_window(row_bytes, ctypes.byref(w)), "pg_row_copy_window")
@@ -574,7 +585,7 @@ __all__ = ["PgError", "TableDesc", "table_desc", "table_geometry", "canon_hash",
            "workspace_size", "project_gate", "lookup_project_gate", "gather_project_workspace_size",
            "gather_project_gate", "nf4_quantize", "fp8_quantize", "project_gate_fp8", "project_gate_context_noalloc", "conv_residual",
            "decode_state_size", "DecodeState", "decode_reset", "decode_lookup", "decode_conv_residual",
-           "collision_workspace_size", "collision_counts", "launch_count", "device_error", "selftest_bounded_waits",
+           "collision_workspace_size", "collision_counts", "launch_count", "device_error", "selftest_bounded_waits", "selftest_training_waits",
            "row_copy_window", "row_copy", "lib",
            "FLAT", "ENGRAM", "PAGEGRAM", "F32", "BF16", "NF4", "GATE_NONE", "GATE_SCALAR", "GATE_CONTEXT",
            "HASH_MULXOR", "HASH_TOY", "PG_NO_ROW"]

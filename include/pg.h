@@ -160,6 +160,19 @@ pg_status pg_device_error(int32_t* code, int32_t clear);
 pg_status pg_selftest_bounded_waits(uint32_t* zero_word, pg_stream_t stream);
 
 /*
+ * pg_selftest_training_waits -- the same for the waits of the training calls: the grid barrier of
+ * the gradients' sort, the one of pg_orthogonalize and its wait for stored tiles, each on a counter
+ * that nothing completes, in kernels without copies, tensor-core operations or TMEM. Each gives up
+ * after about one second; a correct run leaves 131072 | 262144 in the device error word. The
+ * gradients' sums and join are then launched behind the sort that did not finish, and write nothing.
+ *  scratch  device, 128-byte aligned, PG_SELFTEST_SCRATCH bytes, zeroed by the call; its first three
+ *           int32 become 1 where the three waits gave up (in the order above)
+ *  sums     device fp32 [8], 32-byte aligned: unchanged by a correct run
+ */
+#define PG_SELFTEST_SCRATCH 2048
+pg_status pg_selftest_training_waits(void* scratch, float* sums, pg_stream_t stream);
+
+/*
  * Table geometry of a descriptor: number of stored rows (the table's first
  * dimension), bytes per row, and the width of e_t (O*K*r, or r for flat).
  * Any out pointer may be NULL. Validates the descriptor (PG_ERR_VERSION,
