@@ -61,6 +61,7 @@ constexpr int kMaxSide = 16384;
 constexpr int kMaxBatch = 4096;
 constexpr float kHold = 1024.f;         // X, A and Bm are stored times 2^10
 constexpr float kUnhold = 1.f / 1024.f;
+constexpr float kUp = 0x1p90f, kDown = 0x1p-90f;
 constexpr int kNormParts = 128;         // partial sums of squares per matrix, at most
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
@@ -330,15 +331,16 @@ struct Raw8 {
   }
 };
 
-// Partial sums of squares, of x, 2^64 x and 2^-64 x: whichever of the three neither overflows
-// nor vanishes gives the norm. Part `part` of matrix `b` is a contiguous share of it.
+// Partial sums of squares, of x, 2^90 x and 2^-90 x: whichever of the three neither overflows
+// nor vanishes gives the norm, for all finite x (the least, 2^-149, squares to 2^-118; 2^28 values
+// below 2^128 sum to less than 2^104). Part `part` of matrix `b` is a contiguous share of it.
 template <int DT, int THREADS>
 __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[THREADS / 32]) {
   const int64_t share = ((g.size + g.parts - 1) / g.parts + 7) / 8 * 8;
   const int64_t lo = part * share, hi = min(g.size, lo + share), base = b * g.size;
   float sum[3] = {};
   auto add = [&](float x) {
-    const float up = x * 0x1p64f, down = x * 0x1p-64f;
+    const float up = x * kUp, down = x * kDown;
     sum[0] = fmaf(x, x, sum[0]);
     sum[1] = fmaf(up, up, sum[1]);
     sum[2] = fmaf(down, down, sum[2]);
@@ -380,8 +382,10 @@ __device__ void norm_part(const OrthoArgs& g, int b, int part, float (*s_sum)[TH
   }
 }
 
-// 2^10 / (|G|_F + eps) of matrix b, by one warp: lane-strided sums and an xor tree, a fixed order.
-__device__ float held_scale(const OrthoArgs& g, int b) {
+// 2^10 / (|G|_F + eps) of matrix b as a product, by one warp: lane-strided sums and an xor tree, a fixed
+// order. The first factor is the power of two that the norm was summed with: the quotient alone
+// leaves fp32's range for norms below 2^-118, and the norm itself can.
+__device__ float2 held_scale(const OrthoArgs& g, int b) {
   const int lane = threadIdx.x & 31;
   float s[3] = {};
   for (int i = lane; i < g.parts; i += 32)
@@ -391,14 +395,15 @@ __device__ float held_scale(const OrthoArgs& g, int b) {
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int o = 16; o; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-  float norm;
-  if (s[0] > 0x1p-60f && s[0] < 0x1p120f)
-    norm = sqrtf(s[0]);
-  else if (s[0] <= 0x1p-60f)
-    norm = sqrtf(s[1]) * 0x1p-64f;
-  else
-    norm = sqrtf(s[2]) * 0x1p64f;  // also NaN and infinities
-  return kHold / (norm + g.eps);
+  float by = 1.f, sum = s[0];
+  if (s[0] <= 0x1p-60f) {
+    by = kUp;
+    sum = s[1];
+  } else if (!(s[0] < 0x1p120f)) {  // also NaN and infinities
+    by = kDown;
+    sum = s[2];
+  }
+  return make_float2(by, kHold / (sqrtf(sum) + g.eps * by));
 }
 
 __device__ __forceinline__ uint32_t two_half(float lo, float hi) {
@@ -415,7 +420,7 @@ __device__ __forceinline__ uint32_t two_left(uint32_t hi, float x0, float x1) {
 // X0: rows of G scaled and rounded into rows of stride ldx, 8 columns at a time. A block owns a
 // contiguous share of the rows of all matrices.
 template <int DT, int THREADS>
-__device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
+__device__ void scale_rows(const OrthoArgs& g, float2* s_scale) {
   const uint32_t per_row = (g.n + 7) / 8;
   const int64_t rows = static_cast<int64_t>(g.batch) * g.m;
   const int64_t lo = rows * blockIdx.x / gridDim.x, hi = rows * (blockIdx.x + 1) / gridDim.x;
@@ -424,22 +429,22 @@ __device__ void scale_rows(const OrthoArgs& g, float* s_scale) {
     const int64_t r1 = min(hi, static_cast<int64_t>(b + 1) * g.m);
     __syncthreads();
     if (threadIdx.x < 32) {
-      const float s = held_scale(g, b);
+      const float2 s = held_scale(g, b);
       if (threadIdx.x == 0) *s_scale = s;
     }
     __syncthreads();
-    const float scale = *s_scale;
+    const float by = s_scale->x, scale = s_scale->y;
     const uint32_t vecs = static_cast<uint32_t>(r1 - r0) * per_row;  // < 2^31: at most m of at most 2048
     auto store = [&](uint32_t v, const float (&x)[8]) {
       const uint32_t r = v / per_row, j = (v - r * per_row) * 8;
       const int64_t at = (r0 + r) * g.ldx + j;
       uint32_t hi[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) hi[k] = two_half(x[2 * k] * scale, x[2 * k + 1] * scale);
+      for (int k = 0; k < 4; ++k) hi[k] = two_half(x[2 * k] * by * scale, x[2 * k + 1] * by * scale);
       *reinterpret_cast<uint4*>(g.X[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if (g.steps == 1) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) hi[k] = two_left(hi[k], x[2 * k] * scale, x[2 * k + 1] * scale);
+      for (int k = 0; k < 4; ++k) hi[k] = two_left(hi[k], x[2 * k] * by * scale, x[2 * k + 1] * by * scale);
       *reinterpret_cast<uint4*>(g.L[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     };
     if (g.g_vec) {  // n % 8 == 0: a row's pieces follow the row before's
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) ortho_norm_kernel(const __gri
 
 template <int DT>
 __global__ void __launch_bounds__(kPrepThreads, 2) ortho_scale_kernel(const __grid_constant__ OrthoArgs g) {
-  __shared__ float s_scale;
+  __shared__ float2 s_scale;
   scale_rows<DT, kPrepThreads>(g, &s_scale);
 }
 
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars<S> bars_s;
   __shared__ float s_sum[3][kThreads / 32];
-  __shared__ float s_scale;
+  __shared__ float2 s_scale;
   uint8_t* s_epi = ring + T::kRing;                       // the epilogue warps' staging
   Bars<S>* bars = &bars_s;
   volatile int* abort = &bars->abort;

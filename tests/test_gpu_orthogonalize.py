@@ -140,3 +140,15 @@ def test_large_of_any_magnitude(cuda, std):
     G = gaussian(torch.Generator().manual_seed(9), 3, 1200, 1200, F32, cuda, std)
     out = run_ortho(_pg(), G, eps=0.0)
     assert rel(out, held_reference(G, eps=0.0)) <= SAME_PLACES
+
+
+@pytest.mark.parametrize("b,m,n", [(2, 80, 120), (3, 1200, 1200)])
+@pytest.mark.parametrize("std", [1e-44, 1e-39, 1e-37, 1e-33, 1e36, 3e37])
+def test_norms_at_the_ends_of_fp32(cuda, b, m, n, std):
+    # subnormal values; 2^10 / norm past fp32's range; norms past it of values in it. Small norms need eps = 0.
+    G = gaussian(torch.Generator().manual_seed(9), b, m, n, F32, cuda, std)
+    assert bool(G.isfinite().all()) and bool((G != 0).any())
+    out = run_ortho(_pg(), G, eps=0.0)
+    assert rel(out, held_reference(G, eps=0.0)) <= SAME_PLACES
+    if std > 1:
+        assert rel(run_ortho(_pg(), G), held_reference(G)) <= SAME_PLACES
