@@ -49,6 +49,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "pg_async.cuh"
 #include "pg_vec.h"
@@ -1204,6 +1205,8 @@ extern "C" pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batc
   if (st != PG_OK) return st;
   if (steps < 1 || steps > 32) return PG_ERR_SHAPE;
   if (!real_dtype(dtype)) return PG_ERR_DTYPE;
+  // a I is held as fp16 times 2^10: infinite from 64 on, whatever G is
+  if (!(std::fabs(a) < 63.f) || !std::isfinite(b) || !std::isfinite(c)) return PG_ERR_UNSUPPORTED;
   if (batch == 0) return PG_OK;
   if (!G || !out) return PG_ERR_NULL;
   if (!aligned(G, dtype_bytes(dtype)) || !aligned(out, 2) || !aligned(workspace, 16)) return PG_ERR_ALIGN;

@@ -741,6 +741,8 @@ pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32
  * G does not have grow a-fold a step. With the usual coefficients and five steps the result is
  * within 0.002 to 0.0035 of the formulas, relative, 0.0017 of it the bf16 result's rounding, whatever
  * the rank and the spectrum of G.
+ * Coefficients have to keep the entries of X, A and a I + b A + c A A below 64: what reaches 64 becomes
+ * infinite, and the result of its matrix infinite or NaN. |a| >= 63 and coefficients that are not finite are PG_ERR_UNSUPPORTED.
  * A zero matrix gives zeros (eps > 0); infinities and NaN in G make its own matrix NaN.
  *  1 <= m, n <= 16384; 0 <= batch <= 4096; 1 <= steps <= 32 (fewer than 2^31 tiles in all);
  *  workspace device, 16-byte aligned, >= pg_orthogonalize_workspace_size bytes, scratch.

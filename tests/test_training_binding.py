@@ -1,0 +1,30 @@
+"""The training calls' host side (no GPU needed): coefficients, the binding's names and types."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+UNSUPPORTED, DEVICE = 6, 10
+P = ctypes.c_void_p(1 << 20)   # never touched: every call here ends in its host checks
+
+needs_no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where nothing can launch")
+
+
+@pytest.fixture(scope="module")
+def pg():
+    from hashed_head_gram_gb300.build import build
+    build()
+    from hashed_head_gram_gb300 import pg as mod
+    return mod
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("coeffs,want", [
+    ((3.4445, -4.7750, 2.0315), DEVICE), ((62.9, -1.0, 0.0), DEVICE), ((-62.9, 1.0, 0.0), DEVICE),
+    ((3.0, -4.0, 2.0), DEVICE), ((63.0, 0.0, 0.0), UNSUPPORTED), ((-64.0, 0.0, 0.0), UNSUPPORTED),
+    ((math.nan, 0.0, 0.0), UNSUPPORTED), ((1.0, math.inf, 0.0), UNSUPPORTED), ((1.0, 0.0, math.nan), UNSUPPORTED)])
+def test_orthogonalize_coefficients(pg, coeffs, want):
+    # a I is held in fp16 times 2^10
+    got = pg.lib().pg_orthogonalize(P, 1, 1, 8, 8, 5, *coeffs, 1e-7, 1.0, P, P, 1 << 40, None)
+    assert got == want
