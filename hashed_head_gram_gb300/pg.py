@@ -586,7 +586,8 @@ __all__ = ["PgError", "TableDesc", "table_desc", "table_geometry", "canon_hash",
            "gather_project_gate", "nf4_quantize", "fp8_quantize", "project_gate_fp8", "project_gate_context_noalloc", "conv_residual",
            "decode_state_size", "DecodeState", "decode_reset", "decode_lookup", "decode_conv_residual",
            "collision_workspace_size", "collision_counts", "launch_count", "device_error", "selftest_bounded_waits", "selftest_training_waits",
-           "row_copy_window", "row_copy", "lib",
+           "row_copy_window", "row_copy", "embed", "embed_grad_workspace_size", "embed_grad", "lookup_grad_workspace_size",
+           "lookup_grad", "orthogonalize_workspace_size", "orthogonalize", "lib",
            "FLAT", "ENGRAM", "PAGEGRAM", "F32", "BF16", "NF4", "GATE_NONE", "GATE_SCALAR", "GATE_CONTEXT",
            "HASH_MULXOR", "HASH_TOY", "PG_NO_ROW"]
 

@@ -28,3 +28,13 @@ def test_orthogonalize_coefficients(pg, coeffs, want):
     # a I is held in fp16 times 2^10
     got = pg.lib().pg_orthogonalize(P, 1, 1, 8, 8, 5, *coeffs, 1e-7, 1.0, P, P, 1 << 40, None)
     assert got == want
+
+
+def test_star_import_has_the_training_calls(pg):
+    names = {}
+    exec("from hashed_head_gram_gb300.pg import *", names)
+    for call in ("embed", "embed_grad", "lookup_grad", "orthogonalize"):
+        assert names[call] is getattr(pg, call)
+        if call != "embed":
+            assert names[call + "_workspace_size"] is getattr(pg, call + "_workspace_size")
+    assert names["selftest_training_waits"] is pg.selftest_training_waits
