@@ -615,10 +615,13 @@ def _expect(ok: bool, what: str):
         raise ValueError(what)
 
 
+_ID_TYPES = (torch.int32, torch.uint32)  # uint32 values, in either type
+
+
 def _ids(tokens: torch.Tensor, canon_map: Optional[torch.Tensor], vocab: int, err_index: Optional[torch.Tensor]):
     _expect(tokens.dtype == torch.int32, "tokens must be int32")
-    _expect(canon_map is None or (canon_map.element_size() == 4 and canon_map.numel() >= vocab),
-            "canon_map must hold a 32-bit ID for each of the vocab tokens")
+    _expect(canon_map is None or (canon_map.dtype in _ID_TYPES and canon_map.numel() >= vocab),
+            "canon_map must hold an int32 or uint32 ID for each of the vocab tokens")
     _expect(err_index is None or (err_index.dtype == torch.int32 and err_index.numel() >= 1),
             "err_index must be an int32 tensor")
 
@@ -673,7 +676,7 @@ def lookup_grad(desc: TableDesc, tokens: torch.Tensor, grad_e: torch.Tensor, row
     n, width = B * L * heads, (1 if desc.mode == FLAT else heads) * desc.r
     _ids(tokens, canon_map, desc.vocab, err_index)
     _expect(grad_e.numel() == B * L * width and grad_e.shape[-1] == width, "grad_e must be [B * L, e_width]")
-    _expect(rows_out.element_size() == 4 and rows_out.numel() == n, "rows_out must hold one 32-bit row per read")
+    _expect(rows_out.dtype in _ID_TYPES and rows_out.numel() == n, "rows_out must hold one int32 or uint32 row per read")
     _expect(grads_out.numel() == n * desc.r and grads_out.shape[-1] == desc.r, "grads_out must hold one row of width r per read")
     _expect(count_out.dtype == torch.int32 and count_out.numel() >= 1, "count_out must be an int32 tensor")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -38,3 +38,23 @@ def test_star_import_has_the_training_calls(pg):
         if call != "embed":
             assert names[call + "_workspace_size"] is getattr(pg, call + "_workspace_size")
     assert names["selftest_training_waits"] is pg.selftest_training_waits
+
+
+def test_ids_are_integers(pg):
+    from hashed_head_gram_gb300 import workloads as W
+    tok = torch.zeros(1, 4, dtype=torch.int32)
+    table, out = torch.zeros(10, 8), torch.zeros(4, 8)
+    for bad in (torch.zeros(10), torch.zeros(10, dtype=torch.int64)):
+        with pytest.raises(ValueError, match="canon_map"):
+            pg.embed(tok, table, out, 10, canon_map=bad)
+        with pytest.raises(ValueError, match="canon_map"):
+            pg.embed_grad(tok, out, table, 10, None, canon_map=bad)
+    d = pg.table_desc(W.make_workload(1).tables[0], 1024)
+    rest = (torch.zeros(64, 64), torch.zeros(1, dtype=torch.int32), None)
+    with pytest.raises(ValueError, match="rows_out"):
+        pg.lookup_grad(d, tok, torch.zeros(4, 1024), torch.zeros(64), *rest)
+    for dtype in (torch.int32, torch.uint32):  # accepted: the next check is that they are on a GPU
+        with pytest.raises(ValueError, match="CUDA"):
+            pg.embed(tok, table, out, 10, canon_map=torch.zeros(10, dtype=dtype))
+        with pytest.raises(ValueError, match="CUDA"):
+            pg.lookup_grad(d, tok, torch.zeros(4, 1024), torch.zeros(64, dtype=dtype), *rest)
