@@ -11,11 +11,13 @@ IDs, n-grams, hashes and rows, gather + sign + concat (pg_gather_sign_concat), t
 W_V + 4 W_K projection with the RMSNorm-sigmoid gate (tcgen05; pg_project_gate), the
 causal depthwise conv + SiLU + residual into the 4 branch states (pg_conv_residual). The
 other four workloads are measured in the same run (same method, at least 100 timed
-steps) and reported under "workloads": the tiny fp32 tables, the PageGram 200M bf16
+steps) and summarised under "workloads": the tiny fp32 tables, the PageGram 200M bf16
 table (lookup + projection + scalar gate in one launch, pg_gather_project_gate), the
 Engram-style 200M table and the 20B NF4 table (the lookup alone).
 
-Rank 0 prints one JSON line. Under torchrun each rank runs its own batch (seeded by
+Rank 0 prints one JSON line of at most LINE_BYTES to standard output, and all of what was
+measured (every kernel, path and workload, as JSON behind "bench record: ") to standard error.
+Under torchrun each rank runs its own batch (seeded by
 rank; no collective on the data path) and the timing is the max over ranks.
 --impl reference times the CPU oracle on the host cores instead (rank 0 only).
 --kernel runs one kernel at a time on a workload's shapes (timing and profiling).
@@ -43,6 +45,7 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 FP32_FFMA_TFLOPS = 152 * 128 * 2 * 2.07e9 / 1e12
 FP8_OVER_BF16 = 4.5 / 2.25     # nominal dense FP8 / bf16 tensor rates of GB300
 ALL_WORKLOADS = (1, 2, 3, 4, 5)
+LINE_BYTES = 2500              # of the JSON line: what keeps the end of an output keeps all of it
 EXTRA_MIN_STEPS = 100          # timed steps of the workloads besides the headline
 
 # Nominal GB300 figures, reported beside the measured peaks: HBM3e 7.9 TB/s, dense bf16
@@ -845,6 +848,24 @@ def measure_workload(cfg, args, dev, rank, world, steps, headline):
     return out
 
 
+def short_line(line):
+    """The JSON line of a whole record: every required key as it is, of the rest each kernel's time
+    and each workload's rate."""
+    keep = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+            "vs_baseline", "dtype", "data", "config", "gpu_launches", "clocks", "path", "wall_s_timed_loop")
+    out = {k: line[k] for k in keep if k in line}
+    out["e2e"] = {k: v for k, v in line["e2e"].items() if k != "how"}
+    out["roofline"] = {k: v for k, v in line["roofline"].items()
+                       if k in ("bound", "kernel", "achieved", "peak", "unit", "frac", "frac_nominal", "traffic")}
+    out["kernels_ms"] = {name: k["ms"] for name, k in line["kernels"].items()}
+    if "workloads" in line:
+        out["workloads"] = {cfg: {"value": w["value"], "ms_per_step": w["ms_per_step"], "e2e": w["e2e"]["value"],
+                                  "frac": w["roofline"]["frac"]} for cfg, w in line["workloads"].items()}
+    if line.get("cpu_baseline"):
+        out["cpu_baseline"] = {k: line["cpu_baseline"][k] for k in ("value", "unit", "cores", "kind", "cpu_model")}
+    return out
+
+
 def run_gpu(args):
     import torch
 
@@ -882,7 +903,8 @@ def run_gpu(args):
             line["cpu_baseline"] = cpu.get(args.config)
             for cfg in args.extra:
                 extras[str(cfg)]["cpu_baseline"] = cpu.get(cfg)
-        print(json.dumps(line), flush=True)
+        print("bench record: " + json.dumps(line), file=sys.stderr, flush=True)
+        print(json.dumps(short_line(line)), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
