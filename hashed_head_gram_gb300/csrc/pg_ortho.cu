@@ -19,9 +19,11 @@
 // one of A's own size), and the last step takes hi alone (its rounding grows a-fold at most).
 // The other steps' X <- Bm (hi + lo) is Bm hi + a lo, the addend in the epilogue: Bm differs from a I
 // where X has directions, and there lo is a rounding that does not grow. Where Bm is one k-block
-// deep (p <= 128), Bm lo is one more k-block and is taken whole. Relative to the formulas the results
-// are 0.0020-0.0028 off, of which 0.0017 are the bf16 result's own rounding (0.0020 of Gaussian
-// matrices with hi alone; with Bm lo at every size the products would take half as long again).
+// deep (p <= 128), Bm lo is one more k-block and is taken whole, as fast (128 x 1024: 80 us both ways).
+// Relative to the formulas the results are 0.0018-0.0035 off, of which 0.0017 are the bf16 result's own
+// rounding, over ranks from 1 to full, spectra over up to six decades and sides from 24 to 2560. It costs
+// 5 % of a small call and 12 % of the largest (256 x 1024: 80 -> 84 us, five 2560 x 1280: 318 -> 355);
+// Bm lo at every size would add half to the products instead.
 //
 // One cooperative launch does the whole update (large batches: norm and scaling before it): norm,
 // scaling, and 3 * steps products on the tensor cores. The tiles of all products stand in one list,
@@ -35,13 +37,14 @@
 //   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
 //
 // Bound by the tensor cores where the tiles fill them: five 2560 x 1280 matrices need 367 GFLOP
-// (189 us at the measured bf16 rate) and take 320 us, 0.59 of that rate. A step takes 51 us, all
-// that is there once 49 (norm 13, scaling 14, launches, the first fill, the last epilogue). A k-block
-// takes 0.65 us (the rate of a large library product), 41 us of a step; the rest of it is the chain:
-// 75 tiles of A, 75 of Bm and 250 of X on 76 CTA pairs, each
-// product's first loads behind the last stores of the one before. One 768 x 1024 matrix (11 GFLOP)
-// takes 104 us for 15 products: 7 us each of loads from L2 (48 KB a k-block and SM at some 90 GB/s),
-// the first copy, the last epilogue and the counter.
+// (189 us at the measured bf16 rate) and take 355-365 us, 0.52 of that rate: one step 104 us (of them
+// norm 14, scaling 14), the second 58 more, each further one 68. A k-block takes 0.65 us (the rate of a
+// large library product), 41 us of a step; 9 are the low part of X in the epilogue (57 us a step
+// without reading and writing it); the rest is the chain: 75 tiles of A, 75 of Bm and 250 of X on 76
+// CTA pairs, each product's first loads behind the last stores of the one before. One 768 x 1024 matrix
+// (11 GFLOP) takes 109 us for 15 products, 31 the first step and 19.6 each further one: 7 us a product of
+// loads from L2 (48 KB a k-block and SM at some 90 GB/s), the first copy, the last epilogue and the
+// counter.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -67,7 +70,8 @@ constexpr int kNormParts = 128;         // partial sums of squares per matrix, a
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 // A k-block is 128 deep: with 64 the waits, copies and commits that a block costs its two
-// issuing threads, and not the tensor core, set the pace (1280 x 2560: 45 us a step, 41 with 128).
+// issuing threads, and not the tensor core, set the pace (1280 x 2560, X in one part: 45 us a step, 41
+// with 128).
 constexpr int kBK = 128;
 constexpr int kLine = 64;               // fp16 of a 128-byte line: the inner extent of a TMA box
 constexpr int kRowsP = 128;             // rows of P that a CTA stages
@@ -1059,8 +1063,8 @@ bool held_map(CUtensorMap* map, const void* ptr, int batch, int rows, int cols, 
 
 constexpr int kMaxDevices = 64;
 // From this many values on, norm and scaling are launches of their own, with more threads an SM
-// than the products leave them: 5 x 2560 x 1280 366 -> 350 us, 1280 x 2560 213 / 213, and below the
-// two launches cost more than they save (768 x 1024 113 -> 117).
+// than the products leave them: 5 x 2560 x 1280 366 -> 355 us, and below the two launches cost more
+// than they save (1280 x 2560 221 -> 225, 768 x 1024 110 -> 115).
 constexpr int64_t kPrepareFrom = 4 << 20;
 
 // Units (CTAs, or CTA pairs) of the kernel that are resident at once on the current device.
@@ -1158,8 +1162,8 @@ pg_status launch_ortho(OrthoArgs g, cudaStream_t stream) {
 // unit walks (those of one matrix alone, product after product, or all of them spread evenly,
 // whichever is more) at 0.62 us each (a pair's MMAs) against 0.53 us (a single CTA's 48 KB from L2),
 // and 6.4 us more for a pair's pipeline to fill and empty three times. Measured over 5 steps, pair
-// and single, in us: 768 x 1024 150 / 113, 4 of them 161 / 142; 1280 x 1280 184 / 169; 1280 x 2560
-// 217 / 223; 5 of 640 x 1280 164 / 145.
+// and single, in us: 768 x 1024 158 / 110, 4 of them 166 / 140; 1280 x 1280 189 / 166; 1280 x 2560
+// 222 / 222; 5 of 640 x 1280 169 / 145; 5 of 2560 x 1280 356 / 696.
 bool use_pairs(const OrthoArgs& g, int sms) {
   const int q = std::max(g.m, g.n);
   auto step = [&](bool pair) {

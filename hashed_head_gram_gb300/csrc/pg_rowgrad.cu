@@ -19,12 +19,12 @@
 //      and leaves the sums of the others for
 //   3. rowgrad_join_kernel, which adds the parts of a row that crosses tiles, in their order.
 //
-// The floor is the gradient read once and the output written once: 407 MB, 60 us for the million
-// reads of 64 columns. The sums alone take 71 us (372 MB through DRAM while they run, 66 % of its
-// peak: random 128-byte reads, 16-byte loads 8 deep in 5 blocks of 128 threads an SM; 6 blocks
-// spill, 24 % slower; tiles of 16 references make the embedding's calls 6 and 13 % slower, of 64
-// this one 8 %, the other calls within 4 %), and the sort comes before them: 155 us in all. The
-// embedding's sort runs on 32 SMs for 65,536 tokens while the other blocks zero the gradient.
+// The floor is the gradient read once and the output written once: 407 MB, 61 us for the million
+// reads of 64 columns. The sums alone take 71 us (372 MB through DRAM while they run, 0.78 of the
+// measured copy rate: random 128-byte reads, 16-byte loads 8 deep in 5 blocks of 128 threads an SM, where
+// the signed bf16 to fp32 instance spills 28 bytes; 6 blocks spill more, 24 % slower; tiles of 16 references make the embedding's calls 6 and 13 % slower, of 64
+// this one 8 %, the other calls within 4 %), and the sort comes before them: 155 us in all, so it is the
+// whole distance to the floor. The embedding's sort runs on 32 SMs for 65,536 tokens while the other blocks zero the gradient.
 #include "pg_async.cuh"
 #include "pg_hash.cuh"
 #include "pg_vec.h"
@@ -779,7 +779,9 @@ __global__ void __launch_bounds__(kSumThreads, 5)
 
 // Rows that cross tiles: the tile a row starts in adds its parts. A group of lanes per tile, as
 // above; a row over more tiles than a block has groups is added by the whole block, group k
-// taking every per_block-th part (at most one such row starts in a block's tiles).
+// taking every per_block-th part (at most one such row starts in a block's tiles). Of the kFly parts
+// that a round reads about two are in flight: each load has a bound check of its own, and the compiler
+// adds behind it (34 registers).
 template <int OUT, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) rowgrad_join_kernel(const __grid_constant__ SumArgs a, int lanes, int T) {
   __shared__ float s_acc[kJoinThreads][COLS];
