@@ -7,8 +7,9 @@
 // three products of 2 p p q, 2 p p p and 2 p p q operations, the symmetric ones half of that.
 // X stays in G's orientation: where a product needs its columns as the long rows of an
 // operand, the tensor core reads the tile "MN-major" (the descriptor's transpose), and since
-// Bm holds a I the last product has nothing to add. The tiles of A and Bm below the diagonal
-// are neither computed nor stored: an operand that needs one reads its mirror image MN-major.
+// Bm holds a I the last product has only what rounding left (below) to add. The tiles of A and
+// Bm below the diagonal are neither computed nor stored: an operand that needs one reads its
+// mirror image MN-major.
 //
 // Between the products X, A and Bm are held as fp16 scaled by 2^10 (pg.h): 11 significant
 // bits, against the 8 of the bf16 result. That is enough for A and Bm: they multiply X, so their
@@ -19,11 +20,16 @@
 // one of A's own size), and the last step takes hi alone (its rounding grows a-fold at most).
 // The other steps' X <- Bm (hi + lo) is Bm hi + a lo, the addend in the epilogue: Bm differs from a I
 // where X has directions, and there lo is a rounding that does not grow. Where Bm is one k-block
-// deep (p <= 128), Bm lo is one more k-block and is taken whole, as fast (128 x 1024: 80 us both ways).
-// Relative to the formulas the results are 0.0018-0.0035 off, of which 0.0017 are the bf16 result's own
-// rounding, over ranks from 1 to full, spectra over up to six decades and sides from 24 to 2560. It costs
-// 5 % of a small call and 12 % of the largest (256 x 1024: 80 -> 84 us, five 2560 x 1280: 318 -> 355);
-// Bm lo at every size would add half to the products instead.
+// deep (p <= 128), Bm lo is one more k-block and is taken whole, as fast (128 x 1024: 79 us both ways).
+// The diagonals of A and Bm keep fp32: where X's singular values are near one another (a side many times
+// the other) A and Bm are nearly multiples of I, their diagonals' roundings do not average out, and a step
+// stretches them up to fivefold (0.0029 off at 32 x 984 without, 0.0018 with). Their products' epilogues
+// store what rounding left of A's diagonal and the ratio that rounding Bm's changed; Bm's diagonal gets the
+// former's share, b + 2 c A_ii of it, and X's rows (X Bm: columns) are scaled by the ratio.
+// Relative to the formulas the results are 0.0017-0.0028 off, of which 0.0017 are the bf16 result's own
+// rounding, over ranks from 1 to full, spectra over up to six decades and sides from 24 to 2560. The low
+// part and the diagonals cost 3 % of a small call and 13 % of the largest (256 x 1024: 80 -> 82 us, five
+// 2560 x 1280: 316 -> 358); Bm lo at every size would add half to the products instead.
 //
 // One cooperative launch does the whole update (large batches: norm and scaling before it): norm,
 // scaling, and 3 * steps products on the tensor cores. The tiles of all products stand in one list,
@@ -37,12 +43,12 @@
 //   warps 2..9  epilogue: tcgen05.ld, the sum of the three terms, fp16 (or the bf16 result)
 //
 // Bound by the tensor cores where the tiles fill them: five 2560 x 1280 matrices need 367 GFLOP
-// (189 us at the measured bf16 rate) and take 355-365 us, 0.52 of that rate: one step 104 us (of them
+// (189 us at the measured bf16 rate) and take 350-366 us, 0.53 of that rate: one step 104 us (of them
 // norm 14, scaling 14), the second 58 more, each further one 68. A k-block takes 0.65 us (the rate of a
 // large library product), 41 us of a step; 9 are the low part of X in the epilogue (57 us a step
 // without reading and writing it); the rest is the chain: 75 tiles of A, 75 of Bm and 250 of X on 76
 // CTA pairs, each product's first loads behind the last stores of the one before. One 768 x 1024 matrix
-// (11 GFLOP) takes 109 us for 15 products, 31 the first step and 19.6 each further one: 7 us a product of
+// (11 GFLOP) takes 108 us for 15 products, 31 the first step and 19.4 each further one: 7 us a product of
 // loads from L2 (48 KB a k-block and SM at some 90 GB/s), the first copy, the last epilogue and the
 // counter.
 #include <cuda.h>
@@ -53,6 +59,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "pg_async.cuh"
 #include "pg_vec.h"
@@ -94,7 +101,7 @@ struct Tile {
   static constexpr uint32_t kIdesc =                   // kind::f16: fp32 sums, fp16 operands
       (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
   static constexpr size_t kRing = static_cast<size_t>(kStages) * (kPBytes + kQBytes);
-  static constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kStageBytes;
+  static constexpr size_t kSmem = 1024 + kRing + kEpiWarps * (kStageBytes + kChunkN * sizeof(float));
 };
 
 struct OrthoCtrl {
@@ -109,6 +116,8 @@ struct OrthoArgs {
   OrthoCtrl* ctrl;
   float* partial;            // [batch][parts][3]
   __half *X[2], *A, *Bm;     // [batch][m][ldx], [batch][p][ldp]
+  float2* dA;                // [batch][ldp] A's diagonal as held, and what rounding left of it (times 2^10)
+  float* rB;                 // [batch][ldp] Bm's diagonal over what is held of it
   __half* L[2];              // what X's rounding to fp16 left, as X; one buffer unless lo_product
   int* err_word;
   int64_t size;              // m n
@@ -637,9 +646,15 @@ __device__ __forceinline__ bool wait_stored(const OrthoArgs& g, int b, uint32_t 
   }
 }
 
+// The producer tells the epilogue's warps, tile by tile, that what the tile needs is stored: they load their
+// addends and factors while the tile's products run. It is at most the ring's stages and the two
+// accumulators ahead of them, fewer tiles than there are barriers.
+constexpr int kReady = 16;
+static_assert(kReady > Tile<false>::kStages + 4 && kReady > Tile<true>::kStages + 4, "");
+
 template <int S>
 struct Bars {
-  uint64_t full[S], empty[S], acc_full[2], acc_empty[2], done;
+  uint64_t full[S], empty[S], acc_full[2], acc_empty[2], ready[kReady], done;
   uint32_t tmem;
   int abort, ok;
 };
@@ -682,10 +697,11 @@ enum Kind { kMakeA, kMakeB, kMakeX, kMakeXPlain, kMakeOut };  // kMakeXPlain: wi
 // A warp takes 32 rows of a tile (its TMEM lanes) and half of its columns, in chunks. TMEM gives
 // a lane one row; global memory wants neighbouring lanes on one row. So a chunk passes through
 // the warp's shared memory, C the same way in: lane-per-row accesses to global memory (32 lines
-// each) took half of the kernel's time. False once a wait gave up.
-template <bool PAIR, int KIND, int S>
+// each) took half of the kernel's time. TALL: X Bm, whose columns are scaled by Bm's ratios; else its
+// rows. False once a wait gave up.
+template <bool PAIR, int KIND, bool TALL, int S>
 __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, const Work& w, Bars<S>* bars, uint8_t* s_epi,
-                                         uint32_t tmem, uint32_t rank, int acc, uint32_t acc_phase) {
+                                         uint32_t tmem, uint32_t rank, int acc, uint32_t acc_phase, uint32_t nth) {
   using T = Tile<PAIR>;
   constexpr int kC = T::kChunkN, kPieces = kC / 8, kSide = 32 / kPieces;  // 16-byte pieces a row; rows an access covers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -697,6 +713,8 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
   const int lr = lane / kPieces, lc = lane % kPieces;    // this lane's row (of kSide) and piece in a coalesced access
   const float alpha = KIND == kMakeOut ? pr.alpha * g.scale * kUnhold : pr.alpha;
   constexpr bool kAdds = KIND == kMakeB || KIND == kMakeX;
+  constexpr bool kTimesB = KIND != kMakeA && KIND != kMakeB;
+  float* s_col = reinterpret_cast<float*>(s_epi + kEpiWarps * T::kStageBytes) + (warp - 2) * kC;
   const int b = w.b, i = w.i, j = w.j;
   const int row0 = i * T::kM + static_cast<int>(rank) * kRowsP + quarter * 32;
   const int col0 = j * T::kN + half * (T::kN / 2);
@@ -711,9 +729,19 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
         cw[k] = __ldcg(reinterpret_cast<const uint4*>(pr.C + at + static_cast<int64_t>(kSide * k) * pr.ldD + ch * kC));
     }
   };
+  if (KIND != kMakeA &&  // (which needs nothing but its product)
+      !__all_sync(0xffffffffu, wait<false>(smem_addr(&bars->ready[nth % kReady]), nth / kReady & 1u, &bars->abort)))
+    return false;
+  if (kAdds) load_c(0);
+  const bool on_diag = row0 >= col0 && row0 < col0 + T::kN / 2;  // 32 rows and columns of it
+  float2 d = make_float2(0.f, 0.f);
+  if (KIND == kMakeB && on_diag && row0 + lane < pr.M) d = __ldcg(g.dA + static_cast<int64_t>(b) * g.ldp + row0 + lane);
+  const float row_alpha = kTimesB && !TALL && row0 + lane < pr.M
+                              ? alpha * __ldcg(g.rB + static_cast<int64_t>(b) * g.ldp + row0 + lane) : alpha;
+  auto load_ratio = [&](int c) { return c + lane < pr.N ? __ldcg(g.rB + static_cast<int64_t>(b) * g.ldp + c + lane) : 0.f; };
+  float ratio = kTimesB && TALL ? load_ratio(col0) : 0.f;
   if (!__all_sync(0xffffffffu, wait<PAIR>(smem_addr(&bars->acc_full[acc]), acc_phase, &bars->abort))) return false;
   fence_after();
-  if (kAdds) load_c(0);  // (C is there: the tile's loads waited for it)
 #pragma unroll 1
   for (int ch = 0; some && ch < T::kChunks; ++ch) {
     const int c0 = col0 + ch * kC;
@@ -727,12 +755,27 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) *piece(lr + kSide * k, lc) = cw[k];
       if (ch + 1 < T::kChunks) load_c(ch + 1);
-      __syncwarp();
     }
+    if (kTimesB && TALL) {
+      s_col[lane] = alpha * ratio;
+      if (ch + 1 < T::kChunks) ratio = load_ratio(c0 + kC);
+    }
+    if (kAdds || (kTimesB && TALL)) __syncwarp();
     tmem_wait(r);
     float x[kC];
+    if constexpr (kTimesB && TALL) {
 #pragma unroll
-    for (int k = 0; k < kC; ++k) x[k] = alpha * __uint_as_float(r[k]);
+      for (int k = 0; k < kC; k += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(s_col + k);
+        x[k] = f.x * __uint_as_float(r[k]);
+        x[k + 1] = f.y * __uint_as_float(r[k + 1]);
+        x[k + 2] = f.z * __uint_as_float(r[k + 2]);
+        x[k + 3] = f.w * __uint_as_float(r[k + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kC; ++k) x[k] = row_alpha * __uint_as_float(r[k]);
+    }
     if (kAdds) {
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
@@ -745,11 +788,6 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
           x[8 * k + e + 1] = fmaf(pr.beta, f.y, x[8 * k + e + 1]);
         }
       }
-      if (KIND == kMakeB && c0 < row0 + 32 && row0 < c0 + kC) {  // the diagonal crosses the chunk
-#pragma unroll
-        for (int k = 0; k < kC; ++k)
-          if (c0 + k == row0 + lane) x[k] += pr.diag;
-      }
     }
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {  // two columns a word: fp16, or the result in bf16
@@ -757,6 +795,27 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Product& pr, 
       *piece(lane, k) = KIND == kMakeOut
           ? make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]))
           : make_uint4(two_half(v[0], v[1]), two_half(v[2], v[3]), two_half(v[4], v[5]), two_half(v[6], v[7]));
+    }
+    if ((KIND == kMakeA || KIND == kMakeB) && c0 == row0) {  // the chunk's diagonal is the matrix's
+      float t[kC / 2];
+#pragma unroll
+      for (int k = 0; k < kC / 2; ++k) t[k] = (lane & kC / 2) ? x[k + kC / 2] : x[k];
+#pragma unroll
+      for (int s = kC / 4; s; s >>= 1)
+#pragma unroll
+        for (int k = 0; k < s; ++k) t[k] = (lane & s) ? t[k + s] : t[k];
+      float mine = t[0];  // of row and column `lane`
+      if (KIND == kMakeB) mine += pr.diag + fmaf(2.f * g.c * kUnhold * d.x, d.y, g.b * d.y);
+      const __half rounded = __float2half_rn(mine);
+      const float held = __half2float(rounded);
+      const int64_t to = static_cast<int64_t>(b) * g.ldp + row0 + lane;
+      if (KIND == kMakeB) reinterpret_cast<__half*>(piece(lane, lane / 8))[lane % 8] = rounded;
+      if (row0 + lane < pr.M) {
+        if (KIND == kMakeA)
+          g.dA[to] = make_float2(held, mine - held);
+        else
+          g.rB[to] = held != 0.f ? mine / held : 1.f;
+      }
     }
     __syncwarp();
     auto store = [&](uint16_t* to, int64_t ld) {  // the staged chunk, rows of stride ld; to: this lane's first piece
@@ -835,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(smem_addr(&bars->acc_full[s]), 1);
       bar_init(smem_addr(&bars->acc_empty[s]), (PAIR ? 2 : 1) * kEpiWarps);
     }
+    for (int s = 0; s < kReady; ++s) bar_init(smem_addr(&bars->ready[s]), 1);
     bar_init(smem_addr(&bars->done), 1);
     bars->abort = 0;
     bar_init_fence();
@@ -870,13 +930,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       bool fine = true;
-      for (int t = unit; fine && t < total; t += units) {
+      uint32_t nth = 0;
+      for (int t = unit; fine && t < total; t += units, ++nth) {
         const Work w = work_at<PAIR>(g, t);
         const Product pr = product_of<PAIR>(g, maps, w.step, w.kind);
         if (!wait_stored(g, w.b, static_cast<uint32_t>(w.before) * ((PAIR ? 2 : 1) * kEpiWarps), abort)) {
           fine = false;
           break;
         }
+        bar_arrive(smem_addr(&bars->ready[nth % kReady]));
         fence_async_global();  // what the epilogues stored, before the TMA reads it
         const int high_kb = (pr.K + kBK - 1) / kBK, num_kb = high_kb + pr.low;
         const int p0 = w.i * T::kM + static_cast<int>(rank) * kRowsP, q0 = w.j * T::kN + static_cast<int>(rank) * T::kRowsQ;
@@ -956,19 +1018,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     bool fine = true;
-    for (int t = unit; fine && t < total; t += units) {
+    uint32_t nth = 0;
+    for (int t = unit; fine && t < total; t += units, ++nth) {
       const Work w = work_at<PAIR>(g, t);
       const Product pr = product_of<PAIR>(g, maps, w.step, w.kind);
+      auto make_x = [&](auto tall) {
+        constexpr bool kTall = decltype(tall)::value;
+        if (pr.D && pr.C) return epilogue<PAIR, kMakeX, kTall>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase, nth);
+        if (pr.D) return epilogue<PAIR, kMakeXPlain, kTall>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase, nth);
+        return epilogue<PAIR, kMakeOut, kTall>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase, nth);
+      };
       if (w.kind == 0)
-        fine = epilogue<PAIR, kMakeA>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+        fine = epilogue<PAIR, kMakeA, false>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase, nth);
       else if (w.kind == 1)
-        fine = epilogue<PAIR, kMakeB>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
-      else if (pr.D && pr.C)
-        fine = epilogue<PAIR, kMakeX>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
-      else if (pr.D)
-        fine = epilogue<PAIR, kMakeXPlain>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+        fine = epilogue<PAIR, kMakeB, false>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase, nth);
       else
-        fine = epilogue<PAIR, kMakeOut>(g, pr, w, bars, s_epi, tmem, rank, acc, acc_phase);
+        fine = g.m > g.n ? make_x(std::true_type{}) : make_x(std::false_type{});
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -1042,6 +1107,8 @@ size_t carve_ortho(uint8_t* base, int64_t batch, int m, int n, OrthoArgs* o) {
   for (int i = 0; i < 2; ++i) o->X[i] = reinterpret_cast<__half*>(take(sizeof(__half) * batch * m * o->ldx));
   o->A = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
   o->Bm = reinterpret_cast<__half*>(take(sizeof(__half) * batch * p * o->ldp));
+  o->dA = reinterpret_cast<float2*>(take(sizeof(float2) * batch * o->ldp));
+  o->rB = reinterpret_cast<float*>(take(sizeof(float) * batch * o->ldp));
   o->lo_product = p <= kBK;
   for (int i = 0; i < 2; ++i)
     o->L[i] = i && !o->lo_product ? o->L[0] : reinterpret_cast<__half*>(take(sizeof(__half) * batch * m * o->ldx));

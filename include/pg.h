@@ -738,9 +738,10 @@ pg_status pg_lookup_grad(const pg_table_desc* desc, const int32_t* tokens, int32
  * result's; the scale puts magnitudes 6e-8 .. 63 into fp16's normal range, where a norm of at most 1
  * and the usual coefficients keep them below 4), and X as the sum of two such numbers (22 bits;
  * in the last step of the first alone): what rounds X lies in all singular directions, and those that
- * G does not have grow a-fold a step. With the usual coefficients and five steps the result is
- * within 0.002 to 0.0035 of the formulas, relative, 0.0017 of it the bf16 result's rounding, whatever
- * the rank and the spectrum of G.
+ * G does not have grow a-fold a step. The diagonals of A and of a I + b A + c A A count in fp32.
+ * With the usual coefficients and five steps the result is within 0.0017 to 0.003 of the formulas
+ * (norm of the difference over the norm; matrices of fewer than some 200 values: up to 0.007), 0.0017 of it
+ * the bf16 result's rounding, whatever the rank and the spectrum of G.
  * Coefficients have to keep the entries of X, A and a I + b A + c A A below 64: what reaches 64 becomes
  * infinite, and the result of its matrix infinite or NaN. |a| >= 63 and coefficients that are not finite are PG_ERR_UNSUPPORTED.
  * A zero matrix gives zeros (eps > 0); infinities and NaN in G make its own matrix NaN.

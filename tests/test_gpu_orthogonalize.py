@@ -1,10 +1,10 @@
 """pg_orthogonalize where its roundings could grow: matrices of few directions and of decaying
 spectra, against the formulas in 64 bits and against the formulas rounded where the kernel rounds.
 
-What is rounded: A and Bm = a I + b A + c A A to fp16 (half a step: 2^-11 of the entry); X to the sum
-of two fp16 numbers (2^-22), the second of which the last step leaves out (2^-11, times a); the
-result to bf16. A rounding of X lies in all singular directions and grows by a = 3.44 a step
-where G has none (485-fold over five steps), so it has to start at 2^-22; one of A or Bm multiplies X,
+What is rounded: A and Bm = a I + b A + c A A to fp16 (half a step: 2^-11 of the entry) but for their
+diagonals; X to the sum of two fp16 numbers (2^-22), the second of which the last step leaves out (2^-11,
+times a); the result to bf16. A rounding of X lies in all singular directions and grows by a = 3.44 a
+step where G has none (485-fold over five steps), so it has to start at 2^-22; one of A or Bm multiplies X,
 lies only where X has directions, and stays what it is relative to the result.
 """
 import math
@@ -26,7 +26,8 @@ FORMULA = 5 * 5 * 2.0 ** -11 + 3.4445 * 2.0 ** -11 + 2.0 ** -8
 
 
 def held_reference(G, steps=5, coeffs=COEFFS, eps=1e-7, scale=1.0):
-    """The formulas with A, Bm and the two parts of X rounded to fp16 as the kernel holds them."""
+    """The formulas with A, Bm and the two parts of X rounded to fp16 as the kernel holds them, and what that
+    leaves of the diagonals of A and Bm."""
     a, b, c = coeffs
     outs = []
     for g in G.double():
@@ -35,9 +36,13 @@ def held_reference(G, steps=5, coeffs=COEFFS, eps=1e-7, scale=1.0):
         for s in range(steps):
             hi = fp16_held(x)
             lo = fp16_held(x - hi) if s + 1 < steps else torch.zeros_like(x)
-            A = fp16_held(hi @ hi.T)
-            B = fp16_held(a * torch.eye(len(A), dtype=A.dtype, device=A.device) + b * A + c * (A @ A))
-            x = B @ hi + (B @ lo if len(A) <= 128 else a * lo)
+            exact = hi @ hi.T
+            A = fp16_held(exact)
+            left = exact.diagonal() - A.diagonal()
+            exact = b * A + c * (A @ A) + torch.diag(a + left * (b + 2 * c * A.diagonal()))
+            B = fp16_held(exact)
+            ratio = (exact.diagonal() / B.diagonal())[:, None]
+            x = ratio * (B @ (hi + lo)) if len(A) <= 128 else ratio * (B @ hi) + a * lo
         outs.append(scale * (x if g.shape[0] <= g.shape[1] else x.T))
     return torch.stack(outs)
 
@@ -78,6 +83,16 @@ def test_few_directions_in_few_steps(cuda, m, n, steps):
     out = run_ortho(_pg(), G, steps=steps, scale=0.5)
     assert rel(out, held_reference(G, steps, scale=0.5)) <= SAME_PLACES
     assert rel(out, ortho_reference(G, steps, scale=0.5)) <= FORMULA
+
+
+@pytest.mark.parametrize("kind", ["gaussian", "rank11"])
+@pytest.mark.parametrize("m,n", [(32, 984), (1400, 40), (40, 1400), (296, 1536), (1536, 296), (16, 4000)])
+def test_sides_many_times_the_other(cuda, m, n, kind):
+    # singular values near one another, where diagonals rounded to fp16 lose most: what the held forms add
+    # stays below what rounding the result to bf16 does, and independent errors add in squares
+    G = make(kind, 2, m, n, F32, cuda) if kind == "rank11" else gaussian(torch.Generator().manual_seed(m), 2, m, n, F32, cuda)
+    out, ref = run_ortho(_pg(), G), ortho_reference(G, 5)
+    assert rel(out, ref) <= math.sqrt(2.0) * rel(ref.to(BF16), ref)
 
 
 def test_one_direction_per_matrix_of_a_batch(cuda):
