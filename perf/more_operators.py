@@ -13,7 +13,7 @@ none of which hands the logits [N, V] out:
   vocab_distill_grad  the loss, and the gradients of sum_i w_i loss_i with respect to h and W
 
 A target or a listed token outside [0, V) is padding: a row without a target (or whose list is all
-padding) has loss 0 and no gradient. A token listed twice counts with both of its weights.
+padding) has loss 0, lse 0 and no gradient. A token listed twice counts with both of its weights.
 
 `run` computes each in elementary torch operations, or, where `own` is set, through the library's
 calls.
@@ -178,7 +178,7 @@ def _plain_ce(s, grad=False):
     lse = m + total.log()
     loss = torch.where(valid, lse - zt + s.case["z_loss"] * lse * lse, 0)
     if not grad:
-        return loss, lse
+        return loss, torch.where(valid, lse, 0)
     g = e.mul_(((1 + 2 * s.case["z_loss"] * lse) / total)[:, None])
     g.scatter_add_(1, at, torch.full_like(zt, -1.0)[:, None])
     return (loss, *_plain_grads(s, g, valid))
@@ -203,7 +203,7 @@ def _plain_distill(s, grad=False):
     terms = torch.where(p > 0, p * (logp - (zt - lse[:, None])), 0)
     loss = torch.where(valid, terms.sum(1), 0)
     if not grad:
-        return loss, lse
+        return loss, torch.where(valid, lse, 0)
     g = e.mul_((1 / total)[:, None])
     g.scatter_add_(1, at, -p)
     return (loss, *_plain_grads(s, g, valid))
@@ -328,6 +328,7 @@ def exact(case, seed):
             loss[rows][at] = lse[rows][at] - z[at, t[at]] + case["z_loss"] * lse[rows][at] ** 2
             beta = 1.0 + 2.0 * case["z_loss"] * lse[rows]
         if not grad:
+            lse[rows] *= keep
             continue
         w = s.grad_scale * wide * keep.double()
         if s.weights is not None:
