@@ -1,0 +1,194 @@
+// Tensor-core product wrappers (inline PTX, sm_103a) shared by the orthogonalised updates (pg_ortho.cu)
+// and the vocabulary losses (pg_vocab.cu): TMA boxes, tcgen05.mma on one CTA or a CTA pair, TMEM, and
+// operand tiles of 16-bit values read K-major or MN-major. Every wait is bounded.
+#pragma once
+
+#include <cuda.h>
+
+#include "pg_async.cuh"
+
+namespace pg {
+namespace {
+
+// A k-block is 128 deep: with 64 the waits, copies and commits that a block costs its two
+// issuing threads, and not the tensor core, set the pace (orthogonalised updates, 1280 x 2560, X in one
+// part: 45 us a step, 41 with 128).
+constexpr int kBK = 128;
+constexpr int kLine = 64;  // 16-bit values of a 128-byte line: the inner extent of a TMA box
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  if constexpr (!PAIR) {
+    return bar_try_wait(bar, parity);
+  } else {  // threads of the peer CTA arrive on it
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  }
+}
+
+template <bool PAIR>
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = now_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (poll<PAIR>(bar, parity)) return true;
+    if (*abort || now_ns() - t0 > kAsyncWaitNs) return false;
+  }
+}
+
+// Waits for the phase of `parity`; false after about a second or once another role gave up.
+template <bool PAIR>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return poll<PAIR>(bar, parity) || wait_slow<PAIR>(bar, parity, abort);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y),
+        "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y),
+        "r"(z)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+
+// One arrival on `bar` (PAIR: of both CTAs) when the MMAs issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    commit<false>(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Orders generic-proxy accesses to global memory before TMA accesses (and back).
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes: lane i gets row i (after tmem_wait).
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+
+// Waits for the loads into r, which nothing reads before this.
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
+}
+
+// Shared-memory descriptor of an operand tile written by TMA with 128-byte swizzle (61-63 = 2;
+// version 1 at 46-47; start address >> 4 at 0-13), in lines of 64 16-bit values.
+//   K-major: the lines are operand rows, 8-row groups 1024 bytes apart (bits 32-45), and the 64
+//   deeper half of a k-block lies behind all the rows.
+//   MN-major: a line holds 64 operand rows at one k, 8-k groups lie 1024 bytes apart (32-45), and
+//   the next 64 rows lie behind the 128 lines of the first (bits 16-29).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>(mn ? kBK * kLine * 2 >> 4 : 1) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The copies of one operand's k-block k0: its rows from r0 on.
+template <bool PAIR, int ROWS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, const CUtensorMap* map_rows,
+                                             bool mn, int r0, int k0, int b, uint32_t bar) {
+  if (mn) {
+#pragma unroll
+    for (int h = 0; h < ROWS / kLine; ++h)
+      load_box<PAIR>(dst + h * (kBK * kLine * 2), map, bar, r0 + h * kLine, k0, b);
+  } else {
+#pragma unroll
+    for (int h = 0; h < kBK / kLine; ++h)
+      load_box<PAIR>(dst + h * (ROWS * kLine * 2), map_rows, bar, k0 + h * kLine, r0, b);
+  }
+}
+
+}  // namespace
+}  // namespace pg
