@@ -1,0 +1,1351 @@
+// Losses over the vocabulary with their gradients (pg_vocab_ce, pg_vocab_distill and their _grad calls).
+//
+// With z = scale h W^T (h [N, d], W [V, d]; for the distillation scale / T in scale's place), p = softmax(z) and
+// targets w_ij (cross entropy: 1 at t_i; distillation: the teacher's softmax over its list),
+//   lse_i = log sum_j exp z_ij        loss_i = sum_j w_ij log w_ij - sum_j w_ij z_ij + lse_i (+ zl lse_i^2)
+//   dz_ij = g_i (beta_i p_ij - w_ij)  beta_i = 1 + 2 zl lse_i,  g_i = grad_scale row_weight_i
+//   dh = scale dz W,  dW = scale dz^T h
+// Three products of 2 N V d operations; the first alone without gradients.
+//
+// The logits exist only tile by tile in TMEM. A row's targets are few, so their logits are dot products of
+// their own (vocab_targets_kernel, before the first product), and their largest is a reference c_i <= lse_i that the
+// epilogue of the first product knows beforehand: it stores u_ij = exp(z_ij - c_i) and adds up each tile's rows. One
+// small kernel a chunk then has lse_i, the loss and f_i = g_i scale beta_i exp(c_i - lse_i), puts
+//   u_ij - w_ij exp(lse_i - c_i) / beta_i
+// at the targets (from fp32 logits: p - 1 loses nothing where p is close to 1), and
+//   dh_i = f_i (U W)_i,   dW = U^T (f h)
+// are two more products. So the logits are made once, nothing normalises U, and a gradient costs 6 N V d
+// operations; making the logits again in place of keeping U would cost 8. U is kept in bf16, whose exponent takes
+// exp(+-87); u's rounding (2^-8 at most) is a rounding of p. It is kept for a chunk of the rows, 2 GiB at most.
+// A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit of that tile
+// as its reference instead, and the small kernel brings the whole row to the reference lse_i: a pass over the rows
+// that need it and no others.
+//
+// Precision. bf16 operands and bf16 gradients take one product of bf16 operands each. fp32 values are sums of bf16
+// "pieces" (value = p0 + p1 + p2, 8 bits each), and their products the sum of the pieces' products down to 2^-24 (six of
+// nine): fp32 operands are split beforehand, and U and f h have three pieces for an fp32 gradient. All sums are fp32
+// in TMEM.
+//
+// The products: 256 x 256 tiles on CTA pairs (tcgen05, cta_group::2), 128-deep k-blocks of both operands by
+// TMA into a ring of three, two accumulators in TMEM, eight epilogue warps.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "pg_umma.cuh"
+#include "pg_vec.h"
+
+namespace pg {
+namespace {
+
+constexpr int kErrVocab = 524288;        // device error bit: a wait of these products gave up
+constexpr int kMaxVocabWidth = 16384;    // d
+constexpr int64_t kMaxVocab = 1 << 24;
+constexpr int kMaxList = 256;            // teacher tokens a row
+constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (any number gives the same results)
+constexpr int64_t kKeepBytes = 2ll << 30;  // of U
+constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
+constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
+
+constexpr int kTile = 256;
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kStages = 3;
+constexpr int kOperandBytes = 128 * kBK * 2;
+constexpr int kStageBytes = 4096;        // an epilogue warp's: 32 rows of 128 bytes
+constexpr size_t kRing = static_cast<size_t>(kStages) * 2 * kOperandBytes;
+constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kStageBytes;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: fp32 sums, bf16 operands
+                            (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSumLimit = 0x1p57f;     // of a tile's row; above it the row changes its reference
+
+struct VocabMaps {
+  CUtensorMap h, W, U, Ust, F;           // U for loads and (boxes of 32 rows) for stores; F: f h
+};
+
+struct VocabArgs {
+  const void *h, *W;                     // as given
+  const int32_t *targets, *ids;          // [N] or [N, K]
+  const void* tlogits;                   // [N, K]
+  const float* row_weight;
+  float *loss, *lse;
+  int32_t* err;
+  __nv_bfloat16 *hp, *Wp;                // pieces [pieces][rows][dp], or null
+  __nv_bfloat16 *U, *F;                  // [pieces][Nc][Vp], [pieces][Nc][dp]
+  float2* sums;                          // [2 tiles][Nc]: reference (log2), sum
+  float *zk, *wk;                        // [Nc][K] targets' logits (log2), weights (-1: none, or a later place of the same)
+  float *c, *a;                          // [Nc] reference (log2; +inf: no target), the loss's part beside lse
+  float* f;                              // [Nc]
+  float* acc;                            // [V][d] dW over chunks, or null
+  float* parts;                          // [q][Nc][d] of dh, or null
+  void *gh, *gw;
+  int* err_word;
+  int64_t row0;                          // of the chunk
+  int64_t V, Vp;
+  int N, Nc, d, dp, K, rows;             // rows: of this chunk
+  int h_dtype, w_dtype, t_dtype, gh_dtype, gw_dtype;
+  int np_h, np_w, np_u, np_f;            // pieces
+  int accumulate, first, last;           // first, last chunk
+  float k2;                              // scale log2(e)
+  float scale, inv_t, zl, grad_scale;
+  // schedule of the gradients' products
+  int q, tiles2, tiles3, nd, light, delta, heavy;
+  int passes_h, passes_w;                // piece products of dh, dW
+};
+
+// ------------------------------------------------------------------- fp32 values as bf16 pieces
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+
+// x becomes what rounding it to bf16 left; returns the rounded value's bits. (Infinities and NaN leave 0.)
+__device__ __forceinline__ uint16_t take_piece(float& x) {
+  const uint16_t b = bf16_bits(x);
+  const float r = __uint_as_float(static_cast<uint32_t>(b) << 16);
+  x = fabsf(r) <= 3.4e38f ? x - r : 0.f;
+  return b;
+}
+
+// Products of pieces (i, j) with i + j below the larger count: what is left out is below 2^-8 of that of the last kept.
+__host__ __device__ __forceinline__ int passes_of(int a, int b) {
+  const int m = a > b ? a : b;
+  int n = 0;
+  for (int i = 0; i < a; ++i)
+    for (int j = 0; j < b; ++j) n += i + j < m;
+  return n;
+}
+
+__device__ __forceinline__ void piece_of(int a, int b, int pass, int* i, int* j) {
+  const int m = a > b ? a : b;
+  int n = 0;
+  for (*i = 0; *i < a; ++*i)
+    for (*j = 0; *j < b; ++*j)
+      if (*i + *j < m && n++ == pass) return;
+}
+
+// dst [pieces][rows][dp] from src [rows][d], zeros behind a row's end. Also the copy of bf16 rows that TMA cannot
+// take as they are (d % 8 != 0). Bound by memory.
+template <int DT>
+__global__ void __launch_bounds__(256)
+    vocab_split_kernel(const void* src, int64_t rows, int d, int dp, int pieces, __nv_bfloat16* dst) {
+  const int64_t per_row = dp / 8;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= rows * per_row) return;
+  const int64_t r = at / per_row;
+  const int c = static_cast<int>(at - r * per_row) * 8;
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float y[1] = {0.f};
+    if (c + k < d) load_cols<DT, 1>(src, r * d + c + k, y);
+    x[k] = y[0];
+  }
+  for (int p = 0; p < pieces; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = take_piece(x[2 * k]), hi = take_piece(x[2 * k + 1]);
+      w[k] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// --------------------------------------------------------------------------- the targets' logits
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// <h_i, W_j> of up to E rows j by one warp, fp32 in a fixed order.
+template <int HT, int WT, bool VEC, int E>
+__device__ __forceinline__ void warp_dots(const VocabArgs& g, int64_t i, const int64_t (&j)[E], float (&sum)[E]) {
+  constexpr int kStep = VEC ? 8 : 1;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll 2
+  for (int c = lane * kStep; c < g.d; c += 32 * kStep) {
+    float x[kStep], y[E][kStep];
+    load_cols<HT, kStep>(g.h, i * g.d + c, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) load_cols<WT, kStep>(g.W, j[e] * g.d + c, y[e]);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) sum[e] = fmaf(x[k], y[e][k], sum[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = warp_sum(sum[e]);
+}
+
+// A reference that is no logit: +infinity stands for a row without a target.
+__device__ __forceinline__ float as_reference(float z) { return z == INFINITY ? __int_as_float(0x7fffffff) : z; }
+
+// Cross entropy: one warp a row, two rows of W and h read once.
+template <int HT, int WT, bool VEC>
+__global__ void __launch_bounds__(128) vocab_target_kernel(const __grid_constant__ VocabArgs g) {
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= g.rows) return;
+  const int64_t i = g.row0 + r, t = __ldg(g.targets + i);
+  const bool valid = t >= 0 && t < g.V;
+  float z[1] = {0.f};
+  if (valid) {
+    const int64_t j[1] = {t};
+    warp_dots<HT, WT, VEC, 1>(g, i, j, z);
+  }
+  if (lane != 0) return;
+  if (!valid && g.err) atomicMin(reinterpret_cast<unsigned int*>(g.err), static_cast<unsigned int>(i));
+  z[0] *= g.k2;
+  g.zk[r] = z[0];
+  g.wk[r] = valid ? 1.f : -1.f;
+  g.c[r] = valid ? as_reference(z[0]) : INFINITY;
+  g.a[r] = 0.f;
+}
+
+// Distillation: one block a row. The first warp forms the teacher's softmax, all warps the listed tokens' logits,
+// four rows of W at a time.
+constexpr int kListWarps = 8, kListAtOnce = 4;
+
+template <int HT, int WT, bool VEC>
+__global__ void __launch_bounds__(32 * kListWarps) vocab_list_kernel(const __grid_constant__ VocabArgs g) {
+  __shared__ int32_t s_id[kMaxList];
+  __shared__ float s_w[kMaxList], s_z[kMaxList];
+  __shared__ int s_any;
+  const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t i = g.row0 + r;
+  constexpr int kPer = kMaxList / 32;
+  float u[kPer];
+  if (warp == 0) {
+    float top = -INFINITY;
+    bool outside = false, poison = false;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int k = e * 32 + lane;
+      u[e] = -INFINITY;
+      if (k >= g.K) continue;
+      int32_t id = __ldg(g.ids + i * g.K + k);
+      const bool in = id >= 0 && id < g.V;
+      outside |= !in;
+      if (in) {
+        float y[1];
+        if (g.t_dtype == PG_F32) load_cols<PG_F32, 1>(g.tlogits, i * g.K + k, y);
+        else load_cols<PG_BF16, 1>(g.tlogits, i * g.K + k, y);
+        u[e] = y[0] * g.inv_t;
+        poison |= !(u[e] < INFINITY);  // (also NaN, which fmaxf passes over)
+        top = fmaxf(top, u[e]);
+      }
+      s_id[k] = in ? id : -1;
+    }
+    top = warp_max(top);
+    poison = __any_sync(0xffffffffu, poison);
+    outside = __any_sync(0xffffffffu, outside);
+    const bool some = poison || top > -INFINITY;
+    float total = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      u[e] = !some ? -INFINITY : u[e] - (top > -INFINITY ? top : 0.f);
+      total += expf(u[e]);
+    }
+    total = warp_sum(total);
+    const float log_total = logf(total);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int k = e * 32 + lane;
+      u[e] = poison ? __int_as_float(0x7fffffff) : u[e] - log_total;  // log p
+      if (k < g.K) s_w[k] = !some ? 0.f : expf(u[e]);
+    }
+    if (lane == 0) {
+      s_any = some;
+      if (outside && g.err) atomicMin(reinterpret_cast<unsigned int*>(g.err), static_cast<unsigned int>(i));
+    }
+  }
+  __syncthreads();
+  const bool some = s_any != 0;
+  for (int k0 = warp * kListAtOnce; some && k0 < g.K; k0 += warps * kListAtOnce) {
+    int64_t j[kListAtOnce];
+    float z[kListAtOnce];
+#pragma unroll
+    for (int e = 0; e < kListAtOnce; ++e) {
+      const int32_t id = k0 + e < g.K ? s_id[k0 + e] : -1;
+      j[e] = id < 0 ? 0 : id;
+    }
+    warp_dots<HT, WT, VEC, kListAtOnce>(g, i, j, z);
+    if (lane == 0)
+#pragma unroll
+      for (int e = 0; e < kListAtOnce; ++e)
+        if (k0 + e < g.K) s_z[k0 + e] = z[e] * g.k2;
+  }
+  __syncthreads();
+  // what the gradient puts at each token: a token's later places count with its first
+  for (int k = threadIdx.x; k < g.K; k += blockDim.x) {
+    float w = s_w[k];
+    const int32_t id = s_id[k];
+    if (id < 0 || !some) {
+      w = -1.f;
+    } else {
+      for (int e = 0; e < g.K; ++e) {
+        if (e == k || s_id[e] != id) continue;
+        if (e < k) w = -1.f;
+        else if (w >= 0.f) w += s_w[e];
+      }
+    }
+    g.wk[static_cast<int64_t>(r) * g.K + k] = w;
+    g.zk[static_cast<int64_t>(r) * g.K + k] = some ? s_z[k] : 0.f;
+  }
+  if (warp != 0) return;
+  float c = -INFINITY;
+  bool nan = false;
+  for (int k = lane; some && k < g.K; k += 32) {
+    if (s_id[k] < 0) continue;
+    c = fmaxf(c, s_z[k]);
+    nan |= !(s_z[k] == s_z[k]);
+  }
+  c = warp_max(c);
+  if (__any_sync(0xffffffffu, nan)) c = __int_as_float(0x7fffffff);
+  float a = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int k = e * 32 + lane;
+    if (!some || k >= g.K || s_id[k] < 0) continue;
+    const float w = s_w[k];
+    if (!(w == 0.f)) a += w * (u[e] - (s_z[k] - c) * kLn2);
+  }
+  a = warp_sum(a);
+  if (lane == 0) {
+    g.c[r] = some ? as_reference(c) : INFINITY;
+    g.a[r] = some ? a : 0.f;
+  }
+}
+
+// --------------------------------------------------------------------------------- products
+
+enum VocabKind { kSums, kKeep, kGrads };  // logits without and with U; the gradients
+
+// One tile of a product D = P Q^T: the k-blocks [kb0, kb1) of each piece product.
+struct VocabJob {
+  const CUtensorMap *P, *Q;
+  bool p_mn, q_mn;
+  int np_p, np_q, passes;
+  int i, j;                              // tile's row and column
+  int kb0, kb1;
+  int product, part;                     // 0: logits, 1: dh, 2: dW
+};
+
+// The r-th job of this unit; false behind the last.
+// The gradients: first the units of dh (its tiles in q parts along V, part by part so that the units at work read the
+// same rows of W), then the tiles of dW. Where the units of dh do not come out even, those that have one fewer take
+// `delta` tiles of dW more.
+template <int KIND>
+__device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps, int unit, int units, int r, VocabJob* w) {
+  if constexpr (KIND != kGrads) {
+    // tiles that are at work together share their rows of W, and h stays in L2
+    const int nm = (g.rows + kTile - 1) / kTile;
+    const int64_t t = static_cast<int64_t>(r) * units + unit;
+    if (t >= static_cast<int64_t>(nm) * ((g.V + kTile - 1) / kTile)) return false;
+    w->P = &maps.h;
+    w->Q = &maps.W;
+    w->p_mn = w->q_mn = false;
+    w->np_p = g.np_h;
+    w->np_q = g.np_w;
+    w->passes = passes_of(g.np_h, g.np_w);
+    w->i = static_cast<int>(t % nm);
+    w->j = static_cast<int>(t / nm);
+    w->kb0 = 0;
+    w->kb1 = (g.d + kBK - 1) / kBK;
+    w->product = w->part = 0;
+    return true;
+  } else {
+    const int n2 = g.tiles2 * g.q, mine = n2 / units + (unit < g.heavy);
+    if (r < mine) {
+      const int u = r * units + unit, t = u % g.tiles2;
+      const int64_t all = (g.V + kBK - 1) / kBK;
+      w->part = u / g.tiles2;
+      w->P = &maps.U;
+      w->Q = &maps.W;
+      w->p_mn = false;
+      w->q_mn = true;
+      w->np_p = g.gh_dtype == PG_F32 ? g.np_u : 1;
+      w->np_q = g.gh_dtype == PG_F32 ? g.np_w : 1;
+      w->passes = g.passes_h;
+      w->i = t / g.nd;
+      w->j = t % g.nd;
+      w->kb0 = static_cast<int>(all * w->part / g.q);
+      w->kb1 = static_cast<int>(all * (w->part + 1) / g.q);
+      w->product = 1;
+      return true;
+    }
+    r -= mine;
+    int64_t t;
+    if (unit >= g.heavy && r < g.delta) {
+      t = static_cast<int64_t>(r) * g.light + (unit - g.heavy);
+    } else {
+      if (unit >= g.heavy) r -= g.delta;
+      t = static_cast<int64_t>(g.delta) * g.light + static_cast<int64_t>(r) * units + unit;
+    }
+    if (t >= g.tiles3) return false;
+    w->P = &maps.U;
+    w->Q = &maps.F;
+    w->p_mn = w->q_mn = true;
+    w->np_p = g.gw_dtype == PG_F32 ? g.np_u : 1;
+    w->np_q = g.gw_dtype == PG_F32 ? g.np_f : 1;
+    w->passes = g.passes_w;
+    w->i = static_cast<int>(t / g.nd);
+    w->j = static_cast<int>(t % g.nd);
+    w->kb0 = 0;
+    w->kb1 = (g.rows + kBK - 1) / kBK;
+    w->product = 2;
+    w->part = 0;
+    return true;
+  }
+}
+
+struct VocabBars {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 64 at a time. u = 2^(k2 z - c) in fp32 for the
+// row's sum, and to U through the warp's shared memory (32 rows of 128 bytes, swizzled as the TMA store reads them).
+template <bool KEEP>
+__device__ __forceinline__ void logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row,
+                                            int row0, int64_t col0, float k2, float c, bool dead, float* sum) {
+  const int lane = threadIdx.x & 31;
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const int64_t c0 = col0 + h * 64;
+    if (c0 >= g.V) break;
+    uint32_t r[64];
+    tmem_load(from + h * 64, r);
+    tmem_load(from + h * 64 + 32, r + 32);
+    tmem_wait(r);
+    float x[64];
+#pragma unroll
+    for (int k = 0; k < 64; ++k) x[k] = exp2_fast(fmaf(__uint_as_float(r[k]), k2, -c));
+    if (c0 + 64 > g.V) {
+      const int left = static_cast<int>(g.V - c0);
+#pragma unroll
+      for (int k = 0; k < 64; ++k) x[k] = k < left ? x[k] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 64; k += 2) {
+      s0 += x[k];
+      s1 += x[k + 1];
+    }
+    if constexpr (KEEP) {
+#pragma unroll 1
+      for (int p = 0; p < g.np_u; ++p) {
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          w[k] = two_bf16(x[2 * k], x[2 * k + 1]);
+          if (p + 1 < g.np_u) {
+            x[2 * k] -= __uint_as_float(w[k] << 16);
+            x[2 * k + 1] -= __uint_as_float(w[k] & 0xFFFF0000u);
+          }
+          w[k] = dead ? 0u : w[k];  // (a row without a target may hold anything)
+        }
+        if (lane == 0) stores_read();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(s_row + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) store_box(&maps.Ust, smem_addr(s_row), static_cast<int>(c0), row0, p);
+        __syncwarp();
+      }
+    }
+  }
+  *sum = s0 + s1;
+}
+
+template <bool KEEP>
+__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
+                                                uint32_t from, int row0, int half, float c) {
+  const int lane = threadIdx.x & 31;
+  const int64_t col0 = static_cast<int64_t>(w.j) * kTile + half * 128;
+  const bool dead = row0 + lane >= g.rows || c == INFINITY;
+  float sum = 0.f;
+  if (row0 < g.rows && col0 < g.V) logits_half<KEEP>(g, maps, from, s_row, row0, col0, g.k2, c, dead, &sum);
+  float ref = c;
+  const bool over = !dead && !(sum <= kSumLimit);
+  if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the tile's largest for a reference
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      uint32_t r[32];
+      tmem_load(from + h * 32, r);
+      tmem_wait(r);
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (col0 + h * 32 + k < g.V) top = fmaxf(top, __uint_as_float(r[k]) * g.k2);
+    }
+    if (over) ref = top == -INFINITY ? 0.f : top;
+    if (KEEP && lane == 0) stores_done();  // the same places are written again
+    __syncwarp();
+    logits_half<KEEP>(g, maps, from, s_row, row0, col0, g.k2, ref, dead, &sum);
+  }
+  if (row0 + lane < g.rows)
+    g.sums[(2ll * w.j + half) * g.Nc + row0 + lane] = make_float2(ref, sum);
+}
+
+// A gradient's tile. TMEM gives a lane one row; global memory wants neighbouring lanes on one row, so 32 columns
+// at a time pass through the warp's shared memory.
+__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob& w, uint8_t* s_row, uint32_t from, int row0,
+                                              int half) {
+  const int lane = threadIdx.x & 31;
+  const bool dh = w.product == 1, part = dh && g.parts;
+  const int64_t rows = dh ? g.rows : g.V;
+  if (row0 >= rows) return;
+  float f = 1.f;
+  if (dh && !part) f = row0 + lane < rows ? __ldg(g.f + row0 + lane) : 0.f;
+  // where the tile goes, and what is added to it
+  void* dst;
+  int dtype;
+  const float* add32 = nullptr;
+  const __nv_bfloat16* add16 = nullptr;
+  if (part) {
+    dst = g.parts + static_cast<int64_t>(w.part) * g.Nc * g.d;
+    dtype = PG_F32;
+  } else if (dh) {
+    dtype = g.gh_dtype;
+    dst = static_cast<uint8_t*>(g.gh) + g.row0 * g.d * (dtype == PG_F32 ? 4 : 2);
+  } else {
+    const bool through = g.acc && !g.last;
+    dtype = through ? PG_F32 : g.gw_dtype;
+    dst = through ? g.acc : g.gw;
+    if (g.gw_dtype == PG_F32) {
+      if (!g.first || g.accumulate) add32 = static_cast<const float*>(g.gw);
+    } else {
+      if (!g.first) add32 = g.acc;
+      if (g.last && g.accumulate) add16 = static_cast<const __nv_bfloat16*>(g.gw);
+    }
+  }
+  const bool vec = g.d % 4 == 0 && reinterpret_cast<uintptr_t>(dst) % (dtype == PG_F32 ? 16 : 8) == 0 &&
+                   (!add32 || reinterpret_cast<uintptr_t>(add32) % 16 == 0);
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    const int c0 = w.j * kTile + half * 128 + ch * 32;
+    if (c0 >= g.d) break;
+    uint32_t r[32];
+    tmem_load(from + ch * 32, r);
+    tmem_wait(r);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float4 v;
+      float* x = &v.x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = f == 0.f ? 0.f : f * __uint_as_float(r[4 * k + e]);
+      *reinterpret_cast<float4*>(s_row + lane * 128 + ((k ^ (lane & 7)) << 4)) = v;
+    }
+    __syncwarp();
+    if (vec) {  // (d % 4 == 0: four columns are inside or outside together)
+      const int lc = lane & 7, col = c0 + lc * 4;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int lr = 4 * k + (lane >> 3);
+        if (row0 + lr >= rows || col >= g.d) continue;
+        float4 v = *reinterpret_cast<const float4*>(s_row + lr * 128 + ((lc ^ (lr & 7)) << 4));
+        const int64_t at = static_cast<int64_t>(row0 + lr) * g.d + col;
+        if (add32) {
+          const float4 o = *reinterpret_cast<const float4*>(add32 + at);
+          v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+        }
+        if (add16) {
+          const uint2 o = *reinterpret_cast<const uint2*>(add16 + at);
+          v.x += __uint_as_float(o.x << 16); v.y += __uint_as_float(o.x & 0xFFFF0000u);
+          v.z += __uint_as_float(o.y << 16); v.w += __uint_as_float(o.y & 0xFFFF0000u);
+        }
+        if (dtype == PG_F32) *reinterpret_cast<float4*>(static_cast<float*>(dst) + at) = v;
+        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dst) + at) = make_uint2(two_bf16(v.x, v.y), two_bf16(v.z, v.w));
+      }
+    } else {
+      const int col = c0 + lane;
+#pragma unroll 4
+      for (int lr = 0; lr < 32; ++lr) {
+        if (row0 + lr >= rows || col >= g.d) break;
+        float v = *reinterpret_cast<const float*>(s_row + lr * 128 + (((lane >> 2) ^ (lr & 7)) << 4) + (lane & 3) * 4);
+        const int64_t at = static_cast<int64_t>(row0 + lr) * g.d + col;
+        if (add32) v += add32[at];
+        if (add16) v += __bfloat162float(add16[at]);
+        if (dtype == PG_F32) static_cast<float*>(dst)[at] = v;
+        else static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(v);
+      }
+    }
+  }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    vocab_product_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabArgs g) {
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ VocabBars bars_s;
+  VocabBars* bars = &bars_s;
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(smem_addr(&bars->full[s]), 1);
+      bar_init(smem_addr(&bars->empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(smem_addr(&bars->acc_full[s]), 1);
+      bar_init(smem_addr(&bars->acc_empty[s]), 2 * kEpiWarps);
+    }
+    bar_init(smem_addr(&bars->done), 1);
+    bars->abort = 0;
+    bar_init_fence();
+    fence_async_smem();
+  }
+  if (warp == 1) tmem_alloc<true>(smem_addr(&bars->tmem), kTmemCols);
+  fence_before();
+  __syncthreads();
+  pair_sync();  // both CTAs' barriers and TMEM exist before any remote use
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  int stage = 0, acc = 0;
+  uint32_t ring_phase = 0, acc_phase = 0;
+  bool fine = true;
+  VocabJob w;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
+        const int p0 = w.i * kTile + static_cast<int>(rank) * 128, q0 = w.j * kTile + static_cast<int>(rank) * 128;
+        for (int kb = w.kb0; fine && kb < w.kb1; ++kb)
+          for (int pass = 0; pass < w.passes; ++pass) {
+            if (!wait<true>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
+              fine = false;
+              break;
+            }
+            int zp = 0, zq = 0;
+            if (w.passes > 1) piece_of(w.np_p, w.np_q, pass, &zp, &zq);
+            const uint32_t full = smem_addr(&bars->full[stage]);
+            const uint32_t dp = smem_addr(ring + stage * (2 * kOperandBytes)), dq = dp + kOperandBytes;
+            const uint32_t bar = in_cta(full, 0);
+            if (rank == 0) bar_expect(full, 2 * 2 * kOperandBytes);
+            load_operand<true, 128>(dp, w.P, w.P, w.p_mn, p0, kb * kBK, zp, bar);
+            load_operand<true, 128>(dq, w.Q, w.Q, w.q_mn, q0, kb * kBK, zq, bar);
+            if (++stage == kStages) {
+              stage = 0;
+              ring_phase ^= 1u;
+            }
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
+        if (!wait<true>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
+          fine = false;
+          break;
+        }
+        fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * kTile);
+        const uint32_t idesc = kIdesc | (w.p_mn ? 1u << 15 : 0u) | (w.q_mn ? 1u << 16 : 0u);
+        // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
+        // groups of an MN-major tile
+        const uint32_t step_p = w.p_mn ? 2048 >> 4 : 32 >> 4, step_q = w.q_mn ? 2048 >> 4 : 32 >> 4;
+        const uint32_t half_p = w.p_mn ? 4 * step_p : kOperandBytes / 2 >> 4, half_q = w.q_mn ? 4 * step_q : kOperandBytes / 2 >> 4;
+        const int blocks = (w.kb1 - w.kb0) * w.passes;
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (!wait<true>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
+            fine = false;
+            break;
+          }
+          fence_after();
+          const uint32_t sp = smem_addr(ring + stage * (2 * kOperandBytes));
+          const uint64_t dp = operand_desc(sp, w.p_mn), dq = operand_desc(sp + kOperandBytes, w.q_mn);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
+                          (kb | k) != 0);
+          commit<true>(smem_addr(&bars->empty[stage]));
+          if (++stage == kStages) {
+            stage = 0;
+            ring_phase ^= 1u;
+          }
+        }
+        if (!fine) break;
+        commit<true>(smem_addr(&bars->acc_full[acc]));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* s_row = ring + kRing + (warp - 2) * kStageBytes;
+    for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
+      const int row0 = w.i * kTile + static_cast<int>(rank) * 128 + quarter * 32;
+      float c = INFINITY;
+      if (KIND != kGrads && row0 + lane < g.rows) c = __ldg(g.c + row0 + lane);
+      if (!__all_sync(0xffffffffu, wait<true>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
+        fine = false;
+        break;
+      }
+      fence_after();
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kTile + half * 128);
+      if constexpr (KIND == kGrads) grad_epilogue(g, w, s_row, from, row0, half);
+      else logits_epilogue<KIND == kKeep>(g, maps, w, s_row, from, row0, half, c);
+      fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         in_cta(smem_addr(&bars->acc_empty[acc]), 0))
+                     : "memory");
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (KIND == kKeep && lane == 0) stores_done();
+  }
+  if (!fine) {
+    atomicOr(g.err_word, kErrVocab);
+    *abort = 1;
+  }
+  __syncwarp();
+
+  // every copy has landed and every MMA and commit has finished before the CTA (or its peer) may exit and its
+  // TMEM is given back
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      const uint64_t t0 = now_ns();
+      while (!poll<true>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u) && now_ns() - t0 < kAsyncWaitNs / 8) {
+      }
+      if (++stage == kStages) {
+        stage = 0;
+        ring_phase ^= 1u;
+      }
+    }
+  }
+  if (warp == 1 && lane == 0 && rank == 0) {
+    commit_here<true>(smem_addr(&bars->done));
+    const uint64_t t0 = now_ns();
+    while (!poll<true>(smem_addr(&bars->done), 0) && now_ns() - t0 < kAsyncWaitNs) {
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  pair_sync();
+  if (warp == 1) tmem_free<true>(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------- rows, once their sums are there
+
+constexpr int kRowWarps = 16;
+
+// 32 rows a block: their sums over all tiles (a lane a row, tiles spread over the warps, joined in warp order), lse and
+// loss; for the gradients f, the targets' places of U, and f h.
+template <bool GRAD, int HT, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid_constant__ VocabArgs g) {
+  __shared__ float s_ref[kRowWarps][32], s_sum[kRowWarps][32];
+  __shared__ int s_moved[kRowWarps][32];
+  __shared__ float s_to[32], s_f[32], s_lse[32], s_beta[32];
+  __shared__ int s_fix[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * 32, r = r0 + lane;
+  const bool in = r < g.rows;
+  const float c = in ? g.c[r] : INFINITY;
+  const int64_t segs = (g.V + 127) / 128;
+  float ref = c, sum = 0.f;
+  int moved = 0;
+  auto join = [&](float ref2, float sum2) {
+    if (ref2 == ref) {
+      sum += sum2;
+    } else if (ref2 > ref) {
+      sum = sum * exp2f(ref - ref2) + sum2;
+      ref = ref2;
+    } else {
+      sum += sum2 * exp2f(ref2 - ref);
+    }
+  };
+  if (in && c != INFINITY) {
+#pragma unroll 8
+    for (int64_t s = warp; s < segs; s += kRowWarps) {
+      const float2 v = __ldcg(g.sums + s * g.Nc + r);
+      moved |= v.x != c;
+      join(v.x, v.y);
+    }
+  }
+  s_ref[warp][lane] = ref;
+  s_sum[warp][lane] = sum;
+  s_moved[warp][lane] = moved;
+  __syncthreads();
+  if (warp == 0) {
+    for (int k = 1; k < kRowWarps; ++k) {
+      join(s_ref[k][lane], s_sum[k][lane]);
+      moved |= s_moved[k][lane];
+    }
+    const bool alive = in && c != INFINITY;
+    const float lse2 = ref + log2f(sum), lse = lse2 * kLn2;
+    if (in) {
+      const int64_t i = g.row0 + r;
+      if (g.lse) g.lse[i] = alive ? lse : 0.f;
+      if (g.loss) g.loss[i] = alive ? g.a[r] + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;
+      if (GRAD) {
+        float weight = alive ? g.grad_scale * g.scale : 0.f;
+        if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
+        float beta = 1.f + 2.f * g.zl * lse;
+        if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);  // (its part of U is divided by it)
+        const float to = moved ? lse2 : c;
+        const float f = weight == 0.f ? 0.f : weight * beta * exp2f(to - lse2);
+        g.f[r] = f;
+        s_f[lane] = f;
+        s_to[lane] = to;
+        s_lse[lane] = lse2;
+        s_beta[lane] = beta;
+        // a row without weight must not bring its infinities and NaN into dW
+        s_fix[lane] = weight == 0.f && !(fabsf(lse2) < INFINITY) ? 2 : moved;
+        if (!alive) s_fix[lane] = 3;  // (U's row is zero already)
+      }
+    }
+  }
+  if (!GRAD) return;
+  __syncthreads();
+  for (int k = warp; k < 32 && r0 + k < g.rows; k += kRowWarps) {
+    const int row = r0 + k, fix = s_fix[k];
+    const float f = s_f[k], to = s_to[k];
+    if (fix == 1 || fix == 2) {
+      for (int64_t at = lane * 8; at < g.Vp; at += 256) {
+        const float by = fix == 2 ? 0.f : exp2f(__ldcg(g.sums + (at >> 7) * g.Nc + row).x - to);
+        float x[8] = {};
+        for (int p = 0; p < g.np_u; ++p) {
+          float y[8];
+          read_cols<PG_BF16, 8>(g.U, (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += y[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fix == 2 || at + e >= g.V ? 0.f : x[e] * by;
+        for (int p = 0; p < g.np_u; ++p) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = take_piece(x[2 * e]), hi = take_piece(x[2 * e + 1]);
+            w[e] = lo | hi << 16;
+          }
+          *reinterpret_cast<uint4*>(g.U + (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();
+    }
+    if (fix < 2) {
+      const float peak = exp2f(s_lse[k] - to) / s_beta[k];
+      for (int e = lane; e < g.K; e += 32) {
+        const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
+        if (w == -1.f || w == 0.f) continue;
+        const int64_t t = g.ids ? g.ids[(g.row0 + row) * g.K + e] : g.targets[g.row0 + row];
+        float x = exp2f(g.zk[static_cast<int64_t>(row) * g.K + e] - to) - w * peak;
+        for (int p = 0; p < g.np_u; ++p)
+          reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + t] = take_piece(x);
+      }
+    }
+    if (g.F) {
+      constexpr int kStep = VEC ? 8 : 1;
+      for (int col = lane * 8; col < g.dp; col += 256) {
+        float x[8];
+        if (VEC) {
+          float y[kStep];
+#pragma unroll
+          for (int e = 0; e < kStep; ++e) y[e] = 0.f;
+          if (col < g.d) load_cols<HT, kStep>(g.h, (g.row0 + row) * g.d + col, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = y[e % kStep];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float y[1] = {0.f};
+            if (col + e < g.d) load_cols<HT, 1>(g.h, (g.row0 + row) * g.d + col + e, y);
+            x[e] = y[0];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
+        for (int p = 0; p < g.np_f; ++p) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = take_piece(x[2 * e]), hi = take_piece(x[2 * e + 1]);
+            w[e] = lo | hi << 16;
+          }
+          *reinterpret_cast<uint4*>(g.F + (static_cast<int64_t>(p) * g.Nc + row) * g.dp + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+}
+
+// dh from its q parts.
+__global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__ VocabArgs g) {
+  const int64_t n = static_cast<int64_t>(g.rows) * g.d, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= n) return;
+  float x = 0.f;
+  for (int p = 0; p < g.q; ++p) x += g.parts[static_cast<int64_t>(p) * g.Nc * g.d + at];
+  const float f = g.f[at / g.d];
+  x = f == 0.f ? 0.f : f * x;
+  if (g.gh_dtype == PG_F32) static_cast<float*>(g.gh)[g.row0 * g.d + at] = x;
+  else static_cast<__nv_bfloat16*>(g.gh)[g.row0 * g.d + at] = __float2bfloat16_rn(x);
+}
+
+// ------------------------------------------------------------------------------ host side
+
+struct Sizes {
+  int64_t N, V;
+  int d, K;
+  int h_dtype, w_dtype, gh_dtype, gw_dtype;  // gradients: -1 where there is none
+  bool grad;
+};
+
+// Whether an operand needs its own copy: pieces of fp32, or rows that TMA cannot step over.
+bool needs_copy(int dtype, int d) { return dtype == PG_F32 || d % 8 != 0; }
+
+// Units of dh along V: as few parts as leave the pairs evenly busy (k-blocks; a part's sums cost a store and a load of
+// its tile, a k-block's time for 4 MB).
+void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
+  const int nm = (g->Nc + kTile - 1) / kTile;
+  const int64_t nv = (g->V + kTile - 1) / kTile, kv = (g->V + kBK - 1) / kBK, kn = (g->Nc + kBK - 1) / kBK;
+  g->nd = (g->d + kTile - 1) / kTile;
+  g->tiles2 = has_h ? nm * g->nd : 0;
+  g->tiles3 = has_w ? static_cast<int>(nv * g->nd) : 0;
+  g->passes_h = g->gh_dtype == PG_F32 ? passes_of(g->np_u, g->np_w) : 1;
+  g->passes_w = g->gw_dtype == PG_F32 ? passes_of(g->np_u, g->np_f) : 1;
+  const double cost3 = static_cast<double>(kn) * g->passes_w;
+  double best = 0;
+  g->q = 0;
+  for (int q = 1; q <= (has_h ? 16 : 1); ++q) {
+    if (q > 1 && kv < 2ll * q) break;
+    const int64_t n2 = static_cast<int64_t>(g->tiles2) * q;
+    const int a = static_cast<int>(n2 / units), heavy = static_cast<int>(n2 % units), light = units - heavy;
+    const double cost2 = static_cast<double>((kv + q - 1) / q) * g->passes_h;
+    int delta = heavy ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(cost2 / cost3 + 0.5), g->tiles3 / light)) : 0;
+    const int64_t rest = g->tiles3 - static_cast<int64_t>(delta) * light;
+    const double tail = static_cast<double>((rest + units - 1) / units) * cost3;
+    double t = std::max((a + (heavy ? 1 : 0)) * cost2, a * cost2 + delta * cost3) + tail;
+    if (q > 1) t += static_cast<double>(q) * g->Nc * g->d * 8 / 4e6 + 8;
+    if (g->q == 0 || t < best) {
+      best = t;
+      g->q = q;
+      g->heavy = heavy;
+      g->light = light;
+      g->delta = delta;
+    }
+  }
+}
+
+// Sizes of everything, and its place in the workspace (base null: the size alone).
+size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
+  uint8_t* first = base ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 127) & ~uintptr_t(127)) : nullptr;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    uint8_t* ptr = first ? first + at : nullptr;
+    at += static_cast<size_t>((bytes + 127) / 128 * 128);
+    return ptr;
+  };
+  const bool has_h = s.gh_dtype >= 0, has_w = s.gw_dtype >= 0;
+  g->V = s.V;
+  g->Vp = (s.V + 63) / 64 * 64;
+  g->N = static_cast<int>(s.N);
+  g->d = s.d;
+  g->dp = (s.d + 63) / 64 * 64;
+  g->K = s.K;
+  g->h_dtype = s.h_dtype;
+  g->w_dtype = s.w_dtype;
+  g->gh_dtype = s.gh_dtype;
+  g->gw_dtype = s.gw_dtype;
+  g->np_h = s.h_dtype == PG_F32 ? 3 : 1;
+  g->np_w = s.w_dtype == PG_F32 ? 3 : 1;
+  g->np_u = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32 ? 3 : 1;
+  g->np_f = s.gw_dtype == PG_F32 ? 3 : 1;
+  const int64_t tiles = (s.V + kTile - 1) / kTile;
+  int64_t most = s.grad ? kKeepBytes / (g->np_u * g->Vp * 2) : kMaxForwardRows;
+  most = std::min(most, kSumBytes / (16 * tiles));
+  most = std::max<int64_t>(kTile, most / kTile * kTile);
+  const int64_t chunks = (s.N + most - 1) / most;
+  g->Nc = static_cast<int>(((s.N + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
+  const int64_t Nc = g->Nc;
+  g->Wp = needs_copy(s.w_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_w * s.V * g->dp)) : nullptr;
+  g->hp = needs_copy(s.h_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * Nc * g->dp)) : nullptr;
+  g->sums = reinterpret_cast<float2*>(take(16ll * tiles * Nc));
+  g->zk = reinterpret_cast<float*>(take(4ll * Nc * s.K));
+  g->wk = reinterpret_cast<float*>(take(4ll * Nc * s.K));
+  g->c = reinterpret_cast<float*>(take(4 * Nc));
+  g->a = reinterpret_cast<float*>(take(4 * Nc));
+  g->U = nullptr;
+  g->F = nullptr;
+  g->f = g->acc = g->parts = nullptr;
+  if (s.grad) {
+    g->f = reinterpret_cast<float*>(take(4 * Nc));
+    g->U = reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_u * Nc * g->Vp));
+    if (has_w) {
+      g->F = reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_f * Nc * g->dp));
+      if (chunks > 1 && s.gw_dtype == PG_BF16) g->acc = reinterpret_cast<float*>(take(4ll * s.V * s.d));
+    }
+    plan_schedule(g, kPlanUnits, has_h, has_w);
+    if (has_h && g->q > 1) g->parts = reinterpret_cast<float*>(take(4ll * g->q * Nc * s.d));
+  }
+  return at + 128;
+}
+
+// [pieces, rows, cols] bf16 with row stride ld, boxes of 64 columns, 128-byte swizzle.
+bool vocab_map(CUtensorMap* map, const void* ptr, int pieces, int64_t rows, int64_t cols, int64_t ld, int64_t piece_rows,
+               int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(pieces)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(piece_rows) * ld * 2};
+  cuuint32_t box[3] = {kLine, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+// CTA pairs of the kernel that are resident at once on the current device.
+template <int KIND>
+pg_status vocab_units(int* units) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return PG_ERR_DEVICE;
+  *units = known[dev].load(std::memory_order_relaxed);
+  if (*units) return PG_OK;
+  auto kern = vocab_product_kernel<KIND>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * static_cast<unsigned>(sm_count()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (n < 1) return PG_ERR_DEVICE;
+  known[dev].store(n, std::memory_order_relaxed);
+  *units = n;
+  return PG_OK;
+}
+
+template <int KIND>
+pg_status launch_product(const VocabMaps& maps, const VocabArgs& g, int64_t jobs, cudaStream_t stream) {
+  int units;
+  pg_status st = vocab_units<KIND>(&units);
+  if (st != PG_OK) return st;
+  units = static_cast<int>(std::min<int64_t>(units, jobs));
+  VocabArgs a = g;
+  if (KIND == kGrads) {  // the same parts on however many pairs there are
+    const int64_t n2 = static_cast<int64_t>(a.tiles2) * a.q;
+    a.heavy = static_cast<int>(n2 % units);
+    a.light = units - a.heavy;
+    const double cost2 = static_cast<double>((a.V + kBK - 1) / kBK) / a.q * a.passes_h;
+    const double cost3 = static_cast<double>((a.rows + kBK - 1) / kBK) * a.passes_w;
+    a.delta = a.heavy ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(cost2 / cost3 + 0.5), a.tiles3 / a.light)) : 0;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * static_cast<unsigned>(units));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_product_kernel<KIND>, maps, a);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return after_launch(1);
+}
+
+pg_status launch_split(const void* src, int dtype, int64_t rows, int d, int dp, int pieces, __nv_bfloat16* dst, cudaStream_t stream) {
+  const int64_t blocks = (rows * (dp / 8) + 255) / 256;
+  if (blocks >= (1ll << 31)) return PG_ERR_SHAPE;
+  auto fn = dtype == PG_F32 ? vocab_split_kernel<PG_F32> : vocab_split_kernel<PG_BF16>;
+  fn<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(src, rows, d, dp, pieces, dst);
+  return after_launch(1);
+}
+
+using ArgsFn = void (*)(const VocabArgs);
+
+template <int HT, int WT>
+ArgsFn targets_fn(bool list, bool vec) {
+  if (list) return vec ? vocab_list_kernel<HT, WT, true> : vocab_list_kernel<HT, WT, false>;
+  return vec ? vocab_target_kernel<HT, WT, true> : vocab_target_kernel<HT, WT, false>;
+}
+
+ArgsFn rows_fn(bool grad, int ht, bool vec) {
+  if (!grad) return vocab_rows_kernel<false, PG_F32, false>;
+  if (ht == PG_F32) return vec ? vocab_rows_kernel<true, PG_F32, true> : vocab_rows_kernel<true, PG_F32, false>;
+  return vec ? vocab_rows_kernel<true, PG_BF16, true> : vocab_rows_kernel<true, PG_BF16, false>;
+}
+
+pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
+  pg_status st;
+  const bool list = g.ids != nullptr;
+  const bool vec = s.d % 8 == 0 && aligned(g.h, vec_bytes(s.h_dtype)) && aligned(g.W, vec_bytes(s.w_dtype));
+  const ArgsFn targets = s.h_dtype == PG_F32 ? (s.w_dtype == PG_F32 ? targets_fn<PG_F32, PG_F32>(list, vec) : targets_fn<PG_F32, PG_BF16>(list, vec))
+                                             : (s.w_dtype == PG_F32 ? targets_fn<PG_BF16, PG_F32>(list, vec) : targets_fn<PG_BF16, PG_BF16>(list, vec));
+  VocabMaps maps;
+  const int64_t ldw = g.Wp ? g.dp : s.d, ldh = g.hp ? g.dp : s.d;
+  if (g.Wp && (st = launch_split(g.W, s.w_dtype, s.V, s.d, g.dp, g.np_w, g.Wp, stream)) != PG_OK) return st;
+  if (!vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, 128)) return PG_ERR_CUDA;
+  for (int64_t row0 = 0; row0 < s.N; row0 += g.Nc) {
+    g.row0 = row0;
+    g.rows = static_cast<int>(std::min<int64_t>(g.Nc, s.N - row0));
+    g.first = row0 == 0;
+    g.last = row0 + g.Nc >= s.N;
+    const uint8_t* h = static_cast<const uint8_t*>(g.h) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.h_dtype));
+    if (g.hp && (st = launch_split(h, s.h_dtype, g.rows, s.d, g.dp, g.np_h, g.hp, stream)) != PG_OK) return st;
+    if (!vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, 128)) return PG_ERR_CUDA;
+    if (list)
+      targets<<<g.rows, 32 * std::min(kListWarps, (s.K + kListAtOnce - 1) / kListAtOnce), 0, stream>>>(g);
+    else
+      targets<<<(g.rows + 3) / 4, 128, 0, stream>>>(g);
+    if ((st = after_launch(1)) != PG_OK) return st;
+    const int64_t jobs = static_cast<int64_t>((g.rows + kTile - 1) / kTile) * ((s.V + kTile - 1) / kTile);
+    if (s.grad) {
+      if (!vocab_map(&maps.U, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, 128) ||
+          !vocab_map(&maps.Ust, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, 32) ||
+          (g.F && !vocab_map(&maps.F, g.F, g.np_f, g.rows, s.d, g.dp, g.Nc, 128)))
+        return PG_ERR_CUDA;
+      if (!g.F) maps.F = maps.U;
+      st = launch_product<kKeep>(maps, g, jobs, stream);
+    } else {
+      maps.U = maps.Ust = maps.F = maps.h;
+      st = launch_product<kSums>(maps, g, jobs, stream);
+    }
+    if (st != PG_OK) return st;
+    rows_fn(s.grad, s.h_dtype, s.d % 8 == 0 && aligned(g.h, vec_bytes(s.h_dtype)))<<<(g.rows + 31) / 32, 32 * kRowWarps, 0, stream>>>(g);
+    if ((st = after_launch(1)) != PG_OK) return st;
+    const int64_t units = static_cast<int64_t>(g.tiles2) * g.q + g.tiles3;
+    if (!s.grad || units == 0) continue;
+    VocabArgs b = g;
+    if (g.tiles2) b.tiles2 = (g.rows + kTile - 1) / kTile * g.nd;  // a last chunk has fewer rows
+    if ((st = launch_product<kGrads>(maps, b, static_cast<int64_t>(b.tiles2) * b.q + b.tiles3, stream)) != PG_OK) return st;
+    if (g.parts) {
+      const int64_t blocks = (static_cast<int64_t>(g.rows) * s.d + 255) / 256;
+      vocab_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(g);
+      if ((st = after_launch(1)) != PG_OK) return st;
+    }
+  }
+  return PG_OK;
+}
+
+pg_status check_sizes(const Sizes& s) {
+  if (s.N < 0 || s.N >= (1ll << 31) || s.V < 1 || s.V > kMaxVocab || s.d < 1 || s.d > kMaxVocabWidth || s.K < 1 || s.K > kMaxList)
+    return PG_ERR_SHAPE;
+  if (!real_dtype(s.h_dtype) || !real_dtype(s.w_dtype)) return PG_ERR_DTYPE;
+  if (s.grad && ((s.gh_dtype != -1 && !real_dtype(s.gh_dtype)) || (s.gw_dtype != -1 && !real_dtype(s.gw_dtype)))) return PG_ERR_DTYPE;
+  return PG_OK;
+}
+
+pg_status vocab_workspace(const Sizes& s, size_t* bytes) {
+  if (!bytes) return PG_ERR_NULL;
+  pg_status st = check_sizes(s);
+  if (st != PG_OK) return st;
+  VocabArgs g = {};
+  *bytes = s.N == 0 ? 0 : carve_vocab(nullptr, s, &g);
+  return PG_OK;
+}
+
+// What the four calls share, behind their own checks.
+struct Call {
+  Sizes s;
+  const void *h, *W;
+  const int32_t* targets;
+  const int32_t* ids;
+  const void* tlogits;
+  int t_dtype;
+  const float* row_weight;
+  float scale, inv_t, zl, grad_scale;
+  int accumulate;
+  float *loss, *lse;
+  void *gh, *gw;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* err;
+  cudaStream_t stream;
+};
+
+// An operand that TMA reads in place has to start on 16 bytes.
+bool operand_aligned(const void* p, int dtype, int d) { return aligned(p, needs_copy(dtype, d) ? dtype_bytes(dtype) : 16); }
+
+pg_status call_vocab(const Call& c) {
+  size_t need;
+  pg_status st = vocab_workspace(c.s, &need);
+  if (st != PG_OK) return st;
+  const bool list = c.targets == nullptr && c.s.K >= 1 && c.t_dtype >= 0;
+  if (list && !real_dtype(c.t_dtype)) return PG_ERR_DTYPE;
+  if (!std::isfinite(c.scale) || !std::isfinite(c.zl) || !std::isfinite(c.grad_scale) || !std::isfinite(c.inv_t) || !(c.inv_t > 0.f) ||
+      !std::isfinite(c.scale * c.inv_t * kLog2e))
+    return PG_ERR_UNSUPPORTED;
+  const bool has_w = c.s.grad && c.s.gw_dtype >= 0, has_h = c.s.grad && c.s.gh_dtype >= 0;
+  if (c.s.N == 0 && !(has_w && !c.accumulate)) return PG_OK;
+  if (has_w && !c.gw) return PG_ERR_NULL;
+  if (has_w && !aligned(c.gw, dtype_bytes(c.s.gw_dtype))) return PG_ERR_ALIGN;
+  if (c.s.N == 0) {
+    if (device_cc() != 103) return PG_ERR_DEVICE;
+    cudaError_t e = cudaMemsetAsync(c.gw, 0, static_cast<size_t>(c.s.V) * c.s.d * dtype_bytes(c.s.gw_dtype), c.stream);
+    return e == cudaSuccess ? PG_OK : cuda_fail(e);
+  }
+  if (!c.h || !c.W || (list ? !c.ids || !c.tlogits : !c.targets) || (has_h && !c.gh) || (!c.s.grad && !c.loss)) return PG_ERR_NULL;
+  if (!operand_aligned(c.h, c.s.h_dtype, c.s.d) || !operand_aligned(c.W, c.s.w_dtype, c.s.d) || !aligned(c.targets, 4) ||
+      !aligned(c.ids, 4) || (list && !aligned(c.tlogits, dtype_bytes(c.t_dtype))) || !aligned(c.row_weight, 4) || !aligned(c.loss, 4) ||
+      !aligned(c.lse, 4) || !aligned(c.err, 4) || (has_h && !aligned(c.gh, dtype_bytes(c.s.gh_dtype))) || !aligned(c.workspace, 16))
+    return PG_ERR_ALIGN;
+  if (!c.workspace || c.workspace_bytes < need) return PG_ERR_WORKSPACE;
+  if (device_cc() != 103) return PG_ERR_DEVICE;
+  if ((st = prepare_err(c.err, c.stream)) != PG_OK) return st;
+
+  VocabArgs g = {};
+  carve_vocab(static_cast<uint8_t*>(c.workspace), c.s, &g);
+  g.h = c.h;
+  g.W = c.W;
+  g.targets = list ? nullptr : c.targets;
+  g.ids = list ? c.ids : nullptr;
+  g.tlogits = c.tlogits;
+  g.t_dtype = c.t_dtype;
+  g.row_weight = c.row_weight;
+  g.loss = c.loss;
+  g.lse = c.lse;
+  g.err = c.err;
+  g.gh = c.gh;
+  g.gw = c.gw;
+  g.err_word = device_error_word();
+  g.accumulate = c.accumulate;
+  g.scale = c.scale * c.inv_t;
+  g.inv_t = c.inv_t;
+  g.k2 = c.scale * c.inv_t * kLog2e;
+  g.zl = c.zl;
+  g.grad_scale = c.grad_scale;
+  return run_vocab(g, c.s, c.stream);
+}
+
+}  // namespace
+}  // namespace pg
+
+using namespace pg;
+
+extern "C" pg_status pg_vocab_ce_workspace_size(int64_t N, int64_t V, int32_t d, int32_t h_dtype, int32_t w_dtype, size_t* bytes) {
+  return vocab_workspace({N, V, d, 1, h_dtype, w_dtype, -1, -1, false}, bytes);
+}
+
+extern "C" pg_status pg_vocab_ce_grad_workspace_size(int64_t N, int64_t V, int32_t d, int32_t h_dtype, int32_t w_dtype,
+                                                     int32_t gh_dtype, int32_t gw_dtype, size_t* bytes) {
+  return vocab_workspace({N, V, d, 1, h_dtype, w_dtype, gh_dtype, gw_dtype, true}, bytes);
+}
+
+extern "C" pg_status pg_vocab_distill_workspace_size(int64_t N, int64_t V, int32_t d, int32_t K, int32_t h_dtype, int32_t w_dtype,
+                                                     size_t* bytes) {
+  return vocab_workspace({N, V, d, K, h_dtype, w_dtype, -1, -1, false}, bytes);
+}
+
+extern "C" pg_status pg_vocab_distill_grad_workspace_size(int64_t N, int64_t V, int32_t d, int32_t K, int32_t h_dtype,
+                                                          int32_t w_dtype, int32_t gh_dtype, int32_t gw_dtype, size_t* bytes) {
+  return vocab_workspace({N, V, d, K, h_dtype, w_dtype, gh_dtype, gw_dtype, true}, bytes);
+}
+
+extern "C" pg_status pg_vocab_ce(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V, int32_t d,
+                                 const int32_t* targets, float scale, float z_loss, float* loss, float* lse, void* workspace,
+                                 size_t workspace_bytes, int32_t* err_index, pg_stream_t stream) {
+  Call c = {};
+  c.s = {N, V, d, 1, h_dtype, w_dtype, -1, -1, false};
+  c.h = h; c.W = W; c.targets = targets; c.t_dtype = -1;
+  c.scale = scale; c.inv_t = 1.f; c.zl = z_loss;
+  c.loss = loss; c.lse = lse;
+  c.workspace = workspace; c.workspace_bytes = workspace_bytes; c.err = err_index; c.stream = stream;
+  return call_vocab(c);
+}
+
+extern "C" pg_status pg_vocab_ce_grad(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V, int32_t d,
+                                      const int32_t* targets, float scale, float z_loss, const float* row_weight, float grad_scale,
+                                      float* loss, float* lse, void* grad_h, int32_t gh_dtype, void* grad_w, int32_t gw_dtype,
+                                      int32_t accumulate, void* workspace, size_t workspace_bytes, int32_t* err_index,
+                                      pg_stream_t stream) {
+  Call c = {};
+  c.s = {N, V, d, 1, h_dtype, w_dtype, gh_dtype, gw_dtype, true};
+  c.h = h; c.W = W; c.targets = targets; c.t_dtype = -1;
+  c.row_weight = row_weight;
+  c.scale = scale; c.inv_t = 1.f; c.zl = z_loss; c.grad_scale = grad_scale;
+  c.accumulate = accumulate;
+  c.loss = loss; c.lse = lse; c.gh = grad_h; c.gw = grad_w;
+  c.workspace = workspace; c.workspace_bytes = workspace_bytes; c.err = err_index; c.stream = stream;
+  return call_vocab(c);
+}
+
+extern "C" pg_status pg_vocab_distill(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V, int32_t d,
+                                      const int32_t* ids, const void* logits, int32_t logits_dtype, int32_t K, float scale,
+                                      float temperature, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                      int32_t* err_index, pg_stream_t stream) {
+  Call c = {};
+  c.s = {N, V, d, K, h_dtype, w_dtype, -1, -1, false};
+  if (!real_dtype(logits_dtype)) return PG_ERR_DTYPE;
+  c.h = h; c.W = W; c.ids = ids; c.tlogits = logits; c.t_dtype = logits_dtype;
+  c.scale = scale; c.inv_t = 1.f / temperature;
+  c.loss = loss; c.lse = lse;
+  c.workspace = workspace; c.workspace_bytes = workspace_bytes; c.err = err_index; c.stream = stream;
+  return call_vocab(c);
+}
+
+extern "C" pg_status pg_vocab_distill_grad(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V, int32_t d,
+                                           const int32_t* ids, const void* logits, int32_t logits_dtype, int32_t K, float scale,
+                                           float temperature, const float* row_weight, float grad_scale, float* loss, float* lse,
+                                           void* grad_h, int32_t gh_dtype, void* grad_w, int32_t gw_dtype, int32_t accumulate,
+                                           void* workspace, size_t workspace_bytes, int32_t* err_index, pg_stream_t stream) {
+  Call c = {};
+  c.s = {N, V, d, K, h_dtype, w_dtype, gh_dtype, gw_dtype, true};
+  if (!real_dtype(logits_dtype)) return PG_ERR_DTYPE;
+  c.h = h; c.W = W; c.ids = ids; c.tlogits = logits; c.t_dtype = logits_dtype;
+  c.row_weight = row_weight;
+  c.scale = scale; c.inv_t = 1.f / temperature; c.grad_scale = grad_scale;
+  c.accumulate = accumulate;
+  c.loss = loss; c.lse = lse; c.gh = grad_h; c.gw = grad_w;
+  c.workspace = workspace; c.workspace_bytes = workspace_bytes; c.err = err_index; c.stream = stream;
+  return call_vocab(c);
+}

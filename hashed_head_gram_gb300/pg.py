@@ -190,6 +190,24 @@ def _load():
     L.pg_orthogonalize_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
     L.pg_orthogonalize.restype = ctypes.c_int
     L.pg_orthogonalize.argtypes = [vp, i32, i32, i32, i32, i32, f32, f32, f32, f32, f32, vp, vp, sz, vp]
+    L.pg_vocab_ce_workspace_size.restype = ctypes.c_int
+    L.pg_vocab_ce_workspace_size.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(sz)]
+    L.pg_vocab_ce.restype = ctypes.c_int
+    L.pg_vocab_ce.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, f32, f32, vp, vp, vp, sz, vp, vp]
+    L.pg_vocab_ce_grad_workspace_size.restype = ctypes.c_int
+    L.pg_vocab_ce_grad_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    L.pg_vocab_ce_grad.restype = ctypes.c_int
+    L.pg_vocab_ce_grad.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, f32, f32, vp, f32, vp, vp, vp, i32, vp, i32, i32,
+                                   vp, sz, vp, vp]
+    L.pg_vocab_distill_workspace_size.restype = ctypes.c_int
+    L.pg_vocab_distill_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    L.pg_vocab_distill.restype = ctypes.c_int
+    L.pg_vocab_distill.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, vp, i32, i32, f32, f32, vp, vp, vp, sz, vp, vp]
+    L.pg_vocab_distill_grad_workspace_size.restype = ctypes.c_int
+    L.pg_vocab_distill_grad_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    L.pg_vocab_distill_grad.restype = ctypes.c_int
+    L.pg_vocab_distill_grad.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, vp, i32, i32, f32, f32, vp, f32, vp, vp, vp,
+                                        i32, vp, i32, i32, vp, sz, vp, vp]
     return L
 
 
@@ -587,7 +605,9 @@ __all__ = ["PgError", "TableDesc", "table_desc", "table_geometry", "canon_hash",
            "decode_state_size", "DecodeState", "decode_reset", "decode_lookup", "decode_conv_residual",
            "collision_workspace_size", "collision_counts", "launch_count", "device_error", "selftest_bounded_waits", "selftest_training_waits",
            "row_copy_window", "row_copy", "embed", "embed_grad_workspace_size", "embed_grad", "lookup_grad_workspace_size",
-           "lookup_grad", "orthogonalize_workspace_size", "orthogonalize", "lib",
+           "lookup_grad", "orthogonalize_workspace_size", "orthogonalize", "vocab_ce_workspace_size", "vocab_ce",
+           "vocab_ce_grad_workspace_size", "vocab_ce_grad", "vocab_distill_workspace_size", "vocab_distill",
+           "vocab_distill_grad_workspace_size", "vocab_distill_grad", "lib",
            "FLAT", "ENGRAM", "PAGEGRAM", "F32", "BF16", "NF4", "GATE_NONE", "GATE_SCALAR", "GATE_CONTEXT",
            "HASH_MULXOR", "HASH_TOY", "PG_NO_ROW"]
 
@@ -702,3 +722,139 @@ def orthogonalize(G: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, s
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.pg_orthogonalize(_at(G), _dtype(G), batch, m, n, steps, a, b, c, eps, scale, _at(out), _at(workspace),
                                  ws_bytes, _stream(stream)), "pg_orthogonalize")
+
+
+# ------------------------------------------------------------------- losses over the vocabulary
+
+
+def _here(*tensors):
+    """The calls run on the current device: a tensor of another one would be read through a foreign address."""
+    dev = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
+    for t in tensors:
+        _expect(t is None or (t.is_cuda and t.get_device() == dev), "tensors must live on the current CUDA device")
+
+
+def _hidden(h: torch.Tensor, W: torch.Tensor, rows):
+    _expect(h.dim() == 2 and W.dim() == 2 and h.shape[1] == W.shape[1], "h must be [N, d] and W [V, d]")
+    for name, t in rows.items():
+        _expect(t is None or (t.dtype == torch.float32 and t.shape == (h.shape[0],)), f"{name} must be float32 [N]")
+
+
+def _list(h: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor):
+    _expect(ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == h.shape[0], "teacher_ids must be int32 [N, K]")
+    _expect(logits.shape == ids.shape, "teacher_logits must be [N, K]")
+
+
+def _gradients(h: torch.Tensor, W: torch.Tensor, grad_h: Optional[torch.Tensor], grad_W: Optional[torch.Tensor]):
+    _expect(grad_h is None or grad_h.shape == h.shape, "grad_h must be [N, d]")
+    _expect(grad_W is None or grad_W.shape == W.shape, "grad_W must be [V, d]")
+    return -1 if grad_h is None else _dtype(grad_h), -1 if grad_W is None else _dtype(grad_W)
+
+
+def _index(err_index: Optional[torch.Tensor]):
+    _expect(err_index is None or (err_index.dtype == torch.int32 and err_index.numel() >= 1), "err_index must be an int32 tensor")
+
+
+def _code(dtype: Optional[int]) -> int:
+    return -1 if dtype is None else dtype
+
+
+def vocab_ce_workspace_size(N: int, V: int, d: int, h_dtype: int, w_dtype: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pg_vocab_ce_workspace_size(N, V, d, h_dtype, w_dtype, ctypes.byref(n)), "pg_vocab_ce_workspace_size")
+    return n.value
+
+
+def vocab_ce(h: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor, workspace: Optional[torch.Tensor],
+             scale: float = 1.0, z_loss: float = 0.0, lse: Optional[torch.Tensor] = None,
+             err_index: Optional[torch.Tensor] = None, stream=None):
+    """loss[i] = lse[i] - z[i, targets[i]] + z_loss * lse[i]^2 over the logits z = scale * h W^T, which are not
+    stored; h [N, d] and W [V, d] float32 or bfloat16, targets int32 [N] (outside [0, V): no target)."""
+    _hidden(h, W, {"loss": loss, "lse": lse})
+    _expect(targets.dtype == torch.int32 and targets.numel() == h.shape[0], "targets must be int32 [N]")
+    _index(err_index)
+    hd, wd = _dtype(h), _dtype(W)
+    _here(h, W, targets, loss, lse, workspace, err_index)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_vocab_ce(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(targets), scale, z_loss,
+                            _at(loss), _at(lse), _at(workspace), ws_bytes, _at(err_index), _stream(stream)), "pg_vocab_ce")
+
+
+def vocab_ce_grad_workspace_size(N: int, V: int, d: int, h_dtype: int, w_dtype: int, grad_h_dtype: Optional[int],
+                                 grad_W_dtype: Optional[int]) -> int:
+    """The gradients' dtypes: None for one that is not asked for."""
+    n = ctypes.c_size_t()
+    _check(_lib.pg_vocab_ce_grad_workspace_size(N, V, d, h_dtype, w_dtype, _code(grad_h_dtype), _code(grad_W_dtype),
+                                                ctypes.byref(n)), "pg_vocab_ce_grad_workspace_size")
+    return n.value
+
+
+def vocab_ce_grad(h: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss: Optional[torch.Tensor],
+                  grad_h: Optional[torch.Tensor], grad_W: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                  scale: float = 1.0, z_loss: float = 0.0, grad_scale: float = 1.0,
+                  row_weight: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  lse: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
+    """vocab_ce with the gradients of grad_scale * sum_i row_weight[i] * loss[i]: grad_h [N, d] and grad_W [V, d] (added
+    to what is there when accumulate is set), either of them None where it is not asked for."""
+    _hidden(h, W, {"loss": loss, "lse": lse, "row_weight": row_weight})
+    _expect(targets.dtype == torch.int32 and targets.numel() == h.shape[0], "targets must be int32 [N]")
+    _index(err_index)
+    hd, wd = _dtype(h), _dtype(W)
+    ghd, gwd = _gradients(h, W, grad_h, grad_W)
+    _here(h, W, targets, loss, lse, row_weight, grad_h, grad_W, workspace, err_index)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_vocab_ce_grad(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(targets), scale, z_loss,
+                                 _at(row_weight), grad_scale, _at(loss), _at(lse), _at(grad_h), ghd, _at(grad_W), gwd,
+                                 1 if accumulate else 0, _at(workspace), ws_bytes, _at(err_index), _stream(stream)),
+           "pg_vocab_ce_grad")
+
+
+def vocab_distill_workspace_size(N: int, V: int, d: int, K: int, h_dtype: int, w_dtype: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pg_vocab_distill_workspace_size(N, V, d, K, h_dtype, w_dtype, ctypes.byref(n)), "pg_vocab_distill_workspace_size")
+    return n.value
+
+
+def vocab_distill(h: torch.Tensor, W: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                  loss: torch.Tensor, workspace: Optional[torch.Tensor], scale: float = 1.0, temperature: float = 1.0,
+                  lse: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
+    """loss[i] = KL(softmax(teacher_logits[i] / temperature) over the tokens teacher_ids[i], softmax(z[i] / temperature)) with
+    z = scale * h W^T; teacher_ids int32 [N, K] (outside [0, V): no token), teacher_logits [N, K] float32 or bfloat16."""
+    _hidden(h, W, {"loss": loss, "lse": lse})
+    _list(h, teacher_ids, teacher_logits)
+    _index(err_index)
+    hd, wd, td = _dtype(h), _dtype(W), _dtype(teacher_logits)
+    _here(h, W, teacher_ids, teacher_logits, loss, lse, workspace, err_index)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_vocab_distill(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(teacher_ids),
+                                 _at(teacher_logits), td, teacher_ids.shape[1], scale, temperature, _at(loss), _at(lse),
+                                 _at(workspace), ws_bytes, _at(err_index), _stream(stream)), "pg_vocab_distill")
+
+
+def vocab_distill_grad_workspace_size(N: int, V: int, d: int, K: int, h_dtype: int, w_dtype: int, grad_h_dtype: Optional[int],
+                                      grad_W_dtype: Optional[int]) -> int:
+    """The gradients' dtypes: None for one that is not asked for."""
+    n = ctypes.c_size_t()
+    _check(_lib.pg_vocab_distill_grad_workspace_size(N, V, d, K, h_dtype, w_dtype, _code(grad_h_dtype), _code(grad_W_dtype),
+                                                     ctypes.byref(n)), "pg_vocab_distill_grad_workspace_size")
+    return n.value
+
+
+def vocab_distill_grad(h: torch.Tensor, W: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                       loss: Optional[torch.Tensor], grad_h: Optional[torch.Tensor], grad_W: Optional[torch.Tensor],
+                       workspace: Optional[torch.Tensor], scale: float = 1.0, temperature: float = 1.0,
+                       grad_scale: float = 1.0, row_weight: Optional[torch.Tensor] = None, accumulate: bool = False,
+                       lse: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
+    """vocab_distill with the gradients of grad_scale * sum_i row_weight[i] * loss[i], as in vocab_ce_grad."""
+    _hidden(h, W, {"loss": loss, "lse": lse, "row_weight": row_weight})
+    _list(h, teacher_ids, teacher_logits)
+    _index(err_index)
+    hd, wd, td = _dtype(h), _dtype(W), _dtype(teacher_logits)
+    ghd, gwd = _gradients(h, W, grad_h, grad_W)
+    _here(h, W, teacher_ids, teacher_logits, loss, lse, row_weight, grad_h, grad_W, workspace, err_index)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pg_vocab_distill_grad(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(teacher_ids),
+                                      _at(teacher_logits), td, teacher_ids.shape[1], scale, temperature, _at(row_weight),
+                                      grad_scale, _at(loss), _at(lse), _at(grad_h), ghd, _at(grad_W), gwd,
+                                      1 if accumulate else 0, _at(workspace), ws_bytes, _at(err_index), _stream(stream)),
+           "pg_vocab_distill_grad")

@@ -139,7 +139,8 @@ uint64_t pg_launch_count(void);
  * pg_selftest_bounded_waits (2048, 4096), and of pg_project_gate_conv (16384 = a conv item's wait
  * for the tiles of its m-blocks), and of pg_decode_step (32768 = a block's wait at the grid
  * barrier, 65536 = a wait for a row of W), and of the training calls (131072 = the gradients'
- * grid barrier, 262144 = a wait of pg_orthogonalize's products).
+ * grid barrier, 262144 = a wait of pg_orthogonalize's products, 524288 = one of the vocabulary
+ * losses' products).
  * Synchronizes the device. With clear != 0 the word is reset to 0.
  */
 pg_status pg_device_error(int32_t* code, int32_t clear);
@@ -754,6 +755,82 @@ pg_status pg_orthogonalize_workspace_size(int32_t batch, int32_t m, int32_t n, s
 pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batch, int32_t m, int32_t n, int32_t steps, float a,
                            float b, float c, float eps, float scale, void* out, void* workspace,
                            size_t workspace_bytes, pg_stream_t stream);
+
+/*
+ * Losses over the vocabulary: the other end of the model that the memory plugs into, where its last
+ * hidden states h [N, d] meet an output table W [V, d] (the embedding's own table where the two are
+ * tied: pg_embed_grad with accumulate adds the embedding's part to grad_w). The logits
+ *   z_ij = scale <h_i, W_j>
+ * are never stored: they exist tile by tile on chip. The gradient calls keep exp(z_ij - a reference of
+ * row i) for a bounded chunk of the rows in their workspace (2 GiB; at least 256 rows), so that every
+ * product runs once.
+ *
+ * pg_vocab_ce -- softmax cross entropy, one target t_i a row:
+ *   lse_i = log sum_j exp(z_ij);  loss_i = lse_i - z_{i,t_i} + z_loss lse_i^2
+ * pg_vocab_ce_grad -- loss and lse, and the gradients of
+ *   sum_i g_i loss_i,  g_i = grad_scale row_weight_i  (row_weight NULL: ones)
+ *   grad_h = scale dz W,  grad_w = scale dz^T h (+ what is there: accumulate != 0),
+ *   dz_ij = g_i ((1 + 2 z_loss lse_i) exp(z_ij - lse_i) - [j = t_i])
+ * pg_vocab_distill -- distillation from a teacher's top logits u_ik of K listed tokens j_ik: with
+ *   p_i = softmax(u_i / temperature) over the list, q_i = softmax(z_i / temperature) over the vocabulary,
+ *   lse_i = log sum_j exp(z_ij / temperature);  loss_i = sum_k p_ik (log p_ik - log q_i[j_ik])
+ * pg_vocab_distill_grad -- loss and lse, and the gradients of sum_i g_i loss_i (no factor temperature^2):
+ *   dz_ij = g_i / temperature (q_ij - sum of p_ik over k with j_ik = j)
+ *  h           device [N, d], PG_F32 or PG_BF16
+ *  W           device [V, d], PG_F32 or PG_BF16 (either with either)
+ *              h and W aligned to 16 bytes where they are bf16 with d % 8 == 0, else to their element
+ *  targets     device int32 [N]; one outside [0, V) is padding: the row has loss 0, lse 0, no gradient (a
+ *              zero row of grad_h), and its h may hold anything, infinities and NaN too
+ *  ids, logits device int32 [N, K]; PG_F32 or PG_BF16 [N, K]. A place whose token is outside [0, V) is padding
+ *              and takes no part; one whose logit is -infinity has weight 0; a row that has neither weight nor
+ *              token left is padding as above. A token listed twice counts with both weights
+ *  row_weight  device fp32 [N] or NULL. A weight of 0: no gradient, whatever the row holds
+ *  loss        device fp32 [N]; optional in the gradient calls. lse: device fp32 [N], optional
+ *  grad_h      device [N, d]; gh_dtype PG_F32, PG_BF16 or -1 (no such gradient; grad_h is not looked at)
+ *  grad_w      device [V, d]; gw_dtype likewise. Aligned to their elements; they must not overlap anything else
+ *  workspace   device, 16-byte aligned, >= the call's _workspace_size bytes (with the same sizes and types), scratch
+ *  err_index   device int32 [1], or NULL: the smallest row with a target or a listed token outside [0, V), else -1
+ * Sums are fp32. bf16 gradients take the logits' gradients in bf16 (2^-8 of an entry at most) as the tensor
+ * cores do; fp32 operands and fp32 gradients take every value as a sum of three bf16 pieces (24 bits), with three
+ * products of bf16 in place of one where the other operand is bf16, six where it is not. Equal inputs give
+ * equal bits.
+ * 0 <= N < 2^31, 1 <= V <= 2^24, 1 <= d <= 16384, 1 <= K <= 256 (else PG_ERR_SHAPE); scale, z_loss, grad_scale finite,
+ * temperature > 0 and neither it nor scale / temperature out of fp32's range (else PG_ERR_UNSUPPORTED). N == 0 enqueues
+ * nothing, but for zeros in grad_w without accumulate. A device wait that runs out (about a second) sets device
+ * error bit 524288; the outputs are then undefined.
+ */
+pg_status pg_vocab_ce_workspace_size(int64_t N, int64_t V, int32_t d, int32_t h_dtype, int32_t w_dtype, size_t* bytes);
+
+pg_status pg_vocab_ce(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V, int32_t d,
+                      const int32_t* targets, float scale, float z_loss, float* loss, float* lse, void* workspace,
+                      size_t workspace_bytes, int32_t* err_index, pg_stream_t stream);
+
+pg_status pg_vocab_ce_grad_workspace_size(int64_t N, int64_t V, int32_t d, int32_t h_dtype, int32_t w_dtype,
+                                          int32_t gh_dtype, int32_t gw_dtype, size_t* bytes);
+
+pg_status pg_vocab_ce_grad(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V,
+                           int32_t d, const int32_t* targets, float scale, float z_loss, const float* row_weight,
+                           float grad_scale, float* loss, float* lse, void* grad_h, int32_t gh_dtype, void* grad_w,
+                           int32_t gw_dtype, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                           int32_t* err_index, pg_stream_t stream);
+
+pg_status pg_vocab_distill_workspace_size(int64_t N, int64_t V, int32_t d, int32_t K, int32_t h_dtype, int32_t w_dtype,
+                                          size_t* bytes);
+
+pg_status pg_vocab_distill(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V,
+                           int32_t d, const int32_t* ids, const void* logits, int32_t logits_dtype, int32_t K,
+                           float scale, float temperature, float* loss, float* lse, void* workspace,
+                           size_t workspace_bytes, int32_t* err_index, pg_stream_t stream);
+
+pg_status pg_vocab_distill_grad_workspace_size(int64_t N, int64_t V, int32_t d, int32_t K, int32_t h_dtype,
+                                               int32_t w_dtype, int32_t gh_dtype, int32_t gw_dtype, size_t* bytes);
+
+pg_status pg_vocab_distill_grad(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V,
+                                int32_t d, const int32_t* ids, const void* logits, int32_t logits_dtype, int32_t K,
+                                float scale, float temperature, const float* row_weight, float grad_scale, float* loss,
+                                float* lse, void* grad_h, int32_t gh_dtype, void* grad_w, int32_t gw_dtype,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes, int32_t* err_index,
+                                pg_stream_t stream);
 
 /*
  * Diagnostic, no counterpart on the pages: the memory access pattern of a lookup on its

@@ -1,0 +1,221 @@
+"""The losses over the vocabulary against plain implementations in 64 bits: pg_vocab_ce, pg_vocab_distill and their
+gradients.
+
+Tolerances. A logit is an fp32 sum of d products: within (d + 16) 2^-23 of the sum of the products' magnitudes
+(tensor cores may cut where others round; fp32 operands are three bf16 pieces, 2^-24 each, and three of the nine
+products of pieces are left out, 2^-23 together: the 16). exp takes a relative error of 2^-22, of its argument's rounding
+(2^-23 of the logits' size, twice) and a sum of the V terms 300 roundings at most (128 in a tile, then tiles spread over
+16 warps). So lse and log p have E = 2 (d + 16) 2^-23 mag + 2^-22 (2 max|z| + 80). A gradient takes dz with p off by
+E relative, a rounding of each operand it is made of (bf16: U, and f h for grad_W, 2^-8 each; pieces: 2^-22 in all),
+fp32 sums ((terms + 16) 2^-23) and its own rounding.
+"""
+import math
+
+import pytest
+import torch
+
+from tests._helpers import F32_TOL
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _pg():
+    from hashed_head_gram_gb300 import pg
+    return pg
+
+
+def half_step(dtype):
+    return 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+
+
+def offset_view(t, shift):
+    buf = torch.empty(t.numel() + shift, dtype=t.dtype, device=t.device)
+    v = buf[shift:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+def make(seed, N, V, d, hdt, wdt, dev, spread=1.0, K=0, pad=0.1):
+    """Normed hidden states that lean towards their target's row, targets with padding, teacher lists."""
+    gen = torch.Generator().manual_seed(seed)
+    W = torch.randn(V, d, generator=gen) * (spread / math.sqrt(d))
+    t = torch.randint(0, V, (N,), generator=gen, dtype=torch.int32)
+    h = torch.randn(N, d, generator=gen) + torch.rand(N, 1, generator=gen) * 6 * W[t.long()] / spread ** 2
+    gone = torch.rand(N, generator=gen) < pad
+    t[gone] = torch.where(torch.rand(int(gone.sum()), generator=gen) < 0.5, -1, V).to(torch.int32)
+    out = [h.to(hdt).to(dev), W.to(wdt).to(dev), t.to(dev)]
+    if K:
+        ids = torch.randint(0, V, (N, K), generator=gen, dtype=torch.int32)
+        ids[torch.rand(N, K, generator=gen) < 0.1] = -1
+        ids[gone] = V + 7
+        u = torch.randn(N, K, generator=gen) * 3
+        u[torch.rand(N, K, generator=gen) < 0.05] = float("-inf")
+        out += [ids.to(dev), u.to(dev)]
+    return out
+
+
+def reference(h, W, target=None, ids=None, u=None, scale=1.0, T=1.0, z_loss=0.0, weight=None, grad_scale=1.0, grads=True):
+    """loss, lse, dh, dW in 64 bits, and dz and the error that E leaves in it."""
+    h, W = h.double(), W.double()
+    s = scale / T
+    z = s * (h @ W.T)
+    N, V = z.shape
+    mag = abs(s) * (h.abs() @ W.abs().T).amax(1)
+    lse = torch.logsumexp(z, 1)
+    q = torch.zeros_like(z)
+    if ids is None:
+        keep = (target >= 0) & (target < V)
+        at = torch.nonzero(keep)[:, 0]
+        q[at, target[at].long()] = 1.0
+        ent = torch.zeros(N, dtype=torch.float64, device=z.device)
+    else:
+        there = (ids >= 0) & (ids < V)
+        u = torch.where(there, u.double() / T, -math.inf)
+        keep = (u > -math.inf).any(1)
+        p = torch.softmax(torch.where(keep[:, None], u, 0.0), 1)
+        p = torch.where(there & keep[:, None], p, 0.0)
+        q.scatter_add_(1, torch.where(there, ids, 0).long(), p)
+        ent = torch.where(p > 0, p * torch.log(torch.where(p > 0, p, 1.0)), 0.0).sum(1)
+    loss = torch.where(keep, ent - (q * z).nan_to_num().sum(1) + lse + z_loss * lse * lse, 0.0)
+    lse_out = torch.where(keep, lse, 0.0)
+    E = 2 * (h.shape[1] + 16) * 2.0 ** -23 * mag + 2.0 ** -22 * (2 * z.abs().amax(1) + 80)
+    if ids is not None:  # the teacher's own softmax in fp32
+        E = E + 2.0 ** -22 * (4 + torch.where(u > -math.inf, u.abs(), 0.0).amax(1))
+    r = dict(loss=loss, lse=lse_out, E=E, keep=keep)
+    if grads:
+        g = grad_scale * s * keep.double()
+        if weight is not None:
+            g = g * weight.double()
+        beta = 1 + 2 * z_loss * lse
+        prob = torch.softmax(z, 1)
+        dz = torch.where(keep[:, None], g[:, None] * (beta[:, None] * prob - q), 0.0)
+        off = torch.where(keep[:, None], (g.abs() * E)[:, None] * (beta.abs()[:, None] * prob + q * (ids is not None)), 0.0)
+        hk = torch.where(keep[:, None], h, 0.0)
+        r.update(dh=dz @ W, dW=dz.T @ hk, dz=dz, off=off, h=hk, W=W)
+    return r
+
+
+def close(got, want, tol, what):
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float(((got.double() - want).abs() / tol)[bad].max())} of the tolerance"
+
+
+def distance(got, want):
+    return float((got.double() - want).norm())
+
+
+def check_values(r, loss, lse, z_loss=0.0):
+    E = torch.where(r["keep"], r["E"], 0.0)
+    close(lse, r["lse"], E + 2.0 ** -23 * r["lse"].abs(), "lse")
+    close(loss, r["loss"], E * (2 + 2 * abs(z_loss) * r["lse"].abs()) + 2.0 ** -22 * r["loss"].abs(), "loss")
+
+
+def check_grads(r, dh, dW, old=None):
+    dz, off, W, h = r["dz"], r["off"], r["W"], r["h"]
+    N, V = dz.shape
+    if dh is not None:
+        each = half_step(BF16) if dh.dtype == BF16 else 2.0 ** -22
+        tol = (off + each * (dz.abs() + off)) @ W.abs() + (V + 16) * 2.0 ** -23 * (dz.abs() @ W.abs())
+        tol = tol + half_step(dh.dtype) * (r["dh"].abs() + tol)
+        close(dh, r["dh"], tol, "grad_h")
+        # independent roundings add in squares: two of 2^-8 / sqrt(3) at most (bf16). What E leaves in p comes on
+        # top: dz = g (beta p - 1) at a target with p near 1 is the difference of two numbers near g, so an
+        # error of E in p is E / |beta p - 1| of dz (a vocabulary of one token: p = 1, beta - 1 = 2 z_loss lse)
+        assert distance(dh, r["dh"]) <= (2.0 ** -8 if dh.dtype == BF16 else F32_TOL) * float(r["dh"].norm()) + float((off @ W.abs()).norm())
+        assert (dh[~r["keep"]] == 0).all()
+    if dW is not None:
+        each = 2 * half_step(BF16) if dW.dtype == BF16 else 2.0 ** -21
+        tol = (off + each * (dz.abs() + off)).T @ h.abs() + (N + 16) * 2.0 ** -23 * (dz.abs().T @ h.abs())
+        want = r["dW"] if old is None else r["dW"] + old.double()
+        chunk = 0.0 if old is None else half_step(F32) * old.double().abs()
+        tol = tol + chunk + half_step(dW.dtype) * (want.abs() + tol)
+        close(dW, want, tol, "grad_W")
+        if old is None:  # three of them
+            assert distance(dW, r["dW"]) <= (2.0 ** -8 if dW.dtype == BF16 else F32_TOL) * float(r["dW"].norm()) + float((off.T @ h.abs()).norm())
+
+
+def run_ce(h, W, t, ghd=None, gwd=None, shift=0, weight=None, accumulate=None, **kw):
+    """vocab_ce, or with gradient dtypes vocab_ce_grad: loss, lse, grad_h, grad_W. Outputs and workspace start as NaN."""
+    pg = _pg()
+    N, d = h.shape
+    V, dev = W.shape[0], h.device
+    nan = lambda shape, t: offset_view(torch.full(shape, float("nan"), dtype=t, device=dev), shift)  # noqa: E731
+    loss, lse = nan((N,), F32), nan((N,), F32)
+    hd, wd = pg.dtype_code(h.dtype), pg.dtype_code(W.dtype)
+    if ghd is None and gwd is None:
+        ws = torch.full((pg.vocab_ce_workspace_size(N, V, d, hd, wd),), 0xFF, dtype=torch.uint8, device=dev)
+        pg.vocab_ce(h, W, t, loss, ws, lse=lse, **kw)
+        return loss, lse, None, None
+    gh = None if ghd is None else nan((N, d), ghd)
+    gw = None if gwd is None else nan((V, d), gwd) if accumulate is None else accumulate
+    size = pg.vocab_ce_grad_workspace_size(N, V, d, hd, wd, None if ghd is None else pg.dtype_code(ghd),
+                                           None if gwd is None else pg.dtype_code(gwd))
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=dev)
+    pg.vocab_ce_grad(h, W, t, loss, gh, gw, ws, lse=lse, row_weight=weight, accumulate=accumulate is not None, **kw)
+    assert pg.device_error() == 0
+    return loss, lse, gh, gw
+
+
+def run_distill(h, W, ids, u, ghd=None, gwd=None, weight=None, **kw):
+    pg = _pg()
+    N, d = h.shape
+    V, K, dev = W.shape[0], ids.shape[1], h.device
+    nan = lambda shape, t: torch.full(shape, float("nan"), dtype=t, device=dev)  # noqa: E731
+    loss, lse = nan((N,), F32), nan((N,), F32)
+    hd, wd = pg.dtype_code(h.dtype), pg.dtype_code(W.dtype)
+    if ghd is None and gwd is None:
+        ws = torch.full((pg.vocab_distill_workspace_size(N, V, d, K, hd, wd),), 0xFF, dtype=torch.uint8, device=dev)
+        pg.vocab_distill(h, W, ids, u, loss, ws, lse=lse, **kw)
+        return loss, lse, None, None
+    gh = None if ghd is None else nan((N, d), ghd)
+    gw = None if gwd is None else nan((V, d), gwd)
+    size = pg.vocab_distill_grad_workspace_size(N, V, d, K, hd, wd, None if ghd is None else pg.dtype_code(ghd),
+                                                None if gwd is None else pg.dtype_code(gwd))
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=dev)
+    pg.vocab_distill_grad(h, W, ids, u, loss, gh, gw, ws, lse=lse, row_weight=weight, **kw)
+    assert pg.device_error() == 0
+    return loss, lse, gh, gw
+
+
+SHAPES = [(1, 1, 1), (1, 1000, 64), (3, 7, 5), (8, 4096, 256), (200, 300, 72), (256, 256, 128), (257, 513, 130), (300, 1023, 515),
+          (700, 5000, 96), (31, 70001, 40)]
+
+
+@pytest.mark.parametrize("hdt,wdt", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("N,V,d", SHAPES)
+def test_ce(cuda, N, V, d, hdt, wdt):
+    h, W, t = make(N + V + d, N, V, d, hdt, wdt, cuda)
+    r = reference(h, W, t, scale=0.8, z_loss=1e-3, grads=False)
+    loss, lse, _, _ = run_ce(h, W, t, scale=0.8, z_loss=1e-3)
+    assert _pg().device_error() == 0
+    check_values(r, loss, lse, 1e-3)
+
+
+@pytest.mark.parametrize("hdt,wdt,ghd,gwd", [(BF16, BF16, BF16, BF16), (F32, F32, F32, F32), (BF16, F32, BF16, F32),
+                                             (F32, BF16, BF16, BF16), (BF16, BF16, F32, F32), (BF16, BF16, BF16, F32)])
+@pytest.mark.parametrize("N,V,d", SHAPES)
+def test_ce_grad(cuda, N, V, d, hdt, wdt, ghd, gwd):
+    h, W, t = make(2 * N + V + d, N, V, d, hdt, wdt, cuda)
+    weight = torch.rand(N, generator=torch.Generator().manual_seed(5)).to(cuda) * 2 - 0.3
+    r = reference(h, W, t, scale=1.2, z_loss=1e-3, weight=weight, grad_scale=1.0 / N)
+    loss, lse, dh, dW = run_ce(h, W, t, ghd, gwd, weight=weight, scale=1.2, z_loss=1e-3, grad_scale=1.0 / N)
+    check_values(r, loss, lse, 1e-3)
+    check_grads(r, dh, dW)
+
+
+@pytest.mark.parametrize("hdt,wdt,ghd,gwd", [(BF16, BF16, BF16, BF16), (F32, F32, F32, F32), (BF16, F32, BF16, F32)])
+@pytest.mark.parametrize("N,V,d,K", [(1, 1, 1, 1), (1, 1000, 64, 20), (3, 7, 5, 6), (200, 300, 72, 33), (257, 513, 130, 100),
+                                     (700, 5000, 96, 256), (31, 70001, 40, 3)])
+@pytest.mark.parametrize("T", [1.0, 2.5])
+def test_distill(cuda, N, V, d, K, T, hdt, wdt, ghd, gwd):
+    h, W, _, ids, u = make(3 * N + V + d, N, V, d, hdt, wdt, cuda, K=K)
+    if hdt == BF16:
+        u = u.to(BF16)
+    r = reference(h, W, ids=ids, u=u, scale=1.1, T=T, grad_scale=1.0 / N)
+    loss, lse, _, _ = run_distill(h, W, ids, u, scale=1.1, temperature=T)
+    check_values(r, loss, lse)
+    loss, lse, dh, dW = run_distill(h, W, ids, u, ghd, gwd, scale=1.1, temperature=T, grad_scale=1.0 / N)
+    check_values(r, loss, lse)
+    check_grads(r, dh, dW)
