@@ -34,6 +34,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "pg_conv_math.cuh"
 #include "pg_umma.cuh"
 #include "pg_vec.h"
 
@@ -49,23 +50,41 @@ constexpr int64_t kKeepBytes = 2ll << 30;  // of U
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
 constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
 
+constexpr int kPrepThreads = 256;
 constexpr int kTile = 256;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;            // warps 0 and 1 issue copies and products, 4 to 11 are the epilogue's
+constexpr int kEpiFirst = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kStages = 3;
 constexpr int kOperandBytes = 128 * kBK * 2;
-constexpr int kStageBytes = 4096;        // an epilogue warp's: 32 rows of 128 bytes
+constexpr int kStageBytes = 4096;        // an epilogue warp's: 32 rows of 128 bytes, or two buffers of 32 rows of 64
 constexpr size_t kRing = static_cast<size_t>(kStages) * 2 * kOperandBytes;
 constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kStageBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: fp32 sums, bf16 operands
                             (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
 
+// A tensor core cuts what falls below its sum where an fp32 addition rounds, so a sum's error grows with its length, to
+// one side: 1.4e-6 of the logits at d = 2560, 4e-6 with the six products of fp32 operands. Where an fp32 result comes
+// of it, sums longer than this many k-blocks are made in groups, which the epilogue adds up in registers; and the
+// products of pieces run from the smallest to the largest, so that only the largest's additions count.
+constexpr int kGroup = 6;                // bf16 operands (48 additions: 4e-7)
+constexpr int kGroupPieces = 2;          // fp32 operands or gradients
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Sums in groups take 128 registers a thread in the epilogue: its two warpgroups take over what the first does not need.
+constexpr int kLaunchRegs = 168, kIssueRegs = 72, kEpiRegs = 216;
+static_assert(kIssueRegs * 128 + kEpiRegs * 256 <= kLaunchRegs * kThreads, "a warpgroup would wait for registers that nobody gives up");
+
 constexpr float kSumLimit = 0x1p57f;     // of a tile's row; above it the row changes its reference
 
+// The kernels of a call but its first are scheduled while the one before still runs. Each waits for that one's end
+// before it reads or writes memory, and reads what earlier kernels wrote by coherent loads.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct VocabMaps {
-  CUtensorMap h, W, U, Ust, F;           // U for loads and (boxes of 32 rows) for stores; F: f h
+  CUtensorMap h, W, U, Ust, F;           // U for loads and (boxes of 32 rows and columns) for stores; F: f h
 };
 
 struct VocabArgs {
@@ -96,6 +115,7 @@ struct VocabArgs {
   // schedule of the gradients' products
   int q, tiles2, tiles3, nd, light, delta, heavy;
   int passes_h, passes_w;                // piece products of dh, dW
+  int group, group_h, group_w;           // k-blocks that one sum in TMEM takes: logits, dh, dW
 };
 
 // ------------------------------------------------------------------- fp32 values as bf16 pieces
@@ -110,7 +130,18 @@ __device__ __forceinline__ uint16_t take_piece(float& x) {
   return b;
 }
 
-// Products of pieces (i, j) with i + j below the larger count: what is left out is below 2^-8 of that of the last kept.
+__device__ __forceinline__ uint4 take_pieces(float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = take_piece(x[2 * k]), hi = take_piece(x[2 * k + 1]);
+    w[k] = lo | hi << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Products of pieces (i, j) with i + j below the larger count, the smallest first: what is left out is below 2^-8 of
+// the smallest kept.
 __host__ __device__ __forceinline__ int passes_of(int a, int b) {
   const int m = a > b ? a : b;
   int n = 0;
@@ -120,39 +151,34 @@ __host__ __device__ __forceinline__ int passes_of(int a, int b) {
 }
 
 __device__ __forceinline__ void piece_of(int a, int b, int pass, int* i, int* j) {
-  const int m = a > b ? a : b;
   int n = 0;
-  for (*i = 0; *i < a; ++*i)
-    for (*j = 0; *j < b; ++*j)
-      if (*i + *j < m && n++ == pass) return;
+  for (int both = (a > b ? a : b) - 1; both >= 0; --both)
+    for (*i = 0; *i <= both; ++*i) {
+      *j = both - *i;
+      if (*i < a && *j < b && n++ == pass) return;
+    }
 }
 
-// dst [pieces][rows][dp] from src [rows][d], zeros behind a row's end. Also the copy of bf16 rows that TMA cannot
-// take as they are (d % 8 != 0). Bound by memory.
-template <int DT>
-__global__ void __launch_bounds__(256)
-    vocab_split_kernel(const void* src, int64_t rows, int d, int dp, int pieces, __nv_bfloat16* dst) {
-  const int64_t per_row = dp / 8;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= rows * per_row) return;
-  const int64_t r = at / per_row;
+// dst [pieces][rows][dp] from src [rows][d], zeros behind a row's end, 8 columns a thread. Also the copy of bf16 rows
+// that TMA cannot take as they are (d % 8 != 0). Bound by memory.
+template <int DT, bool VEC>
+__device__ void split_rows(const void* src, int64_t rows, int d, int dp, int pieces, __nv_bfloat16* dst, int64_t block) {
+  const int per_row = dp / 8;
+  const int64_t at = block * kPrepThreads + threadIdx.x, r = at / per_row;
+  if (r >= rows) return;
   const int c = static_cast<int>(at - r * per_row) * 8;
-  float x[8];
+  float x[8] = {};
+  if (VEC) {
+    if (c < d) load_cols<DT, 8>(src, r * d + c, x);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float y[1] = {0.f};
-    if (c + k < d) load_cols<DT, 1>(src, r * d + c + k, y);
-    x[k] = y[0];
-  }
-  for (int p = 0; p < pieces; ++p) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = take_piece(x[2 * k]), hi = take_piece(x[2 * k + 1]);
-      w[k] = lo | hi << 16;
+    for (int k = 0; k < 8; ++k) {
+      float y[1] = {0.f};
+      if (c + k < d) load_cols<DT, 1>(src, r * d + c + k, y);
+      x[k] = y[0];
     }
-    *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = take_pieces(x);
 }
 
 // --------------------------------------------------------------------------- the targets' logits
@@ -194,10 +220,10 @@ __device__ __forceinline__ void warp_dots(const VocabArgs& g, int64_t i, const i
 // A reference that is no logit: +infinity stands for a row without a target.
 __device__ __forceinline__ float as_reference(float z) { return z == INFINITY ? __int_as_float(0x7fffffff) : z; }
 
-// Cross entropy: one warp a row, two rows of W and h read once.
+// Cross entropy: one warp a row, a row of h and one of W.
 template <int HT, int WT, bool VEC>
-__global__ void __launch_bounds__(128) vocab_target_kernel(const __grid_constant__ VocabArgs g) {
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+__device__ void target_rows(const VocabArgs& g, int block) {
+  const int r = block * (kPrepThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= g.rows) return;
   const int64_t i = g.row0 + r, t = __ldg(g.targets + i);
   const bool valid = t >= 0 && t < g.V;
@@ -217,14 +243,15 @@ __global__ void __launch_bounds__(128) vocab_target_kernel(const __grid_constant
 
 // Distillation: one block a row. The first warp forms the teacher's softmax, all warps the listed tokens' logits,
 // four rows of W at a time.
-constexpr int kListWarps = 8, kListAtOnce = 4;
+constexpr int kListAtOnce = 4;
 
 template <int HT, int WT, bool VEC>
-__global__ void __launch_bounds__(32 * kListWarps) vocab_list_kernel(const __grid_constant__ VocabArgs g) {
+__device__ void list_row(const VocabArgs& g, int r) {
   __shared__ int32_t s_id[kMaxList];
   __shared__ float s_w[kMaxList], s_z[kMaxList];
   __shared__ int s_any;
-  const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int warps = kPrepThreads / 32;
   const int64_t i = g.row0 + r;
   constexpr int kPer = kMaxList / 32;
   float u[kPer];
@@ -290,7 +317,7 @@ __global__ void __launch_bounds__(32 * kListWarps) vocab_list_kernel(const __gri
   }
   __syncthreads();
   // what the gradient puts at each token: a token's later places count with its first
-  for (int k = threadIdx.x; k < g.K; k += blockDim.x) {
+  for (int k = threadIdx.x; k < g.K; k += kPrepThreads) {
     float w = s_w[k];
     const int32_t id = s_id[k];
     if (id < 0 || !some) {
@@ -330,6 +357,24 @@ __global__ void __launch_bounds__(32 * kListWarps) vocab_list_kernel(const __gri
   }
 }
 
+// What the products need beforehand: the pieces of W (first chunk) and of the chunk's h, and the rows' targets.
+template <int HT, int WT, bool VEC, bool LIST>
+__global__ void __launch_bounds__(kPrepThreads) vocab_prepare_kernel(const __grid_constant__ VocabArgs g, int blocks_w, int blocks_h) {
+  grid_dep_wait();
+  grid_dep_launch();
+  int block = blockIdx.x;
+  if (block < blocks_w) {
+    split_rows<WT, VEC>(g.W, g.V, g.d, g.dp, g.np_w, g.Wp, block);
+  } else if ((block -= blocks_w) < blocks_h) {
+    const uint8_t* h = static_cast<const uint8_t*>(g.h) + g.row0 * g.d * (HT == PG_F32 ? 4 : 2);
+    split_rows<HT, VEC>(h, g.rows, g.d, g.dp, g.np_h, g.hp, block);
+  } else if (LIST) {
+    list_row<HT, WT, VEC>(g, block - blocks_h);
+  } else {
+    target_rows<HT, WT, VEC>(g, block - blocks_h);
+  }
+}
+
 // --------------------------------------------------------------------------------- products
 
 enum VocabKind { kSums, kKeep, kGrads };  // logits without and with U; the gradients
@@ -341,6 +386,7 @@ struct VocabJob {
   int np_p, np_q, passes;
   int i, j;                              // tile's row and column
   int kb0, kb1;
+  int group;                             // k-blocks of one sum in TMEM
   int product, part;                     // 0: logits, 1: dh, 2: dW
 };
 
@@ -365,6 +411,7 @@ __device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps
     w->j = static_cast<int>(t / nm);
     w->kb0 = 0;
     w->kb1 = (g.d + kBK - 1) / kBK;
+    w->group = g.group;
     w->product = w->part = 0;
     return true;
   } else {
@@ -384,6 +431,7 @@ __device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps
       w->j = t % g.nd;
       w->kb0 = static_cast<int>(all * w->part / g.q);
       w->kb1 = static_cast<int>(all * (w->part + 1) / g.q);
+      w->group = g.group_h;
       w->product = 1;
       return true;
     }
@@ -406,6 +454,7 @@ __device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps
     w->j = static_cast<int>(t % g.nd);
     w->kb0 = 0;
     w->kb1 = (g.rows + kBK - 1) / kBK;
+    w->group = g.group_w;
     w->product = 2;
     w->part = 0;
     return true;
@@ -417,6 +466,15 @@ struct VocabBars {
   uint32_t tmem;
   int abort;
 };
+
+// `wait` without a call, across which the sums that the epilogue holds in registers would have to be saved.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (poll<true>(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  while (!poll<true>(bar, parity))
+    if (*abort || now_ns() - t0 > kAsyncWaitNs) return false;
+  return true;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -432,106 +490,130 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// All but the latest of this thread's stores have read their shared memory.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 64 at a time. u = 2^(k2 z - c) in fp32 for the
-// row's sum, and to U through the warp's shared memory (32 rows of 128 bytes, swizzled as the TMA store reads them).
-template <bool KEEP>
-__device__ __forceinline__ void logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row,
-                                            int row0, int64_t col0, float k2, float c, bool dead, float* sum) {
+// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time, from TMEM or (GROUPS) from the sums in
+// registers. u = 2^(k2 z - c) in fp32 for the row's sum, and to U through the warp's shared memory (32 rows of 64 bytes,
+// swizzled as the TMA store reads them; two such buffers in turn, so that a store reads one while the other fills).
+template <bool KEEP, bool GROUPS>
+__device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, const float (&z)[GROUPS ? 128 : 1],
+                                             uint8_t* s_row, int row0, int64_t col0, float c, bool dead) {
   const int lane = threadIdx.x & 31;
-  float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const int64_t c0 = col0 + h * 64;
-    if (c0 >= g.V) break;
-    uint32_t r[64];
-    tmem_load(from + h * 64, r);
-    tmem_load(from + h * 64 + 32, r + 32);
-    tmem_wait(r);
-    float x[64];
+  const uint64_t k2 = pk(g.k2, g.k2), c2 = pk(-c, -c);
+  const bool some_dead = KEEP && __any_sync(0xffffffffu, dead);
+  uint64_t sum[2] = {0, 0};
+  if (KEEP && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // of an earlier tile
+  uint32_t r[GROUPS ? 1 : 2][GROUPS ? 1 : 32];
+  if constexpr (!GROUPS) tmem_load(from, r[0]);
 #pragma unroll
-    for (int k = 0; k < 64; ++k) x[k] = exp2_fast(fmaf(__uint_as_float(r[k]), k2, -c));
-    if (c0 + 64 > g.V) {
+  for (int ch = 0; ch < 4; ++ch) {
+    const int64_t c0 = col0 + ch * 32;
+    if (c0 >= g.V) break;
+    if constexpr (!GROUPS) {
+      tmem_wait(r[ch & 1]);
+      if (ch < 3) tmem_load(from + (ch + 1) * 32, r[(ch + 1) & 1]);
+    }
+    float x[32];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      uint64_t y;
+      if constexpr (GROUPS) y = pk(z[ch * 32 + k], z[ch * 32 + k + 1]);
+      else y = pk(__uint_as_float(r[ch & 1][k]), __uint_as_float(r[ch & 1][k + 1]));
+      upk(fma2(y, k2, c2), x[k], x[k + 1]);
+      x[k] = exp2_fast(x[k]);
+      x[k + 1] = exp2_fast(x[k + 1]);
+    }
+    if (c0 + 32 > g.V) {
       const int left = static_cast<int>(g.V - c0);
 #pragma unroll
-      for (int k = 0; k < 64; ++k) x[k] = k < left ? x[k] : 0.f;
+      for (int k = 0; k < 32; ++k) x[k] = k < left ? x[k] : 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < 64; k += 2) {
-      s0 += x[k];
-      s1 += x[k + 1];
-    }
+    for (int k = 0; k < 32; k += 2) sum[k / 2 & 1] = add2(sum[k / 2 & 1], pk(x[k], x[k + 1]));
     if constexpr (KEEP) {
-#pragma unroll 1
       for (int p = 0; p < g.np_u; ++p) {
-        uint32_t w[32];
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          w[k] = two_bf16(x[2 * k], x[2 * k + 1]);
-          if (p + 1 < g.np_u) {
+        for (int k = 0; k < 16; ++k) w[k] = two_bf16(x[2 * k], x[2 * k + 1]);
+        if (p + 1 < g.np_u) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
             x[2 * k] -= __uint_as_float(w[k] << 16);
             x[2 * k + 1] -= __uint_as_float(w[k] & 0xFFFF0000u);
           }
-          w[k] = dead ? 0u : w[k];  // (a row without a target may hold anything)
         }
+        if (some_dead) {  // (a row without a target may hold anything)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = dead ? 0u : w[k];
+        }
+        uint8_t* buf = s_row + ((ch * g.np_u + p) & 1) * (kStageBytes / 2);
         if (lane == 0) stores_read();
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(s_row + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)) =
               make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) store_box(&maps.Ust, smem_addr(s_row), static_cast<int>(c0), row0, p);
-        __syncwarp();
+        if (lane == 0) store_box(&maps.Ust, smem_addr(buf), static_cast<int>(c0), row0, p);
       }
     }
   }
-  *sum = s0 + s1;
+  if constexpr (!GROUPS) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  float lo, hi;
+  upk(add2(sum[0], sum[1]), lo, hi);
+  return lo + hi;
 }
 
-template <bool KEEP>
-__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
-                                                uint32_t from, int row0, int half, float c) {
+template <bool KEEP, bool GROUPS>
+__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w,
+                                                const float (&z)[GROUPS ? 128 : 1], uint8_t* s_row, uint32_t from, int row0, int half,
+                                                float c) {
   const int lane = threadIdx.x & 31;
   const int64_t col0 = static_cast<int64_t>(w.j) * kTile + half * 128;
+  if (row0 >= g.rows || col0 >= g.V) return;
   const bool dead = row0 + lane >= g.rows || c == INFINITY;
-  float sum = 0.f;
-  if (row0 < g.rows && col0 < g.V) logits_half<KEEP>(g, maps, from, s_row, row0, col0, g.k2, c, dead, &sum);
+  float sum = logits_half<KEEP, GROUPS>(g, maps, from, z, s_row, row0, col0, c, dead);
   float ref = c;
   const bool over = !dead && !(sum <= kSumLimit);
   if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the tile's largest for a reference
     float top = -INFINITY;
-#pragma unroll 1
-    for (int h = 0; h < 4; ++h) {
-      uint32_t r[32];
-      tmem_load(from + h * 32, r);
-      tmem_wait(r);
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (col0 + h * 32 + k < g.V) top = fmaxf(top, __uint_as_float(r[k]) * g.k2);
+    for (int h = 0; h < 4; ++h) {
+      uint32_t r[GROUPS ? 1 : 32];
+      if constexpr (!GROUPS) {
+        tmem_load(from + h * 32, r);
+        tmem_wait(r);
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        float y;
+        if constexpr (GROUPS) y = z[h * 32 + k];
+        else y = __uint_as_float(r[k]);
+        if (col0 + h * 32 + k < g.V) top = fmaxf(top, y * g.k2);
+      }
     }
     if (over) ref = top == -INFINITY ? 0.f : top;
     if (KEEP && lane == 0) stores_done();  // the same places are written again
     __syncwarp();
-    logits_half<KEEP>(g, maps, from, s_row, row0, col0, g.k2, ref, dead, &sum);
+    sum = logits_half<KEEP, GROUPS>(g, maps, from, z, s_row, row0, col0, ref, dead);
   }
-  if (row0 + lane < g.rows)
-    g.sums[(2ll * w.j + half) * g.Nc + row0 + lane] = make_float2(ref, sum);
+  if (row0 + lane < g.rows) g.sums[(2ll * w.j + half) * g.Nc + row0 + lane] = make_float2(ref, sum);
 }
 
 // A gradient's tile. TMEM gives a lane one row; global memory wants neighbouring lanes on one row, so 32 columns
 // at a time pass through the warp's shared memory.
-__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob& w, uint8_t* s_row, uint32_t from, int row0,
-                                              int half) {
+template <bool GROUPS>
+__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob& w, const float (&z)[GROUPS ? 128 : 1], uint8_t* s_row,
+                                              uint32_t from, int row0, int half) {
   const int lane = threadIdx.x & 31;
   const bool dh = w.product == 1, part = dh && g.parts;
   const int64_t rows = dh ? g.rows : g.V;
   if (row0 >= rows) return;
   float f = 1.f;
-  if (dh && !part) f = row0 + lane < rows ? __ldg(g.f + row0 + lane) : 0.f;
+  if (dh && !part) f = row0 + lane < rows ? g.f[row0 + lane] : 0.f;
   // where the tile goes, and what is added to it
   void* dst;
   int dtype;
@@ -556,13 +638,18 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
   }
   const bool vec = g.d % 4 == 0 && reinterpret_cast<uintptr_t>(dst) % (dtype == PG_F32 ? 16 : 8) == 0 &&
                    (!add32 || reinterpret_cast<uintptr_t>(add32) % 16 == 0);
-#pragma unroll 1
+#pragma unroll(GROUPS ? 4 : 1)
   for (int ch = 0; ch < 4; ++ch) {
     const int c0 = w.j * kTile + half * 128 + ch * 32;
     if (c0 >= g.d) break;
     uint32_t r[32];
-    tmem_load(from + ch * 32, r);
-    tmem_wait(r);
+    if constexpr (GROUPS) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(z[ch * 32 + k]);
+    } else {
+      tmem_load(from + ch * 32, r);
+      tmem_wait(r);
+    }
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -575,7 +662,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
     __syncwarp();
     if (vec) {  // (d % 4 == 0: four columns are inside or outside together)
       const int lc = lane & 7, col = c0 + lc * 4;
-#pragma unroll
+#pragma unroll(GROUPS ? 1 : 8)
       for (int k = 0; k < 8; ++k) {
         const int lr = 4 * k + (lane >> 3);
         if (row0 + lr >= rows || col >= g.d) continue;
@@ -595,7 +682,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
       }
     } else {
       const int col = c0 + lane;
-#pragma unroll 4
+#pragma unroll(GROUPS ? 1 : 4)
       for (int lr = 0; lr < 32; ++lr) {
         if (row0 + lr >= rows || col >= g.d) break;
         float v = *reinterpret_cast<const float*>(s_row + lr * 128 + (((lane >> 2) ^ (lr & 7)) << 4) + (lane & 3) * 4);
@@ -609,7 +696,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
   }
 }
 
-template <int KIND>
+template <int KIND, bool GROUPS>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_product_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabArgs g) {
   extern __shared__ uint8_t s_raw[];
@@ -641,98 +728,129 @@ __global__ void __launch_bounds__(kThreads, 1)
   pair_sync();  // both CTAs' barriers and TMEM exist before any remote use
   fence_after();
   const uint32_t tmem = bars->tmem;
+  grid_dep_wait();
+  grid_dep_launch();
 
   int stage = 0, acc = 0;
   uint32_t ring_phase = 0, acc_phase = 0;
   bool fine = true;
   VocabJob w;
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kEpiFirst) {
+    if constexpr (GROUPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 0 && lane == 0) {
       for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
         const int p0 = w.i * kTile + static_cast<int>(rank) * 128, q0 = w.j * kTile + static_cast<int>(rank) * 128;
-        for (int kb = w.kb0; fine && kb < w.kb1; ++kb)
-          for (int pass = 0; pass < w.passes; ++pass) {
-            if (!wait<true>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
-              fine = false;
-              break;
-            }
+        for (int k0 = w.kb0; k0 < w.kb1; k0 += w.group) {
+          const int k1 = min(k0 + w.group, w.kb1);
+          for (int pass = 0; fine && pass < w.passes; ++pass) {
             int zp = 0, zq = 0;
             if (w.passes > 1) piece_of(w.np_p, w.np_q, pass, &zp, &zq);
-            const uint32_t full = smem_addr(&bars->full[stage]);
-            const uint32_t dp = smem_addr(ring + stage * (2 * kOperandBytes)), dq = dp + kOperandBytes;
-            const uint32_t bar = in_cta(full, 0);
-            if (rank == 0) bar_expect(full, 2 * 2 * kOperandBytes);
-            load_operand<true, 128>(dp, w.P, w.P, w.p_mn, p0, kb * kBK, zp, bar);
-            load_operand<true, 128>(dq, w.Q, w.Q, w.q_mn, q0, kb * kBK, zq, bar);
-            if (++stage == kStages) {
-              stage = 0;
-              ring_phase ^= 1u;
+            for (int kb = k0; kb < k1; ++kb) {
+              if (!wait<true>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
+                fine = false;
+                break;
+              }
+              const uint32_t full = smem_addr(&bars->full[stage]);
+              const uint32_t dp = smem_addr(ring + stage * (2 * kOperandBytes)), dq = dp + kOperandBytes;
+              const uint32_t bar = in_cta(full, 0);
+              if (rank == 0) bar_expect(full, 2 * 2 * kOperandBytes);
+              load_operand<true, 128>(dp, w.P, w.P, w.p_mn, p0, kb * kBK, zp, bar);
+              load_operand<true, 128>(dq, w.Q, w.Q, w.q_mn, q0, kb * kBK, zq, bar);
+              if (++stage == kStages) {
+                stage = 0;
+                ring_phase ^= 1u;
+              }
             }
           }
+          if (!fine) break;
+        }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (warp == 1 && lane == 0 && rank == 0) {
       for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
-        if (!wait<true>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
-          fine = false;
-          break;
-        }
-        fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * kTile);
         const uint32_t idesc = kIdesc | (w.p_mn ? 1u << 15 : 0u) | (w.q_mn ? 1u << 16 : 0u);
         // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
         // groups of an MN-major tile
         const uint32_t step_p = w.p_mn ? 2048 >> 4 : 32 >> 4, step_q = w.q_mn ? 2048 >> 4 : 32 >> 4;
         const uint32_t half_p = w.p_mn ? 4 * step_p : kOperandBytes / 2 >> 4, half_q = w.q_mn ? 4 * step_q : kOperandBytes / 2 >> 4;
-        const int blocks = (w.kb1 - w.kb0) * w.passes;
-        for (int kb = 0; kb < blocks; ++kb) {
-          if (!wait<true>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
+        for (int k0 = w.kb0; fine && k0 < w.kb1; k0 += w.group) {
+          if (!wait<true>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
             fine = false;
             break;
           }
           fence_after();
-          const uint32_t sp = smem_addr(ring + stage * (2 * kOperandBytes));
-          const uint64_t dp = operand_desc(sp, w.p_mn), dq = operand_desc(sp + kOperandBytes, w.q_mn);
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * kTile);
+          const int blocks = (min(k0 + w.group, w.kb1) - k0) * w.passes;
+          for (int kb = 0; kb < blocks; ++kb) {
+            if (!wait<true>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
+              fine = false;
+              break;
+            }
+            fence_after();
+            const uint32_t sp = smem_addr(ring + stage * (2 * kOperandBytes));
+            const uint64_t dp = operand_desc(sp, w.p_mn), dq = operand_desc(sp + kOperandBytes, w.q_mn);
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
-                          (kb | k) != 0);
-          commit<true>(smem_addr(&bars->empty[stage]));
-          if (++stage == kStages) {
-            stage = 0;
-            ring_phase ^= 1u;
+            for (int k = 0; k < kBK / 16; ++k)
+              mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
+                            (kb | k) != 0);
+            commit<true>(smem_addr(&bars->empty[stage]));
+            if (++stage == kStages) {
+              stage = 0;
+              ring_phase ^= 1u;
+            }
           }
+          if (!fine) break;
+          commit<true>(smem_addr(&bars->acc_full[acc]));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!fine) break;
-        commit<true>(smem_addr(&bars->acc_full[acc]));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
     }
   } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* s_row = ring + kRing + (warp - 2) * kStageBytes;
+    if constexpr (GROUPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int quarter = warp & 3, half = (warp - kEpiFirst) >> 2;
+    uint8_t* s_row = ring + kRing + (warp - kEpiFirst) * kStageBytes;
     for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
       const int row0 = w.i * kTile + static_cast<int>(rank) * 128 + quarter * 32;
       float c = INFINITY;
-      if (KIND != kGrads && row0 + lane < g.rows) c = __ldg(g.c + row0 + lane);
-      if (!__all_sync(0xffffffffu, wait<true>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
-        fine = false;
-        break;
+      if (KIND != kGrads && row0 + lane < g.rows) c = g.c[row0 + lane];
+      float z[GROUPS ? 128 : 1];
+      const uint32_t warp_from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+      for (int k0 = w.kb0; k0 < w.kb1; k0 += w.group) {
+        if (!__all_sync(0xffffffffu, wait_inline(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
+          fine = false;
+          break;
+        }
+        fence_after();
+        const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
+        if constexpr (GROUPS) {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t r[32];
+            tmem_load(from + ch * 32, r);
+            tmem_wait(r);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z[ch * 32 + k] = k0 == w.kb0 ? __uint_as_float(r[k]) : z[ch * 32 + k] + __uint_as_float(r[k]);
+          }
+        } else if constexpr (KIND == kGrads) {
+          grad_epilogue<false>(g, w, z, s_row, from, row0, half);
+        } else {
+          logits_epilogue<KIND == kKeep, false>(g, maps, w, z, s_row, from, row0, half, c);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           in_cta(smem_addr(&bars->acc_empty[acc]), 0))
+                       : "memory");
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-      fence_after();
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kTile + half * 128);
-      if constexpr (KIND == kGrads) grad_epilogue(g, w, s_row, from, row0, half);
-      else logits_epilogue<KIND == kKeep>(g, maps, w, s_row, from, row0, half, c);
-      fence_before();
-      __syncwarp();
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         in_cta(smem_addr(&bars->acc_empty[acc]), 0))
-                     : "memory");
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      if (!fine) break;
+      if constexpr (GROUPS) {
+        if constexpr (KIND == kGrads) grad_epilogue<true>(g, w, z, s_row, 0, row0, half);
+        else logits_epilogue<KIND == kKeep, true>(g, maps, w, z, s_row, 0, row0, half, c);
+      }
     }
     if (KIND == kKeep && lane == 0) stores_done();
   }
@@ -770,21 +888,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- rows, once their sums are there
 
-constexpr int kRowWarps = 16;
+constexpr int kRowWarps = 16, kRowsPer = 8;
 
-// 32 rows a block: their sums over all tiles (a lane a row, tiles spread over the warps, joined in warp order), lse and
-// loss; for the gradients f, the targets' places of U, and f h.
+// 8 rows a block: their sums over all tiles (four lanes of each of 16 warps share a row's; joined in a fixed order), lse
+// and loss; for the gradients f, the targets' places of U, and f h (two warps a row).
 template <bool GRAD, int HT, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid_constant__ VocabArgs g) {
-  __shared__ float s_ref[kRowWarps][32], s_sum[kRowWarps][32];
-  __shared__ int s_moved[kRowWarps][32];
-  __shared__ float s_to[32], s_f[32], s_lse[32], s_beta[32];
-  __shared__ int s_fix[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * 32, r = r0 + lane;
+  __shared__ float s_ref[kRowWarps][kRowsPer], s_sum[kRowWarps][kRowsPer];
+  __shared__ int s_moved[kRowWarps][kRowsPer], s_fix[kRowsPer];
+  __shared__ float s_to[kRowsPer], s_f[kRowsPer], s_lse[kRowsPer], s_beta[kRowsPer];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (kRowsPer - 1);
+  const int r0 = blockIdx.x * kRowsPer, r = r0 + k;
   const bool in = r < g.rows;
+  grid_dep_wait();
+  grid_dep_launch();
   const float c = in ? g.c[r] : INFINITY;
-  const int64_t segs = (g.V + 127) / 128;
+  const int segs = static_cast<int>((g.V + 127) / 128);
   float ref = c, sum = 0.f;
   int moved = 0;
   auto join = [&](float ref2, float sum2) {
@@ -798,131 +917,139 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     }
   };
   if (in && c != INFINITY) {
+    const float2* at = g.sums + r;
 #pragma unroll 8
-    for (int64_t s = warp; s < segs; s += kRowWarps) {
-      const float2 v = __ldcg(g.sums + s * g.Nc + r);
+    for (int s = warp * 4 + lane / kRowsPer; s < segs; s += 4 * kRowWarps) {
+      const float2 v = at[static_cast<int64_t>(s) * g.Nc];
       moved |= v.x != c;
       join(v.x, v.y);
     }
   }
-  s_ref[warp][lane] = ref;
-  s_sum[warp][lane] = sum;
-  s_moved[warp][lane] = moved;
+#pragma unroll
+  for (int o = kRowsPer; o < 32; o *= 2) {
+    const float ref2 = __shfl_down_sync(0xffffffffu, ref, o), sum2 = __shfl_down_sync(0xffffffffu, sum, o);
+    moved |= __shfl_down_sync(0xffffffffu, moved, o);
+    join(ref2, sum2);
+  }
+  if (lane < kRowsPer) {
+    s_ref[warp][k] = ref;
+    s_sum[warp][k] = sum;
+    s_moved[warp][k] = moved;
+  }
   __syncthreads();
-  if (warp == 0) {
-    for (int k = 1; k < kRowWarps; ++k) {
-      join(s_ref[k][lane], s_sum[k][lane]);
-      moved |= s_moved[k][lane];
+  if (threadIdx.x < kRowsPer && in) {
+    for (int w = 1; w < kRowWarps; ++w) {
+      join(s_ref[w][k], s_sum[w][k]);
+      moved |= s_moved[w][k];
     }
-    const bool alive = in && c != INFINITY;
+    const bool alive = c != INFINITY;
     const float lse2 = ref + log2f(sum), lse = lse2 * kLn2;
-    if (in) {
-      const int64_t i = g.row0 + r;
-      if (g.lse) g.lse[i] = alive ? lse : 0.f;
-      if (g.loss) g.loss[i] = alive ? g.a[r] + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;
-      if (GRAD) {
-        float weight = alive ? g.grad_scale * g.scale : 0.f;
-        if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
-        float beta = 1.f + 2.f * g.zl * lse;
-        if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);  // (its part of U is divided by it)
-        const float to = moved ? lse2 : c;
-        const float f = weight == 0.f ? 0.f : weight * beta * exp2f(to - lse2);
-        g.f[r] = f;
-        s_f[lane] = f;
-        s_to[lane] = to;
-        s_lse[lane] = lse2;
-        s_beta[lane] = beta;
-        // a row without weight must not bring its infinities and NaN into dW
-        s_fix[lane] = weight == 0.f && !(fabsf(lse2) < INFINITY) ? 2 : moved;
-        if (!alive) s_fix[lane] = 3;  // (U's row is zero already)
-      }
+    const int64_t i = g.row0 + r;
+    if (g.lse) g.lse[i] = alive ? lse : 0.f;
+    if (g.loss) g.loss[i] = alive ? g.a[r] + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;
+    if (GRAD) {
+      float weight = alive ? g.grad_scale * g.scale : 0.f;
+      if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
+      float beta = 1.f + 2.f * g.zl * lse;
+      if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);  // (its part of U is divided by it)
+      const float to = moved ? lse2 : c;
+      const float f = weight == 0.f ? 0.f : weight * beta * exp2f(to - lse2);
+      g.f[r] = f;
+      s_f[k] = f;
+      s_to[k] = to;
+      s_lse[k] = lse2;
+      s_beta[k] = beta;
+      // a row without weight must not bring its infinities and NaN into dW; a row without a target is zero already
+      s_fix[k] = !alive ? 3 : weight == 0.f && !(fabsf(lse2) < INFINITY) ? 2 : moved;
     }
   }
   if (!GRAD) return;
   __syncthreads();
-  for (int k = warp; k < 32 && r0 + k < g.rows; k += kRowWarps) {
-    const int row = r0 + k, fix = s_fix[k];
-    const float f = s_f[k], to = s_to[k];
-    if (fix == 1 || fix == 2) {
-      for (int64_t at = lane * 8; at < g.Vp; at += 256) {
-        const float by = fix == 2 ? 0.f : exp2f(__ldcg(g.sums + (at >> 7) * g.Nc + row).x - to);
-        float x[8] = {};
-        for (int p = 0; p < g.np_u; ++p) {
-          float y[8];
-          read_cols<PG_BF16, 8>(g.U, (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at, y);
+  const int mine = warp % kRowsPer, part = warp / kRowsPer, row = r0 + mine;
+  constexpr int kLanes = 32 * (kRowWarps / kRowsPer);
+  const bool some = row < g.rows;
+  const int fix = some ? s_fix[mine] : 3;
+  const float f = some ? s_f[mine] : 0.f, to = some ? s_to[mine] : 0.f;
+  if (fix == 1 || fix == 2) {
+    for (int64_t at = (part * 32 + lane) * 8; at < g.Vp; at += kLanes * 8) {
+      const float by = fix == 2 ? 0.f : exp2f(g.sums[(at >> 7) * g.Nc + row].x - to);
+      float x[8] = {};
+      for (int p = 0; p < g.np_u; ++p) {
+        float y[8];
+        read_cols<PG_BF16, 8>(g.U, (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at, y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] += y[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fix == 2 || at + e >= g.V ? 0.f : x[e] * by;
-        for (int p = 0; p < g.np_u; ++p) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = take_piece(x[2 * e]), hi = take_piece(x[2 * e + 1]);
-            w[e] = lo | hi << 16;
-          }
-          *reinterpret_cast<uint4*>(g.U + (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int e = 0; e < 8; ++e) x[e] += y[e];
       }
-      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fix == 2 || at + e >= g.V ? 0.f : x[e] * by;
+      for (int p = 0; p < g.np_u; ++p)
+        *reinterpret_cast<uint4*>(g.U + (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at) = take_pieces(x);
     }
-    if (fix < 2) {
-      const float peak = exp2f(s_lse[k] - to) / s_beta[k];
-      for (int e = lane; e < g.K; e += 32) {
-        const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
-        if (w == -1.f || w == 0.f) continue;
-        const int64_t t = g.ids ? g.ids[(g.row0 + row) * g.K + e] : g.targets[g.row0 + row];
-        float x = exp2f(g.zk[static_cast<int64_t>(row) * g.K + e] - to) - w * peak;
-        for (int p = 0; p < g.np_u; ++p)
-          reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + t] = take_piece(x);
-      }
+  }
+  __syncthreads();
+  if (!some) return;
+  if (fix < 2) {
+    const float peak = exp2f(s_lse[mine] - to) / s_beta[mine];
+    for (int e = part * 32 + lane; e < g.K; e += kLanes) {
+      const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
+      if (w == -1.f || w == 0.f) continue;
+      const int64_t t = g.ids ? __ldg(g.ids + (g.row0 + row) * g.K + e) : __ldg(g.targets + g.row0 + row);
+      float x = exp2f(g.zk[static_cast<int64_t>(row) * g.K + e] - to) - w * peak;
+      for (int p = 0; p < g.np_u; ++p)
+        reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + t] = take_piece(x);
     }
-    if (g.F) {
-      constexpr int kStep = VEC ? 8 : 1;
-      for (int col = lane * 8; col < g.dp; col += 256) {
-        float x[8];
-        if (VEC) {
-          float y[kStep];
+  }
+  if (!g.F) return;
+  for (int col = (part * 32 + lane) * 8; col < g.dp; col += kLanes * 8) {
+    float x[8] = {};
+    if (VEC) {
+      if (col < g.d) load_cols<HT, VEC ? 8 : 1>(g.h, (g.row0 + row) * g.d + col, reinterpret_cast<float(&)[VEC ? 8 : 1]>(x));
+    } else {
 #pragma unroll
-          for (int e = 0; e < kStep; ++e) y[e] = 0.f;
-          if (col < g.d) load_cols<HT, kStep>(g.h, (g.row0 + row) * g.d + col, y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = y[e % kStep];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float y[1] = {0.f};
-            if (col + e < g.d) load_cols<HT, 1>(g.h, (g.row0 + row) * g.d + col + e, y);
-            x[e] = y[0];
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
-        for (int p = 0; p < g.np_f; ++p) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = take_piece(x[2 * e]), hi = take_piece(x[2 * e + 1]);
-            w[e] = lo | hi << 16;
-          }
-          *reinterpret_cast<uint4*>(g.F + (static_cast<int64_t>(p) * g.Nc + row) * g.dp + col) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        float y[1] = {0.f};
+        if (col + e < g.d) load_cols<HT, 1>(g.h, (g.row0 + row) * g.d + col + e, y);
+        x[e] = y[0];
       }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
+    for (int p = 0; p < g.np_f; ++p)
+      *reinterpret_cast<uint4*>(g.F + (static_cast<int64_t>(p) * g.Nc + row) * g.dp + col) = take_pieces(x);
   }
 }
 
-// dh from its q parts.
+// dh from its q parts, COLS columns a thread.
+template <int COLS>
 __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__ VocabArgs g) {
-  const int64_t n = static_cast<int64_t>(g.rows) * g.d, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= n) return;
-  float x = 0.f;
-  for (int p = 0; p < g.q; ++p) x += g.parts[static_cast<int64_t>(p) * g.Nc * g.d + at];
-  const float f = g.f[at / g.d];
-  x = f == 0.f ? 0.f : f * x;
-  if (g.gh_dtype == PG_F32) static_cast<float*>(g.gh)[g.row0 * g.d + at] = x;
-  else static_cast<__nv_bfloat16*>(g.gh)[g.row0 * g.d + at] = __float2bfloat16_rn(x);
+  grid_dep_wait();
+  grid_dep_launch();
+  const uint32_t per_row = g.d / COLS, n = static_cast<uint32_t>(g.rows) * per_row, t = blockIdx.x * 256u + threadIdx.x;
+  if (t >= n) return;
+  const uint32_t r = t / per_row;
+  const int64_t at = static_cast<int64_t>(t) * COLS;
+  float x[COLS] = {};
+#pragma unroll 4
+  for (int p = 0; p < g.q; ++p) {
+    const float* from = g.parts + static_cast<int64_t>(p) * g.Nc * g.d + at;
+    if constexpr (COLS == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(from);
+      x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
+    } else {
+      x[0] += *from;
+    }
+  }
+  const float f = g.f[r];
+#pragma unroll
+  for (int e = 0; e < COLS; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
+  const int64_t to = g.row0 * g.d + at;
+  if constexpr (COLS == 4) {
+    if (g.gh_dtype == PG_F32) *reinterpret_cast<float4*>(static_cast<float*>(g.gh) + to) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.gh) + to) = make_uint2(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]));
+  } else {
+    if (g.gh_dtype == PG_F32) static_cast<float*>(g.gh)[to] = x[0];
+    else static_cast<__nv_bfloat16*>(g.gh)[to] = __float2bfloat16_rn(x[0]);
+  }
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -947,6 +1074,8 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   g->tiles3 = has_w ? static_cast<int>(nv * g->nd) : 0;
   g->passes_h = g->gh_dtype == PG_F32 ? passes_of(g->np_u, g->np_w) : 1;
   g->passes_w = g->gw_dtype == PG_F32 ? passes_of(g->np_u, g->np_f) : 1;
+  g->group_h = g->gh_dtype == PG_F32 ? kGroupPieces : 1 << 30;  // (a bf16 gradient's own rounding is far above)
+  g->group_w = g->gw_dtype == PG_F32 ? kGroupPieces : 1 << 30;
   const double cost3 = static_cast<double>(kn) * g->passes_w;
   double best = 0;
   g->q = 0;
@@ -994,6 +1123,9 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->np_w = s.w_dtype == PG_F32 ? 3 : 1;
   g->np_u = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32 ? 3 : 1;
   g->np_f = s.gw_dtype == PG_F32 ? 3 : 1;
+  const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 ? kGroupPieces : kGroup;
+  const int groups = (blocks + longest - 1) / longest;
+  g->group = (blocks + groups - 1) / groups;
   const int64_t tiles = (s.V + kTile - 1) / kTile;
   int64_t most = s.grad ? kKeepBytes / (g->np_u * g->Vp * 2) : kMaxForwardRows;
   most = std::min(most, kSumBytes / (16 * tiles));
@@ -1024,24 +1156,24 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   return at + 128;
 }
 
-// [pieces, rows, cols] bf16 with row stride ld, boxes of 64 columns, 128-byte swizzle.
+// [pieces, rows, cols] bf16 with row stride ld, in boxes of box_cols columns (as wide as the swizzle) and box_rows rows.
 bool vocab_map(CUtensorMap* map, const void* ptr, int pieces, int64_t rows, int64_t cols, int64_t ld, int64_t piece_rows,
-               int box_rows) {
+               int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(pieces)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(piece_rows) * ld * 2};
-  cuuint32_t box[3] = {kLine, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int kMaxDevices = 64;
 
 // CTA pairs of the kernel that are resident at once on the current device.
-template <int KIND>
+template <int KIND, bool GROUPS>
 pg_status vocab_units(int* units) {
   static std::atomic<int> known[kMaxDevices];
   int dev = 0;
@@ -1050,7 +1182,11 @@ pg_status vocab_units(int* units) {
   if (dev < 0 || dev >= kMaxDevices) return PG_ERR_DEVICE;
   *units = known[dev].load(std::memory_order_relaxed);
   if (*units) return PG_OK;
-  auto kern = vocab_product_kernel<KIND>;
+  auto kern = vocab_product_kernel<KIND, GROUPS>;
+  cudaFuncAttributes attrs;
+  e = cudaFuncGetAttributes(&attrs, kern);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (GROUPS && attrs.numRegs < kLaunchRegs) return PG_ERR_UNSUPPORTED;  // its warpgroups share out this many
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchAttribute attr[1];
@@ -1072,10 +1208,39 @@ pg_status vocab_units(int* units) {
   return PG_OK;
 }
 
-template <int KIND>
+// A kernel that is scheduled while the one before it in the call still runs (early), of one CTA or pairs.
+template <typename... Params, typename... Args>
+pg_status launch_next(void (*kern)(Params...), int64_t blocks, int threads, size_t smem, bool pair, bool early, cudaStream_t stream,
+                      const Args&... args) {
+  if (blocks >= (1ll << 31)) return PG_ERR_SHAPE;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (early) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e == cudaSuccess ? after_launch(1) : cuda_fail(e);
+}
+
+template <int KIND, bool GROUPS>
 pg_status launch_product(const VocabMaps& maps, const VocabArgs& g, int64_t jobs, cudaStream_t stream) {
   int units;
-  pg_status st = vocab_units<KIND>(&units);
+  pg_status st = vocab_units<KIND, GROUPS>(&units);
   if (st != PG_OK) return st;
   units = static_cast<int>(std::min<int64_t>(units, jobs));
   VocabArgs a = g;
@@ -1087,36 +1252,16 @@ pg_status launch_product(const VocabMaps& maps, const VocabArgs& g, int64_t jobs
     const double cost3 = static_cast<double>((a.rows + kBK - 1) / kBK) * a.passes_w;
     a.delta = a.heavy ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(cost2 / cost3 + 0.5), a.tiles3 / a.light)) : 0;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * static_cast<unsigned>(units));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, vocab_product_kernel<KIND>, maps, a);
-  if (e != cudaSuccess) return cuda_fail(e);
-  return after_launch(1);
+  return launch_next(vocab_product_kernel<KIND, GROUPS>, 2ll * units, kThreads, kSmem, true, true, stream, maps, a);
 }
 
-pg_status launch_split(const void* src, int dtype, int64_t rows, int d, int dp, int pieces, __nv_bfloat16* dst, cudaStream_t stream) {
-  const int64_t blocks = (rows * (dp / 8) + 255) / 256;
-  if (blocks >= (1ll << 31)) return PG_ERR_SHAPE;
-  auto fn = dtype == PG_F32 ? vocab_split_kernel<PG_F32> : vocab_split_kernel<PG_BF16>;
-  fn<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(src, rows, d, dp, pieces, dst);
-  return after_launch(1);
-}
-
+using PrepareFn = void (*)(const VocabArgs, int, int);
 using ArgsFn = void (*)(const VocabArgs);
 
 template <int HT, int WT>
-ArgsFn targets_fn(bool list, bool vec) {
-  if (list) return vec ? vocab_list_kernel<HT, WT, true> : vocab_list_kernel<HT, WT, false>;
-  return vec ? vocab_target_kernel<HT, WT, true> : vocab_target_kernel<HT, WT, false>;
+PrepareFn prepare_fn(bool list, bool vec) {
+  if (list) return vec ? vocab_prepare_kernel<HT, WT, true, true> : vocab_prepare_kernel<HT, WT, false, true>;
+  return vec ? vocab_prepare_kernel<HT, WT, true, false> : vocab_prepare_kernel<HT, WT, false, false>;
 }
 
 ArgsFn rows_fn(bool grad, int ht, bool vec) {
@@ -1128,50 +1273,55 @@ ArgsFn rows_fn(bool grad, int ht, bool vec) {
 pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
   pg_status st;
   const bool list = g.ids != nullptr;
-  const bool vec = s.d % 8 == 0 && aligned(g.h, vec_bytes(s.h_dtype)) && aligned(g.W, vec_bytes(s.w_dtype));
-  const ArgsFn targets = s.h_dtype == PG_F32 ? (s.w_dtype == PG_F32 ? targets_fn<PG_F32, PG_F32>(list, vec) : targets_fn<PG_F32, PG_BF16>(list, vec))
-                                             : (s.w_dtype == PG_F32 ? targets_fn<PG_BF16, PG_F32>(list, vec) : targets_fn<PG_BF16, PG_BF16>(list, vec));
+  const bool vec_h = s.d % 8 == 0 && aligned(g.h, vec_bytes(s.h_dtype)), vec = vec_h && aligned(g.W, vec_bytes(s.w_dtype));
+  const PrepareFn prepare = s.h_dtype == PG_F32
+      ? (s.w_dtype == PG_F32 ? prepare_fn<PG_F32, PG_F32>(list, vec) : prepare_fn<PG_F32, PG_BF16>(list, vec))
+      : (s.w_dtype == PG_F32 ? prepare_fn<PG_BF16, PG_F32>(list, vec) : prepare_fn<PG_BF16, PG_BF16>(list, vec));
   VocabMaps maps;
   const int64_t ldw = g.Wp ? g.dp : s.d, ldh = g.hp ? g.dp : s.d;
-  if (g.Wp && (st = launch_split(g.W, s.w_dtype, s.V, s.d, g.dp, g.np_w, g.Wp, stream)) != PG_OK) return st;
-  if (!vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, 128)) return PG_ERR_CUDA;
+  if (!vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
+  const bool groups = g.group < (s.d + kBK - 1) / kBK;
+  auto split_blocks = [&](int64_t rows) { return (rows * (g.dp / 8) + kPrepThreads - 1) / kPrepThreads; };
   for (int64_t row0 = 0; row0 < s.N; row0 += g.Nc) {
     g.row0 = row0;
     g.rows = static_cast<int>(std::min<int64_t>(g.Nc, s.N - row0));
     g.first = row0 == 0;
     g.last = row0 + g.Nc >= s.N;
+    const int64_t blocks_w = g.Wp && g.first ? split_blocks(s.V) : 0, blocks_h = g.hp ? split_blocks(g.rows) : 0;
+    const int64_t blocks = blocks_w + blocks_h + (list ? g.rows : (g.rows + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
+    if (blocks >= (1ll << 31)) return PG_ERR_SHAPE;
+    st = launch_next(prepare, blocks, kPrepThreads, 0, false, !g.first, stream, g, static_cast<int>(blocks_w), static_cast<int>(blocks_h));
+    if (st != PG_OK) return st;
     const uint8_t* h = static_cast<const uint8_t*>(g.h) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.h_dtype));
-    if (g.hp && (st = launch_split(h, s.h_dtype, g.rows, s.d, g.dp, g.np_h, g.hp, stream)) != PG_OK) return st;
-    if (!vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, 128)) return PG_ERR_CUDA;
-    if (list)
-      targets<<<g.rows, 32 * std::min(kListWarps, (s.K + kListAtOnce - 1) / kListAtOnce), 0, stream>>>(g);
-    else
-      targets<<<(g.rows + 3) / 4, 128, 0, stream>>>(g);
-    if ((st = after_launch(1)) != PG_OK) return st;
+    if (!vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      return PG_ERR_CUDA;
     const int64_t jobs = static_cast<int64_t>((g.rows + kTile - 1) / kTile) * ((s.V + kTile - 1) / kTile);
     if (s.grad) {
-      if (!vocab_map(&maps.U, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, 128) ||
-          !vocab_map(&maps.Ust, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, 32) ||
-          (g.F && !vocab_map(&maps.F, g.F, g.np_f, g.rows, s.d, g.dp, g.Nc, 128)))
+      if (!vocab_map(&maps.U, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+          !vocab_map(&maps.Ust, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
+          (g.F && !vocab_map(&maps.F, g.F, g.np_f, g.rows, s.d, g.dp, g.Nc, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)))
         return PG_ERR_CUDA;
       if (!g.F) maps.F = maps.U;
-      st = launch_product<kKeep>(maps, g, jobs, stream);
+      st = groups ? launch_product<kKeep, true>(maps, g, jobs, stream) : launch_product<kKeep, false>(maps, g, jobs, stream);
     } else {
       maps.U = maps.Ust = maps.F = maps.h;
-      st = launch_product<kSums>(maps, g, jobs, stream);
+      st = groups ? launch_product<kSums, true>(maps, g, jobs, stream) : launch_product<kSums, false>(maps, g, jobs, stream);
     }
     if (st != PG_OK) return st;
-    rows_fn(s.grad, s.h_dtype, s.d % 8 == 0 && aligned(g.h, vec_bytes(s.h_dtype)))<<<(g.rows + 31) / 32, 32 * kRowWarps, 0, stream>>>(g);
-    if ((st = after_launch(1)) != PG_OK) return st;
-    const int64_t units = static_cast<int64_t>(g.tiles2) * g.q + g.tiles3;
-    if (!s.grad || units == 0) continue;
+    st = launch_next(rows_fn(s.grad, s.h_dtype, vec_h), (g.rows + kRowsPer - 1) / kRowsPer, 32 * kRowWarps, 0, false, true, stream, g);
+    if (st != PG_OK) return st;
     VocabArgs b = g;
     if (g.tiles2) b.tiles2 = (g.rows + kTile - 1) / kTile * g.nd;  // a last chunk has fewer rows
-    if ((st = launch_product<kGrads>(maps, b, static_cast<int64_t>(b.tiles2) * b.q + b.tiles3, stream)) != PG_OK) return st;
+    const int64_t units = s.grad ? static_cast<int64_t>(b.tiles2) * b.q + b.tiles3 : 0;
+    if (units == 0) continue;
+    const bool pieces = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32;
+    if ((st = pieces ? launch_product<kGrads, true>(maps, b, units, stream) : launch_product<kGrads, false>(maps, b, units, stream)) != PG_OK)
+      return st;
     if (g.parts) {
-      const int64_t blocks = (static_cast<int64_t>(g.rows) * s.d + 255) / 256;
-      vocab_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(g);
-      if ((st = after_launch(1)) != PG_OK) return st;
+      const bool four = s.d % 4 == 0 && aligned(g.gh, 4 * dtype_bytes(s.gh_dtype));
+      const int64_t threads = static_cast<int64_t>(g.rows) * s.d / (four ? 4 : 1);
+      st = launch_next(four ? vocab_join_kernel<4> : vocab_join_kernel<1>, (threads + 255) / 256, 256, 0, false, true, stream, g);
+      if (st != PG_OK) return st;
     }
   }
   return PG_OK;
