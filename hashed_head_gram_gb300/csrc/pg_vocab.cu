@@ -30,6 +30,8 @@
 // TMA into a ring of three, two accumulators in TMEM, eight epilogue warps.
 #include <cuda_bf16.h>
 
+#include <limits.h>
+
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -48,9 +50,11 @@ constexpr int kMaxList = 256;            // teacher tokens a row
 constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (any number gives the same results)
 constexpr int64_t kKeepBytes = 2ll << 30;  // of U
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
+constexpr int64_t kPartBytes = 256 << 20;  // of dW's parts
 constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
 
 constexpr int kPrepThreads = 256;
+constexpr int kFewRows = 128;             // up to here the first product has W's rows for its tiles' rows
 constexpr int kTile = 256;
 constexpr int kThreads = 384;            // warps 0 and 1 issue copies and products, 4 to 11 are the epilogue's
 constexpr int kEpiFirst = 4;
@@ -62,14 +66,14 @@ constexpr size_t kRing = static_cast<size_t>(kStages) * 2 * kOperandBytes;
 constexpr size_t kSmem = 1024 + kRing + kEpiWarps * kStageBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: fp32 sums, bf16 operands
-                            (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+                            (static_cast<uint32_t>(kTile >> 4) << 24);  // M; N and the layouts go with the job
 
 // A tensor core cuts what falls below its sum where an fp32 addition rounds, so a sum's error grows with its length, to
 // one side: 1.4e-6 of the logits at d = 2560, 4e-6 with the six products of fp32 operands. Where an fp32 result comes
 // of it, sums longer than this many k-blocks are made in groups, which the epilogue adds up in registers; and the
 // products of pieces run from the smallest to the largest, so that only the largest's additions count.
-constexpr int kGroup = 6;                // bf16 operands (48 additions: 4e-7)
-constexpr int kGroupPieces = 2;          // fp32 operands or gradients
+constexpr int kGroup = 10;               // bf16 operands (80 additions: 7e-7)
+constexpr int kGroupPieces = 1;          // fp32 operands or gradients
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Sums in groups take 128 registers a thread in the epilogue: its two warpgroups take over what the first does not need.
@@ -96,12 +100,14 @@ struct VocabArgs {
   int32_t* err;
   __nv_bfloat16 *hp, *Wp;                // pieces [pieces][rows][dp], or null
   __nv_bfloat16 *U, *F;                  // [pieces][Nc][Vp], [pieces][Nc][dp]
-  float2* sums;                          // [2 tiles][Nc]: reference (log2), sum
+  float2* sums;                          // [segments: halves of the first product's tiles][Nc]: reference (log2), sum
   float *zk, *wk;                        // [Nc][K] targets' logits (log2), weights (-1: none, or a later place of the same)
-  float *c, *a;                          // [Nc] reference (log2; +inf: no target), the loss's part beside lse
+  int32_t* sorted;                       // [Nc][K] listed tokens, ascending (zk and wk in their order), then INT_MAX
+  uint16_t* at;                          // [segments + 1][Nc] where in it each segment's tokens begin
+  float *c, *a;                          // [Nc] reference (log2; +inf: no target), the sum of w log w
   float* f;                              // [Nc]
   float* acc;                            // [V][d] dW over chunks, or null
-  float* parts;                          // [q][Nc][d] of dh, or null
+  float *parts, *parts_w;                // [q][Nc][d] of dh, [q_w][V][d] of dW, or null
   void *gh, *gw;
   int* err_word;
   int64_t row0;                          // of the chunk
@@ -113,9 +119,12 @@ struct VocabArgs {
   float k2;                              // scale log2(e)
   float scale, inv_t, zl, grad_scale;
   // schedule of the gradients' products
-  int q, tiles2, tiles3, nd, light, delta, heavy;
+  int q, q_w, tiles2, tiles3, nd, light, delta, heavy;  // parts of dh and dW; tiles of each; tiles a row of them
   int passes_h, passes_w;                // piece products of dh, dW
   int group, group_h, group_w;           // k-blocks that one sum in TMEM takes: logits, dh, dW
+  int wide, seg, seg_log;                // columns of a logits tile, and of a segment of it (its half), and that's log2
+  int at_log;                            // log2 of the tokens that a place of `at` stands for
+  int segs;                              // sums a row
 };
 
 // ------------------------------------------------------------------- fp32 values as bf16 pieces
@@ -238,121 +247,107 @@ __device__ void target_rows(const VocabArgs& g, int block) {
   g.zk[r] = z[0];
   g.wk[r] = valid ? 1.f : -1.f;
   g.c[r] = valid ? as_reference(z[0]) : INFINITY;
-  g.a[r] = 0.f;
 }
 
-// Distillation: one block a row. The first warp forms the teacher's softmax, all warps the listed tokens' logits,
-// four rows of W at a time.
-constexpr int kListAtOnce = 4;
-
+// Distillation: one warp a row. The teacher's softmax; the list sorted by token, so that the tiles of the first product
+// find what is theirs (`at`, where each segment's tokens begin) and keep those logits; and the dot product of the
+// heaviest token, for a reference. (Dot products of all listed tokens took 101 of 1346 us at 8192 x 50,304 x 768 with
+// lists of 32.)
 template <int HT, int WT, bool VEC>
-__device__ void list_row(const VocabArgs& g, int r) {
-  __shared__ int32_t s_id[kMaxList];
-  __shared__ float s_w[kMaxList], s_z[kMaxList];
-  __shared__ int s_any;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int warps = kPrepThreads / 32;
+__device__ void list_rows(const VocabArgs& g, int block) {
+  constexpr int kWarps = kPrepThreads / 32, kPer = kMaxList / 32;
+  __shared__ int32_t s_id[kWarps][kMaxList], s_sorted[kWarps][kMaxList];
+  __shared__ float s_w[kWarps][kMaxList];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = block * kWarps + warp;
+  if (r >= g.rows) return;
   const int64_t i = g.row0 + r;
-  constexpr int kPer = kMaxList / 32;
+  int32_t* ids = s_id[warp];
   float u[kPer];
-  if (warp == 0) {
-    float top = -INFINITY;
-    bool outside = false, poison = false;
+  float top = -INFINITY;
+  bool outside = false, poison = false;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int k = e * 32 + lane;
-      u[e] = -INFINITY;
-      if (k >= g.K) continue;
-      int32_t id = __ldg(g.ids + i * g.K + k);
-      const bool in = id >= 0 && id < g.V;
-      outside |= !in;
-      if (in) {
-        float y[1];
-        if (g.t_dtype == PG_F32) load_cols<PG_F32, 1>(g.tlogits, i * g.K + k, y);
-        else load_cols<PG_BF16, 1>(g.tlogits, i * g.K + k, y);
-        u[e] = y[0] * g.inv_t;
-        poison |= !(u[e] < INFINITY);  // (also NaN, which fmaxf passes over)
-        top = fmaxf(top, u[e]);
-      }
-      s_id[k] = in ? id : -1;
+  for (int e = 0; e < kPer; ++e) {
+    const int k = e * 32 + lane;
+    u[e] = -INFINITY;
+    if (k >= g.K) continue;
+    const int32_t id = __ldg(g.ids + i * g.K + k);
+    const bool in = id >= 0 && id < g.V;
+    outside |= !in;
+    if (in) {
+      float y[1];
+      if (g.t_dtype == PG_F32) load_cols<PG_F32, 1>(g.tlogits, i * g.K + k, y);
+      else load_cols<PG_BF16, 1>(g.tlogits, i * g.K + k, y);
+      u[e] = y[0] * g.inv_t;
+      poison |= !(u[e] < INFINITY);  // (also NaN, which fmaxf passes over)
+      top = fmaxf(top, u[e]);
     }
-    top = warp_max(top);
-    poison = __any_sync(0xffffffffu, poison);
-    outside = __any_sync(0xffffffffu, outside);
-    const bool some = poison || top > -INFINITY;
-    float total = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      u[e] = !some ? -INFINITY : u[e] - (top > -INFINITY ? top : 0.f);
-      total += expf(u[e]);
-    }
-    total = warp_sum(total);
-    const float log_total = logf(total);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int k = e * 32 + lane;
-      u[e] = poison ? __int_as_float(0x7fffffff) : u[e] - log_total;  // log p
-      if (k < g.K) s_w[k] = !some ? 0.f : expf(u[e]);
-    }
-    if (lane == 0) {
-      s_any = some;
-      if (outside && g.err) atomicMin(reinterpret_cast<unsigned int*>(g.err), static_cast<unsigned int>(i));
-    }
+    ids[k] = in ? id : INT_MAX;
   }
-  __syncthreads();
-  const bool some = s_any != 0;
-  for (int k0 = warp * kListAtOnce; some && k0 < g.K; k0 += warps * kListAtOnce) {
-    int64_t j[kListAtOnce];
-    float z[kListAtOnce];
+  top = warp_max(top);
+  poison = __any_sync(0xffffffffu, poison);
+  if (__any_sync(0xffffffffu, outside) && lane == 0 && g.err)
+    atomicMin(reinterpret_cast<unsigned int*>(g.err), static_cast<unsigned int>(i));
+  const bool some = poison || top > -INFINITY;
+  int heaviest = INT_MAX;
+  float total = 0.f;
 #pragma unroll
-    for (int e = 0; e < kListAtOnce; ++e) {
-      const int32_t id = k0 + e < g.K ? s_id[k0 + e] : -1;
-      j[e] = id < 0 ? 0 : id;
-    }
-    warp_dots<HT, WT, VEC, kListAtOnce>(g, i, j, z);
-    if (lane == 0)
-#pragma unroll
-      for (int e = 0; e < kListAtOnce; ++e)
-        if (k0 + e < g.K) s_z[k0 + e] = z[e] * g.k2;
+  for (int e = 0; e < kPer; ++e) {
+    const int k = e * 32 + lane;
+    if (u[e] == top && k < g.K) heaviest = min(heaviest, k);
+    u[e] = !some ? -INFINITY : u[e] - (top > -INFINITY ? top : 0.f);
+    total += expf(u[e]);
   }
-  __syncthreads();
-  // what the gradient puts at each token: a token's later places count with its first
-  for (int k = threadIdx.x; k < g.K; k += kPrepThreads) {
-    float w = s_w[k];
-    const int32_t id = s_id[k];
-    if (id < 0 || !some) {
-      w = -1.f;
-    } else {
-      for (int e = 0; e < g.K; ++e) {
-        if (e == k || s_id[e] != id) continue;
-        if (e < k) w = -1.f;
-        else if (w >= 0.f) w += s_w[e];
-      }
-    }
-    g.wk[static_cast<int64_t>(r) * g.K + k] = w;
-    g.zk[static_cast<int64_t>(r) * g.K + k] = some ? s_z[k] : 0.f;
-  }
-  if (warp != 0) return;
-  float c = -INFINITY;
-  bool nan = false;
-  for (int k = lane; some && k < g.K; k += 32) {
-    if (s_id[k] < 0) continue;
-    c = fmaxf(c, s_z[k]);
-    nan |= !(s_z[k] == s_z[k]);
-  }
-  c = warp_max(c);
-  if (__any_sync(0xffffffffu, nan)) c = __int_as_float(0x7fffffff);
+  total = warp_sum(total);
+  const float log_total = logf(total);
   float a = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     const int k = e * 32 + lane;
-    if (!some || k >= g.K || s_id[k] < 0) continue;
-    const float w = s_w[k];
-    if (!(w == 0.f)) a += w * (u[e] - (s_z[k] - c) * kLn2);
+    const float logp = poison ? __int_as_float(0x7fffffff) : u[e] - log_total, w = !some ? 0.f : expf(logp);
+    if (k < g.K) {
+      s_w[warp][k] = w;
+      if (!some) ids[k] = INT_MAX;
+      if (ids[k] != INT_MAX && !(w == 0.f)) a += w * logp;
+    }
   }
   a = warp_sum(a);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) heaviest = min(heaviest, __shfl_xor_sync(0xffffffffu, heaviest, o));
+  __syncwarp();
+  for (int k = lane; k < g.K; k += 32) {
+    const int32_t id = ids[k];
+    int rank = 0;
+    bool first = true;
+    float w = 0.f;  // what the gradient puts at the token: its later places count with its first
+    for (int e = 0; e < g.K; ++e) {
+      const bool same = ids[e] == id;
+      rank += ids[e] < id || (same && e < k);
+      first &= !(same && e < k);
+      if (same) w += s_w[warp][e];
+    }
+    s_sorted[warp][rank] = id;
+    g.sorted[static_cast<int64_t>(r) * g.K + rank] = id;
+    g.wk[static_cast<int64_t>(r) * g.K + rank] = id == INT_MAX || !first ? -1.f : w;
+  }
+  __syncwarp();
+  const int segs = static_cast<int>((g.V + (1 << g.at_log) - 1) >> g.at_log);
+  for (int q = lane; q <= segs; q += 32) {
+    const int from = q << g.at_log;
+    int lo = 0, hi = g.K;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_sorted[warp][mid] < from) lo = mid + 1;
+      else hi = mid;
+    }
+    g.at[static_cast<int64_t>(q) * g.Nc + r] = static_cast<uint16_t>(lo);
+  }
+  float z[1] = {0.f};
+  if (some) {
+    const int64_t j[1] = {heaviest < g.K && ids[heaviest] != INT_MAX ? ids[heaviest] : 0};
+    warp_dots<HT, WT, VEC, 1>(g, i, j, z);
+  }
   if (lane == 0) {
-    g.c[r] = some ? as_reference(c) : INFINITY;
+    g.c[r] = some ? as_reference(poison ? __int_as_float(0x7fffffff) : z[0] * g.k2) : INFINITY;
     g.a[r] = some ? a : 0.f;
   }
 }
@@ -369,7 +364,7 @@ __global__ void __launch_bounds__(kPrepThreads) vocab_prepare_kernel(const __gri
     const uint8_t* h = static_cast<const uint8_t*>(g.h) + g.row0 * g.d * (HT == PG_F32 ? 4 : 2);
     split_rows<HT, VEC>(h, g.rows, g.d, g.dp, g.np_h, g.hp, block);
   } else if (LIST) {
-    list_row<HT, WT, VEC>(g, block - blocks_h);
+    list_rows<HT, WT, VEC>(g, block - blocks_h);
   } else {
     target_rows<HT, WT, VEC>(g, block - blocks_h);
   }
@@ -384,11 +379,18 @@ struct VocabJob {
   const CUtensorMap *P, *Q;
   bool p_mn, q_mn;
   int np_p, np_q, passes;
-  int i, j;                              // tile's row and column
+  int i;                                 // tile's row, in tiles
+  int64_t col0;                          // its first column
+  int n;                                 // its columns: as many as there are left, to 32
   int kb0, kb1;
+  int64_t depth;                         // of the whole product
   int group;                             // k-blocks of one sum in TMEM
   int product, part;                     // 0: logits, 1: dh, 2: dW
 };
+
+__device__ __forceinline__ int columns(int64_t left, int wide) {
+  return left < wide ? (static_cast<int>(left) + 31) / 32 * 32 : wide;
+}
 
 // The r-th job of this unit; false behind the last.
 // The gradients: first the units of dh (its tiles in q parts along V, part by part so that the units at work read the
@@ -399,18 +401,20 @@ __device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps
   if constexpr (KIND != kGrads) {
     // tiles that are at work together share their rows of W, and h stays in L2
     const int nm = (g.rows + kTile - 1) / kTile;
-    const int64_t t = static_cast<int64_t>(r) * units + unit;
-    if (t >= static_cast<int64_t>(nm) * ((g.V + kTile - 1) / kTile)) return false;
+    const uint32_t t = static_cast<uint32_t>(r) * units + unit;
+    if (t >= static_cast<uint32_t>(nm) * static_cast<uint32_t>((g.V + g.wide - 1) / g.wide)) return false;
     w->P = &maps.h;
     w->Q = &maps.W;
     w->p_mn = w->q_mn = false;
     w->np_p = g.np_h;
     w->np_q = g.np_w;
     w->passes = passes_of(g.np_h, g.np_w);
-    w->i = static_cast<int>(t % nm);
-    w->j = static_cast<int>(t / nm);
+    w->i = static_cast<int>(t % static_cast<uint32_t>(nm));
+    w->col0 = static_cast<int64_t>(t / static_cast<uint32_t>(nm)) * g.wide;
+    w->n = columns(g.V - w->col0, g.wide);
     w->kb0 = 0;
     w->kb1 = (g.d + kBK - 1) / kBK;
+    w->depth = g.d;
     w->group = g.group;
     w->product = w->part = 0;
     return true;
@@ -428,7 +432,9 @@ __device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps
       w->np_q = g.gh_dtype == PG_F32 ? g.np_w : 1;
       w->passes = g.passes_h;
       w->i = t / g.nd;
-      w->j = t % g.nd;
+      w->col0 = t % g.nd * kTile;
+      w->n = columns(g.d - w->col0, kTile);
+      w->depth = g.V;
       w->kb0 = static_cast<int>(all * w->part / g.q);
       w->kb1 = static_cast<int>(all * (w->part + 1) / g.q);
       w->group = g.group_h;
@@ -436,27 +442,31 @@ __device__ __forceinline__ bool job_at(const VocabArgs& g, const VocabMaps& maps
       return true;
     }
     r -= mine;
-    int64_t t;
+    int t;
     if (unit >= g.heavy && r < g.delta) {
-      t = static_cast<int64_t>(r) * g.light + (unit - g.heavy);
+      t = r * g.light + (unit - g.heavy);
     } else {
       if (unit >= g.heavy) r -= g.delta;
-      t = static_cast<int64_t>(g.delta) * g.light + static_cast<int64_t>(r) * units + unit;
+      t = g.delta * g.light + r * units + unit;
     }
-    if (t >= g.tiles3) return false;
+    if (t >= g.tiles3 * g.q_w) return false;
+    w->part = t / g.tiles3;
+    t -= w->part * g.tiles3;
+    const int all = (g.rows + kBK - 1) / kBK;
     w->P = &maps.U;
     w->Q = &maps.F;
     w->p_mn = w->q_mn = true;
     w->np_p = g.gw_dtype == PG_F32 ? g.np_u : 1;
     w->np_q = g.gw_dtype == PG_F32 ? g.np_f : 1;
     w->passes = g.passes_w;
-    w->i = static_cast<int>(t / g.nd);
-    w->j = static_cast<int>(t % g.nd);
-    w->kb0 = 0;
-    w->kb1 = (g.rows + kBK - 1) / kBK;
+    w->i = t / g.nd;
+    w->col0 = t % g.nd * kTile;
+    w->n = columns(g.d - w->col0, kTile);
+    w->depth = g.rows;
+    w->kb0 = static_cast<int>(static_cast<int64_t>(all) * w->part / g.q_w);
+    w->kb1 = static_cast<int>(static_cast<int64_t>(all) * (w->part + 1) / g.q_w);
     w->group = g.group_w;
     w->product = 2;
-    w->part = 0;
     return true;
   }
 }
@@ -468,10 +478,11 @@ struct VocabBars {
 };
 
 // `wait` without a call, across which the sums that the epilogue holds in registers would have to be saved.
+template <bool PAIR>
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (poll<true>(bar, parity)) return true;
+  if (poll<PAIR>(bar, parity)) return true;
   const uint64_t t0 = now_ns();
-  while (!poll<true>(bar, parity))
+  while (!poll<PAIR>(bar, parity))
     if (*abort || now_ns() - t0 > kAsyncWaitNs) return false;
   return true;
 }
@@ -494,39 +505,33 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time, from TMEM or (GROUPS) from the sums in
-// registers. u = 2^(k2 z - c) in fp32 for the row's sum, and to U through the warp's shared memory (32 rows of 64 bytes,
+// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time. u = 2^(k2 z - c) in fp32 for the row's sum, and to U through the warp's shared memory (32 rows of 64 bytes,
 // swizzled as the TMA store reads them; two such buffers in turn, so that a store reads one while the other fills).
-template <bool KEEP, bool GROUPS>
-__device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, const float (&z)[GROUPS ? 128 : 1],
-                                             uint8_t* s_row, int row0, int64_t col0, float c, bool dead) {
+template <bool KEEP>
+__device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row, int row0, int64_t col0, float c, bool dead) {
   const int lane = threadIdx.x & 31;
+  const int64_t end = min(col0 + g.seg, g.V);
   const uint64_t k2 = pk(g.k2, g.k2), c2 = pk(-c, -c);
   const bool some_dead = KEEP && __any_sync(0xffffffffu, dead);
   uint64_t sum[2] = {0, 0};
   if (KEEP && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // of an earlier tile
-  uint32_t r[GROUPS ? 1 : 2][GROUPS ? 1 : 32];
-  if constexpr (!GROUPS) tmem_load(from, r[0]);
+  uint32_t r[2][32];
+  tmem_load(from, r[0]);
 #pragma unroll
   for (int ch = 0; ch < 4; ++ch) {
     const int64_t c0 = col0 + ch * 32;
-    if (c0 >= g.V) break;
-    if constexpr (!GROUPS) {
-      tmem_wait(r[ch & 1]);
-      if (ch < 3) tmem_load(from + (ch + 1) * 32, r[(ch + 1) & 1]);
-    }
+    if (c0 >= end) break;
+    tmem_wait(r[ch & 1]);
+    if (ch < 3) tmem_load(from + (ch + 1) * 32, r[(ch + 1) & 1]);
     float x[32];
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      uint64_t y;
-      if constexpr (GROUPS) y = pk(z[ch * 32 + k], z[ch * 32 + k + 1]);
-      else y = pk(__uint_as_float(r[ch & 1][k]), __uint_as_float(r[ch & 1][k + 1]));
-      upk(fma2(y, k2, c2), x[k], x[k + 1]);
+      upk(fma2(pk(__uint_as_float(r[ch & 1][k]), __uint_as_float(r[ch & 1][k + 1])), k2, c2), x[k], x[k + 1]);
       x[k] = exp2_fast(x[k]);
       x[k + 1] = exp2_fast(x[k + 1]);
     }
-    if (c0 + 32 > g.V) {
-      const int left = static_cast<int>(g.V - c0);
+    if (c0 + 32 > end) {
+      const int left = static_cast<int>(end - c0);
 #pragma unroll
       for (int k = 0; k < 32; ++k) x[k] = k < left ? x[k] : 0.f;
     }
@@ -561,95 +566,130 @@ __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps
       }
     }
   }
-  if constexpr (!GROUPS) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   float lo, hi;
   upk(add2(sum[0], sum[1]), lo, hi);
   return lo + hi;
 }
 
-template <bool KEEP, bool GROUPS>
-__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w,
-                                                const float (&z)[GROUPS ? 128 : 1], uint8_t* s_row, uint32_t from, int row0, int half,
-                                                float c) {
+// The listed tokens of this lane's row that fall into a segment: places [e, end) of the sorted list, the first's token.
+struct Listed {
+  int e, end;
+  int32_t token;
+};
+
+__device__ __forceinline__ Listed listed_in(const VocabArgs& g, int row, int64_t col0) {
+  Listed l = {0, 0, 0};
+  if (row >= g.rows || col0 >= g.V) return l;
+  const int64_t seg = static_cast<uint32_t>(col0) >> g.at_log;
+  l.e = g.at[seg * g.Nc + row];
+  l.end = g.at[(seg + 1) * g.Nc + row];
+  return l;
+}
+
+__device__ __forceinline__ void first_listed(const VocabArgs& g, int row, Listed* l) {
+  if (l->e < l->end) l->token = g.sorted[static_cast<int64_t>(row) * g.K + l->e];
+}
+
+template <bool KEEP>
+__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
+                                                uint32_t from, int row0, int half, float c, Listed listed) {
   const int lane = threadIdx.x & 31;
-  const int64_t col0 = static_cast<int64_t>(w.j) * kTile + half * 128;
+  const int64_t col0 = w.col0 + half * g.seg;
   if (row0 >= g.rows || col0 >= g.V) return;
+  while (__any_sync(0xffffffffu, listed.e < listed.end)) {  // listed tokens' logits, one a row at a time
+    const bool mine = listed.e < listed.end;
+    const int at = mine ? static_cast<int>(listed.token - col0) : -1;
+    float y = 0.f;
+    // TMEM gives all lanes one column: the lanes' columns one after the other, four in flight
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine); left;) {
+      uint32_t v[4];
+      int l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l[k] = left ? __ffs(left) - 1 : 32;
+        left &= left - 1;
+        const int column = __shfl_sync(0xffffffffu, at, l[k] & 31);
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v[k]) : "r"(from + max(column, 0)));
+      }
+      tmem_wait(v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (lane == l[k]) y = __uint_as_float(v[k]);
+    }
+    if (mine) {
+      const int64_t row = static_cast<int64_t>(row0 + lane) * g.K;
+      g.zk[row + listed.e] = y * g.k2;
+      if (++listed.e < listed.end) listed.token = g.sorted[row + listed.e];
+    }
+  }
   const bool dead = row0 + lane >= g.rows || c == INFINITY;
-  float sum = logits_half<KEEP, GROUPS>(g, maps, from, z, s_row, row0, col0, c, dead);
+  float sum = logits_half<KEEP>(g, maps, from, s_row, row0, col0, c, dead);
   float ref = c;
   const bool over = !dead && !(sum <= kSumLimit);
   if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the tile's largest for a reference
     float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 4; ++h) {
-      uint32_t r[GROUPS ? 1 : 32];
-      if constexpr (!GROUPS) {
-        tmem_load(from + h * 32, r);
-        tmem_wait(r);
-      }
+      uint32_t r[32];
+      tmem_load(from + h * 32, r);
+      tmem_wait(r);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        float y;
-        if constexpr (GROUPS) y = z[h * 32 + k];
-        else y = __uint_as_float(r[k]);
-        if (col0 + h * 32 + k < g.V) top = fmaxf(top, y * g.k2);
-      }
+      for (int k = 0; k < 32; ++k)
+        if (h * 32 + k < g.seg && col0 + h * 32 + k < g.V) top = fmaxf(top, __uint_as_float(r[k]) * g.k2);
     }
     if (over) ref = top == -INFINITY ? 0.f : top;
     if (KEEP && lane == 0) stores_done();  // the same places are written again
     __syncwarp();
-    sum = logits_half<KEEP, GROUPS>(g, maps, from, z, s_row, row0, col0, ref, dead);
+    sum = logits_half<KEEP>(g, maps, from, s_row, row0, col0, ref, dead);
   }
-  if (row0 + lane < g.rows) g.sums[(2ll * w.j + half) * g.Nc + row0 + lane] = make_float2(ref, sum);
+  if (row0 + lane < g.rows) g.sums[static_cast<int64_t>(static_cast<uint32_t>(col0) >> g.seg_log) * g.Nc + row0 + lane] = make_float2(ref, sum);
+}
+
+// Where this chunk's dW goes, and what is added to it.
+__device__ __forceinline__ void table_target(const VocabArgs& g, void** dst, int* dtype, const float** add32, const __nv_bfloat16** add16) {
+  const bool through = g.acc && !g.last;
+  *dtype = through ? PG_F32 : g.gw_dtype;
+  *dst = through ? g.acc : g.gw;
+  if (g.gw_dtype == PG_F32) {
+    if (!g.first || g.accumulate) *add32 = static_cast<const float*>(g.gw);
+  } else {
+    if (!g.first) *add32 = g.acc;
+    if (g.last && g.accumulate) *add16 = static_cast<const __nv_bfloat16*>(g.gw);
+  }
 }
 
 // A gradient's tile. TMEM gives a lane one row; global memory wants neighbouring lanes on one row, so 32 columns
 // at a time pass through the warp's shared memory.
-template <bool GROUPS>
-__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob& w, const float (&z)[GROUPS ? 128 : 1], uint8_t* s_row,
-                                              uint32_t from, int row0, int half) {
+__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob& w, uint8_t* s_row, uint32_t from, int row0,
+                                              int half) {
   const int lane = threadIdx.x & 31;
-  const bool dh = w.product == 1, part = dh && g.parts;
+  const bool dh = w.product == 1, part = dh ? g.parts != nullptr : g.parts_w != nullptr;
   const int64_t rows = dh ? g.rows : g.V;
   if (row0 >= rows) return;
   float f = 1.f;
   if (dh && !part) f = row0 + lane < rows ? g.f[row0 + lane] : 0.f;
-  // where the tile goes, and what is added to it
   void* dst;
-  int dtype;
+  int dtype = PG_F32;
   const float* add32 = nullptr;
   const __nv_bfloat16* add16 = nullptr;
   if (part) {
-    dst = g.parts + static_cast<int64_t>(w.part) * g.Nc * g.d;
-    dtype = PG_F32;
+    dst = dh ? g.parts + static_cast<int64_t>(w.part) * g.Nc * g.d : g.parts_w + static_cast<int64_t>(w.part) * g.V * g.d;
   } else if (dh) {
     dtype = g.gh_dtype;
     dst = static_cast<uint8_t*>(g.gh) + g.row0 * g.d * (dtype == PG_F32 ? 4 : 2);
   } else {
-    const bool through = g.acc && !g.last;
-    dtype = through ? PG_F32 : g.gw_dtype;
-    dst = through ? g.acc : g.gw;
-    if (g.gw_dtype == PG_F32) {
-      if (!g.first || g.accumulate) add32 = static_cast<const float*>(g.gw);
-    } else {
-      if (!g.first) add32 = g.acc;
-      if (g.last && g.accumulate) add16 = static_cast<const __nv_bfloat16*>(g.gw);
-    }
+    table_target(g, &dst, &dtype, &add32, &add16);
   }
   const bool vec = g.d % 4 == 0 && reinterpret_cast<uintptr_t>(dst) % (dtype == PG_F32 ? 16 : 8) == 0 &&
                    (!add32 || reinterpret_cast<uintptr_t>(add32) % 16 == 0);
-#pragma unroll(GROUPS ? 4 : 1)
+#pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
-    const int c0 = w.j * kTile + half * 128 + ch * 32;
+    const int c0 = static_cast<int>(w.col0) + half * (kTile / 2) + ch * 32;
     if (c0 >= g.d) break;
     uint32_t r[32];
-    if constexpr (GROUPS) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(z[ch * 32 + k]);
-    } else {
-      tmem_load(from + ch * 32, r);
-      tmem_wait(r);
-    }
+    tmem_load(from + ch * 32, r);
+    tmem_wait(r);
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -662,7 +702,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
     __syncwarp();
     if (vec) {  // (d % 4 == 0: four columns are inside or outside together)
       const int lc = lane & 7, col = c0 + lc * 4;
-#pragma unroll(GROUPS ? 1 : 8)
+#pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int lr = 4 * k + (lane >> 3);
         if (row0 + lr >= rows || col >= g.d) continue;
@@ -682,7 +722,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
       }
     } else {
       const int col = c0 + lane;
-#pragma unroll(GROUPS ? 1 : 4)
+#pragma unroll 4
       for (int lr = 0; lr < 32; ++lr) {
         if (row0 + lr >= rows || col >= g.d) break;
         float v = *reinterpret_cast<const float*>(s_row + lr * 128 + (((lane >> 2) ^ (lr & 7)) << 4) + (lane & 3) * 4);
@@ -739,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (GROUPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0 && lane == 0) {
       for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
-        const int p0 = w.i * kTile + static_cast<int>(rank) * 128, q0 = w.j * kTile + static_cast<int>(rank) * 128;
+        const int p0 = w.i * kTile + static_cast<int>(rank) * 128, q0 = static_cast<int>(w.col0) + static_cast<int>(rank) * (w.n / 2);
         for (int k0 = w.kb0; k0 < w.kb1; k0 += w.group) {
           const int k1 = min(k0 + w.group, w.kb1);
           for (int pass = 0; fine && pass < w.passes; ++pass) {
@@ -768,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1 && lane == 0 && rank == 0) {
       for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
-        const uint32_t idesc = kIdesc | (w.p_mn ? 1u << 15 : 0u) | (w.q_mn ? 1u << 16 : 0u);
+        const uint32_t idesc = kIdesc | (static_cast<uint32_t>(w.n >> 3) << 17) | (w.p_mn ? 1u << 15 : 0u) | (w.q_mn ? 1u << 16 : 0u);
         // 16 k further: 32 bytes along a K-major line (after four, the deeper half), two 8-k
         // groups of an MN-major tile
         const uint32_t step_p = w.p_mn ? 2048 >> 4 : 32 >> 4, step_q = w.q_mn ? 2048 >> 4 : 32 >> 4;
@@ -780,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_after();
           const uint32_t d = tmem + static_cast<uint32_t>(acc * kTile);
-          const int blocks = (min(k0 + w.group, w.kb1) - k0) * w.passes;
-          for (int kb = 0; kb < blocks; ++kb) {
+          const int len = min(k0 + w.group, w.kb1) - k0, blocks = len * w.passes;
+          for (int kb = 0, at = k0; kb < blocks; ++kb) {
             if (!wait<true>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
               fine = false;
               break;
@@ -789,10 +829,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_after();
             const uint32_t sp = smem_addr(ring + stage * (2 * kOperandBytes));
             const uint64_t dp = operand_desc(sp, w.p_mn), dq = operand_desc(sp + kOperandBytes, w.q_mn);
+            const int64_t left = w.depth - static_cast<int64_t>(at) * kBK;  // (what is behind it is zero)
+            if (++at == k0 + len) at = k0;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-              mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
-                            (kb | k) != 0);
+              if (k * 16 < left)
+                mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
+                              (kb | k) != 0);
             commit<true>(smem_addr(&bars->empty[stage]));
             if (++stage == kStages) {
               stage = 0;
@@ -810,33 +853,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (GROUPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quarter = warp & 3, half = (warp - kEpiFirst) >> 2;
     uint8_t* s_row = ring + kRing + (warp - kEpiFirst) * kStageBytes;
-    for (int r = 0; fine && job_at<KIND>(g, maps, unit, units, r, &w); ++r) {
-      const int row0 = w.i * kTile + static_cast<int>(rank) * 128 + quarter * 32;
-      float c = INFINITY;
-      if (KIND != kGrads && row0 + lane < g.rows) c = g.c[row0 + lane];
-      float z[GROUPS ? 128 : 1];
-      const uint32_t warp_from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
-      for (int k0 = w.kb0; k0 < w.kb1; k0 += w.group) {
-        if (!__all_sync(0xffffffffu, wait_inline(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
-          fine = false;
-          break;
-        }
+    // What a tile needs of its rows is read while the tile before is worked on.
+    bool more = job_at<KIND>(g, maps, unit, units, 0, &w);
+    float c = INFINITY, next_c = INFINITY;
+    Listed listed = {0, 0, 0}, next_listed = {0, 0, 0};
+    auto row_of = [&](const VocabJob& job) { return job.i * kTile + static_cast<int>(rank) * 128 + quarter * 32; };
+    auto read_rows = [&](const VocabJob& job) {
+      const int row = row_of(job) + lane;
+      next_c = INFINITY;
+      if (row < g.rows) next_c = g.c[row];
+      if (g.ids) next_listed = listed_in(g, row, job.col0 + half * g.seg);
+    };
+    if (KIND != kGrads && more) {
+      read_rows(w);
+      if (g.ids) first_listed(g, row_of(w) + lane, &next_listed);
+    }
+    for (int r = 0; fine && more; ++r) {
+      const int row0 = row_of(w);
+      VocabJob next;
+      if (KIND != kGrads) {
+        c = next_c;
+        listed = next_listed;
+      }
+      more = job_at<KIND>(g, maps, unit, units, r + 1, &next);
+      if (KIND != kGrads && more) read_rows(next);
+      const uint32_t warp_from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                 static_cast<uint32_t>(half * (KIND == kGrads ? kTile / 2 : g.seg));
+      auto acquire = [&]() {
+        fine = __all_sync(0xffffffffu, wait_inline<true>(smem_addr(&bars->acc_full[acc]), acc_phase, abort));
         fence_after();
-        const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
-        if constexpr (GROUPS) {
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t r[32];
-            tmem_load(from + ch * 32, r);
-            tmem_wait(r);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) z[ch * 32 + k] = k0 == w.kb0 ? __uint_as_float(r[k]) : z[ch * 32 + k] + __uint_as_float(r[k]);
-          }
-        } else if constexpr (KIND == kGrads) {
-          grad_epilogue<false>(g, w, z, s_row, from, row0, half);
-        } else {
-          logits_epilogue<KIND == kKeep, false>(g, maps, w, z, s_row, from, row0, half, c);
-        }
+        return fine;
+      };
+      auto release = [&]() {
         fence_before();
         __syncwarp();
         if (lane == 0)
@@ -845,12 +893,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "memory");
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+      };
+      if (GROUPS && w.kb0 + w.group < w.kb1) {
+        // the groups before the last in registers; the last one's sums go back to TMEM with the others added
+        float z[128];
+#pragma unroll
+        for (int k = 0; k < 128; ++k) z[k] = 0.f;
+        for (int k0 = w.kb0; k0 + w.group < w.kb1; k0 += w.group) {
+          if (!acquire()) break;
+          const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t r[32];
+            tmem_load(from + ch * 32, r);
+            tmem_wait(r);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z[ch * 32 + k] += __uint_as_float(r[k]);
+          }
+          release();
+        }
+        if (!fine || !acquire()) break;
+        const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          if (KIND != kGrads && ch * 32 >= g.seg) break;  // (the columns behind are the other half's)
+          uint32_t r[32];
+          tmem_load(from + ch * 32, r);
+          tmem_wait(r);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) z[ch * 32 + k] += __uint_as_float(r[k]);
+          tmem_store(from + ch * 32, z + ch * 32);
+        }
+        tmem_stored();
+      } else if (!acquire()) {
+        break;
       }
-      if (!fine) break;
-      if constexpr (GROUPS) {
-        if constexpr (KIND == kGrads) grad_epilogue<true>(g, w, z, s_row, 0, row0, half);
-        else logits_epilogue<KIND == kKeep, true>(g, maps, w, z, s_row, 0, row0, half, c);
-      }
+      const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
+      if constexpr (KIND == kGrads) grad_epilogue(g, w, s_row, from, row0, half);
+      else logits_epilogue<KIND == kKeep>(g, maps, w, s_row, from, row0, half, c, listed);
+      release();
+      w = next;
+      if (KIND != kGrads && more && g.ids) first_listed(g, row_of(w) + lane, &next_listed);
     }
     if (KIND == kKeep && lane == 0) stores_done();
   }
@@ -886,6 +969,279 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_free<true>(tmem, kTmemCols);
 }
 
+// ------------------------------------------------------------------------------- few rows
+
+// The first product for up to 128 rows, where reading W is all that counts: W's rows are the tile's rows (128 a CTA), the
+// rows of h its columns (NT of them), so that a stage of the ring holds little beside W and the tensor core waits for
+// it alone. A lane has one row of W and all rows of h; sums over a warp's 32 rows of W (a segment) by halving.
+// 8 x 128,000 x 2560: FEW_TIME, against 152 us on 256 x 256 tiles of pairs, whose ring holds 96 KB of W an SM.
+template <int NT>
+struct Few {
+  static constexpr int kWBytes = 128 * kBK * 2, kHBytes = NT * kBK * 2;
+  static constexpr int kStages = NT == 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr int kThreads = 192;
+  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NT >> 3) << 17) | (8u << 24);
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * (kWBytes + kHBytes);
+};
+
+template <int NT>
+struct FewBars {
+  uint64_t full[Few<NT>::kStages], empty[Few<NT>::kStages], acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+// Lane t of a warp gets op over all lanes of x[t].
+template <typename Op>
+__device__ __forceinline__ float reduce_columns(float (&x)[32], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const bool up = lane & o;
+      const float give = up ? x[k] : x[k + o], keep = up ? x[k + o] : x[k];
+      x[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  return x[0];
+}
+
+// sum 2^ref + sum2 2^ref2 as one, at the larger reference.
+__device__ __forceinline__ void join_sums(float* ref, float* sum, float ref2, float sum2) {
+  if (ref2 == *ref) {
+    *sum += sum2;
+  } else if (ref2 > *ref) {
+    *sum = *sum * exp2f(*ref - ref2) + sum2;
+    *ref = ref2;
+  } else {
+    *sum += sum2 * exp2f(ref2 - *ref);
+  }
+}
+
+template <int NT, bool KEEP>
+__global__ void __launch_bounds__(Few<NT>::kThreads, 1)
+    vocab_few_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabArgs g) {
+  using T = Few<NT>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ FewBars<NT> bars_s;
+  __shared__ float s_c[NT];
+  FewBars<NT>* bars = &bars_s;
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      bar_init(smem_addr(&bars->full[s]), 1);
+      bar_init(smem_addr(&bars->empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(smem_addr(&bars->acc_full[s]), 1);
+      bar_init(smem_addr(&bars->acc_empty[s]), 4);
+    }
+    bar_init(smem_addr(&bars->done), 1);
+    bars->abort = 0;
+    bar_init_fence();
+    fence_async_smem();
+  }
+  if (warp == 1) tmem_alloc<false>(smem_addr(&bars->tmem), 2 * NT);
+  grid_dep_wait();
+  grid_dep_launch();
+  if (threadIdx.x < NT) s_c[threadIdx.x] = threadIdx.x < g.rows ? g.c[threadIdx.x] : INFINITY;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  const int tiles = static_cast<int>((g.V + 127) / 128), blocks = (g.d + kBK - 1) / kBK, passes = passes_of(g.np_w, g.np_h);
+  int stage = 0, acc = 0;
+  uint32_t ring_phase = 0, acc_phase = 0;
+  bool fine = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int t = blockIdx.x; fine && t < tiles; t += gridDim.x)
+        for (int k0 = 0; fine && k0 < blocks; k0 += g.group)
+          for (int pass = 0; fine && pass < passes; ++pass) {
+            int zw = 0, zh = 0;
+            if (passes > 1) piece_of(g.np_w, g.np_h, pass, &zw, &zh);
+            for (int kb = k0; kb < min(k0 + g.group, blocks); ++kb) {
+              if (!wait<false>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
+                fine = false;
+                break;
+              }
+              const uint32_t full = smem_addr(&bars->full[stage]), dw = smem_addr(ring + stage * (T::kWBytes + T::kHBytes));
+              bar_expect(full, T::kWBytes + T::kHBytes);
+              load_operand<false, 128>(dw, &maps.W, &maps.W, false, t * 128, kb * kBK, zw, full);
+              load_operand<false, NT>(dw + T::kWBytes, &maps.h, &maps.h, false, 0, kb * kBK, zh, full);
+              if (++stage == S) {
+                stage = 0;
+                ring_phase ^= 1u;
+              }
+            }
+          }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int t = blockIdx.x; fine && t < tiles; t += gridDim.x)
+        for (int k0 = 0; fine && k0 < blocks; k0 += g.group) {
+          if (!wait<false>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
+            fine = false;
+            break;
+          }
+          fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * NT);
+          const int len = min(g.group, blocks - k0);
+          for (int kb = 0, at = k0; kb < len * passes; ++kb) {
+            if (!wait<false>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
+              fine = false;
+              break;
+            }
+            fence_after();
+            const uint32_t sw = smem_addr(ring + stage * (T::kWBytes + T::kHBytes));
+            const uint64_t dw = operand_desc(sw, false), dh = operand_desc(sw + T::kWBytes, false);
+            const int left = g.d - at * kBK;
+            if (++at == k0 + len) at = k0;
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)
+              if (k * 16 < left)
+                mma_f16<false>(d, dw + (k / 4) * (T::kWBytes / 2 >> 4) + (k % 4) * 2, dh + (k / 4) * (T::kHBytes / 2 >> 4) + (k % 4) * 2,
+                               T::kIdesc, (kb | k) != 0);
+            commit<false>(smem_addr(&bars->empty[stage]));
+            if (++stage == S) {
+              stage = 0;
+              ring_phase ^= 1u;
+            }
+          }
+          if (!fine) break;
+          commit<false>(smem_addr(&bars->acc_full[acc]));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+  } else {
+    const int quarter = warp & 3;
+    float all_ref[NT / 32], all_sum[NT / 32];  // without U: one sum a warp, in a segment of its own
+#pragma unroll
+    for (int k = 0; k < NT / 32; ++k) {
+      all_ref[k] = s_c[k * 32 + lane];
+      all_sum[k] = 0.f;
+    }
+    for (int t = blockIdx.x; fine && t < tiles; t += gridDim.x) {
+      const int64_t v0 = t * 128ll + quarter * 32, v = v0 + lane;
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      float z[NT];
+      for (int k0 = 0; k0 < blocks; k0 += g.group) {
+        if (!__all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
+          fine = false;
+          break;
+        }
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < NT; c += 32) {
+          uint32_t r[32];
+          tmem_load(from + static_cast<uint32_t>(acc * NT + c), r);
+          tmem_wait(r);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) z[c + k] = k0 == 0 ? __uint_as_float(r[k]) : z[c + k] + __uint_as_float(r[k]);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&bars->acc_empty[acc]));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!fine || v0 >= g.V) continue;
+      const bool in = v < g.V;
+      const int64_t seg = v0 >> 5;
+#pragma unroll
+      for (int c0 = 0; c0 < NT; c0 += 32) {
+        if (c0 >= g.rows) break;
+        const int row = c0 + lane;  // the row of h whose sum this lane gets
+        const float c = s_c[row];
+        const bool alive = c != INFINITY;
+        if (g.ids) {
+          int e = 0, end = 0;
+          if (row < g.rows) {
+            e = g.at[static_cast<int64_t>(t) * g.Nc + row];  // (the four warps' tokens)
+            end = g.at[(t + 1ll) * g.Nc + row];
+          }
+          for (uint32_t left = __ballot_sync(0xffffffffu, e < end); left; left &= left - 1) {
+            const int l = __ffs(left) - 1, e1 = __shfl_sync(0xffffffffu, e, l), end1 = __shfl_sync(0xffffffffu, end, l);
+            float y = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y = k == l ? z[c0 + k] : y;
+            for (int j = e1; j < end1; ++j)
+              if (g.sorted[static_cast<int64_t>(c0 + l) * g.K + j] == v) g.zk[static_cast<int64_t>(c0 + l) * g.K + j] = y * g.k2;
+          }
+        }
+        float x[32], ref = c;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = in ? exp2_fast(fmaf(z[c0 + k], g.k2, -s_c[c0 + k])) : 0.f;
+        float u[32];
+        if (KEEP)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) u[k] = x[k];
+        float sum = reduce_columns(x, [](float a, float b) { return a + b; });
+        const bool over = alive && !(sum <= kSumLimit);
+        if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the segment's largest for a reference
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = in ? z[c0 + k] * g.k2 : -INFINITY;
+          const float top = reduce_columns(x, [](float a, float b) { return fmaxf(a, b); });
+          if (over) ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = in ? exp2_fast(fmaf(z[c0 + k], g.k2, -__shfl_sync(0xffffffffu, ref, k))) : 0.f;
+          if (KEEP)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) u[k] = x[k];
+          sum = reduce_columns(x, [](float a, float b) { return a + b; });
+        }
+        if (!KEEP) join_sums(&all_ref[c0 / 32], &all_sum[c0 / 32], ref, sum);
+        else if (row < g.rows) g.sums[seg * g.Nc + row] = make_float2(ref, sum);
+        if (KEEP && in) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (c0 + k >= g.rows) break;
+            if (s_c[c0 + k] == INFINITY) u[k] = 0.f;
+            for (int p = 0; p < g.np_u; ++p)
+              reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + c0 + k) * g.Vp + v] = take_piece(u[k]);
+          }
+        }
+      }
+    }
+    if (!KEEP)
+#pragma unroll
+      for (int k = 0; k < NT / 32; ++k)
+        if (k * 32 + lane < g.rows)
+          g.sums[(blockIdx.x * 4ll + quarter) * g.Nc + k * 32 + lane] = make_float2(all_ref[k], all_sum[k]);
+  }
+  if (!fine) {
+    atomicOr(g.err_word, kErrVocab);
+    *abort = 1;
+  }
+  __syncwarp();
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      const uint64_t t0 = now_ns();
+      while (!poll<false>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u) && now_ns() - t0 < kAsyncWaitNs / 8) {
+      }
+      if (++stage == S) {
+        stage = 0;
+        ring_phase ^= 1u;
+      }
+    }
+  }
+  if (warp == 1 && lane == 0) {
+    commit_here<false>(smem_addr(&bars->done));
+    const uint64_t t0 = now_ns();
+    while (!poll<false>(smem_addr(&bars->done), 0) && now_ns() - t0 < kAsyncWaitNs) {
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_free<false>(tmem, 2 * NT);
+}
+
 // ------------------------------------------------------------------- rows, once their sums are there
 
 constexpr int kRowWarps = 16, kRowsPer = 8;
@@ -896,40 +1252,46 @@ template <bool GRAD, int HT, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid_constant__ VocabArgs g) {
   __shared__ float s_ref[kRowWarps][kRowsPer], s_sum[kRowWarps][kRowsPer];
   __shared__ int s_moved[kRowWarps][kRowsPer], s_fix[kRowsPer];
-  __shared__ float s_to[kRowsPer], s_f[kRowsPer], s_lse[kRowsPer], s_beta[kRowsPer];
+  __shared__ float s_to[kRowsPer], s_f[kRowsPer], s_lse[kRowsPer], s_beta[kRowsPer], s_a[kRowsPer];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (kRowsPer - 1);
   const int r0 = blockIdx.x * kRowsPer, r = r0 + k;
   const bool in = r < g.rows;
   grid_dep_wait();
   grid_dep_launch();
   const float c = in ? g.c[r] : INFINITY;
-  const int segs = static_cast<int>((g.V + 127) / 128);
   float ref = c, sum = 0.f;
   int moved = 0;
-  auto join = [&](float ref2, float sum2) {
-    if (ref2 == ref) {
-      sum += sum2;
-    } else if (ref2 > ref) {
-      sum = sum * exp2f(ref - ref2) + sum2;
-      ref = ref2;
-    } else {
-      sum += sum2 * exp2f(ref2 - ref);
-    }
-  };
   if (in && c != INFINITY) {
     const float2* at = g.sums + r;
-#pragma unroll 8
-    for (int s = warp * 4 + lane / kRowsPer; s < segs; s += 4 * kRowWarps) {
-      const float2 v = at[static_cast<int64_t>(s) * g.Nc];
-      moved |= v.x != c;
-      join(v.x, v.y);
+    constexpr int kFly = 8, kStep = 4 * kRowWarps;
+    for (int s = warp * 4 + lane / kRowsPer; s < g.segs; s += kFly * kStep) {
+      float2 v[kFly];
+#pragma unroll
+      for (int j = 0; j < kFly; ++j) v[j] = at[static_cast<int64_t>(min(s + j * kStep, g.segs - 1)) * g.Nc];
+#pragma unroll
+      for (int j = 0; j < kFly; ++j) {
+        if (s + j * kStep >= g.segs) break;
+        moved |= v[j].x != c;
+        join_sums(&ref, &sum, v[j].x, v[j].y);
+      }
     }
   }
 #pragma unroll
   for (int o = kRowsPer; o < 32; o *= 2) {
     const float ref2 = __shfl_down_sync(0xffffffffu, ref, o), sum2 = __shfl_down_sync(0xffffffffu, sum, o);
     moved |= __shfl_down_sync(0xffffffffu, moved, o);
-    join(ref2, sum2);
+    join_sums(&ref, &sum, ref2, sum2);
+  }
+  if (g.ids && warp < kRowsPer && r0 + warp < g.rows) {  // sum of w (log w - z + c) of row r0 + warp
+    const int row = r0 + warp;
+    const float c1 = __shfl_sync(0xffffffffu, c, warp);
+    float a = 0.f;
+    for (int e = lane; c1 != INFINITY && e < g.K; e += 32) {
+      const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
+      if (w != -1.f && w != 0.f) a += w * (g.zk[static_cast<int64_t>(row) * g.K + e] - c1);
+    }
+    a = g.a[row] - warp_sum(a) * kLn2;
+    if (lane == 0) s_a[warp] = a;
   }
   if (lane < kRowsPer) {
     s_ref[warp][k] = ref;
@@ -939,14 +1301,14 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   __syncthreads();
   if (threadIdx.x < kRowsPer && in) {
     for (int w = 1; w < kRowWarps; ++w) {
-      join(s_ref[w][k], s_sum[w][k]);
+      join_sums(&ref, &sum, s_ref[w][k], s_sum[w][k]);
       moved |= s_moved[w][k];
     }
     const bool alive = c != INFINITY;
     const float lse2 = ref + log2f(sum), lse = lse2 * kLn2;
     const int64_t i = g.row0 + r;
     if (g.lse) g.lse[i] = alive ? lse : 0.f;
-    if (g.loss) g.loss[i] = alive ? g.a[r] + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;
+    if (g.loss) g.loss[i] = alive ? (g.ids ? s_a[k] : 0.f) + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;
     if (GRAD) {
       float weight = alive ? g.grad_scale * g.scale : 0.f;
       if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
@@ -972,7 +1334,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   const float f = some ? s_f[mine] : 0.f, to = some ? s_to[mine] : 0.f;
   if (fix == 1 || fix == 2) {
     for (int64_t at = (part * 32 + lane) * 8; at < g.Vp; at += kLanes * 8) {
-      const float by = fix == 2 ? 0.f : exp2f(g.sums[(at >> 7) * g.Nc + row].x - to);
+      const float by = fix == 2 ? 0.f : exp2f(g.sums[(at >> g.seg_log) * g.Nc + row].x - to);
       float x[8] = {};
       for (int p = 0; p < g.np_u; ++p) {
         float y[8];
@@ -993,7 +1355,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     for (int e = part * 32 + lane; e < g.K; e += kLanes) {
       const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
       if (w == -1.f || w == 0.f) continue;
-      const int64_t t = g.ids ? __ldg(g.ids + (g.row0 + row) * g.K + e) : __ldg(g.targets + g.row0 + row);
+      const int64_t t = g.ids ? g.sorted[static_cast<int64_t>(row) * g.K + e] : __ldg(g.targets + g.row0 + row);
       float x = exp2f(g.zk[static_cast<int64_t>(row) * g.K + e] - to) - w * peak;
       for (int p = 0; p < g.np_u; ++p)
         reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + t] = take_piece(x);
@@ -1019,19 +1381,20 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   }
 }
 
-// dh from its q parts, COLS columns a thread.
+// A gradient from its parts, COLS columns a thread: dh (blocks below blocks_h), dW.
 template <int COLS>
-__global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__ VocabArgs g) {
+__global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__ VocabArgs g, int blocks_h) {
   grid_dep_wait();
   grid_dep_launch();
-  const uint32_t per_row = g.d / COLS, n = static_cast<uint32_t>(g.rows) * per_row, t = blockIdx.x * 256u + threadIdx.x;
-  if (t >= n) return;
-  const uint32_t r = t / per_row;
-  const int64_t at = static_cast<int64_t>(t) * COLS;
+  const bool dh = static_cast<int>(blockIdx.x) < blocks_h;
+  const int64_t rows = dh ? g.rows : g.V, part = (dh ? g.Nc : g.V) * g.d;
+  const int64_t at = (static_cast<int64_t>(blockIdx.x - (dh ? 0 : blocks_h)) * 256 + threadIdx.x) * COLS;
+  if (at >= rows * g.d) return;
+  const float* from = (dh ? g.parts : g.parts_w) + at;
+  const int q = dh ? g.q : g.q_w;
   float x[COLS] = {};
 #pragma unroll 4
-  for (int p = 0; p < g.q; ++p) {
-    const float* from = g.parts + static_cast<int64_t>(p) * g.Nc * g.d + at;
+  for (int p = 0; p < q; ++p, from += part) {
     if constexpr (COLS == 4) {
       const float4 v = *reinterpret_cast<const float4*>(from);
       x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
@@ -1039,16 +1402,30 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__
       x[0] += *from;
     }
   }
-  const float f = g.f[r];
+  void* dst = g.gh;
+  int dtype = g.gh_dtype;
+  int64_t to = at;
+  if (dh) {
+    const float f = g.f[at / g.d];
 #pragma unroll
-  for (int e = 0; e < COLS; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
-  const int64_t to = g.row0 * g.d + at;
-  if constexpr (COLS == 4) {
-    if (g.gh_dtype == PG_F32) *reinterpret_cast<float4*>(static_cast<float*>(g.gh) + to) = make_float4(x[0], x[1], x[2], x[3]);
-    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.gh) + to) = make_uint2(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]));
+    for (int e = 0; e < COLS; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
+    to += g.row0 * g.d;
   } else {
-    if (g.gh_dtype == PG_F32) static_cast<float*>(g.gh)[to] = x[0];
-    else static_cast<__nv_bfloat16*>(g.gh)[to] = __float2bfloat16_rn(x[0]);
+    const float* add32 = nullptr;
+    const __nv_bfloat16* add16 = nullptr;
+    table_target(g, &dst, &dtype, &add32, &add16);
+#pragma unroll
+    for (int e = 0; e < COLS; ++e) {
+      if (add32) x[e] += add32[at + e];
+      if (add16) x[e] += __bfloat162float(add16[at + e]);
+    }
+  }
+  if constexpr (COLS == 4) {
+    if (dtype == PG_F32) *reinterpret_cast<float4*>(static_cast<float*>(dst) + to) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(dst) + to) = make_uint2(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]));
+  } else {
+    if (dtype == PG_F32) static_cast<float*>(dst)[to] = x[0];
+    else static_cast<__nv_bfloat16*>(dst)[to] = __float2bfloat16_rn(x[0]);
   }
 }
 
@@ -1058,17 +1435,28 @@ struct Sizes {
   int64_t N, V;
   int d, K;
   int h_dtype, w_dtype, gh_dtype, gw_dtype;  // gradients: -1 where there is none
-  bool grad;
+  bool grad, list;
 };
 
 // Whether an operand needs its own copy: pieces of fp32, or rows that TMA cannot step over.
 bool needs_copy(int dtype, int d) { return dtype == PG_F32 || d % 8 != 0; }
 
-// Units of dh along V: as few parts as leave the pairs evenly busy (k-blocks; a part's sums cost a store and a load of
-// its tile, a k-block's time for 4 MB).
+// How units of the gradients' products fall on `units` pairs: those of dh first, `heavy` pairs with one more, then those of
+// dW, of which the others take `delta` more.
+void spread(VocabArgs* g, int units, double cost2, double cost3) {
+  const int64_t n2 = static_cast<int64_t>(g->tiles2) * g->q, n3 = static_cast<int64_t>(g->tiles3) * g->q_w;
+  g->heavy = static_cast<int>(n2 % units);
+  g->light = units - g->heavy;
+  g->delta = g->heavy ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(cost2 / cost3 + 0.5), n3 / g->light)) : 0;
+}
+
+// Parts of dh along V and of dW along the rows: as few as leave the pairs evenly busy. In the time of a k-block (0.65 us), a
+// tile takes 4 more (its first loads, its last sums and stores), a part's sums a store and a load of its tile (4 MB a
+// k-block), and their own launch 8. (Tiles of 128 or 64 columns of d for small problems: a k-block takes as long, 4096 x
+// 50,304 x 768 604, 828 and 1367 us with 256, 128 and 64, and 512 x 1024 x 96 in fp32 76, 81 and 74.)
 void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   const int nm = (g->Nc + kTile - 1) / kTile;
-  const int64_t nv = (g->V + kTile - 1) / kTile, kv = (g->V + kBK - 1) / kBK, kn = (g->Nc + kBK - 1) / kBK;
+  const int64_t nv = (g->V + kTile - 1) / kTile, kv = (g->V + kBK - 1) / kBK, kn = (std::min(g->N, g->Nc) + kBK - 1) / kBK;
   g->nd = (g->d + kTile - 1) / kTile;
   g->tiles2 = has_h ? nm * g->nd : 0;
   g->tiles3 = has_w ? static_cast<int>(nv * g->nd) : 0;
@@ -1076,27 +1464,27 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   g->passes_w = g->gw_dtype == PG_F32 ? passes_of(g->np_u, g->np_f) : 1;
   g->group_h = g->gh_dtype == PG_F32 ? kGroupPieces : 1 << 30;  // (a bf16 gradient's own rounding is far above)
   g->group_w = g->gw_dtype == PG_F32 ? kGroupPieces : 1 << 30;
-  const double cost3 = static_cast<double>(kn) * g->passes_w;
-  double best = 0;
-  g->q = 0;
-  for (int q = 1; q <= (has_h ? 16 : 1); ++q) {
-    if (q > 1 && kv < 2ll * q) break;
-    const int64_t n2 = static_cast<int64_t>(g->tiles2) * q;
-    const int a = static_cast<int>(n2 / units), heavy = static_cast<int>(n2 % units), light = units - heavy;
-    const double cost2 = static_cast<double>((kv + q - 1) / q) * g->passes_h;
-    int delta = heavy ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(cost2 / cost3 + 0.5), g->tiles3 / light)) : 0;
-    const int64_t rest = g->tiles3 - static_cast<int64_t>(delta) * light;
-    const double tail = static_cast<double>((rest + units - 1) / units) * cost3;
-    double t = std::max((a + (heavy ? 1 : 0)) * cost2, a * cost2 + delta * cost3) + tail;
-    if (q > 1) t += static_cast<double>(q) * g->Nc * g->d * 8 / 4e6 + 8;
-    if (g->q == 0 || t < best) {
-      best = t;
+  double best = -1;
+  int best_q = 1, best_qw = 1;
+  for (int q = 1; q <= (has_h ? 16 : 1) && (q == 1 || kv >= 2 * q); ++q)
+    for (int qw = 1; qw <= (has_w ? 32 : 1) && (qw == 1 || (kn >= 2 * qw && 4ll * qw * g->V * g->d <= kPartBytes)); qw *= 2) {
       g->q = q;
-      g->heavy = heavy;
-      g->light = light;
-      g->delta = delta;
+      g->q_w = qw;
+      const double cost2 = static_cast<double>((kv + q - 1) / q) * g->passes_h + 4, cost3 = static_cast<double>((kn + qw - 1) / qw) * g->passes_w + 4;
+      spread(g, units, cost2, cost3);
+      const int a = static_cast<int>(static_cast<int64_t>(g->tiles2) * q / units);
+      const int64_t rest = static_cast<int64_t>(g->tiles3) * qw - static_cast<int64_t>(g->delta) * g->light;
+      double t = std::max((a + (g->heavy ? 1 : 0)) * cost2, a * cost2 + g->delta * cost3) + static_cast<double>((rest + units - 1) / units) * cost3;
+      if (q > 1) t += static_cast<double>(q) * g->Nc * g->d * 8 / 4e6;
+      if (qw > 1) t += static_cast<double>(qw) * g->V * g->d * 8 / 4e6;
+      if (q > 1 || qw > 1) t += 8;
+      if (best >= 0 && t >= best) continue;
+      best = t;
+      best_q = q;
+      best_qw = qw;
     }
-  }
+  g->q = best_q;
+  g->q_w = best_qw;
 }
 
 // Sizes of everything, and its place in the workspace (base null: the size alone).
@@ -1126,7 +1514,14 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 ? kGroupPieces : kGroup;
   const int groups = (blocks + longest - 1) / longest;
   g->group = (blocks + groups - 1) / groups;
-  const int64_t tiles = (s.V + kTile - 1) / kTile;
+  // narrower tiles of the logits where the widest leave pairs idle
+  g->wide = kTile;
+  while (g->wide > 64 && (s.N + kTile - 1) / kTile * ((s.V + g->wide - 1) / g->wide) <= kPlanUnits / 2) g->wide /= 2;
+  if (s.N <= kFewRows) g->wide = 64;
+  g->seg = g->wide / 2;
+  g->seg_log = g->seg == 128 ? 7 : g->seg == 64 ? 6 : 5;
+  g->at_log = s.N <= kFewRows ? 7 : g->seg_log;
+  const int64_t tiles = (s.V + g->wide - 1) / g->wide;
   int64_t most = s.grad ? kKeepBytes / (g->np_u * g->Vp * 2) : kMaxForwardRows;
   most = std::min(most, kSumBytes / (16 * tiles));
   most = std::max<int64_t>(kTile, most / kTile * kTile);
@@ -1135,14 +1530,16 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   const int64_t Nc = g->Nc;
   g->Wp = needs_copy(s.w_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_w * s.V * g->dp)) : nullptr;
   g->hp = needs_copy(s.h_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * Nc * g->dp)) : nullptr;
-  g->sums = reinterpret_cast<float2*>(take(16ll * tiles * Nc));
+  g->sums = reinterpret_cast<float2*>(take(8 * std::max(2 * tiles, s.N <= kFewRows ? 4 * ((s.V + 127) / 128) : 0) * Nc));
   g->zk = reinterpret_cast<float*>(take(4ll * Nc * s.K));
   g->wk = reinterpret_cast<float*>(take(4ll * Nc * s.K));
+  g->sorted = s.list ? reinterpret_cast<int32_t*>(take(4ll * Nc * s.K)) : nullptr;
+  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2ll * (2 * tiles + 1) * Nc)) : nullptr;
   g->c = reinterpret_cast<float*>(take(4 * Nc));
   g->a = reinterpret_cast<float*>(take(4 * Nc));
   g->U = nullptr;
   g->F = nullptr;
-  g->f = g->acc = g->parts = nullptr;
+  g->f = g->acc = g->parts = g->parts_w = nullptr;
   if (s.grad) {
     g->f = reinterpret_cast<float*>(take(4 * Nc));
     g->U = reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_u * Nc * g->Vp));
@@ -1152,6 +1549,7 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
     }
     plan_schedule(g, kPlanUnits, has_h, has_w);
     if (has_h && g->q > 1) g->parts = reinterpret_cast<float*>(take(4ll * g->q * Nc * s.d));
+    if (has_w && g->q_w > 1) g->parts_w = reinterpret_cast<float*>(take(4ll * g->q_w * s.V * s.d));
   }
   return at + 128;
 }
@@ -1244,15 +1642,31 @@ pg_status launch_product(const VocabMaps& maps, const VocabArgs& g, int64_t jobs
   if (st != PG_OK) return st;
   units = static_cast<int>(std::min<int64_t>(units, jobs));
   VocabArgs a = g;
-  if (KIND == kGrads) {  // the same parts on however many pairs there are
-    const int64_t n2 = static_cast<int64_t>(a.tiles2) * a.q;
-    a.heavy = static_cast<int>(n2 % units);
-    a.light = units - a.heavy;
-    const double cost2 = static_cast<double>((a.V + kBK - 1) / kBK) / a.q * a.passes_h;
-    const double cost3 = static_cast<double>((a.rows + kBK - 1) / kBK) * a.passes_w;
-    a.delta = a.heavy ? static_cast<int>(std::min<int64_t>(static_cast<int64_t>(cost2 / cost3 + 0.5), a.tiles3 / a.light)) : 0;
-  }
+  if (KIND == kGrads)  // the same parts on however many pairs there are
+    spread(&a, units, static_cast<double>((a.V + kBK - 1) / kBK) / a.q * a.passes_h + 4,
+           static_cast<double>((a.rows + kBK - 1) / kBK) / a.q_w * a.passes_w + 4);
   return launch_next(vocab_product_kernel<KIND, GROUPS>, 2ll * units, kThreads, kSmem, true, true, stream, maps, a);
+}
+
+// CTAs of the first product for few rows. (No more than its tiles: 4 sums a CTA fit in place of 4 a tile.)
+int64_t few_blocks(int64_t V) { return std::min<int64_t>(sm_count(), (V + 127) / 128); }
+
+template <int NT>
+pg_status launch_few(const VocabMaps& maps, const VocabArgs& g, bool keep, cudaStream_t stream) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return PG_ERR_DEVICE;
+  if (!known[dev].load(std::memory_order_relaxed)) {
+    const int bytes = static_cast<int>(Few<NT>::kSmem);
+    if ((e = cudaFuncSetAttribute(vocab_few_kernel<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(vocab_few_kernel<NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+      return cuda_fail(e);
+    known[dev].store(1, std::memory_order_relaxed);
+  }
+  return launch_next(keep ? vocab_few_kernel<NT, true> : vocab_few_kernel<NT, false>, few_blocks(g.V), Few<NT>::kThreads, Few<NT>::kSmem, false, true,
+                     stream, maps, g);
 }
 
 using PrepareFn = void (*)(const VocabArgs, int, int);
@@ -1288,39 +1702,51 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     g.first = row0 == 0;
     g.last = row0 + g.Nc >= s.N;
     const int64_t blocks_w = g.Wp && g.first ? split_blocks(s.V) : 0, blocks_h = g.hp ? split_blocks(g.rows) : 0;
-    const int64_t blocks = blocks_w + blocks_h + (list ? g.rows : (g.rows + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
+    const int64_t blocks = blocks_w + blocks_h + (g.rows + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
     if (blocks >= (1ll << 31)) return PG_ERR_SHAPE;
     st = launch_next(prepare, blocks, kPrepThreads, 0, false, !g.first, stream, g, static_cast<int>(blocks_w), static_cast<int>(blocks_h));
     if (st != PG_OK) return st;
     const uint8_t* h = static_cast<const uint8_t*>(g.h) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.h_dtype));
-    if (!vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    const int few = s.N > kFewRows ? 0 : s.N > 64 ? 128 : s.N > 32 ? 64 : 32;
+    if (!vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, kLine, few ? few : 128,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
       return PG_ERR_CUDA;
-    const int64_t jobs = static_cast<int64_t>((g.rows + kTile - 1) / kTile) * ((s.V + kTile - 1) / kTile);
+    const int64_t jobs = static_cast<int64_t>((g.rows + kTile - 1) / kTile) * ((s.V + g.wide - 1) / g.wide);
     if (s.grad) {
       if (!vocab_map(&maps.U, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
           !vocab_map(&maps.Ust, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
           (g.F && !vocab_map(&maps.F, g.F, g.np_f, g.rows, s.d, g.dp, g.Nc, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)))
         return PG_ERR_CUDA;
       if (!g.F) maps.F = maps.U;
-      st = groups ? launch_product<kKeep, true>(maps, g, jobs, stream) : launch_product<kKeep, false>(maps, g, jobs, stream);
     } else {
       maps.U = maps.Ust = maps.F = maps.h;
-      st = groups ? launch_product<kSums, true>(maps, g, jobs, stream) : launch_product<kSums, false>(maps, g, jobs, stream);
     }
+    if (few)
+      st = few == 32 ? launch_few<32>(maps, g, s.grad, stream) : few == 64 ? launch_few<64>(maps, g, s.grad, stream)
+                                                                             : launch_few<128>(maps, g, s.grad, stream);
+    else if (s.grad)
+      st = groups ? launch_product<kKeep, true>(maps, g, jobs, stream) : launch_product<kKeep, false>(maps, g, jobs, stream);
+    else
+      st = groups ? launch_product<kSums, true>(maps, g, jobs, stream) : launch_product<kSums, false>(maps, g, jobs, stream);
     if (st != PG_OK) return st;
+    g.segs = few && !s.grad ? static_cast<int>(4 * few_blocks(g.V)) : static_cast<int>((g.V + g.seg - 1) / g.seg);
     st = launch_next(rows_fn(s.grad, s.h_dtype, vec_h), (g.rows + kRowsPer - 1) / kRowsPer, 32 * kRowWarps, 0, false, true, stream, g);
     if (st != PG_OK) return st;
     VocabArgs b = g;
     if (g.tiles2) b.tiles2 = (g.rows + kTile - 1) / kTile * g.nd;  // a last chunk has fewer rows
-    const int64_t units = s.grad ? static_cast<int64_t>(b.tiles2) * b.q + b.tiles3 : 0;
+    b.q_w = std::min(g.q_w, (g.rows + kBK - 1) / kBK);             // (no part without a k-block)
+    const int64_t units = s.grad ? static_cast<int64_t>(b.tiles2) * b.q + static_cast<int64_t>(b.tiles3) * b.q_w : 0;
     if (units == 0) continue;
     const bool pieces = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32;
     if ((st = pieces ? launch_product<kGrads, true>(maps, b, units, stream) : launch_product<kGrads, false>(maps, b, units, stream)) != PG_OK)
       return st;
-    if (g.parts) {
-      const bool four = s.d % 4 == 0 && aligned(g.gh, 4 * dtype_bytes(s.gh_dtype));
-      const int64_t threads = static_cast<int64_t>(g.rows) * s.d / (four ? 4 : 1);
-      st = launch_next(four ? vocab_join_kernel<4> : vocab_join_kernel<1>, (threads + 255) / 256, 256, 0, false, true, stream, g);
+    if (g.parts || g.parts_w) {
+      const bool four = s.d % 4 == 0 && (!g.parts || aligned(g.gh, 4 * dtype_bytes(s.gh_dtype))) &&
+                        (!g.parts_w || aligned(g.gw, 4 * dtype_bytes(s.gw_dtype)));
+      auto join_blocks = [&](int64_t rows) { return (rows * s.d / (four ? 4 : 1) + 255) / 256; };
+      const int64_t join_h = g.parts ? join_blocks(g.rows) : 0, join_w = g.parts_w ? join_blocks(s.V) : 0;
+      if (join_h + join_w >= (1ll << 31)) return PG_ERR_SHAPE;
+      st = launch_next(four ? vocab_join_kernel<4> : vocab_join_kernel<1>, join_h + join_w, 256, 0, false, true, stream, b, static_cast<int>(join_h));
       if (st != PG_OK) return st;
     }
   }
@@ -1370,7 +1796,7 @@ pg_status call_vocab(const Call& c) {
   size_t need;
   pg_status st = vocab_workspace(c.s, &need);
   if (st != PG_OK) return st;
-  const bool list = c.targets == nullptr && c.s.K >= 1 && c.t_dtype >= 0;
+  const bool list = c.s.list;
   if (list && !real_dtype(c.t_dtype)) return PG_ERR_DTYPE;
   if (!std::isfinite(c.scale) || !std::isfinite(c.zl) || !std::isfinite(c.grad_scale) || !std::isfinite(c.inv_t) || !(c.inv_t > 0.f) ||
       !std::isfinite(c.scale * c.inv_t * kLog2e))
@@ -1423,29 +1849,29 @@ pg_status call_vocab(const Call& c) {
 using namespace pg;
 
 extern "C" pg_status pg_vocab_ce_workspace_size(int64_t N, int64_t V, int32_t d, int32_t h_dtype, int32_t w_dtype, size_t* bytes) {
-  return vocab_workspace({N, V, d, 1, h_dtype, w_dtype, -1, -1, false}, bytes);
+  return vocab_workspace({N, V, d, 1, h_dtype, w_dtype, -1, -1, false, false}, bytes);
 }
 
 extern "C" pg_status pg_vocab_ce_grad_workspace_size(int64_t N, int64_t V, int32_t d, int32_t h_dtype, int32_t w_dtype,
                                                      int32_t gh_dtype, int32_t gw_dtype, size_t* bytes) {
-  return vocab_workspace({N, V, d, 1, h_dtype, w_dtype, gh_dtype, gw_dtype, true}, bytes);
+  return vocab_workspace({N, V, d, 1, h_dtype, w_dtype, gh_dtype, gw_dtype, true, false}, bytes);
 }
 
 extern "C" pg_status pg_vocab_distill_workspace_size(int64_t N, int64_t V, int32_t d, int32_t K, int32_t h_dtype, int32_t w_dtype,
                                                      size_t* bytes) {
-  return vocab_workspace({N, V, d, K, h_dtype, w_dtype, -1, -1, false}, bytes);
+  return vocab_workspace({N, V, d, K, h_dtype, w_dtype, -1, -1, false, true}, bytes);
 }
 
 extern "C" pg_status pg_vocab_distill_grad_workspace_size(int64_t N, int64_t V, int32_t d, int32_t K, int32_t h_dtype,
                                                           int32_t w_dtype, int32_t gh_dtype, int32_t gw_dtype, size_t* bytes) {
-  return vocab_workspace({N, V, d, K, h_dtype, w_dtype, gh_dtype, gw_dtype, true}, bytes);
+  return vocab_workspace({N, V, d, K, h_dtype, w_dtype, gh_dtype, gw_dtype, true, true}, bytes);
 }
 
 extern "C" pg_status pg_vocab_ce(const void* h, int32_t h_dtype, int64_t N, const void* W, int32_t w_dtype, int64_t V, int32_t d,
                                  const int32_t* targets, float scale, float z_loss, float* loss, float* lse, void* workspace,
                                  size_t workspace_bytes, int32_t* err_index, pg_stream_t stream) {
   Call c = {};
-  c.s = {N, V, d, 1, h_dtype, w_dtype, -1, -1, false};
+  c.s = {N, V, d, 1, h_dtype, w_dtype, -1, -1, false, false};
   c.h = h; c.W = W; c.targets = targets; c.t_dtype = -1;
   c.scale = scale; c.inv_t = 1.f; c.zl = z_loss;
   c.loss = loss; c.lse = lse;
@@ -1459,7 +1885,7 @@ extern "C" pg_status pg_vocab_ce_grad(const void* h, int32_t h_dtype, int64_t N,
                                       int32_t accumulate, void* workspace, size_t workspace_bytes, int32_t* err_index,
                                       pg_stream_t stream) {
   Call c = {};
-  c.s = {N, V, d, 1, h_dtype, w_dtype, gh_dtype, gw_dtype, true};
+  c.s = {N, V, d, 1, h_dtype, w_dtype, gh_dtype, gw_dtype, true, false};
   c.h = h; c.W = W; c.targets = targets; c.t_dtype = -1;
   c.row_weight = row_weight;
   c.scale = scale; c.inv_t = 1.f; c.zl = z_loss; c.grad_scale = grad_scale;
@@ -1474,7 +1900,7 @@ extern "C" pg_status pg_vocab_distill(const void* h, int32_t h_dtype, int64_t N,
                                       float temperature, float* loss, float* lse, void* workspace, size_t workspace_bytes,
                                       int32_t* err_index, pg_stream_t stream) {
   Call c = {};
-  c.s = {N, V, d, K, h_dtype, w_dtype, -1, -1, false};
+  c.s = {N, V, d, K, h_dtype, w_dtype, -1, -1, false, true};
   if (!real_dtype(logits_dtype)) return PG_ERR_DTYPE;
   c.h = h; c.W = W; c.ids = ids; c.tlogits = logits; c.t_dtype = logits_dtype;
   c.scale = scale; c.inv_t = 1.f / temperature;
@@ -1489,7 +1915,7 @@ extern "C" pg_status pg_vocab_distill_grad(const void* h, int32_t h_dtype, int64
                                            void* grad_h, int32_t gh_dtype, void* grad_w, int32_t gw_dtype, int32_t accumulate,
                                            void* workspace, size_t workspace_bytes, int32_t* err_index, pg_stream_t stream) {
   Call c = {};
-  c.s = {N, V, d, K, h_dtype, w_dtype, gh_dtype, gw_dtype, true};
+  c.s = {N, V, d, K, h_dtype, w_dtype, gh_dtype, gw_dtype, true, true};
   if (!real_dtype(logits_dtype)) return PG_ERR_DTYPE;
   c.h = h; c.W = W; c.ids = ids; c.tlogits = logits; c.t_dtype = logits_dtype;
   c.row_weight = row_weight;
