@@ -683,13 +683,15 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
   }
   const bool vec = g.d % 4 == 0 && reinterpret_cast<uintptr_t>(dst) % (dtype == PG_F32 ? 16 : 8) == 0 &&
                    (!add32 || reinterpret_cast<uintptr_t>(add32) % 16 == 0);
-#pragma unroll 1
+  uint32_t r2[2][32];
+  tmem_load(from, r2[0]);
+#pragma unroll
   for (int ch = 0; ch < 4; ++ch) {
     const int c0 = static_cast<int>(w.col0) + half * (kTile / 2) + ch * 32;
     if (c0 >= g.d) break;
-    uint32_t r[32];
-    tmem_load(from + ch * 32, r);
+    uint32_t(&r)[32] = r2[ch & 1];
     tmem_wait(r);
+    if (ch < 3) tmem_load(from + (ch + 1) * 32, r2[(ch + 1) & 1]);
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -734,6 +736,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
       }
     }
   }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 template <int KIND, bool GROUPS>
@@ -887,9 +890,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto release = [&]() {
         fence_before();
         __syncwarp();
+        // (Released to the CTA alone: what the issuing thread waits for are this warp's TMEM loads, which are done. A release
+        // to the cluster waits until the epilogue's global stores are.)
         if (lane == 0)
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                           in_cta(smem_addr(&bars->acc_empty[acc]), 0))
+          asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(smem_addr(&bars->acc_empty[acc]), 0))
                        : "memory");
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
@@ -1006,16 +1010,11 @@ __device__ __forceinline__ float reduce_columns(float (&x)[32], Op op) {
   return x[0];
 }
 
-// sum 2^ref + sum2 2^ref2 as one, at the larger reference.
-__device__ __forceinline__ void join_sums(float* ref, float* sum, float ref2, float sum2) {
-  if (ref2 == *ref) {
-    *sum += sum2;
-  } else if (ref2 > *ref) {
-    *sum = *sum * exp2f(*ref - ref2) + sum2;
-    *ref = ref2;
-  } else {
-    *sum += sum2 * exp2f(ref2 - *ref);
-  }
+// Sums (reference, sum) as one, at the larger reference.
+__device__ __forceinline__ float2 joined(float2 a, float2 b) {
+  if (b.x == a.x) return make_float2(a.x, a.y + b.y);
+  if (b.x > a.x) return make_float2(b.x, a.y * exp2f(a.x - b.x) + b.y);
+  return make_float2(a.x, a.y + b.y * exp2f(b.x - a.x));
 }
 
 template <int NT, bool KEEP>
@@ -1027,6 +1026,8 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   __shared__ FewBars<NT> bars_s;
   __shared__ float s_c[NT];
+  __shared__ float2 s_all[4][KEEP ? 1 : NT];
+  __shared__ __align__(16) uint16_t s_u[KEEP ? 4 : 1][KEEP ? 32 : 1][40];  // (rows of 80 bytes)
   FewBars<NT>* bars = &bars_s;
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1120,99 +1121,121 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
     }
   } else {
     const int quarter = warp & 3;
-    float all_ref[NT / 32], all_sum[NT / 32];  // without U: one sum a warp, in a segment of its own
-#pragma unroll
-    for (int k = 0; k < NT / 32; ++k) {
-      all_ref[k] = s_c[k * 32 + lane];
-      all_sum[k] = 0.f;
+    if (!KEEP) {  // one sum a warp, in a segment of its own
+      for (int k = lane; k < NT; k += 32) s_all[warp - 2][k] = make_float2(s_c[k], 0.f);
+      __syncwarp();
     }
     for (int t = blockIdx.x; fine && t < tiles; t += gridDim.x) {
       const int64_t v0 = t * 128ll + quarter * 32, v = v0 + lane;
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      float z[NT];
-      for (int k0 = 0; k0 < blocks; k0 += g.group) {
-        if (!__all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
-          fine = false;
-          break;
-        }
+      auto acquire = [&]() {
+        fine = __all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort));
         fence_after();
-#pragma unroll
-        for (int c = 0; c < NT; c += 32) {
-          uint32_t r[32];
-          tmem_load(from + static_cast<uint32_t>(acc * NT + c), r);
-          tmem_wait(r);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) z[c + k] = k0 == 0 ? __uint_as_float(r[k]) : z[c + k] + __uint_as_float(r[k]);
-        }
+        return fine;
+      };
+      auto release = [&]() {
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&bars->acc_empty[acc]));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+      };
+      if (g.group < blocks) {  // as in the other products: groups in registers, and back to TMEM with the last
+        float z[NT];
+#pragma unroll
+        for (int k = 0; k < NT; ++k) z[k] = 0.f;
+        for (int k0 = 0; k0 < blocks; k0 += g.group) {
+          if (!acquire()) break;
+          const bool last = k0 + g.group >= blocks;
+#pragma unroll
+          for (int c = 0; c < NT; c += 32) {
+            uint32_t r[32];
+            tmem_load(from + static_cast<uint32_t>(acc * NT + c), r);
+            tmem_wait(r);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z[c + k] += __uint_as_float(r[k]);
+            if (last) tmem_store(from + static_cast<uint32_t>(acc * NT + c), z + c);
+          }
+          if (last) tmem_stored();
+          else release();
+        }
+        if (!fine) break;
+      } else if (!acquire()) {
+        break;
       }
-      if (!fine || v0 >= g.V) continue;
       const bool in = v < g.V;
       const int64_t seg = v0 >> 5;
-#pragma unroll
-      for (int c0 = 0; c0 < NT; c0 += 32) {
-        if (c0 >= g.rows) break;
+      // 32 rows of h at a time. (Unrolled over all of them the code ran out of the instruction cache: 64 x 50,304 x 768 with
+      // U 92 us.)
+#pragma unroll 1
+      for (int c0 = 0; c0 < g.rows && v0 < g.V; c0 += 32) {
+        uint32_t r[32];
+        tmem_load(from + static_cast<uint32_t>(acc * NT + c0), r);
         const int row = c0 + lane;  // the row of h whose sum this lane gets
         const float c = s_c[row];
         const bool alive = c != INFINITY;
-        if (g.ids) {
-          int e = 0, end = 0;
-          if (row < g.rows) {
-            e = g.at[static_cast<int64_t>(t) * g.Nc + row];  // (the four warps' tokens)
-            end = g.at[(t + 1ll) * g.Nc + row];
-          }
-          for (uint32_t left = __ballot_sync(0xffffffffu, e < end); left; left &= left - 1) {
-            const int l = __ffs(left) - 1, e1 = __shfl_sync(0xffffffffu, e, l), end1 = __shfl_sync(0xffffffffu, end, l);
-            float y = 0.f;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) y = k == l ? z[c0 + k] : y;
-            for (int j = e1; j < end1; ++j)
-              if (g.sorted[static_cast<int64_t>(c0 + l) * g.K + j] == v) g.zk[static_cast<int64_t>(c0 + l) * g.K + j] = y * g.k2;
-          }
+        int e = 0, end = 0;
+        if (g.ids && row < g.rows) {
+          e = g.at[static_cast<int64_t>(t) * g.Nc + row];  // (the four warps' tokens)
+          end = g.at[(t + 1ll) * g.Nc + row];
         }
-        float x[32], ref = c;
+        tmem_wait(r);
+        for (uint32_t left = __ballot_sync(0xffffffffu, e < end); left; left &= left - 1) {
+          const int l = __ffs(left) - 1, e1 = __shfl_sync(0xffffffffu, e, l), end1 = __shfl_sync(0xffffffffu, end, l);
+          float y = 0.f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = in ? exp2_fast(fmaf(z[c0 + k], g.k2, -s_c[c0 + k])) : 0.f;
-        float u[32];
-        if (KEEP)
-#pragma unroll
-          for (int k = 0; k < 32; ++k) u[k] = x[k];
-        float sum = reduce_columns(x, [](float a, float b) { return a + b; });
-        const bool over = alive && !(sum <= kSumLimit);
-        if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the segment's largest for a reference
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = in ? z[c0 + k] * g.k2 : -INFINITY;
-          const float top = reduce_columns(x, [](float a, float b) { return fmaxf(a, b); });
-          if (over) ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = in ? exp2_fast(fmaf(z[c0 + k], g.k2, -__shfl_sync(0xffffffffu, ref, k))) : 0.f;
-          if (KEEP)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) u[k] = x[k];
-          sum = reduce_columns(x, [](float a, float b) { return a + b; });
+          for (int k = 0; k < 32; ++k) y = k == l ? __uint_as_float(r[k]) : y;
+          for (int j = e1; j < end1; ++j)
+            if (g.sorted[static_cast<int64_t>(c0 + l) * g.K + j] == v) g.zk[static_cast<int64_t>(c0 + l) * g.K + j] = y * g.k2;
         }
-        if (!KEEP) join_sums(&all_ref[c0 / 32], &all_sum[c0 / 32], ref, sum);
-        else if (row < g.rows) g.sums[seg * g.Nc + row] = make_float2(ref, sum);
-        if (KEEP && in) {
+        float ref = c, sum;
+#pragma unroll 1
+        for (int again = 0; again < 2; ++again) {
+          float x[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            if (c0 + k >= g.rows) break;
-            if (s_c[c0 + k] == INFINITY) u[k] = 0.f;
-            for (int p = 0; p < g.np_u; ++p)
-              reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + c0 + k) * g.Vp + v] = take_piece(u[k]);
+            const float to = again ? __shfl_sync(0xffffffffu, ref, k) : s_c[c0 + k];
+            x[k] = in ? exp2_fast(fmaf(__uint_as_float(r[k]), g.k2, -to)) : 0.f;
           }
+          if (KEEP) {
+            for (int p = 0; p < g.np_u; ++p) {
+              float y[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = x[k];
+              for (int q = 0; q < p; ++q)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) take_piece(y[k]);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s_u[warp - 2][k][lane] = s_c[c0 + k] == INFINITY ? 0 : take_piece(y[k]);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int to = k * 8 + lane / 4;
+                if (c0 + to < g.rows)
+                  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(g.U) + (static_cast<int64_t>(p) * g.Nc + c0 + to) * g.Vp + v0 +
+                                            lane % 4 * 8) = *reinterpret_cast<const uint4*>(&s_u[warp - 2][to][lane % 4 * 8]);
+              }
+            }
+          }
+          sum = reduce_columns(x, [](float a, float b) { return a + b; });
+          const bool over = !again && alive && !(sum <= kSumLimit);
+          if (!__any_sync(0xffffffffu, over)) break;  // else: logits far above the targets', the segment's largest for a reference
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = in ? __uint_as_float(r[k]) * g.k2 : -INFINITY;
+          const float top = reduce_columns(x, [](float a, float b) { return fmaxf(a, b); });
+          if (over) ref = top == -INFINITY ? 0.f : top;
+        }
+        if (KEEP) {
+          if (row < g.rows) g.sums[seg * g.Nc + row] = make_float2(ref, sum);
+        } else {
+          s_all[warp - 2][row] = joined(s_all[warp - 2][row], make_float2(ref, sum));
         }
       }
+      release();
     }
     if (!KEEP)
-#pragma unroll
-      for (int k = 0; k < NT / 32; ++k)
-        if (k * 32 + lane < g.rows)
-          g.sums[(blockIdx.x * 4ll + quarter) * g.Nc + k * 32 + lane] = make_float2(all_ref[k], all_sum[k]);
+      for (int k = lane; k < g.rows; k += 32) g.sums[(blockIdx.x * 4ll + quarter) * g.Nc + k] = s_all[warp - 2][k];
   }
   if (!fine) {
     atomicOr(g.err_word, kErrVocab);
@@ -1250,7 +1273,7 @@ constexpr int kRowWarps = 16, kRowsPer = 8;
 // and loss; for the gradients f, the targets' places of U, and f h (two warps a row).
 template <bool GRAD, int HT, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid_constant__ VocabArgs g) {
-  __shared__ float s_ref[kRowWarps][kRowsPer], s_sum[kRowWarps][kRowsPer];
+  __shared__ float2 s_all[kRowWarps][kRowsPer];
   __shared__ int s_moved[kRowWarps][kRowsPer], s_fix[kRowsPer];
   __shared__ float s_to[kRowsPer], s_f[kRowsPer], s_lse[kRowsPer], s_beta[kRowsPer], s_a[kRowsPer];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (kRowsPer - 1);
@@ -1259,7 +1282,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   grid_dep_wait();
   grid_dep_launch();
   const float c = in ? g.c[r] : INFINITY;
-  float ref = c, sum = 0.f;
+  float2 all = make_float2(c, 0.f);
   int moved = 0;
   if (in && c != INFINITY) {
     const float2* at = g.sums + r;
@@ -1272,15 +1295,15 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
       for (int j = 0; j < kFly; ++j) {
         if (s + j * kStep >= g.segs) break;
         moved |= v[j].x != c;
-        join_sums(&ref, &sum, v[j].x, v[j].y);
+        all = joined(all, v[j]);
       }
     }
   }
 #pragma unroll
   for (int o = kRowsPer; o < 32; o *= 2) {
-    const float ref2 = __shfl_down_sync(0xffffffffu, ref, o), sum2 = __shfl_down_sync(0xffffffffu, sum, o);
+    const float2 other = make_float2(__shfl_down_sync(0xffffffffu, all.x, o), __shfl_down_sync(0xffffffffu, all.y, o));
     moved |= __shfl_down_sync(0xffffffffu, moved, o);
-    join_sums(&ref, &sum, ref2, sum2);
+    all = joined(all, other);
   }
   if (g.ids && warp < kRowsPer && r0 + warp < g.rows) {  // sum of w (log w - z + c) of row r0 + warp
     const int row = r0 + warp;
@@ -1294,18 +1317,17 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     if (lane == 0) s_a[warp] = a;
   }
   if (lane < kRowsPer) {
-    s_ref[warp][k] = ref;
-    s_sum[warp][k] = sum;
+    s_all[warp][k] = all;
     s_moved[warp][k] = moved;
   }
   __syncthreads();
   if (threadIdx.x < kRowsPer && in) {
     for (int w = 1; w < kRowWarps; ++w) {
-      join_sums(&ref, &sum, s_ref[w][k], s_sum[w][k]);
+      all = joined(all, s_all[w][k]);
       moved |= s_moved[w][k];
     }
     const bool alive = c != INFINITY;
-    const float lse2 = ref + log2f(sum), lse = lse2 * kLn2;
+    const float lse2 = all.x + log2f(all.y), lse = lse2 * kLn2;
     const int64_t i = g.row0 + r;
     if (g.lse) g.lse[i] = alive ? lse : 0.f;
     if (g.loss) g.loss[i] = alive ? (g.ids ? s_a[k] : 0.f) + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;

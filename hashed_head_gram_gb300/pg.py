@@ -727,32 +727,58 @@ def orthogonalize(G: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, s
 # ------------------------------------------------------------------- losses over the vocabulary
 
 
-def _here(*tensors):
-    """The calls run on the current device: a tensor of another one would be read through a foreign address."""
-    dev = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
-    for t in tensors:
-        _expect(t is None or (t.is_cuda and t.get_device() == dev), "tensors must live on the current CUDA device")
+def _here(t: Optional[torch.Tensor], dev: int):
+    """_at of a tensor that has to live on device `dev`: the calls run on the current one, where a tensor of another
+    would be read through a foreign address."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("tensors must live on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
 
 
-def _hidden(h: torch.Tensor, W: torch.Tensor, rows):
+def _device() -> int:
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):  # no CUDA: no tensor is on device 0 either
+        return 0
+
+
+def _bytes(workspace: Optional[torch.Tensor]) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _row(t: Optional[torch.Tensor], N: int, what: str):
+    if t is not None and not (t.dtype is torch.float32 and t.dim() == 1 and t.shape[0] == N):
+        raise ValueError(f"{what} must be float32 [N]")
+
+
+def _sizes(h: torch.Tensor, W: torch.Tensor):
     _expect(h.dim() == 2 and W.dim() == 2 and h.shape[1] == W.shape[1], "h must be [N, d] and W [V, d]")
-    for name, t in rows.items():
-        _expect(t is None or (t.dtype == torch.float32 and t.shape == (h.shape[0],)), f"{name} must be float32 [N]")
+    return h.shape[0], W.shape[0], W.shape[1]
 
 
-def _list(h: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor):
-    _expect(ids.dtype == torch.int32 and ids.dim() == 2 and ids.shape[0] == h.shape[0], "teacher_ids must be int32 [N, K]")
+def _targets(targets: torch.Tensor, N: int, err_index: Optional[torch.Tensor]):
+    _expect(targets.dtype is torch.int32 and targets.numel() == N, "targets must be int32 [N]")
+    _index(err_index)
+
+
+def _list(ids: torch.Tensor, logits: torch.Tensor, N: int, err_index: Optional[torch.Tensor]):
+    _expect(ids.dtype is torch.int32 and ids.dim() == 2 and ids.shape[0] == N, "teacher_ids must be int32 [N, K]")
     _expect(logits.shape == ids.shape, "teacher_logits must be [N, K]")
+    _index(err_index)
+
+
+def _index(err_index: Optional[torch.Tensor]):
+    _expect(err_index is None or (err_index.dtype is torch.int32 and err_index.numel() >= 1), "err_index must be an int32 tensor")
 
 
 def _gradients(h: torch.Tensor, W: torch.Tensor, grad_h: Optional[torch.Tensor], grad_W: Optional[torch.Tensor]):
     _expect(grad_h is None or grad_h.shape == h.shape, "grad_h must be [N, d]")
     _expect(grad_W is None or grad_W.shape == W.shape, "grad_W must be [V, d]")
     return -1 if grad_h is None else _dtype(grad_h), -1 if grad_W is None else _dtype(grad_W)
-
-
-def _index(err_index: Optional[torch.Tensor]):
-    _expect(err_index is None or (err_index.dtype == torch.int32 and err_index.numel() >= 1), "err_index must be an int32 tensor")
 
 
 def _code(dtype: Optional[int]) -> int:
@@ -770,14 +796,14 @@ def vocab_ce(h: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss: torc
              err_index: Optional[torch.Tensor] = None, stream=None):
     """loss[i] = lse[i] - z[i, targets[i]] + z_loss * lse[i]^2 over the logits z = scale * h W^T, which are not
     stored; h [N, d] and W [V, d] float32 or bfloat16, targets int32 [N] (outside [0, V): no target)."""
-    _hidden(h, W, {"loss": loss, "lse": lse})
-    _expect(targets.dtype == torch.int32 and targets.numel() == h.shape[0], "targets must be int32 [N]")
-    _index(err_index)
-    hd, wd = _dtype(h), _dtype(W)
-    _here(h, W, targets, loss, lse, workspace, err_index)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_vocab_ce(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(targets), scale, z_loss,
-                            _at(loss), _at(lse), _at(workspace), ws_bytes, _at(err_index), _stream(stream)), "pg_vocab_ce")
+    N, V, d = _sizes(h, W)
+    _targets(targets, N, err_index)
+    _row(loss, N, "loss")
+    _row(lse, N, "lse")
+    hd, wd, dev = _dtype(h), _dtype(W), _device()
+    _check(_lib.pg_vocab_ce(_here(h, dev), hd, N, _here(W, dev), wd, V, d, _here(targets, dev), scale, z_loss, _here(loss, dev),
+                            _here(lse, dev), _here(workspace, dev), _bytes(workspace), _here(err_index, dev), _stream(stream)),
+           "pg_vocab_ce")
 
 
 def vocab_ce_grad_workspace_size(N: int, V: int, d: int, h_dtype: int, w_dtype: int, grad_h_dtype: Optional[int],
@@ -796,17 +822,17 @@ def vocab_ce_grad(h: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss:
                   lse: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
     """vocab_ce with the gradients of grad_scale * sum_i row_weight[i] * loss[i]: grad_h [N, d] and grad_W [V, d] (added
     to what is there when accumulate is set), either of them None where it is not asked for."""
-    _hidden(h, W, {"loss": loss, "lse": lse, "row_weight": row_weight})
-    _expect(targets.dtype == torch.int32 and targets.numel() == h.shape[0], "targets must be int32 [N]")
-    _index(err_index)
-    hd, wd = _dtype(h), _dtype(W)
+    N, V, d = _sizes(h, W)
+    _targets(targets, N, err_index)
+    _row(loss, N, "loss")
+    _row(lse, N, "lse")
+    _row(row_weight, N, "row_weight")
     ghd, gwd = _gradients(h, W, grad_h, grad_W)
-    _here(h, W, targets, loss, lse, row_weight, grad_h, grad_W, workspace, err_index)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_vocab_ce_grad(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(targets), scale, z_loss,
-                                 _at(row_weight), grad_scale, _at(loss), _at(lse), _at(grad_h), ghd, _at(grad_W), gwd,
-                                 1 if accumulate else 0, _at(workspace), ws_bytes, _at(err_index), _stream(stream)),
-           "pg_vocab_ce_grad")
+    hd, wd, dev = _dtype(h), _dtype(W), _device()
+    _check(_lib.pg_vocab_ce_grad(_here(h, dev), hd, N, _here(W, dev), wd, V, d, _here(targets, dev), scale, z_loss,
+                                 _here(row_weight, dev), grad_scale, _here(loss, dev), _here(lse, dev), _here(grad_h, dev), ghd,
+                                 _here(grad_W, dev), gwd, 1 if accumulate else 0, _here(workspace, dev), _bytes(workspace),
+                                 _here(err_index, dev), _stream(stream)), "pg_vocab_ce_grad")
 
 
 def vocab_distill_workspace_size(N: int, V: int, d: int, K: int, h_dtype: int, w_dtype: int) -> int:
@@ -820,15 +846,14 @@ def vocab_distill(h: torch.Tensor, W: torch.Tensor, teacher_ids: torch.Tensor, t
                   lse: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
     """loss[i] = KL(softmax(teacher_logits[i] / temperature) over the tokens teacher_ids[i], softmax(z[i] / temperature)) with
     z = scale * h W^T; teacher_ids int32 [N, K] (outside [0, V): no token), teacher_logits [N, K] float32 or bfloat16."""
-    _hidden(h, W, {"loss": loss, "lse": lse})
-    _list(h, teacher_ids, teacher_logits)
-    _index(err_index)
-    hd, wd, td = _dtype(h), _dtype(W), _dtype(teacher_logits)
-    _here(h, W, teacher_ids, teacher_logits, loss, lse, workspace, err_index)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_vocab_distill(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(teacher_ids),
-                                 _at(teacher_logits), td, teacher_ids.shape[1], scale, temperature, _at(loss), _at(lse),
-                                 _at(workspace), ws_bytes, _at(err_index), _stream(stream)), "pg_vocab_distill")
+    N, V, d = _sizes(h, W)
+    _list(teacher_ids, teacher_logits, N, err_index)
+    _row(loss, N, "loss")
+    _row(lse, N, "lse")
+    hd, wd, td, dev = _dtype(h), _dtype(W), _dtype(teacher_logits), _device()
+    _check(_lib.pg_vocab_distill(_here(h, dev), hd, N, _here(W, dev), wd, V, d, _here(teacher_ids, dev), _here(teacher_logits, dev), td,
+                                 teacher_ids.shape[1], scale, temperature, _here(loss, dev), _here(lse, dev), _here(workspace, dev),
+                                 _bytes(workspace), _here(err_index, dev), _stream(stream)), "pg_vocab_distill")
 
 
 def vocab_distill_grad_workspace_size(N: int, V: int, d: int, K: int, h_dtype: int, w_dtype: int, grad_h_dtype: Optional[int],
@@ -846,15 +871,15 @@ def vocab_distill_grad(h: torch.Tensor, W: torch.Tensor, teacher_ids: torch.Tens
                        grad_scale: float = 1.0, row_weight: Optional[torch.Tensor] = None, accumulate: bool = False,
                        lse: Optional[torch.Tensor] = None, err_index: Optional[torch.Tensor] = None, stream=None):
     """vocab_distill with the gradients of grad_scale * sum_i row_weight[i] * loss[i], as in vocab_ce_grad."""
-    _hidden(h, W, {"loss": loss, "lse": lse, "row_weight": row_weight})
-    _list(h, teacher_ids, teacher_logits)
-    _index(err_index)
-    hd, wd, td = _dtype(h), _dtype(W), _dtype(teacher_logits)
+    N, V, d = _sizes(h, W)
+    _list(teacher_ids, teacher_logits, N, err_index)
+    _row(loss, N, "loss")
+    _row(lse, N, "lse")
+    _row(row_weight, N, "row_weight")
     ghd, gwd = _gradients(h, W, grad_h, grad_W)
-    _here(h, W, teacher_ids, teacher_logits, loss, lse, row_weight, grad_h, grad_W, workspace, err_index)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pg_vocab_distill_grad(_at(h), hd, h.shape[0], _at(W), wd, W.shape[0], W.shape[1], _at(teacher_ids),
-                                      _at(teacher_logits), td, teacher_ids.shape[1], scale, temperature, _at(row_weight),
-                                      grad_scale, _at(loss), _at(lse), _at(grad_h), ghd, _at(grad_W), gwd,
-                                      1 if accumulate else 0, _at(workspace), ws_bytes, _at(err_index), _stream(stream)),
+    hd, wd, td, dev = _dtype(h), _dtype(W), _dtype(teacher_logits), _device()
+    _check(_lib.pg_vocab_distill_grad(_here(h, dev), hd, N, _here(W, dev), wd, V, d, _here(teacher_ids, dev), _here(teacher_logits, dev),
+                                      td, teacher_ids.shape[1], scale, temperature, _here(row_weight, dev), grad_scale, _here(loss, dev),
+                                      _here(lse, dev), _here(grad_h, dev), ghd, _here(grad_W, dev), gwd, 1 if accumulate else 0,
+                                      _here(workspace, dev), _bytes(workspace), _here(err_index, dev), _stream(stream)),
            "pg_vocab_distill_grad")
