@@ -48,7 +48,7 @@ constexpr int kMaxVocabWidth = 16384;    // d
 constexpr int64_t kMaxVocab = 1 << 24;
 constexpr int kMaxList = 256;            // teacher tokens a row
 constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (any number gives the same results)
-constexpr int64_t kKeepBytes = 2ll << 30;  // of U
+constexpr int64_t kKeepBytes = 2ll << 30;  // of U, f h and the pieces of h
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
 constexpr int64_t kPartBytes = 256 << 20;  // of dW's parts
 constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
@@ -1356,7 +1356,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   const float f = some ? s_f[mine] : 0.f, to = some ? s_to[mine] : 0.f;
   if (fix == 1 || fix == 2) {
     for (int64_t at = (part * 32 + lane) * 8; at < g.Vp; at += kLanes * 8) {
-      const float by = fix == 2 ? 0.f : exp2f(g.sums[(at >> g.seg_log) * g.Nc + row].x - to);
+      const float by = fix == 2 ? 0.f : exp2f(0.5f * (g.sums[(at >> g.seg_log) * g.Nc + row].x - to));  // (its square may underflow)
       float x[8] = {};
       for (int p = 0; p < g.np_u; ++p) {
         float y[8];
@@ -1365,7 +1365,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
         for (int e = 0; e < 8; ++e) x[e] += y[e];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fix == 2 || at + e >= g.V ? 0.f : x[e] * by;
+      for (int e = 0; e < 8; ++e) x[e] = fix == 2 || at + e >= g.V ? 0.f : x[e] * by * by;
       for (int p = 0; p < g.np_u; ++p)
         *reinterpret_cast<uint4*>(g.U + (static_cast<int64_t>(p) * g.Nc + row) * g.Vp + at) = take_pieces(x);
     }
@@ -1544,7 +1544,8 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->seg_log = g->seg == 128 ? 7 : g->seg == 64 ? 6 : 5;
   g->at_log = s.N <= kFewRows ? 7 : g->seg_log;
   const int64_t tiles = (s.V + g->wide - 1) / g->wide;
-  int64_t most = s.grad ? kKeepBytes / (g->np_u * g->Vp * 2) : kMaxForwardRows;
+  const int64_t row_bytes = 2 * (g->np_u * g->Vp + (has_w ? g->np_f * g->dp : 0) + (needs_copy(s.h_dtype, s.d) ? g->np_h * g->dp : 0));
+  int64_t most = s.grad ? kKeepBytes / row_bytes : kMaxForwardRows;
   most = std::min(most, kSumBytes / (16 * tiles));
   most = std::max<int64_t>(kTile, most / kTile * kTile);
   const int64_t chunks = (s.N + most - 1) / most;

@@ -92,8 +92,10 @@ def reference(h, W, target=None, ids=None, u=None, scale=1.0, T=1.0, z_loss=0.0,
         prob = torch.softmax(z, 1)
         dz = torch.where(keep[:, None], g[:, None] * (beta[:, None] * prob - q), 0.0)
         off = torch.where(keep[:, None], (g.abs() * E)[:, None] * (beta.abs()[:, None] * prob + q * (ids is not None)), 0.0)
+        # exponentials below 2^-126 of the row's reference, which is at most its sum, are zero, as are such pieces
+        off = torch.where(keep[:, None], off + 2.0 ** -125 * g.abs()[:, None], off)
         hk = torch.where(keep[:, None], h, 0.0)
-        r.update(dh=dz @ W, dW=dz.T @ hk, dz=dz, off=off, h=hk, W=W)
+        r.update(dh=dz @ W, dW=dz.T @ hk, dz=dz, off=off, h=hk, W=W, g=float(g.abs().max()))
     return r
 
 
@@ -122,6 +124,7 @@ def check_grads(r, dh, dW, old=None):
     if dh is not None:
         each = half_step(BF16) if dh.dtype == BF16 else 2.0 ** -22
         tol = (off + each * (dz.abs() + off)) @ W.abs() + (V + 16) * 2.0 ** -23 * (dz.abs() @ W.abs())
+        tol = tol + V * 2.0 ** -126 * max(1.0, r["g"])  # products below the normal range are zero
         tol = tol + half_step(dh.dtype) * (r["dh"].abs() + tol)
         close(dh, r["dh"], tol, "grad_h")
         # two roundings (bf16). What E leaves in p comes on
@@ -134,7 +137,8 @@ def check_grads(r, dh, dW, old=None):
         tol = (off + each * (dz.abs() + off)).T @ h.abs() + (N + 16) * 2.0 ** -23 * (dz.abs().T @ h.abs())
         want = r["dW"] if old is None else r["dW"] + old.double()
         chunk = 0.0 if old is None else half_step(F32) * old.double().abs()
-        tol = tol + chunk + half_step(dW.dtype) * (want.abs() + tol)
+        tol = tol + chunk + N * 2.0 ** -126
+        tol = tol + half_step(dW.dtype) * (want.abs() + tol) + 2.0 ** -126
         close(dW, want, tol, "grad_W")
         if old is None:  # three roundings
             assert not many or distance(dW, r["dW"]) <= (2.0 ** -8 if dW.dtype == BF16 else F32_TOL) * float(r["dW"].norm()) + float((off.T @ h.abs()).norm())
