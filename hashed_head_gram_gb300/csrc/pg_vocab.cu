@@ -45,8 +45,9 @@ namespace {
 
 constexpr int kErrVocab = 524288;        // device error bit: a wait of these products gave up
 constexpr int kMaxVocabWidth = 16384;    // d
-constexpr int64_t kMaxVocab = 1 << 24;
+constexpr int64_t kMaxVocab = (1 << 24) - 1;
 constexpr int kMaxList = 256;            // teacher tokens a row
+constexpr int kAtOnce = 1024;            // segments whose beginnings a block collects
 constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (any number gives the same results)
 constexpr int64_t kKeepBytes = 2ll << 30;  // of U, f h and the pieces of h
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
@@ -249,106 +250,134 @@ __device__ void target_rows(const VocabArgs& g, int block) {
   g.c[r] = valid ? as_reference(z[0]) : INFINITY;
 }
 
-// Distillation: one warp a row. The teacher's softmax; the list sorted by token, so that the tiles of the first product
-// find what is theirs (`at`, where each segment's tokens begin) and keep those logits; and the dot product of the
-// heaviest token, for a reference. (Dot products of all listed tokens took 101 of 1346 us at 8192 x 50,304 x 768 with
-// lists of 32.)
-template <int HT, int WT, bool VEC>
-__device__ void list_rows(const VocabArgs& g, int block) {
-  constexpr int kWarps = kPrepThreads / 32, kPer = kMaxList / 32;
-  __shared__ int32_t s_id[kWarps][kMaxList], s_sorted[kWarps][kMaxList];
-  __shared__ float s_w[kWarps][kMaxList];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = block * kWarps + warp;
-  if (r >= g.rows) return;
-  const int64_t i = g.row0 + r;
-  int32_t* ids = s_id[warp];
-  float u[kPer];
+// 32 R keys, key m * 32 + lane in x[m] of a lane, in ascending order (bitonic).
+template <int R>
+__device__ __forceinline__ void sort_keys(uint32_t (&x)[R]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 2; k <= 32 * R; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j; j /= 2)
+#pragma unroll
+      for (int m = 0; m < R; ++m) {
+        if (j >= 32) {
+          if (m & (j / 32)) continue;
+          const bool up = !(m * 32 & k);
+          const uint32_t a = x[m], b = x[m | j / 32];
+          x[m] = up ? min(a, b) : max(a, b);
+          x[m | j / 32] = up ? max(a, b) : min(a, b);
+        } else {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, x[m], j);
+          const bool up = !((m * 32 + lane) & k);
+          x[m] = up == !(lane & j) ? min(x[m], other) : max(x[m], other);
+        }
+      }
+}
+
+// Distillation: one warp a row, 8 rows a block. The teacher's softmax; the list sorted by token (R registers of a lane), so
+// that the tiles of the first product find what is theirs (`at`, where each segment's tokens begin) and keep those logits;
+// and the dot product of the heaviest token, for a reference. (Dot products of all listed tokens took 101 of 1346 us at
+// 8192 x 50,304 x 768 with lists of 32.) Bound by its instructions: 4096 lists of 64 LIST_TIME us.
+template <int HT, int WT, bool VEC, int R>
+__device__ void list_rows(const VocabArgs& g, int block, uint32_t (*s_key)[kMaxList], float (*s_w)[kMaxList], uint16_t (*s_at)[8]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = block * (kPrepThreads / 32) + warp;
+  const bool there = r < g.rows;
+  const int64_t i = g.row0 + (there ? r : 0);
+  constexpr uint32_t kNone = 0xFFFFFFFFu;  // (tokens are below 2^24 - 1)
+  float u[R];
+  uint32_t key[R];                         // token and place
   float top = -INFINITY;
   bool outside = false, poison = false;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int k = e * 32 + lane;
-    u[e] = -INFINITY;
-    if (k >= g.K) continue;
-    const int32_t id = __ldg(g.ids + i * g.K + k);
-    const bool in = id >= 0 && id < g.V;
-    outside |= !in;
-    if (in) {
+  for (int m = 0; m < R; ++m) {
+    const int k = m * 32 + lane;
+    u[m] = -INFINITY;
+    key[m] = kNone;
+    if (k >= g.K || !there) continue;
+    const int32_t token = __ldg(g.ids + i * g.K + k);
+    if (token >= 0 && token < g.V) {
+      key[m] = static_cast<uint32_t>(token) << 8 | static_cast<uint32_t>(k);
       float y[1];
       if (g.t_dtype == PG_F32) load_cols<PG_F32, 1>(g.tlogits, i * g.K + k, y);
       else load_cols<PG_BF16, 1>(g.tlogits, i * g.K + k, y);
-      u[e] = y[0] * g.inv_t;
-      poison |= !(u[e] < INFINITY);  // (also NaN, which fmaxf passes over)
-      top = fmaxf(top, u[e]);
+      u[m] = y[0] * g.inv_t;
+      poison |= !(u[m] < INFINITY);  // (also NaN, which fmaxf passes over)
+      top = fmaxf(top, u[m]);
+    } else {
+      outside = true;
     }
-    ids[k] = in ? id : INT_MAX;
   }
   top = warp_max(top);
   poison = __any_sync(0xffffffffu, poison);
   if (__any_sync(0xffffffffu, outside) && lane == 0 && g.err)
     atomicMin(reinterpret_cast<unsigned int*>(g.err), static_cast<unsigned int>(i));
   const bool some = poison || top > -INFINITY;
-  int heaviest = INT_MAX;
+  uint32_t heaviest = kNone;
   float total = 0.f;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int k = e * 32 + lane;
-    if (u[e] == top && k < g.K) heaviest = min(heaviest, k);
-    u[e] = !some ? -INFINITY : u[e] - (top > -INFINITY ? top : 0.f);
-    total += expf(u[e]);
+  for (int m = 0; m < R; ++m) {
+    if (u[m] == top) heaviest = min(heaviest, key[m]);
+    if (!some) key[m] = kNone;
+    u[m] = !some ? -INFINITY : u[m] - (top > -INFINITY ? top : 0.f);
+    total += expf(u[m]);
   }
   total = warp_sum(total);
   const float log_total = logf(total);
   float a = 0.f;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int k = e * 32 + lane;
-    const float logp = poison ? __int_as_float(0x7fffffff) : u[e] - log_total, w = !some ? 0.f : expf(logp);
-    if (k < g.K) {
-      s_w[warp][k] = w;
-      if (!some) ids[k] = INT_MAX;
-      if (ids[k] != INT_MAX && !(w == 0.f)) a += w * logp;
-    }
+  for (int m = 0; m < R; ++m) {
+    const float logp = poison ? __int_as_float(0x7fffffff) : u[m] - log_total, w = !some ? 0.f : expf(logp);
+    s_w[warp][m * 32 + lane] = w;
+    if (key[m] != kNone && !(w == 0.f)) a += w * logp;
   }
   a = warp_sum(a);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) heaviest = min(heaviest, __shfl_xor_sync(0xffffffffu, heaviest, o));
-  __syncwarp();
-  for (int k = lane; k < g.K; k += 32) {
-    const int32_t id = ids[k];
-    int rank = 0;
-    bool first = true;
-    float w = 0.f;  // what the gradient puts at the token: its later places count with its first
-    for (int e = 0; e < g.K; ++e) {
-      const bool same = ids[e] == id;
-      rank += ids[e] < id || (same && e < k);
-      first &= !(same && e < k);
-      if (same) w += s_w[warp][e];
-    }
-    s_sorted[warp][rank] = id;
-    g.sorted[static_cast<int64_t>(r) * g.K + rank] = id;
-    g.wk[static_cast<int64_t>(r) * g.K + rank] = id == INT_MAX || !first ? -1.f : w;
-  }
-  __syncwarp();
-  const int segs = static_cast<int>((g.V + (1 << g.at_log) - 1) >> g.at_log);
-  for (int q = lane; q <= segs; q += 32) {
-    const int from = q << g.at_log;
-    int lo = 0, hi = g.K;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_sorted[warp][mid] < from) lo = mid + 1;
-      else hi = mid;
-    }
-    g.at[static_cast<int64_t>(q) * g.Nc + r] = static_cast<uint16_t>(lo);
-  }
+  heaviest = __reduce_min_sync(0xffffffffu, heaviest);
   float z[1] = {0.f};
-  if (some) {
-    const int64_t j[1] = {heaviest < g.K && ids[heaviest] != INT_MAX ? ids[heaviest] : 0};
+  if (some && there) {
+    const int64_t j[1] = {heaviest == kNone ? 0 : heaviest >> 8};
     warp_dots<HT, WT, VEC, 1>(g, i, j, z);
   }
-  if (lane == 0) {
+  sort_keys<R>(key);
+#pragma unroll
+  for (int m = 0; m < R; ++m) s_key[warp][m * 32 + lane] = key[m];
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < R; ++m) {
+    const int k = m * 32 + lane;
+    if (k >= g.K || !there) continue;
+    const uint32_t token = key[m] >> 8;
+    float w = -1.f;  // what the gradient puts at the token: its later places count with its first
+    if (key[m] != kNone && (k == 0 || s_key[warp][k - 1] >> 8 != token)) {
+      w = s_w[warp][key[m] & 255];
+      for (int e = k + 1; e < g.K && s_key[warp][e] >> 8 == token; ++e) w += s_w[warp][s_key[warp][e] & 255];
+    }
+    const int64_t to = static_cast<int64_t>(r) * g.K + k;
+    g.sorted[to] = key[m] == kNone ? INT_MAX : static_cast<int32_t>(token);
+    g.wk[to] = w;
+  }
+  if (lane == 0 && there) {
     g.c[r] = some ? as_reference(poison ? __int_as_float(0x7fffffff) : z[0] * g.k2) : INFINITY;
     g.a[r] = some ? a : 0.f;
+  }
+  // where each segment's tokens begin: a lane walks a run of segments, the block stores its 8 rows' together
+  const int segs = static_cast<int>((g.V + (1 << g.at_log) - 1) >> g.at_log);
+  for (int q0 = 0; q0 <= segs; q0 += kAtOnce) {
+    const int n = min(kAtOnce, segs + 1 - q0), run = (n + 31) / 32;
+    int pos = 0;
+    const uint32_t start = min(static_cast<uint32_t>(q0 + lane * run) << g.at_log, kNone >> 8);
+#pragma unroll
+    for (int step = 16 * R; step; step >>= 1)
+      if ((s_key[warp][pos + step - 1] >> 8) < start) pos += step;
+    if (s_key[warp][pos] >> 8 < start) ++pos;  // (32 R - 1 of them at most so far)
+    for (int q = lane * run; q < min(n, (lane + 1) * run); ++q) {
+      const uint32_t from = min(static_cast<uint32_t>(q0 + q) << g.at_log, kNone >> 8);
+      while (pos < 32 * R && s_key[warp][pos] >> 8 < from) ++pos;
+      s_at[q][warp] = static_cast<uint16_t>(pos);
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < n; q += kPrepThreads)
+      *reinterpret_cast<uint4*>(g.at + static_cast<int64_t>(q0 + q) * g.Nc + block * 8) = *reinterpret_cast<const uint4*>(s_at[q]);
+    __syncthreads();
   }
 }
 
@@ -363,8 +392,15 @@ __global__ void __launch_bounds__(kPrepThreads) vocab_prepare_kernel(const __gri
   } else if ((block -= blocks_w) < blocks_h) {
     const uint8_t* h = static_cast<const uint8_t*>(g.h) + g.row0 * g.d * (HT == PG_F32 ? 4 : 2);
     split_rows<HT, VEC>(h, g.rows, g.d, g.dp, g.np_h, g.hp, block);
-  } else if (LIST) {
-    list_rows<HT, WT, VEC>(g, block - blocks_h);
+  } else if constexpr (LIST) {
+    __shared__ uint32_t s_key[LIST ? 8 : 1][kMaxList];
+    __shared__ float s_w[LIST ? 8 : 1][kMaxList];
+    __shared__ __align__(16) uint16_t s_at[LIST ? kAtOnce : 1][8];
+    block -= blocks_h;
+    if (g.K <= 32) list_rows<HT, WT, VEC, 1>(g, block, s_key, s_w, s_at);
+    else if (g.K <= 64) list_rows<HT, WT, VEC, 2>(g, block, s_key, s_w, s_at);
+    else if (g.K <= 128) list_rows<HT, WT, VEC, 4>(g, block, s_key, s_w, s_at);
+    else list_rows<HT, WT, VEC, 8>(g, block, s_key, s_w, s_at);
   } else {
     target_rows<HT, WT, VEC>(g, block - blocks_h);
   }

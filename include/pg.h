@@ -794,7 +794,7 @@ pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batch, int32_t 
  * cores do; fp32 operands and fp32 gradients take every value as a sum of three bf16 pieces (24 bits), with three
  * products of bf16 in place of one where the other operand is bf16, six where it is not. Equal inputs give
  * equal bits.
- * 0 <= N < 2^31, 1 <= V <= 2^24, 1 <= d <= 16384, 1 <= K <= 256 (else PG_ERR_SHAPE); scale, z_loss, grad_scale finite,
+ * 0 <= N < 2^31, 1 <= V < 2^24, 1 <= d <= 16384, 1 <= K <= 256 (else PG_ERR_SHAPE); scale, z_loss, grad_scale finite,
  * temperature > 0 and neither it nor scale / temperature out of fp32's range (else PG_ERR_UNSUPPORTED). N == 0 enqueues
  * nothing, but for zeros in grad_w without accumulate. A device wait that runs out (about a second) sets device
  * error bit 524288; the outputs are then undefined.

@@ -6,8 +6,8 @@ Tolerances. A logit is an fp32 sum of d products: within (d + 16) 2^-23 of the s
 products of pieces are left out, 2^-23 together: the 16). exp takes a relative error of 2^-22, of its argument's rounding
 (2^-23 of the logits' size, twice) and a sum of the V terms 300 roundings at most (128 in a tile, then tiles spread over
 16 warps). So lse and log p have E = 2 (d + 16) 2^-23 mag + 2^-22 (2 max|z| + 80). A gradient takes dz with p off by
-E relative, a rounding of each operand it is made of (bf16: U, and f h for grad_W, 2^-8 each; pieces: 2^-22 in all),
-fp32 sums ((terms + 16) 2^-23) and its own rounding.
+E relative, a rounding of each operand it is made of (bf16: U, f h for grad_W and an fp32 W for grad_h, 2^-8 each; pieces:
+2^-22 in all), fp32 sums ((terms + 16) 2^-23) and its own rounding.
 """
 import math
 
@@ -58,6 +58,7 @@ def make(seed, N, V, d, hdt, wdt, dev, spread=1.0, K=0, pad=0.1):
 
 def reference(h, W, target=None, ids=None, u=None, scale=1.0, T=1.0, z_loss=0.0, weight=None, grad_scale=1.0, grads=True):
     """loss, lse, dh, dW in 64 bits, and dz and the error that E leaves in it."""
+    w32 = W.dtype == F32
     h, W = h.double(), W.double()
     s = scale / T
     z = s * (h @ W.T)
@@ -83,7 +84,7 @@ def reference(h, W, target=None, ids=None, u=None, scale=1.0, T=1.0, z_loss=0.0,
     E = 2 * (h.shape[1] + 16) * 2.0 ** -23 * mag + 2.0 ** -22 * (2 * z.abs().amax(1) + 80)
     if ids is not None:  # the teacher's own softmax in fp32
         E = E + 2.0 ** -22 * (4 + torch.where(u > -math.inf, u.abs(), 0.0).amax(1))
-    r = dict(loss=loss, lse=lse_out, E=E, keep=keep)
+    r = dict(loss=loss, lse=lse_out, E=E, keep=keep, w32=w32)
     if grads:
         g = grad_scale * s * keep.double()
         if weight is not None:
@@ -122,12 +123,12 @@ def check_grads(r, dh, dW, old=None):
     # mean, about every other time, so the norms are looked at where a few thousand entries take part
     many = N * V >= 4096 and min(N, V) >= 32
     if dh is not None:
-        each = half_step(BF16) if dh.dtype == BF16 else 2.0 ** -22
+        each = (1 + r["w32"]) * half_step(BF16) if dh.dtype == BF16 else 2.0 ** -22
         tol = (off + each * (dz.abs() + off)) @ W.abs() + (V + 16) * 2.0 ** -23 * (dz.abs() @ W.abs())
         tol = tol + V * 2.0 ** -126 * max(1.0, r["g"])  # products below the normal range are zero
         tol = tol + half_step(dh.dtype) * (r["dh"].abs() + tol)
         close(dh, r["dh"], tol, "grad_h")
-        # two roundings (bf16). What E leaves in p comes on
+        # two roundings (bf16; of an fp32 W a third). What E leaves in p comes on
         # top: dz = g (beta p - 1) at a target with p near 1 is the difference of two numbers near g, so an
         # error of E in p is E / |beta p - 1| of dz (a vocabulary of one token: p = 1, beta - 1 = 2 z_loss lse)
         assert not many or distance(dh, r["dh"]) <= (2.0 ** -8 if dh.dtype == BF16 else F32_TOL) * float(r["dh"].norm()) + float((off @ W.abs()).norm())

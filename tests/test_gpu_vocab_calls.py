@@ -145,7 +145,7 @@ def test_nan_and_infinite_teacher_logits_stay_in_their_row(cuda):
 def test_a_list_of_one_is_cross_entropy(cuda):
     h, W, t = make(17, 333, 1000, 96, BF16, BF16, cuda)
     a = run_ce(h, W, t, BF16, BF16, scale=0.9)
-    b = run_distill(h, W, t[:, None].contiguous(), torch.randn(333, 1, device=cuda), BF16, BF16, scale=0.9)
+    b = run_distill(h, W, t[:, None].contiguous(), torch.linspace(-3, 3, 333, device=cuda)[:, None].contiguous(), BF16, BF16, scale=0.9)
     for x, y in zip(a, b):
         close = (x.double() - y.double()).abs()
         assert (close <= 2.0 ** -7 * (x.double().abs() + 1e-3 * x.double().abs().max())).all()
@@ -155,7 +155,7 @@ def test_a_list_of_one_is_cross_entropy(cuda):
 def test_gradients_are_differences(cuda, op):
     N, V, d = 6, 50, 12
     h, W, t, ids, u = make(3, N, V, d, F32, F32, cuda, K=5, pad=0.2)
-    weight = torch.rand(N, device=cuda) + 0.5
+    weight = torch.linspace(0.5, 1.5, N, device=cuda)
 
     def total(hh, WW):
         if op == "ce":
@@ -187,7 +187,7 @@ def test_gradients_are_differences(cuda, op):
 def test_odd_addresses(cuda, N, V, d, ghd, gwd, shift):
     h, W, t = make(N + d, N, V, d, F32, F32, cuda)
     h, W, t = offset_view(h, shift), offset_view(W, shift), offset_view(t, shift)
-    weight = offset_view(torch.rand(N, device=cuda), shift)
+    weight = offset_view(torch.rand(N, generator=torch.Generator().manual_seed(d)).to(cuda), shift)
     r = reference(h, W, t, weight=weight)
     loss, lse, dh, dW = run_ce(h, W, t, ghd, gwd, shift=shift, weight=weight)
     check_values(r, loss, lse)
@@ -235,7 +235,7 @@ def test_no_rows(cuda):
 @pytest.mark.parametrize("N", NS)
 def test_accumulate(cuda, N, gwd):
     h, W, t = make(N, N, 700, 80, BF16, BF16, cuda)
-    old = torch.randn(700, 80, device=cuda).to(gwd)
+    old = torch.randn(700, 80, generator=torch.Generator().manual_seed(N)).to(gwd).to(cuda)
     r = reference(h, W, t)
     gw = old.clone()
     _, _, _, dW = run_ce(h, W, t, None, gwd, accumulate=gw)

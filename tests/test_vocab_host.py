@@ -45,7 +45,7 @@ def distill_grad(L, h=P, hdt=1, N=4, W=P, wdt=1, V=10, d=8, ids=P, u=P, udt=0, K
 
 
 COMMON = [
-    (dict(N=-1), SHAPE), (dict(N=1 << 31), SHAPE), (dict(V=0), SHAPE), (dict(V=(1 << 24) + 1), SHAPE), (dict(d=0), SHAPE),
+    (dict(N=-1), SHAPE), (dict(N=1 << 31), SHAPE), (dict(V=0), SHAPE), (dict(V=1 << 24), SHAPE), (dict(d=0), SHAPE),
     (dict(d=16385), SHAPE), (dict(hdt=2), DTYPE), (dict(wdt=-1), DTYPE), (dict(h=None), NULL), (dict(W=None), NULL),
     (dict(h=EIGHT), ALIGN), (dict(W=EIGHT), ALIGN),                       # read in place: 16 bytes
     (dict(h=TWO, d=7), DEVICE), (dict(W=TWO, d=7), DEVICE),               # copied first: an element's
@@ -93,7 +93,7 @@ def test_workspace_queries(pg):
     assert pg.vocab_ce_workspace_size(64, 50304, 768, 1, 0) >= 6 * 50304 * 768
     assert pg.vocab_distill_workspace_size(4096, 50304, 768, 64, 1, 1) >= 12 * 4096 * 64
     # sizes at both ends
-    for N, V, d in [(1, 1, 1), (1, 1 << 24, 1), (1, 1, 16384), ((1 << 31) - 1, 1, 1), ((1 << 31) - 1, 1 << 24, 16384)]:
+    for N, V, d in [(1, 1, 1), (1, (1 << 24) - 1, 1), (1, 1, 16384), ((1 << 31) - 1, 1, 1), ((1 << 31) - 1, (1 << 24) - 1, 16384)]:
         for dt in (0, 1):
             assert pg.vocab_ce_workspace_size(N, V, d, dt, dt) > 0
             assert pg.vocab_ce_grad_workspace_size(N, V, d, dt, dt, dt, dt) > 0
