@@ -90,6 +90,8 @@ __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.w
 
 struct VocabMaps {
   CUtensorMap h, W, U, Ust, F;           // U for loads and (boxes of 32 rows and columns) for stores; F: f h
+  CUtensorMap Ufew;                      // U in boxes of as many rows as `few` has columns
+  CUtensorMap Gh, Gw;                    // the gradients, for stores
 };
 
 struct VocabArgs {
@@ -124,6 +126,8 @@ struct VocabArgs {
   int passes_h, passes_w;                // piece products of dh, dW
   int group, group_h, group_w;           // k-blocks that one sum in TMEM takes: logits, dh, dW
   int wide, seg, seg_log;                // columns of a logits tile, and of a segment of it (its half), and that's log2
+  int tma_h, tma_w;                      // tiles of dh, dW go out by TMA
+  int few_h;                             // dh is made for few rows
   int at_log;                            // log2 of the tokens that a place of `at` stands for
   int segs;                              // sums a row
 };
@@ -697,8 +701,8 @@ __device__ __forceinline__ void table_target(const VocabArgs& g, void** dst, int
 
 // A gradient's tile. TMEM gives a lane one row; global memory wants neighbouring lanes on one row, so 32 columns
 // at a time pass through the warp's shared memory.
-__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob& w, uint8_t* s_row, uint32_t from, int row0,
-                                              int half) {
+__device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
+                                              uint32_t from, int row0, int half) {
   const int lane = threadIdx.x & 31;
   const bool dh = w.product == 1, part = dh ? g.parts != nullptr : g.parts_w != nullptr;
   const int64_t rows = dh ? g.rows : g.V;
@@ -721,6 +725,43 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabJob
                    (!add32 || reinterpret_cast<uintptr_t>(add32) % 16 == 0);
   uint32_t r2[2][32];
   tmem_load(from, r2[0]);
+  if (dh ? g.tma_h : g.tma_w) {  // rows past the last and columns past d are cut off
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // of an earlier tile
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      const int c0 = static_cast<int>(w.col0) + half * (kTile / 2) + ch * 32;
+      if (c0 >= g.d) break;
+      uint32_t(&r)[32] = r2[ch & 1];
+      tmem_wait(r);
+      if (ch < 3) tmem_load(from + (ch + 1) * 32, r2[(ch + 1) & 1]);
+      float x[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = f == 0.f ? 0.f : f * __uint_as_float(r[k]);
+      uint8_t* buf = s_row;
+      if (dtype == PG_F32) {  // one buffer of 32 rows of 128 bytes
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4*>(buf + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+      } else {                // two of 64, in turn
+        buf += (ch & 1) * (kStageBytes / 2);
+        if (lane == 0) stores_read();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)) =
+              make_uint4(two_bf16(x[8 * k], x[8 * k + 1]), two_bf16(x[8 * k + 2], x[8 * k + 3]), two_bf16(x[8 * k + 4], x[8 * k + 5]),
+                         two_bf16(x[8 * k + 6], x[8 * k + 7]));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) store_box(dh ? &maps.Gh : &maps.Gw, smem_addr(buf), c0, row0, 0);
+    }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    return;
+  }
 #pragma unroll
   for (int ch = 0; ch < 4; ++ch) {
     const int c0 = static_cast<int>(w.col0) + half * (kTile / 2) + ch * 32;
@@ -969,13 +1010,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
-      if constexpr (KIND == kGrads) grad_epilogue(g, w, s_row, from, row0, half);
+      if constexpr (KIND == kGrads) grad_epilogue(g, maps, w, s_row, from, row0, half);
       else logits_epilogue<KIND == kKeep>(g, maps, w, s_row, from, row0, half, c, listed);
       release();
       w = next;
       if (KIND != kGrads && more && g.ids) first_listed(g, row_of(w) + lane, &next_listed);
     }
-    if (KIND == kKeep && lane == 0) stores_done();
+    if (KIND != kSums && lane == 0) stores_done();
   }
   if (!fine) {
     atomicOr(g.err_word, kErrVocab);
@@ -1301,6 +1342,178 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
   if (warp == 1) tmem_free<false>(tmem, 2 * NT);
 }
 
+// dh's parts for few rows, where reading W is all that counts again: the columns of W are the tile's rows (128 a CTA), the
+// rows of U its columns, and the products run along a part of V; the parts are joined as the others are.
+template <int NT>
+__global__ void __launch_bounds__(Few<NT>::kThreads, 1)
+    vocab_few_grad_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabArgs g) {
+  using T = Few<NT>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ FewBars<NT> bars_s;
+  FewBars<NT>* bars = &bars_s;
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      bar_init(smem_addr(&bars->full[s]), 1);
+      bar_init(smem_addr(&bars->empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(smem_addr(&bars->acc_full[s]), 1);
+      bar_init(smem_addr(&bars->acc_empty[s]), 4);
+    }
+    bar_init(smem_addr(&bars->done), 1);
+    bars->abort = 0;
+    bar_init_fence();
+    fence_async_smem();
+  }
+  if (warp == 1) tmem_alloc<false>(smem_addr(&bars->tmem), 2 * NT);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars->tmem;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  const int tiles = (g.d + 127) / 128, all = static_cast<int>((g.V + kBK - 1) / kBK), units = tiles * g.q;
+  const int np_u = g.gh_dtype == PG_F32 ? g.np_u : 1, np_w = g.gh_dtype == PG_F32 ? g.np_w : 1;
+  auto first_block = [&](int part) { return static_cast<int>(static_cast<int64_t>(all) * part / g.q); };
+  int stage = 0, acc = 0;
+  uint32_t ring_phase = 0, acc_phase = 0;
+  bool fine = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int u = blockIdx.x; fine && u < units; u += gridDim.x) {
+        const int part = u / tiles, col0 = (u - part * tiles) * 128, kb1 = first_block(part + 1);
+        for (int k0 = first_block(part); fine && k0 < kb1;) {
+          const int k1 = kb1 - k0 > g.group_h ? k0 + g.group_h : kb1;
+          for (int pass = 0; fine && pass < g.passes_h; ++pass) {
+            int zw = 0, zu = 0;
+            if (g.passes_h > 1) piece_of(np_w, np_u, pass, &zw, &zu);
+            for (int kb = k0; kb < k1; ++kb) {
+              if (!wait<false>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u, abort)) {
+                fine = false;
+                break;
+              }
+              const uint32_t full = smem_addr(&bars->full[stage]), dw = smem_addr(ring + stage * (T::kWBytes + T::kHBytes));
+              bar_expect(full, T::kWBytes + T::kHBytes);
+              load_operand<false, 128>(dw, &maps.W, &maps.W, true, col0, kb * kBK, zw, full);
+              load_operand<false, NT>(dw + T::kWBytes, &maps.Ufew, &maps.Ufew, false, 0, kb * kBK, zu, full);
+              if (++stage == S) {
+                stage = 0;
+                ring_phase ^= 1u;
+              }
+            }
+          }
+          k0 = k1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int u = blockIdx.x; fine && u < units; u += gridDim.x) {
+        const int part = u / tiles, kb1 = first_block(part + 1);
+        for (int k0 = first_block(part); fine && k0 < kb1;) {
+          const int k1 = kb1 - k0 > g.group_h ? k0 + g.group_h : kb1;
+          if (!wait<false>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
+            fine = false;
+            break;
+          }
+          fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * NT);
+          for (int kb = 0, at = k0; kb < (k1 - k0) * g.passes_h; ++kb) {
+            if (!wait<false>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
+              fine = false;
+              break;
+            }
+            fence_after();
+            const uint32_t sw = smem_addr(ring + stage * (T::kWBytes + T::kHBytes));
+            const uint64_t dw = operand_desc(sw, true), du = operand_desc(sw + T::kWBytes, false);
+            const int64_t left = g.V - static_cast<int64_t>(at) * kBK;
+            if (++at == k1) at = k0;
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)
+              if (k * 16 < left)
+                mma_f16<false>(d, dw + k * (2048 >> 4), du + (k / 4) * (T::kHBytes / 2 >> 4) + (k % 4) * 2, T::kIdesc | 1u << 15,
+                               (kb | k) != 0);
+            commit<false>(smem_addr(&bars->empty[stage]));
+            if (++stage == S) {
+              stage = 0;
+              ring_phase ^= 1u;
+            }
+          }
+          if (!fine) break;
+          commit<false>(smem_addr(&bars->acc_full[acc]));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+          k0 = k1;
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    for (int u = blockIdx.x; fine && u < units; u += gridDim.x) {
+      const int part = u / tiles, col = (u - part * tiles) * 128 + quarter * 32 + lane, kb1 = first_block(part + 1);
+      float z[NT];
+#pragma unroll
+      for (int k = 0; k < NT; ++k) z[k] = 0.f;
+      for (int k0 = first_block(part); k0 < kb1; k0 = kb1 - k0 > g.group_h ? k0 + g.group_h : kb1) {
+        if (!__all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
+          fine = false;
+          break;
+        }
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < NT; c += 32) {
+          uint32_t r[32];
+          tmem_load(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * NT + c), r);
+          tmem_wait(r);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) z[c + k] += __uint_as_float(r[k]);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&bars->acc_empty[acc]));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!fine) break;
+      float* to = g.parts + static_cast<int64_t>(part) * g.Nc * g.d + col;
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+        if (k < g.rows && col < g.d) to[static_cast<int64_t>(k) * g.d] = z[k];
+    }
+  }
+  if (!fine) {
+    atomicOr(g.err_word, kErrVocab);
+    *abort = 1;
+  }
+  __syncwarp();
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      const uint64_t t0 = now_ns();
+      while (!poll<false>(smem_addr(&bars->empty[stage]), ring_phase ^ 1u) && now_ns() - t0 < kAsyncWaitNs / 8) {
+      }
+      if (++stage == S) {
+        stage = 0;
+        ring_phase ^= 1u;
+      }
+    }
+  }
+  if (warp == 1 && lane == 0) {
+    commit_here<false>(smem_addr(&bars->done));
+    const uint64_t t0 = now_ns();
+    while (!poll<false>(smem_addr(&bars->done), 0) && now_ns() - t0 < kAsyncWaitNs) {
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_free<false>(tmem, 2 * NT);
+}
+
 // ------------------------------------------------------------------- rows, once their sums are there
 
 constexpr int kRowWarps = 16, kRowsPer = 8;
@@ -1522,6 +1735,20 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   g->passes_w = g->gw_dtype == PG_F32 ? passes_of(g->np_u, g->np_f) : 1;
   g->group_h = g->gh_dtype == PG_F32 ? kGroupPieces : 1 << 30;  // (a bf16 gradient's own rounding is far above)
   g->group_w = g->gw_dtype == PG_F32 ? kGroupPieces : 1 << 30;
+  if (has_h && g->N <= kFewRows) {
+    // few rows: dh by itself, in as many parts as fill the SMs once or twice
+    const int tiles = (g->d + 127) / 128;
+    double best = -1;
+    for (int waves = 1; waves <= 3; ++waves) {
+      const int q = static_cast<int>(std::min<int64_t>(std::max(1, 2 * units * waves / tiles), kv));
+      const double full = static_cast<double>(q) * tiles / (2 * units * ((q * tiles + 2 * units - 1) / (2 * units)));
+      if (full <= best + 0.04) continue;
+      best = full;
+      g->few_h = q;
+    }
+    g->tiles2 = 0;
+    has_h = false;
+  }
   double best = -1;
   int best_q = 1, best_qw = 1;
   for (int q = 1; q <= (has_h ? 16 : 1) && (q == 1 || kv >= 2 * q); ++q)
@@ -1541,7 +1768,7 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
       best_q = q;
       best_qw = qw;
     }
-  g->q = best_q;
+  g->q = g->few_h ? g->few_h : best_q;
   g->q_w = best_qw;
 }
 
@@ -1607,22 +1834,23 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
       if (chunks > 1 && s.gw_dtype == PG_BF16) g->acc = reinterpret_cast<float*>(take(4ll * s.V * s.d));
     }
     plan_schedule(g, kPlanUnits, has_h, has_w);
-    if (has_h && g->q > 1) g->parts = reinterpret_cast<float*>(take(4ll * g->q * Nc * s.d));
+    if (has_h && (g->q > 1 || g->few_h)) g->parts = reinterpret_cast<float*>(take(4ll * g->q * Nc * s.d));
     if (has_w && g->q_w > 1) g->parts_w = reinterpret_cast<float*>(take(4ll * g->q_w * s.V * s.d));
   }
   return at + 128;
 }
 
-// [pieces, rows, cols] bf16 with row stride ld, in boxes of box_cols columns (as wide as the swizzle) and box_rows rows.
+// [pieces, rows, cols] bf16 (or fp32) with row stride ld, in boxes of box_cols columns (as wide as the swizzle) and box_rows rows.
 bool vocab_map(CUtensorMap* map, const void* ptr, int pieces, int64_t rows, int64_t cols, int64_t ld, int64_t piece_rows,
-               int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+               int box_cols, int box_rows, CUtensorMapSwizzle swizzle, bool f32 = false) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(pieces)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(piece_rows) * ld * 2};
+  const cuuint64_t size = f32 ? 4 : 2;
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size, static_cast<cuuint64_t>(piece_rows) * ld * size};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+  return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1728,6 +1956,22 @@ pg_status launch_few(const VocabMaps& maps, const VocabArgs& g, bool keep, cudaS
                      stream, maps, g);
 }
 
+template <int NT>
+pg_status launch_few_grad(const VocabMaps& maps, const VocabArgs& g, cudaStream_t stream) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return PG_ERR_DEVICE;
+  if (!known[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(vocab_few_grad_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Few<NT>::kSmem));
+    if (e != cudaSuccess) return cuda_fail(e);
+    known[dev].store(1, std::memory_order_relaxed);
+  }
+  const int64_t blocks = std::min<int64_t>(sm_count(), static_cast<int64_t>((g.d + 127) / 128) * g.q);
+  return launch_next(vocab_few_grad_kernel<NT>, blocks, Few<NT>::kThreads, Few<NT>::kSmem, false, true, stream, maps, g);
+}
+
 using PrepareFn = void (*)(const VocabArgs, int, int);
 using ArgsFn = void (*)(const VocabArgs);
 
@@ -1777,8 +2021,21 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
           (g.F && !vocab_map(&maps.F, g.F, g.np_f, g.rows, s.d, g.dp, g.Nc, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)))
         return PG_ERR_CUDA;
       if (!g.F) maps.F = maps.U;
+      maps.Ufew = maps.Gh = maps.Gw = maps.U;
+      if (g.few_h && !vocab_map(&maps.Ufew, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, kLine, few, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
+      // tiles that nothing is added to, of matrices that TMA can step over
+      auto out_map = [&](CUtensorMap* map, void* dst, int dtype, int64_t rows) {
+        const bool f32 = dtype == PG_F32;
+        if (s.d % (f32 ? 4 : 8) || !aligned(dst, 16)) return 0;
+        return vocab_map(map, dst, 1, rows, s.d, s.d, rows, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, f32) ? 1 : -1;
+      };
+      const bool through = g.acc && !g.last;
+      g.tma_w = g.F && !g.parts_w && g.first && !g.accumulate ? out_map(&maps.Gw, through ? static_cast<void*>(g.acc) : g.gw, through ? PG_F32 : s.gw_dtype, s.V) : 0;
+      g.tma_h = s.gh_dtype >= 0 && !g.parts
+                    ? out_map(&maps.Gh, static_cast<uint8_t*>(g.gh) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.gh_dtype)), s.gh_dtype, g.rows) : 0;
+      if (g.tma_w < 0 || g.tma_h < 0) return PG_ERR_CUDA;
     } else {
-      maps.U = maps.Ust = maps.F = maps.h;
+      maps.U = maps.Ust = maps.F = maps.Ufew = maps.Gh = maps.Gw = maps.h;
     }
     if (few)
       st = few == 32 ? launch_few<32>(maps, g, s.grad, stream) : few == 64 ? launch_few<64>(maps, g, s.grad, stream)
@@ -1794,10 +2051,14 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     VocabArgs b = g;
     if (g.tiles2) b.tiles2 = (g.rows + kTile - 1) / kTile * g.nd;  // a last chunk has fewer rows
     b.q_w = std::min(g.q_w, (g.rows + kBK - 1) / kBK);             // (no part without a k-block)
+    if (g.few_h) {
+      st = few == 32 ? launch_few_grad<32>(maps, g, stream) : few == 64 ? launch_few_grad<64>(maps, g, stream) : launch_few_grad<128>(maps, g, stream);
+      if (st != PG_OK) return st;
+    }
     const int64_t units = s.grad ? static_cast<int64_t>(b.tiles2) * b.q + static_cast<int64_t>(b.tiles3) * b.q_w : 0;
-    if (units == 0) continue;
+    if (!s.grad) continue;
     const bool pieces = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32;
-    if ((st = pieces ? launch_product<kGrads, true>(maps, b, units, stream) : launch_product<kGrads, false>(maps, b, units, stream)) != PG_OK)
+    if (units && (st = pieces ? launch_product<kGrads, true>(maps, b, units, stream) : launch_product<kGrads, false>(maps, b, units, stream)) != PG_OK)
       return st;
     if (g.parts || g.parts_w) {
       const bool four = s.d % 4 == 0 && (!g.parts || aligned(g.gh, 4 * dtype_bytes(s.gh_dtype))) &&
