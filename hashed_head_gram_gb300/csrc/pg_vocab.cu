@@ -631,18 +631,39 @@ __device__ __forceinline__ void first_listed(const VocabArgs& g, int row, Listed
   if (l->e < l->end) l->token = g.sorted[static_cast<int64_t>(row) * g.K + l->e];
 }
 
+// The listed tokens' logits of a warp's rows and segment. TMEM gives all lanes one column at a time, so a few of them are
+// loaded one by one; from kDense on the columns pass through shared memory, where a lane reads its own.
+constexpr int kDense = 48;
+
 template <bool KEEP>
-__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
-                                                uint32_t from, int row0, int half, float c, Listed listed) {
+__device__ __noinline__ void keep_listed(const VocabArgs& g, uint8_t* s_row, uint32_t from, int row0, int64_t col0, Listed listed) {
   const int lane = threadIdx.x & 31;
-  const int64_t col0 = w.col0 + half * g.seg;
-  if (row0 >= g.rows || col0 >= g.V) return;
-  while (__any_sync(0xffffffffu, listed.e < listed.end)) {  // listed tokens' logits, one a row at a time
+  const int64_t row = static_cast<int64_t>(row0 + lane) * g.K;
+  if (__reduce_add_sync(0xffffffffu, listed.end - listed.e) >= kDense) {
+    if (KEEP && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (of U's tile before)
+    __syncwarp();
+#pragma unroll 1
+    for (int c0 = 0; c0 < g.seg && col0 + c0 < g.V; c0 += 32) {
+      uint32_t r[32];
+      tmem_load(from + c0, r);
+      tmem_wait(r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4*>(s_row + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+      for (; listed.e < listed.end; ++listed.e) {
+        const int at = static_cast<int>(g.sorted[row + listed.e] - col0) - c0;  // ascending
+        if (at >= 32) break;
+        g.zk[row + listed.e] = *reinterpret_cast<const float*>(s_row + lane * 128 + ((at >> 2 ^ (lane & 7)) << 4) + (at & 3) * 4) * g.k2;
+      }
+    }
+    __syncwarp();
+    return;
+  }
+  while (__any_sync(0xffffffffu, listed.e < listed.end)) {  // one a row at a time
     const bool mine = listed.e < listed.end;
     const int at = mine ? static_cast<int>(listed.token - col0) : -1;
     float y = 0.f;
-    // TMEM gives all lanes one column: the lanes' columns one after the other, four in flight
-    for (uint32_t left = __ballot_sync(0xffffffffu, mine); left;) {
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine); left;) {  // four in flight
       uint32_t v[4];
       int l[4];
 #pragma unroll
@@ -658,11 +679,19 @@ __device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabM
         if (lane == l[k]) y = __uint_as_float(v[k]);
     }
     if (mine) {
-      const int64_t row = static_cast<int64_t>(row0 + lane) * g.K;
       g.zk[row + listed.e] = y * g.k2;
       if (++listed.e < listed.end) listed.token = g.sorted[row + listed.e];
     }
   }
+}
+
+template <bool KEEP>
+__device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
+                                                uint32_t from, int row0, int half, float c, Listed listed) {
+  const int lane = threadIdx.x & 31;
+  const int64_t col0 = w.col0 + half * g.seg;
+  if (row0 >= g.rows || col0 >= g.V) return;
+  if (g.ids) keep_listed<KEEP>(g, s_row, from, row0, col0, listed);
   const bool dead = row0 + lane >= g.rows || c == INFINITY;
   float sum = logits_half<KEEP>(g, maps, from, s_row, row0, col0, c, dead);
   float ref = c;
@@ -1104,7 +1133,8 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
   __shared__ FewBars<NT> bars_s;
   __shared__ float s_c[NT];
   __shared__ float2 s_all[4][KEEP ? 1 : NT];
-  __shared__ __align__(16) uint16_t s_u[KEEP ? 4 : 1][KEEP ? 32 : 1][40];  // (rows of 80 bytes)
+  __shared__ __align__(16) float s_z[4][32][33];  // a warp's logits, or its part of U in rows of 80 bytes
+  auto s_u = [&](int w) { return reinterpret_cast<uint16_t(*)[40]>(&s_z[w][0][0]); };
   FewBars<NT>* bars = &bars_s;
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1257,13 +1287,17 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
           end = g.at[(t + 1ll) * g.Nc + row];
         }
         tmem_wait(r);
-        for (uint32_t left = __ballot_sync(0xffffffffu, e < end); left; left &= left - 1) {
-          const int l = __ffs(left) - 1, e1 = __shfl_sync(0xffffffffu, e, l), end1 = __shfl_sync(0xffffffffu, end, l);
-          float y = 0.f;
+        if (__any_sync(0xffffffffu, e < end)) {  // each lane looks its row's tokens up in what the others have
+          float(*z)[33] = s_z[warp - 2];
+          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) y = k == l ? __uint_as_float(r[k]) : y;
-          for (int j = e1; j < end1; ++j)
-            if (g.sorted[static_cast<int64_t>(c0 + l) * g.K + j] == v) g.zk[static_cast<int64_t>(c0 + l) * g.K + j] = y * g.k2;
+          for (int k = 0; k < 32; ++k) z[k][lane] = __uint_as_float(r[k]);
+          __syncwarp();
+          for (const int64_t row_at = static_cast<int64_t>(row) * g.K; e < end; ++e) {
+            const int64_t from_v0 = g.sorted[row_at + e] - v0;
+            if (from_v0 >= 0 && from_v0 < 32) g.zk[row_at + e] = z[lane][from_v0] * g.k2;
+          }
+          __syncwarp();
         }
         float ref = c, sum;
 #pragma unroll 1
@@ -1284,14 +1318,14 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
                 for (int k = 0; k < 32; ++k) take_piece(y[k]);
               __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) s_u[warp - 2][k][lane] = s_c[c0 + k] == INFINITY ? 0 : take_piece(y[k]);
+              for (int k = 0; k < 32; ++k) s_u(warp - 2)[k][lane] = s_c[c0 + k] == INFINITY ? 0 : take_piece(y[k]);
               __syncwarp();
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int to = k * 8 + lane / 4;
                 if (c0 + to < g.rows)
                   *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(g.U) + (static_cast<int64_t>(p) * g.Nc + c0 + to) * g.Vp + v0 +
-                                            lane % 4 * 8) = *reinterpret_cast<const uint4*>(&s_u[warp - 2][to][lane % 4 * 8]);
+                                            lane % 4 * 8) = *reinterpret_cast<const uint4*>(&s_u(warp - 2)[to][lane % 4 * 8]);
               }
             }
           }
@@ -1735,8 +1769,8 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   g->passes_w = g->gw_dtype == PG_F32 ? passes_of(g->np_u, g->np_f) : 1;
   g->group_h = g->gh_dtype == PG_F32 ? kGroupPieces : 1 << 30;  // (a bf16 gradient's own rounding is far above)
   g->group_w = g->gw_dtype == PG_F32 ? kGroupPieces : 1 << 30;
-  if (has_h && g->N <= kFewRows) {
-    // few rows: dh by itself, in as many parts as fill the SMs once or twice
+  if (has_h && g->N <= kFewRows && kv > 8) {
+    // few rows: dh by itself, in as many parts as fill the SMs once or twice (a table of a few k-blocks: with dW)
     const int tiles = (g->d + 127) / 128;
     double best = -1;
     for (int waves = 1; waves <= 3; ++waves) {

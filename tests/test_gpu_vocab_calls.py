@@ -128,6 +128,19 @@ def test_lists_of_every_kind(cuda, N):
     assert err.item() == -1
 
 
+@pytest.mark.parametrize("N,V,K", [(5, 64, 200), (100, 300, 120), (300, 64, 256), (600, 200, 100), (300, 3000, 256)])
+@pytest.mark.parametrize("d", [40, 1500])
+def test_dense_lists(cuda, N, V, K, d):
+    # most tokens of a tile are listed, many of them more than once
+    h, W, _, ids, u = make(N + V + K, N, V, d, BF16, BF16, cuda, K=K)
+    r = reference(h, W, ids=ids, u=u, T=2.0)
+    loss, lse, _, _ = run_distill(h, W, ids, u, temperature=2.0)
+    check_values(r, loss, lse)
+    loss, lse, dh, dW = run_distill(h, W, ids, u, BF16, F32, temperature=2.0)
+    check_values(r, loss, lse)
+    check_grads(r, dh, dW)
+
+
 def test_nan_and_infinite_teacher_logits_stay_in_their_row(cuda):
     h, W, _, ids, u = make(31, 300, 700, 80, BF16, BF16, cuda, K=8, pad=0.0)
     ids = ids.clamp(min=0)
