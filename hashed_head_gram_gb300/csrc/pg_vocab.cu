@@ -126,6 +126,7 @@ struct VocabArgs {
   int passes_h, passes_w;                // piece products of dh, dW
   int group, group_h, group_w;           // k-blocks that one sum in TMEM takes: logits, dh, dW
   int wide, seg, seg_log;                // columns of a logits tile, and of a segment of it (its half), and that's log2
+  int twice;                             // U is made once lse is there, by the logits again
   int tma_h, tma_w;                      // tiles of dh, dW go out by TMA
   int few_h;                             // dh is made for few rows
   int at_log;                            // log2 of the tokens that a place of `at` stands for
@@ -281,7 +282,7 @@ __device__ __forceinline__ void sort_keys(uint32_t (&x)[R]) {
 // Distillation: one warp a row, 8 rows a block. The teacher's softmax; the list sorted by token (R registers of a lane), so
 // that the tiles of the first product find what is theirs (`at`, where each segment's tokens begin) and keep those logits;
 // and the dot product of the heaviest token, for a reference. (Dot products of all listed tokens took 101 of 1346 us at
-// 8192 x 50,304 x 768 with lists of 32.) Bound by its instructions: 4096 lists of 64 LIST_TIME us.
+// 8192 x 50,304 x 768 with lists of 32.) Bound by its instructions: 4096 lists of 64 12 us.
 template <int HT, int WT, bool VEC, int R>
 __device__ void list_rows(const VocabArgs& g, int block, uint32_t (*s_key)[kMaxList], float (*s_w)[kMaxList], uint16_t (*s_at)[8]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = block * (kPrepThreads / 32) + warp;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kPrepThreads) vocab_prepare_kernel(const __gri
 
 // --------------------------------------------------------------------------------- products
 
-enum VocabKind { kSums, kKeep, kGrads };  // logits without and with U; the gradients
+enum VocabKind { kSums, kKeep, kGrads, kAgain };  // logits without and with U; the gradients; the logits again, for U alone
 
 // One tile of a product D = P Q^T: the k-blocks [kb0, kb1) of each piece product.
 struct VocabJob {
@@ -547,8 +548,10 @@ __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait
 
 // Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time. u = 2^(k2 z - c) in fp32 for the row's sum, and to U through the warp's shared memory (32 rows of 64 bytes,
 // swizzled as the TMA store reads them; two such buffers in turn, so that a store reads one while the other fills).
-template <bool KEEP>
-__device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row, int row0, int64_t col0, float c, bool dead) {
+template <int KIND>
+__device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row, int row0, int64_t col0,
+                                             float c, bool dead, float f) {
+  constexpr bool KEEP = KIND != kSums;
   const int lane = threadIdx.x & 31;
   const int64_t end = min(col0 + g.seg, g.V);
   const uint64_t k2 = pk(g.k2, g.k2), c2 = pk(-c, -c);
@@ -575,8 +578,13 @@ __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps
 #pragma unroll
       for (int k = 0; k < 32; ++k) x[k] = k < left ? x[k] : 0.f;
     }
+    if constexpr (KIND == kAgain) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 2) sum[k / 2 & 1] = add2(sum[k / 2 & 1], pk(x[k], x[k + 1]));
+      for (int k = 0; k < 32; ++k) x[k] *= f;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) sum[k / 2 & 1] = add2(sum[k / 2 & 1], pk(x[k], x[k + 1]));
+    }
     if constexpr (KEEP) {
       for (int p = 0; p < g.np_u; ++p) {
         uint32_t w[16];
@@ -685,15 +693,21 @@ __device__ __noinline__ void keep_listed(const VocabArgs& g, uint8_t* s_row, uin
   }
 }
 
-template <bool KEEP>
+template <int KIND>
 __device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabMaps& maps, const VocabJob& w, uint8_t* s_row,
                                                 uint32_t from, int row0, int half, float c, Listed listed) {
+  constexpr bool KEEP = KIND != kSums;
   const int lane = threadIdx.x & 31;
   const int64_t col0 = w.col0 + half * g.seg;
   if (row0 >= g.rows || col0 >= g.V) return;
+  if constexpr (KIND == kAgain) {  // c is lse, and f the row's part of the gradient
+    const float f = row0 + lane < g.rows ? g.f[row0 + lane] : 0.f;
+    logits_half<KIND>(g, maps, from, s_row, row0, col0, c, f == 0.f, f);
+    return;
+  }
   if (g.ids) keep_listed<KEEP>(g, s_row, from, row0, col0, listed);
   const bool dead = row0 + lane >= g.rows || c == INFINITY;
-  float sum = logits_half<KEEP>(g, maps, from, s_row, row0, col0, c, dead);
+  float sum = logits_half<KIND>(g, maps, from, s_row, row0, col0, c, dead, 1.f);
   float ref = c;
   const bool over = !dead && !(sum <= kSumLimit);
   if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the tile's largest for a reference
@@ -710,7 +724,7 @@ __device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabM
     if (over) ref = top == -INFINITY ? 0.f : top;
     if (KEEP && lane == 0) stores_done();  // the same places are written again
     __syncwarp();
-    sum = logits_half<KEEP>(g, maps, from, s_row, row0, col0, ref, dead);
+    sum = logits_half<KIND>(g, maps, from, s_row, row0, col0, ref, dead, 1.f);
   }
   if (row0 + lane < g.rows) g.sums[static_cast<int64_t>(static_cast<uint32_t>(col0) >> g.seg_log) * g.Nc + row0 + lane] = make_float2(ref, sum);
 }
@@ -737,7 +751,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabMap
   const int64_t rows = dh ? g.rows : g.V;
   if (row0 >= rows) return;
   float f = 1.f;
-  if (dh && !part) f = row0 + lane < rows ? g.f[row0 + lane] : 0.f;
+  if (dh && !part && !g.twice) f = row0 + lane < rows ? g.f[row0 + lane] : 0.f;
   void* dst;
   int dtype = PG_F32;
   const float* add32 = nullptr;
@@ -971,11 +985,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = row_of(job) + lane;
       next_c = INFINITY;
       if (row < g.rows) next_c = g.c[row];
-      if (g.ids) next_listed = listed_in(g, row, job.col0 + half * g.seg);
+      if (KIND != kAgain && g.ids) next_listed = listed_in(g, row, job.col0 + half * g.seg);
     };
     if (KIND != kGrads && more) {
       read_rows(w);
-      if (g.ids) first_listed(g, row_of(w) + lane, &next_listed);
+      if (KIND != kAgain && g.ids) first_listed(g, row_of(w) + lane, &next_listed);
     }
     for (int r = 0; fine && more; ++r) {
       const int row0 = row_of(w);
@@ -1040,10 +1054,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
       if constexpr (KIND == kGrads) grad_epilogue(g, maps, w, s_row, from, row0, half);
-      else logits_epilogue<KIND == kKeep>(g, maps, w, s_row, from, row0, half, c, listed);
+      else logits_epilogue<KIND>(g, maps, w, s_row, from, row0, half, c, listed);
       release();
       w = next;
-      if (KIND != kGrads && more && g.ids) first_listed(g, row_of(w) + lane, &next_listed);
+      if (KIND != kGrads && KIND != kAgain && more && g.ids) first_listed(g, row_of(w) + lane, &next_listed);
     }
     if (KIND != kSums && lane == 0) stores_done();
   }
@@ -1084,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The first product for up to 128 rows, where reading W is all that counts: W's rows are the tile's rows (128 a CTA), the
 // rows of h its columns (NT of them), so that a stage of the ring holds little beside W and the tensor core waits for
 // it alone. A lane has one row of W and all rows of h; sums over a warp's 32 rows of W (a segment) by halving.
-// 8 x 128,000 x 2560: FEW_TIME, against 152 us on 256 x 256 tiles of pairs, whose ring holds 96 KB of W an SM.
+// 8 x 128,000 x 2560: 100 us, 6.55 TB/s, against 152 us on 256 x 256 tiles of pairs, whose ring holds 96 KB of W an SM.
 template <int NT>
 struct Few {
   static constexpr int kWBytes = 128 * kBK * 2, kHBytes = NT * kBK * 2;
@@ -1619,7 +1633,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
       if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
       float beta = 1.f + 2.f * g.zl * lse;
       if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);  // (its part of U is divided by it)
-      const float to = moved ? lse2 : c;
+      const float to = moved || g.twice ? lse2 : c;
       const float f = weight == 0.f ? 0.f : weight * beta * exp2f(to - lse2);
       g.f[r] = f;
       s_f[k] = f;
@@ -1631,12 +1645,15 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     }
   }
   if (!GRAD) return;
+  if (g.twice && threadIdx.x < kRowsPer && in && c != INFINITY) g.c[r] = s_lse[k];
   __syncthreads();
   const int mine = warp % kRowsPer, part = warp / kRowsPer, row = r0 + mine;
   constexpr int kLanes = 32 * (kRowWarps / kRowsPer);
   const bool some = row < g.rows;
-  const int fix = some ? s_fix[mine] : 3;
-  const float f = some ? s_f[mine] : 0.f, to = some ? s_to[mine] : 0.f;
+  const int fix = some && !g.twice ? s_fix[mine] : 3;
+  float f = some ? s_f[mine] : 0.f;
+  if (g.twice && f != 0.f) f = 1.f;  // (U has it; rows without a gradient may still hold anything)
+  const float to = some ? s_to[mine] : 0.f;
   if (fix == 1 || fix == 2) {
     for (int64_t at = (part * 32 + lane) * 8; at < g.Vp; at += kLanes * 8) {
       const float by = fix == 2 ? 0.f : exp2f(0.5f * (g.sums[(at >> g.seg_log) * g.Nc + row].x - to));  // (its square may underflow)
@@ -1686,6 +1703,26 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   }
 }
 
+// The targets' places of a U that was made with lse and f: one warp a row.
+__global__ void __launch_bounds__(256) vocab_targets_kernel(const __grid_constant__ VocabArgs g) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= g.rows) return;
+  const float lse2 = g.c[r], f = g.f[r];
+  if (f == 0.f || lse2 == INFINITY) return;
+  float beta = 1.f + 2.f * g.zl * (lse2 * kLn2);
+  if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);
+  for (int e = lane; e < g.K; e += 32) {
+    const float w = g.wk[static_cast<int64_t>(r) * g.K + e];
+    if (w == -1.f || w == 0.f) continue;
+    const int64_t t = g.ids ? g.sorted[static_cast<int64_t>(r) * g.K + e] : __ldg(g.targets + g.row0 + r);
+    float x = f * (exp2f(g.zk[static_cast<int64_t>(r) * g.K + e] - lse2) - w / beta);
+    for (int p = 0; p < g.np_u; ++p)
+      reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + r) * g.Vp + t] = take_piece(x);
+  }
+}
+
 // A gradient from its parts, COLS columns a thread: dh (blocks below blocks_h), dW.
 template <int COLS>
 __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__ VocabArgs g, int blocks_h) {
@@ -1711,7 +1748,7 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(const __grid_constant__
   int dtype = g.gh_dtype;
   int64_t to = at;
   if (dh) {
-    const float f = g.f[at / g.d];
+    const float f = g.twice ? 1.f : g.f[at / g.d];
 #pragma unroll
     for (int e = 0; e < COLS; ++e) x[e] = f == 0.f ? 0.f : f * x[e];
     to += g.row0 * g.d;
@@ -1829,7 +1866,10 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->np_h = s.h_dtype == PG_F32 ? 3 : 1;
   g->np_w = s.w_dtype == PG_F32 ? 3 : 1;
   g->np_u = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32 ? 3 : 1;
-  g->np_f = s.gw_dtype == PG_F32 ? 3 : 1;
+  // An fp32 dW of bf16 operands: f h has 24 bits, so U and f h take six products. With f in U, made from the logits a second
+  // time, what is left of f h is h (without the rows that have no gradient): three products and one more of the logits (3001 x 32,003 x 515: 741 -> 622 us).
+  g->twice = s.grad && s.gw_dtype == PG_F32 && s.h_dtype == PG_BF16 && s.w_dtype == PG_BF16 && s.N > kFewRows;
+  g->np_f = s.gw_dtype == PG_F32 && !g->twice ? 3 : 1;
   const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 ? kGroupPieces : kGroup;
   const int groups = (blocks + longest - 1) / longest;
   g->group = (blocks + groups - 1) / groups;
@@ -2064,7 +2104,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
         return vocab_map(map, dst, 1, rows, s.d, s.d, rows, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, f32) ? 1 : -1;
       };
       const bool through = g.acc && !g.last;
-      g.tma_w = g.F && !g.parts_w && g.first && !g.accumulate ? out_map(&maps.Gw, through ? static_cast<void*>(g.acc) : g.gw, through ? PG_F32 : s.gw_dtype, s.V) : 0;
+      g.tma_w = s.gw_dtype >= 0 && !g.parts_w && g.first && !g.accumulate ? out_map(&maps.Gw, through ? static_cast<void*>(g.acc) : g.gw, through ? PG_F32 : s.gw_dtype, s.V) : 0;
       g.tma_h = s.gh_dtype >= 0 && !g.parts
                     ? out_map(&maps.Gh, static_cast<uint8_t*>(g.gh) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.gh_dtype)), s.gh_dtype, g.rows) : 0;
       if (g.tma_w < 0 || g.tma_h < 0) return PG_ERR_CUDA;
@@ -2074,7 +2114,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     if (few)
       st = few == 32 ? launch_few<32>(maps, g, s.grad, stream) : few == 64 ? launch_few<64>(maps, g, s.grad, stream)
                                                                              : launch_few<128>(maps, g, s.grad, stream);
-    else if (s.grad)
+    else if (s.grad && !g.twice)
       st = groups ? launch_product<kKeep, true>(maps, g, jobs, stream) : launch_product<kKeep, false>(maps, g, jobs, stream);
     else
       st = groups ? launch_product<kSums, true>(maps, g, jobs, stream) : launch_product<kSums, false>(maps, g, jobs, stream);
@@ -2082,6 +2122,11 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     g.segs = few && !s.grad ? static_cast<int>(4 * few_blocks(g.V)) : static_cast<int>((g.V + g.seg - 1) / g.seg);
     st = launch_next(rows_fn(s.grad, s.h_dtype, vec_h), (g.rows + kRowsPer - 1) / kRowsPer, 32 * kRowWarps, 0, false, true, stream, g);
     if (st != PG_OK) return st;
+    if (g.twice) {
+      st = groups ? launch_product<kAgain, true>(maps, g, jobs, stream) : launch_product<kAgain, false>(maps, g, jobs, stream);
+      if (st != PG_OK) return st;
+      if ((st = launch_next(vocab_targets_kernel, (g.rows + 7) / 8, 256, 0, false, true, stream, g)) != PG_OK) return st;
+    }
     VocabArgs b = g;
     if (g.tiles2) b.tiles2 = (g.rows + kTile - 1) / kTile * g.nd;  // a last chunk has fewer rows
     b.q_w = std::min(g.q_w, (g.rows + kBK - 1) / kBK);             // (no part without a k-block)

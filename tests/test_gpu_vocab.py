@@ -93,8 +93,9 @@ def reference(h, W, target=None, ids=None, u=None, scale=1.0, T=1.0, z_loss=0.0,
         prob = torch.softmax(z, 1)
         dz = torch.where(keep[:, None], g[:, None] * (beta[:, None] * prob - q), 0.0)
         off = torch.where(keep[:, None], (g.abs() * E)[:, None] * (beta.abs()[:, None] * prob + q * (ids is not None)), 0.0)
-        # exponentials below 2^-126 of the row's reference, which is at most its sum, are zero, as are such pieces
-        off = torch.where(keep[:, None], off + 2.0 ** -125 * g.abs()[:, None], off)
+        # exponentials below 2^-126 of the row's reference, which is at most its sum, are zero, as are such pieces; and
+        # pieces of dz below 2^-126 where U is dz
+        off = torch.where(keep[:, None], off + 2.0 ** -125 * (1 + g.abs()[:, None]), off)
         hk = torch.where(keep[:, None], h, 0.0)
         r.update(dh=dz @ W, dW=dz.T @ hk, dz=dz, off=off, h=hk, W=W, g=float(g.abs().max()))
     return r
