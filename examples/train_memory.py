@@ -1,8 +1,8 @@
 """Trains a small hashed N-gram memory with the library's training calls.
 
-    python examples/train_memory.py [--steps 40] [--tokens 8192]
+    python examples/train_memory.py [--steps 40] [--tokens 8192] [--loss distance|tokens|distill]
 
-One step, all of it on the current stream and without a host synchronisation:
+One step of `train`, all of it on the current stream and without a host synchronisation:
 
   x     = pg.embed(tokens)                          token embedding, scaled
   e, y  = pg.gather_project_gate(tokens, x)         lookup, W_V and the scalar gate: y = x + g e W^T
@@ -14,6 +14,13 @@ One step, all of it on the current stream and without a host synchronisation:
 
 The loss is the squared distance to the outputs of a teacher of the same shape (random
 embedding, table and projection), so it can be driven towards zero.
+
+`train_tokens` trains the same memory to predict tokens, with the embedding's table for an output table too:
+
+  dy, dE = pg.vocab_ce_grad(y, E, next tokens)      or pg.vocab_distill_grad(y, E, a teacher's top logits)
+  dE    += pg.embed_grad(tokens, dy)                the embedding's part of the tied table's gradient
+
+and the rest as above.
 """
 import argparse
 import os
@@ -107,12 +114,92 @@ def train(steps=40, n_tokens=8192, seed=0, device="cuda"):
     return losses
 
 
+class TokenTrainer:
+    """A Memory whose embedding is also its output table, and what a step of it needs."""
+
+    def __init__(self, model, N, K=0, logit_scale=0.5):
+        dev = model.E.device
+        self.model, self.K, self.logit_scale = model, K, logit_scale
+        self.bufs = model.buffers(N)
+        reads, r = N * model.desc.num_orders * model.desc.K, model.desc.r
+        self.dy = torch.empty(N, model.d, dtype=torch.bfloat16, device=dev)
+        self.dE, self.dT = torch.empty_like(model.E), torch.empty(reads, r, device=dev)
+        self.rows = torch.empty(reads, dtype=torch.int32, device=dev)
+        self.count = torch.empty(1, dtype=torch.int32, device=dev)
+        self.loss = torch.empty(N, device=dev)
+        sizes = [pg.lookup_grad_workspace_size(model.desc, N), pg.embed_grad_workspace_size(N, model.vocab, model.d),
+                 pg.orthogonalize_workspace_size(1, model.d, model.din)]
+        if K:
+            sizes.append(pg.vocab_distill_grad_workspace_size(N, model.vocab, model.d, K, pg.BF16, pg.BF16, pg.BF16, pg.F32))
+        else:
+            sizes.append(pg.vocab_ce_grad_workspace_size(N, model.vocab, model.d, pg.BF16, pg.BF16, pg.BF16, pg.F32))
+        self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=dev)  # one after the other on one stream
+        self.momentum, self.update = torch.zeros_like(model.W), torch.empty_like(model.W, dtype=torch.bfloat16)
+
+    def gradients(self, tokens, targets=None, teacher=None):
+        """Fills loss, dy, dE (both of its parts), rows and dT; returns e, y and dW. targets int32 like tokens (-1: none), or
+        teacher (ids, logits)."""
+        m = self.model
+        self.E16 = m.E.bfloat16()
+        e, y = m.forward(tokens, self.bufs)
+        mean = 1.0 / tokens.numel()
+        if teacher is None:
+            pg.vocab_ce_grad(y, self.E16, targets, self.loss, self.dy, self.dE, self.ws, scale=self.logit_scale, grad_scale=mean)
+        else:
+            pg.vocab_distill_grad(y, self.E16, *teacher, self.loss, self.dy, self.dE, self.ws, scale=self.logit_scale, grad_scale=mean)
+        dW = m.g * (self.dy.T @ e).float()
+        de = m.g * (self.dy @ m.W16)
+        pg.embed_grad(tokens, self.dy, self.dE, m.vocab, self.ws, scale=m.scale, accumulate=True)
+        pg.lookup_grad(m.desc, tokens, de, self.rows, self.dT, self.count, self.ws)
+        return e, y, dW
+
+    def step(self, tokens, targets=None, teacher=None, lr=0.02):
+        m = self.model
+        _, _, dW = self.gradients(tokens, targets, teacher)
+        self.momentum.mul_(0.9).add_(dW)
+        pg.orthogonalize(self.momentum, self.update, self.ws, scale=max(1.0, m.d / m.din) ** 0.5)
+        m.E.sub_(self.dE / (self.dE.square().mean(1, keepdim=True).sqrt() + 1e-6) * m.E.square().mean().sqrt(), alpha=lr)
+        at = torch.where(self.rows < 0, m.T.shape[0] - 1, self.rows.long())  # PG_NO_ROW: the spare row
+        m.T.index_add_(0, at, self.dT / (self.dT.square().mean(1, keepdim=True).sqrt() + 1e-9), alpha=-lr)
+        m.W.sub_(self.update.float(), alpha=lr)
+        m.refresh()
+        return self.loss.mean()
+
+
+def train_tokens(steps=40, n_tokens=8192, seed=0, device="cuda", K=0):
+    """Next-token prediction; with K > 0 distillation of a teacher's K top logits instead. Returns every step's loss."""
+    spec = W.TableSpec("memory", W.MODE_PAGEGRAM, K=8, S=4, r=64, row_dtype=W.DT_BF16, pages=[499, 491], hash_seed=7)
+    vocab, d, B = 512, 256, 8
+    rng = np.random.default_rng(seed)
+    start = W.zipf_ids(rng, vocab, 1.1, n_tokens // B * B).reshape(B, -1).astype(np.int64)
+    stream = start.copy()
+    for t in range(2, stream.shape[1]):  # mostly a function of the two tokens before
+        rule = (stream[:, t - 1] * 31 + stream[:, t - 2] * 17 + 5) % vocab
+        stream[:, t] = np.where(rng.random(B) < 0.8, rule, start[:, t])
+    tokens = torch.from_numpy(stream.astype(np.int32)).to(device)
+    targets = torch.full_like(tokens, -1)
+    targets[:, :-1] = tokens[:, 1:]
+    N = tokens.numel()
+    trainer = TokenTrainer(Memory(spec, vocab, d, seed + 2, device, std=1.0), N, K)
+    teacher = None
+    if K:
+        t = Memory(spec, vocab, d, seed + 1, device, std=1.0)
+        y = t.forward(tokens, t.buffers(N))[1].float()
+        logits, ids = torch.topk(trainer.logit_scale * y @ t.E.T, K)
+        teacher = ids.int().contiguous(), logits.contiguous()
+    losses = torch.empty(steps, device=device)
+    for i in range(steps):
+        losses[i] = trainer.step(tokens, targets, teacher)
+    return losses
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=40)
     ap.add_argument("--tokens", type=int, default=8192)
+    ap.add_argument("--loss", choices=["distance", "tokens", "distill"], default="distance")
     a = ap.parse_args()
-    losses = train(a.steps, a.tokens).tolist()
+    losses = (train(a.steps, a.tokens) if a.loss == "distance" else train_tokens(a.steps, a.tokens, K=16 if a.loss == "distill" else 0)).tolist()
     for i in range(0, a.steps, max(1, a.steps // 10)):
         print(f"step {i:4d}  loss {losses[i]:.5f}")
     print(f"step {a.steps - 1:4d}  loss {losses[-1]:.5f}")

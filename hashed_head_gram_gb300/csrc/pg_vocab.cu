@@ -51,7 +51,8 @@ constexpr int kAtOnce = 1024;            // segments whose beginnings a block co
 constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (any number gives the same results)
 constexpr int64_t kKeepBytes = 2ll << 30;  // of U, f h and the pieces of h
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
-constexpr int64_t kPartBytes = 256 << 20;  // of dW's parts
+constexpr int kMaxParts = 32;              // of a gradient, and
+constexpr int kPartTiles = 152;            // tiles that they come to, at most
 constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
 
 constexpr int kPrepThreads = 256;
@@ -1810,7 +1811,7 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
     // few rows: dh by itself, in as many parts as fill the SMs once or twice (a table of a few k-blocks: with dW)
     const int tiles = (g->d + 127) / 128;
     double best = -1;
-    for (int waves = 1; waves <= 3; ++waves) {
+    for (int waves = 1; waves <= 2; ++waves) {
       const int q = static_cast<int>(std::min<int64_t>(std::max(1, 2 * units * waves / tiles), kv));
       const double full = static_cast<double>(q) * tiles / (2 * units * ((q * tiles + 2 * units - 1) / (2 * units)));
       if (full <= best + 0.04) continue;
@@ -1822,8 +1823,8 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   }
   double best = -1;
   int best_q = 1, best_qw = 1;
-  for (int q = 1; q <= (has_h ? 16 : 1) && (q == 1 || kv >= 2 * q); ++q)
-    for (int qw = 1; qw <= (has_w ? 32 : 1) && (qw == 1 || (kn >= 2 * qw && 4ll * qw * g->V * g->d <= kPartBytes)); qw *= 2) {
+  for (int q = 1; q <= (has_h ? kMaxParts : 1) && (q == 1 || (kv >= 2 * q && static_cast<int64_t>(q) * g->tiles2 <= kPartTiles)); ++q)
+    for (int qw = 1; qw <= (has_w ? kMaxParts : 1) && (qw == 1 || (kn >= 2 * qw && static_cast<int64_t>(qw) * g->tiles3 <= kPartTiles)); qw *= 2) {
       g->q = q;
       g->q_w = qw;
       const double cost2 = static_cast<double>((kv + q - 1) / q) * g->passes_h + 4, cost3 = static_cast<double>((kn + qw - 1) / qw) * g->passes_w + 4;
@@ -1843,7 +1844,8 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   g->q_w = best_qw;
 }
 
-// Sizes of everything, and its place in the workspace (base null: the size alone).
+// Sizes of everything, and its place in the workspace (base null: the size alone). What is reserved never falls as the
+// rows become more, though tiles and parts are then cut in other ways: a workspace for N rows serves any call of fewer.
 size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   uint8_t* first = base ? reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 127) & ~uintptr_t(127)) : nullptr;
   size_t at = 0;
@@ -1852,7 +1854,7 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
     at += static_cast<size_t>((bytes + 127) / 128 * 128);
     return ptr;
   };
-  const bool has_h = s.gh_dtype >= 0, has_w = s.gw_dtype >= 0;
+  const bool has_h = s.gh_dtype >= 0, has_w = s.gw_dtype >= 0, is_few = s.N <= kFewRows;
   g->V = s.V;
   g->Vp = (s.V + 63) / 64 * 64;
   g->N = static_cast<int>(s.N);
@@ -1867,49 +1869,61 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->np_w = s.w_dtype == PG_F32 ? 3 : 1;
   g->np_u = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32 ? 3 : 1;
   // An fp32 dW of bf16 operands: f h has 24 bits, so U and f h take six products. With f in U, made from the logits a second
-  // time, what is left of f h is h (without the rows that have no gradient): three products and one more of the logits (3001 x 32,003 x 515: 741 -> 622 us).
-  g->twice = s.grad && s.gw_dtype == PG_F32 && s.h_dtype == PG_BF16 && s.w_dtype == PG_BF16 && s.N > kFewRows;
-  g->np_f = s.gw_dtype == PG_F32 && !g->twice ? 3 : 1;
+  // time, what is left of f h is h (without the rows that have no gradient): three products and one more of the logits
+  // (3001 x 32,003 x 515: 741 -> 622 us).
+  g->twice = s.grad && s.gw_dtype == PG_F32 && s.h_dtype == PG_BF16 && s.w_dtype == PG_BF16 && !is_few;
+  const int np_f = s.gw_dtype == PG_F32 ? 3 : 1;
+  g->np_f = g->twice ? 1 : np_f;
   const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 ? kGroupPieces : kGroup;
   const int groups = (blocks + longest - 1) / longest;
   g->group = (blocks + groups - 1) / groups;
   // narrower tiles of the logits where the widest leave pairs idle
   g->wide = kTile;
   while (g->wide > 64 && (s.N + kTile - 1) / kTile * ((s.V + g->wide - 1) / g->wide) <= kPlanUnits / 2) g->wide /= 2;
-  if (s.N <= kFewRows) g->wide = 64;
+  if (is_few) g->wide = 64;
   g->seg = g->wide / 2;
   g->seg_log = g->seg == 128 ? 7 : g->seg == 64 ? 6 : 5;
-  g->at_log = s.N <= kFewRows ? 7 : g->seg_log;
-  const int64_t tiles = (s.V + g->wide - 1) / g->wide;
-  const int64_t row_bytes = 2 * (g->np_u * g->Vp + (has_w ? g->np_f * g->dp : 0) + (needs_copy(s.h_dtype, s.d) ? g->np_h * g->dp : 0));
-  int64_t most = s.grad ? kKeepBytes / row_bytes : kMaxForwardRows;
-  most = std::min(most, kSumBytes / (16 * tiles));
+  g->at_log = is_few ? 7 : g->seg_log;
+  const int64_t widest = (s.V + kTile - 1) / kTile;  // tiles a row of them
+  const int64_t row_bytes = 2 * (g->np_u * g->Vp + (has_w ? np_f * g->dp : 0) + (needs_copy(s.h_dtype, s.d) ? g->np_h * g->dp : 0));
+  int64_t most = std::min(s.grad ? kKeepBytes / row_bytes : kMaxForwardRows, kSumBytes / (16 * widest));
   most = std::max<int64_t>(kTile, most / kTile * kTile);
   const int64_t chunks = (s.N + most - 1) / most;
   g->Nc = static_cast<int>(((s.N + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
-  const int64_t Nc = g->Nc;
+  const int64_t rows = std::min(most, (s.N + kTile - 1) / kTile * kTile);  // room for these (Nc of them or more)
   g->Wp = needs_copy(s.w_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_w * s.V * g->dp)) : nullptr;
-  g->hp = needs_copy(s.h_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * Nc * g->dp)) : nullptr;
-  g->sums = reinterpret_cast<float2*>(take(8 * std::max(2 * tiles, s.N <= kFewRows ? 4 * ((s.V + 127) / 128) : 0) * Nc));
-  g->zk = reinterpret_cast<float*>(take(4ll * Nc * s.K));
-  g->wk = reinterpret_cast<float*>(take(4ll * Nc * s.K));
-  g->sorted = s.list ? reinterpret_cast<int32_t*>(take(4ll * Nc * s.K)) : nullptr;
-  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2ll * (2 * tiles + 1) * Nc)) : nullptr;
-  g->c = reinterpret_cast<float*>(take(4 * Nc));
-  g->a = reinterpret_cast<float*>(take(4 * Nc));
+  g->hp = needs_copy(s.h_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * rows * g->dp)) : nullptr;
+  // (narrower tiles are kPlanUnits at most, for a chunk of kTile rows; few rows have a sum for 32 columns, or four a CTA of 128)
+  g->sums = reinterpret_cast<float2*>(take(16 * std::max({widest * rows, static_cast<int64_t>(kPlanUnits) * kTile,
+                                                          std::max((s.V + 63) / 64, 2 * ((s.V + 127) / 128)) * kTile})));
+  g->zk = reinterpret_cast<float*>(take(4ll * rows * s.K));
+  g->wk = reinterpret_cast<float*>(take(4ll * rows * s.K));
+  g->sorted = s.list ? reinterpret_cast<int32_t*>(take(4ll * rows * s.K)) : nullptr;
+  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2 * std::max<int64_t>((2 * widest + 1) * rows, int64_t{3} * kPlanUnits * kTile))) : nullptr;
+  g->c = reinterpret_cast<float*>(take(4 * rows));
+  g->a = reinterpret_cast<float*>(take(4 * rows));
   g->U = nullptr;
   g->F = nullptr;
   g->f = g->acc = g->parts = g->parts_w = nullptr;
   if (s.grad) {
-    g->f = reinterpret_cast<float*>(take(4 * Nc));
-    g->U = reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_u * Nc * g->Vp));
+    g->f = reinterpret_cast<float*>(take(4 * rows));
+    g->U = reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_u * rows * g->Vp));
     if (has_w) {
-      g->F = reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_f * Nc * g->dp));
+      g->F = reinterpret_cast<__nv_bfloat16*>(take(2ll * np_f * rows * g->dp));
       if (chunks > 1 && s.gw_dtype == PG_BF16) g->acc = reinterpret_cast<float*>(take(4ll * s.V * s.d));
     }
     plan_schedule(g, kPlanUnits, has_h, has_w);
-    if (has_h && (g->q > 1 || g->few_h)) g->parts = reinterpret_cast<float*>(take(4ll * g->q * Nc * s.d));
-    if (has_w && g->q_w > 1) g->parts_w = reinterpret_cast<float*>(take(4ll * g->q_w * s.V * s.d));
+    const int64_t kv = (s.V + kBK - 1) / kBK, kn = (std::min(s.N, rows) + kBK - 1) / kBK;
+    if (has_h) {  // parts of a chunk's rows, or for few rows of kTile
+      const int64_t some = std::min<int64_t>(kMaxParts * rows / kTile, kPartTiles / g->nd);
+      const int64_t few = std::min<int64_t>(kv, std::max(1, 4 * kPlanUnits / ((s.d + 127) / 128)));
+      float* to = reinterpret_cast<float*>(take(4ll * kTile * s.d * std::max({some, few, int64_t{1}})));
+      if (g->q > 1 || g->few_h) g->parts = to;
+    }
+    if (has_w && kn >= 4) {
+      float* to = reinterpret_cast<float*>(take(4ll * s.V * s.d * std::min({int64_t{kMaxParts}, kn / 2, kPartTiles / (widest * g->nd)})));
+      if (g->q_w > 1) g->parts_w = to;
+    }
   }
   return at + 128;
 }

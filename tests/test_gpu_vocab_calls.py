@@ -394,3 +394,16 @@ def test_offsets_past_32_bits(cuda, N):
     dh = sum(p[:, lo:lo + 200_000] @ W[lo:lo + 200_000].double() for lo in range(0, V, 200_000))
     assert float((gh.double() - dh).norm() / dh.norm()) <= 2.0 ** -7
     assert not gw.isnan().any()
+
+
+def test_a_workspace_serves_calls_of_fewer_rows(cuda):
+    pg = _pg()
+    h, W, t, ids, u = make(90, 1500, 2000, 264, BF16, BF16, cuda, K=20)
+    size = pg.vocab_distill_grad_workspace_size(1500, 2000, 264, 20, 1, 1, 1, 0)
+    ws = torch.full((size + 512,), 0x5A, dtype=torch.uint8, device=cuda)
+    for N in (1500, 1, 31, 64, 128, 129, 255, 257, 400, 513, 1024, 1499):
+        o = [torch.empty(N, device=cuda), torch.empty(N, 264, dtype=BF16, device=cuda), torch.empty(2000, 264, device=cuda)]
+        pg.vocab_distill_grad(h[:N], W, ids[:N], u[:N], *o, ws[:size])
+        check_grads(reference(h[:N], W, ids=ids[:N], u=u[:N]), o[1], o[2])
+        assert (ws[size:] == 0x5A).all()
+    assert pg.device_error() == 0

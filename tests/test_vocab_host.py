@@ -86,6 +86,7 @@ def test_workspace_queries(pg):
     # exp of the logits for a chunk of rows, 2 GiB at most, however many rows there are
     small = pg.vocab_ce_grad_workspace_size(4096, 50304, 768, 1, 1, 1, 1)
     assert 2 * 4096 * 50304 <= small <= 2 * 4096 * 50304 + (1 << 28)
+    assert pg.vocab_ce_grad_workspace_size(4, 100, 8, 1, 1, 1, 1) <= 1 << 20
     for N in (65536, 1 << 24, (1 << 31) - 1):
         assert pg.vocab_ce_grad_workspace_size(N, 50304, 768, 1, 1, 1, 1) <= (2 << 30) + (1 << 30)
     # the forward call keeps sums and, of fp32 operands, their pieces
@@ -98,6 +99,19 @@ def test_workspace_queries(pg):
             assert pg.vocab_ce_workspace_size(N, V, d, dt, dt) > 0
             assert pg.vocab_ce_grad_workspace_size(N, V, d, dt, dt, dt, dt) > 0
             assert pg.vocab_distill_grad_workspace_size(N, V, d, 256, dt, dt, None, dt) > 0
+
+
+@pytest.mark.parametrize("V,d", [(1, 1), (10, 8), (300, 72), (1024, 256), (5000, 2560), (50304, 768), (128000, 33)])
+def test_a_workspace_serves_fewer_rows(pg, V, d):
+    rows = sorted({*range(1, 140), *(128 * k + r for k in range(1, 90) for r in (-1, 0, 1)), *(2 ** k + r for k in range(13, 31) for r in (-1, 0, 1)),
+                   *(int(1.13 ** k) for k in range(60, 175))})
+    for hd, wd, ghd, gwd in [(1, 1, 1, 1), (0, 0, 0, 0), (1, 1, None, 0), (1, 0, 0, None), (1, 1, 1, 0)]:
+        last = [0] * 4
+        for N in rows:
+            now = [pg.vocab_ce_workspace_size(N, V, d, hd, wd), pg.vocab_ce_grad_workspace_size(N, V, d, hd, wd, ghd, gwd),
+                   pg.vocab_distill_workspace_size(N, V, d, 30, hd, wd), pg.vocab_distill_grad_workspace_size(N, V, d, 30, hd, wd, ghd, gwd)]
+            assert all(a >= b for a, b in zip(now, last)), (N, now, last)
+            last = now
 
 
 def test_binding_checks_sizes_and_types(pg):
