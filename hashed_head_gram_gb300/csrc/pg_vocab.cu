@@ -7,27 +7,35 @@
 //   dh = scale dz W,  dW = scale dz^T h
 // Three products of 2 N V d operations; the first alone without gradients.
 //
-// The logits exist only tile by tile in TMEM. A row's targets are few, so their logits are dot products of
-// their own (vocab_targets_kernel, before the first product), and their largest is a reference c_i <= lse_i that the
-// epilogue of the first product knows beforehand: it stores u_ij = exp(z_ij - c_i) and adds up each tile's rows. One
-// small kernel a chunk then has lse_i, the loss and f_i = g_i scale beta_i exp(c_i - lse_i), puts
+// The logits exist only tile by tile in TMEM. A row has a reference c_i <= lse_i that the epilogue of the first
+// product knows beforehand: the logit of its target, or of the heaviest token of its list, a dot product of its own
+// (vocab_prepare_kernel). The epilogue stores u_ij = exp(z_ij - c_i), adds up each tile's rows and keeps the listed
+// tokens' logits. One small kernel a chunk (vocab_rows_kernel) then has lse_i, the loss and
+// f_i = g_i scale beta_i exp(c_i - lse_i), puts
 //   u_ij - w_ij exp(lse_i - c_i) / beta_i
 // at the targets (from fp32 logits: p - 1 loses nothing where p is close to 1), and
 //   dh_i = f_i (U W)_i,   dW = U^T (f h)
 // are two more products. So the logits are made once, nothing normalises U, and a gradient costs 6 N V d
 // operations; making the logits again in place of keeping U would cost 8. U is kept in bf16, whose exponent takes
-// exp(+-87); u's rounding (2^-8 at most) is a rounding of p. It is kept for a chunk of the rows, 2 GiB at most.
-// A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit of that tile
-// as its reference instead, and the small kernel brings the whole row to the reference lse_i: a pass over the rows
-// that need it and no others.
+// exp(+-87); u's rounding (2^-8 at most) is a rounding of p, and that of f h another of dW's. It is kept for a chunk of
+// the rows, 2 GiB at most. A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit
+// of that tile as its reference instead, and vocab_rows_kernel brings the whole row to the reference lse_i: a pass over the
+// rows that need it and no others.
 //
 // Precision. bf16 operands and bf16 gradients take one product of bf16 operands each. fp32 values are sums of bf16
 // "pieces" (value = p0 + p1 + p2, 8 bits each), and their products the sum of the pieces' products down to 2^-24 (six of
-// nine): fp32 operands are split beforehand, and U and f h have three pieces for an fp32 gradient. All sums are fp32
-// in TMEM.
+// nine): fp32 operands are split beforehand, and U and f h have three pieces for an fp32 gradient. (An fp32 dW of bf16
+// operands has f in U, which takes the logits a second time, and h as it is.) All sums are fp32 in TMEM, and long ones that an
+// fp32 result comes of are made in groups.
 //
 // The products: 256 x 256 tiles on CTA pairs (tcgen05, cta_group::2), 128-deep k-blocks of both operands by
-// TMA into a ring of three, two accumulators in TMEM, eight epilogue warps.
+// TMA into a ring of three, two accumulators in TMEM, eight epilogue warps. Up to 128 rows, where reading W is all that
+// counts, the first product and dh have kernels of their own in which W's rows and columns are the tile's rows.
+//
+// Bound by the tensor cores, and in long calls by the power limit (the measured bf16 rate: 1914 TFLOP/s for a short
+// product, 1721 for seconds of them). 16,384 x 50,304 x 768: 734-753 us, 1.68-1.72 PFLOP/s. With gradients, 65,536 x 50,304 x 768:
+// 10.2 ms, 1.49; 8192 x 128,000 x 2560: 9.9 ms, 1.63. Of 2.33 ms a chunk of 16,384 rows by 768 (at full clocks) the first
+// product is 0.77 (0.62 without U: its stores go through L2 beside 16 TB/s of operand loads), the other two 1.41.
 #include <cuda_bf16.h>
 
 #include <limits.h>
@@ -52,7 +60,7 @@ constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (a
 constexpr int64_t kKeepBytes = 2ll << 30;  // of U, f h and the pieces of h
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
 constexpr int kMaxParts = 32;              // of a gradient, and
-constexpr int kPartTiles = 152;            // tiles that they come to, at most
+constexpr int kPartTiles = 640;            // tiles that they come to, at most
 constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
 
 constexpr int kPrepThreads = 256;
@@ -218,7 +226,7 @@ __device__ __forceinline__ void warp_dots(const VocabArgs& g, int64_t i, const i
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.f;
-#pragma unroll 2
+#pragma unroll 8
   for (int c = lane * kStep; c < g.d; c += 32 * kStep) {
     float x[kStep], y[E][kStep];
     load_cols<HT, kStep>(g.h, i * g.d + c, x);

@@ -762,8 +762,8 @@ pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batch, int32_t 
  * tied: pg_embed_grad with accumulate adds the embedding's part to grad_w). The logits
  *   z_ij = scale <h_i, W_j>
  * are never stored: they exist tile by tile on chip. The gradient calls keep exp(z_ij - a reference of
- * row i) for a bounded chunk of the rows in their workspace (2 GiB; at least 256 rows), so that every
- * product runs once.
+ * row i) for a bounded chunk of the rows in their workspace (2 GiB; at least 256 rows), so that the
+ * logits need not be made again.
  *
  * pg_vocab_ce -- softmax cross entropy, one target t_i a row:
  *   lse_i = log sum_j exp(z_ij);  loss_i = lse_i - z_{i,t_i} + z_loss lse_i^2
@@ -788,12 +788,13 @@ pg_status pg_orthogonalize(const void* G, int32_t dtype, int32_t batch, int32_t 
  *  loss        device fp32 [N]; optional in the gradient calls. lse: device fp32 [N], optional
  *  grad_h      device [N, d]; gh_dtype PG_F32, PG_BF16 or -1 (no such gradient; grad_h is not looked at)
  *  grad_w      device [V, d]; gw_dtype likewise. Aligned to their elements; they must not overlap anything else
- *  workspace   device, 16-byte aligned, >= the call's _workspace_size bytes (with the same sizes and types), scratch
+ *  workspace   device, 16-byte aligned, >= the call's _workspace_size bytes, scratch. With the other sizes and the types
+ *              the same, the size for N rows serves any call of fewer
  *  err_index   device int32 [1], or NULL: the smallest row with a target or a listed token outside [0, V), else -1
- * Sums are fp32. bf16 gradients take the logits' gradients in bf16 (2^-8 of an entry at most) as the tensor
- * cores do; fp32 operands and fp32 gradients take every value as a sum of three bf16 pieces (24 bits), with three
- * products of bf16 in place of one where the other operand is bf16, six where it is not. Equal inputs give
- * equal bits.
+ * Sums are fp32. bf16 gradients are products of values rounded to bf16 (2^-8 of each at most): the logits'
+ * gradients, the rows of h scaled by their part of them (grad_w), an fp32 W (grad_h). fp32 operands and fp32
+ * gradients take every value as a sum of three bf16 pieces (24 bits), with three products of bf16 in place of one
+ * where the other operand is bf16, six where it is not: errors of 1e-6 or so. Equal inputs give equal bits.
  * 0 <= N < 2^31, 1 <= V < 2^24, 1 <= d <= 16384, 1 <= K <= 256 (else PG_ERR_SHAPE); scale, z_loss, grad_scale finite,
  * temperature > 0 and neither it nor scale / temperature out of fp32's range (else PG_ERR_UNSUPPORTED). N == 0 enqueues
  * nothing, but for zeros in grad_w without accumulate. A device wait that runs out (about a second) sets device

@@ -407,3 +407,54 @@ def test_a_workspace_serves_calls_of_fewer_rows(cuda):
         check_grads(reference(h[:N], W, ids=ids[:N], u=u[:N]), o[1], o[2])
         assert (ws[size:] == 0x5A).all()
     assert pg.device_error() == 0
+
+
+@pytest.mark.parametrize("N", [5, 150])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_the_widest_rows(cuda, N, dt):
+    h, W, t = make(N, N, 300, 16384, dt, dt, cuda)
+    r = reference(h, W, t)
+    loss, lse, dh, dW = run_ce(h, W, t, dt, dt)
+    check_values(r, loss, lse)
+    check_grads(r, dh, dW)
+
+
+def test_the_largest_vocabulary(cuda):
+    V, N, d = (1 << 24) - 1, 3, 8
+    gen = torch.Generator(device=cuda).manual_seed(6)
+    W = torch.randn(V, d, generator=gen, device=cuda).to(BF16)
+    h = torch.randn(N, d, generator=gen, device=cuda).to(BF16)
+    ids = torch.tensor([[V - 1, 0, V - 1, 12345678], [V, V - 2, -1, 5], [V - 1, V, -7, V + 1]], dtype=torch.int32, device=cuda)
+    u = torch.tensor([[1.0, 2.0, 0.5, -1.0], [3.0, 0.0, 9.0, 0.5], [1.0, 5.0, 6.0, 7.0]], device=cuda)
+    r = reference(h, W, ids=ids, u=u)
+    loss, lse, dh, dW = run_distill(h, W, ids, u, BF16, BF16)
+    check_values(r, loss, lse)
+    check_grads(r, dh, dW)
+    t = torch.tensor([V - 1, V, 0], dtype=torch.int32, device=cuda)
+    loss, lse, _, _ = run_ce(h, W, t)
+    check_values(reference(h, W, t, grads=False), loss, lse)
+
+
+@pytest.mark.parametrize("N", NS)
+def test_what_is_left_out(cuda, N):
+    # no loss, no lse, one gradient or none; scales of zero; a workspace that starts on 16 bytes
+    pg = _pg()
+    h, W, t, ids, u = make(N, N, 700, 80, BF16, BF16, cuda, K=5)
+    full = run_ce(h, W, t, BF16, BF16)
+    for ghd, gwd in [(1, None), (None, 1), (None, None)]:
+        size = pg.vocab_ce_grad_workspace_size(N, 700, 80, 1, 1, ghd, gwd)
+        ws = torch.empty(size + 16, dtype=torch.uint8, device=cuda)[16:]
+        gh = None if ghd is None else torch.empty_like(h)
+        gw = None if gwd is None else torch.empty_like(W)
+        pg.vocab_ce_grad(h, W, t, None, gh, gw, ws)
+        assert gh is None or torch.equal(gh, full[2])
+        assert gw is None or torch.equal(gw, full[3])
+    loss, lse, dh, dW = run_ce(h, W, t, BF16, F32, scale=0.0)
+    keep = (t >= 0) & (t < 700)
+    assert ((lse - math.log(700)).abs() <= 1e-5)[keep].all() and (dh == 0).all() and (dW == 0).all()
+    _, _, dh, dW = run_distill(h, W, ids, u, BF16, F32, grad_scale=0.0)
+    assert (dh == 0).all() and (dW == 0).all()
+    with pytest.raises(ValueError, match="contiguous"):
+        pg.vocab_ce(h[:, ::2], W[:, ::2], t, torch.empty(N, device=cuda), None)
+    with pytest.raises(pg.PgError):
+        pg.vocab_ce(h, W, t, torch.empty(N, device=cuda), torch.empty(100, dtype=torch.uint8, device=cuda))
