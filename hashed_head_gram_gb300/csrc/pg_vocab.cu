@@ -80,10 +80,20 @@ constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: 
 
 // A tensor core cuts what falls below its sum where an fp32 addition rounds, so a sum's error grows with its length, to
 // one side: 1.4e-6 of the logits at d = 2560, 4e-6 with the six products of fp32 operands. Where an fp32 result comes
-// of it, sums longer than this many k-blocks are made in groups, which the epilogue adds up in registers; and the
-// products of pieces run from the smallest to the largest, so that only the largest's additions count.
-constexpr int kGroup = 10;               // bf16 operands (80 additions: 7e-7)
+// of it, sums longer than kGroup k-blocks are made in groups, which the epilogue adds up in registers. Products of pieces
+// run from the smallest to the largest, k-block by k-block, and of the largest every kCut instructions (of 16 k) make a sum of
+// their own, so that next to nothing is cut: fp32 gradients at 512 x 1024 x 96 1.2e-5 off in one sum, 1.5e-6 a k-block, CUT_ERROR so.
+constexpr int kGroup = 10;               // (80 additions: 7e-7)
 constexpr int kGroupPieces = 1;          // fp32 operands or gradients
+constexpr int kCut = 2;
+
+// How many sums a tile's product along k-blocks [kb0, kb1) of `depth` is made of.
+__host__ __device__ __forceinline__ int sums_of(int kb0, int kb1, int group, int passes, int64_t depth) {
+  if (passes == 1) return group < kb1 - kb0 ? (kb1 - kb0 + group - 1) / group : 1;
+  const int64_t left = (depth - static_cast<int64_t>(kb1 - 1) * kBK + 15) / 16;  // instructions of the last k-block
+  const int steps = left < kBK / 16 ? static_cast<int>(left) : kBK / 16;
+  return (kb1 - kb0 - 1) * (1 + kBK / 16 / kCut) + 1 + (steps + kCut - 1) / kCut;
+}
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Sums in groups take 128 registers a thread in the epilogue: its two warpgroups take over what the first does not need.
@@ -945,15 +955,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // groups of an MN-major tile
         const uint32_t step_p = w.p_mn ? 2048 >> 4 : 32 >> 4, step_q = w.q_mn ? 2048 >> 4 : 32 >> 4;
         const uint32_t half_p = w.p_mn ? 4 * step_p : kOperandBytes / 2 >> 4, half_q = w.q_mn ? 4 * step_q : kOperandBytes / 2 >> 4;
-        for (int k0 = w.kb0; fine && k0 < w.kb1; k0 += w.group) {
-          if (!wait<true>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
-            fine = false;
-            break;
-          }
+        uint32_t d = 0, more_of_it = 0;
+        auto begin = [&]() {
+          fine = fine && wait<true>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort);
           fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * kTile);
+          d = tmem + static_cast<uint32_t>(acc * kTile);
+          more_of_it = 0;
+        };
+        auto finish = [&]() {
+          commit<true>(smem_addr(&bars->acc_full[acc]));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        };
+        for (int k0 = w.kb0; fine && k0 < w.kb1; k0 += w.group) {
           const int len = min(k0 + w.group, w.kb1) - k0, blocks = len * w.passes;
-          for (int kb = 0, at = k0; kb < blocks; ++kb) {
+          begin();
+          for (int kb = 0, at = k0; fine && kb < blocks; ++kb) {
             if (!wait<true>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
               fine = false;
               break;
@@ -962,22 +979,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sp = smem_addr(ring + stage * (2 * kOperandBytes));
             const uint64_t dp = operand_desc(sp, w.p_mn), dq = operand_desc(sp + kOperandBytes, w.q_mn);
             const int64_t left = w.depth - static_cast<int64_t>(at) * kBK;  // (what is behind it is zero)
+            const bool cut = GROUPS && w.passes > 1 && kb >= blocks - len;
             if (++at == k0 + len) at = k0;
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              if (k * 16 < left)
-                mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc,
-                              (kb | k) != 0);
+            for (int k = 0; k < kBK / 16; ++k) {
+              if (k * 16 >= left) break;
+              if (k % kCut == 0 && cut) {
+                finish();
+                begin();
+              }
+              if (!fine) break;
+              mma_f16<true>(d, dp + (k / 4) * half_p + (k % 4) * step_p, dq + (k / 4) * half_q + (k % 4) * step_q, idesc, more_of_it);
+              more_of_it = 1;
+            }
+            if (!fine) break;
             commit<true>(smem_addr(&bars->empty[stage]));
             if (++stage == kStages) {
               stage = 0;
               ring_phase ^= 1u;
             }
           }
-          if (!fine) break;
-          commit<true>(smem_addr(&bars->acc_full[acc]));
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
+          if (fine) finish();
         }
       }
     }
@@ -1027,12 +1049,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
-      if (GROUPS && w.kb0 + w.group < w.kb1) {
-        // the groups before the last in registers; the last one's sums go back to TMEM with the others added
+      const int sums = GROUPS ? sums_of(w.kb0, w.kb1, w.group, w.passes, w.depth) : 1;
+      if (GROUPS && sums > 1) {
+        // all but the last in registers; the last goes back to TMEM with the others added
         float z[128];
 #pragma unroll
         for (int k = 0; k < 128; ++k) z[k] = 0.f;
-        for (int k0 = w.kb0; k0 + w.group < w.kb1; k0 += w.group) {
+        for (int k = 1; k < sums; ++k) {
           if (!acquire()) break;
           const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
 #pragma unroll
@@ -1146,6 +1169,57 @@ __device__ __forceinline__ float2 joined(float2 a, float2 b) {
   return make_float2(a.x, a.y + b.y * exp2f(b.x - a.x));
 }
 
+// The issuing thread's part of a group: k-blocks [k0, k0 + len) of each product of pieces, W K-major or MN-major.
+template <int NT, bool MN>
+__device__ __forceinline__ void few_products(FewBars<NT>* bars, volatile int* abort, uint32_t tmem, uint32_t ring, int k0, int len, int passes,
+                                             int64_t depth, int* stage, uint32_t* ring_phase, int* acc, uint32_t* acc_phase, bool* fine) {
+  using T = Few<NT>;
+  uint32_t d = 0, more = 0;
+  auto begin = [&]() {
+    *fine = *fine && wait<false>(smem_addr(&bars->acc_empty[*acc]), *acc_phase ^ 1u, abort);
+    fence_after();
+    d = tmem + static_cast<uint32_t>(*acc * NT);
+    more = 0;
+  };
+  auto finish = [&]() {
+    commit<false>(smem_addr(&bars->acc_full[*acc]));
+    *acc ^= 1;
+    if (*acc == 0) *acc_phase ^= 1u;
+  };
+  begin();
+  for (int kb = 0, at = k0; *fine && kb < len * passes; ++kb) {
+    if (!wait<false>(smem_addr(&bars->full[*stage]), *ring_phase, abort)) {
+      *fine = false;
+      break;
+    }
+    fence_after();
+    const uint32_t sw = ring + *stage * (T::kWBytes + T::kHBytes);
+    const uint64_t dw = operand_desc(sw, MN), dh = operand_desc(sw + T::kWBytes, false);
+    const int64_t left = depth - static_cast<int64_t>(at) * kBK;
+    const bool cut = passes > 1 && kb >= len * (passes - 1);
+    if (++at == k0 + len) at = k0;
+#pragma unroll
+    for (int k = 0; k < kBK / 16; ++k) {
+      if (k * 16 >= left) break;
+      if (k % kCut == 0 && cut) {
+        finish();
+        begin();
+      }
+      if (!*fine) break;
+      mma_f16<false>(d, MN ? dw + k * (2048 >> 4) : dw + (k / 4) * (T::kWBytes / 2 >> 4) + (k % 4) * 2,
+                     dh + (k / 4) * (T::kHBytes / 2 >> 4) + (k % 4) * 2, T::kIdesc | (MN ? 1u << 15 : 0u), more);
+      more = 1;
+    }
+    if (!*fine) break;
+    commit<false>(smem_addr(&bars->empty[*stage]));
+    if (++*stage == T::kStages) {
+      *stage = 0;
+      *ring_phase ^= 1u;
+    }
+  }
+  if (*fine) finish();
+}
+
 template <int NT, bool KEEP>
 __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
     vocab_few_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabArgs g) {
@@ -1215,38 +1289,8 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
     if (lane == 0) {
       for (int t = blockIdx.x; fine && t < tiles; t += gridDim.x)
         for (int k0 = 0; fine && k0 < blocks; k0 += g.group) {
-          if (!wait<false>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
-            fine = false;
-            break;
-          }
-          fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * NT);
           const int len = min(g.group, blocks - k0);
-          for (int kb = 0, at = k0; kb < len * passes; ++kb) {
-            if (!wait<false>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
-              fine = false;
-              break;
-            }
-            fence_after();
-            const uint32_t sw = smem_addr(ring + stage * (T::kWBytes + T::kHBytes));
-            const uint64_t dw = operand_desc(sw, false), dh = operand_desc(sw + T::kWBytes, false);
-            const int left = g.d - at * kBK;
-            if (++at == k0 + len) at = k0;
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              if (k * 16 < left)
-                mma_f16<false>(d, dw + (k / 4) * (T::kWBytes / 2 >> 4) + (k % 4) * 2, dh + (k / 4) * (T::kHBytes / 2 >> 4) + (k % 4) * 2,
-                               T::kIdesc, (kb | k) != 0);
-            commit<false>(smem_addr(&bars->empty[stage]));
-            if (++stage == S) {
-              stage = 0;
-              ring_phase ^= 1u;
-            }
-          }
-          if (!fine) break;
-          commit<false>(smem_addr(&bars->acc_full[acc]));
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
+          few_products<NT, false>(bars, abort, tmem, smem_addr(ring), k0, len, passes, g.d, &stage, &ring_phase, &acc, &acc_phase, &fine);
         }
     }
   } else {
@@ -1270,13 +1314,14 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
-      if (g.group < blocks) {  // as in the other products: groups in registers, and back to TMEM with the last
+      const int sums = sums_of(0, blocks, g.group, passes, g.d);
+      if (sums > 1) {  // as in the other products: in registers, and back to TMEM with the last
         float z[NT];
 #pragma unroll
         for (int k = 0; k < NT; ++k) z[k] = 0.f;
-        for (int k0 = 0; k0 < blocks; k0 += g.group) {
+        for (int n = 1; n <= sums; ++n) {
           if (!acquire()) break;
-          const bool last = k0 + g.group >= blocks;
+          const bool last = n == sums;
 #pragma unroll
           for (int c = 0; c < NT; c += 32) {
             uint32_t r[32];
@@ -1474,37 +1519,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
         const int part = u / tiles, kb1 = first_block(part + 1);
         for (int k0 = first_block(part); fine && k0 < kb1;) {
           const int k1 = kb1 - k0 > g.group_h ? k0 + g.group_h : kb1;
-          if (!wait<false>(smem_addr(&bars->acc_empty[acc]), acc_phase ^ 1u, abort)) {
-            fine = false;
-            break;
-          }
-          fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * NT);
-          for (int kb = 0, at = k0; kb < (k1 - k0) * g.passes_h; ++kb) {
-            if (!wait<false>(smem_addr(&bars->full[stage]), ring_phase, abort)) {
-              fine = false;
-              break;
-            }
-            fence_after();
-            const uint32_t sw = smem_addr(ring + stage * (T::kWBytes + T::kHBytes));
-            const uint64_t dw = operand_desc(sw, true), du = operand_desc(sw + T::kWBytes, false);
-            const int64_t left = g.V - static_cast<int64_t>(at) * kBK;
-            if (++at == k1) at = k0;
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              if (k * 16 < left)
-                mma_f16<false>(d, dw + k * (2048 >> 4), du + (k / 4) * (T::kHBytes / 2 >> 4) + (k % 4) * 2, T::kIdesc | 1u << 15,
-                               (kb | k) != 0);
-            commit<false>(smem_addr(&bars->empty[stage]));
-            if (++stage == S) {
-              stage = 0;
-              ring_phase ^= 1u;
-            }
-          }
-          if (!fine) break;
-          commit<false>(smem_addr(&bars->acc_full[acc]));
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
+          few_products<NT, true>(bars, abort, tmem, smem_addr(ring), k0, k1 - k0, g.passes_h, g.V, &stage, &ring_phase, &acc, &acc_phase, &fine);
           k0 = k1;
         }
       }
@@ -1516,7 +1531,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
       float z[NT];
 #pragma unroll
       for (int k = 0; k < NT; ++k) z[k] = 0.f;
-      for (int k0 = first_block(part); k0 < kb1; k0 = kb1 - k0 > g.group_h ? k0 + g.group_h : kb1) {
+      for (int n = sums_of(first_block(part), kb1, g.group_h, g.passes_h, g.V); n; --n) {
         if (!__all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
           fine = false;
           break;
@@ -2093,7 +2108,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
   VocabMaps maps;
   const int64_t ldw = g.Wp ? g.dp : s.d, ldh = g.hp ? g.dp : s.d;
   if (!vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
-  const bool groups = g.group < (s.d + kBK - 1) / kBK;
+  const bool groups = sums_of(0, (s.d + kBK - 1) / kBK, g.group, passes_of(g.np_h, g.np_w), s.d) > 1;
   auto split_blocks = [&](int64_t rows) { return (rows * (g.dp / 8) + kPrepThreads - 1) / kPrepThreads; };
   for (int64_t row0 = 0; row0 < s.N; row0 += g.Nc) {
     g.row0 = row0;
