@@ -156,6 +156,16 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
       : "r"(addr));
 }
 
+// 16 of them.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+
 // The same 32 columns from registers (after tmem_stored, this warp's loads see them).
 __device__ __forceinline__ void tmem_store(uint32_t addr, const float* r) {
   asm volatile(

@@ -81,18 +81,20 @@ constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: 
 // A tensor core cuts what falls below its sum where an fp32 addition rounds, so a sum's error grows with its length, to
 // one side: 1.4e-6 of the logits at d = 2560, 4e-6 with the six products of fp32 operands. Where an fp32 result comes
 // of it, sums longer than kGroup k-blocks are made in groups, which the epilogue adds up in registers. Products of pieces
-// run from the smallest to the largest, k-block by k-block, and of the largest every kCut instructions (of 16 k) make a sum of
-// their own, so that next to nothing is cut: fp32 gradients at 512 x 1024 x 96 1.2e-5 off in one sum, 1.5e-6 a k-block, CUT_ERROR so.
+// run from the smallest to the largest, k-block by k-block, and of the largest every few instructions (of 16 k) make a sum of
+// their own, so that next to nothing is cut. With 2, 4 and 8 of them everywhere: 512 x 1024 x 96 in fp32 41, 39 and 37.5 us, its
+// gradients 6e-7, 1.3e-6 and 1.7e-6 off; 3001 x 32,003 x 515 with an fp32 dW 763, 681 and 640 us. The logits' errors count most,
+// as exp makes them relative ones: 2 for them and where the six products of a gradient hide it, 4 where there are three.
 constexpr int kGroup = 10;               // (80 additions: 7e-7)
 constexpr int kGroupPieces = 1;          // fp32 operands or gradients
-constexpr int kCut = 2;
+__host__ __device__ __forceinline__ int cut_of(bool logits, int passes) { return logits || passes >= 6 ? 2 : 4; }
 
 // How many sums a tile's product along k-blocks [kb0, kb1) of `depth` is made of.
-__host__ __device__ __forceinline__ int sums_of(int kb0, int kb1, int group, int passes, int64_t depth) {
+__host__ __device__ __forceinline__ int sums_of(int kb0, int kb1, int group, int passes, int64_t depth, int cut) {
   if (passes == 1) return group < kb1 - kb0 ? (kb1 - kb0 + group - 1) / group : 1;
   const int64_t left = (depth - static_cast<int64_t>(kb1 - 1) * kBK + 15) / 16;  // instructions of the last k-block
   const int steps = left < kBK / 16 ? static_cast<int>(left) : kBK / 16;
-  return (kb1 - kb0 - 1) * (1 + kBK / 16 / kCut) + 1 + (steps + kCut - 1) / kCut;
+  return (kb1 - kb0 - 1) * (1 + kBK / 16 / cut) + 1 + (steps + cut - 1) / cut;
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -979,12 +981,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sp = smem_addr(ring + stage * (2 * kOperandBytes));
             const uint64_t dp = operand_desc(sp, w.p_mn), dq = operand_desc(sp + kOperandBytes, w.q_mn);
             const int64_t left = w.depth - static_cast<int64_t>(at) * kBK;  // (what is behind it is zero)
-            const bool cut = GROUPS && w.passes > 1 && kb >= blocks - len;
+            const int cut = GROUPS && w.passes > 1 && kb >= blocks - len ? cut_of(KIND != kGrads, w.passes) : 0;
             if (++at == k0 + len) at = k0;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k) {
               if (k * 16 >= left) break;
-              if (k % kCut == 0 && cut) {
+              if (cut && (k & (cut - 1)) == 0) {
                 finish();
                 begin();
               }
@@ -1049,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
-      const int sums = GROUPS ? sums_of(w.kb0, w.kb1, w.group, w.passes, w.depth) : 1;
+      const int sums = GROUPS ? sums_of(w.kb0, w.kb1, w.group, w.passes, w.depth, cut_of(KIND != kGrads, w.passes)) : 1;
       if (GROUPS && sums > 1) {
         // all but the last in registers; the last goes back to TMEM with the others added
         float z[128];
@@ -1058,13 +1060,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 1; k < sums; ++k) {
           if (!acquire()) break;
           const uint32_t from = warp_from + static_cast<uint32_t>(acc * kTile);
+          uint32_t r[2][16];  // 16 columns come while the 16 before are added
+          tmem_load16(from, r[0]);
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t r[32];
-            tmem_load(from + ch * 32, r);
-            tmem_wait(r);
+          for (int ch = 0; ch < 8; ++ch) {
+            tmem_wait(r[ch & 1]);
+            if (ch < 7) tmem_load16(from + (ch + 1) * 16, r[(ch + 1) & 1]);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) z[ch * 32 + k] += __uint_as_float(r[k]);
+            for (int k = 0; k < 16; ++k) z[ch * 16 + k] += __uint_as_float(r[ch & 1][k]);
           }
           release();
         }
@@ -1196,12 +1199,12 @@ __device__ __forceinline__ void few_products(FewBars<NT>* bars, volatile int* ab
     const uint32_t sw = ring + *stage * (T::kWBytes + T::kHBytes);
     const uint64_t dw = operand_desc(sw, MN), dh = operand_desc(sw + T::kWBytes, false);
     const int64_t left = depth - static_cast<int64_t>(at) * kBK;
-    const bool cut = passes > 1 && kb >= len * (passes - 1);
+    const int cut = passes > 1 && kb >= len * (passes - 1) ? cut_of(!MN, passes) : 0;
     if (++at == k0 + len) at = k0;
 #pragma unroll
     for (int k = 0; k < kBK / 16; ++k) {
       if (k * 16 >= left) break;
-      if (k % kCut == 0 && cut) {
+      if (cut && (k & (cut - 1)) == 0) {
         finish();
         begin();
       }
@@ -1314,7 +1317,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
-      const int sums = sums_of(0, blocks, g.group, passes, g.d);
+      const int sums = sums_of(0, blocks, g.group, passes, g.d, cut_of(true, passes));
       if (sums > 1) {  // as in the other products: in registers, and back to TMEM with the last
         float z[NT];
 #pragma unroll
@@ -1531,7 +1534,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
       float z[NT];
 #pragma unroll
       for (int k = 0; k < NT; ++k) z[k] = 0.f;
-      for (int n = sums_of(first_block(part), kb1, g.group_h, g.passes_h, g.V); n; --n) {
+      for (int n = sums_of(first_block(part), kb1, g.group_h, g.passes_h, g.V, cut_of(false, g.passes_h)); n; --n) {
         if (!__all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort))) {
           fine = false;
           break;
@@ -2108,7 +2111,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
   VocabMaps maps;
   const int64_t ldw = g.Wp ? g.dp : s.d, ldh = g.hp ? g.dp : s.d;
   if (!vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
-  const bool groups = sums_of(0, (s.d + kBK - 1) / kBK, g.group, passes_of(g.np_h, g.np_w), s.d) > 1;
+  const bool groups = sums_of(0, (s.d + kBK - 1) / kBK, g.group, passes_of(g.np_h, g.np_w), s.d, 2) > 1;
   auto split_blocks = [&](int64_t rows) { return (rows * (g.dp / 8) + kPrepThreads - 1) / kPrepThreads; };
   for (int64_t row0 = 0; row0 < s.N; row0 += g.Nc) {
     g.row0 = row0;
