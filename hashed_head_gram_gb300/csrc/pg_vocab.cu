@@ -1946,8 +1946,9 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
       float* to = reinterpret_cast<float*>(take(4ll * kTile * s.d * std::max({some, few, int64_t{1}})));
       if (g->q > 1 || g->few_h) g->parts = to;
     }
-    if (has_w && kn >= 4) {
-      float* to = reinterpret_cast<float*>(take(4ll * s.V * s.d * std::min({int64_t{kMaxParts}, kn / 2, kPartTiles / (widest * g->nd)})));
+    const int64_t parts_w = std::min({int64_t{kMaxParts}, kn / 2, kPartTiles / (widest * g->nd)});
+    if (has_w && parts_w > 1) {  // (one part goes where the gradient goes)
+      float* to = reinterpret_cast<float*>(take(4ll * s.V * s.d * parts_w));
       if (g->q_w > 1) g->parts_w = to;
     }
   }
