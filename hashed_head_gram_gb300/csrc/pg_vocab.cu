@@ -579,6 +579,7 @@ __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps
   const bool some_dead = KEEP && __any_sync(0xffffffffu, dead);
   uint64_t sum[2] = {0, 0};
   if (KEEP && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // of an earlier tile
+  __syncwarp();
   uint32_t r[2][32];
   tmem_load(from, r[0]);
 #pragma unroll
@@ -632,6 +633,7 @@ __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps
         fence_async_smem();
         __syncwarp();
         if (lane == 0) store_box(&maps.Ust, smem_addr(buf), static_cast<int>(c0), row0, p);
+        __syncwarp();  // (TMEM's loads and waits want all lanes at once)
       }
     }
   }
@@ -684,8 +686,8 @@ __device__ __noinline__ void keep_listed(const VocabArgs& g, uint8_t* s_row, uin
         if (at >= 32) break;
         g.zk[row + listed.e] = *reinterpret_cast<const float*>(s_row + lane * 128 + ((at >> 2 ^ (lane & 7)) << 4) + (at & 3) * 4) * g.k2;
       }
+      __syncwarp();
     }
-    __syncwarp();
     return;
   }
   while (__any_sync(0xffffffffu, listed.e < listed.end)) {  // one a row at a time
@@ -822,6 +824,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabMap
       fence_async_smem();
       __syncwarp();
       if (lane == 0) store_box(dh ? &maps.Gh : &maps.Gw, smem_addr(buf), c0, row0, 0);
+      __syncwarp();
     }
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     return;
@@ -876,6 +879,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabMap
         else static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(v);
       }
     }
+    __syncwarp();
   }
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
