@@ -30,7 +30,8 @@
 //
 // The products: 256 x 256 tiles on CTA pairs (tcgen05, cta_group::2), 128-deep k-blocks of both operands by
 // TMA into a ring of three, two accumulators in TMEM, eight epilogue warps. Up to 128 rows, where reading W is all that
-// counts, the first product and dh have kernels of their own in which W's rows and columns are the tile's rows.
+// counts, the first product and dh have kernels of their own in which W's rows and columns are the tile's rows; up to 8
+// rows of an fp32 W, kernels of fp32 FMAs.
 //
 // Bound by the tensor cores, and in long calls by the power limit (the measured bf16 rate: 1914 TFLOP/s for a short
 // product, 1721 for seconds of them). 16,384 x 50,304 x 768: 734-753 us, 1.68-1.72 PFLOP/s. With gradients, 65,536 x 50,304 x 768:
@@ -64,6 +65,9 @@ constexpr int kPartTiles = 640;            // tiles that they come to, at most
 constexpr int kMaxForwardRows = 16384;   // h of that many rows stays in L2 while W passes by
 
 constexpr int kPrepThreads = 256;
+constexpr int kFewTable = 1024;           // above it dh of few rows is made by itself
+constexpr int kSmallRows = 8;             // up to here an fp32 W takes FMAs in place of products of pieces
+constexpr int kSmallThreads = 256;
 constexpr int kFewRows = 128;             // up to here the first product has W's rows for its tiles' rows
 constexpr int kTile = 256;
 constexpr int kThreads = 384;            // warps 0 and 1 issue copies and products, 4 to 11 are the epilogue's
@@ -150,6 +154,7 @@ struct VocabArgs {
   int twice;                             // U is made once lse is there, by the logits again
   int tma_h, tma_w;                      // tiles of dh, dW go out by TMA
   int few_h;                             // dh is made for few rows
+  int small;                             // few rows and an fp32 W: FMAs
   int at_log;                            // log2 of the tokens that a place of `at` stands for
   int segs;                              // sums a row
 };
@@ -1227,6 +1232,67 @@ __device__ __forceinline__ void few_products(FewBars<NT>* bars, volatile int* ab
   if (*fine) finish();
 }
 
+// A warp's segment of 32 rows of W (a lane each) and 32 rows of h from c0 on, with the logits in r: keeps listed tokens' logits
+// and (keep) the segment's part of U, and gives lane k the reference and sum of row c0 + k. z is the warp's shared memory.
+__device__ __forceinline__ float2 segment_sum(const VocabArgs& g, bool keep, const uint32_t (&r)[32], float (*z)[33], const float* s_c, int c0,
+                                              int64_t v0, int e, int end) {
+  const int lane = threadIdx.x & 31, row = c0 + lane;
+  const bool in = v0 + lane < g.V;
+  auto s_u = reinterpret_cast<uint16_t(*)[40]>(&z[0][0]);  // rows of 80 bytes
+  const float c = s_c[row];
+  const bool alive = c != INFINITY;
+  if (__any_sync(0xffffffffu, e < end)) {  // each lane looks its row's tokens up in what the others have
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) z[k][lane] = __uint_as_float(r[k]);
+    __syncwarp();
+    for (const int64_t row_at = static_cast<int64_t>(row) * g.K; e < end; ++e) {
+      const int64_t from_v0 = g.sorted[row_at + e] - v0;
+      if (from_v0 >= 0 && from_v0 < 32) g.zk[row_at + e] = z[lane][from_v0] * g.k2;
+    }
+    __syncwarp();
+  }
+  float ref = c, sum;
+#pragma unroll 1
+  for (int again = 0; again < 2; ++again) {
+    float x[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float to = again ? __shfl_sync(0xffffffffu, ref, k) : s_c[c0 + k];
+      x[k] = in ? exp2_fast(fmaf(__uint_as_float(r[k]), g.k2, -to)) : 0.f;
+    }
+    if (keep) {
+      for (int p = 0; p < g.np_u; ++p) {
+        float y[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = x[k];
+        for (int q = 0; q < p; ++q)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) take_piece(y[k]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s_u[k][lane] = s_c[c0 + k] == INFINITY ? 0 : take_piece(y[k]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int to = k * 8 + lane / 4;
+          if (c0 + to < g.rows)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(g.U) + (static_cast<int64_t>(p) * g.Nc + c0 + to) * g.Vp + v0 +
+                                      lane % 4 * 8) = *reinterpret_cast<const uint4*>(&s_u[to][lane % 4 * 8]);
+        }
+      }
+    }
+    sum = reduce_columns(x, [](float a, float b) { return a + b; });
+    const bool over = !again && alive && !(sum <= kSumLimit);
+    if (!__any_sync(0xffffffffu, over)) break;  // else: logits far above the targets', the segment's largest for a reference
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = in ? __uint_as_float(r[k]) * g.k2 : -INFINITY;
+    const float top = reduce_columns(x, [](float a, float b) { return fmaxf(a, b); });
+    if (over) ref = top == -INFINITY ? 0.f : top;
+  }
+  return make_float2(ref, sum);
+}
+
 template <int NT, bool KEEP>
 __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
     vocab_few_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabArgs g) {
@@ -1237,8 +1303,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
   __shared__ FewBars<NT> bars_s;
   __shared__ float s_c[NT];
   __shared__ float2 s_all[4][KEEP ? 1 : NT];
-  __shared__ __align__(16) float s_z[4][32][33];  // a warp's logits, or its part of U in rows of 80 bytes
-  auto s_u = [&](int w) { return reinterpret_cast<uint16_t(*)[40]>(&s_z[w][0][0]); };
+  __shared__ __align__(16) float s_z[4][32][33];
   FewBars<NT>* bars = &bars_s;
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1307,7 +1372,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
       __syncwarp();
     }
     for (int t = blockIdx.x; fine && t < tiles; t += gridDim.x) {
-      const int64_t v0 = t * 128ll + quarter * 32, v = v0 + lane;
+      const int64_t v0 = t * 128ll + quarter * 32;
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
       auto acquire = [&]() {
         fine = __all_sync(0xffffffffu, wait_inline<false>(smem_addr(&bars->acc_full[acc]), acc_phase, abort));
@@ -1345,7 +1410,6 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
       } else if (!acquire()) {
         break;
       }
-      const bool in = v < g.V;
       const int64_t seg = v0 >> 5;
       // 32 rows of h at a time. (Unrolled over all of them the code ran out of the instruction cache: 64 x 50,304 x 768 with
       // U 92 us.)
@@ -1354,68 +1418,17 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
         uint32_t r[32];
         tmem_load(from + static_cast<uint32_t>(acc * NT + c0), r);
         const int row = c0 + lane;  // the row of h whose sum this lane gets
-        const float c = s_c[row];
-        const bool alive = c != INFINITY;
         int e = 0, end = 0;
         if (g.ids && row < g.rows) {
           e = g.at[static_cast<int64_t>(t) * g.Nc + row];  // (the four warps' tokens)
           end = g.at[(t + 1ll) * g.Nc + row];
         }
         tmem_wait(r);
-        if (__any_sync(0xffffffffu, e < end)) {  // each lane looks its row's tokens up in what the others have
-          float(*z)[33] = s_z[warp - 2];
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) z[k][lane] = __uint_as_float(r[k]);
-          __syncwarp();
-          for (const int64_t row_at = static_cast<int64_t>(row) * g.K; e < end; ++e) {
-            const int64_t from_v0 = g.sorted[row_at + e] - v0;
-            if (from_v0 >= 0 && from_v0 < 32) g.zk[row_at + e] = z[lane][from_v0] * g.k2;
-          }
-          __syncwarp();
-        }
-        float ref = c, sum;
-#pragma unroll 1
-        for (int again = 0; again < 2; ++again) {
-          float x[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float to = again ? __shfl_sync(0xffffffffu, ref, k) : s_c[c0 + k];
-            x[k] = in ? exp2_fast(fmaf(__uint_as_float(r[k]), g.k2, -to)) : 0.f;
-          }
-          if (KEEP) {
-            for (int p = 0; p < g.np_u; ++p) {
-              float y[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = x[k];
-              for (int q = 0; q < p; ++q)
-#pragma unroll
-                for (int k = 0; k < 32; ++k) take_piece(y[k]);
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) s_u(warp - 2)[k][lane] = s_c[c0 + k] == INFINITY ? 0 : take_piece(y[k]);
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int to = k * 8 + lane / 4;
-                if (c0 + to < g.rows)
-                  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(g.U) + (static_cast<int64_t>(p) * g.Nc + c0 + to) * g.Vp + v0 +
-                                            lane % 4 * 8) = *reinterpret_cast<const uint4*>(&s_u(warp - 2)[to][lane % 4 * 8]);
-              }
-            }
-          }
-          sum = reduce_columns(x, [](float a, float b) { return a + b; });
-          const bool over = !again && alive && !(sum <= kSumLimit);
-          if (!__any_sync(0xffffffffu, over)) break;  // else: logits far above the targets', the segment's largest for a reference
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = in ? __uint_as_float(r[k]) * g.k2 : -INFINITY;
-          const float top = reduce_columns(x, [](float a, float b) { return fmaxf(a, b); });
-          if (over) ref = top == -INFINITY ? 0.f : top;
-        }
+        const float2 got = segment_sum(g, KEEP, r, s_z[warp - 2], s_c, c0, v0, e, end);
         if (KEEP) {
-          if (row < g.rows) g.sums[seg * g.Nc + row] = make_float2(ref, sum);
+          if (row < g.rows) g.sums[seg * g.Nc + row] = got;
         } else {
-          s_all[warp - 2][row] = joined(s_all[warp - 2][row], make_float2(ref, sum));
+          s_all[warp - 2][row] = joined(s_all[warp - 2][row], got);
         }
       }
       release();
@@ -1591,6 +1604,195 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
   fence_before();
   __syncthreads();
   if (warp == 1) tmem_free<false>(tmem, 2 * NT);
+}
+
+// ------------------------------------------------------------- rows so few that fp32 additions keep up with W
+
+// A lane's four of 128 columns of a row from c0 on, zeros behind its end: neighbours, or (not VEC) 32 apart, so that a warp's
+// loads are lines either way. W's do not stay in the L1 cache, which h has to itself.
+template <bool VEC>
+__device__ __forceinline__ int column_of(int k) {
+  const int lane = threadIdx.x & 31;
+  return VEC ? lane * 4 + k : lane + 32 * k;
+}
+
+template <bool VEC>
+__device__ __forceinline__ float4 four_of(const float* row, int c0, int d) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int c = c0 + column_of<VEC>(0);
+  if (VEC) {
+    if (c < d)
+      asm("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(row + c));
+  } else {
+    if (c < d) v.x = __ldg(row + c);
+    if (c + 32 < d) v.y = __ldg(row + c + 32);
+    if (c + 64 < d) v.z = __ldg(row + c + 64);
+    if (c + 96 < d) v.w = __ldg(row + c + 96);
+  }
+  return v;
+}
+
+template <int HT, bool VEC>
+__device__ __forceinline__ float4 four_of_h(const VocabArgs& g, int row, int c0) {
+  const int c = c0 + column_of<VEC>(0);
+  const int64_t at = static_cast<int64_t>(row) * g.d + c;
+  if (VEC && c >= g.d) return make_float4(0.f, 0.f, 0.f, 0.f);
+  if (VEC && HT == PG_F32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(g.h) + at));
+  float x[4] = {};
+  if (VEC) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(g.h) + at));
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float y[1] = {0.f};
+      if (c + 32 * k < g.d) load_cols<HT, 1>(g.h, at + 32 * k, y);
+      x[k] = y[0];
+    }
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// The first product of an fp32 W with up to 8 rows of h, in fp32 FMAs: W is read once, as it is, and no pieces of it are made.
+// A warp has a segment of 32 rows of W, four of them at a time, its lanes along d (both halves of a packed FMA along d, too);
+// h comes from the L1 cache. Bound by the loads under way: 8 x 128,000 x 2560 347 us, 3.8 TB/s (in pieces 1120, of which 477
+// make them and 640 the six products, whose sums in TMEM follow one another), 8 x 10,000 x 768 39 us (49). Sixteen rows, two of
+// W at a time, take longer than pieces unless W is far larger than L2 (16 x 10,000 x 768 76 us and 49).
+template <int HT, bool VEC>
+__global__ void __launch_bounds__(kSmallThreads, 2) vocab_small_kernel(const __grid_constant__ VocabArgs g, int keep) {
+  constexpr int NB = kSmallRows, R = 32 / NB, kWarps = kSmallThreads / 32;
+  __shared__ float s_c[32];
+  __shared__ __align__(16) float s_z[kWarps][32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (threadIdx.x < 32) s_c[threadIdx.x] = threadIdx.x < g.rows ? g.c[threadIdx.x] : INFINITY;
+  __syncthreads();
+  const int segs = static_cast<int>((g.V + 31) / 32);
+  const float* W = static_cast<const float*>(g.W);
+  float(*z)[33] = s_z[warp];
+  for (int seg = warp * gridDim.x + blockIdx.x; seg < segs; seg += gridDim.x * kWarps) {
+    const int64_t v0 = seg * 32ll;
+#pragma unroll 1
+    for (int i = 0; i < NB; ++i) {  // (rows past V are read as the last one, and left out by the sums)
+      const float* rows[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) rows[k] = W + min(v0 + i * R + k, g.V - 1) * g.d;
+      uint64_t sum[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) sum[k] = 0;
+      float4 w[R], next[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) w[k] = four_of<VEC>(rows[k], 0, g.d);
+#pragma unroll 2
+      for (int c = 0; c < g.d; c += 128) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) next[k] = four_of<VEC>(rows[k], c + 128, g.d);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const float4 x = four_of_h<HT, VEC>(g, min(n, g.rows - 1), c);
+#pragma unroll
+          for (int k = 0; k < R; ++k) {
+            sum[k * NB + n] = fma2(pk(w[k].x, w[k].y), pk(x.x, x.y), sum[k * NB + n]);
+            sum[k * NB + n] = fma2(pk(w[k].z, w[k].w), pk(x.z, x.w), sum[k * NB + n]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) w[k] = next[k];
+      }
+      float x[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        float lo, hi;
+        upk(sum[k], lo, hi);
+        x[k] = lo + hi;
+      }
+      __syncwarp();
+      z[lane % NB][i * R + lane / NB] = reduce_columns(x, [](float a, float b) { return a + b; });
+    }
+    __syncwarp();
+    uint32_t r[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = k < NB ? __float_as_uint(z[k][lane]) : 0u;
+    __syncwarp();
+    int e = 0, end = 0;
+    if (g.ids && lane < g.rows) {
+      e = g.at[(v0 >> g.at_log) * g.Nc + lane];
+      end = g.at[((v0 >> g.at_log) + 1) * g.Nc + lane];
+    }
+    const float2 got = segment_sum(g, keep, r, z, s_c, 0, v0, e, end);
+    if (lane < g.rows) g.sums[static_cast<int64_t>(seg) * g.Nc + lane] = got;
+    __syncwarp();
+  }
+}
+
+// dh's parts likewise: a warp has 128 columns of W (four a lane) and every eighth 32 rows of the part, with their U in its shared
+// memory; the block's warps add up in turn. 8 x 128,000 x 2560 347 us (pieces 620).
+template <bool VEC>
+__global__ void __launch_bounds__(kSmallThreads, 2) vocab_small_grad_kernel(const __grid_constant__ VocabArgs g) {
+  constexpr int NB = kSmallRows, kWarps = kSmallThreads / 32, kFly = 8;
+  __shared__ __align__(16) float s_u[kWarps][32][NB];
+  __shared__ __align__(16) float s_sum[NB][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tiles = (g.d + 127) / 128, part = blockIdx.x / tiles, first = (blockIdx.x - part * tiles) * 128;
+  const int64_t all = (g.V + kBK - 1) / kBK, begin = all * part / g.q * kBK, end = min(all * (part + 1) / g.q * kBK, g.V);
+  const int np_u = g.gh_dtype == PG_F32 ? g.np_u : 1;
+  const float* W = static_cast<const float*>(g.W);
+  uint64_t sum[NB][2];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) sum[n][0] = sum[n][1] = 0;
+  for (int64_t v0 = begin + warp * 32; v0 < end; v0 += kWarps * 32) {
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      float u = 0.f;
+      if (n < g.rows && v0 + lane < end)
+        for (int p = 0; p < np_u; ++p) u += __bfloat162float(g.U[(static_cast<int64_t>(p) * g.Nc + n) * g.Vp + v0 + lane]);
+      s_u[warp][lane][n] = u;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32 && v0 + k0 < end; k0 += kFly) {
+      float4 w[kFly];
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (v0 + k0 + k < end) w[k] = four_of<VEC>(W + (v0 + k0 + k) * g.d, first, g.d);
+      }
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+#pragma unroll
+        for (int n = 0; n < NB; n += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(&s_u[warp][k0 + k][n]);
+          const float* each = &u.x;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            sum[n + m][0] = fma2(pk(w[k].x, w[k].y), pk(each[m], each[m]), sum[n + m][0]);
+            sum[n + m][1] = fma2(pk(w[k].z, w[k].w), pk(each[m], each[m]), sum[n + m][1]);
+          }
+        }
+      }
+    }
+  }
+  for (int turn = 0; turn < kWarps; ++turn) {
+    if (turn == warp) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        float v[4];
+        upk(sum[n][0], v[0], v[1]);
+        upk(sum[n][1], v[2], v[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_sum[n][column_of<VEC>(k)] = turn ? s_sum[n][column_of<VEC>(k)] + v[k] : v[k];
+      }
+    }
+    __syncthreads();
+  }
+  float* to = g.parts + static_cast<int64_t>(part) * g.Nc * g.d;
+  for (int k = threadIdx.x; k < g.rows * 128; k += kSmallThreads)
+    if (first + k % 128 < g.d) to[static_cast<int64_t>(k / 128) * g.d + first + k % 128] = s_sum[k / 128][k % 128];
 }
 
 // ------------------------------------------------------------------- rows, once their sums are there
@@ -1837,7 +2039,7 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
   g->passes_w = g->gw_dtype == PG_F32 ? passes_of(g->np_u, g->np_f) : 1;
   g->group_h = g->gh_dtype == PG_F32 ? kGroupPieces : 1 << 30;  // (a bf16 gradient's own rounding is far above)
   g->group_w = g->gw_dtype == PG_F32 ? kGroupPieces : 1 << 30;
-  if (has_h && g->N <= kFewRows && kv > 8) {
+  if (has_h && g->N <= kFewRows && g->V > kFewTable) {
     // few rows: dh by itself, in as many parts as fill the SMs once or twice (a table of a few k-blocks: with dW)
     const int tiles = (g->d + 127) / 128;
     double best = -1;
@@ -1904,6 +2106,7 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->twice = s.grad && s.gw_dtype == PG_F32 && s.h_dtype == PG_BF16 && s.w_dtype == PG_BF16 && !is_few;
   const int np_f = s.gw_dtype == PG_F32 ? 3 : 1;
   g->np_f = g->twice ? 1 : np_f;
+  g->small = s.N <= kSmallRows && s.w_dtype == PG_F32 && (!has_h || s.V > kFewTable);
   const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 ? kGroupPieces : kGroup;
   const int groups = (blocks + longest - 1) / longest;
   g->group = (blocks + groups - 1) / groups;
@@ -1921,8 +2124,8 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   const int64_t chunks = (s.N + most - 1) / most;
   g->Nc = static_cast<int>(((s.N + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
   const int64_t rows = std::min(most, (s.N + kTile - 1) / kTile * kTile);  // room for these (Nc of them or more)
-  g->Wp = needs_copy(s.w_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_w * s.V * g->dp)) : nullptr;
-  g->hp = needs_copy(s.h_dtype, s.d) ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * rows * g->dp)) : nullptr;
+  g->Wp = needs_copy(s.w_dtype, s.d) && !g->small ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_w * s.V * g->dp)) : nullptr;
+  g->hp = needs_copy(s.h_dtype, s.d) && !g->small ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * rows * g->dp)) : nullptr;
   // (narrower tiles are kPlanUnits at most, for a chunk of kTile rows; few rows have a sum for 32 columns, or four a CTA of 128)
   g->sums = reinterpret_cast<float2*>(take(16 * std::max({widest * rows, static_cast<int64_t>(kPlanUnits) * kTile,
                                                           std::max((s.V + 63) / 64, 2 * ((s.V + 127) / 128)) * kTile})));
@@ -2091,6 +2294,23 @@ pg_status launch_few_grad(const VocabMaps& maps, const VocabArgs& g, cudaStream_
   return launch_next(vocab_few_grad_kernel<NT>, blocks, Few<NT>::kThreads, Few<NT>::kSmem, false, true, stream, maps, g);
 }
 
+// Two blocks an SM, as the kernel's registers allow, or as many as there are segments for.
+template <int HT, bool VEC>
+pg_status launch_small_of(const VocabArgs& g, bool keep, cudaStream_t stream) {
+  const int64_t blocks = std::min<int64_t>(2 * sm_count(), (g.V + 31) / 32);
+  return launch_next(vocab_small_kernel<HT, VEC>, blocks, kSmallThreads, 0, false, true, stream, g, static_cast<int>(keep));
+}
+
+pg_status launch_small(const VocabArgs& g, bool keep, bool vec, cudaStream_t stream) {
+  if (g.h_dtype == PG_F32) return vec ? launch_small_of<PG_F32, true>(g, keep, stream) : launch_small_of<PG_F32, false>(g, keep, stream);
+  return vec ? launch_small_of<PG_BF16, true>(g, keep, stream) : launch_small_of<PG_BF16, false>(g, keep, stream);
+}
+
+pg_status launch_small_grad(const VocabArgs& g, bool vec, cudaStream_t stream) {
+  return launch_next(vec ? vocab_small_grad_kernel<true> : vocab_small_grad_kernel<false>, static_cast<int64_t>((g.d + 127) / 128) * g.q,
+                     kSmallThreads, 0, false, true, stream, g);
+}
+
 using PrepareFn = void (*)(const VocabArgs, int, int);
 using ArgsFn = void (*)(const VocabArgs);
 
@@ -2110,12 +2330,13 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
   pg_status st;
   const bool list = g.ids != nullptr;
   const bool vec_h = s.d % 8 == 0 && aligned(g.h, vec_bytes(s.h_dtype)), vec = vec_h && aligned(g.W, vec_bytes(s.w_dtype));
+  const bool vec_four = s.d % 4 == 0 && aligned(g.W, 16) && aligned(g.h, 4 * dtype_bytes(s.h_dtype));
   const PrepareFn prepare = s.h_dtype == PG_F32
       ? (s.w_dtype == PG_F32 ? prepare_fn<PG_F32, PG_F32>(list, vec) : prepare_fn<PG_F32, PG_BF16>(list, vec))
       : (s.w_dtype == PG_F32 ? prepare_fn<PG_BF16, PG_F32>(list, vec) : prepare_fn<PG_BF16, PG_BF16>(list, vec));
   VocabMaps maps;
   const int64_t ldw = g.Wp ? g.dp : s.d, ldh = g.hp ? g.dp : s.d;
-  if (!vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
+  if (!g.small && !vocab_map(&maps.W, g.Wp ? g.Wp : g.W, g.np_w, s.V, s.d, ldw, s.V, kLine, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
   const bool groups = sums_of(0, (s.d + kBK - 1) / kBK, g.group, passes_of(g.np_h, g.np_w), s.d, 2) > 1;
   auto split_blocks = [&](int64_t rows) { return (rows * (g.dp / 8) + kPrepThreads - 1) / kPrepThreads; };
   for (int64_t row0 = 0; row0 < s.N; row0 += g.Nc) {
@@ -2130,7 +2351,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     if (st != PG_OK) return st;
     const uint8_t* h = static_cast<const uint8_t*>(g.h) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.h_dtype));
     const int few = s.N > kFewRows ? 0 : s.N > 64 ? 128 : s.N > 32 ? 64 : 32;
-    if (!vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, kLine, few ? few : 128,
+    if (!g.small && !vocab_map(&maps.h, g.hp ? static_cast<const void*>(g.hp) : h, g.np_h, g.rows, s.d, ldh, g.rows, kLine, few ? few : 128,
                    CU_TENSOR_MAP_SWIZZLE_128B))
       return PG_ERR_CUDA;
     const int64_t jobs = static_cast<int64_t>((g.rows + kTile - 1) / kTile) * ((s.V + g.wide - 1) / g.wide);
@@ -2141,7 +2362,8 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
         return PG_ERR_CUDA;
       if (!g.F) maps.F = maps.U;
       maps.Ufew = maps.Gh = maps.Gw = maps.U;
-      if (g.few_h && !vocab_map(&maps.Ufew, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, kLine, few, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
+      if (g.small) maps.h = maps.W = maps.U;
+      if (g.few_h && !g.small && !vocab_map(&maps.Ufew, g.U, g.np_u, g.rows, s.V, g.Vp, g.Nc, kLine, few, CU_TENSOR_MAP_SWIZZLE_128B)) return PG_ERR_CUDA;
       // tiles that nothing is added to, of matrices that TMA can step over
       auto out_map = [&](CUtensorMap* map, void* dst, int dtype, int64_t rows) {
         const bool f32 = dtype == PG_F32;
@@ -2154,9 +2376,11 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
                     ? out_map(&maps.Gh, static_cast<uint8_t*>(g.gh) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.gh_dtype)), s.gh_dtype, g.rows) : 0;
       if (g.tma_w < 0 || g.tma_h < 0) return PG_ERR_CUDA;
     } else {
-      maps.U = maps.Ust = maps.F = maps.Ufew = maps.Gh = maps.Gw = maps.h;
+      maps.U = maps.Ust = maps.F = maps.Ufew = maps.Gh = maps.Gw = maps.h;  // (small: no map is looked at)
     }
-    if (few)
+    if (g.small)
+      st = launch_small(g, s.grad, vec_four, stream);
+    else if (few)
       st = few == 32 ? launch_few<32>(maps, g, s.grad, stream) : few == 64 ? launch_few<64>(maps, g, s.grad, stream)
                                                                              : launch_few<128>(maps, g, s.grad, stream);
     else if (s.grad && !g.twice)
@@ -2164,7 +2388,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     else
       st = groups ? launch_product<kSums, true>(maps, g, jobs, stream) : launch_product<kSums, false>(maps, g, jobs, stream);
     if (st != PG_OK) return st;
-    g.segs = few && !s.grad ? static_cast<int>(4 * few_blocks(g.V)) : static_cast<int>((g.V + g.seg - 1) / g.seg);
+    g.segs = few && !s.grad && !g.small ? static_cast<int>(4 * few_blocks(g.V)) : static_cast<int>((g.V + g.seg - 1) / g.seg);
     st = launch_next(rows_fn(s.grad, s.h_dtype, vec_h), (g.rows + kRowsPer - 1) / kRowsPer, 32 * kRowWarps, 0, false, true, stream, g);
     if (st != PG_OK) return st;
     if (g.twice) {
@@ -2175,7 +2399,9 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
     VocabArgs b = g;
     if (g.tiles2) b.tiles2 = (g.rows + kTile - 1) / kTile * g.nd;  // a last chunk has fewer rows
     b.q_w = std::min(g.q_w, (g.rows + kBK - 1) / kBK);             // (no part without a k-block)
-    if (g.few_h) {
+    if (g.few_h && g.small) {
+      if ((st = launch_small_grad(g, vec_four, stream)) != PG_OK) return st;
+    } else if (g.few_h) {
       st = few == 32 ? launch_few_grad<32>(maps, g, stream) : few == 64 ? launch_few_grad<64>(maps, g, stream) : launch_few_grad<128>(maps, g, stream);
       if (st != PG_OK) return st;
     }

@@ -233,6 +233,36 @@ def test_distill(cuda, N, V, d, K, T, hdt, wdt, ghd, gwd):
     check_grads(r, dh, dW)
 
 
+# Up to 8 rows an fp32 W is multiplied in fp32: four values of a row at a time, or one where d is odd or W
+# starts on 4 bytes alone; more segments and parts than warps; last segments and parts of one row. Beside them more rows, which
+# take W in pieces
+@pytest.mark.parametrize("hdt,ghd,gwd", [(F32, F32, F32), (F32, BF16, BF16), (F32, BF16, F32), (BF16, F32, None), (BF16, BF16, None), (F32, None, F32),
+                                         (BF16, None, None)])
+@pytest.mark.parametrize("N,V,d,shift", [(1, 1025, 4, 0), (1, 1025, 64, 1), (5, 80000, 260, 0), (5, 40000, 260, 3), (8, 20481, 129, 0), (9, 1153, 2052, 0),
+                                         (7, 30000, 65, 0), (8, 30001, 520, 0), (6, 1100, 1021, 0), (17, 20000, 68, 0), (128, 3000, 320, 2)])
+def test_few_rows_of_an_fp32_table(cuda, N, V, d, shift, hdt, ghd, gwd):
+    h, W, t = make(5 * N + V + d, N, V, d, hdt, F32, cuda)
+    W = offset_view(W, shift)
+    r = reference(h, W, t, scale=0.9, z_loss=1e-3, grad_scale=1.0 / N)
+    loss, lse, dh, dW = run_ce(h, W, t, ghd, gwd, scale=0.9, z_loss=1e-3, **({} if ghd is None and gwd is None else {"grad_scale": 1.0 / N}))
+    check_values(r, loss, lse, 1e-3)
+    check_grads(r, dh, dW)
+
+
+def test_few_rows_of_an_fp32_table_lists_and_large_logits(cuda):
+    # tokens far above the target (rows that change their reference) and lists over all of the table's tiles
+    for N, V, d in [(3, 5000, 100), (8, 21000, 72), (5, 90001, 33), (128, 2049, 130)]:
+        h, W, t, ids, u = make(N + V, N, V, d, F32, F32, cuda, K=100)
+        r = reference(h, W, ids=ids, u=u, scale=1.1, T=2.0, grad_scale=1.0 / N)
+        loss, lse, dh, dW = run_distill(h, W, ids, u, F32, F32, scale=1.1, temperature=2.0, grad_scale=1.0 / N)
+        check_values(r, loss, lse)
+        check_grads(r, dh, dW)
+        r = reference(40 * h, W, t, grad_scale=1.0 / N)
+        loss, lse, dh, dW = run_ce(40 * h, W, t, F32, F32, grad_scale=1.0 / N)
+        check_values(r, loss, lse)
+        check_grads(r, dh, dW)
+
+
 @pytest.mark.parametrize("hdt,ghd,gwd", [(BF16, BF16, BF16), (F32, F32, F32)])
 @pytest.mark.parametrize("N,V,d", [(20011, 300, 72), (9000, 1024, 256), (4097, 64, 33)])
 def test_many_rows_of_a_small_table(cuda, N, V, d, hdt, ghd, gwd):

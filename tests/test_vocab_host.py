@@ -89,9 +89,11 @@ def test_workspace_queries(pg):
     assert pg.vocab_ce_grad_workspace_size(4, 100, 8, 1, 1, 1, 1) <= 1 << 20
     for N in (65536, 1 << 24, (1 << 31) - 1):
         assert pg.vocab_ce_grad_workspace_size(N, 50304, 768, 1, 1, 1, 1) <= (2 << 30) + (1 << 30)
-    # the forward call keeps sums and, of fp32 operands, their pieces
+    # the forward call keeps sums and, of fp32 operands, their pieces; up to 8 rows take W as it is
     assert pg.vocab_ce_workspace_size(1 << 20, 50304, 768, 1, 1) <= 1 << 28
     assert pg.vocab_ce_workspace_size(64, 50304, 768, 1, 0) >= 6 * 50304 * 768
+    assert pg.vocab_ce_workspace_size(8, 50304, 768, 1, 0) <= 1 << 24
+    assert pg.vocab_ce_grad_workspace_size(8, 1024, 768, 1, 0, 1, 1) >= 6 * 1024 * 768
     assert pg.vocab_distill_workspace_size(4096, 50304, 768, 64, 1, 1) >= 12 * 4096 * 64
     # sizes at both ends
     for N, V, d in [(1, 1, 1), (1, (1 << 24) - 1, 1), (1, 1, 16384), ((1 << 31) - 1, 1, 1), ((1 << 31) - 1, (1 << 24) - 1, 16384)]:
