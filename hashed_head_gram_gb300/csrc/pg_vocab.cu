@@ -89,7 +89,9 @@ constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: 
 // their own, so that next to nothing is cut. With 2, 4 and 8 of them everywhere: 512 x 1024 x 96 in fp32 41, 39 and 37.5 us, its
 // gradients 6e-7, 1.3e-6 and 1.7e-6 off; 3001 x 32,003 x 515 with an fp32 dW 763, 681 and 640 us. The logits' errors count most,
 // as exp makes them relative ones: 2 for them and where the six products of a gradient hide it, 4 where there are three.
-constexpr int kGroup = 10;               // (80 additions: 7e-7)
+// What is cut leans to one side in every row, so a table's gradient over many rows gathers it: fp32 dW of bf16 operands, 11,708
+// x 604 x 1200, was 2.1e-5 off with logits in one sum and is 1.9e-6 off with one a k-block (8192 x 50,304 x 768 4.14 and 4.69 ms).
+constexpr int kGroup = 10;               // bf16 operands and gradients (80 additions: 7e-7)
 constexpr int kGroupPieces = 1;          // fp32 operands or gradients
 __host__ __device__ __forceinline__ int cut_of(bool logits, int passes) { return logits || passes >= 6 ? 2 : 4; }
 
@@ -2107,7 +2109,7 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   const int np_f = s.gw_dtype == PG_F32 ? 3 : 1;
   g->np_f = g->twice ? 1 : np_f;
   g->small = s.N <= kSmallRows && s.w_dtype == PG_F32 && (!has_h || s.V > kFewTable);
-  const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 ? kGroupPieces : kGroup;
+  const int blocks = (s.d + kBK - 1) / kBK, longest = g->np_h * g->np_w > 1 || g->np_u > 1 ? kGroupPieces : kGroup;
   const int groups = (blocks + longest - 1) / longest;
   g->group = (blocks + groups - 1) / groups;
   // narrower tiles of the logits where the widest leave pairs idle

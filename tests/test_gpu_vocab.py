@@ -274,6 +274,33 @@ def test_many_rows_of_a_small_table(cuda, N, V, d, hdt, ghd, gwd):
     check_grads(r, dh, dW)
 
 
+def gathered(dz, p, z, h):
+    """What the cuts of tensor-core sums come to in dW, as a norm: one a k-block of 128 for the logits, one a 64 rows for dW."""
+    # Each addition (of 16 products) cuts below 2^-23 of the sum, always to one side, so logits are off by 8 2^-23 |z| at most and
+    # their errors add up over the rows, the targets' too, which the row's sum has from there
+    cut = 8 * 2.0 ** -23 * z.abs()
+    first = p * (cut - (p * cut).sum(1, keepdim=True)) / z.shape[0]
+    # and dW's sums of four additions by 4 2^-23 of each
+    second = sum((dz[i:i + 64].T @ h[i:i + 64]).abs() for i in range(0, z.shape[0], 64))
+    return float((first.T @ h).norm()) + 4 * 2.0 ** -23 * float(second.norm())
+
+
+@pytest.mark.parametrize("N,V,d", [(20011, 600, 760), (11708, 604, 1200), (3001, 1100, 2500)])
+def test_an_fp32_table_gradient_gathers_little_of_what_sums_cut(cuda, N, V, d):
+    # states that lean to their targets by up to 12 logits, a few targets in most rows
+    gen = torch.Generator().manual_seed(N)
+    W = (torch.randn(V, d, generator=gen) / math.sqrt(d)).to(BF16)
+    t = (torch.rand(N, generator=gen) ** 3 * V).to(torch.int32)
+    h = (torch.randn(N, d, generator=gen) + torch.rand(N, 1, generator=gen) * 12 * W[t.long()].float()).to(BF16)
+    h, W, t = h.to(cuda), W.to(cuda), t.to(cuda)
+    r = reference(h, W, t, grad_scale=1.0 / N)
+    loss, lse, dh, dW = run_ce(h, W, t, BF16, F32, grad_scale=1.0 / N)
+    z = h.double() @ W.double().T
+    # beside the cuts roundings of 2^-21 or so of each of dz's values, which add in squares, and of the sums in fp32
+    each = 2.0 ** -21 * float(((r["dz"] ** 2).T @ h.double() ** 2).sqrt().norm()) + 2.0 ** -21 * float(r["dW"].norm())
+    assert distance(dW, r["dW"]) <= gathered(r["dz"], torch.softmax(z, 1), z, h.double()) + each
+
+
 @pytest.mark.parametrize("ghd,gwd,accumulate", [(F32, BF16, False), (F32, BF16, True), (F32, F32, False), (F32, F32, True), (None, F32, False),
                                                 (F32, None, False)])
 def test_rows_in_chunks(cuda, ghd, gwd, accumulate):
