@@ -2104,7 +2104,7 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->np_u = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32 ? 3 : 1;
   // An fp32 dW of bf16 operands: f h has 24 bits, so U and f h take six products. With f in U, made from the logits a second
   // time, what is left of f h is h (without the rows that have no gradient): three products and one more of the logits
-  // (3001 x 32,003 x 515, one sum a k-block: 741 -> 622 us).
+  // (3001 x 32,003 x 512 900 -> 810 us, 8192 x 50,304 x 768 5.37 -> 4.67 ms).
   g->twice = s.grad && s.gw_dtype == PG_F32 && s.h_dtype == PG_BF16 && s.w_dtype == PG_BF16 && !is_few;
   const int np_f = s.gw_dtype == PG_F32 ? 3 : 1;
   g->np_f = g->twice ? 1 : np_f;

@@ -458,3 +458,64 @@ def test_what_is_left_out(cuda, N):
         pg.vocab_ce(h[:, ::2], W[:, ::2], t, torch.empty(N, device=cuda), None)
     with pytest.raises(pg.PgError):
         pg.vocab_ce(h, W, t, torch.empty(N, device=cuda), torch.empty(100, dtype=torch.uint8, device=cuda))
+
+
+# Up to 8 rows of an fp32 table have kernels of their own; d = 100 and 33: four values at a time, and one
+@pytest.mark.parametrize("d", [100, 33])
+@pytest.mark.parametrize("hdt", [F32, BF16])
+def test_few_rows_of_an_fp32_table_in_every_way(cuda, d, hdt):
+    pg = _pg()
+    N, V = 7, 3001
+    h, W, t = make(d, N, V, d, hdt, F32, cuda)
+    t[:2] = torch.tensor([-1, V], device=cuda)
+    t[2:4] = torch.tensor([0, V - 1], device=cuda)
+    weight = torch.tensor([1.0, 2.0, 0.5, 1.0, 0.0, 3.0, 1.0], device=cuda)
+    r = reference(h, W, t, weight=weight, z_loss=1e-3)
+    first = run_ce(h, W, t, hdt, F32, weight=weight, z_loss=1e-3)
+    check_values(r, first[0], first[1], 1e-3)
+    check_grads(r, first[2], first[3])
+    for fill in (float("nan"), float("inf"), torch.finfo(hdt).max):  # padded rows hold anything
+        h2 = h.clone()
+        h2[:2] = fill
+        assert all(torch.equal(a, b) for a, b in zip(first, run_ce(h2, W, t, hdt, F32, weight=weight, z_loss=1e-3)))
+    h2 = h.clone()
+    h2[4] = float("nan")  # a row of weight zero has no gradient, whatever its loss
+    second = run_ce(h2, W, t, hdt, F32, weight=weight, z_loss=1e-3)
+    assert torch.equal(first[2], second[2]) and torch.equal(first[3], second[3])
+    # guards around outputs and workspace; another stream, then a graph replayed on other inputs
+    size = pg.vocab_ce_grad_workspace_size(N, V, d, pg.dtype_code(hdt), 0, 0, 0)
+    guard = 512
+    bufs = [torch.full((n + 2 * guard,), 7.5, device=cuda) for n in (N, N * d, V * d)]
+    ws = torch.full((size + 2 * guard,), 0x5A, dtype=torch.uint8, device=cuda)
+    loss, gh, gw = (b[guard:-guard].view(s) for b, s in zip(bufs, [(N,), (N, d), (V, d)]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        pg.vocab_ce_grad(h, W, t, loss, gh, gw, ws[guard:-guard])
+    torch.cuda.current_stream().wait_stream(side)
+    check_grads(reference(h, W, t), gh, gw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pg.vocab_ce_grad(h, W, t, loss, gh, gw, ws[guard:-guard])
+    for seed in (5, 6):
+        for a, b in zip((h, W, t), make(seed, N, V, d, hdt, F32, cuda)):
+            a.copy_(b)
+        graph.replay()
+        got = [x.clone() for x in (loss, gh, gw)]
+        pg.vocab_ce_grad(h, W, t, loss, gh, gw, ws[guard:-guard])
+        assert all(torch.equal(a, b) for a, b in zip(got, (loss, gh, gw)))
+        check_grads(reference(h, W, t), gh, gw)
+    torch.cuda.synchronize()
+    assert pg.device_error() == 0
+    for b in bufs:
+        assert (b[:guard] == 7.5).all() and (b[-guard:] == 7.5).all()
+    assert (ws[:guard] == 0x5A).all() and (ws[-guard:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("V,d", [(1100, 16384), (1 << 22, 8)])
+def test_few_rows_of_the_widest_and_longest_fp32_tables(cuda, V, d):
+    h, W, t = make(V, 8, V, d, F32, F32, cuda)
+    r = reference(h, W, t)
+    loss, lse, dh, dW = run_ce(h, W, t, F32, F32)
+    check_values(r, loss, lse)
+    check_grads(r, dh, dW)
