@@ -307,6 +307,13 @@ __device__ __forceinline__ void sort_keys(uint32_t (&x)[R]) {
       }
 }
 
+// (u - top) / T of a finite u. The difference first: u / T may be infinite where the list's differences are ordinary, and is
+// rounded at u's size. Where the difference passes fp32's range (signs differ), T is divided by first.
+__device__ __forceinline__ float over_temperature(float u, float top, float inv_t) {
+  const float d = u - top;
+  return d > -INFINITY ? d * inv_t : u * inv_t - top * inv_t;
+}
+
 // Distillation: one warp a row, 8 rows a block. The teacher's softmax; the list sorted by token (R registers of a lane), so
 // that the tiles of the first product find what is theirs (`at`, where each segment's tokens begin) and keep those logits;
 // and the dot product of the heaviest token, for a reference. (Dot products of all listed tokens took 101 of 1346 us at
@@ -333,7 +340,7 @@ __device__ void list_rows(const VocabArgs& g, int block, uint32_t (*s_key)[kMaxL
       float y[1];
       if (g.t_dtype == PG_F32) load_cols<PG_F32, 1>(g.tlogits, i * g.K + k, y);
       else load_cols<PG_BF16, 1>(g.tlogits, i * g.K + k, y);
-      u[m] = y[0] * g.inv_t;
+      u[m] = y[0];
       poison |= !(u[m] < INFINITY);  // (also NaN, which fmaxf passes over)
       top = fmaxf(top, u[m]);
     } else {
@@ -351,7 +358,7 @@ __device__ void list_rows(const VocabArgs& g, int block, uint32_t (*s_key)[kMaxL
   for (int m = 0; m < R; ++m) {
     if (u[m] == top) heaviest = min(heaviest, key[m]);
     if (!some) key[m] = kNone;
-    u[m] = !some ? -INFINITY : u[m] - (top > -INFINITY ? top : 0.f);
+    u[m] = u[m] == -INFINITY ? -INFINITY : over_temperature(u[m], top, g.inv_t);
     total += expf(u[m]);
   }
   total = warp_sum(total);
