@@ -19,8 +19,8 @@
 // operations; making the logits again in place of keeping U would cost 8. U is kept in bf16, whose exponent takes
 // exp(+-87); u's rounding (2^-8 at most) is a rounding of p, and that of f h another of dW's. It is kept for a chunk of
 // the rows, 2 GiB at most. A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit
-// of that tile as its reference instead, and vocab_rows_kernel brings the whole row to the reference lse_i: a pass over the
-// rows that need it and no others.
+// of that tile as its reference instead, and vocab_rows_kernel brings the whole row to the largest of its references: a pass over
+// the rows that need it and no others. (lse itself is no reference: it is rounded at its own size, which may be far above a loss.)
 //
 // Precision. bf16 operands and bf16 gradients take one product of bf16 operands each. fp32 values are sums of bf16
 // "pieces" (value = p0 + p1 + p2, 8 bits each), and their products the sum of the pieces' products down to 2^-24 (six of
@@ -153,7 +153,7 @@ struct VocabArgs {
   int passes_h, passes_w;                // piece products of dh, dW
   int group, group_h, group_w;           // k-blocks that one sum in TMEM takes: logits, dh, dW
   int wide, seg, seg_log;                // columns of a logits tile, and of a segment of it (its half), and that's log2
-  int twice;                             // U is made once lse is there, by the logits again
+  int twice;                             // U is made once the rows' sums are there, by the logits again
   int tma_h, tma_w;                      // tiles of dh, dW go out by TMA
   int few_h;                             // dh is made for few rows
   int small;                             // few rows and an fp32 W: FMAs
@@ -737,7 +737,7 @@ __device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabM
   const int lane = threadIdx.x & 31;
   const int64_t col0 = w.col0 + half * g.seg;
   if (row0 >= g.rows || col0 >= g.V) return;
-  if constexpr (KIND == kAgain) {  // c is lse, and f the row's part of the gradient
+  if constexpr (KIND == kAgain) {  // f is the row's part of the gradient over its sum
     const float f = row0 + lane < g.rows ? g.f[row0 + lane] : 0.f;
     logits_half<KIND>(g, maps, from, s_row, row0, col0, c, f == 0.f, f);
     return;
@@ -1814,7 +1814,7 @@ template <bool GRAD, int HT, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid_constant__ VocabArgs g) {
   __shared__ float2 s_all[kRowWarps][kRowsPer];
   __shared__ int s_moved[kRowWarps][kRowsPer], s_fix[kRowsPer];
-  __shared__ float s_to[kRowsPer], s_f[kRowsPer], s_lse[kRowsPer], s_beta[kRowsPer], s_a[kRowsPer];
+  __shared__ float s_ref[kRowsPer], s_f[kRowsPer], s_peak[kRowsPer], s_a[kRowsPer];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (kRowsPer - 1);
   const int r0 = blockIdx.x * kRowsPer, r = r0 + k;
   const bool in = r < g.rows;
@@ -1869,25 +1869,24 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     const float lse2 = all.x + log2f(all.y), lse = lse2 * kLn2;
     const int64_t i = g.row0 + r;
     if (g.lse) g.lse[i] = alive ? lse : 0.f;
-    if (g.loss) g.loss[i] = alive ? (g.ids ? s_a[k] : 0.f) + (lse2 - c) * kLn2 + g.zl * lse * lse : 0.f;
+    // What follows is relative to the row's reference: of lse itself only 2^-24 is known, of exp(lse - reference) 2^-24 too
+    if (g.loss) g.loss[i] = alive ? (g.ids ? s_a[k] : 0.f) + (all.x - c + log2f(all.y)) * kLn2 + g.zl * lse * lse : 0.f;
     if (GRAD) {
       float weight = alive ? g.grad_scale * g.scale : 0.f;
       if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
       float beta = 1.f + 2.f * g.zl * lse;
       if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);  // (its part of U is divided by it)
-      const float to = moved || g.twice ? lse2 : c;
-      const float f = weight == 0.f ? 0.f : weight * beta * exp2f(to - lse2);
+      const float f = weight == 0.f ? 0.f : weight * beta / all.y;
       g.f[r] = f;
       s_f[k] = f;
-      s_to[k] = to;
-      s_lse[k] = lse2;
-      s_beta[k] = beta;
+      s_ref[k] = all.x;
+      s_peak[k] = all.y / beta;  // what a weight of 1 takes off U
       // a row without weight must not bring its infinities and NaN into dW; a row without a target is zero already
       s_fix[k] = !alive ? 3 : weight == 0.f && !(fabsf(lse2) < INFINITY) ? 2 : moved;
     }
   }
   if (!GRAD) return;
-  if (g.twice && threadIdx.x < kRowsPer && in && c != INFINITY) g.c[r] = s_lse[k];
+  if (g.twice && threadIdx.x < kRowsPer && in && c != INFINITY) g.c[r] = s_ref[k];
   __syncthreads();
   const int mine = warp % kRowsPer, part = warp / kRowsPer, row = r0 + mine;
   constexpr int kLanes = 32 * (kRowWarps / kRowsPer);
@@ -1895,7 +1894,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   const int fix = some && !g.twice ? s_fix[mine] : 3;
   float f = some ? s_f[mine] : 0.f;
   if (g.twice && f != 0.f) f = 1.f;  // (U has it; rows without a gradient may still hold anything)
-  const float to = some ? s_to[mine] : 0.f;
+  const float to = some ? s_ref[mine] : 0.f;
   if (fix == 1 || fix == 2) {
     for (int64_t at = (part * 32 + lane) * 8; at < g.Vp; at += kLanes * 8) {
       const float by = fix == 2 ? 0.f : exp2f(0.5f * (g.sums[(at >> g.seg_log) * g.Nc + row].x - to));  // (its square may underflow)
@@ -1914,13 +1913,17 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   }
   __syncthreads();
   if (!some) return;
-  if (fix < 2) {
-    const float peak = exp2f(s_lse[mine] - to) / s_beta[mine];
+  if (s_fix[mine] < 2) {  // (a U that is made later gets these by vocab_targets_kernel)
     for (int e = part * 32 + lane; e < g.K; e += kLanes) {
-      const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
+      const int64_t at = static_cast<int64_t>(row) * g.K + e;
+      const float w = g.wk[at];
       if (w == -1.f || w == 0.f) continue;
-      const int64_t t = g.ids ? g.sorted[static_cast<int64_t>(row) * g.K + e] : __ldg(g.targets + g.row0 + row);
-      float x = exp2f(g.zk[static_cast<int64_t>(row) * g.K + e] - to) - w * peak;
+      const int64_t t = g.ids ? g.sorted[at] : __ldg(g.targets + g.row0 + row);
+      float x = exp2f(g.zk[at] - to) - w * s_peak[mine];
+      if (g.twice) {
+        g.zk[at] = s_f[mine] * x;
+        continue;
+      }
       for (int p = 0; p < g.np_u; ++p)
         reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + t] = take_piece(x);
     }
@@ -1945,21 +1948,18 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
   }
 }
 
-// The targets' places of a U that was made with lse and f: one warp a row.
+// The targets' places of a U that was made with f (vocab_rows_kernel has left them in zk): one warp a row.
 __global__ void __launch_bounds__(256) vocab_targets_kernel(const __grid_constant__ VocabArgs g) {
   grid_dep_wait();
   grid_dep_launch();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= g.rows) return;
-  const float lse2 = g.c[r], f = g.f[r];
-  if (f == 0.f || lse2 == INFINITY) return;
-  float beta = 1.f + 2.f * g.zl * (lse2 * kLn2);
-  if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);
+  if (r >= g.rows || g.f[r] == 0.f) return;
   for (int e = lane; e < g.K; e += 32) {
-    const float w = g.wk[static_cast<int64_t>(r) * g.K + e];
+    const int64_t at = static_cast<int64_t>(r) * g.K + e;
+    const float w = g.wk[at];
     if (w == -1.f || w == 0.f) continue;
-    const int64_t t = g.ids ? g.sorted[static_cast<int64_t>(r) * g.K + e] : __ldg(g.targets + g.row0 + r);
-    float x = f * (exp2f(g.zk[static_cast<int64_t>(r) * g.K + e] - lse2) - w / beta);
+    const int64_t t = g.ids ? g.sorted[at] : __ldg(g.targets + g.row0 + r);
+    float x = g.zk[at];
     for (int p = 0; p < g.np_u; ++p)
       reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + r) * g.Vp + t] = take_piece(x);
   }
