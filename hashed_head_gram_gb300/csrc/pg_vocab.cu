@@ -13,7 +13,8 @@
 // tokens' logits. One small kernel a chunk (vocab_rows_kernel) then has lse_i, the loss and
 // f_i = g_i scale beta_i exp(c_i - lse_i), puts
 //   u_ij - w_ij exp(lse_i - c_i) / beta_i
-// at the targets (from fp32 logits: p - 1 loses nothing where p is close to 1), and
+// at the targets (from fp32 logits; cross entropy keeps its sums without the target's term, so that 1 - p and a small loss are the
+// others' sum and no difference of numbers near 1), and
 //   dh_i = f_i (U W)_i,   dW = U^T (f h)
 // are two more products. So the logits are made once, nothing normalises U, and a gradient costs 6 N V d
 // operations; making the logits again in place of keeping U would cost 8. U is kept in bf16, whose exponent takes
@@ -131,8 +132,9 @@ struct VocabArgs {
   __nv_bfloat16 *hp, *Wp;                // pieces [pieces][rows][dp], or null
   __nv_bfloat16 *U, *F;                  // [pieces][Nc][Vp], [pieces][Nc][dp]
   float2* sums;                          // [segments: halves of the first product's tiles][Nc]: reference (log2), sum
-  float *zk, *wk;                        // [Nc][K] targets' logits (log2), weights (-1: none, or a later place of the same)
+  float *zk, *wk;                        // [Nc][K] targets' logits (without scale), weights (-1: none, or a later place of the same)
   int32_t* sorted;                       // [Nc][K] listed tokens, ascending (zk and wk in their order), then INT_MAX
+  const int32_t* listed;                 // sorted, or the chunk's targets
   uint16_t* at;                          // [segments + 1][Nc] where in it each segment's tokens begin
   float *c, *a;                          // [Nc] reference (log2; +inf: no target), the sum of w log w
   float* f;                              // [Nc]
@@ -277,10 +279,9 @@ __device__ void target_rows(const VocabArgs& g, int block) {
   }
   if (lane != 0) return;
   if (!valid && g.err) atomicMin(reinterpret_cast<unsigned int*>(g.err), static_cast<unsigned int>(i));
-  z[0] *= g.k2;
   g.zk[r] = z[0];
   g.wk[r] = valid ? 1.f : -1.f;
-  g.c[r] = valid ? as_reference(z[0]) : INFINITY;
+  g.c[r] = valid ? as_reference(z[0] * g.k2) : INFINITY;
 }
 
 // 32 R keys, key m * 32 + lane in x[m] of a lane, in ascending order (bitonic).
@@ -582,15 +583,16 @@ __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time. u = 2^(k2 z - c) in fp32 for the row's sum, and to U through the warp's shared memory (32 rows of 64 bytes,
-// swizzled as the TMA store reads them; two such buffers in turn, so that a store reads one while the other fills).
+// swizzled as the TMA store reads them; two such buffers in turn, so that a store reads one while the other fills). skip: the
+// column of the row's target, which its sum leaves out, or -1.
 template <int KIND>
 __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row, int row0, int64_t col0,
-                                             float c, bool dead, float f) {
+                                             float c, bool dead, float f, int skip) {
   constexpr bool KEEP = KIND != kSums;
   const int lane = threadIdx.x & 31;
   const int64_t end = min(col0 + g.seg, g.V);
   const uint64_t k2 = pk(g.k2, g.k2), c2 = pk(-c, -c);
-  const bool some_dead = KEEP && __any_sync(0xffffffffu, dead);
+  const bool some_dead = KEEP && __any_sync(0xffffffffu, dead), some_skip = KIND != kAgain && __any_sync(0xffffffffu, skip >= 0);
   uint64_t sum[2] = {0, 0};
   if (KEEP && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // of an earlier tile
   __syncwarp();
@@ -613,6 +615,11 @@ __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps
       const int left = static_cast<int>(end - c0);
 #pragma unroll
       for (int k = 0; k < 32; ++k) x[k] = k < left ? x[k] : 0.f;
+    }
+    const uint32_t out = skip >> 5 == ch ? 1u << (skip & 31) : 0u;
+    if (some_skip && __any_sync(0xffffffffu, out)) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = out >> k & 1 ? 0.f : x[k];
     }
     if constexpr (KIND == kAgain) {
 #pragma unroll
@@ -657,18 +664,29 @@ __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps
   return lo + hi;
 }
 
-// The listed tokens of this lane's row that fall into a segment: places [e, end) of the sorted list, the first's token.
+// Token t's place among `wide` tokens from col0 on, or -1. (One past V is in no sum.)
+__device__ __forceinline__ int place_in(int32_t t, int64_t col0, int wide) {
+  const uint32_t at = static_cast<uint32_t>(t) - static_cast<uint32_t>(col0);
+  return at < static_cast<uint32_t>(wide) ? static_cast<int>(at) : -1;
+}
+
+// The listed tokens of this lane's row that fall into a segment: places [e, end) of the sorted list, the first's token. Cross
+// entropy: its target, wherever that is. (Read a tile ahead: nothing is done with it before.)
 struct Listed {
   int e, end;
   int32_t token;
 };
 
 __device__ __forceinline__ Listed listed_in(const VocabArgs& g, int row, int64_t col0) {
-  Listed l = {0, 0, 0};
+  Listed l = {0, 0, -1};
   if (row >= g.rows || col0 >= g.V) return l;
-  const int64_t seg = static_cast<uint32_t>(col0) >> g.at_log;
-  l.e = g.at[seg * g.Nc + row];
-  l.end = g.at[(seg + 1) * g.Nc + row];
+  if (g.ids) {
+    const int64_t seg = static_cast<uint32_t>(col0) >> g.at_log;
+    l.e = g.at[seg * g.Nc + row];
+    l.end = g.at[(seg + 1) * g.Nc + row];
+  } else {
+    l.token = g.listed[row];
+  }
   return l;
 }
 
@@ -698,7 +716,7 @@ __device__ __noinline__ void keep_listed(const VocabArgs& g, uint8_t* s_row, uin
       for (; listed.e < listed.end; ++listed.e) {
         const int at = static_cast<int>(g.sorted[row + listed.e] - col0) - c0;  // ascending
         if (at >= 32) break;
-        g.zk[row + listed.e] = *reinterpret_cast<const float*>(s_row + lane * 128 + ((at >> 2 ^ (lane & 7)) << 4) + (at & 3) * 4) * g.k2;
+        g.zk[row + listed.e] = *reinterpret_cast<const float*>(s_row + lane * 128 + ((at >> 2 ^ (lane & 7)) << 4) + (at & 3) * 4);
       }
       __syncwarp();
     }
@@ -724,7 +742,7 @@ __device__ __noinline__ void keep_listed(const VocabArgs& g, uint8_t* s_row, uin
         if (lane == l[k]) y = __uint_as_float(v[k]);
     }
     if (mine) {
-      g.zk[row + listed.e] = y * g.k2;
+      g.zk[row + listed.e] = y;
       if (++listed.e < listed.end) listed.token = g.sorted[row + listed.e];
     }
   }
@@ -739,12 +757,15 @@ __device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabM
   if (row0 >= g.rows || col0 >= g.V) return;
   if constexpr (KIND == kAgain) {  // f is the row's part of the gradient over its sum
     const float f = row0 + lane < g.rows ? g.f[row0 + lane] : 0.f;
-    logits_half<KIND>(g, maps, from, s_row, row0, col0, c, f == 0.f, f);
+    logits_half<KIND>(g, maps, from, s_row, row0, col0, c, f == 0.f, f, -1);
     return;
   }
+  // A target's own term is not in its row's sum: vocab_rows_kernel adds it, and has what p leaves over without a difference of
+  // numbers near one
+  const int skip = g.ids ? -1 : place_in(listed.token, col0, g.seg);
   if (g.ids) keep_listed<KEEP>(g, s_row, from, row0, col0, listed);
   const bool dead = row0 + lane >= g.rows || c == INFINITY;
-  float sum = logits_half<KIND>(g, maps, from, s_row, row0, col0, c, dead, 1.f);
+  float sum = logits_half<KIND>(g, maps, from, s_row, row0, col0, c, dead, 1.f, skip);
   float ref = c;
   const bool over = !dead && !(sum <= kSumLimit);
   if (__any_sync(0xffffffffu, over)) {  // logits far above the targets': the tile's largest for a reference
@@ -761,7 +782,7 @@ __device__ __forceinline__ void logits_epilogue(const VocabArgs& g, const VocabM
     if (over) ref = top == -INFINITY ? 0.f : top;
     if (KEEP && lane == 0) stores_done();  // the same places are written again
     __syncwarp();
-    sum = logits_half<KIND>(g, maps, from, s_row, row0, col0, ref, dead, 1.f);
+    sum = logits_half<KIND>(g, maps, from, s_row, row0, col0, ref, dead, 1.f, skip);
   }
   if (row0 + lane < g.rows) g.sums[static_cast<int64_t>(static_cast<uint32_t>(col0) >> g.seg_log) * g.Nc + row0 + lane] = make_float2(ref, sum);
 }
@@ -1030,13 +1051,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // What a tile needs of its rows is read while the tile before is worked on.
     bool more = job_at<KIND>(g, maps, unit, units, 0, &w);
     float c = INFINITY, next_c = INFINITY;
-    Listed listed = {0, 0, 0}, next_listed = {0, 0, 0};
+    Listed listed = {0, 0, -1}, next_listed = {0, 0, -1};
     auto row_of = [&](const VocabJob& job) { return job.i * kTile + static_cast<int>(rank) * 128 + quarter * 32; };
     auto read_rows = [&](const VocabJob& job) {
       const int row = row_of(job) + lane;
       next_c = INFINITY;
       if (row < g.rows) next_c = g.c[row];
-      if (KIND != kAgain && g.ids) next_listed = listed_in(g, row, job.col0 + half * g.seg);
+      if (KIND != kAgain) next_listed = listed_in(g, row, job.col0 + half * g.seg);
     };
     if (KIND != kGrads && more) {
       read_rows(w);
@@ -1242,9 +1263,10 @@ __device__ __forceinline__ void few_products(FewBars<NT>* bars, volatile int* ab
 }
 
 // A warp's segment of 32 rows of W (a lane each) and 32 rows of h from c0 on, with the logits in r: keeps listed tokens' logits
-// and (keep) the segment's part of U, and gives lane k the reference and sum of row c0 + k. z is the warp's shared memory.
+// and (keep) the segment's part of U, and gives lane k the reference and sum of row c0 + k (without its target, which lane
+// `skip` of the warp has, if any). z is the warp's shared memory.
 __device__ __forceinline__ float2 segment_sum(const VocabArgs& g, bool keep, const uint32_t (&r)[32], float (*z)[33], const float* s_c, int c0,
-                                              int64_t v0, int e, int end) {
+                                              int64_t v0, int e, int end, int skip) {
   const int lane = threadIdx.x & 31, row = c0 + lane;
   const bool in = v0 + lane < g.V;
   auto s_u = reinterpret_cast<uint16_t(*)[40]>(&z[0][0]);  // rows of 80 bytes
@@ -1257,9 +1279,14 @@ __device__ __forceinline__ float2 segment_sum(const VocabArgs& g, bool keep, con
     __syncwarp();
     for (const int64_t row_at = static_cast<int64_t>(row) * g.K; e < end; ++e) {
       const int64_t from_v0 = g.sorted[row_at + e] - v0;
-      if (from_v0 >= 0 && from_v0 < 32) g.zk[row_at + e] = z[lane][from_v0] * g.k2;
+      if (from_v0 >= 0 && from_v0 < 32) g.zk[row_at + e] = z[lane][from_v0];
     }
     __syncwarp();
+  }
+  uint32_t terms = in ? 0xffffffffu : 0;   // rows of h in whose sums this lane's row of W is
+  if (__any_sync(0xffffffffu, skip >= 0)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) terms &= __shfl_sync(0xffffffffu, skip, k) == lane ? ~(1u << k) : 0xffffffffu;
   }
   float ref = c, sum;
 #pragma unroll 1
@@ -1268,7 +1295,7 @@ __device__ __forceinline__ float2 segment_sum(const VocabArgs& g, bool keep, con
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float to = again ? __shfl_sync(0xffffffffu, ref, k) : s_c[c0 + k];
-      x[k] = in ? exp2_fast(fmaf(__uint_as_float(r[k]), g.k2, -to)) : 0.f;
+      x[k] = terms >> k & 1 ? exp2_fast(fmaf(__uint_as_float(r[k]), g.k2, -to)) : 0.f;
     }
     if (keep) {
       for (int p = 0; p < g.np_u; ++p) {
@@ -1427,13 +1454,14 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
         uint32_t r[32];
         tmem_load(from + static_cast<uint32_t>(acc * NT + c0), r);
         const int row = c0 + lane;  // the row of h whose sum this lane gets
-        int e = 0, end = 0;
+        int e = 0, end = 0, skip = -1;
         if (g.ids && row < g.rows) {
           e = g.at[static_cast<int64_t>(t) * g.Nc + row];  // (the four warps' tokens)
           end = g.at[(t + 1ll) * g.Nc + row];
         }
+        if (!g.ids && row < g.rows) skip = place_in(g.listed[row], v0, 32);
         tmem_wait(r);
-        const float2 got = segment_sum(g, KEEP, r, s_z[warp - 2], s_c, c0, v0, e, end);
+        const float2 got = segment_sum(g, KEEP, r, s_z[warp - 2], s_c, c0, v0, e, end, skip);
         if (KEEP) {
           if (row < g.rows) g.sums[seg * g.Nc + row] = got;
         } else {
@@ -1725,12 +1753,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2) vocab_small_kernel(const __g
 #pragma unroll
     for (int k = 0; k < 32; ++k) r[k] = k < NB ? __float_as_uint(z[k][lane]) : 0u;
     __syncwarp();
-    int e = 0, end = 0;
+    int e = 0, end = 0, skip = -1;
     if (g.ids && lane < g.rows) {
       e = g.at[(v0 >> g.at_log) * g.Nc + lane];
       end = g.at[((v0 >> g.at_log) + 1) * g.Nc + lane];
     }
-    const float2 got = segment_sum(g, keep, r, z, s_c, 0, v0, e, end);
+    if (!g.ids && lane < g.rows) skip = place_in(g.listed[lane], v0, 32);
+    const float2 got = segment_sum(g, keep, r, z, s_c, 0, v0, e, end, skip);
     if (lane < g.rows) g.sums[static_cast<int64_t>(seg) * g.Nc + lane] = got;
     __syncwarp();
   }
@@ -1814,13 +1843,13 @@ template <bool GRAD, int HT, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid_constant__ VocabArgs g) {
   __shared__ float2 s_all[kRowWarps][kRowsPer];
   __shared__ int s_moved[kRowWarps][kRowsPer], s_fix[kRowsPer];
-  __shared__ float s_ref[kRowsPer], s_f[kRowsPer], s_peak[kRowsPer], s_a[kRowsPer];
+  __shared__ float s_ref[kRowsPer], s_f[kRowsPer], s_peak[kRowsPer], s_place[kRowsPer], s_a[kRowsPer];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (kRowsPer - 1);
   const int r0 = blockIdx.x * kRowsPer, r = r0 + k;
   const bool in = r < g.rows;
   grid_dep_wait();
   grid_dep_launch();
-  const float c = in ? g.c[r] : INFINITY;
+  const float c = in ? g.c[r] : INFINITY, target_z = in && !g.ids ? g.zk[r] : 0.f;
   float2 all = make_float2(c, 0.f);
   int moved = 0;
   if (in && c != INFINITY) {
@@ -1850,7 +1879,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     float a = 0.f;
     for (int e = lane; c1 != INFINITY && e < g.K; e += 32) {
       const float w = g.wk[static_cast<int64_t>(row) * g.K + e];
-      if (w != -1.f && w != 0.f) a += w * (g.zk[static_cast<int64_t>(row) * g.K + e] - c1);
+      if (w != -1.f && w != 0.f) a += w * fmaf(g.zk[static_cast<int64_t>(row) * g.K + e], g.k2, -c1);
     }
     a = g.a[row] - warp_sum(a) * kLn2;
     if (lane == 0) s_a[warp] = a;
@@ -1865,24 +1894,33 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
       all = joined(all, s_all[w][k]);
       moved |= s_moved[w][k];
     }
-    const bool alive = c != INFINITY;
-    const float lse2 = all.x + log2f(all.y), lse = lse2 * kLn2;
+    const bool alive = c != INFINITY, target = alive && !g.ids;
+    // What follows is relative to the row's reference: of lse itself only 2^-24 is known, of exp(lse - reference) 2^-24 too.
+    // Cross entropy: the target's own term, beside the sum of the others
+    const float d = target ? fmaf(target_z, g.k2, -all.x) : 0.f, own = target ? exp2f(d) : 0.f, sum = all.y + own;
+    const float lse = (all.x + log2f(sum)) * kLn2;
     const int64_t i = g.row0 + r;
     if (g.lse) g.lse[i] = alive ? lse : 0.f;
-    // What follows is relative to the row's reference: of lse itself only 2^-24 is known, of exp(lse - reference) 2^-24 too
-    if (g.loss) g.loss[i] = alive ? (g.ids ? s_a[k] : 0.f) + (all.x - c + log2f(all.y)) * kLn2 + g.zl * lse * lse : 0.f;
+    if (g.loss) {
+      const float loss = g.ids ? s_a[k] + (all.x - c + log2f(sum)) * kLn2 : all.y <= own ? log1pf(all.y / own) : (log2f(sum) - d) * kLn2;
+      g.loss[i] = alive ? loss + g.zl * lse * lse : 0.f;
+    }
     if (GRAD) {
       float weight = alive ? g.grad_scale * g.scale : 0.f;
       if (alive && g.row_weight) weight *= __ldg(g.row_weight + i);
-      float beta = 1.f + 2.f * g.zl * lse;
-      if (fabsf(beta) < 1e-6f) beta = copysignf(1e-6f, beta);  // (its part of U is divided by it)
-      const float f = weight == 0.f ? 0.f : weight * beta / all.y;
+      float more = 2.f * g.zl * lse, beta = 1.f + more;
+      if (fabsf(beta) < 1e-6f) {  // (its part of U is divided by it)
+        beta = copysignf(1e-6f, beta);
+        more = beta - 1.f;
+      }
+      const float f = weight == 0.f ? 0.f : weight * beta / sum;
       g.f[r] = f;
       s_f[k] = f;
       s_ref[k] = all.x;
-      s_peak[k] = all.y / beta;  // what a weight of 1 takes off U
+      s_peak[k] = sum / beta;                       // what a weight of 1 takes off U
+      s_place[k] = fmaf(own, more, -all.y) / beta;  // own - sum / beta, of what p leaves over
       // a row without weight must not bring its infinities and NaN into dW; a row without a target is zero already
-      s_fix[k] = !alive ? 3 : weight == 0.f && !(fabsf(lse2) < INFINITY) ? 2 : moved;
+      s_fix[k] = !alive ? 3 : weight == 0.f && !(fabsf(lse) < INFINITY) ? 2 : moved;
     }
   }
   if (!GRAD) return;
@@ -1918,14 +1956,13 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
       const int64_t at = static_cast<int64_t>(row) * g.K + e;
       const float w = g.wk[at];
       if (w == -1.f || w == 0.f) continue;
-      const int64_t t = g.ids ? g.sorted[at] : __ldg(g.targets + g.row0 + row);
-      float x = exp2f(g.zk[at] - to) - w * s_peak[mine];
+      float x = g.ids ? exp2_fast(fmaf(g.zk[at], g.k2, -to)) - w * s_peak[mine] : s_place[mine];
       if (g.twice) {
         g.zk[at] = s_f[mine] * x;
         continue;
       }
       for (int p = 0; p < g.np_u; ++p)
-        reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + t] = take_piece(x);
+        reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + row) * g.Vp + g.listed[at]] = take_piece(x);
     }
   }
   if (!g.F) return;
@@ -1958,10 +1995,9 @@ __global__ void __launch_bounds__(256) vocab_targets_kernel(const __grid_constan
     const int64_t at = static_cast<int64_t>(r) * g.K + e;
     const float w = g.wk[at];
     if (w == -1.f || w == 0.f) continue;
-    const int64_t t = g.ids ? g.sorted[at] : __ldg(g.targets + g.row0 + r);
     float x = g.zk[at];
     for (int p = 0; p < g.np_u; ++p)
-      reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + r) * g.Vp + t] = take_piece(x);
+      reinterpret_cast<uint16_t*>(g.U)[(static_cast<int64_t>(p) * g.Nc + r) * g.Vp + g.listed[at]] = take_piece(x);
   }
 }
 
@@ -2351,6 +2387,7 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
   for (int64_t row0 = 0; row0 < s.N; row0 += g.Nc) {
     g.row0 = row0;
     g.rows = static_cast<int>(std::min<int64_t>(g.Nc, s.N - row0));
+    g.listed = list ? g.sorted : g.targets + row0;
     g.first = row0 == 0;
     g.last = row0 + g.Nc >= s.N;
     const int64_t blocks_w = g.Wp && g.first ? split_blocks(s.V) : 0, blocks_h = g.hp ? split_blocks(g.rows) : 0;

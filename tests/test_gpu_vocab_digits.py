@@ -75,3 +75,94 @@ def test_weights_of_rows_whose_logits_are_all_large(cuda, N, V, d, hdt, wdt, ghd
     dz = torch.where(others, 2 * p, 0.0)
     for dW in (run_ce(h, W, t, ghd, gwd, scale=scale, grad_scale=2.0)[3], run_distill(h, W, ids, u, ghd, gwd, scale=scale, grad_scale=2.0)[3]):
         check(dz, rel * dz, h, W, None, torch.where(others[:, None], dW, 0.0), scale)
+
+
+@pytest.mark.parametrize("hdt,wdt,ghd,gwd", TYPES)
+@pytest.mark.parametrize("N", NS)
+@pytest.mark.parametrize("V,d", [(700, 64), (3000, 520)])
+def test_rows_whose_logits_are_all_large(cuda, N, V, d, hdt, wdt, ghd, gwd):
+    # the differences are exact, lse itself is only known to 2^-24 of 4000
+    h, W, t, scale = level(N, V, d, hdt, wdt, cuda)
+    z = logits(h, W, scale)
+    lse = z.logsumexp(1)
+    p = torch.softmax(z, 1)
+    rel = 2.0 ** -22 * (2 * float(z.amax(1).sub(z.amin(1)).max()) + 80)
+    one = torch.zeros_like(p).scatter(1, t.long()[:, None], 1.0)
+    want = lse - z.gather(1, t.long()[:, None])[:, 0]
+    loss, got, dh, dW = run_ce(h, W, t, ghd, gwd, scale=scale, grad_scale=2.0)
+    for x in (loss, run_ce(h, W, t, scale=scale)[0]):
+        close(x, want, rel + 2.0 ** -23 * want, "loss")
+    close(got, lse, 2.0 ** -22 * lse, "lse")
+    check(2 * (p - one), 2 * rel * p, h, W, dh, dW, scale)
+    # a teacher of two tokens, weights 3 : 1
+    ids = torch.stack([t, (t + 1) % V], 1).int().contiguous()
+    u = torch.tensor([math.log(3.0), 0.0], device=cuda).repeat(N, 1)
+    q = 0.75 * one + 0.25 * torch.zeros_like(p).scatter(1, ids[:, 1:].long(), 1.0)
+    want = 0.75 * math.log(0.75) + 0.25 * math.log(0.25) - (q * (z - lse[:, None])).sum(1)
+    loss, got, dh, dW = run_distill(h, W, ids, u, ghd, gwd, scale=scale, grad_scale=2.0)
+    for x in (loss, run_distill(h, W, ids, u, scale=scale)[0]):
+        close(x, want, rel + 2.0 ** -20 * (1 + want.abs()), "loss")
+    close(got, lse, 2.0 ** -22 * lse, "lse")
+    check(2 * (p - q), 2 * rel * p + 2 * 2.0 ** -21 * q, h, W, dh, dW, scale)
+
+
+def confident(N, V, d, hdt, wdt, cuda, whole):
+    """Rows whose target is 8 to 70 above the others, or (whole) 12 to 60 with logits that are whole numbers / 4."""
+    gen = torch.Generator().manual_seed(N + V + d + whole)
+    t = torch.randperm(V, generator=gen)[:N].to(torch.int32)
+    if whole:
+        W = (torch.rand(V, d, generator=gen) < 0.5).float() * 2 - 1      # <W_t, W_t> = d, others a few sqrt(d) at most
+        h = torch.randint(1, 3, (N, 1), generator=gen).float() * W[t.long()]
+        h = h + torch.randint(-1, 2, (N, d), generator=gen).float()
+        scale = 0.25
+    else:
+        W = torch.randn(V, d, generator=gen) / math.sqrt(d)
+        W = W.to(wdt).float()
+        gap = 15 + 70 * torch.rand(N, 1, generator=gen)
+        h = gap * W[t.long()] / (W[t.long()] ** 2).sum(1, keepdim=True) + 0.1 * torch.randn(N, d, generator=gen)
+        scale = 1.0
+    return h.to(hdt).to(cuda), W.to(wdt).to(cuda), t.to(cuda), scale
+
+
+def exact_rows(h, W, t, scale):
+    """z, softmax without the target's place, and one minus the target's p, without the difference of numbers near one."""
+    z = logits(h, W, scale)
+    at = t.long()[:, None]
+    zt = z.gather(1, at)
+    others = torch.exp(z - zt).scatter(1, at, 0.0)
+    rest = others.sum(1, keepdim=True)             # (1 - p) / p
+    return z, zt, others / (1 + rest), rest / (1 + rest), torch.log1p(rest)[:, 0]
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("hdt,wdt,ghd,gwd", TYPES)
+@pytest.mark.parametrize("V,d", [(700, 128), (5003, 144)])
+@pytest.mark.parametrize("N", NS)
+def test_rows_that_are_sure_of_their_target(cuda, N, V, d, hdt, wdt, ghd, gwd, whole):
+    h, W, t, scale = confident(N, V, d, hdt, wdt, cuda, whole)
+    z, zt, p, missing, want = exact_rows(h, W, t, scale)
+    assert float(missing.min()) < 1e-7 and (N < 60 or ((missing > 1e-20) & (missing < 1e-3)).sum() > N // 4)
+    far = float((zt - z).abs().max())
+    rel = 2.0 ** -22 * (2 * far + 80) + (0.0 if whole else 2 * logit_errors(h, W, scale))
+    rel = rel if whole else rel[:, None]
+    row = rel if whole else rel[:, 0]
+    for zl in (0.0, 1e-3):
+        lse = z.logsumexp(1)
+        beta1 = 2 * zl * lse[:, None]              # beta - 1
+        loss, got_lse, dh, dW = run_ce(h, W, t, ghd, gwd, scale=scale, z_loss=zl)
+        forward = run_ce(h, W, t, scale=scale, z_loss=zl)
+        lse_off = (0.0 if whole else logit_errors(h, W, scale)) + 2.0 ** -22 * (lse.abs() + 1)
+        for got in (loss, forward[0]):
+            if zl == 0:
+                assert (got >= 0).all()
+                close(got, want, row * want + 2.0 ** -125, "loss")
+            else:
+                close(got, want + zl * lse ** 2, row * want + zl * lse ** 2 * 2.0 ** -21 + 2 * zl * lse.abs() * lse_off + 2.0 ** -125, "loss")
+        for got in (got_lse, forward[1]):
+            close(got, lse, lse_off, "lse")
+        dz = (1 + beta1) * p
+        dz = dz.scatter(1, t.long()[:, None], beta1 * (1 - missing) - missing)
+        b_off = 2 * zl * lse_off[:, None] + 2.0 ** -22 * beta1.abs()
+        part = (rel * (1 + beta1) + b_off) * p
+        part = part.scatter(1, t.long()[:, None], rel * missing + (rel * missing + 2.0 ** -22) * beta1.abs() + b_off)
+        check(dz, part, h, W, dh, dW, scale)
