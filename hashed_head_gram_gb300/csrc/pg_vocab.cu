@@ -21,7 +21,7 @@
 // exp(+-87); u's rounding (2^-8 at most) is a rounding of p, and that of f h another of dW's. It is kept for a chunk of
 // the rows, 2 GiB at most. A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit
 // of that tile as its reference instead, and vocab_rows_kernel brings the whole row to the largest of its references: a pass over
-// the rows that need it and no others. (lse itself is no reference: it is rounded at its own size, which may be far above a loss.)
+// the rows that need it and no others. (Only where a row's weight is next to nothing is lse the reference.)
 //
 // Precision. bf16 operands and bf16 gradients take one product of bf16 operands each. fp32 values are sums of bf16
 // "pieces" (value = p0 + p1 + p2, 8 bits each), and their products the sum of the pieces' products down to 2^-24 (six of
@@ -110,6 +110,9 @@ constexpr int kLaunchRegs = 168, kIssueRegs = 72, kEpiRegs = 216;
 static_assert(kIssueRegs * 128 + kEpiRegs * 256 <= kLaunchRegs * kThreads, "a warpgroup would wait for registers that nobody gives up");
 
 constexpr float kSumLimit = 0x1p57f;     // of a tile's row; above it the row changes its reference
+// A row's factor weight / sum below this takes lse for the row's reference, so that its sum is 1: f h has pieces 2^-16 of it, and
+// h may be small, where numbers end at 2^-126. (With weights of 1 no sum comes near.)
+constexpr float kLeastFactor = 0x1p-90f;
 
 // The kernels of a call but its first are scheduled while the one before still runs. Each waits for that one's end
 // before it reads or writes memory, and reads what earlier kernels wrote by coherent loads.
@@ -1897,7 +1900,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
     const bool alive = c != INFINITY, target = alive && !g.ids;
     // What follows is relative to the row's reference: of lse itself only 2^-24 is known, of exp(lse - reference) 2^-24 too.
     // Cross entropy: the target's own term, beside the sum of the others
-    const float d = target ? fmaf(target_z, g.k2, -all.x) : 0.f, own = target ? exp2f(d) : 0.f, sum = all.y + own;
+    const float d = target ? fmaf(target_z, g.k2, -all.x) : 0.f;
+    float own = target ? exp2f(d) : 0.f, sum = all.y + own;
     const float lse = (all.x + log2f(sum)) * kLn2;
     const int64_t i = g.row0 + r;
     if (g.lse) g.lse[i] = alive ? lse : 0.f;
@@ -1913,10 +1917,17 @@ __global__ void __launch_bounds__(32 * kRowWarps) vocab_rows_kernel(const __grid
         beta = copysignf(1e-6f, beta);
         more = beta - 1.f;
       }
+      float to = all.x;
+      if (weight != 0.f && fabsf(weight * beta) < sum * kLeastFactor) {  // (rounded or not, to is what U is brought to)
+        to += log2f(sum);
+        const float by = exp2f(all.x - to);
+        own *= by, all.y *= by, sum *= by;
+        moved |= to != all.x;
+      }
       const float f = weight == 0.f ? 0.f : weight * beta / sum;
       g.f[r] = f;
       s_f[k] = f;
-      s_ref[k] = all.x;
+      s_ref[k] = to;
       s_peak[k] = sum / beta;                       // what a weight of 1 takes off U
       s_place[k] = fmaf(own, more, -all.y) / beta;  // own - sum / beta, of what p leaves over
       // a row without weight must not bring its infinities and NaN into dW; a row without a target is zero already

@@ -166,3 +166,31 @@ def test_rows_that_are_sure_of_their_target(cuda, N, V, d, hdt, wdt, ghd, gwd, w
         part = (rel * (1 + beta1) + b_off) * p
         part = part.scatter(1, t.long()[:, None], rel * missing + (rel * missing + 2.0 ** -22) * beta1.abs() + b_off)
         check(dz, part, h, W, dh, dW, scale)
+
+
+@pytest.mark.parametrize("hdt,wdt,ghd,gwd", TYPES)
+@pytest.mark.parametrize("N", NS)
+@pytest.mark.parametrize("small", [1e-20, 1e-28])
+def test_small_weights_of_rows_far_from_their_target(cuda, N, hdt, wdt, ghd, gwd, small):
+    # logits up to 38 above the target's: sums below 2^57 of the target's term, which keep their reference
+    V, d = 700, 64
+    gen = torch.Generator().manual_seed(N)
+    W = torch.randint(-1, 2, (V, d), generator=gen).float()
+    h = torch.randint(-1, 2, (N, d), generator=gen).float()
+    t = torch.randint(0, V, (N,), generator=gen, dtype=torch.int32)
+    W[:, 0] = 64.0
+    W[t.long(), 0] = 36.0
+    h[:, 0] = 4.0                                  # 28 below the others, give or take a few
+    h, W, t = h.to(hdt).to(cuda), W.to(wdt).to(cuda), t.to(cuda)
+    scale = 0.25
+    z = logits(h, W, scale)
+    p = torch.softmax(z, 1)
+    rel = 2.0 ** -22 * (2 * float(z.amax(1).sub(z.amin(1)).max()) + 80)
+    one = torch.zeros_like(p).scatter(1, t.long()[:, None], 1.0)
+    _, _, dh, dW = run_ce(h, W, t, ghd, gwd, scale=scale, grad_scale=small)
+    check(small * (p - one), small * rel * (p + one), h, W, dh, dW, scale)
+    # two rows of every three have ordinary weights
+    weight = torch.where(torch.arange(N) % 3 == 0, small, 0.5).to(cuda)
+    _, _, dh, dW = run_ce(h, W, t, ghd, gwd, scale=scale, weight=weight)
+    g = weight.double()[:, None]
+    check(g * (p - one), g * rel * (p + one), h, W, dh, dW, scale)
