@@ -59,7 +59,7 @@ constexpr int64_t kMaxVocab = (1 << 24) - 1;
 constexpr int kMaxList = 256;            // teacher tokens a row
 constexpr int kAtOnce = 1024;            // segments whose beginnings a block collects
 constexpr int kPlanUnits = 76;           // CTA pairs that the plan counts on (any number gives the same results)
-constexpr int64_t kKeepBytes = 2ll << 30;  // of U, f h and the pieces of h
+constexpr int64_t kKeepBytes = 2ll << 30;  // of U, f h, the pieces of h and the lists
 constexpr int64_t kSumBytes = 256 << 20;   // of the tiles' sums
 constexpr int kMaxParts = 32;              // of a gradient, and
 constexpr int kPartTiles = 640;            // tiles that they come to, at most
@@ -2174,7 +2174,8 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->seg_log = g->seg == 128 ? 7 : g->seg == 64 ? 6 : 5;
   g->at_log = is_few ? 7 : g->seg_log;
   const int64_t widest = (s.V + kTile - 1) / kTile;  // tiles a row of them
-  const int64_t row_bytes = 2 * (g->np_u * g->Vp + (has_w ? np_f * g->dp : 0) + (needs_copy(s.h_dtype, s.d) ? g->np_h * g->dp : 0));
+  const int64_t row_bytes = 2 * (g->np_u * g->Vp + (has_w ? np_f * g->dp : 0) + (needs_copy(s.h_dtype, s.d) ? g->np_h * g->dp : 0)) +
+                            (s.list ? 12ll * s.K + 2 * (2 * widest + 1) : 0);  // lists: zk, wk, sorted, at
   int64_t most = std::min(s.grad ? kKeepBytes / row_bytes : kMaxForwardRows, kSumBytes / (16 * widest));
   most = std::max<int64_t>(kTile, most / kTile * kTile);
   const int64_t chunks = (s.N + most - 1) / most;
