@@ -828,6 +828,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& g, const VocabMap
   const bool vec = g.d % 4 == 0 && reinterpret_cast<uintptr_t>(dst) % (dtype == PG_F32 ? 16 : 8) == 0 &&
                    (!add32 || reinterpret_cast<uintptr_t>(add32) % 16 == 0);
   uint32_t r2[2][32];
+  __syncwarp();  // (of the last rows' tile some lanes have read f)
   tmem_load(from, r2[0]);
   if (dh ? g.tma_h : g.tma_w) {  // rows past the last and columns past d are cut off
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // of an earlier tile
@@ -1463,6 +1464,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
           end = g.at[(t + 1ll) * g.Nc + row];
         }
         if (!g.ids && row < g.rows) skip = place_in(g.listed[row], v0, 32);
+        __syncwarp();  // (TMEM's loads and waits want all lanes at once)
         tmem_wait(r);
         const float2 got = segment_sum(g, KEEP, r, s_z[warp - 2], s_c, c0, v0, e, end, skip);
         if (KEEP) {
@@ -1470,6 +1472,7 @@ __global__ void __launch_bounds__(Few<NT>::kThreads, 1)
         } else {
           s_all[warp - 2][row] = joined(s_all[warp - 2][row], got);
         }
+        __syncwarp();
       }
       release();
     }
