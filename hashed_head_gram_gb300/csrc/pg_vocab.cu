@@ -96,13 +96,45 @@ constexpr int kGroup = 10;               // bf16 operands and gradients (80 addi
 constexpr int kGroupPieces = 1;          // fp32 operands or gradients
 __host__ __device__ __forceinline__ int cut_of(bool logits, int passes) { return logits || passes >= 6 ? 2 : 4; }
 
-// How many sums a tile's product along k-blocks [kb0, kb1) of `depth` is made of.
-__host__ __device__ __forceinline__ int sums_of(int kb0, int kb1, int group, int passes, int64_t depth, int cut) {
-  if (passes == 1) return group < kb1 - kb0 ? (kb1 - kb0 + group - 1) / group : 1;
-  const int64_t left = (depth - static_cast<int64_t>(kb1 - 1) * kBK + 15) / 16;  // instructions of the last k-block
+// How many sums a tile's product along k-blocks [kb0, kb1) of `depth` is made of. Of pieces: one of the small products a group, and
+// of the largest one every `cut` instructions, of which the last k-block has as many as there is depth for.
+__host__ __device__ constexpr int sums_of(int kb0, int kb1, int group, int passes, int64_t depth, int cut) {
+  const int groups = group < kb1 - kb0 ? (kb1 - kb0 + group - 1) / group : 1;
+  if (passes == 1) return groups;
+  const int64_t left = (depth - static_cast<int64_t>(kb1 - 1) * kBK + 15) / 16;
   const int steps = left < kBK / 16 ? static_cast<int>(left) : kBK / 16;
-  return (kb1 - kb0 - 1) * (1 + kBK / 16 / cut) + 1 + (steps + cut - 1) / cut;
+  return groups + (kb1 - kb0 - 1) * (kBK / 16 / cut) + (steps + cut - 1) / cut;
 }
+
+// The same as the issuing threads make them (vocab_product_kernel, few_products), counted: an epilogue that waited for another
+// number would wait in vain.
+constexpr int sums_issued(int kb0, int kb1, int group, int passes, int64_t depth, int cut) {
+  int n = 0;
+  for (int k0 = kb0; k0 < kb1; k0 += group < kb1 - k0 ? group : kb1 - k0) {
+    const int len = group < kb1 - k0 ? group : kb1 - k0;
+    ++n;
+    for (int kb = 0, at = k0; kb < len * passes; ++kb) {
+      const int64_t left = depth - static_cast<int64_t>(at) * kBK;
+      if (++at == k0 + len) at = k0;
+      for (int k = 0; k < kBK / 16 && k * 16 < left; ++k)
+        if (passes > 1 && kb >= len * (passes - 1) && k % cut == 0) ++n;
+    }
+  }
+  return n;
+}
+
+constexpr bool sums_agree() {
+  const int all[] = {1, 2, 3, 10, 1 << 30}, pieces[] = {1, 3, 6};
+  for (int group : all)
+    for (int passes : pieces)
+      for (int cut = 2; cut <= 8; cut *= 2)
+        for (int kb0 = 0; kb0 < 3; ++kb0)
+          for (int64_t depth = kb0 * kBK + 1; depth <= (kb0 + 7) * kBK; depth += 61)
+            for (int kb1 = static_cast<int>((depth + kBK - 1) / kBK); kb1 > kb0; kb1 -= 2)
+              if (sums_of(kb0, kb1, group, passes, depth, cut) != sums_issued(kb0, kb1, group, passes, depth, cut)) return false;
+  return true;
+}
+static_assert(sums_agree(), "the epilogue waits for other sums than are made");
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Sums in groups take 128 registers a thread in the epilogue: its two warpgroups take over what the first does not need.
