@@ -202,19 +202,23 @@ struct VocabArgs {
 
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// x becomes what rounding it to bf16 left; returns the rounded value's bits. (Infinities and NaN leave 0.)
+// x becomes what rounding it to bf16 left; returns the rounded value's bits. (Infinities and NaN leave 0.) FULL: x may be any
+// number, also one of those next to fp32's largest that rounding would make infinite; they take bf16's largest.
+template <bool FULL = false>
 __device__ __forceinline__ uint16_t take_piece(float& x) {
-  const uint16_t b = bf16_bits(x);
+  uint16_t b = bf16_bits(x);
+  if (FULL && (b & 0x7fff) == 0x7f80 && fabsf(x) < INFINITY) --b;
   const float r = __uint_as_float(static_cast<uint32_t>(b) << 16);
   x = fabsf(r) <= 3.4e38f ? x - r : 0.f;
   return b;
 }
 
+template <bool FULL = false>
 __device__ __forceinline__ uint4 take_pieces(float (&x)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = take_piece(x[2 * k]), hi = take_piece(x[2 * k + 1]);
+    const uint32_t lo = take_piece<FULL>(x[2 * k]), hi = take_piece<FULL>(x[2 * k + 1]);
     w[k] = lo | hi << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -258,7 +262,7 @@ __device__ void split_rows(const void* src, int64_t rows, int d, int dp, int pie
       x[k] = y[0];
     }
   }
-  for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = take_pieces(x);
+  for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = take_pieces<DT == PG_F32>(x);
 }
 
 // --------------------------------------------------------------------------- the targets' logits

@@ -10,7 +10,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_vocab import BF16, F32, close, half_step, run_ce, run_distill
+from tests.test_gpu_vocab import BF16, F32, close, half_step, make, reference, run_ce, run_distill
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,27 @@ def test_small_weights_of_rows_far_from_their_target(cuda, N, hdt, wdt, ghd, gwd
     _, _, dh, dW = run_ce(h, W, t, ghd, gwd, scale=scale, weight=weight)
     g = weight.double()[:, None]
     check(g * (p - one), g * rel * (p + one), h, W, dh, dW, scale)
+
+
+@pytest.mark.parametrize("hdt,wdt", [(F32, F32), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("N", NS + [9])
+def test_fp32_values_beyond_the_largest_of_bf16(cuda, N, hdt, wdt):
+    # finite, and multiplied by zeros: they must not become infinities
+    h, W, t = make(N, N, 1200, 80, hdt, wdt, cuda)
+    for x, y in ((W, h), (h, W)):
+        if x.dtype == F32:
+            hh, ww = h.clone(), W.clone()
+            (ww if x is W else hh)[:, 5] = torch.finfo(F32).max
+            (hh if x is W else ww)[:, 5] = 0.0
+            plain_h, plain_w = hh.clone(), ww.clone()
+            plain_h[:, 5] = plain_w[:, 5] = 0.0
+            r = reference(plain_h, plain_w, t)
+            loss, lse, _, _ = run_ce(hh, ww, t)
+            E = torch.where(r["keep"], r["E"], 0.0)
+            close(loss, r["loss"], 2 * E + 2.0 ** -22 * r["loss"].abs(), "loss")
+            close(lse, r["lse"], E + 2.0 ** -23 * r["lse"].abs(), "lse")
+            if x is W:  # (grad_W does not have W in it)
+                _, _, _, dW = run_ce(hh, ww, t, None, F32)
+                assert dW.isfinite().all()
+                _, _, _, want = run_ce(plain_h, plain_w, t, None, F32)
+                assert torch.equal(dW, want)
