@@ -19,7 +19,7 @@
 // are two more products. So the logits are made once, nothing normalises U, and a gradient costs 6 N V d
 // operations; making the logits again in place of keeping U would cost 8. U is kept in bf16, whose exponent takes
 // exp(+-87); u's rounding (2^-8 at most) is a rounding of p, and that of f h another of dW's. It is kept for a chunk of
-// the rows, 2 GiB at most. A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit
+// the rows, 2 GiB or 256 rows where those take more. A tile's row whose sum passes 2^57 (logits 40 above the targets') takes the row's largest logit
 // of that tile as its reference instead, and vocab_rows_kernel brings the whole row to the largest of its references: a pass over
 // the rows that need it and no others. (Only where a row's weight is next to nothing is lse the reference.)
 //
@@ -2159,7 +2159,7 @@ void plan_schedule(VocabArgs* g, int units, bool has_h, bool has_w) {
       const int a = static_cast<int>(static_cast<int64_t>(g->tiles2) * q / units);
       const int64_t rest = static_cast<int64_t>(g->tiles3) * qw - static_cast<int64_t>(g->delta) * g->light;
       double t = std::max((a + (g->heavy ? 1 : 0)) * cost2, a * cost2 + g->delta * cost3) + static_cast<double>((rest + units - 1) / units) * cost3;
-      if (q > 1) t += static_cast<double>(q) * g->Nc * g->d * 8 / 4e6;
+      if (q > 1) t += static_cast<double>(q) * nm * kTile * g->d * 8 / 4e6;
       if (qw > 1) t += static_cast<double>(qw) * g->V * g->d * 8 / 4e6;
       if (q > 1 || qw > 1) t += 8;
       if (best >= 0 && t >= best) continue;
@@ -2218,17 +2218,19 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   int64_t most = std::min(s.grad ? kKeepBytes / row_bytes : kMaxForwardRows, kSumBytes / (16 * widest));
   most = std::max<int64_t>(kTile, most / kTile * kTile);
   const int64_t chunks = (s.N + most - 1) / most;
-  g->Nc = static_cast<int>(((s.N + chunks - 1) / chunks + kTile - 1) / kTile * kTile);
-  const int64_t rows = std::min(most, (s.N + kTile - 1) / kTile * kTile);  // room for these (Nc of them or more)
+  const int unit = is_few ? kRowsPer : kTile;  // (few rows: those that are there, to the lists' blocks)
+  g->Nc = static_cast<int>(((s.N + chunks - 1) / chunks + unit - 1) / unit * unit);
+  const int64_t rows = std::min(most, (s.N + unit - 1) / unit * unit);  // room for these (Nc of them or more)
   g->Wp = needs_copy(s.w_dtype, s.d) && !g->small ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_w * s.V * g->dp)) : nullptr;
   g->hp = needs_copy(s.h_dtype, s.d) && !g->small ? reinterpret_cast<__nv_bfloat16*>(take(2ll * g->np_h * rows * g->dp)) : nullptr;
   // (narrower tiles are kPlanUnits at most, for a chunk of kTile rows; few rows have a sum for 32 columns, or four a CTA of 128)
-  g->sums = reinterpret_cast<float2*>(take(16 * std::max({widest * rows, static_cast<int64_t>(kPlanUnits) * kTile,
-                                                          std::max((s.V + 63) / 64, 2 * ((s.V + 127) / 128)) * kTile})));
+  const int64_t sums_few = 2 * ((s.V + 127) / 128);
+  g->sums = reinterpret_cast<float2*>(take(16 * (is_few ? std::max(sums_few * rows, int64_t{kTile})
+                                                        : std::max({widest * rows, static_cast<int64_t>(kPlanUnits) * kTile, sums_few * kTile}))));
   g->zk = reinterpret_cast<float*>(take(4ll * rows * s.K));
   g->wk = reinterpret_cast<float*>(take(4ll * rows * s.K));
   g->sorted = s.list ? reinterpret_cast<int32_t*>(take(4ll * rows * s.K)) : nullptr;
-  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2 * std::max<int64_t>((2 * widest + 1) * rows, int64_t{3} * kPlanUnits * kTile))) : nullptr;
+  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2 * (is_few ? (2 * widest + 1) * rows : std::max<int64_t>((2 * widest + 1) * rows, int64_t{3} * kPlanUnits * kTile)))) : nullptr;
   g->c = reinterpret_cast<float*>(take(4 * rows));
   g->a = reinterpret_cast<float*>(take(4 * rows));
   g->U = nullptr;
@@ -2243,10 +2245,10 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
     }
     plan_schedule(g, kPlanUnits, has_h, has_w);
     const int64_t kv = (s.V + kBK - 1) / kBK, kn = (std::min(s.N, rows) + kBK - 1) / kBK;
-    if (has_h) {  // parts of a chunk's rows, or for few rows of kTile
-      const int64_t some = std::min<int64_t>(kMaxParts * rows / kTile, kPartTiles / g->nd);
+    if (has_h) {  // parts of a chunk's rows, or as many as few rows have
+      const int64_t some = std::min<int64_t>(kMaxParts * (is_few ? 1 : rows / kTile), kPartTiles / g->nd);
       const int64_t few = std::min<int64_t>(kv, std::max(1, 4 * kPlanUnits / ((s.d + 127) / 128)));
-      float* to = reinterpret_cast<float*>(take(4ll * kTile * s.d * std::max({some, few, int64_t{1}})));
+      float* to = reinterpret_cast<float*>(take(4ll * (is_few ? rows : kTile) * s.d * std::max({some, few, int64_t{1}})));
       if (g->q > 1 || g->few_h) g->parts = to;
     }
     const int64_t parts_w = std::min({int64_t{kMaxParts}, kn / 2, kPartTiles / (widest * g->nd)});

@@ -31,3 +31,17 @@ def test_forward_lists_are_bounded(pg):
     for N in (1 << 20, (1 << 31) - 1):
         assert pg.vocab_distill_workspace_size(N, 64, 96, 256, 1, 1) <= 1 << 28
         assert pg.vocab_distill_workspace_size(N, 50304, 768, 256, 1, 1) <= 1 << 28
+
+
+def test_few_rows_reserve_their_own(pg):
+    # U and the sums of the rows that there are (to eight), not of a tile of 256
+    V = (1 << 24) - 1
+    assert pg.vocab_ce_grad_workspace_size(1, V, 8, 1, 1, None, 0) <= 8 * (6 * V + V // 4 + 64) + (1 << 20)
+    assert pg.vocab_ce_grad_workspace_size(8, 128000, 2560, 1, 1, 1, 1) <= 8 * (2 * 128000 + 128000 // 4) + 4 * 8 * 2560 * 64 + (1 << 20)
+    assert pg.vocab_distill_grad_workspace_size(1, 1000, 64, 256, 1, 1, 1, 0) <= 1 << 19
+    for N, V, d in [(1, 5000, 64), (31, 50304, 768), (128, 50304, 768)]:
+        few = -(-N // 8) * 8
+        for hd, wd, ghd, gwd in [(1, 1, 1, 1), (0, 0, 0, 0)]:
+            size = pg.vocab_ce_grad_workspace_size(N, V, d, hd, wd, ghd, gwd)
+            parts = 4 * few * d * max(32, 304 // -(-d // 128) + 1)
+            assert size <= few * (6 * (V + 64) + V // 2 + 24 * d) + parts + 6 * V * d + (1 << 20), (N, size)
