@@ -203,13 +203,14 @@ struct VocabArgs {
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
 // x becomes what rounding it to bf16 left; returns the rounded value's bits. (Infinities and NaN leave 0.) FULL: x may be any
-// number, also one of those next to fp32's largest that rounding would make infinite; they take bf16's largest.
+// number, also one next to fp32's largest, which rounding would make infinite: at most bf16's largest is taken. (Infinities and
+// NaN are the next piece's then. For all three pieces, with comparisons of the bits: 16 x 128,000 x 2560 1204 us, 1130 like this.)
 template <bool FULL = false>
 __device__ __forceinline__ uint16_t take_piece(float& x) {
-  uint16_t b = bf16_bits(x);
-  if (FULL && (b & 0x7fff) == 0x7f80 && fabsf(x) < INFINITY) --b;
+  constexpr float kMost = 0x1.FEp127f;
+  const uint16_t b = bf16_bits(FULL ? fminf(fmaxf(x, -kMost), kMost) : x);
   const float r = __uint_as_float(static_cast<uint32_t>(b) << 16);
-  x = fabsf(r) <= 3.4e38f ? x - r : 0.f;
+  x = FULL || fabsf(r) <= 3.4e38f ? x - r : 0.f;
   return b;
 }
 
@@ -262,7 +263,8 @@ __device__ void split_rows(const void* src, int64_t rows, int d, int dp, int pie
       x[k] = y[0];
     }
   }
-  for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = take_pieces<DT == PG_F32>(x);
+  *reinterpret_cast<uint4*>(dst + r * dp + c) = take_pieces<DT == PG_F32>(x);
+  for (int p = 1; p < pieces; ++p) *reinterpret_cast<uint4*>(dst + (p * rows + r) * dp + c) = take_pieces(x);
 }
 
 // --------------------------------------------------------------------------- the targets' logits
