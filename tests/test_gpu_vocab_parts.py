@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.test_gpu_vocab import BF16, F32, check_grads, check_values, make, reference, run_distill
+from tests.test_gpu_vocab import BF16, F32, _pg, check_grads, check_values, make, reference, run_ce, run_distill
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +19,51 @@ def test_lists_in_chunks(cuda, N, V, d, K, ghd, gwd):
     loss, lse, dh, dW = run_distill(h, W, ids, u, ghd, gwd, grad_scale=0.01)
     check_values(r, loss, lse)
     check_grads(r, dh, dW)
+
+
+@pytest.mark.parametrize("hdt,gwd", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("N,V,d", [(20011, 300, 72), (9000, 1024, 256), (4097, 64, 33), (20011, 300, 33)])
+def test_parts_are_added_to_what_is_there(cuda, N, V, d, hdt, gwd):
+    # grad_W's few tiles are cut along the rows; joining the parts adds the old gradient (four columns at a time, and one)
+    h, W, t = make(N + d, N, V, d, hdt, hdt, cuda)
+    r = reference(h, W, t, grad_scale=1.0 / N)
+    old = (torch.randn(V, d, generator=torch.Generator().manual_seed(N)) * 0.01).to(gwd).to(cuda)
+    gw = old.clone()
+    run_ce(h, W, t, BF16, gwd, grad_scale=1.0 / N, accumulate=gw)
+    check_grads(r, None, gw, old)
+    ids, u = t[:, None].contiguous(), torch.zeros(N, 1, device=cuda)
+    pg = _pg()
+    gw.copy_(old)
+    loss = torch.empty(N, device=cuda)
+    code = pg.dtype_code(hdt)
+    ws = torch.empty(pg.vocab_distill_grad_workspace_size(N, V, d, 1, code, code, None, pg.dtype_code(gwd)), dtype=torch.uint8, device=cuda)
+    pg.vocab_distill_grad(h, W, ids, u, loss, None, gw, ws, grad_scale=1.0 / N, accumulate=True)
+    check_grads(r, None, gw, old)
+
+
+def test_losses_take_no_device_memory(cuda):
+    # all that the calls use is the caller's: outputs, gradients and workspace
+    pg = _pg()
+    cases = []
+    for N, V, d, K, dt in [(8, 5000, 256, 20, BF16), (300, 5000, 256, 20, BF16), (5, 3000, 64, 7, F32), (200, 3000, 64, 7, F32)]:
+        h, W, t, ids, u = make(N, N, V, d, dt, dt, cuda, K=K)
+        code = pg.dtype_code(dt)
+        size = max(pg.vocab_ce_grad_workspace_size(N, V, d, code, code, code, 0), pg.vocab_distill_grad_workspace_size(N, V, d, K, code, code, code, 0))
+        cases.append((h, W, t, ids, u, torch.empty(N, device=cuda), torch.empty_like(h), torch.empty(V, d, device=cuda),
+                      torch.empty(size, dtype=torch.uint8, device=cuda)))
+
+    def calls():
+        for h, W, t, ids, u, loss, gh, gw, ws in cases:
+            pg.vocab_ce(h, W, t, loss, ws)
+            pg.vocab_distill(h, W, ids, u, loss, ws)
+            pg.vocab_ce_grad(h, W, t, loss, gh, gw, ws)
+            pg.vocab_distill_grad(h, W, ids, u, loss, gh, gw, ws)
+
+    calls()  # loads the device code
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    for _ in range(3):
+        calls()
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free
+    assert pg.device_error() == 0
