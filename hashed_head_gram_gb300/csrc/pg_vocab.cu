@@ -303,8 +303,10 @@ __device__ __forceinline__ void warp_dots(const VocabArgs& g, int64_t i, const i
   for (int e = 0; e < E; ++e) sum[e] = warp_sum(sum[e]);
 }
 
-// A reference that is no logit: +infinity stands for a row without a target.
-__device__ __forceinline__ float as_reference(float z) { return z == INFINITY ? __int_as_float(0x7fffffff) : z; }
+// A logit as a reference: +infinity stands for a row without a target, and what is relative to -infinity is NaN.
+__device__ __forceinline__ float as_reference(float z) {
+  return z == INFINITY ? __int_as_float(0x7fffffff) : z == -INFINITY ? -0x1.FFFFFEp127f : z;
+}
 
 // Cross entropy: one warp a row, a row of h and one of W.
 template <int HT, int WT, bool VEC>

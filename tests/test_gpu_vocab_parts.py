@@ -67,3 +67,19 @@ def test_losses_take_no_device_memory(cuda):
     torch.cuda.synchronize()
     assert torch.cuda.mem_get_info()[0] == free
     assert pg.device_error() == 0
+
+
+@pytest.mark.parametrize("N", [5, 300])
+def test_a_list_whose_heaviest_token_is_out_of_reach(cuda, N):
+    # its logit is -infinity in fp32: so is log q, and the loss infinite; what is pushed down and up is finite
+    h, W, _, ids, u = make(N, N, 700, 80, F32, F32, cuda, K=4, pad=0.0)
+    h[:, 0], W[:, 0] = 1e20, 0.0
+    ids[:] = torch.tensor([7, 8, 9, 10], dtype=torch.int32, device=cuda)
+    u[:] = torch.tensor([3.0, 0.0, 0.0, 0.0], device=cuda)
+    W[7, 0] = -1e20
+    loss, lse, _, dW = run_distill(h, W, ids, u, None, F32)
+    assert (loss == float("inf")).all() and lse.isfinite().all()
+    forward, _, _, _ = run_distill(h, W, ids, u)
+    assert (forward == float("inf")).all()
+    _, _, dh, _ = run_distill(h, W, ids, u, F32, None)
+    assert dh[:, 1:].isfinite().all()
