@@ -35,9 +35,9 @@
 // rows of an fp32 W, kernels of fp32 FMAs.
 //
 // Bound by the tensor cores, and in long calls by the power limit (the measured bf16 rate: 1914 TFLOP/s for a short
-// product, 1721 for seconds of them). 16,384 x 50,304 x 768: 734-753 us, 1.68-1.72 PFLOP/s. With gradients, 65,536 x 50,304 x 768:
-// 10.2 ms, 1.49; 8192 x 128,000 x 2560: 9.9 ms, 1.63. Of 2.33 ms a chunk of 16,384 rows by 768 (at full clocks) the first
-// product is 0.77 (0.62 without U: its stores go through L2 beside 16 TB/s of operand loads), the other two 1.41.
+// product, 1721 for seconds of them). 16,384 x 50,304 x 768: 762-779 us, 1.63-1.66 PFLOP/s. With gradients, 65,536 x 50,304 x 768:
+// 10.1-10.5 ms, 1.45-1.50; 8192 x 128,000 x 2560: 10.1-10.6 ms, 1.52-1.60. Of 2.33 ms a chunk of 16,384 rows by 768 (at full
+// clocks) the first product is 0.77 (0.62 without U: its stores go through L2 beside 16 TB/s of operand loads), the other two 1.41.
 #include <cuda_bf16.h>
 
 #include <limits.h>
@@ -87,12 +87,13 @@ constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |  // kind::f16: 
 // one side: 1.4e-6 of the logits at d = 2560, 4e-6 with the six products of fp32 operands. Where an fp32 result comes
 // of it, sums longer than kGroup k-blocks are made in groups, which the epilogue adds up in registers. Products of pieces
 // run from the smallest to the largest, k-block by k-block, and of the largest every few instructions (of 16 k) make a sum of
-// their own, so that next to nothing is cut. With 2, 4 and 8 of them everywhere: 512 x 1024 x 96 in fp32 41, 39 and 37.5 us, its
-// gradients 6e-7, 1.3e-6 and 1.7e-6 off; 3001 x 32,003 x 515 with an fp32 dW 763, 681 and 640 us. The logits' errors count most,
-// as exp makes them relative ones: 2 for them and where the six products of a gradient hide it, 4 where there are three.
+// their own, so that next to nothing is cut. With 2, 4 and 8 of them everywhere: 512 x 1024 x 96 in fp32 42, 39 and 38.5 us, its
+// gradients 1.3e-7, 1.7e-7 and 2.7e-7 off; 3001 x 32,003 x 515 with an fp32 dW 876, 787 and 745 us. The logits' errors count most,
+// as exp makes them relative ones: 2 for them and where the six products of a gradient hide it, 4 where there are three (821 us).
 // What is cut leans to one side in every row, so a table's gradient over many rows gathers it: fp32 dW of bf16 operands, 11,708
-// x 604 x 1200, was 2.1e-5 off with logits in one sum and is 1.9e-6 off with one a k-block (8192 x 50,304 x 768 4.14 and 4.69 ms).
-constexpr int kGroup = 10;               // bf16 operands and gradients (80 additions: 7e-7)
+// x 604 x 1200, is 3.3e-7 off with logits in sums of ten k-blocks, 1.5e-7 of two and 1.4e-7 of one (8192 x 50,304 x 768 3.11, 3.38
+// and 3.58 ms).
+constexpr int kGroup = 10;               // bf16 operands and gradients (80 additions: 7e-7 of a logit)
 constexpr int kGroupPieces = 1;          // fp32 operands or gradients
 __host__ __device__ __forceinline__ int cut_of(bool logits, int passes) { return logits || passes >= 6 ? 2 : 4; }
 
@@ -167,7 +168,7 @@ struct VocabArgs {
   __nv_bfloat16 *hp, *Wp;                // pieces [pieces][rows][dp], or null
   __nv_bfloat16 *U, *F;                  // [pieces][Nc][Vp], [pieces][Nc][dp]
   float2* sums;                          // [segments: halves of the first product's tiles][Nc]: reference (log2), sum
-  float *zk, *wk;                        // [Nc][K] targets' logits (without scale), weights (-1: none, or a later place of the same)
+  float *zk, *wk;                        // [Nc][K] targets' logits <h, W_j>, weights (-1: none, or a later place of the same)
   int32_t* sorted;                       // [Nc][K] listed tokens, ascending (zk and wk in their order), then INT_MAX
   const int32_t* listed;                 // sorted, or the chunk's targets
   uint16_t* at;                          // [segments + 1][Nc] where in it each segment's tokens begin
@@ -1739,8 +1740,9 @@ __device__ __forceinline__ float4 four_of_h(const VocabArgs& g, int row, int c0)
 
 // The first product of an fp32 W with up to 8 rows of h, in fp32 FMAs: W is read once, as it is, and no pieces of it are made.
 // A warp has a segment of 32 rows of W, four of them at a time, its lanes along d (both halves of a packed FMA along d, too);
-// h comes from the L1 cache. Bound by the loads under way: 8 x 128,000 x 2560 347 us, 3.8 TB/s (in pieces 1120, of which 477
-// make them and 640 the six products, whose sums in TMEM follow one another), 8 x 10,000 x 768 39 us (49). Sixteen rows, two of
+// h comes from the L1 cache. Bound by the loads under way (two blocks an SM leave 128 registers a thread, of which the fp32 kernel
+// spills 368 bytes): 8 x 128,000 x 2560 347 us, 3.8 TB/s, the call 355-362 (in pieces 1130, of which 477 make them and 640 the six
+// products, whose sums in TMEM follow one another), 8 x 10,000 x 768 39 us (49). Sixteen rows, two of
 // W at a time, take longer than pieces unless W is far larger than L2 (16 x 10,000 x 768 76 us and 49).
 template <int HT, bool VEC>
 __global__ void __launch_bounds__(kSmallThreads, 2) vocab_small_kernel(const __grid_constant__ VocabArgs g, int keep) {
@@ -2201,7 +2203,7 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->np_u = s.gh_dtype == PG_F32 || s.gw_dtype == PG_F32 ? 3 : 1;
   // An fp32 dW of bf16 operands: f h has 24 bits, so U and f h take six products. With f in U, made from the logits a second
   // time, what is left of f h is h (without the rows that have no gradient): three products and one more of the logits
-  // (3001 x 32,003 x 512 900 -> 810 us, 8192 x 50,304 x 768 5.37 -> 4.67 ms).
+  // (3001 x 32,003 x 515 1025 -> 820 us, 8192 x 50,304 x 768 4.36 -> 3.58 ms).
   g->twice = s.grad && s.gw_dtype == PG_F32 && s.h_dtype == PG_BF16 && s.w_dtype == PG_BF16 && !is_few;
   const int np_f = s.gw_dtype == PG_F32 ? 3 : 1;
   g->np_f = g->twice ? 1 : np_f;
