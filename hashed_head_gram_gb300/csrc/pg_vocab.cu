@@ -626,9 +626,9 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time. u = 2^(k2 z - c) in fp32 for the row's sum, and to U through the warp's shared memory (32 rows of 64 bytes,
-// swizzled as the TMA store reads them; two such buffers in turn, so that a store reads one while the other fills). skip: the
-// column of the row's target, which its sum leaves out, or -1.
+// Logits of a tile: a warp has 32 rows (a lane each) and 128 columns, 32 at a time. u = 2^(k2 z - c) in fp32 for the row's sum,
+// and to U through the warp's shared memory (32 rows of 64 bytes, swizzled as the TMA store reads them; two such buffers in turn, so
+// that a store reads one while the other fills). skip: the column of the row's target, which its sum leaves out, or -1.
 template <int KIND>
 __device__ __forceinline__ float logits_half(const VocabArgs& g, const VocabMaps& maps, uint32_t from, uint8_t* s_row, int row0, int64_t col0,
                                              float c, bool dead, float f, int skip) {
@@ -2236,7 +2236,8 @@ size_t carve_vocab(uint8_t* base, const Sizes& s, VocabArgs* g) {
   g->zk = reinterpret_cast<float*>(take(4ll * rows * s.K));
   g->wk = reinterpret_cast<float*>(take(4ll * rows * s.K));
   g->sorted = s.list ? reinterpret_cast<int32_t*>(take(4ll * rows * s.K)) : nullptr;
-  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2 * (is_few ? (2 * widest + 1) * rows : std::max<int64_t>((2 * widest + 1) * rows, int64_t{3} * kPlanUnits * kTile)))) : nullptr;
+  const int64_t places = (2 * widest + 1) * rows;
+  g->at = s.list ? reinterpret_cast<uint16_t*>(take(2 * (is_few ? places : std::max(places, int64_t{3} * kPlanUnits * kTile)))) : nullptr;
   g->c = reinterpret_cast<float*>(take(4 * rows));
   g->a = reinterpret_cast<float*>(take(4 * rows));
   g->U = nullptr;
@@ -2476,7 +2477,8 @@ pg_status run_vocab(VocabArgs g, const Sizes& s, cudaStream_t stream) {
         return vocab_map(map, dst, 1, rows, s.d, s.d, rows, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, f32) ? 1 : -1;
       };
       const bool through = g.acc && !g.last;
-      g.tma_w = s.gw_dtype >= 0 && !g.parts_w && g.first && !g.accumulate ? out_map(&maps.Gw, through ? static_cast<void*>(g.acc) : g.gw, through ? PG_F32 : s.gw_dtype, s.V) : 0;
+      g.tma_w = s.gw_dtype >= 0 && !g.parts_w && g.first && !g.accumulate
+                    ? out_map(&maps.Gw, through ? static_cast<void*>(g.acc) : g.gw, through ? PG_F32 : s.gw_dtype, s.V) : 0;
       g.tma_h = s.gh_dtype >= 0 && !g.parts
                     ? out_map(&maps.Gh, static_cast<uint8_t*>(g.gh) + row0 * s.d * static_cast<int64_t>(dtype_bytes(s.gh_dtype)), s.gh_dtype, g.rows) : 0;
       if (g.tma_w < 0 || g.tma_h < 0) return PG_ERR_CUDA;
